@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "zp_aux.cuh"
+#include "zp_chunk.cuh"
 #include "zp_internal.cuh"
 
 using zp::Workspace;
@@ -759,6 +760,161 @@ zp_status zp_global_redundancy_gram(zp_cache *c, const int32_t *block_tables,
     a.sticky = c->ws.sticky;
     return zp::launch_gram_redundancy(a, c->d, static_cast<int>(units), c->num_sms,
                                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ZP_OK
+               : ZP_ERR_CUDA;
+}
+
+// What the calls on a ragged chunk share.
+static zp_status chunk_checks(const zp_cache *c, int32_t layer, const int32_t *block_tables,
+                              int32_t bt_stride, int32_t num_rows, const int32_t *lengths,
+                              int32_t R, const int32_t *starts, int32_t total)
+{
+    if (!c || !block_tables || !lengths || !starts)
+        return ZP_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= c->L || R < 0 || R > c->max_requests || num_rows < 1 ||
+        bt_stride < 1 || total < 0)
+        return ZP_ERR_INVALID_ARG;
+    if (!aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(starts, 4))
+        return ZP_ERR_INVALID_ARG;
+    if (static_cast<long long>(bt_stride) * c->b >= (1ll << 31))
+        return ZP_ERR_UNSUPPORTED;
+    return ZP_OK;
+}
+
+// A row stride in elements: whole 16-byte vectors, no overlap of two rows.
+static bool row_stride_ok(int64_t stride, long long row) { return stride >= row && stride % 8 == 0; }
+
+zp_status zp_append_kv_chunk(zp_cache *c, int32_t layer, const void *k_new, int64_t k_stride,
+                             const void *v_new, int64_t v_stride, const int32_t *starts,
+                             int32_t total, const int32_t *block_tables, int32_t bt_stride,
+                             int32_t num_rows, const int32_t *lengths, const int32_t *req_idx,
+                             int32_t R, void *stream)
+{
+    NvtxRange nvtx("zp_append_kv_chunk");
+    const zp_status st =
+        chunk_checks(c, layer, block_tables, bt_stride, num_rows, lengths, R, starts, total);
+    if (st != ZP_OK)
+        return st;
+    const long long row = static_cast<long long>(c->Hkv) * c->d;
+    if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+        !row_stride_ok(k_stride, row) || !row_stride_ok(v_stride, row))
+        return ZP_ERR_INVALID_ARG;
+    if (R == 0 || total == 0)
+        return ZP_OK;
+    if (!on_device(c))
+        return ZP_ERR_INVALID_ARG;
+    zp::ChunkKvArgs a{};
+    a.kpool = static_cast<__nv_bfloat16 *>(c->kpools[layer]);
+    a.vpool = static_cast<__nv_bfloat16 *>(c->vpools[layer]);
+    a.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    a.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.starts = starts;
+    a.total = total;
+    a.tables = block_tables;
+    a.stride = bt_stride;
+    a.num_rows = num_rows;
+    a.lengths = lengths;
+    a.req_idx = req_idx;
+    a.R = R;
+    a.Hkv = c->Hkv;
+    a.d = c->d;
+    a.num_blocks = c->num_blocks;
+    a.sticky = c->ws.sticky;
+    return zp::launch_append_kv_chunk(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ZP_OK
+               : ZP_ERR_CUDA;
+}
+
+zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t q_stride,
+                              const int32_t *starts, int32_t total, const int32_t *block_tables,
+                              int32_t bt_stride, int32_t num_rows, const int32_t *lengths,
+                              const int32_t *req_idx, int32_t R, float scale, void *out,
+                              void *stream)
+{
+    NvtxRange nvtx("zp_paged_chunk_attn");
+    const zp_status st =
+        chunk_checks(c, layer, block_tables, bt_stride, num_rows, lengths, R, starts, total);
+    if (st != ZP_OK)
+        return st;
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) ||
+        !row_stride_ok(q_stride, static_cast<long long>(c->Hq) * c->d) || !std::isfinite(scale))
+        return ZP_ERR_INVALID_ARG;
+    if (R == 0 || total == 0)
+        return ZP_OK;
+    if (!on_device(c))
+        return ZP_ERR_INVALID_ARG;
+    zp::ChunkAttnArgs a{};
+    a.kmap = c->ws.kmaps + layer;
+    a.vmap = c->ws.vmaps + layer;
+    a.kpool = static_cast<const __nv_bfloat16 *>(c->kpools[layer]);
+    a.vpool = static_cast<const __nv_bfloat16 *>(c->vpools[layer]);
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.q_stride = q_stride;
+    a.starts = starts;
+    a.total = total;
+    a.tables = block_tables;
+    a.stride = bt_stride;
+    a.num_rows = num_rows;
+    a.lengths = lengths;
+    a.req_idx = req_idx;
+    a.R = R;
+    a.Hkv = c->Hkv;
+    a.Hq = c->Hq;
+    a.num_blocks = c->num_blocks;
+    a.logit_scale = scale * 1.4426950408889634f;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.sticky = c->ws.sticky;
+    return zp::launch_chunk_attn(a, c->d, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ZP_OK
+               : ZP_ERR_CUDA;
+}
+
+zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *starts,
+                          int32_t total, const void *target_probs, const void *draft_probs,
+                          int32_t prob_dtype, int32_t vocab, int64_t prob_stride,
+                          const float *accept_u, const float *sample_u, int32_t *lengths,
+                          int32_t num_rows, const int32_t *req_idx, int32_t R, int32_t *accepted,
+                          int32_t *next_tokens, void *stream)
+{
+    NvtxRange nvtx("zp_verify_draft");
+    if (!c || !tokens || !starts || !target_probs || !accept_u || !sample_u || !accepted ||
+        !next_tokens)
+        return ZP_ERR_INVALID_ARG;
+    if (R < 0 || R > c->max_requests || total < 0 || vocab < 1 || prob_stride < vocab ||
+        (lengths && num_rows < 1))
+        return ZP_ERR_INVALID_ARG;
+    if (prob_dtype != ZP_DTYPE_F32 && prob_dtype != ZP_DTYPE_BF16)
+        return ZP_ERR_UNSUPPORTED;
+    const size_t esz = prob_dtype == ZP_DTYPE_F32 ? 4 : 2;
+    if (!aligned(target_probs, esz) || !aligned(draft_probs, esz) || !aligned(tokens, 4) ||
+        !aligned(starts, 4) || !aligned(accept_u, 4) || !aligned(sample_u, 4) ||
+        !aligned(lengths, 4) || !aligned(accepted, 4) || !aligned(next_tokens, 4))
+        return ZP_ERR_INVALID_ARG;
+    if (R == 0 || total == 0)
+        return ZP_OK;
+    if (!on_device(c))
+        return ZP_ERR_INVALID_ARG;
+    zp::VerifyArgs a{};
+    a.tokens = tokens;
+    a.starts = starts;
+    a.total = total;
+    a.target = target_probs;
+    a.draft = draft_probs;
+    a.vocab = vocab;
+    a.prob_stride = prob_stride;
+    a.accept_u = accept_u;
+    a.sample_u = sample_u;
+    a.lengths = lengths;
+    a.num_rows = num_rows;
+    a.req_idx = req_idx;
+    a.R = R;
+    a.accepted = accepted;
+    a.next = next_tokens;
+    a.sticky = c->ws.sticky;
+    return zp::launch_verify_draft(a, prob_dtype == ZP_DTYPE_BF16,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? ZP_OK
                : ZP_ERR_CUDA;
 }

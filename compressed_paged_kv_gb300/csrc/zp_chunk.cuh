@@ -1,0 +1,103 @@
+// zp_chunk.cuh -- launch arguments and shared device code of the calls on a
+// ragged chunk of new tokens: K/V rows written into the cache
+// (zp_chunk_append.cu), attention over the cache (zp_chunk_attn.cu) and the
+// verification of drafted tokens (zp_verify.cu).  Internal: not part of the
+// C ABI.
+//
+// The chunk of request i is rows starts[i] .. starts[i+1]-1 of the packed
+// tensors; its last token is the last of the request's lengths[row] tokens.
+#pragma once
+
+#include "zp_internal.cuh"
+
+namespace zp {
+
+struct ChunkKvArgs {
+    __nv_bfloat16 *kpool, *vpool;
+    const __nv_bfloat16 *k_new, *v_new;
+    int64_t k_stride, v_stride;  // elements from a token to the next
+    const int32_t *starts;
+    int32_t total;
+    const int32_t *tables;
+    int32_t stride, num_rows;
+    const int32_t *lengths;
+    const int32_t *req_idx;
+    int32_t R, Hkv, d, num_blocks;
+    int32_t *sticky;
+};
+
+struct ChunkAttnArgs {
+    const CUtensorMap *kmap;
+    const CUtensorMap *vmap;
+    const __nv_bfloat16 *kpool, *vpool;
+    const __nv_bfloat16 *q;
+    int64_t q_stride;  // elements from a token to the next
+    const int32_t *starts;
+    int32_t total;
+    const int32_t *tables;
+    int32_t stride, num_rows;
+    const int32_t *lengths;
+    const int32_t *req_idx;
+    int32_t R, Hkv, Hq, num_blocks;
+    float logit_scale;  // scale * log2(e)
+    __nv_bfloat16 *out;
+    int32_t *sticky;
+};
+
+struct VerifyArgs {
+    const int32_t *tokens;
+    const int32_t *starts;
+    int32_t total;
+    const void *target, *draft;  // draft: null when the drafted tokens come without probabilities
+    int32_t vocab;
+    int64_t prob_stride;  // elements from a row to the next
+    const float *accept_u, *sample_u;
+    int32_t *lengths;  // null: not committed
+    int32_t num_rows;
+    const int32_t *req_idx;
+    int32_t R;
+    int32_t *accepted, *next;
+    int32_t *sticky;
+};
+
+cudaError_t launch_append_kv_chunk(const ChunkKvArgs &a, cudaStream_t s);
+cudaError_t launch_chunk_attn(const ChunkAttnArgs &a, int d, cudaStream_t s);
+cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+// One request's chunk: its first packed row, its tokens, its table row and
+// cached length.
+struct ChunkReq {
+    int first, n, row, len;
+};
+
+// Reads and checks request i: true with n >= 1 when it has work; an empty
+// chunk is no work (its row and length are not read), and one whose offsets,
+// row or length are out of range sets *bad.
+template <class Args>
+__device__ __forceinline__ bool chunk_request(const Args &a, int i, ChunkReq &c, bool *bad)
+{
+    *bad = false;
+    c.first = a.starts[i];
+    const int end = a.starts[i + 1];
+    c.n = end - c.first;
+    if (c.first < 0 || end < c.first || end > a.total) {
+        *bad = true;
+        return false;
+    }
+    if (c.n == 0)
+        return false;
+    c.row = a.req_idx ? a.req_idx[i] : i;
+    if (c.row < 0 || c.row >= a.num_rows) {
+        *bad = true;
+        return false;
+    }
+    c.len = a.lengths[c.row];
+    *bad = c.len < c.n || c.len > a.stride * kBlk;
+    return !*bad;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace zp

@@ -8,6 +8,7 @@ The functions keep the C names (``zp_cache_create``, ``zp_compress``,
 ``zp_compress_prefill``, ``zp_compress_prefill_workspace_size``, ``zp_global_redundancy``,
 ``zp_global_redundancy_gram``,
 ``zp_alloc_rows``, ``zp_release_rows``, ``zp_fork_rows``,
+``zp_append_kv_chunk``, ``zp_paged_chunk_attn``, ``zp_verify_draft``,
 ``zp_cache_status``, ``zp_cache_destroy``, ``zp_status_string``) and take raw integers (device pointers, a cudaStream_t
 as an int).  ``Cache`` wraps them for torch tensors: it reads ``data_ptr()``
 and the current stream, and keeps the pool tensors alive.
@@ -27,7 +28,11 @@ ERR_DEVICE_CHECK = -4
 ERR_CUDA = -5
 ERR_TIMEOUT = -6
 
+DTYPE_F32 = 0
+DTYPE_BF16 = 1
+
 P = ctypes.c_void_p
+I64 = ctypes.c_int64
 I32 = ctypes.c_int32
 
 
@@ -97,6 +102,14 @@ def lib():
         L.zp_release_rows.restype = I32
         L.zp_fork_rows.argtypes = [P, P, I32, I32, P, P, P, I32, P, P]
         L.zp_fork_rows.restype = I32
+        L.zp_append_kv_chunk.argtypes = [P, I32, P, I64, P, I64, P, I32, P, I32, I32, P, P, I32, P]
+        L.zp_append_kv_chunk.restype = I32
+        L.zp_paged_chunk_attn.argtypes = [P, I32, P, I64, P, I32, P, I32, I32, P, P, I32,
+                                          ctypes.c_float, P, P]
+        L.zp_paged_chunk_attn.restype = I32
+        L.zp_verify_draft.argtypes = [P, P, P, I32, P, P, I32, I32, I64, P, P, P, I32, P, I32, P,
+                                      P, P]
+        L.zp_verify_draft.restype = I32
         L.zp_global_redundancy.argtypes = [P, P, I32, I32, P, P, I32, P, P]
         L.zp_global_redundancy.restype = I32
         L.zp_global_redundancy_gram.argtypes = [P, P, I32, I32, P, P, I32, P, P]
@@ -209,6 +222,31 @@ def zp_fork_rows(handle, block_tables, bt_stride, num_rows, lengths, src_rows, d
                               P(src_rows), P(dst_rows), n, P(refcount), P(stream or None))
 
 
+def zp_append_kv_chunk(handle, layer, k_new, k_stride, v_new, v_stride, starts, total,
+                       block_tables, bt_stride, num_rows, lengths, req_idx, R, stream) -> int:
+    return lib().zp_append_kv_chunk(P(handle), layer, P(k_new), k_stride, P(v_new), v_stride,
+                                    P(starts), total, P(block_tables), bt_stride, num_rows,
+                                    P(lengths), P(req_idx or None), R, P(stream or None))
+
+
+def zp_paged_chunk_attn(handle, layer, q, q_stride, starts, total, block_tables, bt_stride,
+                        num_rows, lengths, req_idx, R, scale, out, stream) -> int:
+    return lib().zp_paged_chunk_attn(P(handle), layer, P(q), q_stride, P(starts), total,
+                                     P(block_tables), bt_stride, num_rows, P(lengths),
+                                     P(req_idx or None), R, float(scale), P(out),
+                                     P(stream or None))
+
+
+def zp_verify_draft(handle, tokens, starts, total, target_probs, draft_probs, prob_dtype, vocab,
+                    prob_stride, accept_u, sample_u, lengths, num_rows, req_idx, R, accepted,
+                    next_tokens, stream) -> int:
+    return lib().zp_verify_draft(P(handle), P(tokens), P(starts), total, P(target_probs),
+                                 P(draft_probs or None), prob_dtype, vocab, prob_stride,
+                                 P(accept_u), P(sample_u), P(lengths or None), num_rows,
+                                 P(req_idx or None), R, P(accepted), P(next_tokens),
+                                 P(stream or None))
+
+
 def zp_global_redundancy(handle, block_tables, bt_stride, num_rows, lengths, req_idx, R, red_out,
                          stream) -> int:
     return lib().zp_global_redundancy(P(handle), P(block_tables), bt_stride, num_rows,
@@ -240,6 +278,27 @@ def _stream(stream):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _row_stride(t, what, inner, dtype):
+    """Elements between the rows of a packed tensor [total, *inner] whose rows
+    are each contiguous."""
+    n = 1
+    for dim, size in zip(reversed(range(1, t.dim())), reversed(inner)):
+        if t.shape[dim] != size or (t.stride(dim) != n and size > 1):
+            raise ValueError(f"{what} must be [total, {', '.join(map(str, inner))}] with "
+                             f"contiguous rows, got {tuple(t.shape)} strides {t.stride()}")
+        n *= size
+    if t.dim() != 1 + len(inner) or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{what} must be a {1 + len(inner)}-D {dtype} CUDA tensor")
+    return t.stride(0) if t.shape[0] > 1 else n
+
+
+def _ints(t, what, n, dtype=None):
+    import torch
+    dtype = dtype or torch.int32
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor of {n} elements")
 
 
 class Cache:
@@ -337,6 +396,90 @@ class Cache:
                           lengths.data_ptr(), _ptr(req_idx), k_new.shape[0], _stream(stream))
         if check and st != OK:
             raise ZpError(st, "zp_append_kv")
+        return st
+
+    def append_kv_chunk(self, layer, k_new, v_new, starts, block_tables, lengths, req_idx=None,
+                        stream=None, check=True):
+        """k_new, v_new: [total, Hkv, d] bf16, each token's row contiguous (a
+        slice of a packed projection output is passed as it is)."""
+        ks = _row_stride(k_new, "k_new", (self.Hkv, self.d), self.k_pools[0].dtype)
+        vs = _row_stride(v_new, "v_new", (self.Hkv, self.d), self.k_pools[0].dtype)
+        if k_new.shape[0] != v_new.shape[0]:
+            raise ValueError("k_new and v_new must hold the same tokens")
+        R = starts.numel() - 1
+        self._chunk_ints(starts, block_tables, lengths, req_idx, R)
+        st = zp_append_kv_chunk(self.handle, layer, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                                starts.data_ptr(), k_new.shape[0], block_tables.data_ptr(),
+                                block_tables.shape[1], block_tables.shape[0],
+                                lengths.data_ptr(), _ptr(req_idx), R, _stream(stream))
+        if check and st != OK:
+            raise ZpError(st, "zp_append_kv_chunk")
+        return st
+
+    def chunk_attn(self, layer, q, starts, block_tables, lengths, scale, out, req_idx=None,
+                   stream=None, check=True):
+        """q: [total, Hq, d] bf16, each token's row contiguous; out: the same
+        shape, contiguous."""
+        qs = _row_stride(q, "q", (self.Hq, self.d), self.k_pools[0].dtype)
+        _ints(out, "out", q.numel(), self.k_pools[0].dtype)
+        R = starts.numel() - 1
+        self._chunk_ints(starts, block_tables, lengths, req_idx, R)
+        st = zp_paged_chunk_attn(self.handle, layer, q.data_ptr(), qs, starts.data_ptr(),
+                                 q.shape[0], block_tables.data_ptr(), block_tables.shape[1],
+                                 block_tables.shape[0], lengths.data_ptr(), _ptr(req_idx), R,
+                                 scale, out.data_ptr(), _stream(stream))
+        if check and st != OK:
+            raise ZpError(st, "zp_paged_chunk_attn")
+        return st
+
+    def _chunk_ints(self, starts, block_tables, lengths, req_idx, R):
+        _ints(starts, "starts", 1)
+        _ints(block_tables, "block_tables", 1)
+        rows = block_tables.shape[0]
+        _ints(lengths, "lengths", rows)
+        if req_idx is not None:
+            _ints(req_idx, "req_idx", R)
+        elif R > rows:
+            raise ValueError(f"{R} chunks for {rows} table rows")
+
+    def verify_draft(self, tokens, starts, target_probs, accept_u, sample_u, accepted,
+                     next_tokens, draft_probs=None, lengths=None, req_idx=None, stream=None,
+                     check=True):
+        """target_probs, draft_probs: [total, vocab] fp32 or bf16 with the same
+        row stride."""
+        import torch
+        if target_probs.dim() != 2:
+            raise ValueError("target_probs must be [total, vocab]")
+        total, vocab = target_probs.shape
+        dtype = target_probs.dtype
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("target_probs must be float32 or bfloat16")
+        ps = _row_stride(target_probs, "target_probs", (vocab,), dtype)
+        if draft_probs is not None:
+            ds = _row_stride(draft_probs, "draft_probs", (vocab,), dtype)
+            if draft_probs.shape[0] != total or (total > 1 and ds != ps):
+                raise ValueError("draft_probs must have target_probs' rows and row stride")
+        R = starts.numel() - 1
+        _ints(starts, "starts", 1)
+        _ints(tokens, "tokens", total)
+        _ints(accept_u, "accept_u", total, torch.float32)
+        _ints(sample_u, "sample_u", R, torch.float32)
+        _ints(accepted, "accepted", R)
+        _ints(next_tokens, "next_tokens", R)
+        rows = 0
+        if lengths is not None:
+            rows = lengths.numel()
+            _ints(lengths, "lengths", R if req_idx is None else 1)
+            if req_idx is not None:
+                _ints(req_idx, "req_idx", R)
+        st = zp_verify_draft(self.handle, tokens.data_ptr(), starts.data_ptr(), total,
+                             target_probs.data_ptr(), _ptr(draft_probs),
+                             DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16, vocab, ps,
+                             accept_u.data_ptr(), sample_u.data_ptr(), _ptr(lengths), rows,
+                             _ptr(req_idx), R, accepted.data_ptr(), next_tokens.data_ptr(),
+                             _stream(stream))
+        if check and st != OK:
+            raise ZpError(st, "zp_verify_draft")
         return st
 
     def alloc_rows(self, block_tables, lengths, counts, free_ids, free_count, refcount,

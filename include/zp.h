@@ -59,6 +59,10 @@ typedef int32_t zp_status;
 #define ZP_ERR_CUDA (-5)          /* a CUDA runtime call failed */
 #define ZP_ERR_TIMEOUT (-6)       /* a bounded device-side wait gave up */
 
+/* Element types of probability rows (zp_verify_draft). */
+#define ZP_DTYPE_F32 0
+#define ZP_DTYPE_BF16 1
+
 typedef struct zp_cache zp_cache;
 
 /* Shape of the cache and the caller's per-layer pools.
@@ -373,6 +377,114 @@ zp_status zp_fork_rows(zp_cache *cache, int32_t *block_tables, int32_t bt_stride
 zp_status zp_append_kv(zp_cache *cache, int32_t layer, const void *k_new, const void *v_new,
                        const int32_t *block_tables, int32_t bt_stride, int32_t num_rows,
                        const int32_t *lengths, const int32_t *req_idx, int32_t R, void *stream);
+
+/* ------------------------------------------------- chunks of new tokens
+ * The three calls below take a ragged batch of chunks: a prompt, a piece of
+ * one, or the tokens of a speculative step (the last accepted token and the
+ * drafted ones).  Request i brings n_i = starts[i+1] - starts[i] tokens,
+ * packed one request after the other: its chunk is rows starts[i] ..
+ * starts[i+1]-1 of every packed tensor of `total` rows.
+ *
+ *  starts        device int32 [R + 1], 0 <= starts[0] <= ... <= starts[R] <=
+ *                total.  An empty chunk (n_i = 0) is skipped and its row not
+ *                looked at, so a padded batch repeats the last offset; packed
+ *                rows of no chunk are not read as tokens and their outputs not
+ *                written
+ *  total         packed rows of the tensors (their allocation's bound)
+ *  lengths       device int32 [num_rows]: the tokens of the row INCLUDING the
+ *                chunk, n_i <= lengths[row] <= bt_stride * b; token j of the
+ *                chunk is at position lengths[row] - n_i + j.  Blocks for them
+ *                are reserved before: zp_alloc_rows for a whole prompt,
+ *                zp_append_slots once per token of a speculative step.  A
+ *                prompt computed in pieces passes its progress here, an array
+ *                of the caller's own, not the length it was reserved with.
+ *  row strides   in elements, between the rows of consecutive tokens: at least
+ *                a row, a multiple of 8 (the q, k and v of one packed
+ *                projection output are passed as they lie)
+ * Offsets, rows, lengths or block ids out of range are recorded as
+ * ZP_ERR_DEVICE_CHECK in the sticky status; such a request is skipped (a bad
+ * block id: its outputs are undefined, its row is not written). */
+
+/* Writes one layer's keys and values of the chunks into their slots ("Paged
+ * KV cache and continuous batching for LLMs", "How it works"): the many-token
+ * form of zp_append_kv.  Blocks other rows share must have been replaced
+ * before (zp_append_slots does); the rows of the batch are distinct.
+ *
+ *  k_new, v_new  device bf16 [total][num_kv_heads][head_dim], 16-byte aligned,
+ *                tokens k_stride / v_stride elements apart
+ *  block_tables, req_idx  as in zp_append_kv (read only) */
+zp_status zp_append_kv_chunk(zp_cache *cache, int32_t layer, const void *k_new, int64_t k_stride,
+                             const void *v_new, int64_t v_stride, const int32_t *starts,
+                             int32_t total, const int32_t *block_tables, int32_t bt_stride,
+                             int32_t num_rows, const int32_t *lengths, const int32_t *req_idx,
+                             int32_t R, void *stream);
+
+/* Attention of the chunks over the paged cache, causal: for token j of chunk
+ * i and query head hq (kv head hq / (Hq/Hkv)),
+ *     out = sum_t softmax_t(scale * q . k_t) v_t,   t <= lengths[row] - n_i + j,
+ * with fp32 statistics and accumulation and one round-to-nearest-even to bf16
+ * (the probabilities are rounded to bf16 for the product with V).  The
+ * chunk's own keys and values are read from the cache: zp_append_kv_chunk
+ * comes before.  The many-query form of zp_paged_decode_attn, for any n_i from
+ * one token to a whole prompt, mixed in one batch.  Keys and values a token
+ * does not see do not change its output, whatever bits they hold; an output
+ * element whose token sees a value element that is not finite is not finite.
+ *
+ *  q             device bf16 [total][Hq][d], 16-byte aligned, tokens q_stride
+ *                elements apart
+ *  block_tables, req_idx  as in zp_paged_decode_attn (read only)
+ *  out           device bf16 [total][Hq][d], contiguous, 16-byte aligned */
+zp_status zp_paged_chunk_attn(zp_cache *cache, int32_t layer, const void *q, int64_t q_stride,
+                              const int32_t *starts, int32_t total, const int32_t *block_tables,
+                              int32_t bt_stride, int32_t num_rows, const int32_t *lengths,
+                              const int32_t *req_idx, int32_t R, float scale, void *out,
+                              void *stream);
+
+/* Verifies drafted tokens against the target model's probabilities, from
+ * given random numbers (speculative sampling: the tokens kept are distributed
+ * as the target's).  Chunk i holds the request's last accepted token and
+ * then its drafted ones; packed row starts[i] + j of target_probs (p) is the
+ * target's distribution after token j, so it judges token j + 1, and the same
+ * row of draft_probs (q) the one token j + 1 was drafted from:
+ *     token x = tokens[starts[i] + j + 1] is accepted when all drafted tokens
+ *     before it are and  accept_u[starts[i] + j] * q(x) < p(x)
+ *     (q(x) = 1 when draft_probs is NULL: tokens proposed without
+ *     probabilities);
+ *     accepted[i] = the number accepted, a, 0 <= a < n_i;
+ *     next_tokens[i] is drawn from the weights of row starts[i] + a:
+ *     max(p - q, 0) where token a + 1 was rejected (p with the rejected token
+ *     left out when draft_probs is NULL), p where every drafted token was
+ *     accepted: the lowest index whose running sum exceeds sample_u[i] times
+ *     the sum of all weights.
+ * The products and sums are formed in more than 32 bits and in a fixed order.
+ * Weights need not sum to 1; one that is not a positive finite number (a NaN
+ * among them) counts as zero.  A rejected row with no weight left (p <= q
+ * everywhere, by rounding) is drawn from p instead.  With `lengths` the
+ * rejected tokens leave the cache: lengths[row] -= n_i - 1 - a (their blocks
+ * stay reserved for the row).  A request with an empty chunk is skipped: its
+ * outputs and length are not written.
+ *
+ *  tokens        device int32 [total]; tokens[starts[i]] is not read
+ *  target_probs  device [total][vocab] of prob_dtype, rows prob_stride
+ *                elements apart (any, >= vocab)
+ *  draft_probs   NULL or the same layout; the last row of a chunk is not read
+ *  prob_dtype    ZP_DTYPE_F32 or ZP_DTYPE_BF16
+ *  accept_u      device fp32 [total], in [0, 1); the last of a chunk is not read
+ *  sample_u      device fp32 [R], in [0, 1)
+ *  lengths       NULL, or device int32 [num_rows], n_i <= lengths[row], in/out
+ *  req_idx       device int32 [R] distinct rows, or NULL for rows 0..R-1;
+ *                only read with lengths
+ *  accepted, next_tokens  device int32 [R]
+ * Offsets out of range (nothing is written), a row or length out of range (the
+ * length is not written), a drafted token outside [0, vocab) (counted as
+ * rejected, next_tokens -1), or a row without any weight (next_tokens -1) are
+ * recorded as ZP_ERR_DEVICE_CHECK in the sticky status. */
+zp_status zp_verify_draft(zp_cache *cache, const int32_t *tokens, const int32_t *starts,
+                          int32_t total, const void *target_probs, const void *draft_probs,
+                          int32_t prob_dtype, int32_t vocab, int64_t prob_stride,
+                          const float *accept_u, const float *sample_u, int32_t *lengths,
+                          int32_t num_rows, const int32_t *req_idx, int32_t R, int32_t *accepted,
+                          int32_t *next_tokens, void *stream);
 
 /* Redundancy of every key against ALL keys of its (request, layer, kv
  * head): the O(N^2 b^2) score that the Lightning Redundancy Score replaces
