@@ -157,6 +157,8 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     const size_t o_ap_occ = A.take(4 * static_cast<size_t>(D.num_blocks));
     const size_t o_ap_last = A.take(4 * static_cast<size_t>(D.num_blocks));
     const size_t o_ap_plan = A.take(16 * static_cast<size_t>(D.max_requests));
+    const size_t o_ca_arr = A.take(8 * static_cast<size_t>(c->num_sms));
+    const size_t o_ca_part = A.take(4 * zp::chunk_attn_part_floats(D.head_dim, c->num_sms));
     const size_t total = A.take(0);
 
     if (cudaMalloc(&c->base, total) != cudaSuccess) {
@@ -190,6 +192,8 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     ws.ap_occ = reinterpret_cast<int32_t *>(b + o_ap_occ);
     ws.ap_last = reinterpret_cast<int32_t *>(b + o_ap_last);
     ws.ap_plan = reinterpret_cast<int4 *>(b + o_ap_plan);
+    ws.ca_arrived = reinterpret_cast<uint32_t *>(b + o_ca_arr);
+    ws.ca_part = reinterpret_cast<float *>(b + o_ca_part);
     c->kpools.assign(D.k_pools, D.k_pools + D.num_layers);
     c->vpools.assign(D.v_pools, D.v_pools + D.num_layers);
 
@@ -206,6 +210,7 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     ok = ok && cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
          cudaMemset(b + o_rowmark, 0, 4 * static_cast<size_t>(D.max_requests)) == cudaSuccess &&
          cudaMemset(b + o_ap_call, 0, o_ap_occ - o_ap_call) == cudaSuccess &&
+         cudaMemset(b + o_ca_arr, 0, 8 * static_cast<size_t>(c->num_sms)) == cudaSuccess &&
          cudaMemcpy(ws.kmaps, kmaps.data(), sizeof(CUtensorMap) * D.num_layers,
                     cudaMemcpyHostToDevice) == cudaSuccess &&
          cudaMemcpy(ws.vmaps, vmaps.data(), sizeof(CUtensorMap) * D.num_layers,
@@ -848,10 +853,8 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     zp::ChunkAttnArgs a{};
     a.kmap = c->ws.kmaps + layer;
     a.vmap = c->ws.vmaps + layer;
-    a.kpool = static_cast<const __nv_bfloat16 *>(c->kpools[layer]);
-    a.vpool = static_cast<const __nv_bfloat16 *>(c->vpools[layer]);
-    a.q = static_cast<const __nv_bfloat16 *>(q);
-    a.q_stride = q_stride;
+    if (!zp::encode_chunk_q_map(&a.qmap, q, total, q_stride, c->Hq, c->Hq / c->Hkv, c->d))
+        return ZP_ERR_UNSUPPORTED;
     a.starts = starts;
     a.total = total;
     a.tables = block_tables;
@@ -865,8 +868,11 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     a.num_blocks = c->num_blocks;
     a.logit_scale = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16 *>(out);
+    a.part = c->ws.ca_part;
+    a.arrived = c->ws.ca_arrived;
     a.sticky = c->ws.sticky;
-    return zp::launch_chunk_attn(a, c->d, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return zp::launch_chunk_attn(a, c->d, c->num_sms, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
                ? ZP_OK
                : ZP_ERR_CUDA;
 }
@@ -929,6 +935,10 @@ zp_status zp_cache_status(zp_cache *c, void *stream, int32_t *out_status)
     if (cudaMemcpyAsync(&v, c->ws.sticky, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaMemsetAsync(c->ws.sticky, 0, 4, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
+        return ZP_ERR_CUDA;
+    // a chunk attention that gave up waiting may have left its arrivals uncounted
+    if (v == ZP_ERR_TIMEOUT &&
+        cudaMemsetAsync(c->ws.ca_arrived, 0, 8 * static_cast<size_t>(c->num_sms), s) != cudaSuccess)
         return ZP_ERR_CUDA;
     *out_status = v;
     return ZP_OK;

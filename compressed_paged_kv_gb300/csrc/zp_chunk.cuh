@@ -29,9 +29,7 @@ struct ChunkKvArgs {
 struct ChunkAttnArgs {
     const CUtensorMap *kmap;
     const CUtensorMap *vmap;
-    const __nv_bfloat16 *kpool, *vpool;
-    const __nv_bfloat16 *q;
-    int64_t q_stride;  // elements from a token to the next
+    CUtensorMap qmap;  // q as [total][Hq][d]: boxes of 64 dims x a group's heads x a tile's tokens
     const int32_t *starts;
     int32_t total;
     const int32_t *tables;
@@ -41,6 +39,8 @@ struct ChunkAttnArgs {
     int32_t R, Hkv, Hq, num_blocks;
     float logit_scale;  // scale * log2(e)
     __nv_bfloat16 *out;
+    float *part;        // partial results of the items cut between CTAs
+    uint32_t *arrived;  // [2 * SMs] of them that are written; 0 between calls
     int32_t *sticky;
 };
 
@@ -61,7 +61,12 @@ struct VerifyArgs {
 };
 
 cudaError_t launch_append_kv_chunk(const ChunkKvArgs &a, cudaStream_t s);
-cudaError_t launch_chunk_attn(const ChunkAttnArgs &a, int d, cudaStream_t s);
+cudaError_t launch_chunk_attn(const ChunkAttnArgs &a, int d, int sms, cudaStream_t s);
+// Floats of ChunkAttnArgs::part for a GPU of `sms` SMs.
+size_t chunk_attn_part_floats(int d, int sms);
+// The map ChunkAttnArgs::qmap of a packed q (tokens `stride` elements apart).
+bool encode_chunk_q_map(CUtensorMap *map, const void *q, int total, int64_t stride, int Hq, int G,
+                        int d);
 cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, cudaStream_t s);
 
 #ifdef __CUDACC__
@@ -76,7 +81,7 @@ struct ChunkReq {
 // chunk is no work (its row and length are not read), and one whose offsets,
 // row or length are out of range sets *bad.
 template <class Args>
-__device__ __forceinline__ bool chunk_request(const Args &a, int i, ChunkReq &c, bool *bad)
+__host__ __device__ __forceinline__ bool chunk_request(const Args &a, int i, ChunkReq &c, bool *bad)
 {
     *bad = false;
     c.first = a.starts[i];

@@ -50,6 +50,9 @@ struct Workspace {
     int32_t *ap_occ;      // [num_blocks] writers of a block in this call
     int32_t *ap_last;     // [num_blocks] last writer of a block in this call
     int4 *ap_plan;        // [max_requests] tail block, fresh block, rows to copy, trigger slot
+    // chunk attention (zp_paged_chunk_attn) keeps its own
+    float *ca_part;       // partial results of the work items cut between SMs
+    uint32_t *ca_arrived; // [2 * SMs] of them that are written; 0 between calls
 };
 
 // ------------------------------------------------------------ launch args
