@@ -843,7 +843,7 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         chunk_checks(c, layer, block_tables, bt_stride, num_rows, lengths, R, starts, total);
     if (st != ZP_OK)
         return st;
-    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) ||
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 32) ||
         !row_stride_ok(q_stride, static_cast<long long>(c->Hq) * c->d) || !std::isfinite(scale))
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)

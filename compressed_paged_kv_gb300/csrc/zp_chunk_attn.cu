@@ -49,12 +49,28 @@ namespace zp {
 namespace {
 
 constexpr int kTile = 128;             // query rows a tile, keys a tile
-constexpr int kCaThreads = 384;
+constexpr int kSmWarps = 8;            // softmax warps a query tile
+constexpr int kCaThreads = (2 * kSmWarps + 4) * 32;
+constexpr int kSmRegs = 104, kOtherRegs = 64;  // registers a thread after the split
+static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4),
+              "the split draws on the registers of the launch");
 constexpr int kItemCost = 128;         // an item's fixed cost, in keys
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
 constexpr int kMaxSpan = 30;           // CTAs an item is cut over, about (a lane each joins them)
+constexpr int kMmaWarp = 2 * kSmWarps + 1;
 constexpr int kTmemCols = 512;         // S/P of A, of B; O of A, of B
 constexpr float kRescale = 8.f;        // log2 of the growth that rescales O
+
+// What every CTA works out at its start.
+struct CaPlan {
+    long long cost;   // of all items
+    long long share;  // of a CTA
+    long long lo, hi; // this CTA's share
+    long long x0;     // cost before request i0
+    ChunkReq c0;      // the request `lo` falls into
+    int i0;
+    int ctas;         // CTAs with a share
+};
 
 template <int D>
 struct CaSmem {
@@ -62,31 +78,22 @@ struct CaSmem {
     static constexpr int PANEL = kTile * 128;            // bytes of 128 rows of 64 dims
     static constexpr int TILE = PANELS * PANEL;
     static constexpr int NS = D == 128 ? 5 : 10;         // K/V ring stages
-    static constexpr int XC = D / 4;                     // columns a round of the halves' join
+    static constexpr int XC = D / 4;                     // columns of O a step of the epilogue
     static constexpr int off_q = 0;                      // Q of A, Q of B
     static constexpr int off_ring = off_q + 2 * TILE;
-    static constexpr int off_bad = off_ring + NS * TILE;  // int [3][D]: cleared positions
-    static constexpr int off_flag = off_bad + 3 * D * 4;  // int [3]; [3]: unused
+    static constexpr int off_max = off_ring + NS * TILE;  // float [2][2][128]: maxima of row halves
+    static constexpr int off_flag = off_max + 4 * kTile * 4;  // int [2][2]: elements were cleared
     static constexpr int off_plan = off_flag + 16;        // CaPlan
-    static constexpr int off_scan = off_plan + 64;        // int64 [12]
-    static constexpr int off_bar = off_scan + 96;
-    // full[NS], empty[NS], dirty[NS], clean[NS], Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull,
-    // Qempty, done
-    static constexpr int NBAR = 4 * NS + 8 + 3;
+    static constexpr int off_scan = off_plan + 80;        // int64 [warps]
+    static constexpr int off_bar = off_scan + kCaThreads / 32 * 8;
+    // full[NS], empty[NS], Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull[2], Qempty[2], dirty,
+    // clean, half, done
+    static constexpr int NBAR = 2 * NS + 12 + 4;
     static constexpr int off_tmem = off_bar + NBAR * 8;
     static constexpr int off_last = off_tmem + 8;         // int [2]
     static constexpr int BYTES = off_last + 8;
-    static constexpr int ALLOC = BYTES + 1024;
-    static_assert(ALLOC <= 232448, "shared memory of a CTA");
-};
-
-// What every CTA works out at its start.
-struct CaPlan {
-    long long cost;   // of all items
-    long long lo, hi; // this CTA's share
-    long long x0;     // cost before request i0
-    int ctas;         // CTAs with a share
-    int i0;           // the request `lo` falls into
+    static_assert(sizeof(CaPlan) <= 80 && off_bar % 8 == 0, "layout");
+    static_assert(BYTES <= 232448, "shared memory of a CTA");
 };
 
 struct CaItem {
@@ -130,9 +137,32 @@ __host__ __device__ __forceinline__ int cut_tile(long long x, int kt)
     return k < kt ? static_cast<int>(k) : kt;
 }
 
+// n / d for n >= 0, d > 0: 32-bit where it can be (a 64-bit division is slow).
+__host__ __device__ __forceinline__ long long quotient(long long n, long long d)
+{
+    if (((n | d) >> 32) == 0)
+        return static_cast<uint32_t>(n) / static_cast<uint32_t>(d);
+    return n / d;
+}
+
 __host__ __device__ __forceinline__ long long share_border(const CaPlan &pl, int b)
 {
-    return pl.cost * b / pl.ctas;
+    const long long x = pl.share * b;
+    return x < pl.cost ? x : pl.cost;
+}
+
+// Shares over at most `grid` CTAs: none below kMinShare (about), and no item
+// over more than kMaxSpan + 2 of them.
+__host__ __device__ __forceinline__ void make_shares(CaPlan &pl, long long cost, int longest, int grid)
+{
+    const float span = kMaxSpan * (static_cast<float>(cost) / (longest + kItemCost));
+    const long long most = cost / kMinShare;
+    int ctas = most < grid ? static_cast<int>(most) : grid;
+    if (span < ctas)
+        ctas = static_cast<int>(span);
+    pl.cost = cost;
+    pl.ctas = ctas < 1 ? 1 : ctas;
+    pl.share = quotient(cost + pl.ctas - 1, pl.ctas);
 }
 
 // Walks this CTA's items; every role walks the same ones on its own.
@@ -154,27 +184,34 @@ struct CaWalk {
         it.kb = it.x + it.w > pl.hi ? cut_tile(pl.hi - it.x, it.kt) : it.kt;
     }
 
+    __host__ __device__ __forceinline__ void entered(int i)
+    {
+        it.i = i;
+        it.pairs = pair_count(it.c.n, tpt);
+        it.span = head_cost(it.c, tpt);
+    }
+
     __host__ __device__ __forceinline__ bool request(int i)
     {
         bool bad;
         for (; i < a.R; ++i)
             if (chunk_request(a, i, it.c, &bad))
                 break;
-        it.i = i;
         if (i >= a.R)
             return false;
-        it.pairs = pair_count(it.c.n, tpt);
-        it.span = head_cost(it.c, tpt);
+        entered(i);
         return true;
     }
 
     // The first item of the share; false when there is none.
     __host__ __device__ __forceinline__ bool begin()
     {
-        if (pl.lo >= pl.hi || !request(pl.i0))
+        if (pl.lo >= pl.hi)
             return false;
+        it.c = pl.c0;
+        entered(pl.i0);
         const long long off = pl.lo - pl.x0;
-        it.h = static_cast<int>(off / it.span);
+        it.h = static_cast<int>(quotient(off, it.span));
         const long long rem = off - it.h * it.span;
         int p0 = 0, p1 = it.pairs - 1;
         while (p0 < p1) {  // the last pair that begins at or before the border
@@ -328,6 +365,24 @@ __device__ __forceinline__ void st_wait()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  The instructions that take uniform
+// registers (products, tensor copies) issue back to back only where the
+// compiler knows that a single lane runs them.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
+// A converged warp's bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -352,6 +407,22 @@ __device__ __forceinline__ void add2(float &x, float &y, float u, float v)
         : "f"(u), "f"(v));
 }
 
+// The positions of cleared value elements of a CTA's items, behind the slots
+// of the partial results: int [2][D], written only when there are some.
+template <int D>
+__device__ __forceinline__ int *cleared_ptr(float *part)
+{
+    return reinterpret_cast<int *>(part + static_cast<size_t>(2 * gridDim.x) * (2 * kTile * (D + 2))) +
+           static_cast<size_t>(blockIdx.x) * 2 * D;
+}
+
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // The workspace slot of a partial result: O [256][D], then (max, sum) [256].
 template <int D>
 __device__ __forceinline__ float *slot_ptr(float *part, int slot)
@@ -363,7 +434,7 @@ __device__ __forceinline__ float *slot_ptr(float *part, int slot)
 
 size_t chunk_attn_part_floats(int d, int sms)
 {
-    return static_cast<size_t>(2 * sms) * 2 * kTile * (d + 2);
+    return static_cast<size_t>(2 * sms) * (2 * kTile * (d + 2) + d);
 }
 
 template <int D>
@@ -372,18 +443,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 {
     using S = CaSmem<D>;
     constexpr int PANELS = S::PANELS, NS = S::NS, XC = S::XC;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    extern __shared__ __align__(1024) uint8_t smem_aligned[];
+    uint8_t *sm = smem_aligned;
+    if (smem_u32(sm) & 1023u) {  // the swizzled tiles need it
+        if (threadIdx.x == 0)
+            set_error(a.sticky, ZP_ERR_UNSUPPORTED);
+        return;
+    }
     uint8_t *sQ = sm + S::off_q, *ring = sm + S::off_ring;
-    int *sBad = reinterpret_cast<int *>(sm + S::off_bad);
+    float *sMax = reinterpret_cast<float *>(sm + S::off_max);
     int *sFlag = reinterpret_cast<int *>(sm + S::off_flag);
     CaPlan &plan = *reinterpret_cast<CaPlan *>(sm + S::off_plan);
     long long *scan = reinterpret_cast<long long *>(sm + S::off_scan);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::off_bar);
-    uint64_t *empty = full + NS, *dirty = empty + NS, *clean = dirty + NS;
-    uint64_t *sfull = clean + NS, *pready = sfull + 2, *ofull = pready + 2, *oempty = ofull + 2;
-    uint64_t *qfull = oempty + 2, *qempty = qfull + 1, *done = qempty + 1;
+    uint64_t *empty = full + NS, *sfull = empty + NS, *pready = sfull + 2, *ofull = pready + 2;
+    uint64_t *oempty = ofull + 2, *qfull = oempty + 2, *qempty = qfull + 2;
+    uint64_t *dirty = qempty + 2, *clean = dirty + 1, *half = clean + 1, *done = half + 1;
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sm + S::off_tmem);
     int *sLast = reinterpret_cast<int *>(sm + S::off_last);
 
@@ -394,22 +469,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&dirty[s], 1);
-            mbar_init(&clean[s], 2);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sfull[x], 1);
-            mbar_init(&pready[x], 4);
+            mbar_init(&pready[x], kSmWarps);
             mbar_init(&ofull[x], 1);
-            mbar_init(&oempty[x], 4);
+            mbar_init(&oempty[x], kSmWarps);
+            mbar_init(&qfull[x], 1);
+            mbar_init(&qempty[x], 2);  // its last S, and A's word that nothing else uses it
         }
-        mbar_init(qfull, 1);
-        // the item's last S, the join of a single item's halves, the two cleaners
-        mbar_init(qempty, 4);
+        mbar_init(dirty, 1);
+        mbar_init(clean, 2);
+        mbar_init(half, kSmWarps);
         mbar_init(done, 1);
         fence_mbar_init();
     }
-    if (wi == 9) {
+    if (wi == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(sTmem)),
                      "r"(kTmemCols)
@@ -457,34 +532,21 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 before += scan[w];
             cost += scan[w];
         }
-        const long long wmax = sLast[0] + kItemCost;
-        int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), cost / kMinShare));
-        if (cost > 0)
-            ctas = static_cast<int>(min(static_cast<long long>(ctas), kMaxSpan * cost / wmax));
-        ctas = max(ctas, 1);
         CaPlan p;
-        p.cost = cost;
-        p.ctas = ctas;
-        p.lo = p.hi = cost;
-        p.x0 = 0;
-        p.i0 = a.R;
-        if (static_cast<int>(blockIdx.x) < ctas) {
-            p.lo = share_border(p, blockIdx.x);
-            p.hi = share_border(p, blockIdx.x + 1);
-        }
+        make_shares(p, cost, sLast[0], static_cast<int>(gridDim.x));
+        p.lo = share_border(p, blockIdx.x);
+        p.hi = share_border(p, blockIdx.x + 1);
         if (tid == 0 && p.lo >= p.hi)
             plan = p;
-        if (p.lo < p.hi && before <= p.lo && p.lo < before + mine) {
+        if (before <= p.lo && p.lo < before + mine) {
             for (int i = r0; i < r1; ++i) {  // the request the share begins in
-                ChunkReq c;
                 bool bad;
-                if (!chunk_request(a, i, c, &bad))
+                if (!chunk_request(a, i, p.c0, &bad))
                     continue;
-                const long long w = a.Hkv * head_cost(c, tpt);
-                if (p.lo < before + w) {
-                    p.i0 = i;
+                p.i0 = i;
+                const long long w = a.Hkv * head_cost(p.c0, tpt);
+                if (p.lo < before + w)
                     break;
-                }
                 before += w;
             }
             p.x0 = before;
@@ -497,15 +559,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const uint32_t tmem = *sTmem;
     bool bad = false;
 
-    if (wi >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (wi >= 2 * kSmWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         CaWalk wk{a, plan, tpt, {}};
-        if (wi == 8) {
+        if (wi == kMmaWarp - 1) {
             // ----------------------------------------------------- producer
-            uint32_t pos = 0, items = 0;
+            uint32_t loaded = 0, cur = 0, par = 0, qs = 0;  // ring cursor and parity, query tiles
             for (bool more = wk.begin(); more && !bad; more = wk.next()) {
                 const CaItem &it = wk.it;
-                const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
+                const int len = it.kb - it.ka;
                 const int32_t *trow = a.tables + (size_t)it.c.row * a.stride;
                 const int nblk = (it.c.len + kBlk - 1) / kBlk;
                 // pool row of a cache block of this kv head, negative past the
@@ -523,51 +585,36 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 // ids of four key tiles at a time, a lane a block, the next four ahead
                 int ids = block_y(it.ka * 8 + lane);
                 int ids_next = len > 4 ? block_y((it.ka + 4) * 8 + lane) : 0;
-                if (lane == 0)
-                    bad = items > 0 && !mbar_wait(qempty, (items - 1) & 1);
-                bad = __shfl_sync(0xffffffffu, bad, 0);
-                if (bad)
-                    break;
-                const int tiles = it.single ? 1 : 2;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(qfull, tiles * PANELS * G * tpt * 128);
-                __syncwarp();
-                if (lane < tiles * PANELS) {
-                    const int x = lane / PANELS, p = lane % PANELS;
-                    asm volatile(
-                        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx"
-                        "::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                            smem_u32(sQ + x * S::TILE + p * S::PANEL)),
-                        "l"(&a.qmap), "r"(p * 64), "r"(it.h * G), "r"(it.c.first + it.tok0 + x * tpt),
-                        "r"(smem_u32(qfull))
-                        : "memory");
-                }
-                ++items;
                 int base = 0;  // key tile `ids` begins at
                 auto stage = [&](int t, bool v) {
-                    const int s = pos % NS;
-                    if (lane == 0) {
-                        bad = pos >= NS && !mbar_wait(&empty[s], (pos / NS - 1) & 1);
-                        if (!bad) {
-                            mbar_arrive_expect_tx(&full[s], S::TILE);
-                            // a V tile to be cleaned: the cleaners may not look at the
-                            // stage's `full` before it stands at this load
-                            if (v && (it.ka + t + 1) * kTile > pos0 + 1)
-                                mbar_arrive(&dirty[s]);
-                        }
-                    }
-                    bad = __shfl_sync(0xffffffffu, bad, 0);
-                    if (bad)
+                    if (loaded >= NS && !warp_wait(&empty[cur], par ^ 1)) {
+                        bad = true;
                         return;
+                    }
                     // a V tile may lie one group behind the K tile loaded before it
-                    const int q = lane / PANELS, p = lane % PANELS;
-                    const int src = (t - base) * 8 + (q & 7);
-                    const int y0 = __shfl_sync(0xffffffffu, ids, src & 31);
-                    const int y1 = __shfl_sync(0xffffffffu, ids_next, src & 31);
-                    if (lane < 8 * PANELS)
-                        tma_load_2d(ring + s * S::TILE + p * S::PANEL + q * kBlk * 128,
-                                    v ? a.vmap : a.kmap, p * 64, src < 32 ? y0 : y1, &full[s]);
-                    ++pos;
+                    const int src = (t - base) * 8;
+                    const int from = src < 32 ? ids : ids_next;
+                    int y[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        y[q] = __shfl_sync(0xffffffffu, from, (src & 31) + q);
+                    const CUtensorMap *map = v ? a.vmap : a.kmap;
+                    uint8_t *dst = ring + cur * S::TILE;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full[cur], S::TILE);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+#pragma unroll
+                            for (int p = 0; p < PANELS; ++p)
+                                tma_load_2d(dst + p * S::PANEL + q * kBlk * 128, map, p * 64, y[q],
+                                            &full[cur]);
+                    }
+                    __syncwarp();
+                    ++loaded;
+                    if (++cur == NS) {
+                        cur = 0;
+                        par ^= 1;
+                    }
                 };
                 auto advance = [&](int t) {  // V tile t is the oldest still to come
                     if (t - base >= 4) {
@@ -576,8 +623,31 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         ids_next = base + 4 < len ? block_y((it.ka + base + 4) * 8 + lane) : 0;
                     }
                 };
+                // the first K tile before Q: it does not wait for the item before
+                stage(0, false);
+                if (bad)
+                    break;
+                for (int x = 0; x < (it.single ? 1 : 2); ++x, ++qs) {
+                    const int j = qs & 1;
+                    if (qs >= 2 && !warp_wait(&qempty[j], ((qs >> 1) - 1) & 1)) {
+                        bad = true;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&qfull[j], PANELS * G * tpt * 128);
+#pragma unroll
+                        for (int p = 0; p < PANELS; ++p)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
+                                "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                    smem_u32(sQ + j * S::TILE + p * S::PANEL)),
+                                "l"(&a.qmap), "r"(p * 64), "r"(it.h * G),
+                                "r"(it.c.first + it.tok0 + x * tpt), "r"(smem_u32(&qfull[j]))
+                                : "memory");
+                    }
+                    __syncwarp();
+                }
                 if (it.single) {
-                    stage(0, false);
                     for (int t = 0; t < len && !bad; ++t) {
                         advance(t);
                         if (t + 1 < len)
@@ -588,241 +658,349 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 } else {
                     for (int t = 0; t < len && !bad; ++t) {
                         advance(t);
-                        stage(t, false);
+                        if (t > 0)
+                            stage(t, false);
                         if (!bad)
                             stage(t, true);
                     }
                 }
             }
             // every copy issued has landed before the CTA may exit
-            if (lane == 0) {
-                bool ok = items == 0 || mbar_wait(qfull, (items - 1) & 1);
-                for (uint32_t j = pos > NS ? pos - NS : 0; j < pos; ++j)
-                    ok &= mbar_wait(&full[j % NS], (j / NS) & 1);
-                bad |= !ok;
-            }
-        } else if (wi == 9) {
+            for (uint32_t j = qs > 2 ? qs - 2 : 0; j < qs; ++j)
+                bad |= !warp_wait(&qfull[j & 1], (j >> 1) & 1);
+            for (uint32_t j = loaded > NS ? loaded - NS : 0; j < loaded; ++j)
+                bad |= !warp_wait(&full[j % NS], (j / NS) & 1);
+        } else if (wi == kMmaWarp) {
             // ----------------------------------------------------- products
+            // The whole warp walks and waits; one lane issues.
             constexpr uint32_t ID_S = ca_idesc(kTile, false), ID_O = ca_idesc(D, true);
-            uint32_t base = 0, items = 0, cleaned = 0;  // cleaned: a parity bit a stage
-            uint32_t np[2] = {0u, 0u}, no[2] = {0u, 0u};
+            constexpr uint32_t STEP = S::TILE >> 4;
+            const uint64_t qdesc = ca_desc(smem_u32(sQ), 16), kdesc = ca_desc(smem_u32(ring), 16);
+            const uint64_t vdesc = ca_desc(smem_u32(ring), S::PANEL);
+            uint32_t qs = 0, cleaned = 0, items = 0;
+            uint32_t np[2] = {0u, 0u}, no[2] = {0u, 0u}, ow[2] = {0u, 0u};  // ow: Oempty waited for
+            uint32_t last_use[2] = {0u, 0u};  // the item that used O last
+            struct Cursor {  // a ring stage and the parity of its load
+                uint32_t s, par;
+                __device__ __forceinline__ void advance(uint32_t n)
+                {
+                    s += n;
+                    if (s >= NS) {
+                        s -= NS;
+                        par ^= 1;
+                    }
+                }
+            } base{0u, 0u};  // the item's first stage
             auto wait = [&](uint64_t *bar, uint32_t parity) {
-                if (!bad && !mbar_wait(bar, parity))
+                if (!bad && !warp_wait(bar, parity))
                     bad = true;
             };
             for (bool more = wk.begin(); more && !bad; more = wk.next()) {
                 const CaItem &it = wk.it;
                 const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
-                if (lane == 0) {
-                    const bool single = it.single;
-                    // A's key tiles of a pair: the ones its last token sees
-                    const int na = (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile;
-                    const int cnt[2] = {single ? (len + 1) / 2 : max(0, min(it.kb, na) - it.ka),
-                                        single ? len / 2 : len};
-                    auto kpos = [&](int t) {
-                        return base + (single ? (t ? 2 * t - 1 : 0) : 2 * t);
-                    };
-                    auto vpos = [&](int t) {
-                        return base + (single && t + 1 < len ? 2 * t + 2 : 2 * t + 1);
-                    };
-                    auto need = [&](uint32_t pos) { wait(&full[pos % NS], (pos / NS) & 1); };
-                    auto product_s = [&](int x, int t) {
-                        const uint32_t kb = smem_u32(ring + (kpos(t) % NS) * S::TILE);
-                        const uint32_t qb = smem_u32(sQ + (single ? 0 : x) * S::TILE);
-                        fence_after();
+                const bool single = it.single;
+                ++items;
+                // A's key tiles of a pair: the ones its last token sees
+                const int na = (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile;
+                const int cnt0 = single ? (len + 1) / 2 : max(0, min(it.kb, na) - it.ka);
+                // the next K and V tiles: a pair loads K0 V0 K1 V1 .., a single
+                // item K0 K1 V0 K2 V1 ..
+                Cursor kc = base, vc = base;
+                vc.advance(single && len > 1 ? 2 : 1);
+                int kn = 0, vn = 0;
+                auto k_done = [&] {  // K tile kn is read by the products issued
+                    if (elect_one())
+                        mma_commit(&empty[kc.s]);
+                    __syncwarp();
+                    kc.advance(single && kn == 0 ? 1 : 2);
+                    ++kn;
+                };
+                auto v_done = [&] {
+                    if (elect_one())
+                        mma_commit(&empty[vc.s]);
+                    __syncwarp();
+                    vc.advance(single && vn + 2 >= len ? 1 : 2);
+                    ++vn;
+                };
+                auto need_k = [&] { wait(&full[kc.s], kc.par); };
+                auto product_s = [&](int x) {  // S of tile x with K tile kn
+                    const uint64_t qd = qdesc + ((qs + (single ? 0 : x)) & 1) * STEP;
+                    const uint64_t kd = kdesc + kc.s * STEP;
+                    fence_after();
+                    if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t o = (ks >> 2) * S::PANEL + (ks & 3) * 32;
-                            mma_ss(tmem + x * kTile, ca_desc(qb + o, 16), ca_desc(kb + o, 16), ID_S,
-                                   ks > 0);
+                            const uint32_t o = ((ks >> 2) * S::PANEL + (ks & 3) * 32) >> 4;
+                            mma_ss(tmem + x * kTile, qd + o, kd + o, ID_S, ks > 0);
                         }
                         mma_commit(&sfull[x]);
-                    };
-                    auto product_o = [&](int x, int t, bool first, bool last) {
-                        wait(&pready[x], np[x]++ & 1);
-                        if (first) {
-                            if (no[x] > 0)
-                                wait(&oempty[x], (no[x] - 1) & 1);
-                            ++no[x];
-                        }
-                        if (bad)
-                            return;
-                        fence_after();
-                        const uint32_t vb = smem_u32(ring + (vpos(t) % NS) * S::TILE);
+                    }
+                    __syncwarp();
+                };
+                auto o_free = [&](int x) {  // the epilogue of O's last use has read it
+                    if (ow[x] < no[x])
+                        wait(&oempty[x], ow[x]++ & 1);
+                };
+                auto product_o = [&](int x, bool first, bool last) {  // with V tile vn
+                    wait(&pready[x], np[x]++ & 1);
+                    if (first) {
+                        o_free(x);
+                        ++no[x];
+                        last_use[x] = items;
+                    }
+                    if (bad)
+                        return;
+                    fence_after();
+                    const uint64_t vd = vdesc + vc.s * STEP;
+                    if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kTile / 16; ++ks)
                             mma_ts(tmem + 256 + x * kTile, tmem + x * kTile + ks * 8,
-                                   ca_desc(vb + ks * 2048, S::PANEL), ID_O, !first || ks > 0);
+                                   vd + ks * (2048 >> 4), ID_O, !first || ks > 0);
                         if (last)
                             mma_commit(&ofull[x]);
-                    };
-                    auto need_v = [&](int t) {
-                        const uint32_t pos = vpos(t);
-                        need(pos);
-                        if ((it.ka + t + 1) * kTile > pos0 + 1) {
-                            wait(&clean[pos % NS], (cleaned >> (pos % NS)) & 1);
-                            cleaned ^= 1u << (pos % NS);
-                        }
-                    };
-                    auto release = [&](uint32_t pos) { mma_commit(&empty[pos % NS]); };
-                    wait(qfull, items & 1);
-                    need(kpos(0));
-                    if (!bad && cnt[0] > 0)
-                        product_s(0, 0);
-                    if (single) {
-                        release(kpos(0));
-                        if (len > 1) {
-                            need(kpos(1));
-                            if (!bad) {
-                                product_s(1, 1);
-                                release(kpos(1));
-                            }
-                        }
-                        for (int t = 0; t < len && !bad; ++t) {
-                            const int x = t & 1;
-                            need_v(t);
-                            product_o(x, t, t < 2, t + 2 >= len);
+                    }
+                    __syncwarp();
+                };
+                // V tile vn is there; if it holds keys some row does not see, the
+                // cleaners start now, beside the softmax of the tile's S
+                auto hides = [&] { return (it.ka + vn + 1) * kTile > pos0 + 1; };
+                auto need_v = [&] {
+                    wait(&full[vc.s], vc.par);
+                    if (!bad && hides()) {
+                        // their buffer is free: no epilogue of two items ago runs
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (last_use[x] + 1 < items)
+                                o_free(x);
+                        if (elect_one())
+                            mbar_arrive(dirty);
+                        __syncwarp();
+                    }
+                };
+                auto cleaned_v = [&] {
+                    if (hides())
+                        wait(clean, cleaned++ & 1);
+                };
+                auto q_there = [&](uint32_t j) { wait(&qfull[j & 1], (j >> 1) & 1); };
+                auto q_read = [&](uint32_t j) {
+                    if (elect_one())
+                        mma_commit(&qempty[j & 1]);
+                    __syncwarp();
+                };
+                need_k();
+                q_there(qs);
+                if (bad)
+                    break;
+                if (cnt0 > 0)
+                    product_s(0);
+                if (single) {
+                    k_done();
+                    if (len > 1) {
+                        need_k();
+                        if (bad)
+                            break;
+                        product_s(1);
+                        k_done();
+                    }
+                    if (len <= 2)
+                        q_read(qs);
+                    for (int t = 0; t < len; ++t) {
+                        const int x = t & 1;
+                        need_v();
+                        cleaned_v();
+                        if (x == 0)
+                            product_o(0, t == 0, t + 2 >= len);
+                        else
+                            product_o(1, t == 1, t + 2 >= len);
+                        if (bad)
+                            break;
+                        v_done();
+                        if (t + 2 < len) {
+                            need_k();
                             if (bad)
                                 break;
-                            release(vpos(t));
-                            if (t + 2 < len) {
-                                need(kpos(t + 2));
-                                if (bad)
-                                    break;
-                                product_s(x, t + 2);
-                                release(kpos(t + 2));
-                            }
-                        }
-                    } else {
-                        if (!bad) {
-                            product_s(1, 0);
-                            release(kpos(0));
-                        }
-                        for (int t = 0; t < len && !bad; ++t) {
-                            need_v(t);
-                            if (t + 1 < len)
-                                need(kpos(t + 1));
-                            if (bad)
-                                break;
-                            if (t < cnt[0]) {
-                                product_o(0, t, t == 0, t + 1 == cnt[0]);
-                                if (bad)
-                                    break;
-                                if (t + 1 < cnt[0])
-                                    product_s(0, t + 1);
-                            }
-                            product_o(1, t, t == 0, t + 1 == len);
-                            if (bad)
-                                break;
-                            release(vpos(t));
-                            if (t + 1 < len) {
-                                product_s(1, t + 1);
-                                release(kpos(t + 1));
-                            }
+                            product_s(x);
+                            k_done();
+                            if (t + 3 == len)
+                                q_read(qs);
                         }
                     }
-                    mma_commit(qempty);
+                } else {
+                    if (cnt0 <= 1)
+                        q_read(qs);
+                    q_there(qs + 1);
+                    if (bad)
+                        break;
+                    product_s(1);
+                    k_done();
+                    if (len == 1)
+                        q_read(qs + 1);
+                    for (int t = 0; t < len; ++t) {
+                        need_v();
+                        if (t + 1 < len)
+                            need_k();
+                        cleaned_v();
+                        if (bad)
+                            break;
+                        if (t < cnt0) {
+                            product_o(0, t == 0, t + 1 == cnt0);
+                            if (bad)
+                                break;
+                            if (t + 1 < cnt0) {
+                                product_s(0);
+                                if (t + 2 == cnt0)
+                                    q_read(qs);
+                            }
+                        }
+                        product_o(1, t == 0, t + 1 == len);
+                        if (bad)
+                            break;
+                        v_done();
+                        if (t + 1 < len) {
+                            product_s(1);
+                            k_done();
+                            if (t + 2 == len)
+                                q_read(qs + 1);
+                        }
+                    }
                 }
-                bad = __shfl_sync(0xffffffffu, bad, 0);
-                base += 2 * len;
-                ++items;
+                for (int n = 2 * len; n > 0; n -= NS)
+                    base.advance(min(n, NS));
+                qs += single ? 1 : 2;
             }
-            if (lane == 0) {  // every product issued is done before the tensor memory is freed
+            // every product issued is done before the tensor memory is freed
+            if (elect_one())
                 mma_commit(done);
-                bad |= !mbar_wait(done, 0);
-            }
             __syncwarp();
+            bad |= !warp_wait(done, 0);
         } else {
             // ----------------------------------------------- cleaning of V
-            const int w2 = wi - 10;
-            uint32_t base = 0, items = 0, dirtied = 0;  // dirtied: a parity bit a stage
-            // (a warp that gave up still passes the barrier of every item)
-            for (bool more = wk.begin(); more; more = wk.next()) {
+            const int w2 = wi - kMmaWarp - 1;  // the half of the columns this warp cleans
+            uint32_t base = 0, items = 0, dirtied = 0;
+            for (bool more = wk.begin(); more && !bad; more = wk.next()) {
                 const CaItem &it = wk.it;
                 const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
-                const int buf = items % 3;
-                // Q of this item arrived: the S products of the item before are
-                // done, so only the epilogues of the two items before still read
-                // their buffers
-                if (!bad && !mbar_wait(qfull, items & 1))
-                    bad = true;
-                bad = __any_sync(0xffffffffu, bad);
-                if (lane == 0)
-                    mbar_arrive(qempty);
-                for (int c = w2 * 32 + lane; c < D; c += 64)
-                    sBad[buf * D + c] = 0x7fffffff;
-                if (w2 == 0 && lane == 0)
-                    sFlag[buf] = 0;
-                bar_sync(3, 64);
-                int t = max(0, (pos0 + 1) / kTile - it.ka);
-                for (; t < len && !bad; ++t) {
+                const int buf = items & 1;
+                const int t0 = max(0, (pos0 + 1) / kTile - it.ka);  // first tile with hidden keys
+                bool hit = false;
+                int *cleared = cleared_ptr<D>(a.part) + buf * D;
+                for (int t = t0; t < len && !bad; ++t) {
                     const int k0 = (it.ka + t) * kTile;
-                    if (k0 + kTile <= pos0 + 1)
-                        continue;
                     const uint32_t pos =
                         base + (it.single && t + 1 < len ? 2 * t + 2 : 2 * t + 1);
                     const int s = pos % NS;
-                    if (!mbar_wait(&dirty[s], dirtied >> s & 1) ||
-                        !mbar_wait(&full[s], (pos / NS) & 1))
+                    // the products' warp has seen the tile arrive, and waits for `clean`
+                    if (!mbar_wait(dirty, dirtied & 1) || !mbar_wait(&full[s], (pos / NS) & 1))
                         bad = true;
-                    dirtied ^= 1u << s;
+                    ++dirtied;
                     bad = __any_sync(0xffffffffu, bad);
                     if (bad)
                         break;
-                    constexpr int CPR = D / 8, RPW = 32 / CPR;  // chunks a row, rows a warp
-                    const int ch = lane % CPR;
-                    for (int r = max(0, pos0 + 1 - k0) + w2 * RPW + lane / CPR; r < kTile;
-                         r += 2 * RPW) {
-                        const uint32_t at =
-                            smem_u32(ring + s * S::TILE) + swz(r, ch, kTile);
-                        if (k0 + r >= it.c.len) {
-                            st_shared_v4(at, make_uint4(0u, 0u, 0u, 0u));
-                            continue;
-                        }
-                        uint4 v = ld_shared_v4(at);
-                        uint32_t *e = reinterpret_cast<uint32_t *>(&v);
-                        uint32_t hit = 0;
+                    if (t == t0 && lane == 0)
+                        sFlag[2 * buf + w2] = 0;
+                    // HC chunks of 16 bytes of a row are this warp's: RPW rows at a time,
+                    // UN of those in flight
+                    constexpr int HC = D / 16, RPW = 32 / HC, UN = 4;
+                    const int ch = w2 * HC + lane % HC;
+                    const uint32_t tile = smem_u32(ring + s * S::TILE);
+                    for (int rb = max(0, pos0 + 1 - k0) + lane / HC; rb - lane / HC < kTile;
+                         rb += UN * RPW) {
+                        uint4 v[UN];
+                        bool odd = false;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            if ((e[x] & 0x7f80u) == 0x7f80u) {
-                                hit |= 1u << (2 * x);
-                                e[x] &= 0xffff0000u;
-                            }
-                            if ((e[x] & 0x7f800000u) == 0x7f800000u) {
-                                hit |= 2u << (2 * x);
-                                e[x] &= 0xffffu;
-                            }
+                        for (int u = 0; u < UN; ++u) {
+                            const int r = min(rb + u * RPW, kTile - 1);
+                            v[u] = ld_shared_v4(tile + swz(r, ch, kTile));
                         }
-                        if (hit) {
-                            st_shared_v4(at, v);
-                            for (int x = 0; x < 8; ++x)
-                                if (hit >> x & 1)
-                                    atomicMin(&sBad[buf * D + ch * 8 + x], k0 + r);
-                            sFlag[buf] = 1;
+#pragma unroll
+                        for (int u = 0; u < UN; ++u) {
+                            // an exponent of all ones carries into the element's top bit
+                            const uint32_t m = 0x7f807f80u, c = 0x00800080u;
+                            const int r = rb + u * RPW;
+                            odd |= r < kTile && k0 + r < it.c.len &&
+                                   ((((v[u].x & m) + c) | ((v[u].y & m) + c) |
+                                     ((v[u].z & m) + c) | ((v[u].w & m) + c)) &
+                                    0x80008000u) != 0;
+                        }
+#pragma unroll
+                        for (int u = 0; u < UN; ++u) {
+                            const int r = rb + u * RPW;
+                            if (r < kTile && k0 + r >= it.c.len)
+                                st_shared_v4(tile + swz(r, ch, kTile), make_uint4(0u, 0u, 0u, 0u));
+                        }
+                        if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+                            for (int u = 0; u < UN; ++u) {
+                                const int r = rb + u * RPW;
+                                const bool mine = r < kTile && k0 + r < it.c.len;
+                                const uint32_t at = tile + swz(min(r, kTile - 1), ch, kTile);
+                                uint4 w = ld_shared_v4(at);
+                                uint32_t found = 0;
+                                auto word = [&](uint32_t &e, int x) {
+                                    if ((e & 0x7f80u) == 0x7f80u) {
+                                        found |= 1u << x;
+                                        e &= 0xffff0000u;
+                                    }
+                                    if ((e & 0x7f800000u) == 0x7f800000u) {
+                                        found |= 2u << x;
+                                        e &= 0xffffu;
+                                    }
+                                };
+                                word(w.x, 0);
+                                word(w.y, 2);
+                                word(w.z, 4);
+                                word(w.w, 6);
+                                if (!__any_sync(0xffffffffu, mine && found))
+                                    continue;
+                                if (!hit) {  // the item's first: this warp's columns
+                                    for (int x = lane; x < D / 2; x += 32)
+                                        __stcg(cleared + w2 * (D / 2) + x, 0x7fffffff);
+                                    if (lane == 0)
+                                        sFlag[2 * buf + w2] = 1;
+                                    __threadfence();
+                                    __syncwarp();
+                                    hit = true;
+                                }
+                                if (mine && found) {
+                                    st_shared_v4(at, w);
+                                    for (int x = 0; x < 8; ++x)
+                                        if (found >> x & 1)
+                                            atomicMin(cleared + ch * 8 + x, k0 + r);
+                                }
+                            }
                         }
                     }
+                    if (hit)
+                        __threadfence();
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(&clean[s]);
+                        mbar_arrive(clean);
                 }
                 base += 2 * len;
                 ++items;
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSmRegs));
         // ------------------------------------------------------- softmax
-        const int x = wi >> 2;                 // tile A or B
+        // A row belongs to two threads, of warps w (columns 0 .. 63 of S and the
+        // first half of O's) and w + 4 (the others), which exchange its maximum
+        constexpr int HK = kTile / 2, HD = D / 2;
+        const int x = wi / kSmWarps;           // tile A or B
         const int wq = wi & 3;                 // tensor-memory lanes 32 wq ..
+        const int hf = (wi >> 2) & 1;          // the row's half
         const int r = wq * 32 + lane;          // row of the tile
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t tS = tmem + x * kTile + lane_off, tO = tmem + 256 + x * kTile + lane_off;
+        const uint32_t tS = tmem + x * kTile + lane_off, tO = tmem + 256 + x * kTile + lane_off + hf * HD;
+        float *max_mine = sMax + (x * 2 + hf) * kTile + r, *max_other = sMax + (x * 2 + 1 - hf) * kTile + r;
+        const uint32_t pair_bar = 1 + x * 4 + wq;  // the barrier of this warp and its other half
         const bool neg = a.logit_scale < 0.f;
         const float ls = fmaxf(fabsf(a.logit_scale), 1e-30f);
         const float grow = kRescale / ls;
         const int rtok = r / G, rg = r - rtok * G;
-        uint32_t ns = 0, no = 0, items = 0;
+        uint32_t ns = 0, no = 0, items = 0, halves = 0, qs = 0;
         CaWalk wk{a, plan, tpt, {}};
         for (bool more = wk.begin(); more; more = wk.next()) {
             const CaItem &it = wk.it;
@@ -838,8 +1016,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             const int na = (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile;
             const int cnt = single ? (x == 0 ? (len + 1) / 2 : len / 2)
                                    : (x == 0 ? max(0, min(it.kb, na) - it.ka) : len);
-            if (!single && tid == 0)
-                mbar_arrive(qempty);  // nothing but S reads Q
+            const uint32_t slot_q = qs & 1;
+            if (!single && tid == 0) {  // only S reads the queries of a pair
+                mbar_arrive(&qempty[0]);
+                mbar_arrive(&qempty[1]);
+            }
+            qs += single ? 1 : 2;
             float mref = -INFINITY, negm = 0.f;
             float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
             for (int t = 0; t < cnt; ++t) {
@@ -848,64 +1030,57 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     bad = true;
                 ++ns;
                 bad = __any_sync(0xffffffffu, bad);
-                if (bad)
-                    break;
+                if (bad) {  // a warp that gave up still passes every barrier of its pair
+                    if (live)
+                        bar_sync(pair_bar, 64);
+                    continue;
+                }
                 fence_after();
                 if (live) {
-                    uint32_t sr[kTile];
+                    uint32_t sr[HK];
 #pragma unroll
-                    for (int o = 0; o < kTile; o += 16)
-                        ld16(tS + o, sr, o);
+                    for (int o = 0; o < HK; o += 16)
+                        ld16(tS + hf * HK + o, sr, o);
                     ld_wait(sr);
                     float *s = reinterpret_cast<float *>(sr);
                     if (neg) {
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c)
+                        for (int c = 0; c < HK; ++c)
                             s[c] = -s[c];
                     }
                     if (k0 + kTile > wlim) {
-                        const int m = lim - k0;
+                        const int m = lim - k0 - hf * HK;
 #pragma unroll
-                        for (int c = 0; c < kTile; ++c)
+                        for (int c = 0; c < HK; ++c)
                             s[c] = c < m ? s[c] : -INFINITY;
                     }
                     float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int c = 4; c < kTile; c += 8) {
+                    for (int c = 4; c < HK; c += 8) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            mx[e] = c + 4 + e < kTile ? fmaxf(fmaxf(mx[e], s[c + e]), s[c + 4 + e])
-                                                      : fmaxf(mx[e], s[c + e]);
+                            mx[e] = c + 4 + e < HK ? fmaxf(fmaxf(mx[e], s[c + e]), s[c + 4 + e])
+                                                   : fmaxf(mx[e], s[c + e]);
                     }
-                    const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    *max_mine = m_new;
+                    bar_sync(pair_bar, 64);  // also: both halves of S are in registers
+                    m_new = fmaxf(m_new, *max_other);
                     const bool up = t == 0 ? m_new > -INFINITY : m_new > mref + grow;
-                    if (__any_sync(0xffffffffu, up)) {
+                    float f = 1.f;
+                    if (up) {
                         const float old = negm;
                         const bool fresh = mref == -INFINITY;
-                        if (up) {
-                            mref = m_new;
-                            negm = -m_new * ls;
-                        }
-                        if (t > 0) {
-                            const float f = !up ? 1.f : fresh ? 0.f : ex2_approx(negm - old);
-                            l0 *= f;
-                            l1 *= f;
-                            l2 *= f;
-                            l3 *= f;
-#pragma unroll 1
-                            for (int o = 0; o < D; o += 16) {
-                                uint32_t ov[16];
-                                ld16(tO + o, ov, 0);
-                                ld_wait(ov);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
-                                st16(tO + o, ov, 0);
-                            }
-                        }
+                        mref = m_new;
+                        negm = -m_new * ls;
+                        f = fresh ? 0.f : ex2_approx(negm - old);
+                        l0 *= f;
+                        l1 *= f;
+                        l2 *= f;
+                        l3 *= f;
                     }
 #pragma unroll
-                    for (int c = 0; c < kTile; c += 32) {
+                    for (int c = 0; c < HK; c += 32) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -920,7 +1095,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             pk[e / 2] = pack_bf16x2(s[c + e], s[c + e + 1]);
                             pk[e / 2 + 1] = pack_bf16x2(s[c + e + 2], s[c + e + 3]);
                         }
-                        st16(tS + c / 2, pk, 0);
+                        st16(tS + hf * (HK / 2) + c / 2, pk, 0);
+                    }
+                    // O by the factor, this half of the row in flight at once
+                    if (t > 0 && __any_sync(0xffffffffu, up)) {
+                        uint32_t ov[HD];
+#pragma unroll
+                        for (int o = 0; o < HD; o += 16)
+                            ld16(tO + o, ov, o);
+                        ld_wait(ov);
+#pragma unroll
+                        for (int o = 0; o < HD; o += 16) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                ov[o + e] = __float_as_uint(__uint_as_float(ov[o + e]) * f);
+                            st16(tO + o, ov, o);
+                        }
                     }
                     st_wait();
                 }
@@ -939,27 +1129,80 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 fence_after();
             }
             bad = __any_sync(0xffffffffu, bad);
-            const int buf = items % 3;
+            if (cnt > 0) {  // the other half's sum
+                *max_mine = l;
+                bar_sync(pair_bar, 64);
+                const float other = *max_other;
+                l = hf == 0 ? l + other : other + l;
+                bar_sync(pair_bar, 64);  // read before the next maximum is written
+            }
+            const int buf = items & 1;
             ++items;
-            // only the tiles that were cleaned order the flag before this read
-            const int last_tile = it.ka + (single ? 2 * (cnt - 1) + x : cnt - 1);
-            const bool poisoned =
-                !bad && cnt > 0 && (last_tile + 1) * kTile > pos0 + 1 && sFlag[buf] != 0;
             const bool whole = it.ka == 0 && it.kb == it.kt;
             const bool join = single && len > 1;  // B holds the odd key tiles
-            // exchange area of the halves: Q of B (a single item has one tile)
-            float4 *xo = reinterpret_cast<float4 *>(sQ + S::TILE);
-            float2 *xm = reinterpret_cast<float2 *>(sQ + S::TILE + S::TILE / 2);
-            auto load_o = [&](int c, uint32_t (&v)[XC]) {  // XC columns of O, poisoned ones NaN
-                if (cnt > 0 && live && !bad) {
+            // (max, sum) of a B half goes to A through the item's Q, which S has read
+            float2 *sHalf = reinterpret_cast<float2 *>(sQ + slot_q * S::TILE);
+            if (single && x == 1) {
+                if (join) {  // A reads both halves of O: the lanes are the same
+                    if (hf == 0)
+                        sHalf[r] = make_float2(m, l);
+                    fence_proxy_async_smem();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(half);
+                }
+                continue;
+            }
+            float fa = 1.f, fb = 0.f;
+            if (join) {
+                if (!bad && !mbar_wait(half, halves & 1))
+                    bad = true;
+                ++halves;
+                bad = __any_sync(0xffffffffu, bad);
+                fence_after();
+                const float2 mb = sHalf[r];
+                const float mm = fmaxf(m, mb.x);
+                fa = m == -INFINITY ? 0.f : ex2_approx(m - mm);
+                fb = mb.x == -INFINITY ? 0.f : ex2_approx(mb.x - mm);
+                m = mm;
+                l = l * fa + mb.y * fb;
+            }
+            if (single) {  // Q may be loaded over
+                fence_proxy_async_smem();
+                bar_sync(9, 32 * kSmWarps);
+                if (tid == 0)
+                    mbar_arrive(&qempty[slot_q]);
+            }
+            // only the tiles that were cleaned order the flag before this read
+            const int last_tile = it.ka + (single ? len : cnt) - 1;
+            const bool poisoned =
+                !bad && cnt > 0 && (last_tile + 1) * kTile > pos0 + 1 && sFlag[2 * buf + hf] != 0;
+            const bool read_o = cnt > 0 && live && !bad;
+            // XC columns of O, the halves joined, poisoned ones NaN
+            auto load_o = [&](int c, uint32_t (&v)[XC]) {
+                if (read_o) {
 #pragma unroll
                     for (int o = 0; o < XC; o += 16)
                         ld16(tO + c + o, v, o);
-                    ld_wait(v);
+                    if (join) {
+                        uint32_t w[XC];
+#pragma unroll
+                        for (int o = 0; o < XC; o += 16)
+                            ld16(tO + kTile + c + o, w, o);
+                        ld_wait(v);
+                        ld_wait(w);
+#pragma unroll
+                        for (int e = 0; e < XC; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * fa +
+                                                   __uint_as_float(w[e]) * fb);
+                    } else {
+                        ld_wait(v);
+                    }
                     if (poisoned) {
 #pragma unroll
                         for (int e = 0; e < XC; ++e)
-                            if (sBad[buf * D + c + e] < lim)
+                            if (__ldcg(cleared_ptr<D>(a.part) + buf * D + hf * HD + c + e) < lim)
                                 v[e] = 0x7fffffffu;
                     }
                 } else {
@@ -972,42 +1215,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 if (cnt > 0) {
                     fence_before();
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0) {
                         mbar_arrive(&oempty[x]);
-                }
-            };
-            if (single && x == 1) {
-                if (join) {
-                    xm[r] = make_float2(m, l);
-                    for (int c = 0; c < D; c += XC) {
-                        uint32_t v[XC];
-                        load_o(c, v);
-#pragma unroll
-                        for (int e = 0; e < XC; e += 4)
-                            xo[(e / 4) * kTile + r] =
-                                make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]),
-                                            __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-                        if (c + XC >= D)
-                            o_done();
-                        fence_proxy_async_smem();  // Q is loaded over it next
-                        bar_sync(4, 256);          // this round is written
-                        bar_sync(5, 256);          // and read
+                        if (join)
+                            mbar_arrive(&oempty[1]);
                     }
                 }
-                continue;
-            }
-            float fa = 1.f, fb = 0.f;
+            };
             int bs = 0;
             unsigned parts = 1;
             float *slot = nullptr;
             if (!whole) {
                 // the shares the item is cut over: lane k looks at share bs + k
-                bs = static_cast<int>(min(static_cast<long long>(plan.ctas - 1),
-                                          it.x * plan.ctas / plan.cost));
-                while (bs + 1 < plan.ctas && share_border(plan, bs + 1) <= it.x)
-                    ++bs;
-                while (share_border(plan, bs) > it.x)
-                    --bs;
+                bs = static_cast<int>(quotient(it.x, plan.share));
                 const int b = bs + lane;
                 bool some = false;
                 if (b < plan.ctas) {
@@ -1023,80 +1243,56 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             }
             const int row = x * kTile + r;  // within a slot
             const size_t tok_row = static_cast<size_t>(it.c.first + it.tok0 + tile_tok + rtok);
-            __nv_bfloat16 *dst = a.out + (tok_row * a.Hq + it.h * G + rg) * D;
-            float inv = 1.f;
+            __nv_bfloat16 *dst = a.out + (tok_row * a.Hq + it.h * G + rg) * D + hf * HD;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-            for (int c = 0; c < D; c += XC) {
+            for (int c = 0; c < HD; c += XC) {
                 uint32_t v[XC];
                 load_o(c, v);
-                if (c + XC >= D)
+                if (c + XC >= HD)
                     o_done();
-                if (join) {
-                    bar_sync(4, 256);
-                    if (c == 0) {
-                        const float2 mb = xm[r];
-                        const float mm = fmaxf(m, mb.x);
-                        fa = m == -INFINITY ? 0.f : ex2_approx(m - mm);
-                        fb = mb.x == -INFINITY ? 0.f : ex2_approx(mb.x - mm);
-                        m = mm;
-                        l = l * fa + mb.y * fb;
-                    }
-#pragma unroll
-                    for (int e = 0; e < XC; e += 4) {
-                        const float4 w = xo[(e / 4) * kTile + r];
-                        v[e] = __float_as_uint(__uint_as_float(v[e]) * fa + w.x * fb);
-                        v[e + 1] = __float_as_uint(__uint_as_float(v[e + 1]) * fa + w.y * fb);
-                        v[e + 2] = __float_as_uint(__uint_as_float(v[e + 2]) * fa + w.z * fb);
-                        v[e + 3] = __float_as_uint(__uint_as_float(v[e + 3]) * fa + w.w * fb);
-                    }
-                    fence_proxy_async_smem();
-                    bar_sync(5, 256);
-                }
-                if (c == 0)
-                    inv = l == 0.f ? 0.f : 1.f / l;
                 if (r < rows && !bad) {
                     if (whole) {
 #pragma unroll
-                        for (int e = 0; e < XC; e += 8) {
-                            uint4 o;
-                            o.x = pack_bf16x2(__uint_as_float(v[e]) * inv,
-                                              __uint_as_float(v[e + 1]) * inv);
-                            o.y = pack_bf16x2(__uint_as_float(v[e + 2]) * inv,
-                                              __uint_as_float(v[e + 3]) * inv);
-                            o.z = pack_bf16x2(__uint_as_float(v[e + 4]) * inv,
-                                              __uint_as_float(v[e + 5]) * inv);
-                            o.w = pack_bf16x2(__uint_as_float(v[e + 6]) * inv,
-                                              __uint_as_float(v[e + 7]) * inv);
-                            st_global_v4(dst + c + e, o);
+                        for (int e = 0; e < XC; e += 16) {
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                o[k] = pack_bf16x2(__uint_as_float(v[e + 2 * k]) * inv,
+                                                   __uint_as_float(v[e + 2 * k + 1]) * inv);
+                            st_global_v8(dst + c + e, o);
                         }
                     } else {
+                        float *to = slot + static_cast<size_t>(row) * D + hf * HD + c;
 #pragma unroll
-                        for (int e = 0; e < XC; e += 4)
-                            st_global_v4(slot + static_cast<size_t>(row) * D + c + e,
-                                         make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]));
+                        for (int e = 0; e < XC; e += 8) {
+                            uint32_t o[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                o[k] = v[e + k];
+                            st_global_v8(to + e, o);
+                        }
                     }
                 }
             }
-            if (single && tid == 0)
-                mbar_arrive(qempty);  // the halves are joined: Q may be loaded over
             if (whole)
                 continue;
             // a partial result: the last of the item's shares to arrive joins them
-            if (r < rows)
+            if (r < rows && hf == 0)
                 reinterpret_cast<float2 *>(slot + 2 * kTile * D)[row] = make_float2(m, l);
             __threadfence();
-            bar_sync(1 + x, 128);
-            if (r == 0) {
+            bar_sync(9 + x, 32 * kSmWarps);
+            if (r == 0 && hf == 0) {
                 const unsigned n = __popc(parts);
                 sLast[x] = atomicInc(&a.arrived[2 * bs + x], n - 1) == n - 1;
             }
-            bar_sync(1 + x, 128);
+            bar_sync(9 + x, 32 * kSmWarps);
             if (!sLast[x])
                 continue;
             __threadfence();
             constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes a row, rows a warp
             const int first = __ffs(parts) - 1;
-            for (int rr = wq * RPW + lane / LPR; rr < rows; rr += 4 * RPW) {
+            for (int rr = (hf * 4 + wq) * RPW + lane / LPR; rr < rows; rr += kSmWarps * RPW) {
                 const int cc = (lane % LPR) * 4;
                 const int srow = x * kTile + rr;
                 float M = -INFINITY;
@@ -1135,7 +1331,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         set_error(a.sticky, ZP_ERR_TIMEOUT);
     fence_before();
     __syncthreads();
-    if (wi == 9) {
+    if (wi == kMmaWarp) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)
@@ -1148,7 +1344,7 @@ static cudaError_t launch_chunk_attn_t(const ChunkAttnArgs &a, int sms, cudaStre
 {
     using S = CaSmem<D>;
     const cudaError_t e = cudaFuncSetAttribute(
-        zp_chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::ALLOC);
+        zp_chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (e != cudaSuccess)
         return e;
     cudaLaunchAttribute attr[1];
@@ -1157,7 +1353,7 @@ static cudaError_t launch_chunk_attn_t(const ChunkAttnArgs &a, int sms, cudaStre
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(sms), 1, 1);
     cfg.blockDim = dim3(kCaThreads, 1, 1);
-    cfg.dynamicSmemBytes = S::ALLOC;
+    cfg.dynamicSmemBytes = S::BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

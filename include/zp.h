@@ -433,7 +433,7 @@ zp_status zp_append_kv_chunk(zp_cache *cache, int32_t layer, const void *k_new, 
  *  q             device bf16 [total][Hq][d], 16-byte aligned, tokens q_stride
  *                elements apart
  *  block_tables, req_idx  as in zp_paged_decode_attn (read only)
- *  out           device bf16 [total][Hq][d], contiguous, 16-byte aligned */
+ *  out           device bf16 [total][Hq][d], contiguous, 32-byte aligned */
 zp_status zp_paged_chunk_attn(zp_cache *cache, int32_t layer, const void *q, int64_t q_stride,
                               const int32_t *starts, int32_t total, const int32_t *block_tables,
                               int32_t bt_stride, int32_t num_rows, const int32_t *lengths,

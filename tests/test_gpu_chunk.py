@@ -276,7 +276,7 @@ def test_refused_on_the_host():
     before = [b.kp[0].clone(), b.vp[0].clone()]
     bad = zp.ERR_INVALID_ARG
     assert attn(layer=1) == bad and attn(layer=-1) == bad
-    assert attn(q=b.q.data_ptr() + 2) == bad and attn(out=b.out.data_ptr() + 8) == bad
+    assert attn(q=b.q.data_ptr() + 2) == bad and attn(out=b.out.data_ptr() + 16) == bad
     assert attn(qs=255) == bad and attn(qs=260) == bad and attn(qs=-256) == bad
     assert attn(total=-1) == bad and attn(R=-1) == bad and attn(R=3) == bad
     assert attn(stride=0) == bad and attn(rows=0) == bad and attn(starts=0) == bad
