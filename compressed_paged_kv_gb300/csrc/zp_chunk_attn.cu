@@ -57,7 +57,9 @@ static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4)
 constexpr int kItemCost = 128;         // an item's fixed cost, in keys
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
 constexpr int kMaxSpan = 30;           // CTAs an item is cut over, about (a lane each joins them)
-constexpr int kMmaWarp = 2 * kSmWarps + 1;
+constexpr int kLoadWarp = 2 * kSmWarps;       // then the products' warps of A and of B, the cleaner
+constexpr int kMmaWarp = kLoadWarp + 1;
+constexpr int kBufs = 8;               // records of cleared elements (an item each, in turn)
 constexpr int kTmemCols = 512;         // S/P of A, of B; O of A, of B
 constexpr float kRescale = 8.f;        // log2 of the growth that rescales O
 
@@ -82,13 +84,13 @@ struct CaSmem {
     static constexpr int off_q = 0;                      // Q of A, Q of B
     static constexpr int off_ring = off_q + 2 * TILE;
     static constexpr int off_max = off_ring + NS * TILE;  // float [2][2][128]: maxima of row halves
-    static constexpr int off_flag = off_max + 4 * kTile * 4;  // int [2][2]: elements were cleared
-    static constexpr int off_plan = off_flag + 16;        // CaPlan
+    static constexpr int off_flag = off_max + 4 * kTile * 4;  // int [kBufs]: elements were cleared
+    static constexpr int off_plan = off_flag + kBufs * 4;     // CaPlan
     static constexpr int off_scan = off_plan + 80;        // int64 [warps]
     static constexpr int off_bar = off_scan + kCaThreads / 32 * 8;
-    // full[NS], empty[NS], Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull[2], Qempty[2], dirty,
-    // clean, half, done
-    static constexpr int NBAR = 2 * NS + 12 + 4;
+    // full[NS], empty[NS], clean[NS], Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull[2], Qempty[2],
+    // dirty[2], turn[2], half, taken, done
+    static constexpr int NBAR = 3 * NS + 16 + 3;
     static constexpr int off_tmem = off_bar + NBAR * 8;
     static constexpr int off_last = off_tmem + 8;         // int [2]
     static constexpr int BYTES = off_last + 8;
@@ -377,10 +379,19 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// A converged warp's bounded wait.
+// Bounded waits: a try suspends the warp for some microseconds, so that this is
+// a matter of seconds, and every wait here is for this CTA's own work.
+constexpr uint32_t kCaSpins = 1u << 19;
+
+__device__ __forceinline__ bool ca_wait(uint64_t *bar, uint32_t parity)
+{
+    return mbar_wait(bar, parity, kCaSpins);
+}
+
+// A converged warp's wait.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, ca_wait(bar, parity));
 }
 
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t threads)
@@ -408,12 +419,12 @@ __device__ __forceinline__ void add2(float &x, float &y, float u, float v)
 }
 
 // The positions of cleared value elements of a CTA's items, behind the slots
-// of the partial results: int [2][D], written only when there are some.
+// of the partial results: int [kBufs][D], written only when there are some.
 template <int D>
 __device__ __forceinline__ int *cleared_ptr(float *part)
 {
     return reinterpret_cast<int *>(part + static_cast<size_t>(2 * gridDim.x) * (2 * kTile * (D + 2))) +
-           static_cast<size_t>(blockIdx.x) * 2 * D;
+           static_cast<size_t>(blockIdx.x) * kBufs * D;
 }
 
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
@@ -434,7 +445,7 @@ __device__ __forceinline__ float *slot_ptr(float *part, int slot)
 
 size_t chunk_attn_part_floats(int d, int sms)
 {
-    return static_cast<size_t>(2 * sms) * (2 * kTile * (d + 2) + d);
+    return static_cast<size_t>(sms) * (4 * kTile * (d + 2) + kBufs * d);
 }
 
 template <int D>
@@ -456,9 +467,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     CaPlan &plan = *reinterpret_cast<CaPlan *>(sm + S::off_plan);
     long long *scan = reinterpret_cast<long long *>(sm + S::off_scan);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::off_bar);
-    uint64_t *empty = full + NS, *sfull = empty + NS, *pready = sfull + 2, *ofull = pready + 2;
-    uint64_t *oempty = ofull + 2, *qfull = oempty + 2, *qempty = qfull + 2;
-    uint64_t *dirty = qempty + 2, *clean = dirty + 1, *half = clean + 1, *done = half + 1;
+    uint64_t *empty = full + NS, *clean = empty + NS, *sfull = clean + NS, *pready = sfull + 2;
+    uint64_t *ofull = pready + 2, *oempty = ofull + 2, *qfull = oempty + 2, *qempty = qfull + 2;
+    uint64_t *dirty = qempty + 2, *turn = dirty + 2, *half = turn + 2, *taken = half + 1, *done = taken + 1;
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sm + S::off_tmem);
     int *sLast = reinterpret_cast<int *>(sm + S::off_last);
 
@@ -468,7 +479,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);  // both products' warps have passed it
+            mbar_init(&clean[s], 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sfull[x], 1);
@@ -476,12 +488,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             mbar_init(&ofull[x], 1);
             mbar_init(&oempty[x], kSmWarps);
             mbar_init(&qfull[x], 1);
-            mbar_init(&qempty[x], 2);  // its last S, and A's word that nothing else uses it
+            mbar_init(&qempty[x], 2);
+            mbar_init(&dirty[x], 1);
+            mbar_init(&turn[x], 1);
         }
-        mbar_init(dirty, 1);
-        mbar_init(clean, 2);
         mbar_init(half, kSmWarps);
-        mbar_init(done, 1);
+        mbar_init(taken, kSmWarps);
+        mbar_init(done, 2);
+        mbar_arrive(&turn[0]);  // A begins
         fence_mbar_init();
     }
     if (wi == kMmaWarp) {
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (wi >= 2 * kSmWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         CaWalk wk{a, plan, tpt, {}};
-        if (wi == kMmaWarp - 1) {
+        if (wi == kLoadWarp) {
             // ----------------------------------------------------- producer
             uint32_t loaded = 0, cur = 0, par = 0, qs = 0;  // ring cursor and parity, query tiles
             for (bool more = wk.begin(); more && !bad; more = wk.next()) {
@@ -670,218 +684,204 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 bad |= !warp_wait(&qfull[j & 1], (j >> 1) & 1);
             for (uint32_t j = loaded > NS ? loaded - NS : 0; j < loaded; ++j)
                 bad |= !warp_wait(&full[j % NS], (j / NS) & 1);
-        } else if (wi == kMmaWarp) {
+        } else if (wi <= kMmaWarp + 1) {
             // ----------------------------------------------------- products
-            // The whole warp walks and waits; one lane issues.
+            // One warp a stream, so that the waits of one lie beside the products of
+            // the other (the issue of a product waits for a place in a short queue).
+            // They take turns at P V and the next S: products of both in the queue
+            // at once would end at the same time, and so would the two softmaxes,
+            // with nothing left to run beside them.  Both walk the ring in its
+            // order and pass every stage, used or not: a stage's parity then never
+            // runs ahead of a warp.  The whole warp walks and waits; one lane issues.
             constexpr uint32_t ID_S = ca_idesc(kTile, false), ID_O = ca_idesc(D, true);
             constexpr uint32_t STEP = S::TILE >> 4;
+            const int x = wi - kMmaWarp;
             const uint64_t qdesc = ca_desc(smem_u32(sQ), 16), kdesc = ca_desc(smem_u32(ring), 16);
             const uint64_t vdesc = ca_desc(smem_u32(ring), S::PANEL);
-            uint32_t qs = 0, cleaned = 0, items = 0;
-            uint32_t np[2] = {0u, 0u}, no[2] = {0u, 0u}, ow[2] = {0u, 0u};  // ow: Oempty waited for
-            uint32_t last_use[2] = {0u, 0u};  // the item that used O last
-            struct Cursor {  // a ring stage and the parity of its load
-                uint32_t s, par;
-                __device__ __forceinline__ void advance(uint32_t n)
-                {
-                    s += n;
-                    if (s >= NS) {
-                        s -= NS;
-                        par ^= 1;
-                    }
-                }
-            } base{0u, 0u};  // the item's first stage
+            const uint32_t tS = tmem + x * kTile, tO = tmem + 256 + x * kTile;
+            uint32_t cur = 0, par = 0, cleaned = 0;  // ring stage and parity; a parity bit a stage
+            uint32_t qs = 0, np = 0, no = 0, ow = 0;  // ow: Oempty waited for
+            uint32_t items = 0, last_use = 0;        // the item that used O last
+            uint32_t turns = 0;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (!bad && !warp_wait(bar, parity))
                     bad = true;
+            };
+            auto o_free = [&] {  // the epilogue of O's last use has read it
+                if (ow < no)
+                    wait(&oempty[x], ow++ & 1);
+            };
+            auto pass = [&](uint64_t *bar, bool used) {  // when the products issued are done, or now
+                if (elect_one()) {
+                    if (used)
+                        mma_commit(bar);
+                    else
+                        mbar_arrive(bar);
+                }
+                __syncwarp();
+            };
+            auto step_on = [&](bool used) {
+                pass(&empty[cur], used);
+                if (++cur == NS) {
+                    cur = 0;
+                    par ^= 1;
+                }
             };
             for (bool more = wk.begin(); more && !bad; more = wk.next()) {
                 const CaItem &it = wk.it;
                 const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
                 const bool single = it.single;
                 ++items;
-                // A's key tiles of a pair: the ones its last token sees
-                const int na = (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile;
-                const int cnt0 = single ? (len + 1) / 2 : max(0, min(it.kb, na) - it.ka);
-                // the next K and V tiles: a pair loads K0 V0 K1 V1 .., a single
-                // item K0 K1 V0 K2 V1 ..
-                Cursor kc = base, vc = base;
-                vc.advance(single && len > 1 ? 2 : 1);
-                int kn = 0, vn = 0;
-                auto k_done = [&] {  // K tile kn is read by the products issued
-                    if (elect_one())
-                        mma_commit(&empty[kc.s]);
-                    __syncwarp();
-                    kc.advance(single && kn == 0 ? 1 : 2);
-                    ++kn;
-                };
-                auto v_done = [&] {
-                    if (elect_one())
-                        mma_commit(&empty[vc.s]);
-                    __syncwarp();
-                    vc.advance(single && vn + 2 >= len ? 1 : 2);
-                    ++vn;
-                };
-                auto need_k = [&] { wait(&full[kc.s], kc.par); };
-                auto product_s = [&](int x) {  // S of tile x with K tile kn
-                    const uint64_t qd = qdesc + ((qs + (single ? 0 : x)) & 1) * STEP;
-                    const uint64_t kd = kdesc + kc.s * STEP;
-                    fence_after();
+                // the cleared elements of an item are kept until kBufs items on:
+                // this stream's epilogue of two items ago has read its own
+                if (last_use + 1 < items)
+                    o_free();
+                // the stream's key tiles: t with t % 2 == x of a single item; of a
+                // pair all for B, the ones its last token sees for A
+                const int na = x == 0 ? (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile : it.kb;
+                const int cnt = single ? (len + 1 - x) / 2 : max(0, min(it.kb, na) - it.ka);
+                const int last = single ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
+                const uint32_t slot = single ? qs : qs + x;
+                const uint64_t qd = qdesc + (slot & 1) * STEP;
+                auto product_s = [&](int t) {  // S with the K tile t of stage `cur`
+                    const uint64_t kd = kdesc + cur * STEP;
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             const uint32_t o = ((ks >> 2) * S::PANEL + (ks & 3) * 32) >> 4;
-                            mma_ss(tmem + x * kTile, qd + o, kd + o, ID_S, ks > 0);
+                            mma_ss(tS, qd + o, kd + o, ID_S, ks > 0);
                         }
                         mma_commit(&sfull[x]);
+                        if (t == last)
+                            mma_commit(&qempty[slot & 1]);
                     }
                     __syncwarp();
+                    step_on(true);
                 };
-                auto o_free = [&](int x) {  // the epilogue of O's last use has read it
-                    if (ow[x] < no[x])
-                        wait(&oempty[x], ow[x]++ & 1);
+                auto skip = [&] {  // a stage of the other stream's
+                    wait(&full[cur], par);
+                    if (!bad)
+                        step_on(false);
                 };
-                auto product_o = [&](int x, bool first, bool last) {  // with V tile vn
-                    wait(&pready[x], np[x]++ & 1);
-                    if (first) {
-                        o_free(x);
-                        ++no[x];
-                        last_use[x] = items;
+                auto hides = [&](int t) { return (it.ka + t + 1) * kTile > pos0 + 1; };
+                auto skip_v = [&](int t) {
+                    if (hides(t))
+                        cleaned ^= 1u << cur;
+                    skip();
+                };
+                // P V with V tile t, then S with K tile `next` (the stage behind it)
+                auto burst = [&](int t, int next) {
+                    wait(&full[cur], par);
+                    if (hides(t)) {
+                        // it holds keys some row does not see: cleaned beside the
+                        // softmax of the tile's S
+                        if (!bad && (single || x == 1))
+                            pass(&dirty[x], false);
+                        wait(&clean[cur], cleaned >> cur & 1);
+                        cleaned ^= 1u << cur;
                     }
+                    const bool more_s = next <= last;
+                    if (next < len) {
+                        const bool wrap = cur + 1 == NS;
+                        wait(&full[wrap ? 0 : cur + 1], par ^ wrap);
+                    }
+                    const bool first = t == (single ? x : 0);
+                    wait(&pready[x], np++ & 1);
+                    if (first) {
+                        o_free();
+                        ++no;
+                        last_use = items;
+                    }
+                    wait(&turn[x], turns++ & 1);
                     if (bad)
                         return;
+                    const uint64_t vd = vdesc + cur * STEP;
                     fence_after();
-                    const uint64_t vd = vdesc + vc.s * STEP;
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kTile / 16; ++ks)
-                            mma_ts(tmem + 256 + x * kTile, tmem + x * kTile + ks * 8,
-                                   vd + ks * (2048 >> 4), ID_O, !first || ks > 0);
-                        if (last)
+                            mma_ts(tO, tS + ks * 8, vd + ks * (2048 >> 4), ID_O, !first || ks > 0);
+                        if (t == last)
                             mma_commit(&ofull[x]);
                     }
                     __syncwarp();
+                    step_on(true);
+                    if (more_s)
+                        product_s(next);
+                    else if (next < len)
+                        step_on(false);
+                    pass(&turn[1 - x], false);
                 };
-                // V tile vn is there; if it holds keys some row does not see, the
-                // cleaners start now, beside the softmax of the tile's S
-                auto hides = [&] { return (it.ka + vn + 1) * kTile > pos0 + 1; };
-                auto need_v = [&] {
-                    wait(&full[vc.s], vc.par);
-                    if (!bad && hides()) {
-                        // their buffer is free: no epilogue of two items ago runs
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if (last_use[x] + 1 < items)
-                                o_free(x);
-                        if (elect_one())
-                            mbar_arrive(dirty);
-                        __syncwarp();
-                    }
+                auto no_burst = [&] {
+                    wait(&turn[x], turns++ & 1);
+                    if (!bad)
+                        pass(&turn[1 - x], false);
                 };
-                auto cleaned_v = [&] {
-                    if (hides())
-                        wait(clean, cleaned++ & 1);
-                };
-                auto q_there = [&](uint32_t j) { wait(&qfull[j & 1], (j >> 1) & 1); };
-                auto q_read = [&](uint32_t j) {
-                    if (elect_one())
-                        mma_commit(&qempty[j & 1]);
-                    __syncwarp();
-                };
-                need_k();
-                q_there(qs);
+                wait(&qfull[qs & 1], (qs >> 1) & 1);
+                if (!single)
+                    wait(&qfull[(qs + 1) & 1], ((qs + 1) >> 1) & 1);
                 if (bad)
                     break;
-                if (cnt0 > 0)
-                    product_s(0);
-                if (single) {
-                    k_done();
-                    if (len > 1) {
-                        need_k();
-                        if (bad)
-                            break;
-                        product_s(1);
-                        k_done();
-                    }
-                    if (len <= 2)
-                        q_read(qs);
-                    for (int t = 0; t < len; ++t) {
-                        const int x = t & 1;
-                        need_v();
-                        cleaned_v();
-                        if (x == 0)
-                            product_o(0, t == 0, t + 2 >= len);
-                        else
-                            product_o(1, t == 1, t + 2 >= len);
-                        if (bad)
-                            break;
-                        v_done();
-                        if (t + 2 < len) {
-                            need_k();
-                            if (bad)
-                                break;
-                            product_s(x);
-                            k_done();
-                            if (t + 3 == len)
-                                q_read(qs);
-                        }
-                    }
-                } else {
-                    if (cnt0 <= 1)
-                        q_read(qs);
-                    q_there(qs + 1);
+                if (!single)
+                    pass(&qempty[(qs + 1 - x) & 1], false);  // the other stream's queries
+                if (cnt == 0)
+                    pass(&qempty[slot & 1], false);
+                auto first_s = [&](bool mine, int t) {
+                    wait(&full[cur], par);
                     if (bad)
-                        break;
-                    product_s(1);
-                    k_done();
-                    if (len == 1)
-                        q_read(qs + 1);
-                    for (int t = 0; t < len; ++t) {
-                        need_v();
-                        if (t + 1 < len)
-                            need_k();
-                        cleaned_v();
-                        if (bad)
-                            break;
-                        if (t < cnt0) {
-                            product_o(0, t == 0, t + 1 == cnt0);
-                            if (bad)
-                                break;
-                            if (t + 1 < cnt0) {
-                                product_s(0);
-                                if (t + 2 == cnt0)
-                                    q_read(qs);
-                            }
+                        return;
+                    if (!mine) {
+                        step_on(false);
+                        return;
+                    }
+                    fence_after();
+                    product_s(t);
+                };
+                if (single) {  // K0 K1 | V0 K2 | V1 K3 | ..: the groups in turn A's and B's
+                    first_s(x == 0, 0);
+                    if (len > 1)
+                        first_s(x == 1, 1);
+                    for (int t = 0; t < len && !bad; t += 2) {
+                        if (x == 1) {
+                            skip_v(t);
+                            if (t + 2 < len)
+                                skip();
                         }
-                        product_o(1, t == 0, t + 1 == len);
-                        if (bad)
-                            break;
-                        v_done();
-                        if (t + 1 < len) {
-                            product_s(1);
-                            k_done();
-                            if (t + 2 == len)
-                                q_read(qs + 1);
+                        if (t + x < len)
+                            burst(t + x, t + x + 2);
+                        else
+                            no_burst();
+                        if (x == 0 && t + 1 < len) {
+                            skip_v(t + 1);
+                            if (t + 3 < len)
+                                skip();
+                        }
+                    }
+                } else {  // K0 | V0 K1 | V1 K2 | ..
+                    first_s(cnt > 0, 0);
+                    for (int t = 0; t < len && !bad; ++t) {
+                        if (t < cnt) {
+                            burst(t, t + 1);
+                        } else {
+                            skip_v(t);
+                            if (t + 1 < len)
+                                skip();
+                            no_burst();
                         }
                     }
                 }
-                for (int n = 2 * len; n > 0; n -= NS)
-                    base.advance(min(n, NS));
                 qs += single ? 1 : 2;
             }
             // every product issued is done before the tensor memory is freed
-            if (elect_one())
-                mma_commit(done);
-            __syncwarp();
+            pass(done, true);
             bad |= !warp_wait(done, 0);
         } else {
             // ----------------------------------------------- cleaning of V
-            const int w2 = wi - kMmaWarp - 1;  // the half of the columns this warp cleans
-            uint32_t base = 0, items = 0, dirtied = 0;
+            uint32_t base = 0, items = 0, dirtied[2] = {0u, 0u};
             for (bool more = wk.begin(); more && !bad; more = wk.next()) {
                 const CaItem &it = wk.it;
                 const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
-                const int buf = items & 1;
+                const int buf = items % kBufs;
                 const int t0 = max(0, (pos0 + 1) / kTile - it.ka);  // first tile with hidden keys
                 bool hit = false;
                 int *cleared = cleared_ptr<D>(a.part) + buf * D;
@@ -890,21 +890,21 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     const uint32_t pos =
                         base + (it.single && t + 1 < len ? 2 * t + 2 : 2 * t + 1);
                     const int s = pos % NS;
-                    // the products' warp has seen the tile arrive, and waits for `clean`
-                    if (!mbar_wait(dirty, dirtied & 1) || !mbar_wait(&full[s], (pos / NS) & 1))
+                    // a products' warp has seen the tile arrive, and waits for `clean`
+                    const bool by_a = it.single && !(t & 1);
+                    if (!warp_wait(by_a ? &dirty[0] : &dirty[1], (by_a ? dirtied[0] : dirtied[1]) & 1) ||
+                        !warp_wait(&full[s], (pos / NS) & 1)) {
                         bad = true;
-                    ++dirtied;
-                    bad = __any_sync(0xffffffffu, bad);
-                    if (bad)
                         break;
+                    }
+                    ++dirtied[by_a ? 0 : 1];
                     if (t == t0 && lane == 0)
-                        sFlag[2 * buf + w2] = 0;
-                    // HC chunks of 16 bytes of a row are this warp's: RPW rows at a time,
-                    // UN of those in flight
-                    constexpr int HC = D / 16, RPW = 32 / HC, UN = 4;
-                    const int ch = w2 * HC + lane % HC;
+                        sFlag[buf] = 0;
+                    // CPR chunks of 16 bytes a row, RPW rows at a time, UN of those in flight
+                    constexpr int CPR = D / 8, RPW = 32 / CPR, UN = 8;
+                    const int ch = lane % CPR;
                     const uint32_t tile = smem_u32(ring + s * S::TILE);
-                    for (int rb = max(0, pos0 + 1 - k0) + lane / HC; rb - lane / HC < kTile;
+                    for (int rb = max(0, pos0 + 1 - k0) + lane / CPR; rb - lane / CPR < kTile;
                          rb += UN * RPW) {
                         uint4 v[UN];
                         bool odd = false;
@@ -953,11 +953,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                 word(w.w, 6);
                                 if (!__any_sync(0xffffffffu, mine && found))
                                     continue;
-                                if (!hit) {  // the item's first: this warp's columns
-                                    for (int x = lane; x < D / 2; x += 32)
-                                        __stcg(cleared + w2 * (D / 2) + x, 0x7fffffff);
+                                if (!hit) {  // the item's first
+                                    for (int x = lane; x < D; x += 32)
+                                        __stcg(cleared + x, 0x7fffffff);
                                     if (lane == 0)
-                                        sFlag[2 * buf + w2] = 1;
+                                        sFlag[buf] = 1;
                                     __threadfence();
                                     __syncwarp();
                                     hit = true;
@@ -976,7 +976,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(clean);
+                        mbar_arrive(&clean[s]);
                 }
                 base += 2 * len;
                 ++items;
@@ -1000,7 +1000,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const float ls = fmaxf(fabsf(a.logit_scale), 1e-30f);
         const float grow = kRescale / ls;
         const int rtok = r / G, rg = r - rtok * G;
-        uint32_t ns = 0, no = 0, items = 0, halves = 0, qs = 0;
+        uint32_t ns = 0, no = 0, items = 0, halves = 0;
+        bool lent = false;  // B: its (max, sum) of a join lie in sMax
         CaWalk wk{a, plan, tpt, {}};
         for (bool more = wk.begin(); more; more = wk.next()) {
             const CaItem &it = wk.it;
@@ -1016,17 +1017,17 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             const int na = (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile;
             const int cnt = single ? (x == 0 ? (len + 1) / 2 : len / 2)
                                    : (x == 0 ? max(0, min(it.kb, na) - it.ka) : len);
-            const uint32_t slot_q = qs & 1;
-            if (!single && tid == 0) {  // only S reads the queries of a pair
-                mbar_arrive(&qempty[0]);
-                mbar_arrive(&qempty[1]);
+            if (lent && cnt > 0) {  // A has taken what B left in place of its maxima
+                if (!bad && !ca_wait(taken, halves++ & 1))
+                    bad = true;
+                bad = __any_sync(0xffffffffu, bad);
+                lent = false;
             }
-            qs += single ? 1 : 2;
             float mref = -INFINITY, negm = 0.f;
             float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
             for (int t = 0; t < cnt; ++t) {
                 const int k0 = (it.ka + (single ? 2 * t + x : t)) * kTile;
-                if (!bad && !mbar_wait(&sfull[x], ns & 1))
+                if (!bad && !ca_wait(&sfull[x], ns & 1))
                     bad = true;
                 ++ns;
                 bad = __any_sync(0xffffffffu, bad);
@@ -1123,7 +1124,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             float l = (l0 + l1) + (l2 + l3);
             float m = mref == -INFINITY ? -INFINITY : -negm;  // base 2, scaled
             if (cnt > 0) {
-                if (!bad && !mbar_wait(&ofull[x], no & 1))
+                if (!bad && !ca_wait(&ofull[x], no & 1))
                     bad = true;
                 ++no;
                 fence_after();
@@ -1136,17 +1137,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 l = hf == 0 ? l + other : other + l;
                 bar_sync(pair_bar, 64);  // read before the next maximum is written
             }
-            const int buf = items & 1;
+            const int buf = items % kBufs;
             ++items;
             const bool whole = it.ka == 0 && it.kb == it.kt;
             const bool join = single && len > 1;  // B holds the odd key tiles
-            // (max, sum) of a B half goes to A through the item's Q, which S has read
-            float2 *sHalf = reinterpret_cast<float2 *>(sQ + slot_q * S::TILE);
             if (single && x == 1) {
                 if (join) {  // A reads both halves of O: the lanes are the same
-                    if (hf == 0)
-                        sHalf[r] = make_float2(m, l);
-                    fence_proxy_async_smem();
+                    *max_mine = hf == 0 ? m : l;
+                    lent = true;
                     fence_before();
                     __syncwarp();
                     if (lane == 0)
@@ -1156,28 +1154,25 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             }
             float fa = 1.f, fb = 0.f;
             if (join) {
-                if (!bad && !mbar_wait(half, halves & 1))
+                if (!bad && !ca_wait(half, halves & 1))
                     bad = true;
                 ++halves;
                 bad = __any_sync(0xffffffffu, bad);
                 fence_after();
-                const float2 mb = sHalf[r];
-                const float mm = fmaxf(m, mb.x);
+                const float mb = sMax[2 * kTile + r], lb = sMax[3 * kTile + r];
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(taken);
+                const float mm = fmaxf(m, mb);
                 fa = m == -INFINITY ? 0.f : ex2_approx(m - mm);
-                fb = mb.x == -INFINITY ? 0.f : ex2_approx(mb.x - mm);
+                fb = mb == -INFINITY ? 0.f : ex2_approx(mb - mm);
                 m = mm;
-                l = l * fa + mb.y * fb;
-            }
-            if (single) {  // Q may be loaded over
-                fence_proxy_async_smem();
-                bar_sync(9, 32 * kSmWarps);
-                if (tid == 0)
-                    mbar_arrive(&qempty[slot_q]);
+                l = l * fa + lb * fb;
             }
             // only the tiles that were cleaned order the flag before this read
             const int last_tile = it.ka + (single ? len : cnt) - 1;
             const bool poisoned =
-                !bad && cnt > 0 && (last_tile + 1) * kTile > pos0 + 1 && sFlag[2 * buf + hf] != 0;
+                !bad && cnt > 0 && (last_tile + 1) * kTile > pos0 + 1 && sFlag[buf] != 0;
             const bool read_o = cnt > 0 && live && !bad;
             // XC columns of O, the halves joined, poisoned ones NaN
             auto load_o = [&](int c, uint32_t (&v)[XC]) {
