@@ -853,6 +853,10 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     zp::ChunkAttnArgs a{};
     a.kmap = c->ws.kmaps + layer;
     a.vmap = c->ws.vmaps + layer;
+    a.kpool = static_cast<const __nv_bfloat16 *>(c->kpools[layer]);
+    a.vpool = static_cast<const __nv_bfloat16 *>(c->vpools[layer]);
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.q_stride = q_stride;
     if (!zp::encode_chunk_q_map(&a.qmap, q, total, q_stride, c->Hq, c->Hq / c->Hkv, c->d))
         return ZP_ERR_UNSUPPORTED;
     a.starts = starts;

@@ -29,6 +29,8 @@ struct ChunkKvArgs {
 struct ChunkAttnArgs {
     const CUtensorMap *kmap;
     const CUtensorMap *vmap;
+    const __nv_bfloat16 *kpool, *vpool, *q;
+    int64_t q_stride;  // elements from a token of q to the next
     CUtensorMap qmap;  // q as [total][Hq][d]: boxes of 64 dims x a group's heads x a tile's tokens
     const int32_t *starts;
     int32_t total;

@@ -15,24 +15,26 @@
 // the tensor cores work for one while the other is in its softmax, and each
 // K/V tile is staged once for up to 256 rows.
 //
-// Twelve warps:
-//   warps 0-3, 4-7  softmax of A and of B, a thread a row: the row of S from
-//           tensor memory, a running maximum and sum (fp32, base 2), P
-//           rounded to bf16 over S in tensor memory.  O is rescaled only when
-//           a maximum grows by more than 2^8 (p stays below 2^8, which
-//           changes no relative error), in place in tensor memory, between
-//           the products: S's arrival says that the product before it is
-//           done.  Then the epilogue.
-//   warp 8  TMA producer: Q once per item, K and V through one ring of 128-key
-//           stages (a box a cache block and 64 dims, 128-byte swizzle).
-//   warp 9  one lane issues tcgen05.mma (kind::f16, bf16 -> fp32): S from
-//           shared memory, P V with P from tensor memory and V as an
-//           MN-major operand.
-//   warps 10, 11  clean the V tiles that hold keys hidden from some row: a
-//           probability of 0 times an infinity or NaN would be NaN.  Rows past
-//           the length become 0; elements that are not finite at positions
-//           past the item's first become 0, their lowest position is kept a
-//           column, and the epilogue gives NaN to the rows that see it.
+// Twenty warps:
+//   warps 0-7, 8-15  softmax of A and of B, a row of S a pair of threads (64
+//           columns each, out of tensor memory; they exchange their maxima): a
+//           running maximum and sum (fp32, base 2), P rounded to bf16 over S in
+//           tensor memory.  O is rescaled only when a maximum grows by more
+//           than 2^8 (p stays below 2^8, which changes no relative error), in
+//           place in tensor memory, between the products: S's arrival says that
+//           the product before it is done.  Then the epilogue.
+//   warp 16 walks the items, describes each in shared memory for the others,
+//           and loads Q once per item and the K tiles (TMA, a box a cache block
+//           and 64 dims, 128-byte swizzle) into a ring of their own
+//   warps 17, 18  the products of A and of B: tcgen05.mma (kind::f16, bf16 ->
+//           fp32), S from shared memory, P V with P from tensor memory and V as
+//           an MN-major operand
+//   warp 19 loads the V tiles into theirs
+//
+// A key past the length or hidden from a row has probability 0, but 0 times an
+// infinity or NaN is NaN.  The V rows past the length in the last block are
+// cleared in shared memory; a row whose O came out NaN while its tiles held
+// values hidden from it is computed again with plain fp32 arithmetic.
 //
 // The grid is one CTA an SM.  Every CTA adds up the cost of all items (the
 // keys each reads, plus kItemCost) from the device arrays and takes an equal,
@@ -57,9 +59,10 @@ static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4)
 constexpr int kItemCost = 128;         // an item's fixed cost, in keys
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
 constexpr int kMaxSpan = 30;           // CTAs an item is cut over, about (a lane each joins them)
-constexpr int kLoadWarp = 2 * kSmWarps;       // then the products' warps of A and of B, the cleaner
+constexpr int kLoadWarp = 2 * kSmWarps;       // then the products' warps of A and of B, V's loader
 constexpr int kMmaWarp = kLoadWarp + 1;
-constexpr int kBufs = 8;               // records of cleared elements (an item each, in turn)
+constexpr int kLoadVWarp = kLoadWarp + 3;
+constexpr int kDescs = 4;              // item descriptions in flight
 constexpr int kTmemCols = 512;         // S/P of A, of B; O of A, of B
 constexpr float kRescale = 8.f;        // log2 of the growth that rescales O
 
@@ -74,28 +77,42 @@ struct CaPlan {
     int ctas;         // CTAs with a share
 };
 
+// A work item as the other warps need it.
+struct CaDesc {
+    int row0;    // packed row of its first token
+    int ntok;    // its tokens; 0: no more items
+    int h;       // kv head
+    int pos0;    // position of its first token
+    int len;     // cached tokens of the request
+    int row;     // the request's table row
+    int ka, kb;  // this CTA's key tiles
+    int kt;      // all its key tiles
+    int w;       // cost
+    long long x; // cost before it
+};
+
 template <int D>
 struct CaSmem {
     static constexpr int PANELS = D / 64;
     static constexpr int PANEL = kTile * 128;            // bytes of 128 rows of 64 dims
     static constexpr int TILE = PANELS * PANEL;
-    static constexpr int NS = D == 128 ? 5 : 10;         // K/V ring stages
+    static constexpr int NK = D == 128 ? 2 : 5, NV = D == 128 ? 3 : 5;  // stages of K and of V
     static constexpr int XC = D / 4;                     // columns of O a step of the epilogue
     static constexpr int off_q = 0;                      // Q of A, Q of B
-    static constexpr int off_ring = off_q + 2 * TILE;
-    static constexpr int off_max = off_ring + NS * TILE;  // float [2][2][128]: maxima of row halves
-    static constexpr int off_flag = off_max + 4 * kTile * 4;  // int [kBufs]: elements were cleared
-    static constexpr int off_plan = off_flag + kBufs * 4;     // CaPlan
-    static constexpr int off_scan = off_plan + 80;        // int64 [warps]
+    static constexpr int off_k = off_q + 2 * TILE;
+    static constexpr int off_v = off_k + NK * TILE;
+    static constexpr int off_max = off_v + NV * TILE;    // float [2][2][128]: maxima of row halves
+    static constexpr int off_desc = off_max + 4 * kTile * 4;  // CaDesc [kDescs]
+    static constexpr int off_plan = off_desc + kDescs * static_cast<int>(sizeof(CaDesc));
+    static constexpr int off_scan = off_plan + static_cast<int>(sizeof(CaPlan));  // int64 [warps]
     static constexpr int off_bar = off_scan + kCaThreads / 32 * 8;
-    // full[NS], empty[NS], clean[NS], Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull[2], Qempty[2],
-    // dirty[2], turn[2], half, taken, done
-    static constexpr int NBAR = 3 * NS + 16 + 3;
+    // K full, empty; V full, empty; Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull[2],
+    // Qempty[2], turn[2]; described, read [kDescs]; half, taken, done
+    static constexpr int NBAR = 2 * NK + 2 * NV + 14 + 2 * kDescs + 3;
     static constexpr int off_tmem = off_bar + NBAR * 8;
     static constexpr int off_last = off_tmem + 8;         // int [2]
     static constexpr int BYTES = off_last + 8;
-    static_assert(sizeof(CaPlan) <= 80 && off_bar % 8 == 0, "layout");
-    static_assert(BYTES <= 232448, "shared memory of a CTA");
+    static_assert(BYTES <= 232448 && off_desc % 8 == 0 && off_bar % 8 == 0, "shared memory");
 };
 
 struct CaItem {
@@ -418,15 +435,6 @@ __device__ __forceinline__ void add2(float &x, float &y, float u, float v)
         : "f"(u), "f"(v));
 }
 
-// The positions of cleared value elements of a CTA's items, behind the slots
-// of the partial results: int [kBufs][D], written only when there are some.
-template <int D>
-__device__ __forceinline__ int *cleared_ptr(float *part)
-{
-    return reinterpret_cast<int *>(part + static_cast<size_t>(2 * gridDim.x) * (2 * kTile * (D + 2))) +
-           static_cast<size_t>(blockIdx.x) * kBufs * D;
-}
-
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t (&v)[8])
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
@@ -445,7 +453,7 @@ __device__ __forceinline__ float *slot_ptr(float *part, int slot)
 
 size_t chunk_attn_part_floats(int d, int sms)
 {
-    return static_cast<size_t>(sms) * (4 * kTile * (d + 2) + kBufs * d);
+    return static_cast<size_t>(2 * sms) * (2 * kTile * (d + 2));
 }
 
 template <int D>
@@ -453,23 +461,23 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     zp_chunk_attn_kernel(const __grid_constant__ ChunkAttnArgs a)
 {
     using S = CaSmem<D>;
-    constexpr int PANELS = S::PANELS, NS = S::NS, XC = S::XC;
-    extern __shared__ __align__(1024) uint8_t smem_aligned[];
-    uint8_t *sm = smem_aligned;
+    constexpr int PANELS = S::PANELS, NK = S::NK, NV = S::NV, XC = S::XC;
+    extern __shared__ __align__(1024) uint8_t sm[];
     if (smem_u32(sm) & 1023u) {  // the swizzled tiles need it
         if (threadIdx.x == 0)
             set_error(a.sticky, ZP_ERR_UNSUPPORTED);
         return;
     }
-    uint8_t *sQ = sm + S::off_q, *ring = sm + S::off_ring;
+    uint8_t *sQ = sm + S::off_q, *sK = sm + S::off_k, *sV = sm + S::off_v;
     float *sMax = reinterpret_cast<float *>(sm + S::off_max);
-    int *sFlag = reinterpret_cast<int *>(sm + S::off_flag);
+    CaDesc *sDesc = reinterpret_cast<CaDesc *>(sm + S::off_desc);
     CaPlan &plan = *reinterpret_cast<CaPlan *>(sm + S::off_plan);
     long long *scan = reinterpret_cast<long long *>(sm + S::off_scan);
-    uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::off_bar);
-    uint64_t *empty = full + NS, *clean = empty + NS, *sfull = clean + NS, *pready = sfull + 2;
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + S::off_bar), *kempty = kfull + NK;
+    uint64_t *vfull = kempty + NK, *vempty = vfull + NV, *sfull = vempty + NV, *pready = sfull + 2;
     uint64_t *ofull = pready + 2, *oempty = ofull + 2, *qfull = oempty + 2, *qempty = qfull + 2;
-    uint64_t *dirty = qempty + 2, *turn = dirty + 2, *half = turn + 2, *taken = half + 1, *done = taken + 1;
+    uint64_t *turn = qempty + 2, *described = turn + 2, *read = described + kDescs;
+    uint64_t *half = read + kDescs, *taken = half + 1, *done = taken + 1;
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sm + S::off_tmem);
     int *sLast = reinterpret_cast<int *>(sm + S::off_last);
 
@@ -477,10 +485,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     const int G = a.Hq / a.Hkv, tpt = tile_tokens(G);
 
     if (tid == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);  // both products' warps have passed it
-            mbar_init(&clean[s], 1);
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(&kfull[s], 1);
+            mbar_init(&kempty[s], 2);  // both products' warps have passed it
+        }
+        for (int s = 0; s < NV; ++s) {
+            mbar_init(&vfull[s], 1);
+            mbar_init(&vempty[s], 2);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sfull[x], 1);
@@ -489,8 +500,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             mbar_init(&oempty[x], kSmWarps);
             mbar_init(&qfull[x], 1);
             mbar_init(&qempty[x], 2);
-            mbar_init(&dirty[x], 1);
             mbar_init(&turn[x], 1);
+        }
+        for (int s = 0; s < kDescs; ++s) {
+            mbar_init(&described[s], 1);
+            mbar_init(&read[s], 2 * kSmWarps + 3);
         }
         mbar_init(half, kSmWarps);
         mbar_init(taken, kSmWarps);
@@ -572,179 +586,233 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     fence_after();
     const uint32_t tmem = *sTmem;
     bool bad = false;
+    uint32_t nd = 0;  // items this warp has gone through
+
+    // The next item's description, or null at the end; a warp lets it go with
+    // `leave` once it no longer reads it.  (A warp that gave up still follows
+    // the descriptions: the barriers of its group count on it.)
+    auto enter = [&]() -> const CaDesc * {
+        const int j = nd % kDescs;
+        if (!warp_wait(&described[j], (nd / kDescs) & 1)) {
+            bad = true;
+            return nullptr;
+        }
+        return sDesc[j].ntok ? &sDesc[j] : nullptr;
+    };
+    auto leave = [&] {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&read[nd % kDescs]);
+        ++nd;
+    };
 
     if (wi >= 2 * kSmWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        CaWalk wk{a, plan, tpt, {}};
+        // The tiles of a ring: eight cache blocks of 16 keys, PANELS boxes each.
+        // A lane holds the pool row of a block of this kv head (negative past the
+        // request's blocks: the load then fills zeros), four tiles at a time and
+        // the next four ahead.
+        auto block_y = [&](const CaDesc &d, int q) {
+            if (q * kBlk >= d.len)
+                return -kBlk;
+            const int blk = a.tables[(size_t)d.row * a.stride + q];
+            if (blk < 0 || blk >= a.num_blocks) {
+                set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
+                return -kBlk;
+            }
+            return (blk * a.Hkv + d.h) * kBlk;
+        };
+        auto load_tile = [&](const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int ids, int t) {
+            int y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                y[q] = __shfl_sync(0xffffffffu, ids, (t & 3) * 8 + q);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(bar, S::TILE);
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+#pragma unroll
+                    for (int p = 0; p < PANELS; ++p)
+                        tma_load_2d(dst + p * S::PANEL + q * kBlk * 128, map, p * 64, y[q], bar);
+            }
+            __syncwarp();
+        };
         if (wi == kLoadWarp) {
-            // ----------------------------------------------------- producer
+            // ------------------------------------------- the items, Q and K
             uint32_t loaded = 0, cur = 0, par = 0, qs = 0;  // ring cursor and parity, query tiles
-            for (bool more = wk.begin(); more && !bad; more = wk.next()) {
+            CaWalk wk{a, plan, tpt, {}};
+            bool more = wk.begin();
+            for (; !bad; more = wk.next()) {
                 const CaItem &it = wk.it;
-                const int len = it.kb - it.ka;
-                const int32_t *trow = a.tables + (size_t)it.c.row * a.stride;
-                const int nblk = (it.c.len + kBlk - 1) / kBlk;
-                // pool row of a cache block of this kv head, negative past the
-                // request's blocks (the load then fills zeros)
-                auto block_y = [&](int q) {
-                    if (q >= nblk)
-                        return -kBlk;
-                    const int blk = trow[q];
-                    if (blk < 0 || blk >= a.num_blocks) {
-                        set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
-                        return -kBlk;
-                    }
-                    return (blk * a.Hkv + it.h) * kBlk;
-                };
-                // ids of four key tiles at a time, a lane a block, the next four ahead
-                int ids = block_y(it.ka * 8 + lane);
-                int ids_next = len > 4 ? block_y((it.ka + 4) * 8 + lane) : 0;
-                int base = 0;  // key tile `ids` begins at
-                auto stage = [&](int t, bool v) {
-                    if (loaded >= NS && !warp_wait(&empty[cur], par ^ 1)) {
-                        bad = true;
-                        return;
-                    }
-                    // a V tile may lie one group behind the K tile loaded before it
-                    const int src = (t - base) * 8;
-                    const int from = src < 32 ? ids : ids_next;
-                    int y[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        y[q] = __shfl_sync(0xffffffffu, from, (src & 31) + q);
-                    const CUtensorMap *map = v ? a.vmap : a.kmap;
-                    uint8_t *dst = ring + cur * S::TILE;
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&full[cur], S::TILE);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-#pragma unroll
-                            for (int p = 0; p < PANELS; ++p)
-                                tma_load_2d(dst + p * S::PANEL + q * kBlk * 128, map, p * 64, y[q],
-                                            &full[cur]);
-                    }
-                    __syncwarp();
-                    ++loaded;
-                    if (++cur == NS) {
-                        cur = 0;
-                        par ^= 1;
-                    }
-                };
-                auto advance = [&](int t) {  // V tile t is the oldest still to come
-                    if (t - base >= 4) {
-                        base += 4;
-                        ids = ids_next;
-                        ids_next = base + 4 < len ? block_y((it.ka + base + 4) * 8 + lane) : 0;
-                    }
-                };
-                // the first K tile before Q: it does not wait for the item before
-                stage(0, false);
-                if (bad)
+                const int j = nd % kDescs;
+                if (nd >= kDescs && !warp_wait(&read[j], (nd / kDescs - 1) & 1)) {
+                    bad = true;
                     break;
-                for (int x = 0; x < (it.single ? 1 : 2); ++x, ++qs) {
-                    const int j = qs & 1;
-                    if (qs >= 2 && !warp_wait(&qempty[j], ((qs >> 1) - 1) & 1)) {
+                }
+                CaDesc d;
+                d.row0 = it.c.first + it.tok0;
+                d.ntok = more ? it.ntok : 0;
+                d.h = it.h;
+                d.pos0 = it.c.len - it.c.n + it.tok0;
+                d.len = it.c.len;
+                d.row = it.c.row;
+                d.ka = it.ka;
+                d.kb = it.kb;
+                d.kt = it.kt;
+                d.w = it.w;
+                d.x = it.x;
+                if (lane == 0) {
+                    sDesc[j] = d;
+                    mbar_arrive(&described[j]);
+                }
+                __syncwarp();
+                ++nd;
+                if (!more)
+                    break;
+                const int len = d.kb - d.ka;
+                int ids = block_y(d, d.ka * 8 + lane);
+                int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
+                const int tiles = it.single ? 1 : 2;
+                for (int t = 0; t < len; ++t) {
+                    if (t > 0 && (t & 3) == 0) {
+                        ids = ids_next;
+                        ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
+                    }
+                    if (loaded >= NK && !warp_wait(&kempty[cur], par ^ 1)) {
                         bad = true;
                         break;
                     }
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(&qfull[j], PANELS * G * tpt * 128);
+                    load_tile(a.kmap, sK + cur * S::TILE, &kfull[cur], ids, t);
+                    ++loaded;
+                    if (++cur == NK) {
+                        cur = 0;
+                        par ^= 1;
+                    }
+                    if (t > 0)
+                        continue;
+                    // Q behind the first K tile, which does not wait for the item before
+                    for (int x = 0; x < tiles; ++x, ++qs) {
+                        const int k = qs & 1;
+                        if (qs >= 2 && !warp_wait(&qempty[k], ((qs >> 1) - 1) & 1)) {
+                            bad = true;
+                            break;
+                        }
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(&qfull[k], PANELS * G * tpt * 128);
 #pragma unroll
-                        for (int p = 0; p < PANELS; ++p)
-                            asm volatile(
-                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
-                                "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                    smem_u32(sQ + j * S::TILE + p * S::PANEL)),
-                                "l"(&a.qmap), "r"(p * 64), "r"(it.h * G),
-                                "r"(it.c.first + it.tok0 + x * tpt), "r"(smem_u32(&qfull[j]))
-                                : "memory");
+                            for (int p = 0; p < PANELS; ++p)
+                                asm volatile(
+                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
+                                    "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                        smem_u32(sQ + k * S::TILE + p * S::PANEL)),
+                                    "l"(&a.qmap), "r"(p * 64), "r"(d.h * G),
+                                    "r"(d.row0 + x * tpt), "r"(smem_u32(&qfull[k]))
+                                    : "memory");
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if (it.single) {
-                    for (int t = 0; t < len && !bad; ++t) {
-                        advance(t);
-                        if (t + 1 < len)
-                            stage(t + 1, false);
-                        if (!bad)
-                            stage(t, true);
-                    }
-                } else {
-                    for (int t = 0; t < len && !bad; ++t) {
-                        advance(t);
-                        if (t > 0)
-                            stage(t, false);
-                        if (!bad)
-                            stage(t, true);
-                    }
+                    if (bad)
+                        break;
                 }
             }
             // every copy issued has landed before the CTA may exit
-            for (uint32_t j = qs > 2 ? qs - 2 : 0; j < qs; ++j)
-                bad |= !warp_wait(&qfull[j & 1], (j >> 1) & 1);
-            for (uint32_t j = loaded > NS ? loaded - NS : 0; j < loaded; ++j)
-                bad |= !warp_wait(&full[j % NS], (j / NS) & 1);
-        } else if (wi <= kMmaWarp + 1) {
+            for (uint32_t k = qs > 2 ? qs - 2 : 0; k < qs; ++k)
+                bad |= !warp_wait(&qfull[k & 1], (k >> 1) & 1);
+            for (uint32_t k = loaded > NK ? loaded - NK : 0; k < loaded; ++k)
+                bad |= !warp_wait(&kfull[k % NK], (k / NK) & 1);
+        } else if (wi == kLoadVWarp) {
+            // ------------------------------------------------------------- V
+            uint32_t loaded = 0, cur = 0, par = 0;
+            while (const CaDesc *dp = bad ? nullptr : enter()) {
+                const CaDesc d = *dp;
+                leave();
+                const int len = d.kb - d.ka;
+                int ids = block_y(d, d.ka * 8 + lane);
+                int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
+                for (int t = 0; t < len; ++t) {
+                    if (t > 0 && (t & 3) == 0) {
+                        ids = ids_next;
+                        ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
+                    }
+                    if (loaded >= NV && !warp_wait(&vempty[cur], par ^ 1)) {
+                        bad = true;
+                        break;
+                    }
+                    load_tile(a.vmap, sV + cur * S::TILE, &vfull[cur], ids, t);
+                    ++loaded;
+                    if (++cur == NV) {
+                        cur = 0;
+                        par ^= 1;
+                    }
+                }
+            }
+            for (uint32_t k = loaded > NV ? loaded - NV : 0; k < loaded; ++k)
+                bad |= !warp_wait(&vfull[k % NV], (k / NV) & 1);
+        } else {
             // ----------------------------------------------------- products
             // One warp a stream, so that the waits of one lie beside the products of
             // the other (the issue of a product waits for a place in a short queue).
             // They take turns at P V and the next S: products of both in the queue
             // at once would end at the same time, and so would the two softmaxes,
-            // with nothing left to run beside them.  Both walk the ring in its
-            // order and pass every stage, used or not: a stage's parity then never
-            // runs ahead of a warp.  The whole warp walks and waits; one lane issues.
+            // with nothing left to run beside them.  Both pass every stage of the
+            // rings, used or not: a stage's parity then never runs ahead of a warp.
+            // The whole warp waits; one lane issues.
             constexpr uint32_t ID_S = ca_idesc(kTile, false), ID_O = ca_idesc(D, true);
             constexpr uint32_t STEP = S::TILE >> 4;
             const int x = wi - kMmaWarp;
-            const uint64_t qdesc = ca_desc(smem_u32(sQ), 16), kdesc = ca_desc(smem_u32(ring), 16);
-            const uint64_t vdesc = ca_desc(smem_u32(ring), S::PANEL);
+            const uint64_t qdesc = ca_desc(smem_u32(sQ), 16), kdesc = ca_desc(smem_u32(sK), 16);
+            const uint64_t vdesc = ca_desc(smem_u32(sV), S::PANEL);
             const uint32_t tS = tmem + x * kTile, tO = tmem + 256 + x * kTile;
-            uint32_t cur = 0, par = 0, cleaned = 0;  // ring stage and parity; a parity bit a stage
-            uint32_t qs = 0, np = 0, no = 0, ow = 0;  // ow: Oempty waited for
-            uint32_t items = 0, last_use = 0;        // the item that used O last
-            uint32_t turns = 0;
+            uint32_t kc = 0, kpar = 0, vc = 0, vpar = 0;  // ring cursors and parities
+            uint32_t qs = 0, np = 0, no = 0, turns = 0;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (!bad && !warp_wait(bar, parity))
                     bad = true;
             };
-            auto o_free = [&] {  // the epilogue of O's last use has read it
-                if (ow < no)
-                    wait(&oempty[x], ow++ & 1);
-            };
-            auto pass = [&](uint64_t *bar, bool used) {  // when the products issued are done, or now
-                if (elect_one()) {
-                    if (used)
-                        mma_commit(bar);
-                    else
-                        mbar_arrive(bar);
+            auto k_on = [&] {
+                if (++kc == NK) {
+                    kc = 0;
+                    kpar ^= 1;
                 }
+            };
+            auto v_on = [&] {
+                if (++vc == NV) {
+                    vc = 0;
+                    vpar ^= 1;
+                }
+            };
+            auto tell = [&](uint64_t *bar) {
+                if (elect_one())
+                    mbar_arrive(bar);
                 __syncwarp();
             };
-            auto step_on = [&](bool used) {
-                pass(&empty[cur], used);
-                if (++cur == NS) {
-                    cur = 0;
-                    par ^= 1;
-                }
-            };
-            for (bool more = wk.begin(); more && !bad; more = wk.next()) {
-                const CaItem &it = wk.it;
-                const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
-                const bool single = it.single;
-                ++items;
-                // the cleared elements of an item are kept until kBufs items on:
-                // this stream's epilogue of two items ago has read its own
-                if (last_use + 1 < items)
-                    o_free();
+            while (const CaDesc *dp = bad ? nullptr : enter()) {
+                const int len = dp->kb - dp->ka, ka = dp->ka, kb = dp->kb, cached = dp->len;
+                const bool single = dp->ntok <= tpt;
                 // the stream's key tiles: t with t % 2 == x of a single item; of a
                 // pair all for B, the ones its last token sees for A
-                const int na = x == 0 ? (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile : it.kb;
-                const int cnt = single ? (len + 1 - x) / 2 : max(0, min(it.kb, na) - it.ka);
+                const int na = x == 0 ? (dp->pos0 + min(dp->ntok, tpt) + kTile - 1) / kTile : kb;
+                leave();
+                const int cnt = single ? (len + 1 - x) / 2 : max(0, min(kb, na) - ka);
                 const int last = single ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
                 const uint32_t slot = single ? qs : qs + x;
                 const uint64_t qd = qdesc + (slot & 1) * STEP;
-                auto product_s = [&](int t) {  // S with the K tile t of stage `cur`
-                    const uint64_t kd = kdesc + cur * STEP;
+                auto skip_k = [&] {  // a tile of the other stream's
+                    wait(&kfull[kc], kpar);
+                    if (bad)
+                        return;
+                    tell(&kempty[kc]);
+                    k_on();
+                };
+                auto skip_v = [&] {
+                    wait(&vfull[vc], vpar);
+                    if (bad)
+                        return;
+                    tell(&vempty[vc]);
+                    v_on();
+                };
+                auto product_s = [&](int t) {  // S with K tile t, which has arrived
+                    const uint64_t kd = kdesc + kc * STEP;
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
@@ -752,70 +820,74 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             mma_ss(tS, qd + o, kd + o, ID_S, ks > 0);
                         }
                         mma_commit(&sfull[x]);
+                        mma_commit(&kempty[kc]);
                         if (t == last)
                             mma_commit(&qempty[slot & 1]);
                     }
                     __syncwarp();
-                    step_on(true);
+                    k_on();
                 };
-                auto skip = [&] {  // a stage of the other stream's
-                    wait(&full[cur], par);
-                    if (!bad)
-                        step_on(false);
+                auto first_s = [&](bool mine, int t) {
+                    if (!mine) {
+                        skip_k();
+                        return;
+                    }
+                    wait(&kfull[kc], kpar);
+                    if (bad)
+                        return;
+                    fence_after();
+                    product_s(t);
                 };
-                auto hides = [&](int t) { return (it.ka + t + 1) * kTile > pos0 + 1; };
-                auto skip_v = [&](int t) {
-                    if (hides(t))
-                        cleaned ^= 1u << cur;
-                    skip();
-                };
-                // P V with V tile t, then S with K tile `next` (the stage behind it)
+                // P V with V tile t, then S with K tile `next`
                 auto burst = [&](int t, int next) {
-                    wait(&full[cur], par);
-                    if (hides(t)) {
-                        // it holds keys some row does not see: cleaned beside the
-                        // softmax of the tile's S
-                        if (!bad && (single || x == 1))
-                            pass(&dirty[x], false);
-                        wait(&clean[cur], cleaned >> cur & 1);
-                        cleaned ^= 1u << cur;
+                    wait(&vfull[vc], vpar);
+                    const int fill = cached - (ka + t) * kTile;  // rows of the tile that are cached
+                    if (fill < kTile && (fill & (kBlk - 1)) && !bad) {
+                        // the rest of the last cache block: whatever it holds counts as 0
+                        const int end = (fill + kBlk - 1) / kBlk * kBlk;
+                        for (int c = lane; c < (end - fill) * (D / 8); c += 32)
+                            st_shared_v4(smem_u32(sV + vc * S::TILE) +
+                                             swz(fill + c / (D / 8), c % (D / 8), kTile),
+                                         make_uint4(0u, 0u, 0u, 0u));
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    const bool more_s = next <= last;
-                    if (next < len) {
-                        const bool wrap = cur + 1 == NS;
-                        wait(&full[wrap ? 0 : cur + 1], par ^ wrap);
-                    }
+                    if (next < len)
+                        wait(&kfull[kc], kpar);
                     const bool first = t == (single ? x : 0);
                     wait(&pready[x], np++ & 1);
-                    if (first) {
-                        o_free();
+                    if (first) {  // the epilogue of O's last use has read it
+                        if (no > 0)
+                            wait(&oempty[x], (no - 1) & 1);
                         ++no;
-                        last_use = items;
                     }
                     wait(&turn[x], turns++ & 1);
                     if (bad)
                         return;
-                    const uint64_t vd = vdesc + cur * STEP;
+                    const uint64_t vd = vdesc + vc * STEP;
                     fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kTile / 16; ++ks)
                             mma_ts(tO, tS + ks * 8, vd + ks * (2048 >> 4), ID_O, !first || ks > 0);
+                        mma_commit(&vempty[vc]);
                         if (t == last)
                             mma_commit(&ofull[x]);
                     }
                     __syncwarp();
-                    step_on(true);
-                    if (more_s)
+                    v_on();
+                    if (next <= last)
                         product_s(next);
-                    else if (next < len)
-                        step_on(false);
-                    pass(&turn[1 - x], false);
+                    tell(&turn[1 - x]);
+                    if (next < len && next > last) {
+                        tell(&kempty[kc]);
+                        k_on();
+                    }
                 };
                 auto no_burst = [&] {
                     wait(&turn[x], turns++ & 1);
                     if (!bad)
-                        pass(&turn[1 - x], false);
+                        tell(&turn[1 - x]);
                 };
                 wait(&qfull[qs & 1], (qs >> 1) & 1);
                 if (!single)
@@ -823,49 +895,38 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 if (bad)
                     break;
                 if (!single)
-                    pass(&qempty[(qs + 1 - x) & 1], false);  // the other stream's queries
+                    tell(&qempty[(qs + 1 - x) & 1]);  // the other stream's queries
                 if (cnt == 0)
-                    pass(&qempty[slot & 1], false);
-                auto first_s = [&](bool mine, int t) {
-                    wait(&full[cur], par);
-                    if (bad)
-                        return;
-                    if (!mine) {
-                        step_on(false);
-                        return;
-                    }
-                    fence_after();
-                    product_s(t);
-                };
-                if (single) {  // K0 K1 | V0 K2 | V1 K3 | ..: the groups in turn A's and B's
+                    tell(&qempty[slot & 1]);
+                if (single) {  // K0 K1, then V0 K2 | V1 K3 | ..: in turn A's and B's
                     first_s(x == 0, 0);
                     if (len > 1)
                         first_s(x == 1, 1);
                     for (int t = 0; t < len && !bad; t += 2) {
                         if (x == 1) {
-                            skip_v(t);
+                            skip_v();
                             if (t + 2 < len)
-                                skip();
+                                skip_k();
                         }
                         if (t + x < len)
                             burst(t + x, t + x + 2);
                         else
                             no_burst();
                         if (x == 0 && t + 1 < len) {
-                            skip_v(t + 1);
+                            skip_v();
                             if (t + 3 < len)
-                                skip();
+                                skip_k();
                         }
                     }
-                } else {  // K0 | V0 K1 | V1 K2 | ..
+                } else {  // K0, then V0 K1 | V1 K2 | ..
                     first_s(cnt > 0, 0);
                     for (int t = 0; t < len && !bad; ++t) {
                         if (t < cnt) {
                             burst(t, t + 1);
                         } else {
-                            skip_v(t);
+                            skip_v();
                             if (t + 1 < len)
-                                skip();
+                                skip_k();
                             no_burst();
                         }
                     }
@@ -873,165 +934,61 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 qs += single ? 1 : 2;
             }
             // every product issued is done before the tensor memory is freed
-            pass(done, true);
+            if (elect_one())
+                mma_commit(done);
+            __syncwarp();
             bad |= !warp_wait(done, 0);
-        } else {
-            // ----------------------------------------------- cleaning of V
-            uint32_t base = 0, items = 0, dirtied[2] = {0u, 0u};
-            for (bool more = wk.begin(); more && !bad; more = wk.next()) {
-                const CaItem &it = wk.it;
-                const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
-                const int buf = items % kBufs;
-                const int t0 = max(0, (pos0 + 1) / kTile - it.ka);  // first tile with hidden keys
-                bool hit = false;
-                int *cleared = cleared_ptr<D>(a.part) + buf * D;
-                for (int t = t0; t < len && !bad; ++t) {
-                    const int k0 = (it.ka + t) * kTile;
-                    const uint32_t pos =
-                        base + (it.single && t + 1 < len ? 2 * t + 2 : 2 * t + 1);
-                    const int s = pos % NS;
-                    // a products' warp has seen the tile arrive, and waits for `clean`
-                    const bool by_a = it.single && !(t & 1);
-                    if (!warp_wait(by_a ? &dirty[0] : &dirty[1], (by_a ? dirtied[0] : dirtied[1]) & 1) ||
-                        !warp_wait(&full[s], (pos / NS) & 1)) {
-                        bad = true;
-                        break;
-                    }
-                    ++dirtied[by_a ? 0 : 1];
-                    if (t == t0 && lane == 0)
-                        sFlag[buf] = 0;
-                    // CPR chunks of 16 bytes a row, RPW rows at a time, UN of those in flight
-                    constexpr int CPR = D / 8, RPW = 32 / CPR, UN = 8;
-                    const int ch = lane % CPR;
-                    const uint32_t tile = smem_u32(ring + s * S::TILE);
-                    for (int rb = max(0, pos0 + 1 - k0) + lane / CPR; rb - lane / CPR < kTile;
-                         rb += UN * RPW) {
-                        uint4 v[UN];
-                        bool odd = false;
-#pragma unroll
-                        for (int u = 0; u < UN; ++u) {
-                            const int r = min(rb + u * RPW, kTile - 1);
-                            v[u] = ld_shared_v4(tile + swz(r, ch, kTile));
-                        }
-#pragma unroll
-                        for (int u = 0; u < UN; ++u) {
-                            // an exponent of all ones carries into the element's top bit
-                            const uint32_t m = 0x7f807f80u, c = 0x00800080u;
-                            const int r = rb + u * RPW;
-                            odd |= r < kTile && k0 + r < it.c.len &&
-                                   ((((v[u].x & m) + c) | ((v[u].y & m) + c) |
-                                     ((v[u].z & m) + c) | ((v[u].w & m) + c)) &
-                                    0x80008000u) != 0;
-                        }
-#pragma unroll
-                        for (int u = 0; u < UN; ++u) {
-                            const int r = rb + u * RPW;
-                            if (r < kTile && k0 + r >= it.c.len)
-                                st_shared_v4(tile + swz(r, ch, kTile), make_uint4(0u, 0u, 0u, 0u));
-                        }
-                        if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-                            for (int u = 0; u < UN; ++u) {
-                                const int r = rb + u * RPW;
-                                const bool mine = r < kTile && k0 + r < it.c.len;
-                                const uint32_t at = tile + swz(min(r, kTile - 1), ch, kTile);
-                                uint4 w = ld_shared_v4(at);
-                                uint32_t found = 0;
-                                auto word = [&](uint32_t &e, int x) {
-                                    if ((e & 0x7f80u) == 0x7f80u) {
-                                        found |= 1u << x;
-                                        e &= 0xffff0000u;
-                                    }
-                                    if ((e & 0x7f800000u) == 0x7f800000u) {
-                                        found |= 2u << x;
-                                        e &= 0xffffu;
-                                    }
-                                };
-                                word(w.x, 0);
-                                word(w.y, 2);
-                                word(w.z, 4);
-                                word(w.w, 6);
-                                if (!__any_sync(0xffffffffu, mine && found))
-                                    continue;
-                                if (!hit) {  // the item's first
-                                    for (int x = lane; x < D; x += 32)
-                                        __stcg(cleared + x, 0x7fffffff);
-                                    if (lane == 0)
-                                        sFlag[buf] = 1;
-                                    __threadfence();
-                                    __syncwarp();
-                                    hit = true;
-                                }
-                                if (mine && found) {
-                                    st_shared_v4(at, w);
-                                    for (int x = 0; x < 8; ++x)
-                                        if (found >> x & 1)
-                                            atomicMin(cleared + ch * 8 + x, k0 + r);
-                                }
-                            }
-                        }
-                    }
-                    if (hit)
-                        __threadfence();
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&clean[s]);
-                }
-                base += 2 * len;
-                ++items;
-            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSmRegs));
         // ------------------------------------------------------- softmax
         // A row belongs to two threads, of warps w (columns 0 .. 63 of S and the
-        // first half of O's) and w + 4 (the others), which exchange its maximum
+        // first half of O's) and w + 4 (the others), which exchange its maximum.
         constexpr int HK = kTile / 2, HD = D / 2;
         const int x = wi / kSmWarps;           // tile A or B
         const int wq = wi & 3;                 // tensor-memory lanes 32 wq ..
         const int hf = (wi >> 2) & 1;          // the row's half
         const int r = wq * 32 + lane;          // row of the tile
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-        const uint32_t tS = tmem + x * kTile + lane_off, tO = tmem + 256 + x * kTile + lane_off + hf * HD;
-        float *max_mine = sMax + (x * 2 + hf) * kTile + r, *max_other = sMax + (x * 2 + 1 - hf) * kTile + r;
+        const uint32_t tS = tmem + x * kTile + lane_off;
+        const uint32_t tO = tmem + 256 + x * kTile + lane_off + hf * HD;
+        float *max_mine = sMax + (x * 2 + hf) * kTile + r;
+        float *max_other = sMax + (x * 2 + 1 - hf) * kTile + r;
         const uint32_t pair_bar = 1 + x * 4 + wq;  // the barrier of this warp and its other half
-        const bool neg = a.logit_scale < 0.f;
         const float ls = fmaxf(fabsf(a.logit_scale), 1e-30f);
         const float grow = kRescale / ls;
-        const int rtok = r / G, rg = r - rtok * G;
-        uint32_t ns = 0, no = 0, items = 0, halves = 0;
+        uint32_t ns = 0, no = 0, halves = 0;
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
-        CaWalk wk{a, plan, tpt, {}};
-        for (bool more = wk.begin(); more; more = wk.next()) {
-            const CaItem &it = wk.it;
-            const int len = it.kb - it.ka, pos0 = it.c.len - it.c.n + it.tok0;
-            const bool single = it.single;
+        while (const CaDesc *dp = enter()) {
+            const bool single = dp->ntok <= tpt;
+            const int len = dp->kb - dp->ka, pos0 = dp->pos0;
             const int tile_tok = single || x == 0 ? 0 : tpt;       // its first token in the item
-            const int toks = min(it.ntok - tile_tok, tpt);         // its tokens
-            const int rows = toks * G;
-            const int tok = min(rtok, toks - 1);                   // rows past the last follow it
+            const int toks = min(dp->ntok - tile_tok, tpt);        // its tokens
+            const int tok = min(r / G, toks - 1);                  // rows past the last follow it
             const int lim = pos0 + tile_tok + tok + 1;             // keys the row sees
-            const int wlim = __shfl_sync(0xffffffffu, lim, 0);     // ... the warp's first row
-            const bool live = wq * 32 < rows;
-            const int na = (pos0 + min(it.ntok, tpt) + kTile - 1) / kTile;
-            const int cnt = single ? (x == 0 ? (len + 1) / 2 : len / 2)
-                                   : (x == 0 ? max(0, min(it.kb, na) - it.ka) : len);
+            const bool live = wq * 32 < toks * G;
+            int cnt = single ? (len + 1 - x) / 2 : len;            // key tiles
+            if (!single && x == 0)
+                cnt = max(0, min(dp->kb, (pos0 + tpt + kTile - 1) / kTile) - dp->ka);
             if (lent && cnt > 0) {  // A has taken what B left in place of its maxima
                 if (!bad && !ca_wait(taken, halves++ & 1))
                     bad = true;
                 bad = __any_sync(0xffffffffu, bad);
                 lent = false;
             }
+            // keys the thread's half of the next tile still holds for the row, and
+            // for the warp's first row: fewer than all, and the tile is masked
+            int m_lim = lim - (dp->ka + (single ? x : 0)) * kTile - hf * HK;
+            const int m_slack = __shfl_sync(0xffffffffu, lim, 0) - lim;
+            const int m_step = single ? 2 * kTile : kTile;
             float mref = -INFINITY, negm = 0.f;
-            float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-            for (int t = 0; t < cnt; ++t) {
-                const int k0 = (it.ka + (single ? 2 * t + x : t)) * kTile;
+            float l0 = 0.f, l1 = 0.f;
+            for (int t = 0; t < cnt; ++t, m_lim -= m_step) {
                 if (!bad && !ca_wait(&sfull[x], ns & 1))
                     bad = true;
                 ++ns;
                 bad = __any_sync(0xffffffffu, bad);
-                if (bad) {  // a warp that gave up still passes every barrier of its pair
+                if (bad) {
                     if (live)
                         bar_sync(pair_bar, 64);
                     continue;
@@ -1044,16 +1001,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         ld16(tS + hf * HK + o, sr, o);
                     ld_wait(sr);
                     float *s = reinterpret_cast<float *>(sr);
-                    if (neg) {
+                    if (a.logit_scale < 0.f) {
 #pragma unroll
                         for (int c = 0; c < HK; ++c)
                             s[c] = -s[c];
                     }
-                    if (k0 + kTile > wlim) {
-                        const int m = lim - k0 - hf * HK;
+                    if (m_lim + m_slack < HK) {
 #pragma unroll
                         for (int c = 0; c < HK; ++c)
-                            s[c] = c < m ? s[c] : -INFINITY;
+                            s[c] = c < m_lim ? s[c] : -INFINITY;
                     }
                     float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -1077,24 +1033,17 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         f = fresh ? 0.f : ex2_approx(negm - old);
                         l0 *= f;
                         l1 *= f;
-                        l2 *= f;
-                        l3 *= f;
                     }
 #pragma unroll
                     for (int c = 0; c < HK; c += 32) {
                         uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
+                        for (int e = 0; e < 32; e += 2) {
                             fma2(s[c + e], s[c + e + 1], ls, negm);
-                            fma2(s[c + e + 2], s[c + e + 3], ls, negm);
                             s[c + e] = ex2_approx(s[c + e]);
                             s[c + e + 1] = ex2_approx(s[c + e + 1]);
-                            s[c + e + 2] = ex2_approx(s[c + e + 2]);
-                            s[c + e + 3] = ex2_approx(s[c + e + 3]);
                             add2(l0, l1, s[c + e], s[c + e + 1]);
-                            add2(l2, l3, s[c + e + 2], s[c + e + 3]);
                             pk[e / 2] = pack_bf16x2(s[c + e], s[c + e + 1]);
-                            pk[e / 2 + 1] = pack_bf16x2(s[c + e + 2], s[c + e + 3]);
                         }
                         st16(tS + hf * (HK / 2) + c / 2, pk, 0);
                     }
@@ -1121,25 +1070,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     mbar_arrive(&pready[x]);
             }
             // ----------------------------------------------------- epilogue
-            float l = (l0 + l1) + (l2 + l3);
+            const CaDesc &d = *dp;
+            float l = l0 + l1;
             float m = mref == -INFINITY ? -INFINITY : -negm;  // base 2, scaled
             if (cnt > 0) {
                 if (!bad && !ca_wait(&ofull[x], no & 1))
                     bad = true;
                 ++no;
                 fence_after();
-            }
-            bad = __any_sync(0xffffffffu, bad);
-            if (cnt > 0) {  // the other half's sum
-                *max_mine = l;
+                bad = __any_sync(0xffffffffu, bad);
+                *max_mine = l;  // the other half's sum
                 bar_sync(pair_bar, 64);
                 const float other = *max_other;
                 l = hf == 0 ? l + other : other + l;
                 bar_sync(pair_bar, 64);  // read before the next maximum is written
             }
-            const int buf = items % kBufs;
-            ++items;
-            const bool whole = it.ka == 0 && it.kb == it.kt;
+            const bool whole = d.ka == 0 && d.kb == d.kt;
             const bool join = single && len > 1;  // B holds the odd key tiles
             if (single && x == 1) {
                 if (join) {  // A reads both halves of O: the lanes are the same
@@ -1150,6 +1096,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     if (lane == 0)
                         mbar_arrive(half);
                 }
+                leave();
                 continue;
             }
             float fa = 1.f, fb = 0.f;
@@ -1169,12 +1116,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 m = mm;
                 l = l * fa + lb * fb;
             }
-            // only the tiles that were cleaned order the flag before this read
-            const int last_tile = it.ka + (single ? len : cnt) - 1;
-            const bool poisoned =
-                !bad && cnt > 0 && (last_tile + 1) * kTile > pos0 + 1 && sFlag[buf] != 0;
             const bool read_o = cnt > 0 && live && !bad;
-            // XC columns of O, the halves joined, poisoned ones NaN
+            // XC columns of O, the halves joined
             auto load_o = [&](int c, uint32_t (&v)[XC]) {
                 if (read_o) {
 #pragma unroll
@@ -1193,12 +1136,6 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                                    __uint_as_float(w[e]) * fb);
                     } else {
                         ld_wait(v);
-                    }
-                    if (poisoned) {
-#pragma unroll
-                        for (int e = 0; e < XC; ++e)
-                            if (__ldcg(cleared_ptr<D>(a.part) + buf * D + hf * HD + c + e) < lim)
-                                v[e] = 0x7fffffffu;
                     }
                 } else {
 #pragma unroll
@@ -1222,31 +1159,37 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             float *slot = nullptr;
             if (!whole) {
                 // the shares the item is cut over: lane k looks at share bs + k
-                bs = static_cast<int>(quotient(it.x, plan.share));
+                bs = static_cast<int>(quotient(d.x, plan.share));
                 const int b = bs + lane;
                 bool some = false;
                 if (b < plan.ctas) {
                     const long long lo = share_border(plan, b), hi = share_border(plan, b + 1);
-                    if (lo < it.x + it.w) {
-                        const int k0 = lo > it.x ? cut_tile(lo - it.x, it.kt) : 0;
-                        const int k1 = hi < it.x + it.w ? cut_tile(hi - it.x, it.kt) : it.kt;
+                    if (lo < d.x + d.w) {
+                        const int k0 = lo > d.x ? cut_tile(lo - d.x, d.kt) : 0;
+                        const int k1 = hi < d.x + d.w ? cut_tile(hi - d.x, d.kt) : d.kt;
                         some = k0 < k1;
                     }
                 }
                 parts = __ballot_sync(0xffffffffu, some);
-                slot = slot_ptr<D>(a.part, 2 * blockIdx.x + (it.ka == 0));
+                slot = slot_ptr<D>(a.part, 2 * blockIdx.x + (d.ka == 0));
             }
+            const bool mine = r < toks * G;
             const int row = x * kTile + r;  // within a slot
-            const size_t tok_row = static_cast<size_t>(it.c.first + it.tok0 + tile_tok + rtok);
-            __nv_bfloat16 *dst = a.out + (tok_row * a.Hq + it.h * G + rg) * D + hf * HD;
+            __nv_bfloat16 *dst =
+                a.out +
+                (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + d.h * G + r % G) * D + hf * HD;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            float odd = 0.f;  // becomes NaN with any element of O
 #pragma unroll 1
             for (int c = 0; c < HD; c += XC) {
                 uint32_t v[XC];
                 load_o(c, v);
                 if (c + XC >= HD)
                     o_done();
-                if (r < rows && !bad) {
+#pragma unroll
+                for (int e = 0; e < XC; ++e)
+                    odd += __uint_as_float(v[e]) * 0.f;
+                if (mine && !bad) {
                     if (whole) {
 #pragma unroll
                         for (int e = 0; e < XC; e += 16) {
@@ -1270,10 +1213,61 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     }
                 }
             }
-            if (whole)
+            // Not finite, and values hidden from the row lay in its tiles: the row's
+            // half once more, a row a warp, from the keys that it sees
+            unsigned again = __ballot_sync(
+                0xffffffffu, mine && !bad && odd != odd && lim < min(d.len, d.kb * kTile));
+            __syncwarp();
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                const int lim_r = __shfl_sync(0xffffffffu, lim, src);
+                const float m_r = __shfl_sync(0xffffffffu, m, src);
+                const float inv_r = __shfl_sync(0xffffffffu, inv, src);
+                const int rr = wq * 32 + src;
+                constexpr int QE = D / 32, OE = HD / 32;  // elements a lane of q and of O
+                const size_t tk = static_cast<size_t>(d.row0 + tile_tok + rr / G);
+                const int hq = d.h * G + rr % G;
+                float q[QE], o[OE];
+#pragma unroll
+                for (int e = 0; e < QE; ++e)
+                    q[e] = __bfloat162float(a.q[tk * a.q_stride + hq * D + e * 32 + lane]);
+#pragma unroll
+                for (int e = 0; e < OE; ++e)
+                    o[e] = 0.f;
+                for (int key = d.ka * kTile; key < min(lim_r, d.kb * kTile); ++key) {
+                    int blk = a.tables[static_cast<size_t>(d.row) * a.stride + key / kBlk];
+                    blk = blk < 0 || blk >= a.num_blocks ? 0 : blk;
+                    const size_t at =
+                        ((static_cast<size_t>(blk) * a.Hkv + d.h) * kBlk + key % kBlk) * D;
+                    float s = 0.f;
+#pragma unroll
+                    for (int e = 0; e < QE; ++e)
+                        s = fmaf(q[e], __bfloat162float(a.kpool[at + e * 32 + lane]), s);
+#pragma unroll
+                    for (int w = 16; w; w >>= 1)
+                        s += __shfl_xor_sync(0xffffffffu, s, w);
+                    const float p =
+                        ex2_approx(fmaf(a.logit_scale < 0.f ? -s : s, ls, -m_r));
+#pragma unroll
+                    for (int e = 0; e < OE; ++e)
+                        o[e] = fmaf(p, __bfloat162float(a.vpool[at + hf * HD + e * 32 + lane]), o[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < OE; ++e) {
+                    const int c = hf * HD + e * 32 + lane;
+                    if (whole)
+                        a.out[(tk * a.Hq + hq) * D + c] = __float2bfloat16_rn(o[e] * inv_r);
+                    else
+                        slot[static_cast<size_t>(x * kTile + rr) * D + c] = o[e];
+                }
+            }
+            if (whole) {
+                leave();
                 continue;
+            }
             // a partial result: the last of the item's shares to arrive joins them
-            if (r < rows && hf == 0)
+            if (mine && hf == 0)
                 reinterpret_cast<float2 *>(slot + 2 * kTile * D)[row] = make_float2(m, l);
             __threadfence();
             bar_sync(9 + x, 32 * kSmWarps);
@@ -1282,44 +1276,46 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 sLast[x] = atomicInc(&a.arrived[2 * bs + x], n - 1) == n - 1;
             }
             bar_sync(9 + x, 32 * kSmWarps);
-            if (!sLast[x])
-                continue;
-            __threadfence();
-            constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes a row, rows a warp
-            const int first = __ffs(parts) - 1;
-            for (int rr = (hf * 4 + wq) * RPW + lane / LPR; rr < rows; rr += kSmWarps * RPW) {
-                const int cc = (lane % LPR) * 4;
-                const int srow = x * kTile + rr;
-                float M = -INFINITY;
-                for (unsigned q = parts; q; q &= q - 1) {
-                    const int k = __ffs(q) - 1;
-                    const float *sp = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
-                    M = fmaxf(M, __ldcg(reinterpret_cast<const float2 *>(sp + 2 * kTile * D) + srow).x);
+            if (sLast[x]) {
+                __threadfence();
+                constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes a row, rows a warp
+                const int first = __ffs(parts) - 1;
+                for (int rr = (hf * 4 + wq) * RPW + lane / LPR; rr < toks * G;
+                     rr += kSmWarps * RPW) {
+                    const int cc = (lane % LPR) * 4;
+                    const int srow = x * kTile + rr;
+                    float M = -INFINITY;
+                    for (unsigned q = parts; q; q &= q - 1) {
+                        const int k = __ffs(q) - 1;
+                        const float *sp = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
+                        M = fmaxf(M, __ldcg(reinterpret_cast<const float2 *>(sp + 2 * kTile * D) +
+                                            srow).x);
+                    }
+                    float L = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (unsigned q = parts; q; q &= q - 1) {
+                        const int k = __ffs(q) - 1;
+                        const float *sp = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
+                        const float2 ml =
+                            __ldcg(reinterpret_cast<const float2 *>(sp + 2 * kTile * D) + srow);
+                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(
+                            sp + static_cast<size_t>(srow) * D + cc));
+                        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                        L += ml.y * f;
+                        o.x += w.x * f;
+                        o.y += w.y * f;
+                        o.z += w.z * f;
+                        o.w += w.w * f;
+                    }
+                    const float iv = L == 0.f ? 0.f : 1.f / L;
+                    __nv_bfloat16 *d2 =
+                        a.out + (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq + d.h * G +
+                                 rr % G) * D + cc;
+                    *reinterpret_cast<uint2 *>(d2) =
+                        make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
                 }
-                float L = 0.f;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (unsigned q = parts; q; q &= q - 1) {
-                    const int k = __ffs(q) - 1;
-                    const float *sp = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
-                    const float2 ml =
-                        __ldcg(reinterpret_cast<const float2 *>(sp + 2 * kTile * D) + srow);
-                    const float4 w = __ldcg(reinterpret_cast<const float4 *>(
-                        sp + static_cast<size_t>(srow) * D + cc));
-                    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-                    L += ml.y * f;
-                    o.x += w.x * f;
-                    o.y += w.y * f;
-                    o.z += w.z * f;
-                    o.w += w.w * f;
-                }
-                const float iv = L == 0.f ? 0.f : 1.f / L;
-                const int tk = rr / G;
-                __nv_bfloat16 *d2 =
-                    a.out + (static_cast<size_t>(it.c.first + it.tok0 + tile_tok + tk) * a.Hq +
-                             it.h * G + rr - tk * G) * D + cc;
-                *reinterpret_cast<uint2 *>(d2) =
-                    make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
             }
+            leave();
         }
     }
     if (bad)

@@ -110,24 +110,29 @@ def test_scores_that_climb_or_fall(rise):
 
 def test_hidden_tokens_do_not_reach_a_row():
     """Not-finite keys and values at positions a token does not see leave its
-    output as it is, bit for bit."""
-    spans = [(40, 200), (130, 130), (300, 1000)]
+    output within the bound of the clean 64-bit result (rows that shared a tile
+    with them are computed again in another order of additions)."""
+    spans = [(40, 200), (130, 130), (300, 1000), (9, 515)]
     b = Batch(spans, 2, 8, 128, seed=5)
     cache = b.cache()
-    b.attn(cache)
-    clean = b.out.clone()
+    want = []
+    for i, (n, T) in enumerate(spans):
+        k, v = b.rows_of(i)
+        a = int(b.starts_np[i])
+        want.append(attn_ref(b.q[a:a + n], k, v, b.scale))
     for i, (n, T) in enumerate(spans):
         cut = T - n // 2  # positions from here on are poisoned
         for pool, bad in ((b.kp[0], math.nan), (b.vp[0], math.inf)):
             pos = torch.arange(cut, T, device=b.dev)
             blk = b.tables[i].long()[pos // B]
             pool[blk, :, pos % B] = bad
-    b.out.fill_(7.0)
     b.attn(cache)
+    assert cache.status() == zp.OK
     for i, (n, T) in enumerate(spans):
         a = int(b.starts_np[i])
         m = n - n // 2
-        assert torch.equal(_bits(b.out[a:a + m]), _bits(clean[a:a + m])), i
+        err = (b.out[a:a + m].double() - want[i][0][:m]).abs()
+        assert bool((err <= want[i][1][:m]).all()), i
         assert not bool(torch.isfinite(b.out[a + m:a + n]).any()), i
 
 
@@ -136,14 +141,15 @@ def test_hidden_tokens_do_not_reach_a_row():
 def test_visible_value_that_is_not_finite(t, bad):
     b = Batch([(60, 300)], 1, 4, 64, seed=6, heavy=0.0)
     cache = b.cache()
-    b.attn(cache)
-    clean = b.out.clone()
+    k, v = b.rows_of(0)
+    want, tol = attn_ref(b.q, k, v, b.scale)
     b.vp[0][b.tables[0, t // B].long(), 0, t % B, 5] = bad
     b.attn(cache)
+    assert cache.status() == zp.OK
     hit = torch.zeros(60, 4, 64, dtype=torch.bool, device=b.dev)
     hit[max(0, t - 240):, :, 5] = True
     assert not bool(torch.isfinite(b.out[hit]).any())
-    assert torch.equal(_bits(b.out[~hit]), _bits(clean[~hit]))
+    assert bool(((b.out.double() - want).abs() <= tol)[~hit].all())
 
 
 def test_query_that_is_not_finite_stays_in_its_row():
