@@ -280,16 +280,12 @@ struct CaWalk {
 // swizzle.  K-major: 8-row groups 1024 bytes apart (the leading offset is not
 // used).  MN-major: groups of 8 along K 1024 bytes apart, panels of 64 along
 // N `lead` bytes apart.
-__device__ __forceinline__ uint64_t ca_desc(uint32_t saddr, uint32_t lead)
+// Only the low word differs between operands of one layout.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead)
 {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3ffffu) >> 4);
-    d |= static_cast<uint64_t>(lead >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+    return ((saddr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // kind::f16, bf16 x bf16 -> fp32, M = 128, N = n, A K-major, B K- or MN-major.
 __host__ __device__ constexpr uint32_t ca_idesc(int n, bool b_mn)
@@ -298,25 +294,27 @@ __host__ __device__ constexpr uint32_t ca_idesc(int n, bool b_mn)
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kTile >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc,
                                        uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc,
                                        uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(blo), "r"(idesc), "r"(accumulate), "n"(kDescHi)
         : "memory");
 }
 
@@ -760,8 +758,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             constexpr uint32_t ID_S = ca_idesc(kTile, false), ID_O = ca_idesc(D, true);
             constexpr uint32_t STEP = S::TILE >> 4;
             const int x = wi - kMmaWarp;
-            const uint64_t qdesc = ca_desc(smem_u32(sQ), 16), kdesc = ca_desc(smem_u32(sK), 16);
-            const uint64_t vdesc = ca_desc(smem_u32(sV), S::PANEL);
+            const uint32_t qdesc = desc_lo(smem_u32(sQ), 16), kdesc = desc_lo(smem_u32(sK), 16);
+            const uint32_t vdesc = desc_lo(smem_u32(sV), S::PANEL);
             const uint32_t tS = tmem + x * kTile, tO = tmem + 256 + x * kTile;
             uint32_t kc = 0, kpar = 0, vc = 0, vpar = 0;  // ring cursors and parities
             uint32_t qs = 0, np = 0, no = 0, turns = 0;
@@ -796,7 +794,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 const int cnt = single ? (len + 1 - x) / 2 : max(0, min(kb, na) - ka);
                 const int last = single ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
                 const uint32_t slot = single ? qs : qs + x;
-                const uint64_t qd = qdesc + (slot & 1) * STEP;
+                const uint32_t qd = __shfl_sync(0xffffffffu, qdesc + (slot & 1) * STEP, 0);
                 auto skip_k = [&] {  // a tile of the other stream's
                     wait(&kfull[kc], kpar);
                     if (bad)
@@ -811,21 +809,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     tell(&vempty[vc]);
                     v_on();
                 };
-                auto product_s = [&](int t) {  // S with K tile t, which has arrived
-                    const uint64_t kd = kdesc + kc * STEP;
-                    if (elect_one()) {
+                auto issue_s = [&](uint32_t kd, int from, int to) {
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t o = ((ks >> 2) * S::PANEL + (ks & 3) * 32) >> 4;
-                            mma_ss(tS, qd + o, kd + o, ID_S, ks > 0);
-                        }
-                        mma_commit(&sfull[x]);
-                        mma_commit(&kempty[kc]);
-                        if (t == last)
-                            mma_commit(&qempty[slot & 1]);
+                    for (int ks = from; ks < to; ++ks) {
+                        const uint32_t o = ((ks >> 2) * S::PANEL + (ks & 3) * 32) >> 4;
+                        mma_ss(tS, qd + o, kd + o, ID_S, ks > 0);
                     }
-                    __syncwarp();
-                    k_on();
+                };
+                auto done_s = [&](int t) {
+                    mma_commit(&sfull[x]);
+                    mma_commit(&kempty[kc]);
+                    if (t == last)
+                        mma_commit(&qempty[slot & 1]);
                 };
                 auto first_s = [&](bool mine, int t) {
                     if (!mine) {
@@ -836,7 +831,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     if (bad)
                         return;
                     fence_after();
-                    product_s(t);
+                    const uint32_t kd = __shfl_sync(0xffffffffu, kdesc + kc * STEP, 0);
+                    if (elect_one()) {
+                        issue_s(kd, 0, D / 16);
+                        done_s(t);
+                    }
+                    __syncwarp();
+                    k_on();
                 };
                 // P V with V tile t, then S with K tile `next`
                 auto burst = [&](int t, int next) {
@@ -855,16 +856,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     if (next < len)
                         wait(&kfull[kc], kpar);
                     const bool first = t == (single ? x : 0);
-                    wait(&pready[x], np++ & 1);
                     if (first) {  // the epilogue of O's last use has read it
                         if (no > 0)
                             wait(&oempty[x], (no - 1) & 1);
                         ++no;
                     }
+                    const uint32_t vd = __shfl_sync(0xffffffffu, vdesc + vc * STEP, 0);
+                    const uint32_t kd = __shfl_sync(0xffffffffu, kdesc + kc * STEP, 0);
+                    const bool more_s = next <= last;
                     wait(&turn[x], turns++ & 1);
+                    wait(&pready[x], np++ & 1);
                     if (bad)
                         return;
-                    const uint64_t vd = vdesc + vc * STEP;
                     fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -873,12 +876,20 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         mma_commit(&vempty[vc]);
                         if (t == last)
                             mma_commit(&ofull[x]);
+                        // the other stream wakes up while the rest is queued
+                        if (more_s) {
+                            issue_s(kd, 0, D / 32);
+                            mbar_arrive(&turn[1 - x]);
+                            issue_s(kd, D / 32, D / 16);
+                            done_s(next);
+                        } else {
+                            mbar_arrive(&turn[1 - x]);
+                        }
                     }
                     __syncwarp();
                     v_on();
-                    if (next <= last)
-                        product_s(next);
-                    tell(&turn[1 - x]);
+                    if (more_s)
+                        k_on();
                     if (next < len && next > last) {
                         tell(&kempty[kc]);
                         k_on();
