@@ -207,7 +207,8 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
              zp::encode_row_map(&krmaps[l], D.k_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim) &&
              zp::encode_row_map(&vrmaps[l], D.v_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim);
     }
-    ok = ok && cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
+    ok = ok && zp::prepare_chunk_attn(D.head_dim) == cudaSuccess &&
+         cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
          cudaMemset(b + o_rowmark, 0, 4 * static_cast<size_t>(D.max_requests)) == cudaSuccess &&
          cudaMemset(b + o_ap_call, 0, o_ap_occ - o_ap_call) == cudaSuccess &&
          cudaMemset(b + o_ca_arr, 0, 8 * static_cast<size_t>(c->num_sms)) == cudaSuccess &&
@@ -923,7 +924,7 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
     a.accepted = accepted;
     a.next = next_tokens;
     a.sticky = c->ws.sticky;
-    return zp::launch_verify_draft(a, prob_dtype == ZP_DTYPE_BF16,
+    return zp::launch_verify_draft(a, prob_dtype == ZP_DTYPE_BF16, c->num_sms,
                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? ZP_OK
                : ZP_ERR_CUDA;

@@ -69,7 +69,9 @@ size_t chunk_attn_part_floats(int d, int sms);
 // The map ChunkAttnArgs::qmap of a packed q (tokens `stride` elements apart).
 bool encode_chunk_q_map(CUtensorMap *map, const void *q, int total, int64_t stride, int Hq, int G,
                         int d);
-cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, int sms, cudaStream_t s);
+// Once a device, before launch_chunk_attn.
+cudaError_t prepare_chunk_attn(int d);
 
 #ifdef __CUDACC__
 

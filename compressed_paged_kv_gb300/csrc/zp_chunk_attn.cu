@@ -1341,14 +1341,20 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
 }
 
+cudaError_t prepare_chunk_attn(int d)
+{
+    return d == 64 ? cudaFuncSetAttribute(zp_chunk_attn_kernel<64>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          CaSmem<64>::BYTES)
+                   : cudaFuncSetAttribute(zp_chunk_attn_kernel<128>,
+                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          CaSmem<128>::BYTES);
+}
+
 template <int D>
 static cudaError_t launch_chunk_attn_t(const ChunkAttnArgs &a, int sms, cudaStream_t s)
 {
     using S = CaSmem<D>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        zp_chunk_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
-    if (e != cudaSuccess)
-        return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

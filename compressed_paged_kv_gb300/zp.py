@@ -224,27 +224,23 @@ def zp_fork_rows(handle, block_tables, bt_stride, num_rows, lengths, src_rows, d
 
 def zp_append_kv_chunk(handle, layer, k_new, k_stride, v_new, v_stride, starts, total,
                        block_tables, bt_stride, num_rows, lengths, req_idx, R, stream) -> int:
-    return lib().zp_append_kv_chunk(P(handle), layer, P(k_new), k_stride, P(v_new), v_stride,
-                                    P(starts), total, P(block_tables), bt_stride, num_rows,
-                                    P(lengths), P(req_idx or None), R, P(stream or None))
+    # plain integers: their pointer arguments are declared, so ctypes converts them
+    return lib().zp_append_kv_chunk(handle, layer, k_new, k_stride, v_new, v_stride, starts, total,
+                                    block_tables, bt_stride, num_rows, lengths, req_idx, R, stream)
 
 
 def zp_paged_chunk_attn(handle, layer, q, q_stride, starts, total, block_tables, bt_stride,
                         num_rows, lengths, req_idx, R, scale, out, stream) -> int:
-    return lib().zp_paged_chunk_attn(P(handle), layer, P(q), q_stride, P(starts), total,
-                                     P(block_tables), bt_stride, num_rows, P(lengths),
-                                     P(req_idx or None), R, float(scale), P(out),
-                                     P(stream or None))
+    return lib().zp_paged_chunk_attn(handle, layer, q, q_stride, starts, total, block_tables,
+                                     bt_stride, num_rows, lengths, req_idx, R, scale, out, stream)
 
 
 def zp_verify_draft(handle, tokens, starts, total, target_probs, draft_probs, prob_dtype, vocab,
                     prob_stride, accept_u, sample_u, lengths, num_rows, req_idx, R, accepted,
                     next_tokens, stream) -> int:
-    return lib().zp_verify_draft(P(handle), P(tokens), P(starts), total, P(target_probs),
-                                 P(draft_probs or None), prob_dtype, vocab, prob_stride,
-                                 P(accept_u), P(sample_u), P(lengths or None), num_rows,
-                                 P(req_idx or None), R, P(accepted), P(next_tokens),
-                                 P(stream or None))
+    return lib().zp_verify_draft(handle, tokens, starts, total, target_probs, draft_probs,
+                                 prob_dtype, vocab, prob_stride, accept_u, sample_u, lengths,
+                                 num_rows, req_idx, R, accepted, next_tokens, stream)
 
 
 def zp_global_redundancy(handle, block_tables, bt_stride, num_rows, lengths, req_idx, R, red_out,
@@ -275,29 +271,38 @@ def _ptr(t):
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    # the handle of the current stream without building a Stream object (3 us
+    # less a call), where torch has it
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _row_stride(t, what, inner, dtype):
     """Elements between the rows of a packed tensor [total, *inner] whose rows
     are each contiguous."""
+    shape, strides = t.shape, t.stride()
     n = 1
-    for dim, size in zip(reversed(range(1, t.dim())), reversed(inner)):
-        if t.shape[dim] != size or (t.stride(dim) != n and size > 1):
-            raise ValueError(f"{what} must be [total, {', '.join(map(str, inner))}] with "
-                             f"contiguous rows, got {tuple(t.shape)} strides {t.stride()}")
+    ok = len(shape) == 1 + len(inner) and t.dtype == dtype and t.is_cuda
+    for dim in range(len(inner), 0, -1):
+        if not ok:
+            break
+        size = inner[dim - 1]
+        ok = shape[dim] == size and (strides[dim] == n or size <= 1)
         n *= size
-    if t.dim() != 1 + len(inner) or t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{what} must be a {1 + len(inner)}-D {dtype} CUDA tensor")
-    return t.stride(0) if t.shape[0] > 1 else n
+    if not ok:
+        raise ValueError(f"{what} must be a {dtype} CUDA tensor [total, "
+                         f"{', '.join(map(str, inner))}] with contiguous rows, got {t.dtype} "
+                         f"{tuple(shape)} strides {strides}")
+    return strides[0] if shape[0] > 1 else n
 
 
-def _ints(t, what, n, dtype=None):
-    import torch
-    dtype = dtype or torch.int32
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+def _flat(t, what, n, dtype):
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor of {n} elements")
 
 
@@ -312,6 +317,7 @@ class Cache:
                 raise ValueError("pools must be contiguous 4-D bf16 CUDA tensors")
         nb, hkv, b, d = k_pools[0].shape
         self.k_pools, self.v_pools = list(k_pools), list(v_pools)
+        self.dtype, self.int32, self.float32 = torch.bfloat16, torch.int32, torch.float32
         self.L, self.Hkv, self.Hq, self.d, self.b, self.num_blocks = (
             len(k_pools), hkv, num_q_heads, d, b, nb)
         kp = (P * self.L)(*[t.data_ptr() for t in k_pools])
@@ -402,16 +408,17 @@ class Cache:
                         stream=None, check=True):
         """k_new, v_new: [total, Hkv, d] bf16, each token's row contiguous (a
         slice of a packed projection output is passed as it is)."""
-        ks = _row_stride(k_new, "k_new", (self.Hkv, self.d), self.k_pools[0].dtype)
-        vs = _row_stride(v_new, "v_new", (self.Hkv, self.d), self.k_pools[0].dtype)
-        if k_new.shape[0] != v_new.shape[0]:
+        row = (self.Hkv, self.d)
+        ks = _row_stride(k_new, "k_new", row, self.dtype)
+        vs = _row_stride(v_new, "v_new", row, self.dtype)
+        total = k_new.shape[0]
+        if v_new.shape[0] != total:
             raise ValueError("k_new and v_new must hold the same tokens")
-        R = starts.numel() - 1
-        self._chunk_ints(starts, block_tables, lengths, req_idx, R)
+        R, rows = self._chunk_ints(starts, block_tables, lengths, req_idx)
         st = zp_append_kv_chunk(self.handle, layer, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-                                starts.data_ptr(), k_new.shape[0], block_tables.data_ptr(),
-                                block_tables.shape[1], block_tables.shape[0],
-                                lengths.data_ptr(), _ptr(req_idx), R, _stream(stream))
+                                starts.data_ptr(), total, block_tables.data_ptr(),
+                                block_tables.shape[1], rows, lengths.data_ptr(), _ptr(req_idx), R,
+                                _stream(stream))
         if check and st != OK:
             raise ZpError(st, "zp_append_kv_chunk")
         return st
@@ -420,61 +427,61 @@ class Cache:
                    stream=None, check=True):
         """q: [total, Hq, d] bf16, each token's row contiguous; out: the same
         shape, contiguous."""
-        qs = _row_stride(q, "q", (self.Hq, self.d), self.k_pools[0].dtype)
-        _ints(out, "out", q.numel(), self.k_pools[0].dtype)
-        R = starts.numel() - 1
-        self._chunk_ints(starts, block_tables, lengths, req_idx, R)
+        qs = _row_stride(q, "q", (self.Hq, self.d), self.dtype)
+        _flat(out, "out", q.numel(), self.dtype)
+        R, rows = self._chunk_ints(starts, block_tables, lengths, req_idx)
         st = zp_paged_chunk_attn(self.handle, layer, q.data_ptr(), qs, starts.data_ptr(),
-                                 q.shape[0], block_tables.data_ptr(), block_tables.shape[1],
-                                 block_tables.shape[0], lengths.data_ptr(), _ptr(req_idx), R,
-                                 scale, out.data_ptr(), _stream(stream))
+                                 q.shape[0], block_tables.data_ptr(), block_tables.shape[1], rows,
+                                 lengths.data_ptr(), _ptr(req_idx), R, scale, out.data_ptr(),
+                                 _stream(stream))
         if check and st != OK:
             raise ZpError(st, "zp_paged_chunk_attn")
         return st
 
-    def _chunk_ints(self, starts, block_tables, lengths, req_idx, R):
-        _ints(starts, "starts", 1)
-        _ints(block_tables, "block_tables", 1)
+    def _chunk_ints(self, starts, block_tables, lengths, req_idx):
+        """Checks the index tensors of a chunk call: (chunks, table rows)."""
+        i32 = self.int32
+        R = starts.shape[0] - 1
         rows = block_tables.shape[0]
-        _ints(lengths, "lengths", rows)
+        _flat(starts, "starts", 1, i32)
+        _flat(block_tables, "block_tables", 1, i32)
+        _flat(lengths, "lengths", rows, i32)
         if req_idx is not None:
-            _ints(req_idx, "req_idx", R)
+            _flat(req_idx, "req_idx", R, i32)
         elif R > rows:
             raise ValueError(f"{R} chunks for {rows} table rows")
+        return R, rows
 
     def verify_draft(self, tokens, starts, target_probs, accept_u, sample_u, accepted,
                      next_tokens, draft_probs=None, lengths=None, req_idx=None, stream=None,
                      check=True):
         """target_probs, draft_probs: [total, vocab] fp32 or bf16 with the same
         row stride."""
-        import torch
-        if target_probs.dim() != 2:
-            raise ValueError("target_probs must be [total, vocab]")
+        i32, f32, dtype = self.int32, self.float32, target_probs.dtype
+        if target_probs.dim() != 2 or dtype not in (f32, self.dtype):
+            raise ValueError("target_probs must be [total, vocab], float32 or bfloat16")
         total, vocab = target_probs.shape
-        dtype = target_probs.dtype
-        if dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError("target_probs must be float32 or bfloat16")
         ps = _row_stride(target_probs, "target_probs", (vocab,), dtype)
         if draft_probs is not None:
             ds = _row_stride(draft_probs, "draft_probs", (vocab,), dtype)
-            if draft_probs.shape[0] != total or (total > 1 and ds != ps):
+            if draft_probs.shape[0] != total or ds != ps:
                 raise ValueError("draft_probs must have target_probs' rows and row stride")
-        R = starts.numel() - 1
-        _ints(starts, "starts", 1)
-        _ints(tokens, "tokens", total)
-        _ints(accept_u, "accept_u", total, torch.float32)
-        _ints(sample_u, "sample_u", R, torch.float32)
-        _ints(accepted, "accepted", R)
-        _ints(next_tokens, "next_tokens", R)
+        R = starts.shape[0] - 1
+        _flat(starts, "starts", 1, i32)
+        _flat(tokens, "tokens", total, i32)
+        _flat(accept_u, "accept_u", total, f32)
+        _flat(sample_u, "sample_u", R, f32)
+        _flat(accepted, "accepted", R, i32)
+        _flat(next_tokens, "next_tokens", R, i32)
         rows = 0
         if lengths is not None:
-            rows = lengths.numel()
-            _ints(lengths, "lengths", R if req_idx is None else 1)
+            rows = lengths.shape[0]
+            _flat(lengths, "lengths", R if req_idx is None else 1, i32)
             if req_idx is not None:
-                _ints(req_idx, "req_idx", R)
+                _flat(req_idx, "req_idx", R, i32)
         st = zp_verify_draft(self.handle, tokens.data_ptr(), starts.data_ptr(), total,
                              target_probs.data_ptr(), _ptr(draft_probs),
-                             DTYPE_F32 if dtype == torch.float32 else DTYPE_BF16, vocab, ps,
+                             DTYPE_F32 if dtype == f32 else DTYPE_BF16, vocab, ps,
                              accept_u.data_ptr(), sample_u.data_ptr(), _ptr(lengths), rows,
                              _ptr(req_idx), R, accepted.data_ptr(), next_tokens.data_ptr(),
                              _stream(stream))
