@@ -19,21 +19,24 @@
 // Knuth's error-free sums): about 46 bits.  The warps' sums are joined in 64
 // bits.
 //
-// One cluster of kVfCtas CTAs a request.  A warp owns a contiguous run of the
-// deciding row and reads it (of p and q) once, 16 bytes a lane; every CTA gets
+// One cluster of CTAs a request.  A warp owns a contiguous run of the deciding
+// row and reads it (of p and q) once, 16 bytes a lane and kVfBatch of them in
+// flight, leaving its lanes' sums in shared memory now and then; every CTA gets
 // every warp's sum through distributed shared memory, and the warp that the
-// level falls into goes through its own run a second time (out of L2) for the
-// token.  Bound by the bytes of the deciding rows for large batches, and by
-// the chain of dependent reads (offsets -> tokens -> their probabilities ->
-// row -> sums -> run) for small ones.
+// level falls into finds the stretch of its run from the sums it left, reads
+// that a second time (out of L2) and finds the token.  Bound by the bytes of
+// the deciding rows for large batches, and by the chain of dependent reads
+// (offsets -> tokens -> their probabilities -> row -> sums -> stretch) for
+// small ones.
 #include "zp_chunk.cuh"
 
 namespace zp {
 
 namespace {
 
-constexpr int kVfCtas = 8;    // of a cluster: the portable most
+constexpr int kVfCtas = 8;    // of a cluster, at most: the portable most
 constexpr int kVfBatch = 4;   // vectors of p and of q a lane has in flight
+constexpr int kVfMarks = 64;  // sums left by the warps of a CTA, together
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -64,7 +67,7 @@ struct Row {
     const T *p, *q;  // q: null when nothing is taken off
     int skip;        // a token left out, or -1
     int vocab, first, count;
-    bool alike;      // q (if any) lies in its 16-byte vectors as p does
+    int lo, hi;      // the vectors that lie whole in the row and that q (if any) has alike
 
     __device__ __forceinline__ Row(const T *p_, const T *q_, int skip_, int vocab_)
         : p(p_), q(q_), skip(skip_), vocab(vocab_)
@@ -72,24 +75,24 @@ struct Row {
         const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
         first = -mis;
         count = (mis + vocab + VE - 1) / VE;
-        alike = !q || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+        lo = mis ? 1 : 0;
+        hi = first + count * VE == vocab ? count : count - 1;
+        if (q && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15))
+            hi = 0;
     }
 
-    // Weights w + e, exactly, of the elements e0 .. from p (in w) and q (in b).
+    // Weights w + e, exactly, of the elements e0 .. from p (in w) and, with Q, q
+    // (in b).  Only p > q counts, where (p - d) - q is the error of d = p - q.
+    template <bool Q>
     __device__ __forceinline__ void weigh(int e0, float (&w)[VE], const float (&b)[VE],
                                           float (&e)[VE]) const
     {
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
-            float d = w[k], r = 0.f;
-            if (q) {
-                d = w[k] - b[k];
-                const float t = d - w[k];
-                r = (w[k] - (d - t)) - (b[k] + t);
-            }
-            const bool some = d > 0.f && d < INFINITY && e0 + k != skip;
+            const float d = Q ? w[k] - b[k] : w[k];
+            const bool some = d > 0.f && d < INFINITY && (Q || e0 + k != skip);
+            e[k] = Q && some ? (w[k] - d) - b[k] : 0.f;
             w[k] = some ? d : 0.f;
-            e[k] = some ? r : 0.f;
         }
     }
 
@@ -104,16 +107,63 @@ struct Row {
             w[k] = in ? to_f32(p[e0 + k]) : 0.f;
             b[k] = in && q ? to_f32(q[e0 + k]) : 0.f;
         }
-        weigh(e0, w, b, e);
+        if (q)
+            weigh<true>(e0, w, b, e);
+        else
+            weigh<false>(e0, w, b, e);
+    }
+
+    // The vectors v, v + 32, .. (kVfBatch of them) of a row with lo < hi: `take`
+    // gets each one's number and weights, 0 outside lo .. hi - 1.
+    template <bool Q, class F>
+    __device__ __forceinline__ void batch(int v, F take) const
+    {
+        uint4 up[kVfBatch], uq[kVfBatch];
+#pragma unroll
+        for (int u = 0; u < kVfBatch; ++u) {
+            const int at = first + min(max(v + u * 32, lo), hi - 1) * VE;
+            up[u] = ld_global_nc_v4(p + at);
+            if (Q)
+                uq[u] = ld_global_nc_v4(q + at);
+        }
+#pragma unroll
+        for (int u = 0; u < kVfBatch; ++u) {
+            const int i = v + u * 32;
+            float w[VE], b[VE], e[VE];
+            if (i < lo || i >= hi)
+                up[u] = make_uint4(0u, 0u, 0u, 0u);
+            unpack(up[u], w);
+            if (Q)
+                unpack(uq[u], b);
+            weigh<Q>(first + i * VE, w, b, e);
+            take(u, w, e);
+        }
+    }
+
+    // The same of any vectors below `end`, those outside with weight 0.
+    template <class F>
+    __device__ __forceinline__ void ragged(int v, int end, F take) const
+    {
+#pragma unroll 1
+        for (int u = 0; u < kVfBatch; ++u, v += 32) {
+            float w[VE], e[VE];
+            if (v < end) {
+                weights(v, w, e);
+            } else {
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    w[k] = e[k] = 0.f;
+            }
+            take(u, w, e);
+        }
     }
 };
 
-// (s, c) += w + e.
+// (s, c) += w + e, none of them below 0 but e.
 __device__ __forceinline__ void add_exact(float &s, float &c, float w, float e)
 {
     const float t = s + w;
-    const float z = t - s;
-    c += ((s - (t - z)) + (w - z)) + e;
+    c += (fminf(s, w) - (t - fmaxf(s, w))) + e;
     s = t;
 }
 
@@ -140,21 +190,21 @@ __device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v)
 
 }  // namespace
 
-// NT threads a CTA.  Many requests: 128, so that the chains of many clusters
-// run beside each other (1,024 threads an SM are 19 requests' CTAs of 8 warps
-// ... 76 of 4); few: 512, so that one row has as many loads in flight.
+// NT threads a CTA: 128 for many requests, so that the chains of many clusters
+// run beside each other, 512 for few, so that a row has as many loads in
+// flight.
 template <class T, int NT>
-__global__ void __cluster_dims__(kVfCtas, 1, 1) __launch_bounds__(NT, 1024 / NT)
-    zp_verify_kernel(const VerifyArgs a)
+__global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyArgs a, int ctas)
 {
-    constexpr int VE = Row<T>::VE, kVfWarps = NT / 32;
-    constexpr int kVfRuns = kVfCtas * kVfWarps;  // of a row, a warp each
-    __shared__ double sums[2][kVfRuns];  // every run's, by the row's order; one set a pass
+    constexpr int VE = Row<T>::VE, WARPS = NT / 32, MARKS = kVfMarks / WARPS;
+    constexpr int STEP = kVfBatch * 32;           // vectors of a batch
+    __shared__ double sums[2][kVfCtas * WARPS];   // every run's, in the row's order; one set a pass
+    __shared__ float2 marks[WARPS][MARKS][32];    // the lanes' sums after a stretch of the run
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int i = blockIdx.x / kVfCtas;
+    const int i = blockIdx.x / ctas, runs = ctas * WARPS;
     const int first = a.starts[i], end = a.starts[i + 1];
     const bool ok = first >= 0 && end >= first && end <= a.total;
     if (!ok || first == end) {  // the whole cluster alike
@@ -218,64 +268,36 @@ __global__ void __cluster_dims__(kVfCtas, 1, 1) __launch_bounds__(NT, 1024 / NT)
         const bool left = pass == 0 && reject;  // what a rejection leaves; else p itself
         const Row<T> row(target + row_at, left && draft ? draft + row_at : nullptr,
                          left && !draft ? x : -1, a.vocab);
-        // this warp's run of vectors
-        const int per = (row.count + kVfRuns - 1) / kVfRuns;
-        const int run = rank * kVfWarps + wi;
-        const int v0 = min(row.count, run * per), v1 = min(row.count, v0 + per);
+        // this warp's run: whole batches, `stretch` of them to a mark
+        const int per = ((row.count + runs - 1) / runs + STEP - 1) / STEP;
+        const int stretch = (per + MARKS - 1) / MARKS;
+        const int run = rank * WARPS + wi;
+        const int v0 = min(row.count, run * per * STEP), v1 = min(row.count, v0 + per * STEP);
         float s = 0.f, c = 0.f;
-        auto take = [&](float (&w)[VE], const float (&e)[VE]) {
+        auto add = [&](int, const float (&w)[VE], const float (&e)[VE]) {
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 add_exact(s, c, w[k], e[k]);
         };
-        // the vectors that lie whole in the row, kVfBatch a lane at a time
-        const int i0 = max(v0, 1), i1 = row.alike ? min(v1, row.count - 1) : i0;
-        int v = i0 + lane;
-        for (; v - lane + kVfBatch * 32 <= i1; v += kVfBatch * 32) {
-            uint4 up[kVfBatch], uq[kVfBatch];
-            const int e0 = row.first + v * VE;
-#pragma unroll
-            for (int u = 0; u < kVfBatch; ++u) {
-                up[u] = ld_global_nc_v4(row.p + e0 + u * 32 * VE);
+        for (int v = v0, n = 0; v < v1; v += STEP, ++n) {
+            if (row.lo < row.hi) {
                 if (row.q)
-                    uq[u] = ld_global_nc_v4(row.q + e0 + u * 32 * VE);
+                    row.template batch<true>(v + lane, add);
+                else
+                    row.template batch<false>(v + lane, add);
+                // the row's ends
+                const int edge = lane == 0 ? (row.lo ? 0 : -1)
+                                           : (row.hi < row.count ? row.count - 1 : -1);
+                if (lane < 2 && edge >= v && edge < v + STEP) {
+                    float w[VE], e[VE];
+                    row.weights(edge, w, e);
+                    add(0, w, e);
+                }
+            } else {
+                row.ragged(v + lane, v1, add);
             }
-#pragma unroll
-            for (int u = 0; u < kVfBatch; ++u) {
-                float w[VE], b[VE], e[VE];
-                unpack(up[u], w);
-                unpack(uq[u], b);
-                row.weigh(e0 + u * 32 * VE, w, b, e);
-                take(w, e);
-            }
-        }
-        for (; v < i1; v += 32) {
-            float w[VE], b[VE], e[VE];
-            const int e0 = row.first + v * VE;
-            unpack(ld_global_nc_v4(row.p + e0), w);
-            if (row.q)
-                unpack(ld_global_nc_v4(row.q + e0), b);
-            row.weigh(e0, w, b, e);
-            take(w, e);
-        }
-        // and the others: the row's ends, or all of it
-        if (row.alike) {
-            if (lane == 0 && v0 == 0 && v1 > 0) {
-                float w[VE], e[VE];
-                row.weights(0, w, e);
-                take(w, e);
-            }
-            if (lane == 1 && v0 < v1 && v1 == row.count && row.count > 1) {
-                float w[VE], e[VE];
-                row.weights(row.count - 1, w, e);
-                take(w, e);
-            }
-        } else {
-            for (v = v0 + lane; v < v1; v += 32) {
-                float w[VE], e[VE];
-                row.weights(v, w, e);
-                take(w, e);
-            }
+            if ((n + 1) % stretch == 0)
+                marks[wi][n / stretch][lane] = make_float2(s, c);
         }
         double mine = static_cast<double>(s) + static_cast<double>(c);
 #pragma unroll
@@ -283,15 +305,15 @@ __global__ void __cluster_dims__(kVfCtas, 1, 1) __launch_bounds__(NT, 1024 / NT)
             mine += __shfl_xor_sync(0xffffffffu, mine, o);
         if (pass == 0)
             cluster_wait();
-        if (lane < kVfCtas)
+        if (lane < ctas)
             st_dsmem_f64(dsmem_addr(&sums[pass][run], lane), mine);
         cluster_sync();
-        // every warp: the runs' sums, kVfRuns / 32 a lane, and the level's run
-        constexpr int PL = kVfRuns / 32;
+        // every warp: the runs' sums, PL a lane, and the level's run
+        constexpr int PL = (kVfCtas * WARPS + 31) / 32;
         double part[PL], local = 0.0;
 #pragma unroll
         for (int k = 0; k < PL; ++k) {
-            part[k] = sums[pass][lane * PL + k];
+            part[k] = lane * PL + k < runs ? sums[pass][lane * PL + k] : 0.0;
             local += part[k];
         }
         const double upto = warp_scan(local, lane);
@@ -331,73 +353,133 @@ __global__ void __cluster_dims__(kVfCtas, 1, 1) __launch_bounds__(NT, 1024 / NT)
         }
         if (target_run != run)
             return;
-        // the token within this warp's run
-        int last = -1;
-        for (int vb = v0; vb < v1; vb += 32) {
-            const int v = vb + lane;
-            float w[VE], e[VE];
-            double sum = 0.0;
+        // the stretch, by the marks; then the step of 32 vectors, the lane and the
+        // element that pass the level
+        int from = 0;  // batches before the stretch
+        {
+            const int n = (v1 - v0 + STEP - 1) / STEP / stretch;  // marks left
+            for (int k = 0; k < n; ++k) {
+                const float2 mk = marks[wi][k][lane];
+                double upto = static_cast<double>(mk.x) + static_cast<double>(mk.y);
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    upto += __shfl_xor_sync(0xffffffffu, upto, o);
+                if (hit_before + upto > level)
+                    break;
+                from = (k + 1) * stretch;
+                mine = upto;  // what lies before the stretch
+            }
+            if (from)
+                hit_before += mine;
+        }
+        int last = -1, low = -1;
+        for (int vb = v0 + from * STEP; vb < v1; vb += STEP) {
+            double sum[kVfBatch], step[kVfBatch];
             int top = -1;
-            if (v < v1) {
-                row.weights(v, w, e);
+            auto one = [&](int u, const float (&w)[VE], const float (&e)[VE]) {
+                float ps = 0.f, pc = 0.f;
 #pragma unroll
                 for (int k = 0; k < VE; ++k) {
-                    sum += static_cast<double>(w[k]) + static_cast<double>(e[k]);
+                    add_exact(ps, pc, w[k], e[k]);
                     if (w[k] > 0.f)
-                        top = row.first + v * VE + k;
+                        top = row.first + (vb + u * 32 + lane) * VE + k;
                 }
-            }
-            const double incl = hit_before + warp_scan(sum, lane);
-            const unsigned got = __ballot_sync(0xffffffffu, top >= 0 && incl > level);
-            if (got) {
-                const int l = __ffs(got) - 1;
-                if (lane == l) {
-                    double at = incl - sum;
-                    int tok = top;
+                const double d = static_cast<double>(ps) + static_cast<double>(pc);
+#pragma unroll
+                for (int z = 0; z < kVfBatch; ++z)
+                    if (z == u)
+                        sum[z] = step[z] = d;
+            };
+            if (vb < row.lo || vb + STEP > row.hi)
+                row.ragged(vb + lane, v1, one);
+            else if (row.q)
+                row.template batch<true>(vb + lane, one);
+            else
+                row.template batch<false>(vb + lane, one);
+#pragma unroll
+            for (int o = 16; o; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < kVfBatch; ++u)
+                    step[u] += __shfl_xor_sync(0xffffffffu, step[u], o);
+#pragma unroll
+            for (int u = 0; u < kVfBatch; ++u) {
+                if (!(step[u] > 0.0 && hit_before + step[u] > level)) {
+                    hit_before += step[u];
+                    continue;
+                }
+                const double incl = hit_before + warp_scan(sum[u], lane);
+                unsigned got = __ballot_sync(0xffffffffu, sum[u] > 0.0 && incl > level);
+                if (!got)  // the level lies at the step's very end
+                    got = 0x80000000u >> __clz(__ballot_sync(0xffffffffu, sum[u] > 0.0));
+                if (lane == __ffs(got) - 1) {
+                    const int v = vb + u * 32 + lane;
+                    float w[VE], e[VE];
+                    row.weights(v, w, e);
+                    double at = incl - sum[u];
+                    int tok = -1;
 #pragma unroll
                     for (int k = 0; k < VE; ++k) {
-                        at += static_cast<double>(w[k]) + static_cast<double>(e[k]);
-                        if (w[k] > 0.f && at > level) {
+                        if (!(w[k] > 0.f))
+                            continue;
+                        if (tok < 0 || !(at > level))
                             tok = row.first + v * VE + k;
-                            break;
-                        }
+                        at += static_cast<double>(w[k]) + static_cast<double>(e[k]);
                     }
                     a.next[i] = tok;
                 }
                 return;
             }
             last = max(last, __reduce_max_sync(0xffffffffu, top));
-            hit_before = __shfl_sync(0xffffffffu, incl, 31);
         }
-        if (lane == 0)  // the level lies at the run's very end
-            a.next[i] = last;
+        // the level lies at the run's very end: its last token with weight
+        for (int vb = v0; vb < v0 + from * STEP && last < 0; vb += 32) {
+            int top = -1;
+            if (vb + lane < v1) {
+                float w[VE], e[VE];
+                row.weights(vb + lane, w, e);
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    if (w[k] > 0.f)
+                        top = row.first + (vb + lane) * VE + k;
+            }
+            low = max(low, __reduce_max_sync(0xffffffffu, top));
+        }
+        if (lane == 0)
+            a.next[i] = max(last, low);
         return;
     }
 }
 
 template <class T, int NT>
-static cudaError_t launch_verify_t(const VerifyArgs &a, cudaStream_t s)
+static cudaError_t launch_verify_t(const VerifyArgs &a, int ctas, cudaStream_t s)
 {
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.R) * kVfCtas, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.R) * static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(NT, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, zp_verify_kernel<T, NT>, a);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, zp_verify_kernel<T, NT>, a, ctas);
 }
 
 cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, int sms, cudaStream_t s)
 {
-    // 512 threads a CTA while all clusters then run at once, two CTAs an SM
-    const bool few = static_cast<long long>(a.R) * kVfCtas <= 2ll * sms;
-    if (bf16)
-        return few ? launch_verify_t<__nv_bfloat16, 512>(a, s)
-                   : launch_verify_t<__nv_bfloat16, 128>(a, s);
-    return few ? launch_verify_t<float, 512>(a, s) : launch_verify_t<float, 128>(a, s);
+    // An SM holds 1,024 of these threads.  All clusters at once where that goes:
+    // eight CTAs of 512 threads, else of 128, else four or two of those.
+    const long long R = a.R;
+    if (R * kVfCtas <= 2ll * sms)
+        return bf16 ? launch_verify_t<__nv_bfloat16, 512>(a, kVfCtas, s)
+                    : launch_verify_t<float, 512>(a, kVfCtas, s);
+    const int ctas = R * 8 <= 8ll * sms ? 8 : R * 4 <= 8ll * sms ? 4 : 2;
+    return bf16 ? launch_verify_t<__nv_bfloat16, 128>(a, ctas, s)
+                : launch_verify_t<float, 128>(a, ctas, s);
 }
 
 }  // namespace zp
