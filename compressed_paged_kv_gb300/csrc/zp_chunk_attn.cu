@@ -20,9 +20,10 @@
 //           columns each, out of tensor memory; they exchange their maxima): a
 //           running maximum and sum (fp32, base 2), P rounded to bf16 over S in
 //           tensor memory.  O is rescaled only when a maximum grows by more
-//           than 2^8 (p stays below 2^8, which changes no relative error), in
-//           place in tensor memory, between the products: S's arrival says that
-//           the product before it is done.  Then the epilogue.
+//           than 2^20 over the one it is held against (p stays below 2^20: no
+//           relative error changes, and sums of 2^31 of them times values up to
+//           2^76 fit fp32), in place in tensor memory, between the products: S's
+//           arrival says that the product before it is done.  Then the epilogue.
 //   warp 16 walks the items, describes each in shared memory for the others,
 //           and loads Q once per item and the K tiles (TMA, a box a cache block
 //           and 64 dims, 128-byte swizzle) into a ring of their own
@@ -56,7 +57,7 @@ constexpr int kCaThreads = (2 * kSmWarps + 4) * 32;
 constexpr int kSmRegs = 104, kOtherRegs = 64;  // registers a thread after the split
 static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4),
               "the split draws on the registers of the launch");
-constexpr int kItemCost = 128;         // an item's fixed cost, in keys
+constexpr int kItemCost = 256;         // an item's fixed cost, in keys
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
 constexpr int kMaxSpan = 30;           // CTAs an item is cut over, about (a lane each joins them)
 constexpr int kLoadWarp = 2 * kSmWarps;       // then the products' warps of A and of B, V's loader
@@ -64,7 +65,7 @@ constexpr int kMmaWarp = kLoadWarp + 1;
 constexpr int kLoadVWarp = kLoadWarp + 3;
 constexpr int kDescs = 4;              // item descriptions in flight
 constexpr int kTmemCols = 512;         // S/P of A, of B; O of A, of B
-constexpr float kRescale = 8.f;        // log2 of the growth that rescales O
+constexpr float kRescale = 20.f;       // log2 of the growth that rescales O
 
 // What every CTA works out at its start.
 struct CaPlan {
@@ -1289,41 +1290,78 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             bar_sync(9 + x, 32 * kSmWarps);
             if (sLast[x]) {
                 __threadfence();
-                constexpr int LPR = D / 4, RPW = 32 / LPR;  // lanes a row, rows a warp
+                // RB rows a warp at a time: lane k weighs share bs + k, then every lane
+                // adds up EL columns over the shares
+                constexpr int EL = D / 32, RB = 4;
                 const int first = __ffs(parts) - 1;
-                for (int rr = (hf * 4 + wq) * RPW + lane / LPR; rr < toks * G;
-                     rr += kSmWarps * RPW) {
-                    const int cc = (lane % LPR) * 4;
-                    const int srow = x * kTile + rr;
-                    float M = -INFINITY;
+                const bool in = parts >> lane & 1;
+                const float2 *ml_p = reinterpret_cast<const float2 *>(
+                                         slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
+                                         2 * kTile * D) + x * kTile;
+                for (int r0 = (hf * 4 + wq) * RB; r0 < toks * G; r0 += kSmWarps * RB) {
+                    float f[RB], L[RB], o[RB][EL];
+#pragma unroll
+                    for (int u = 0; u < RB; ++u) {
+                        const float2 ml = in ? __ldcg(ml_p + r0 + u) : make_float2(-INFINITY, 0.f);
+                        f[u] = ml.x;
+                        L[u] = ml.y;
+                    }
+#pragma unroll
+                    for (int u = 0; u < RB; ++u) {
+                        float M = f[u];
+#pragma unroll
+                        for (int w = 16; w; w >>= 1)
+                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+                        f[u] = f[u] == -INFINITY ? 0.f : ex2_approx(f[u] - M);
+                        L[u] *= f[u];
+#pragma unroll
+                        for (int w = 16; w; w >>= 1)
+                            L[u] += __shfl_xor_sync(0xffffffffu, L[u], w);
+#pragma unroll
+                        for (int e = 0; e < EL; ++e)
+                            o[u][e] = 0.f;
+                    }
                     for (unsigned q = parts; q; q &= q - 1) {
                         const int k = __ffs(q) - 1;
-                        const float *sp = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
-                        M = fmaxf(M, __ldcg(reinterpret_cast<const float2 *>(sp + 2 * kTile * D) +
-                                            srow).x);
+                        const float *o_p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
+                                           static_cast<size_t>(x * kTile + r0) * D + lane * EL;
+                        float w[RB][EL];
+#pragma unroll
+                        for (int u = 0; u < RB; ++u) {
+                            if (EL == 4) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o_p + u * D));
+                                w[u][0] = v.x;
+                                w[u][1] = v.y;
+                                w[u][EL - 2] = v.z;
+                                w[u][EL - 1] = v.w;
+                            } else {
+                                const float2 v = __ldcg(reinterpret_cast<const float2 *>(o_p + u * D));
+                                w[u][0] = v.x;
+                                w[u][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < RB; ++u) {
+                            const float fk = __shfl_sync(0xffffffffu, f[u], k);
+#pragma unroll
+                            for (int e = 0; e < EL; ++e)
+                                o[u][e] += w[u][e] * fk;
+                        }
                     }
-                    float L = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (unsigned q = parts; q; q &= q - 1) {
-                        const int k = __ffs(q) - 1;
-                        const float *sp = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
-                        const float2 ml =
-                            __ldcg(reinterpret_cast<const float2 *>(sp + 2 * kTile * D) + srow);
-                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(
-                            sp + static_cast<size_t>(srow) * D + cc));
-                        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-                        L += ml.y * f;
-                        o.x += w.x * f;
-                        o.y += w.y * f;
-                        o.z += w.z * f;
-                        o.w += w.w * f;
+#pragma unroll
+                    for (int u = 0; u < RB; ++u) {
+                        const int rr = r0 + u;
+                        if (rr >= toks * G)
+                            continue;
+                        const float iv = L[u] == 0.f ? 0.f : 1.f / L[u];
+                        __nv_bfloat16 *d2 =
+                            a.out + (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq +
+                                     d.h * G + rr % G) * D + lane * EL;
+#pragma unroll
+                        for (int e = 0; e < EL; e += 2)
+                            *reinterpret_cast<uint32_t *>(d2 + e) =
+                                pack_bf16x2(o[u][e] * iv, o[u][e + 1] * iv);
                     }
-                    const float iv = L == 0.f ? 0.f : 1.f / L;
-                    __nv_bfloat16 *d2 =
-                        a.out + (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq + d.h * G +
-                                 rr % G) * D + cc;
-                    *reinterpret_cast<uint2 *>(d2) =
-                        make_uint2(pack_bf16x2(o.x * iv, o.y * iv), pack_bf16x2(o.z * iv, o.w * iv));
                 }
             }
             leave();
