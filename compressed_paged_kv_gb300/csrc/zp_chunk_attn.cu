@@ -395,13 +395,29 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Bounded waits: a try suspends the warp for some microseconds, so that this is
-// a matter of seconds, and every wait here is for this CTA's own work.
-constexpr uint32_t kCaSpins = 1u << 19;
+// Bounded waits, all for this CTA's own work: 4 M tries of 20 clocks and more (a
+// try may suspend the warp for microseconds).  No sleeping in between: a wait
+// here ends within microseconds, and the 64 ns naps of mbar_wait cost 10 to 30 %
+// of the kernel's time (256 speculative chunks 314 -> 295 us, 16 prompts 752 ->
+// 687 us).
+constexpr uint32_t kCaSpins = 1u << 22;
 
 __device__ __forceinline__ bool ca_wait(uint64_t *bar, uint32_t parity)
 {
-    return mbar_wait(bar, parity, kCaSpins);
+    const uint32_t addr = smem_u32(bar);
+    for (uint32_t i = 0; i < kCaSpins; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (done)
+            return true;
+    }
+    return false;
 }
 
 // A converged warp's wait.
@@ -756,7 +772,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             // with nothing left to run beside them.  Both pass every stage of the
             // rings, used or not: a stage's parity then never runs ahead of a warp.
             // The whole warp waits; one lane issues.
-            constexpr uint32_t ID_S = ca_idesc(kTile, false), ID_O = ca_idesc(D, true);
+            // (a negative scale negates Q in the product: bit 13)
+            const uint32_t ID_S = ca_idesc(kTile, false) | (a.logit_scale < 0.f ? 1u << 13 : 0u);
+            constexpr uint32_t ID_O = ca_idesc(D, true);
             constexpr uint32_t STEP = S::TILE >> 4;
             const int x = wi - kMmaWarp;
             const uint32_t qdesc = desc_lo(smem_u32(sQ), 16), kdesc = desc_lo(smem_u32(sK), 16);
@@ -1013,11 +1031,6 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         ld16(tS + hf * HK + o, sr, o);
                     ld_wait(sr);
                     float *s = reinterpret_cast<float *>(sr);
-                    if (a.logit_scale < 0.f) {
-#pragma unroll
-                        for (int c = 0; c < HK; ++c)
-                            s[c] = -s[c];
-                    }
                     if (m_lim + m_slack < HK) {
 #pragma unroll
                         for (int c = 0; c < HK; ++c)

@@ -289,11 +289,10 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
 }
 
 // Bounded wait on a phase of an mbarrier; false when the bound was hit.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
-                                          uint32_t spins = kWaitSpins)
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
 {
     const uint32_t addr = smem_u32(bar);
-    for (uint32_t i = 0; i < spins; ++i) {
+    for (uint32_t i = 0; i < kWaitSpins; ++i) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"

@@ -108,6 +108,17 @@ def test_scores_that_climb_or_fall(rise):
     b.check_attn()
 
 
+@pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-6, 0.7])
+@pytest.mark.parametrize("d", [64, 128])
+def test_other_scales(scale, d):
+    b = Batch([(70, 600), (3, 400), (200, 200)], 2, 8, d, seed=15, heavy=0.0)
+    b.scale = scale
+    cache = b.cache()
+    b.attn(cache)
+    assert cache.status() == zp.OK
+    b.check_attn()
+
+
 def test_hidden_tokens_do_not_reach_a_row():
     """Not-finite keys and values at positions a token does not see leave its
     output within the bound of the clean 64-bit result (rows that shared a tile
