@@ -14,10 +14,10 @@
 // the sum at every border gets about V * 2^-25 of the draws wrong (0.5 % at
 // 150,000), so 32-bit sums will not do, and 64-bit additions run at a 64th of
 // the 32-bit rate here.  p - q is therefore taken with its rounding error
-// (both are fp32, the error is one too), and a thread adds up pairs of a
-// 32-bit sum and the sum of its rounding errors (T. J. Dekker's and D. E.
-// Knuth's error-free sums): about 46 bits.  The warps' sums are joined in 64
-// bits.
+// (both are fp32, the error is one too), and every sum is a pair of fp32 numbers,
+// the second one what the first has lost (T. J. Dekker's and D. E. Knuth's
+// error-free sums): about 46 bits.  (With the sums of warps and CTAs joined in 64
+// bits the joins alone took 10 us of a call.)
 //
 // One cluster of CTAs a request.  A warp owns a contiguous run of the deciding
 // row and reads it (of p and q) once, 16 bytes a lane and kVfBatch of them in
@@ -167,25 +167,61 @@ __device__ __forceinline__ void add_exact(float &s, float &c, float w, float e)
     s = t;
 }
 
-__device__ __forceinline__ double shfl_up(double v, int o)
+// h + l, h the nearest fp32 number to it.
+struct Pair {
+    float h, l;
+};
+
+__device__ __forceinline__ Pair normal(float h, float l)  // |l| well below |h|, or h = 0
 {
-    return __shfl_up_sync(0xffffffffu, v, o);
+    const float t = h + l;
+    return {t, l - (t - h)};
 }
 
-__device__ __forceinline__ double warp_scan(double v, int lane)
+__device__ __forceinline__ Pair operator+(const Pair &a, const Pair &b)
+{
+    const float t = a.h + b.h, z = t - a.h;
+    return normal(t, ((a.h - (t - z)) + (b.h - z)) + (a.l + b.l));
+}
+
+__device__ __forceinline__ bool operator>(const Pair &a, const Pair &b)
+{
+    return a.h > b.h || (a.h == b.h && a.l > b.l);
+}
+
+__device__ __forceinline__ Pair shfl_xor(const Pair &v, int o)
+{
+    return {__shfl_xor_sync(0xffffffffu, v.h, o), __shfl_xor_sync(0xffffffffu, v.l, o)};
+}
+
+__device__ __forceinline__ Pair shfl(const Pair &v, int src)
+{
+    return {__shfl_sync(0xffffffffu, v.h, src), __shfl_sync(0xffffffffu, v.l, src)};
+}
+
+__device__ __forceinline__ Pair warp_sum(Pair v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = v + shfl_xor(v, o);
+    return v;
+}
+
+__device__ __forceinline__ Pair warp_scan(Pair v, int lane)
 {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = shfl_up(v, o);
+        const Pair y = {__shfl_up_sync(0xffffffffu, v.h, o), __shfl_up_sync(0xffffffffu, v.l, o)};
         if (lane >= o)
-            v += y;
+            v = y + v;
     }
     return v;
 }
 
-__device__ __forceinline__ void st_dsmem_f64(uint32_t addr, double v)
+__device__ __forceinline__ void st_dsmem_pair(uint32_t addr, const Pair &v)
 {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.h), "f"(v.l)
+                 : "memory");
 }
 
 }  // namespace
@@ -198,8 +234,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
 {
     constexpr int VE = Row<T>::VE, WARPS = NT / 32, MARKS = kVfMarks / WARPS;
     constexpr int STEP = kVfBatch * 32;           // vectors of a batch
-    __shared__ double sums[2][kVfCtas * WARPS];   // every run's, in the row's order; one set a pass
-    __shared__ float2 marks[WARPS][MARKS][32];    // the lanes' sums after a stretch of the run
+    __shared__ __align__(8) Pair sums[2][kVfCtas * WARPS];  // every run's, in the row's order, a pass
+    __shared__ Pair marks[WARPS][MARKS][32];  // the lanes' sums after a stretch of the run
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
@@ -297,28 +333,25 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
                 row.ragged(v + lane, v1, add);
             }
             if ((n + 1) % stretch == 0)
-                marks[wi][n / stretch][lane] = make_float2(s, c);
+                marks[wi][n / stretch][lane] = normal(s, c);
         }
-        double mine = static_cast<double>(s) + static_cast<double>(c);
-#pragma unroll
-        for (int o = 16; o; o >>= 1)
-            mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        const Pair mine = warp_sum(normal(s, c));
         if (pass == 0)
             cluster_wait();
         if (lane < ctas)
-            st_dsmem_f64(dsmem_addr(&sums[pass][run], lane), mine);
+            st_dsmem_pair(dsmem_addr(&sums[pass][run], lane), mine);
         cluster_sync();
         // every warp: the runs' sums, PL a lane, and the level's run
         constexpr int PL = (kVfCtas * WARPS + 31) / 32;
-        double part[PL], local = 0.0;
+        Pair part[PL], local = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < PL; ++k) {
-            part[k] = lane * PL + k < runs ? sums[pass][lane * PL + k] : 0.0;
-            local += part[k];
+            part[k] = lane * PL + k < runs ? sums[pass][lane * PL + k] : Pair{0.f, 0.f};
+            local = local + part[k];
         }
-        const double upto = warp_scan(local, lane);
-        const double all = __shfl_sync(0xffffffffu, upto, 31);
-        if (!(all > 0.0)) {
+        const Pair upto = warp_scan(local, lane);
+        const Pair all = shfl(upto, 31);
+        if (!(all.h > 0.f)) {
             if (left)
                 continue;  // p <= q everywhere: drawn from p
             if (rank == 0 && threadIdx.x == 0) {
@@ -327,54 +360,58 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
             }
             return;
         }
-        const double level = static_cast<double>(a.sample_u[i]) * all;
-        double before = upto - local;
+        const float r = a.sample_u[i], rh = r * all.h;
+        const Pair level = normal(rh, fmaf(r, all.h, -rh) + r * all.l);
+        Pair before = {__shfl_up_sync(0xffffffffu, upto.h, 1), __shfl_up_sync(0xffffffffu, upto.l, 1)};
+        if (lane == 0)
+            before = {0.f, 0.f};
         int hit = -1, tail = -1;  // the run that passes the level; the last with any weight
-        double hit_before = 0.0;
+        Pair hit_before = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < PL; ++k) {
-            if (part[k] > 0.0) {
+            const Pair after = before + part[k];
+            if (part[k].h > 0.f) {
                 tail = lane * PL + k;
-                if (hit < 0 && before + part[k] > level) {
+                if (hit < 0 && after > level) {
                     hit = tail;
                     hit_before = before;
                 }
             }
-            before += part[k];
+            before = after;
         }
         const unsigned m = __ballot_sync(0xffffffffu, hit >= 0);
         int target_run;
         if (m) {
             target_run = __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
-            hit_before = __shfl_sync(0xffffffffu, hit_before, __ffs(m) - 1);
+            hit_before = shfl(hit_before, __ffs(m) - 1);
         } else {  // sample_u not below 1: the last token with weight
             target_run = __reduce_max_sync(0xffffffffu, tail);
-            hit_before = -INFINITY;
         }
+        const bool at_end = m == 0;
         if (target_run != run)
             return;
         // the stretch, by the marks; then the step of 32 vectors, the lane and the
         // element that pass the level
         int from = 0;  // batches before the stretch
-        {
-            const int n = (v1 - v0 + STEP - 1) / STEP / stretch;  // marks left
-            for (int k = 0; k < n; ++k) {
-                const float2 mk = marks[wi][k][lane];
-                double upto = static_cast<double>(mk.x) + static_cast<double>(mk.y);
-#pragma unroll
-                for (int o = 16; o; o >>= 1)
-                    upto += __shfl_xor_sync(0xffffffffu, upto, o);
-                if (hit_before + upto > level)
-                    break;
-                from = (k + 1) * stretch;
-                mine = upto;  // what lies before the stretch
+        if (!at_end) {
+            Pair skipped = {0.f, 0.f};
+            int k0 = 0, k1 = (v1 - v0 + STEP - 1) / STEP / stretch;  // marks left
+            while (k0 < k1) {  // the first mark past the level
+                const int k = (k0 + k1) / 2;
+                const Pair upto_k = warp_sum(marks[wi][k][lane]);
+                if (hit_before + upto_k > level) {
+                    k1 = k;
+                } else {
+                    k0 = k + 1;
+                    skipped = upto_k;
+                }
             }
-            if (from)
-                hit_before += mine;
+            from = k0 * stretch;
+            hit_before = hit_before + skipped;
         }
         int last = -1, low = -1;
         for (int vb = v0 + from * STEP; vb < v1; vb += STEP) {
-            double sum[kVfBatch], step[kVfBatch];
+            Pair sum[kVfBatch], step[kVfBatch];
             int top = -1;
             auto one = [&](int u, const float (&w)[VE], const float (&e)[VE]) {
                 float ps = 0.f, pc = 0.f;
@@ -384,7 +421,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
                     if (w[k] > 0.f)
                         top = row.first + (vb + u * 32 + lane) * VE + k;
                 }
-                const double d = static_cast<double>(ps) + static_cast<double>(pc);
+                const Pair d = normal(ps, pc);
 #pragma unroll
                 for (int z = 0; z < kVfBatch; ++z)
                     if (z == u)
@@ -400,22 +437,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
             for (int o = 16; o; o >>= 1)
 #pragma unroll
                 for (int u = 0; u < kVfBatch; ++u)
-                    step[u] += __shfl_xor_sync(0xffffffffu, step[u], o);
+                    step[u] = step[u] + shfl_xor(step[u], o);
 #pragma unroll
             for (int u = 0; u < kVfBatch; ++u) {
-                if (!(step[u] > 0.0 && hit_before + step[u] > level)) {
-                    hit_before += step[u];
+                if (at_end || !(step[u].h > 0.f && hit_before + step[u] > level)) {
+                    hit_before = hit_before + step[u];
                     continue;
                 }
-                const double incl = hit_before + warp_scan(sum[u], lane);
-                unsigned got = __ballot_sync(0xffffffffu, sum[u] > 0.0 && incl > level);
+                const Pair incl = hit_before + warp_scan(sum[u], lane);
+                unsigned got = __ballot_sync(0xffffffffu, sum[u].h > 0.f && incl > level);
                 if (!got)  // the level lies at the step's very end
-                    got = 0x80000000u >> __clz(__ballot_sync(0xffffffffu, sum[u] > 0.0));
-                if (lane == __ffs(got) - 1) {
+                    got = 0x80000000u >> __clz(__ballot_sync(0xffffffffu, sum[u].h > 0.f));
+                const int src = __ffs(got) - 1;
+                Pair at = {__shfl_up_sync(0xffffffffu, incl.h, 1),
+                           __shfl_up_sync(0xffffffffu, incl.l, 1)};
+                if (lane == 0)
+                    at = hit_before;
+                if (lane == src) {
                     const int v = vb + u * 32 + lane;
                     float w[VE], e[VE];
                     row.weights(v, w, e);
-                    double at = incl - sum[u];
                     int tok = -1;
 #pragma unroll
                     for (int k = 0; k < VE; ++k) {
@@ -423,7 +464,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
                             continue;
                         if (tok < 0 || !(at > level))
                             tok = row.first + v * VE + k;
-                        at += static_cast<double>(w[k]) + static_cast<double>(e[k]);
+                        at = at + Pair{w[k], e[k]};
                     }
                     a.next[i] = tok;
                 }

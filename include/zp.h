@@ -460,7 +460,8 @@ zp_status zp_paged_chunk_attn(zp_cache *cache, int32_t layer, const void *q, int
  *     accepted: the lowest index whose running sum exceeds sample_u[i] times
  *     the sum of all weights.
  * The products and sums are formed in more than 32 bits and in a fixed order.
- * Weights need not sum to 1; one that is not a positive finite number (a NaN
+ * Weights need not sum to 1 (their sum is an fp32 number, though); one that is
+ * not a positive finite number (a NaN
  * among them) counts as zero.  A rejected row with no weight left (p <= q
  * everywhere, by rounding) is drawn from p instead.  With `lengths` the
  * rejected tokens leave the cache: lengths[row] -= n_i - 1 - a (their blocks
