@@ -59,6 +59,31 @@ __device__ __forceinline__ void unpack(const uint4 &u, float (&v)[8])
     }
 }
 
+// Two fp32 numbers, added or subtracted at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ float low2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float high2(uint64_t v)
+{
+    return __uint_as_float(static_cast<uint32_t>(v >> 32));
+}
+
 // A row as 16-byte vectors of p: vector i holds elements first + i * VE ..; the
 // first and the last one may lie partly outside.
 template <class T>
@@ -113,8 +138,8 @@ struct Row {
             weigh<false>(e0, w, b, e);
     }
 
-    // The vectors v, v + 32, .. (kVfBatch of them) of a row with lo < hi: `take`
-    // gets each one's number and weights, 0 outside lo .. hi - 1.
+    // The vectors v, v + 32, .. (kVfBatch of them) of a row with lo < hi, zeros
+    // outside lo .. hi - 1: `take` gets each one's number and bits of p and q.
     template <bool Q, class F>
     __device__ __forceinline__ void batch(int v, F take) const
     {
@@ -123,23 +148,66 @@ struct Row {
         for (int u = 0; u < kVfBatch; ++u) {
             const int at = first + min(max(v + u * 32, lo), hi - 1) * VE;
             up[u] = ld_global_nc_v4(p + at);
-            if (Q)
-                uq[u] = ld_global_nc_v4(q + at);
+            uq[u] = Q ? ld_global_nc_v4(q + at) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kVfBatch; ++u) {
             const int i = v + u * 32;
-            float w[VE], b[VE], e[VE];
             if (i < lo || i >= hi)
-                up[u] = make_uint4(0u, 0u, 0u, 0u);
-            unpack(up[u], w);
-            if (Q)
-                unpack(uq[u], b);
-            weigh<Q>(first + i * VE, w, b, e);
-            take(u, w, e);
+                up[u] = uq[u] = make_uint4(0u, 0u, 0u, 0u);
+            take(u, up[u], uq[u]);
         }
     }
 
+    // The weights of vector i from its bits, every one tested.
+    template <bool Q>
+    __device__ __forceinline__ void weights_of(int i, const uint4 &up, const uint4 &uq,
+                                               float (&w)[VE], float (&e)[VE]) const
+    {
+        float b[VE];
+        unpack(up, w);
+        if (Q)
+            unpack(uq, b);
+        weigh<Q>(first + i * VE, w, b, e);
+    }
+
+    // Adds the weights of vector i, from its bits, to the two sums (s, c).  For
+    // finite numbers: others make the sums infinite or NaN.
+    template <bool Q>
+    __device__ __forceinline__ void add_fast(int i, const uint4 &up, const uint4 &uq, uint64_t &s,
+                                             uint64_t &c) const
+    {
+        float w[VE], b[VE];
+        unpack(up, w);
+        if (Q) {
+            unpack(uq, b);
+#pragma unroll
+            for (int k = 0; k < VE; ++k)  // q where p exceeds it, else p: nothing left
+                b[k] = fminf(b[k], w[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                w[k] = fmaxf(w[k], 0.f);
+            const unsigned at = static_cast<unsigned>(skip - (first + i * VE));
+            if (at < static_cast<unsigned>(VE) && skip >= 0) {
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    w[k] = k == static_cast<int>(at) ? 0.f : w[k];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < VE; k += 2) {
+            uint64_t d = pack2(w[k], w[k + 1]);
+            if (Q) {
+                const uint64_t pq = d, b2 = pack2(b[k], b[k + 1]);
+                d = sub2(pq, b2);
+                c = add2(c, sub2(sub2(pq, d), b2));
+            }
+            const uint64_t t = add2(s, d), z = sub2(t, s);
+            c = add2(c, add2(sub2(s, sub2(t, z)), sub2(d, z)));
+            s = t;
+        }
+    }
     // The same of any vectors below `end`, those outside with weight 0.
     template <class F>
     __device__ __forceinline__ void ragged(int v, int end, F take) const
@@ -234,7 +302,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
 {
     constexpr int VE = Row<T>::VE, WARPS = NT / 32, MARKS = kVfMarks / WARPS;
     constexpr int STEP = kVfBatch * 32;           // vectors of a batch
-    __shared__ __align__(8) Pair sums[2][kVfCtas * WARPS];  // every run's, in the row's order, a pass
+    __shared__ __align__(8) Pair sums[4][kVfCtas * WARPS];  // every run's, in the row's order, a pass
     __shared__ Pair marks[WARPS][MARKS][32];  // the lanes' sums after a stretch of the run
     pdl_wait();
     pdl_launch_dependents();
@@ -300,8 +368,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
         return;
     cluster_arrive();  // paired below: the sums go to CTAs that have started
 
-    for (int pass = 0; pass < 2; ++pass) {
-        const bool left = pass == 0 && reject;  // what a rejection leaves; else p itself
+    bool left = reject;   // what a rejection leaves; else p itself
+    bool strict = false;  // every weight tested
+    for (int pass = 0; pass < 4; ++pass) {
         const Row<T> row(target + row_at, left && draft ? draft + row_at : nullptr,
                          left && !draft ? x : -1, a.vocab);
         // this warp's run: whole batches, `stretch` of them to a mark
@@ -309,18 +378,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
         const int stretch = (per + MARKS - 1) / MARKS;
         const int run = rank * WARPS + wi;
         const int v0 = min(row.count, run * per * STEP), v1 = min(row.count, v0 + per * STEP);
-        float s = 0.f, c = 0.f;
+        uint64_t s2 = 0, c2 = 0;  // two sums and what they lost
+        float s = 0.f, c = 0.f;   // and one of tested weights
         auto add = [&](int, const float (&w)[VE], const float (&e)[VE]) {
 #pragma unroll
             for (int k = 0; k < VE; ++k)
                 add_exact(s, c, w[k], e[k]);
         };
+        auto total = [&] {
+            return (normal(low2(s2), low2(c2)) + normal(high2(s2), high2(c2))) + normal(s, c);
+        };
         for (int v = v0, n = 0; v < v1; v += STEP, ++n) {
-            if (row.lo < row.hi) {
+            if (!strict && row.lo < row.hi) {
                 if (row.q)
-                    row.template batch<true>(v + lane, add);
+                    row.template batch<true>(v + lane, [&](int u, const uint4 &up, const uint4 &uq) {
+                        row.template add_fast<true>(v + u * 32 + lane, up, uq, s2, c2);
+                    });
                 else
-                    row.template batch<false>(v + lane, add);
+                    row.template batch<false>(v + lane, [&](int u, const uint4 &up, const uint4 &uq) {
+                        row.template add_fast<false>(v + u * 32 + lane, up, uq, s2, c2);
+                    });
                 // the row's ends
                 const int edge = lane == 0 ? (row.lo ? 0 : -1)
                                            : (row.hi < row.count ? row.count - 1 : -1);
@@ -333,9 +410,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
                 row.ragged(v + lane, v1, add);
             }
             if ((n + 1) % stretch == 0)
-                marks[wi][n / stretch][lane] = normal(s, c);
+                marks[wi][n / stretch][lane] = total();
         }
-        const Pair mine = warp_sum(normal(s, c));
+        const Pair mine = warp_sum(total());
         if (pass == 0)
             cluster_wait();
         if (lane < ctas)
@@ -351,9 +428,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
         }
         const Pair upto = warp_scan(local, lane);
         const Pair all = shfl(upto, 31);
+        if (!(all.h < INFINITY) && !strict) {
+            strict = true;
+            continue;
+        }
         if (!(all.h > 0.f)) {
-            if (left)
-                continue;  // p <= q everywhere: drawn from p
+            if (left) {  // p <= q everywhere: drawn from p
+                left = strict = false;
+                continue;
+            }
             if (rank == 0 && threadIdx.x == 0) {
                 a.next[i] = -1;
                 set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
@@ -430,9 +513,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
             if (vb < row.lo || vb + STEP > row.hi)
                 row.ragged(vb + lane, v1, one);
             else if (row.q)
-                row.template batch<true>(vb + lane, one);
+                row.template batch<true>(vb + lane, [&](int u, const uint4 &up, const uint4 &uq) {
+                    float w[VE], e[VE];
+                    row.template weights_of<true>(vb + u * 32 + lane, up, uq, w, e);
+                    one(u, w, e);
+                });
             else
-                row.template batch<false>(vb + lane, one);
+                row.template batch<false>(vb + lane, [&](int u, const uint4 &up, const uint4 &uq) {
+                    float w[VE], e[VE];
+                    row.template weights_of<false>(vb + u * 32 + lane, up, uq, w, e);
+                    one(u, w, e);
+                });
 #pragma unroll
             for (int o = 16; o; o >>= 1)
 #pragma unroll

@@ -461,9 +461,9 @@ zp_status zp_paged_chunk_attn(zp_cache *cache, int32_t layer, const void *q, int
  *     the sum of all weights.
  * The products and sums are formed in more than 32 bits and in a fixed order.
  * Weights need not sum to 1 (their sum is an fp32 number, though); one that is
- * not a positive finite number (a NaN
- * among them) counts as zero.  A rejected row with no weight left (p <= q
- * everywhere, by rounding) is drawn from p instead.  With `lengths` the
+ * not a positive finite number (a NaN among them) counts as zero.  A rejected
+ * row with no weight left (p <= q everywhere, by rounding) is drawn from p
+ * instead.  With `lengths` the
  * rejected tokens leave the cache: lengths[row] -= n_i - 1 - a (their blocks
  * stay reserved for the row).  A request with an empty chunk is skipped: its
  * outputs and length are not written.
