@@ -782,9 +782,22 @@ static zp_status chunk_checks(const zp_cache *c, int32_t layer, const int32_t *b
         return ZP_ERR_INVALID_ARG;
     if (!aligned(block_tables, 4) || !aligned(lengths, 4) || !aligned(starts, 4))
         return ZP_ERR_INVALID_ARG;
-    if (static_cast<long long>(bt_stride) * c->b >= (1ll << 31))
+    if (static_cast<long long>(bt_stride) * c->b > (1ll << 30))  // lengths and costs are 32-bit
         return ZP_ERR_UNSUPPORTED;
     return ZP_OK;
+}
+
+// Whether x bytes at p and y bytes at q share any; a null pointer shares none.
+static bool overlap(const void *p, unsigned long long x, const void *q, unsigned long long y)
+{
+    const unsigned long long a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p && q && a < b + y && b < a + x;
+}
+
+// Bytes of `total` bf16 rows of `row` elements, `stride` elements apart.
+static unsigned long long row_bytes(int total, long long stride, long long row)
+{
+    return 2ull * (static_cast<unsigned long long>(total - 1) * stride + row);
 }
 
 // A row stride in elements: whole 16-byte vectors, no overlap of two rows.
@@ -807,6 +820,11 @@ zp_status zp_append_kv_chunk(zp_cache *c, int32_t layer, const void *k_new, int6
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
+    const unsigned long long pool = 2ull * c->num_blocks * c->b * row;
+    for (const void *p : {c->kpools[layer], c->vpools[layer]})
+        if (overlap(p, pool, k_new, row_bytes(total, k_stride, row)) ||
+            overlap(p, pool, v_new, row_bytes(total, v_stride, row)))
+            return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
     zp::ChunkKvArgs a{};
@@ -844,11 +862,14 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         chunk_checks(c, layer, block_tables, bt_stride, num_rows, lengths, R, starts, total);
     if (st != ZP_OK)
         return st;
-    if (!q || !out || !aligned(q, 16) || !aligned(out, 32) ||
-        !row_stride_ok(q_stride, static_cast<long long>(c->Hq) * c->d) || !std::isfinite(scale))
+    const long long row = static_cast<long long>(c->Hq) * c->d;
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 32) || !row_stride_ok(q_stride, row) ||
+        !std::isfinite(scale))
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
+    if (overlap(q, row_bytes(total, q_stride, row), out, row_bytes(total, row, row)))
+        return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
     zp::ChunkAttnArgs a{};
@@ -896,7 +917,7 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
     if (R < 0 || R > c->max_requests || total < 0 || vocab < 1 || prob_stride < vocab ||
         (lengths && num_rows < 1))
         return ZP_ERR_INVALID_ARG;
-    if (prob_dtype != ZP_DTYPE_F32 && prob_dtype != ZP_DTYPE_BF16)
+    if ((prob_dtype != ZP_DTYPE_F32 && prob_dtype != ZP_DTYPE_BF16) || vocab > (1 << 30))
         return ZP_ERR_UNSUPPORTED;
     const size_t esz = prob_dtype == ZP_DTYPE_F32 ? 4 : 2;
     if (!aligned(target_probs, esz) || !aligned(draft_probs, esz) || !aligned(tokens, 4) ||
@@ -905,6 +926,23 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
+    // the CTAs of a request read the inputs each for itself: no output may change them
+    const unsigned long long probs =
+        esz * (static_cast<unsigned long long>(total - 1) * prob_stride + vocab);
+    const unsigned long long per_row = 4ull * total, per_request = 4ull * R;
+    const struct { const void *p; unsigned long long n; }
+        outs[] = {{accepted, per_request}, {next_tokens, per_request}, {lengths, 4ull * num_rows}},
+        ins[] = {{tokens, per_row}, {accept_u, per_row}, {sample_u, per_request},
+                 {starts, per_request + 4}, {lengths ? req_idx : nullptr, per_request},
+                 {target_probs, probs}, {draft_probs, probs}};
+    for (int i = 0; i < 3; ++i) {
+        for (int k = 0; k < i; ++k)
+            if (overlap(outs[i].p, outs[i].n, outs[k].p, outs[k].n))
+                return ZP_ERR_INVALID_ARG;
+        for (const auto &in : ins)
+            if (overlap(outs[i].p, outs[i].n, in.p, in.n))
+                return ZP_ERR_INVALID_ARG;
+    }
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
     zp::VerifyArgs a{};

@@ -17,7 +17,7 @@ constexpr int kCkThreads = 256;
 
 // The last i in [0, R) with starts[i] <= t, or 0 (the caller checks that the
 // chunk holds t): every round the 32 lanes probe the range at equal steps.
-__device__ __forceinline__ int find_request(const int32_t *starts, int R, int t, int lane)
+__device__ __forceinline__ int find_request(const int32_t *starts, int R, long long t, int lane)
 {
     int lo = 0, n = R;
     while (n > 1) {
@@ -38,7 +38,8 @@ __global__ void __launch_bounds__(kCkThreads) zp_append_kv_chunk_kernel(const Ch
 {
     pdl_wait();
     pdl_launch_dependents();
-    const int t = static_cast<int>((blockIdx.x * static_cast<unsigned>(kCkThreads) + threadIdx.x) >> 5);
+    const long long t =
+        blockIdx.x * static_cast<long long>(kCkThreads / 32) + static_cast<int>(threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     ChunkReq c;
     bool bad = false;
@@ -54,7 +55,7 @@ __global__ void __launch_bounds__(kCkThreads) zp_append_kv_chunk_kernel(const Ch
     const int i = find_request(a.starts, a.R, t, lane);
     if (!chunk_request(a, i, c, &bad) || t < c.first || t >= c.first + c.n)
         return;  // a bad request, or a row of no request: padding
-    const int p = c.len - c.n + (t - c.first);
+    const int p = c.len - c.n + static_cast<int>(t - c.first);
     const int blk = a.tables[(size_t)c.row * a.stride + p / kBlk];
     if (blk < 0 || blk >= a.num_blocks) {
         if (lane == 0)
@@ -63,8 +64,8 @@ __global__ void __launch_bounds__(kCkThreads) zp_append_kv_chunk_kernel(const Ch
     }
     const int vpr = a.d / 8;  // 16-byte vectors per head row
     const int nv = a.Hkv * vpr;
-    const uint4 *ks = reinterpret_cast<const uint4 *>(a.k_new + (size_t)t * a.k_stride);
-    const uint4 *vs = reinterpret_cast<const uint4 *>(a.v_new + (size_t)t * a.v_stride);
+    const uint4 *ks = reinterpret_cast<const uint4 *>(a.k_new + t * a.k_stride);
+    const uint4 *vs = reinterpret_cast<const uint4 *>(a.v_new + t * a.v_stride);
     uint4 *kd = reinterpret_cast<uint4 *>(a.kpool);
     uint4 *vd = reinterpret_cast<uint4 *>(a.vpool);
     const size_t base = (size_t)blk * a.Hkv * kBlk + p % kBlk;

@@ -43,8 +43,6 @@
 // ones both fill the GPU.  An item cut by a border leaves partial results (m,
 // l, O) in the handle's workspace, and the CTA that arrives last joins them in
 // the fixed order of the shares: results do not depend on the timing.
-#include <cudaTypedefs.h>
-
 #include "zp_chunk.cuh"
 
 namespace zp {
@@ -395,12 +393,14 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Bounded waits, all for this CTA's own work: 4 M tries of 20 clocks and more (a
-// try may suspend the warp for microseconds).  No sleeping in between: a wait
-// here ends within microseconds, and the 64 ns naps of mbar_wait cost 10 to 30 %
-// of the kernel's time (256 speculative chunks 314 -> 295 us, 16 prompts 752 ->
-// 687 us).
-constexpr uint32_t kCaSpins = 1u << 22;
+// Bounded waits, all for this CTA's own work: 32 M tries, which the hardware
+// lets last 72 clocks (with 640 threads waiting) to 2,600 (with one): seconds.
+// A wait ends within microseconds, but for the rows that are computed twice
+// (see the end of the epilogue): those of an item over 100,000 keys hold its CTA
+// up for 2.8 s, and no wait ran out.  No sleeping in between: the 64 ns naps of
+// mbar_wait cost 10 to 30 % of the kernel's time (256 speculative chunks 314 ->
+// 295 us, 16 prompts 752 -> 687 us), and a look at the clock as much.
+constexpr uint32_t kCaSpins = 1u << 25;
 
 __device__ __forceinline__ bool ca_wait(uint64_t *bar, uint32_t parity)
 {
@@ -1277,6 +1277,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll
                     for (int e = 0; e < OE; ++e)
                         o[e] = fmaf(p, __bfloat162float(a.vpool[at + hf * HD + e * 32 + lane]), o[e]);
+                    bool over = true;  // nothing changes a NaN any more
+#pragma unroll
+                    for (int e = 0; e < OE; ++e)
+                        over = over && o[e] != o[e];
+                    if (__all_sync(0xffffffffu, over))
+                        break;
                 }
 #pragma unroll
                 for (int e = 0; e < OE; ++e) {

@@ -26,7 +26,9 @@
  *    the same call skips its writes; read the word with zp_cache_status.
  *  - A handle serves at most one call of each entry point in flight at a
  *    time.  zp_compress may run concurrently with zp_paged_decode_attn and
- *    zp_append_kv on another stream when they touch disjoint requests.
+ *    zp_append_kv on another stream when they touch disjoint requests, and
+ *    so may zp_append_kv_chunk, zp_paged_chunk_attn and zp_verify_draft beside
+ *    each other and any other call.
  *    zp_compress, zp_compress_prefill, zp_append_slots, zp_alloc_rows,
  *    zp_release_rows and zp_fork_rows change the free stack or refcounts:
  *    order them (one stream, or events).  More concurrency needs
@@ -398,9 +400,11 @@ zp_status zp_append_kv(zp_cache *cache, int32_t layer, const void *k_new, const 
  *                zp_append_slots once per token of a speculative step.  A
  *                prompt computed in pieces passes its progress here, an array
  *                of the caller's own, not the length it was reserved with.
+ *  bt_stride     bt_stride * b <= 2^30 (ZP_ERR_UNSUPPORTED beyond)
  *  row strides   in elements, between the rows of consecutive tokens: at least
  *                a row, a multiple of 8 (the q, k and v of one packed
  *                projection output are passed as they lie)
+ * Outputs share no memory with inputs or each other (ZP_ERR_INVALID_ARG).
  * Offsets, rows, lengths or block ids out of range are recorded as
  * ZP_ERR_DEVICE_CHECK in the sticky status; such a request is skipped (a bad
  * block id: its outputs are undefined, its row is not written). */
