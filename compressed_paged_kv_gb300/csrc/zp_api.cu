@@ -815,7 +815,7 @@ zp_status zp_append_kv_chunk(zp_cache *c, int32_t layer, const void *k_new, int6
     if (st != ZP_OK)
         return st;
     const long long row = static_cast<long long>(c->Hkv) * c->d;
-    if (!k_new || !v_new || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+    if ((total > 0 && (!k_new || !v_new)) || !aligned(k_new, 16) || !aligned(v_new, 16) ||
         !row_stride_ok(k_stride, row) || !row_stride_ok(v_stride, row))
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
@@ -863,7 +863,7 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     if (st != ZP_OK)
         return st;
     const long long row = static_cast<long long>(c->Hq) * c->d;
-    if (!q || !out || !aligned(q, 16) || !aligned(out, 32) || !row_stride_ok(q_stride, row) ||
+    if ((total > 0 && (!q || !out)) || !aligned(q, 16) || !aligned(out, 32) || !row_stride_ok(q_stride, row) ||
         !std::isfinite(scale))
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
@@ -911,8 +911,8 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
                           int32_t *next_tokens, void *stream)
 {
     NvtxRange nvtx("zp_verify_draft");
-    if (!c || !tokens || !starts || !target_probs || !accept_u || !sample_u || !accepted ||
-        !next_tokens)
+    if (!c || !starts || (total > 0 && (!tokens || !target_probs || !accept_u)) ||
+        (R > 0 && (!sample_u || !accepted || !next_tokens)))
         return ZP_ERR_INVALID_ARG;
     if (R < 0 || R > c->max_requests || total < 0 || vocab < 1 || prob_stride < vocab ||
         (lengths && num_rows < 1))

@@ -392,7 +392,8 @@ zp_status zp_append_kv(zp_cache *cache, int32_t layer, const void *k_new, const 
  *                looked at, so a padded batch repeats the last offset; packed
  *                rows of no chunk are not read as tokens and their outputs not
  *                written
- *  total         packed rows of the tensors (their allocation's bound)
+ *  total         packed rows of the tensors (their allocation's bound); with 0
+ *                their pointers may be NULL
  *  lengths       device int32 [num_rows]: the tokens of the row INCLUDING the
  *                chunk, n_i <= lengths[row] <= bt_stride * b; token j of the
  *                chunk is at position lengths[row] - n_i + j.  Blocks for them

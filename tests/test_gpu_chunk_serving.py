@@ -375,7 +375,7 @@ def test_packed_rows_past_32_bits():
 # ------------------------------------------------------------- verification
 
 def _verify(cache, tokens, starts, p, q, u, r, R=None, **kw):
-    R = R or starts.numel() - 1
+    R = starts.numel() - 1 if R is None else R
     acc, nxt = (torch.full((R,), -7, dtype=I32, device=DEV) for _ in range(2))
     cache.verify_draft(tokens, starts, p, u, r, acc, nxt, draft_probs=q, **kw)
     return acc, nxt
@@ -546,6 +546,24 @@ def test_shared_memory_is_refused():
     assert cache.status() == zp.OK
     assert torch.equal(_bits(b.q), _bits(keep)) and torch.equal(_bits(b.kp[0]), _bits(before))
     assert not bool(acc.any()) and not bool(toks.any())
+
+
+def test_batches_of_nothing():
+    """No packed row at all (tensors without memory), and no request."""
+    b = Batch([(0, 40), (0, 0)], 2, 4, 64, seed=38)
+    cache = b.cache()
+    lengths = b.lengths.clone()
+    none = torch.empty(0, dtype=I32, device=DEV)
+    f32 = torch.empty(0, device=DEV)
+    for starts, R in ((b.starts, 2), (b.starts[:1], 0)):
+        b.starts = starts
+        b.append(cache)
+        b.attn(cache)
+        acc, nxt = _verify(cache, none, starts, torch.empty(0, 10, device=DEV), None, f32,
+                           torch.rand(R, device=DEV), R=R, lengths=b.lengths)
+        assert acc.tolist() == [-7] * R and nxt.tolist() == [-7] * R
+    assert cache.status() == zp.OK
+    assert torch.equal(b.lengths, lengths)
 
 
 def test_sizes_beyond_the_limits_are_refused():
