@@ -38,7 +38,7 @@
 // values hidden from it is computed again with plain fp32 arithmetic.
 //
 // The grid is one CTA an SM.  Every CTA adds up the cost of all items (the
-// keys each reads, plus kItemCost) from the device arrays and takes an equal,
+// keys each reads, plus a fixed part) from the device arrays and takes an equal,
 // contiguous share, cut at key tiles, so that few long rows and many short
 // ones both fill the GPU.  An item cut by a border leaves partial results (m,
 // l, O) in the handle's workspace, and the CTA that arrives last joins them in
@@ -55,7 +55,13 @@ constexpr int kCaThreads = (2 * kSmWarps + 4) * 32;
 constexpr int kSmRegs = 104, kOtherRegs = 64;  // registers a thread after the split
 static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4),
               "the split draws on the registers of the launch");
-constexpr int kItemCost = 256;         // an item's fixed cost, in keys
+// Costs, in keys of a pair (measured: 1.4 us for 128 of them, 0.6 for 128 of a
+// single item, whose streams take half the tiles each, and 2.7 to 2.9 us between
+// the last tile of an item and the first of the next).  With a single item's
+// keys at full cost 60 single tokens beside two prompt pieces take 85 us, not 75.
+constexpr int kItemCost = 320;         // an item's fixed cost
+constexpr int kSingle = 8;             // 16ths of a pair's cost that a single item's key takes
+constexpr int kSnap = 3;               // key tiles that an item is not cut off for
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
 constexpr int kMaxSpan = 30;           // CTAs an item is cut over, about (a lane each joins them)
 constexpr int kLoadWarp = 2 * kSmWarps;       // then the products' warps of A and of B, V's loader
@@ -129,6 +135,12 @@ struct CaItem {
 
 __host__ __device__ __forceinline__ int tile_tokens(int G) { return kTile / G; }
 
+// Cost of an item whose last token sees `vis` keys.
+__host__ __device__ __forceinline__ int item_cost(int vis, bool single)
+{
+    return kItemCost + (single ? vis / 16 * kSingle : vis);
+}
+
 // Cost of the first p pairs of one kv head, p < pairs (all but the last are whole).
 __host__ __device__ __forceinline__ long long pair_prefix(const ChunkReq &c, int w2, int p)
 {
@@ -141,18 +153,34 @@ __host__ __device__ __forceinline__ int pair_count(int n, int tpt)
     return n <= tpt ? 1 : (n + 2 * tpt - 1) / (2 * tpt);
 }
 
-__host__ __device__ __forceinline__ long long head_cost(const ChunkReq &c, int tpt)
+// Tokens of a request's last item.
+__host__ __device__ __forceinline__ int last_tokens(int n, int tpt)
 {
-    return pair_prefix(c, 2 * tpt, pair_count(c.n, tpt) - 1) + c.len + kItemCost;
+    return n - (pair_count(n, tpt) - 1) * 2 * tpt;
 }
 
-// Key tile at which a border `x` of cost into an item of `kt` tiles cuts it.
-__host__ __device__ __forceinline__ int cut_tile(long long x, int kt)
+__host__ __device__ __forceinline__ long long head_cost(const ChunkReq &c, int tpt)
+{
+    return pair_prefix(c, 2 * tpt, pair_count(c.n, tpt) - 1) +
+           item_cost(c.len, last_tokens(c.n, tpt) <= tpt);
+}
+
+// The cost of the request's longest item.
+__host__ __device__ __forceinline__ int longest_item(const ChunkReq &c, int tpt)
+{
+    const int last = last_tokens(c.n, tpt);
+    return max(item_cost(c.len, last <= tpt), last < c.n ? item_cost(c.len - last, false) : 0);
+}
+
+// Key tile at which a border `x` of cost into an item of `kt` tiles cuts it; an
+// end of at most kSnap tiles is not cut off.
+__host__ __device__ __forceinline__ int cut_tile(long long x, int kt, bool single)
 {
     if (x <= kItemCost)
         return 0;
-    const long long k = (x - kItemCost + kTile / 2) / kTile;
-    return k < kt ? static_cast<int>(k) : kt;
+    const long long keys = single ? (x - kItemCost) * 16 / kSingle : x - kItemCost;
+    const long long k = (keys + kTile / 2) / kTile;
+    return k <= kSnap ? 0 : k + kSnap < kt ? static_cast<int>(k) : kt;
 }
 
 // n / d for n >= 0, d > 0: 32-bit where it can be (a 64-bit division is slow).
@@ -171,9 +199,10 @@ __host__ __device__ __forceinline__ long long share_border(const CaPlan &pl, int
 
 // Shares over at most `grid` CTAs: none below kMinShare (about), and no item
 // over more than kMaxSpan + 2 of them.
-__host__ __device__ __forceinline__ void make_shares(CaPlan &pl, long long cost, int longest, int grid)
+__host__ __device__ __forceinline__ void make_shares(CaPlan &pl, long long cost, int longest,
+                                                     int grid)
 {
-    const float span = kMaxSpan * (static_cast<float>(cost) / (longest + kItemCost));
+    const float span = kMaxSpan * (static_cast<float>(cost) / max(longest, 1));
     const long long most = cost / kMinShare;
     int ctas = most < grid ? static_cast<int>(most) : grid;
     if (span < ctas)
@@ -197,9 +226,9 @@ struct CaWalk {
         it.single = it.ntok <= tpt;
         const int vis = it.c.len - it.c.n + it.tok0 + it.ntok;
         it.kt = (vis + kTile - 1) / kTile;
-        it.w = vis + kItemCost;
-        it.ka = it.x < pl.lo ? cut_tile(pl.lo - it.x, it.kt) : 0;
-        it.kb = it.x + it.w > pl.hi ? cut_tile(pl.hi - it.x, it.kt) : it.kt;
+        it.w = item_cost(vis, it.single);
+        it.ka = it.x < pl.lo ? cut_tile(pl.lo - it.x, it.kt, it.single) : 0;
+        it.kb = it.x + it.w > pl.hi ? cut_tile(pl.hi - it.x, it.kt, it.single) : it.kt;
     }
 
     __host__ __device__ __forceinline__ void entered(int i)
@@ -534,6 +563,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (tid == kLoadWarp * 32) {  // the maps' first use waits for them else
+        asm volatile("prefetch.tensormap [%0];" ::"l"(a.kmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(a.vmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&a.qmap) : "memory");
+    }
     pdl_wait();  // launched early: everything of the kernels before it is visible from here
     pdl_launch_dependents();
 
@@ -548,7 +582,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             bool bad;
             if (chunk_request(a, i, c, &bad)) {
                 mine += a.Hkv * head_cost(c, tpt);
-                longest = max(longest, c.len);
+                longest = max(longest, longest_item(c, tpt));
             }
             if (bad && blockIdx.x == 0)
                 set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
@@ -655,6 +689,28 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (wi == kLoadWarp) {
             // ------------------------------------------- the items, Q and K
             uint32_t loaded = 0, cur = 0, par = 0, qs = 0;  // ring cursor and parity, query tiles
+            auto load_q = [&](const CaDesc &d, int tiles) {
+                for (int x = 0; x < tiles; ++x, ++qs) {
+                    const int k = qs & 1;
+                    if (qs >= 2 && !warp_wait(&qempty[k], ((qs >> 1) - 1) & 1)) {
+                        bad = true;
+                        break;
+                    }
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&qfull[k], PANELS * G * tpt * 128);
+#pragma unroll
+                        for (int p = 0; p < PANELS; ++p)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
+                                "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                                    smem_u32(sQ + k * S::TILE + p * S::PANEL)),
+                                "l"(&a.qmap), "r"(p * 64), "r"(d.h * G),
+                                "r"(d.row0 + x * tpt), "r"(smem_u32(&qfull[k]))
+                                : "memory");
+                    }
+                    __syncwarp();
+                }
+            };
             CaWalk wk{a, plan, tpt, {}};
             bool more = wk.begin();
             for (; !bad; more = wk.next()) {
@@ -688,6 +744,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 int ids = block_y(d, d.ka * 8 + lane);
                 int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
                 const int tiles = it.single ? 1 : 2;
+                const bool q_early = qs == 0;  // the first item's: while the block ids come
+                if (q_early)
+                    load_q(d, tiles);
                 for (int t = 0; t < len; ++t) {
                     if (t > 0 && (t & 3) == 0) {
                         ids = ids_next;
@@ -706,26 +765,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     if (t > 0)
                         continue;
                     // Q behind the first K tile, which does not wait for the item before
-                    for (int x = 0; x < tiles; ++x, ++qs) {
-                        const int k = qs & 1;
-                        if (qs >= 2 && !warp_wait(&qempty[k], ((qs >> 1) - 1) & 1)) {
-                            bad = true;
-                            break;
-                        }
-                        if (elect_one()) {
-                            mbar_arrive_expect_tx(&qfull[k], PANELS * G * tpt * 128);
-#pragma unroll
-                            for (int p = 0; p < PANELS; ++p)
-                                asm volatile(
-                                    "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
-                                    "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                                        smem_u32(sQ + k * S::TILE + p * S::PANEL)),
-                                    "l"(&a.qmap), "r"(p * 64), "r"(d.h * G),
-                                    "r"(d.row0 + x * tpt), "r"(smem_u32(&qfull[k]))
-                                    : "memory");
-                        }
-                        __syncwarp();
-                    }
+                    if (!q_early)
+                        load_q(d, tiles);
                     if (bad)
                         break;
                 }
@@ -1096,6 +1137,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             }
             // ----------------------------------------------------- epilogue
             const CaDesc &d = *dp;
+            int tl = tid;  // (keeps what follows from it out of the key loop's registers)
+            asm volatile("" : "+r"(tl));
+            const int lane = tl & 31, wq = (tl >> 5) & 3, hf = (tl >> 7) & 1, r = wq * 32 + lane;
             float l = l0 + l1;
             float m = mref == -INFINITY ? -INFINITY : -negm;  // base 2, scaled
             if (cnt > 0) {
@@ -1190,8 +1234,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 if (b < plan.ctas) {
                     const long long lo = share_border(plan, b), hi = share_border(plan, b + 1);
                     if (lo < d.x + d.w) {
-                        const int k0 = lo > d.x ? cut_tile(lo - d.x, d.kt) : 0;
-                        const int k1 = hi < d.x + d.w ? cut_tile(hi - d.x, d.kt) : d.kt;
+                        const int k0 = lo > d.x ? cut_tile(lo - d.x, d.kt, single) : 0;
+                        const int k1 =
+                            hi < d.x + d.w ? cut_tile(hi - d.x, d.kt, single) : d.kt;
                         some = k0 < k1;
                     }
                 }
@@ -1202,7 +1247,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             const int row = x * kTile + r;  // within a slot
             __nv_bfloat16 *dst =
                 a.out +
-                (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + d.h * G + r % G) * D + hf * HD;
+                (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + d.h * G + r % G) * D +
+                hf * HD;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             float odd = 0.f;  // becomes NaN with any element of O
 #pragma unroll 1
@@ -1276,7 +1322,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         ex2_approx(fmaf(a.logit_scale < 0.f ? -s : s, ls, -m_r));
 #pragma unroll
                     for (int e = 0; e < OE; ++e)
-                        o[e] = fmaf(p, __bfloat162float(a.vpool[at + hf * HD + e * 32 + lane]), o[e]);
+                        o[e] =
+                            fmaf(p, __bfloat162float(a.vpool[at + hf * HD + e * 32 + lane]), o[e]);
                     bool over = true;  // nothing changes a NaN any more
 #pragma unroll
                     for (int e = 0; e < OE; ++e)
@@ -1309,77 +1356,188 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             bar_sync(9 + x, 32 * kSmWarps);
             if (sLast[x]) {
                 __threadfence();
-                // RB rows a warp at a time: lane k weighs share bs + k, then every lane
-                // adds up EL columns over the shares
-                constexpr int EL = D / 32, RB = 4;
-                const int first = __ffs(parts) - 1;
-                const bool in = parts >> lane & 1;
-                const float2 *ml_p = reinterpret_cast<const float2 *>(
-                                         slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
-                                         2 * kTile * D) + x * kTile;
-                for (int r0 = (hf * 4 + wq) * RB; r0 < toks * G; r0 += kSmWarps * RB) {
-                    float f[RB], L[RB], o[RB][EL];
-#pragma unroll
-                    for (int u = 0; u < RB; ++u) {
-                        const float2 ml = in ? __ldcg(ml_p + r0 + u) : make_float2(-INFINITY, 0.f);
-                        f[u] = ml.x;
-                        L[u] = ml.y;
-                    }
-#pragma unroll
-                    for (int u = 0; u < RB; ++u) {
-                        float M = f[u];
-#pragma unroll
-                        for (int w = 16; w; w >>= 1)
-                            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-                        f[u] = f[u] == -INFINITY ? 0.f : ex2_approx(f[u] - M);
-                        L[u] *= f[u];
-#pragma unroll
-                        for (int w = 16; w; w >>= 1)
-                            L[u] += __shfl_xor_sync(0xffffffffu, L[u], w);
-#pragma unroll
-                        for (int e = 0; e < EL; ++e)
-                            o[u][e] = 0.f;
-                    }
+                if constexpr (D == 64) {
+                    // A warp joins every eighth row, lane k weighs the k-th of them; then RW
+                    // rows at once, RB times, two shares in flight: 9 -> 4 us a pair's join.
+                    // With 128 dims the key loop loses registers to it (16 prompts 657 -> 697
+                    // us).
+                    constexpr int RW = 128 / D, RB = 4, ROWS = kTile / kSmWarps;
+                    const int first = __ffs(parts) - 1, rows = toks * G;
+                    const int w0 = hf * 4 + wq;
+                    const int row = min(w0 + (lane % ROWS) * kSmWarps, rows - 1);  // this lane's
+                    auto part_at = [&](int k) {
+                        return slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
+                               static_cast<size_t>(x * kTile) * D;
+                    };
+                    auto ml_at = [&](int k) {
+                        const float *p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
+                        return __ldcg(reinterpret_cast<const float2 *>(p + 2 * kTile * D) +
+                                      x * kTile + row);
+                    };
+                    float M = -INFINITY, L = 0.f;
                     for (unsigned q = parts; q; q &= q - 1) {
-                        const int k = __ffs(q) - 1;
-                        const float *o_p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
-                                           static_cast<size_t>(x * kTile + r0) * D + lane * EL;
-                        float w[RB][EL];
+                        const float2 ml = ml_at(__ffs(q) - 1);
+                        const float up = fmaxf(M, ml.x);
+                        if (up > -INFINITY)
+                            L = L * ex2_approx(M - up) + ml.y * ex2_approx(ml.x - up);
+                        M = up;
+                    }
+                    const float iv = L == 0.f ? 0.f : 1.f / L;
+                    auto weight = [&](float m) {
+                        return m == -INFINITY ? 0.f : ex2_approx(m - M) * iv;
+                    };
+                    const size_t to =
+                        (static_cast<size_t>(d.row0 + tile_tok + row / G) * a.Hq + d.h * G +
+                         row % G) * D;
+                    const int col = lane % (D / 4) * 4, sub = lane / (D / 4);
+#pragma unroll 1
+                    for (int u0 = 0; u0 < ROWS; u0 += RB * RW) {
+                        if (w0 + u0 * kSmWarps >= rows)
+                            break;
+                        float4 o[RB];
 #pragma unroll
-                        for (int u = 0; u < RB; ++u) {
-                            if (EL == 4) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4 *>(o_p + u * D));
-                                w[u][0] = v.x;
-                                w[u][1] = v.y;
-                                w[u][EL - 2] = v.z;
-                                w[u][EL - 1] = v.w;
-                            } else {
-                                const float2 v = __ldcg(reinterpret_cast<const float2 *>(o_p + u * D));
-                                w[u][0] = v.x;
-                                w[u][1] = v.y;
+                        for (int u = 0; u < RB; ++u)
+                            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (unsigned q = parts; q;) {
+                            const int k0 = __ffs(q) - 1;
+                            q &= q - 1;
+                            const int k1 = q ? __ffs(q) - 1 : k0;
+                            const bool two = q != 0;
+                            q &= q - 1;
+                            const float *p0 = part_at(k0) + col, *p1 = part_at(k1) + col;
+                            float4 v0[RB], v1[RB];
+#pragma unroll
+                            for (int u = 0; u < RB; ++u) {
+                                const int at = (w0 + (u0 + u * RW + sub) * kSmWarps) * D;
+                                v0[u] = __ldcg(reinterpret_cast<const float4 *>(p0 + at));
+                                v1[u] = __ldcg(reinterpret_cast<const float4 *>(p1 + at));
+                            }
+                            const float f0 = weight(ml_at(k0).x);
+                            const float f1 = two ? weight(ml_at(k1).x) : 0.f;
+#pragma unroll
+                            for (int u = 0; u < RB; ++u) {
+                                const float g0 = __shfl_sync(0xffffffffu, f0, u0 + u * RW + sub);
+                                const float g1 = __shfl_sync(0xffffffffu, f1, u0 + u * RW + sub);
+                                o[u].x += v0[u].x * g0;
+                                o[u].y += v0[u].y * g0;
+                                o[u].z += v0[u].z * g0;
+                                o[u].w += v0[u].w * g0;
+                                if (two) {  // of the only one, it would be added twice
+                                    o[u].x += v1[u].x * g1;
+                                    o[u].y += v1[u].y * g1;
+                                    o[u].z += v1[u].z * g1;
+                                    o[u].w += v1[u].w * g1;
+                                }
                             }
                         }
 #pragma unroll
                         for (int u = 0; u < RB; ++u) {
-                            const float fk = __shfl_sync(0xffffffffu, f[u], k);
-#pragma unroll
-                            for (int e = 0; e < EL; ++e)
-                                o[u][e] += w[u][e] * fk;
+                            const int k = u0 + u * RW + sub;
+                            const unsigned long long t = __shfl_sync(0xffffffffu, to, k);
+                            if (w0 + k * kSmWarps < rows)
+                                *reinterpret_cast<uint2 *>(a.out + t + col) =
+                                    make_uint2(pack_bf16x2(o[u].x, o[u].y),
+                                               pack_bf16x2(o[u].z, o[u].w));
                         }
                     }
+                } else {
+                    // RB rows a warp at a time: lane k weighs share bs + k, then every lane
+                    // adds up EL columns over the shares, two of them in flight
+                    constexpr int EL = D / 32, RB = 4;
+                    const int first = __ffs(parts) - 1;
+                    const bool in = parts >> lane & 1;
+                    const float2 *ml_p = reinterpret_cast<const float2 *>(
+                                             slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
+                                             2 * kTile * D) + x * kTile;
+                    const int r_begin = (hf * 4 + wq) * RB;
+                    float2 ml[RB];
+                    auto load_ml = [&](int r0) {
 #pragma unroll
-                    for (int u = 0; u < RB; ++u) {
-                        const int rr = r0 + u;
-                        if (rr >= toks * G)
-                            continue;
-                        const float iv = L[u] == 0.f ? 0.f : 1.f / L[u];
-                        __nv_bfloat16 *d2 =
-                            a.out + (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq +
-                                     d.h * G + rr % G) * D + lane * EL;
+                        for (int u = 0; u < RB; ++u)
+                            ml[u] = in ? __ldcg(ml_p + r0 + u) : make_float2(-INFINITY, 0.f);
+                    };
+                    if (r_begin < toks * G)
+                        load_ml(r_begin);
+                    for (int r0 = r_begin; r0 < toks * G; r0 += kSmWarps * RB) {
+                        float f[RB], o[RB][EL];
 #pragma unroll
-                        for (int e = 0; e < EL; e += 2)
-                            *reinterpret_cast<uint32_t *>(d2 + e) =
-                                pack_bf16x2(o[u][e] * iv, o[u][e + 1] * iv);
+                        for (int u = 0; u < RB; ++u) {
+                            float M = ml[u].x;
+#pragma unroll
+                            for (int w = 16; w; w >>= 1)
+                                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+                            f[u] = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - M);
+                            float L = ml[u].y * f[u];
+#pragma unroll
+                            for (int w = 16; w; w >>= 1)
+                                L += __shfl_xor_sync(0xffffffffu, L, w);
+                            f[u] *= L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                            for (int e = 0; e < EL; ++e)
+                                o[u][e] = 0.f;
+                        }
+                        if (r0 + kSmWarps * RB < toks * G)
+                            load_ml(r0 + kSmWarps * RB);
+                        for (unsigned q = parts; q;) {
+                            const int k0 = __ffs(q) - 1;
+                            q &= q - 1;
+                            const int k1 = q ? __ffs(q) - 1 : -1;
+                            q &= q - 1;
+                            float w[2][RB][EL];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int k = h ? k1 : k0;
+                                const float *o_p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
+                                                   static_cast<size_t>(x * kTile + r0) * D + lane * EL;
+#pragma unroll
+                                for (int u = 0; u < RB; ++u) {
+#pragma unroll
+                                    for (int e = 0; e < EL; ++e)
+                                        w[h][u][e] = 0.f;
+                                    if (k < 0)
+                                        continue;
+                                    if (EL == 4) {
+                                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                                            o_p + u * D));
+                                        w[h][u][0] = v.x;
+                                        w[h][u][1] = v.y;
+                                        w[h][u][EL - 2] = v.z;
+                                        w[h][u][EL - 1] = v.w;
+                                    } else {
+                                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(
+                                            o_p + u * D));
+                                        w[h][u][0] = v.x;
+                                        w[h][u][1] = v.y;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int k = h ? k1 : k0;
+                                if (k < 0)
+                                    continue;
+#pragma unroll
+                                for (int u = 0; u < RB; ++u) {
+                                    const float fk = __shfl_sync(0xffffffffu, f[u], k);
+#pragma unroll
+                                    for (int e = 0; e < EL; ++e)
+                                        o[u][e] += w[h][u][e] * fk;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < RB; ++u) {
+                            const int rr = r0 + u;
+                            if (rr >= toks * G)
+                                continue;
+                            __nv_bfloat16 *d2 =
+                                a.out + (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq +
+                                         d.h * G + rr % G) * D + lane * EL;
+#pragma unroll
+                            for (int e = 0; e < EL; e += 2)
+                                *reinterpret_cast<uint32_t *>(d2 + e) =
+                                    pack_bf16x2(o[u][e], o[u][e + 1]);
+                        }
                     }
                 }
             }

@@ -31,6 +31,7 @@ static int rnd(int n)  // the same numbers on every machine
 struct Part {
     int cta, ka, kb, kt, w;
     long long x;
+    bool single;
 };
 
 int main()
@@ -69,7 +70,7 @@ int main()
             bool bad;
             if (chunk_request(a, i, c, &bad)) {
                 cost += Hkv * head_cost(c, tpt);
-                longest = std::max(longest, c.len);
+                longest = std::max(longest, longest_item(c, tpt));
             }
             CHECK(!bad);
         }
@@ -100,7 +101,7 @@ int main()
                 const CaItem &t = walk.it;
                 CHECK(t.ka < t.kb);
                 CHECK(t.single == (t.ntok <= tpt) && t.ntok >= 1 && t.ntok <= 2 * tpt);
-                seen[{t.i, t.h, t.p}].push_back({b, t.ka, t.kb, t.kt, t.w, t.x});
+                seen[{t.i, t.h, t.p}].push_back({b, t.ka, t.kb, t.kt, t.w, t.x, t.single});
                 if (t.ka != 0 || t.kb != t.kt)
                     ++(t.ka == 0 ? heads : tails);
             }
@@ -132,8 +133,9 @@ int main()
                         const long long x = v[0].x, end = x + v[0].w;
                         if (lo >= end)
                             break;
-                        const int k0 = lo > x ? cut_tile(lo - x, v[0].kt) : 0;
-                        const int k1 = hi < end ? cut_tile(hi - x, v[0].kt) : v[0].kt;
+                        const int k0 = lo > x ? cut_tile(lo - x, v[0].kt, v[0].single) : 0;
+                        const int k1 =
+                            hi < end ? cut_tile(hi - x, v[0].kt, v[0].single) : v[0].kt;
                         if (k0 >= k1)
                             continue;
                         CHECK(k < v.size() && v[k].cta == b);
