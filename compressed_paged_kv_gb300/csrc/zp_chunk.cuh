@@ -82,29 +82,22 @@ struct ChunkReq {
 };
 
 // Reads and checks request i: true with n >= 1 when it has work; an empty
-// chunk is no work (its row and length are not read), and one whose offsets,
-// row or length are out of range sets *bad.
+// chunk is no work (whatever its row and length are), and one whose offsets,
+// row or length are out of range sets *bad.  The loads do not wait for the
+// checks: a chain of two (or, with req_idx, three) of them costs most of a
+// microsecond each.
 template <class Args>
 __host__ __device__ __forceinline__ bool chunk_request(const Args &a, int i, ChunkReq &c, bool *bad)
 {
-    *bad = false;
+    c.row = a.req_idx ? a.req_idx[i] : i;
+    const bool fits = c.row >= 0 && c.row < a.num_rows;
+    c.len = a.lengths[fits ? c.row : 0];
     c.first = a.starts[i];
     const int end = a.starts[i + 1];
     c.n = end - c.first;
-    if (c.first < 0 || end < c.first || end > a.total) {
-        *bad = true;
-        return false;
-    }
-    if (c.n == 0)
-        return false;
-    c.row = a.req_idx ? a.req_idx[i] : i;
-    if (c.row < 0 || c.row >= a.num_rows) {
-        *bad = true;
-        return false;
-    }
-    c.len = a.lengths[c.row];
-    *bad = c.len < c.n || c.len > a.stride * kBlk;
-    return !*bad;
+    const bool offsets = c.first >= 0 && end >= c.first && end <= a.total;
+    *bad = !offsets || (c.n > 0 && !(fits && c.len >= c.n && c.len <= a.stride * kBlk));
+    return !*bad && c.n > 0;
 }
 
 #endif  // __CUDACC__

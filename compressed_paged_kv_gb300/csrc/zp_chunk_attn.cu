@@ -61,7 +61,6 @@ static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4)
 // keys at full cost 60 single tokens beside two prompt pieces take 85 us, not 75.
 constexpr int kItemCost = 320;         // an item's fixed cost
 constexpr int kSingle = 8;             // 16ths of a pair's cost that a single item's key takes
-constexpr int kSnap = 3;               // key tiles that an item is not cut off for
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
 constexpr int kMaxSpan = 30;           // CTAs an item is cut over, about (a lane each joins them)
 constexpr int kLoadWarp = 2 * kSmWarps;       // then the products' warps of A and of B, V's loader
@@ -172,15 +171,14 @@ __host__ __device__ __forceinline__ int longest_item(const ChunkReq &c, int tpt)
     return max(item_cost(c.len, last <= tpt), last < c.n ? item_cost(c.len - last, false) : 0);
 }
 
-// Key tile at which a border `x` of cost into an item of `kt` tiles cuts it; an
-// end of at most kSnap tiles is not cut off.
+// Key tile at which a border `x` of cost into an item of `kt` tiles cuts it.
 __host__ __device__ __forceinline__ int cut_tile(long long x, int kt, bool single)
 {
     if (x <= kItemCost)
         return 0;
     const long long keys = single ? (x - kItemCost) * 16 / kSingle : x - kItemCost;
     const long long k = (keys + kTile / 2) / kTile;
-    return k <= kSnap ? 0 : k + kSnap < kt ? static_cast<int>(k) : kt;
+    return k < kt ? static_cast<int>(k) : kt;
 }
 
 // n / d for n >= 0, d > 0: 32-bit where it can be (a 64-bit division is slow).
