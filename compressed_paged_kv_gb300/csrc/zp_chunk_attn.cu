@@ -458,6 +458,18 @@ __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
+{
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Two fp32 operations at once.
 __device__ __forceinline__ void fma2(float &x, float &y, float m, float c)
 {
@@ -1020,12 +1032,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const int r = wq * 32 + lane;          // row of the tile
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + x * kTile + lane_off;
-        const uint32_t tO = tmem + 256 + x * kTile + lane_off + hf * HD;
-        float *max_mine = sMax + (x * 2 + hf) * kTile + r;
-        float *max_other = sMax + (x * 2 + 1 - hf) * kTile + r;
+        const uint32_t tH = tS + hf * HK, tP = tS + hf * (HK / 2);  // this half of S and of P
+        const uint32_t tO = (D == 128 ? tH : tP) + 256;             // and of O
+        static_assert(HD == (D == 128 ? HK : HK / 2), "O's half lies behind S's or P's");
+        const uint32_t max_at = smem_u32(sMax + (x * 2 + hf) * kTile + r);
+        constexpr uint32_t kOther = kTile * 4;  // max_at ^ kOther: the other half's
+        static_assert(S::off_max % (2 * kOther) == 0, "the halves differ in one bit");
         const uint32_t pair_bar = 1 + x * 4 + wq;  // the barrier of this warp and its other half
         const float ls = fmaxf(fabsf(a.logit_scale), 1e-30f);
-        const float grow = kRescale / ls;
         uint32_t ns = 0, no = 0, halves = 0;
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
         while (const CaDesc *dp = enter()) {
@@ -1045,14 +1059,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 bad = __any_sync(0xffffffffu, bad);
                 lent = false;
             }
-            // keys the thread's half of the next tile still holds for the row, and
-            // for the warp's first row: fewer than all, and the tile is masked
+            // keys the thread's half of the next tile still holds for the row: fewer
+            // than all for any row of the warp, and the tile is masked
             int m_lim = lim - (dp->ka + (single ? x : 0)) * kTile - hf * HK;
-            const int m_slack = __shfl_sync(0xffffffffu, lim, 0) - lim;
             const int m_step = single ? 2 * kTile : kTile;
             float mref = -INFINITY, negm = 0.f;
             float l0 = 0.f, l1 = 0.f;
-            for (int t = 0; t < cnt; ++t, m_lim -= m_step) {
+            for (int t = cnt; t > 0; --t, m_lim -= m_step) {
                 if (!bad && !ca_wait(&sfull[x], ns & 1))
                     bad = true;
                 ++ns;
@@ -1067,10 +1080,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     uint32_t sr[HK];
 #pragma unroll
                     for (int o = 0; o < HK; o += 16)
-                        ld16(tS + hf * HK + o, sr, o);
+                        ld16(tH + o, sr, o);
                     ld_wait(sr);
                     float *s = reinterpret_cast<float *>(sr);
-                    if (m_lim + m_slack < HK) {
+                    if (__any_sync(0xffffffffu, m_lim < HK)) {
 #pragma unroll
                         for (int c = 0; c < HK; ++c)
                             s[c] = c < m_lim ? s[c] : -INFINITY;
@@ -1084,14 +1097,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                                    : fmaxf(mx[e], s[c + e]);
                     }
                     float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    *max_mine = m_new;
+                    st_shared_f32(max_at, m_new);
                     bar_sync(pair_bar, 64);  // also: both halves of S are in registers
-                    m_new = fmaxf(m_new, *max_other);
-                    const bool up = t == 0 ? m_new > -INFINITY : m_new > mref + grow;
+                    m_new = fmaxf(m_new, ld_shared_f32(max_at ^ kOther));
+                    const bool up = (m_new - mref) * ls > kRescale;  // or the first: infinite
                     float f = 1.f;
+                    bool rescale = false;
                     if (up) {
                         const float old = negm;
-                        const bool fresh = mref == -INFINITY;
+                        const bool fresh = mref == -INFINITY;  // (O holds nothing yet)
+                        rescale = !fresh;
                         mref = m_new;
                         negm = -m_new * ls;
                         f = fresh ? 0.f : ex2_approx(negm - old);
@@ -1109,10 +1124,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             add2(l0, l1, s[c + e], s[c + e + 1]);
                             pk[e / 2] = pack_bf16x2(s[c + e], s[c + e + 1]);
                         }
-                        st16(tS + hf * (HK / 2) + c / 2, pk, 0);
+                        st16(tP + c / 2, pk, 0);
                     }
                     // O by the factor, this half of the row in flight at once
-                    if (t > 0 && __any_sync(0xffffffffu, up)) {
+                    if (__any_sync(0xffffffffu, rescale)) {
                         uint32_t ov[HD];
 #pragma unroll
                         for (int o = 0; o < HD; o += 16)
@@ -1146,9 +1161,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 ++no;
                 fence_after();
                 bad = __any_sync(0xffffffffu, bad);
-                *max_mine = l;  // the other half's sum
+                st_shared_f32(max_at, l);  // for the other half
                 bar_sync(pair_bar, 64);
-                const float other = *max_other;
+                const float other = ld_shared_f32(max_at ^ kOther);
                 l = hf == 0 ? l + other : other + l;
                 bar_sync(pair_bar, 64);  // read before the next maximum is written
             }
@@ -1156,7 +1171,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             const bool join = single && len > 1;  // B holds the odd key tiles
             if (single && x == 1) {
                 if (join) {  // A reads both halves of O: the lanes are the same
-                    *max_mine = hf == 0 ? m : l;
+                    st_shared_f32(max_at, hf == 0 ? m : l);
                     lent = true;
                     fence_before();
                     __syncwarp();
