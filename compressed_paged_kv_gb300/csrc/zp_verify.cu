@@ -294,9 +294,7 @@ __device__ __forceinline__ void st_dsmem_pair(uint32_t addr, const Pair &v)
 
 }  // namespace
 
-// NT threads a CTA: 128 for many requests, so that the chains of many clusters
-// run beside each other, 512 for few, so that a row has as many loads in
-// flight.
+// NT threads a CTA: see launch_verify_draft.
 template <class T, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyArgs a, int ctas)
 {
@@ -603,15 +601,25 @@ static cudaError_t launch_verify_t(const VerifyArgs &a, int ctas, cudaStream_t s
 
 cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, int sms, cudaStream_t s)
 {
-    // An SM holds 1,024 of these threads.  All clusters at once where that goes:
-    // eight CTAs of 512 threads, else of 128, else four or two of those.
-    const long long R = a.R;
-    if (R * kVfCtas <= 2ll * sms)
-        return bf16 ? launch_verify_t<__nv_bfloat16, 512>(a, kVfCtas, s)
-                    : launch_verify_t<float, 512>(a, kVfCtas, s);
-    const int ctas = R * 8 <= 8ll * sms ? 8 : R * 4 <= 8ll * sms ? 4 : 2;
-    return bf16 ? launch_verify_t<__nv_bfloat16, 128>(a, ctas, s)
-                : launch_verify_t<float, 128>(a, ctas, s);
+    // Small CTAs, as many as give every warp of theirs a batch, up to eight a
+    // request (256 requests of a vocabulary of 2,000: 7.4 us with one, 15.6 with
+    // eight) and up to what the SMs hold at once, 1,024 threads each (256 of
+    // 151,936: 52 us with four, 54 with eight, 74 with two).  A few requests with
+    // long rows get CTAs of twice the threads, for twice the loads in flight (48
+    // of 151,936: 20 us, not 24; but 48 of 32,000, two batches a warp of the small
+    // CTAs: 9.7, not 8.9).
+    constexpr int kSmall = 128, kLarge = 256;
+    const long long R = a.R, vectors = (static_cast<long long>(a.vocab) * (bf16 ? 2 : 4) + 15) / 16;
+    const int step = kSmall * kVfBatch;  // vectors of a batch of every warp of a small CTA
+    if (R * kVfCtas <= 1024 / kLarge * sms && vectors > 2 * kVfCtas * step)
+        return bf16 ? launch_verify_t<__nv_bfloat16, kLarge>(a, kVfCtas, s)
+                    : launch_verify_t<float, kLarge>(a, kVfCtas, s);
+    int ctas = 1;
+    while (ctas < kVfCtas && ctas * step < vectors &&
+           (ctas == 1 || R * 2 * ctas <= 1024 / kSmall * static_cast<long long>(sms)))
+        ctas *= 2;
+    return bf16 ? launch_verify_t<__nv_bfloat16, kSmall>(a, ctas, s)
+                : launch_verify_t<float, kSmall>(a, ctas, s);
 }
 
 }  // namespace zp
