@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const int r0 = min(a.R, tid * per), r1 = min(a.R, r0 + per);
         long long mine = 0;
         int longest = 0;
+        ChunkReq c;  // the last one
         for (int i = r0; i < r1; ++i) {
-            ChunkReq c;
             bool bad;
             if (chunk_request(a, i, c, &bad)) {
                 mine += a.Hkv * head_cost(c, tpt);
@@ -623,11 +623,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             atomicMax(&sLast[0], longest);
         }
         __syncthreads();
-        long long before = incl - mine, cost = 0;
-        for (int w = 0; w < kCaThreads / 32; ++w) {
-            if (w < wi)
-                before += scan[w];
-            cost += scan[w];
+        long long before = incl - mine, cost;
+        {
+            long long v = lane < kCaThreads / 32 ? scan[lane] : 0;
+            const long long own = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o)
+                    v += y;
+            }
+            cost = __shfl_sync(0xffffffffu, v, 31);
+            before += __shfl_sync(0xffffffffu, v - own, wi);
         }
         CaPlan p;
         make_shares(p, cost, sLast[0], static_cast<int>(gridDim.x));
@@ -636,7 +643,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (tid == 0 && p.lo >= p.hi)
             plan = p;
         if (before <= p.lo && p.lo < before + mine) {
-            for (int i = r0; i < r1; ++i) {  // the request the share begins in
+            p.i0 = r0;
+            p.c0 = c;
+            for (int i = r0; i < r1 && per > 1; ++i) {  // the request the share begins in
                 bool bad;
                 if (!chunk_request(a, i, p.c0, &bad))
                     continue;
