@@ -20,16 +20,16 @@
 // bits the joins alone took 10 us of a call.)
 //
 // One cluster of CTAs a request.  A warp owns a contiguous run of the deciding
-// row and reads it (of p and q) once, 16 bytes a lane and kVfBatch of them in
-// flight, leaving its lanes' sums in shared memory now and then; every CTA gets
+// row and reads it (of p and q) once, 16 bytes a lane and 2 kVfBatch of them under
+// way, leaving its lanes' sums in shared memory now and then; every CTA gets
 // every warp's sum through distributed shared memory, and the warp that the
 // level falls into finds the stretch of its run from the sums it left, reads
 // that a second time (out of L2) and finds the token.  Bound by the bytes of
 // the deciding rows for large batches (256 requests of 151,936 fp32 p and q: 218
-// MB in 52 us = 4.2 TB/s, 0.62 of the copy peak; the clusters of rejected tokens
-// read twice as much as the others), and by the chain of dependent reads (offsets
-// -> tokens -> their probabilities -> row -> sums -> stretch) for small ones (one
-// request of 32,000: 7 us).
+// MB in 48.5 us = 4.5 TB/s, 0.66 of the copy peak; the clusters of rejected
+// tokens read twice as much as the others), and by the chain of dependent reads
+// (offsets -> tokens -> their probabilities -> row -> sums -> stretch) for small
+// ones (one request of 32,000: 6.6 us).
 #include "zp_chunk.cuh"
 
 namespace zp {
@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kVfCtas = 8;    // of a cluster, at most: the portable most
 constexpr int kVfBatch = 4;   // vectors of p and of q a lane has in flight
-constexpr int kVfMarks = 64;  // sums left by the warps of a CTA, together
+constexpr int kVfMarks = 32;  // sums left by the warps of a CTA, together
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -80,10 +80,27 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b)
     asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
     return v;
 }
-__device__ __forceinline__ float low2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float low2(uint64_t v)
+{
+    return __uint_as_float(static_cast<uint32_t>(v));
+}
 __device__ __forceinline__ float high2(uint64_t v)
 {
     return __uint_as_float(static_cast<uint32_t>(v >> 32));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // A row as 16-byte vectors of p: vector i holds elements first + i * VE ..; the
@@ -210,6 +227,54 @@ struct Row {
             s = t;
         }
     }
+
+    // The same of the vectors v0 + lane, + 32, .. below v1, through this lane's ring
+    // of 2 kVfBatch vectors, of p or of p and q: a copy is always under way, where a
+    // batch's loads wait for its additions (256 requests 51.7 -> 48.5 us).  `ends` and
+    // `mark` are called after each kVfBatch vectors.  A lane reads what it copied
+    // itself, so its own waits are enough.
+    template <bool Q, class E, class M>
+    __device__ __forceinline__ void stream(uint4 *ring, int v0, int v1, int lane, uint64_t &s,
+                                           uint64_t &c, E ends, M mark) const
+    {
+        constexpr int DEPTH = Q ? kVfBatch : 2 * kVfBatch;
+        const uint32_t at = smem_u32(ring);
+        auto fetch = [&](int k, int stage) {  // vector k of the lane
+            const int v = v0 + lane + k * 32;
+            if (v >= lo && v < hi && v < v1) {
+                const int e0 = first + v * VE;
+                cp_async16(at + stage * 512, p + e0);
+                if (Q)
+                    cp_async16(at + (DEPTH + stage) * 512, q + e0);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k)
+            fetch(k, k);
+        int n = 0;
+#pragma unroll 1
+        for (int v = v0; v < v1; v += kVfBatch * 32, ++n) {
+            const int half = Q ? 0 : (n & 1) * kVfBatch;
+#pragma unroll
+            for (int u = 0; u < kVfBatch; ++u) {
+                cp_async_wait<DEPTH - 1>();
+                const int i = v + u * 32 + lane;
+                uint4 up = make_uint4(0u, 0u, 0u, 0u), uq = up;
+                if (i >= lo && i < hi) {
+                    up = ring[(half + u) * 32];
+                    if (Q)
+                        uq = ring[(DEPTH + half + u) * 32];
+                }
+                add_fast<Q>(i, up, uq, s, c);
+                fetch(n * kVfBatch + u + DEPTH, half + u);
+            }
+            ends(v);
+            mark(n);
+        }
+        cp_async_wait<0>();
+    }
+
     // The same of any vectors below `end`, those outside with weight 0.
     template <class F>
     __device__ __forceinline__ void ragged(int v, int end, F take) const
@@ -304,6 +369,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
     constexpr int STEP = kVfBatch * 32;           // vectors of a batch
     __shared__ __align__(8) Pair sums[4][kVfCtas * WARPS];  // every run's, in the row's order, a pass
     __shared__ Pair marks[WARPS][MARKS][32];  // the lanes' sums after a stretch of the run
+    __shared__ uint4 ring[WARPS][2 * kVfBatch][32];  // the lanes' vectors on their way
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, wi = threadIdx.x >> 5;
@@ -388,29 +454,37 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
         auto total = [&] {
             return (normal(low2(s2), low2(c2)) + normal(high2(s2), high2(c2))) + normal(s, c);
         };
-        for (int v = v0, n = 0; v < v1; v += STEP, ++n) {
-            if (!strict && row.lo < row.hi) {
-                if (row.q)
-                    row.template batch<true>(v + lane, [&](int u, const uint4 &up, const uint4 &uq) {
-                        row.template add_fast<true>(v + u * 32 + lane, up, uq, s2, c2);
-                    });
-                else
-                    row.template batch<false>(v + lane, [&](int u, const uint4 &up, const uint4 &uq) {
-                        row.template add_fast<false>(v + u * 32 + lane, up, uq, s2, c2);
-                    });
-                // the row's ends
-                const int edge = lane == 0 ? (row.lo ? 0 : -1)
-                                           : (row.hi < row.count ? row.count - 1 : -1);
-                if (lane < 2 && edge >= v && edge < v + STEP) {
-                    float w[VE], e[VE];
-                    row.weights(edge, w, e);
-                    add(0, w, e);
-                }
-            } else {
-                row.ragged(v + lane, v1, add);
-            }
+        auto mark = [&](int n) {
             if ((n + 1) % stretch == 0)
                 marks[wi][n / stretch][lane] = total();
+        };
+        auto ends = [&](int v) {  // the row's, where they lie in this batch
+            const int edge = lane == 0 ? (row.lo ? 0 : -1)
+                                       : (row.hi < row.count ? row.count - 1 : -1);
+            if (lane < 2 && edge >= v && edge < v + STEP) {
+                float w[VE], e[VE];
+                row.weights(edge, w, e);
+                add(0, w, e);
+            }
+        };
+        if (strict || row.lo >= row.hi) {
+            for (int v = v0, n = 0; v < v1; v += STEP, ++n) {
+                row.ragged(v + lane, v1, add);
+                mark(n);
+            }
+        } else if (row.q) {
+            row.template stream<true>(&ring[wi][0][lane], v0, v1, lane, s2, c2, ends, mark);
+        } else if (sizeof(T) == 4) {  // (not where a vector holds eight weights to add:
+            // 128 requests of 128,000 without q 18.9 us this way, 18.2 by batches)
+            row.template stream<false>(&ring[wi][0][lane], v0, v1, lane, s2, c2, ends, mark);
+        } else {
+            for (int v = v0, n = 0; v < v1; v += STEP, ++n) {
+                row.template batch<false>(v + lane, [&](int u, const uint4 &up, const uint4 &uq) {
+                    row.template add_fast<false>(v + u * 32 + lane, up, uq, s2, c2);
+                });
+                ends(v);
+                mark(n);
+            }
         }
         const Pair mine = warp_sum(total());
         if (pass == 0)
@@ -606,14 +680,13 @@ cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, int sms, cudaStr
     // Small CTAs, as many as give every warp of theirs a batch, up to eight a
     // request (256 requests of a vocabulary of 2,000: 7.4 us with one, 15.6 with
     // eight) and up to what the SMs hold at once, 1,024 threads each (256 of
-    // 151,936: 52 us with four, 54 with eight, 74 with two).  A few requests with
-    // long rows get CTAs of twice the threads, for twice the loads in flight (48
-    // of 151,936: 20 us, not 24; but 48 of 32,000, two batches a warp of the small
-    // CTAs: 9.7, not 8.9).
+    // 151,936: 52 us with four, 54 with eight, 74 with two).  Up to two CTAs an SM
+    // and long rows: CTAs of twice the threads, for twice the loads in flight (32
+    // requests of 151,936: 14.0 us, not 15.7; but 48 of 50,257: 12.1, not 10.2).
     constexpr int kSmall = 128, kLarge = 256;
     const long long R = a.R, vectors = (static_cast<long long>(a.vocab) * (bf16 ? 2 : 4) + 15) / 16;
     const int step = kSmall * kVfBatch;  // vectors of a batch of every warp of a small CTA
-    if (R * kVfCtas <= 1024 / kLarge * sms && vectors > 2 * kVfCtas * step)
+    if (R * kVfCtas <= 2ll * sms && vectors > 2 * kVfCtas * step)
         return bf16 ? launch_verify_t<__nv_bfloat16, kLarge>(a, kVfCtas, s)
                     : launch_verify_t<float, kLarge>(a, kVfCtas, s);
     int ctas = 1;
