@@ -46,7 +46,7 @@
 //
 // Measured, 32 heads of 128 over 8 kv heads: 2,048 tokens over 32,049, 1.04
 // TFLOP in 0.64 ms = 1.63 PFLOP/s (0.73 ms in a row: the power limit), 0.84 of
-// the library products' rate; 16 prompts of 331 to 4,007 tokens in 0.64 ms = 1.2
+// the library products' rate; 16 prompts of 331 to 4,007 tokens in 0.63 ms = 1.2
 // PFLOP/s; 256 speculative chunks over 1,024 to 2,040 tokens, 1.64 GB in 0.28 ms
 // = 5.9 TB/s, 0.87 of the copy peak.  What bounds it: in the first two the chain
 // of a stream (product -> softmax -> product; tensor pipe 60 % busy, issue slots
