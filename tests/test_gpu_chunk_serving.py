@@ -348,6 +348,16 @@ def test_a_second_result_is_within_the_same_bound(spans, d):
         assert bool(ok.all())
 
 
+@pytest.mark.parametrize("n,T,Hkv,Hq,d", [(9000, 9000, 1, 2, 64), (7001, 12345, 1, 5, 128)])
+def test_a_long_prompt(n, T, Hkv, Hq, d):
+    """A whole prompt of thousands of tokens, and a piece as long."""
+    b = Batch([(n, T)], Hkv, Hq, d, seed=41)
+    cache = b.cache()
+    b.attn(cache)
+    assert cache.status() == zp.OK
+    b.check_attn()
+
+
 def test_packed_rows_past_32_bits():
     """The last rows of packed tensors of more than 2^27 rows (2^33 elements)."""
     n, T, total = 21, 90, (1 << 27) + 40
@@ -459,6 +469,51 @@ def test_weights_that_are_not_finite(draft, V):
     starts = _ints([2 * i for i in range(R + 1)])
     cache = _pool_cache(R)
     q = q if draft else None
+    acc, nxt = _verify(cache, toks, starts, p, q, u, r)
+    assert cache.status() == zp.OK
+    assert (acc.tolist(), nxt.tolist()) == _plain(toks, starts, p, q, u, r)
+
+
+@pytest.mark.parametrize("dtype,draft", [(torch.float32, True), (torch.float32, False),
+                                         (torch.bfloat16, True), (torch.bfloat16, False)])
+@pytest.mark.parametrize("R,V", [(700, 500), (320, 40000), (160, 40001), (64, 9001), (30, 70003),
+                                 (3, 33000)])
+def test_every_cluster_size(dtype, draft, R, V):
+    """Batches and vocabularies for clusters of one, two, four and eight CTAs of
+    either size."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(39)
+    total = 2 * R
+    x = 2 * torch.randn(total, V, generator=g, device=DEV)
+    p = torch.softmax(x, 1).to(dtype)
+    q = torch.softmax(x + 0.5 * torch.randn(total, V, generator=g, device=DEV), 1).to(dtype)
+    toks = torch.multinomial(q.float(), 1, generator=g)[:, 0].int().roll(1)
+    u, r = torch.rand(total, generator=g, device=DEV), torch.rand(R, generator=g, device=DEV)
+    starts = _ints([2 * i for i in range(R + 1)])
+    q = q if draft else None
+    cache = _pool_cache(R)
+    acc, nxt = _verify(cache, toks, starts, p, q, u, r)
+    assert cache.status() == zp.OK
+    assert (acc.tolist(), nxt.tolist()) == _plain(toks, starts, p, q, u, r)
+
+
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("V", [5000, 70001])
+def test_16_bit_weights_that_are_not_finite(draft, V):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(40)
+    total, R = 16, 8
+    x = torch.randn(total, V, generator=g, device=DEV)
+    p = torch.softmax(x, 1).bfloat16()
+    q = torch.softmax(x + torch.randn(total, V, generator=g, device=DEV), 1).bfloat16()
+    toks = torch.randint(10, V, (total,), generator=g, device=DEV).int()
+    for row in range(total):  # positions no drafted token has
+        t = p if row % 3 or not draft else q
+        t[row, row % 10] = [math.nan, math.inf, -math.inf, -0.5][row % 4]
+    u, r = torch.rand(total, generator=g, device=DEV), torch.rand(R, generator=g, device=DEV)
+    starts = _ints([2 * i for i in range(R + 1)])
+    q = q if draft else None
+    cache = _pool_cache(R)
     acc, nxt = _verify(cache, toks, starts, p, q, u, r)
     assert cache.status() == zp.OK
     assert (acc.tolist(), nxt.tolist()) == _plain(toks, starts, p, q, u, r)
