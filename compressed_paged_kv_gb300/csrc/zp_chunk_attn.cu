@@ -1475,12 +1475,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 } else {
                     // RB rows a warp at a time: lane k weighs share bs + k, then every lane
                     // adds up EL columns over the shares, two of them in flight
-                    constexpr int EL = D / 32, RB = 4;
+                    constexpr int EL = 4, RB = 4;
                     const int first = __ffs(parts) - 1;
                     const bool in = parts >> lane & 1;
-                    const float2 *ml_p = reinterpret_cast<const float2 *>(
-                                             slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
-                                             2 * kTile * D) + x * kTile;
+                    const float2 *ml_p =
+                        reinterpret_cast<const float2 *>(
+                            slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
+                            2 * kTile * D) + x * kTile;
                     const int r_begin = (hf * 4 + wq) * RB;
                     float2 ml[RB];
                     auto load_ml = [&](int r0) {
@@ -1519,8 +1520,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int k = h ? k1 : k0;
-                                const float *o_p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
-                                                   static_cast<size_t>(x * kTile + r0) * D + lane * EL;
+                                const float *o_p =
+                                    slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
+                                    static_cast<size_t>(x * kTile + r0) * D + lane * EL;
 #pragma unroll
                                 for (int u = 0; u < RB; ++u) {
 #pragma unroll
@@ -1528,19 +1530,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                         w[h][u][e] = 0.f;
                                     if (k < 0)
                                         continue;
-                                    if (EL == 4) {
-                                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                                            o_p + u * D));
-                                        w[h][u][0] = v.x;
-                                        w[h][u][1] = v.y;
-                                        w[h][u][EL - 2] = v.z;
-                                        w[h][u][EL - 1] = v.w;
-                                    } else {
-                                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(
-                                            o_p + u * D));
-                                        w[h][u][0] = v.x;
-                                        w[h][u][1] = v.y;
-                                    }
+                                    const float4 v =
+                                        __ldcg(reinterpret_cast<const float4 *>(o_p + u * D));
+                                    w[h][u][0] = v.x;
+                                    w[h][u][1] = v.y;
+                                    w[h][u][2] = v.z;
+                                    w[h][u][3] = v.w;
                                 }
                             }
 #pragma unroll
