@@ -111,7 +111,7 @@ struct CaSmem {
     static constexpr int PANEL = kTile * 128;            // bytes of 128 rows of 64 dims
     static constexpr int TILE = PANELS * PANEL;
     static constexpr int NK = D == 128 ? 2 : 5, NV = D == 128 ? 3 : 5;  // stages of K and of V
-    static constexpr int XC = D / 4;                     // columns of O a step of the epilogue
+    static constexpr int XC = 16;  // columns of O a step of the epilogue
     static constexpr int off_q = 0;                      // Q of A, Q of B
     static constexpr int off_k = off_q + 2 * TILE;
     static constexpr int off_v = off_k + NK * TILE;
@@ -410,6 +410,14 @@ __device__ __forceinline__ void st16(uint32_t t, const uint32_t (&v)[N], int o)
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
         "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(t),
         ZP_IN16(v, o)
+        : "memory");
+}
+
+__device__ __forceinline__ void st8(uint32_t t, const uint32_t (&v)[8])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
         : "memory");
 }
 
@@ -1045,6 +1053,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         // A row belongs to two threads, of warps w (columns 0 .. 63 of S and the
         // first half of O's) and w + 4 (the others), which exchange its maximum.
         constexpr int HK = kTile / 2, HD = D / 2;
+        // columns of P a store: the widest that the registers allow (16 prompts of 128
+        // dims 642 us with 16, 621 with 32; with 64 dims 32 spills three times as much)
+        constexpr int PC = D == 128 ? 32 : 16;
         const int x = wi / kSmWarps;           // tile A or B
         const int wq = wi & 3;                 // tensor-memory lanes 32 wq ..
         const int hf = (wi >> 2) & 1;          // the row's half
@@ -1133,17 +1144,20 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         l1 *= f;
                     }
 #pragma unroll
-                    for (int c = 0; c < HK; c += 32) {
-                        uint32_t pk[16];
+                    for (int c = 0; c < HK; c += PC) {
+                        uint32_t pk[PC / 2];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < PC; e += 2) {
                             fma2(s[c + e], s[c + e + 1], ls, negm);
                             s[c + e] = ex2_approx(s[c + e]);
                             s[c + e + 1] = ex2_approx(s[c + e + 1]);
                             add2(l0, l1, s[c + e], s[c + e + 1]);
                             pk[e / 2] = pack_bf16x2(s[c + e], s[c + e + 1]);
                         }
-                        st16(tP + c / 2, pk, 0);
+                        if constexpr (PC == 32)
+                            st16(tP + c / 2, pk, 0);
+                        else
+                            st8(tP + c / 2, pk);
                     }
                     // O by the factor, this half of the row in flight at once
                     if (__any_sync(0xffffffffu, rescale)) {
@@ -1169,9 +1183,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             }
             // ----------------------------------------------------- epilogue
             const CaDesc &d = *dp;
-            int tl = tid;  // (keeps what follows from it out of the key loop's registers)
-            asm volatile("" : "+r"(tl));
-            const int lane = tl & 31, wq = (tl >> 5) & 3, hf = (tl >> 7) & 1, r = wq * 32 + lane;
+            int G = a.Hq / a.Hkv;  // (what follows from it stays out of the key loop's registers)
+            asm volatile("" : "+r"(G));
             float l = l0 + l1;
             float m = mref == -INFINITY ? -INFINITY : -negm;  // base 2, scaled
             if (cnt > 0) {
@@ -1221,14 +1234,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             // XC columns of O, the halves joined
             auto load_o = [&](int c, uint32_t (&v)[XC]) {
                 if (read_o) {
-#pragma unroll
-                    for (int o = 0; o < XC; o += 16)
-                        ld16(tO + c + o, v, o);
+                    ld16(tO + c, v, 0);
                     if (join) {
                         uint32_t w[XC];
-#pragma unroll
-                        for (int o = 0; o < XC; o += 16)
-                            ld16(tO + kTile + c + o, w, o);
+                        ld16(tO + kTile + c, w, 0);
                         ld_wait(v);
                         ld_wait(w);
 #pragma unroll
@@ -1294,15 +1303,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     odd += __uint_as_float(v[e]) * 0.f;
                 if (mine && !bad) {
                     if (whole) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int e = 0; e < XC; e += 16) {
-                            uint32_t o[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                o[k] = pack_bf16x2(__uint_as_float(v[e + 2 * k]) * inv,
-                                                   __uint_as_float(v[e + 2 * k + 1]) * inv);
-                            st_global_v8(dst + c + e, o);
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            o[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * inv,
+                                               __uint_as_float(v[2 * k + 1]) * inv);
+                        st_global_v8(dst + c, o);
                     } else {
                         float *to = slot + static_cast<size_t>(row) * D + hf * HD + c;
 #pragma unroll
