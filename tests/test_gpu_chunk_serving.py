@@ -244,6 +244,38 @@ def test_calls_at_once_on_disjoint_requests():
             assert torch.equal(x, y)
 
 
+def test_chunks_beside_a_compression():
+    """zp_compress of two full rows on one stream, a chunk's append and
+    attention of the others on another, one handle: as one after the other."""
+    N, w = 8, 8
+    spans = [(70, 900), (5, 333), (130, 2000), (0, N * B), (0, N * B)]
+    wq = torch.randn(1, 2, 8, w, 128, device=DEV).bfloat16()
+    results = []
+    for at_once in (False, True, True, True):
+        b = Batch(spans, 2, 8, 128, seed=29)
+        nb = b.kp[0].shape[0]
+        cache = b.cache()
+        refs = torch.zeros(nb, dtype=I32, device=DEV)
+        refs[b.tables[b.tables >= 0].long()] = 1
+        unused = torch.nonzero(refs == 0).flatten().int()
+        free = torch.cat([unused, torch.zeros(nb - unused.numel(), dtype=I32, device=DEV)])
+        count = _ints([unused.numel()])
+        s = [torch.cuda.Stream(), torch.cuda.Stream()] if at_once else [None, None]
+        torch.cuda.synchronize()
+        cache.compress(b.tables, b.lengths, wq, N, w, 0.5, free, count, refs,
+                       req_idx=_ints([3, 4]), stream=s[0])
+        for _ in range(3):
+            b.append(cache, stream=s[1])
+            b.attn(cache, stream=s[1])
+        torch.cuda.synchronize()
+        assert cache.status() == zp.OK
+        assert b.lengths.tolist()[3:] == [(N - 1) * B] * 2
+        results.append([b.out, b.kp[0], b.vp[0], b.tables])
+        for got, want in zip(results[-1], results[0]):
+            view = (lambda t: _bits(t)) if got.dtype == torch.bfloat16 else (lambda t: t)
+            assert torch.equal(view(got), view(want))
+
+
 def test_two_handles_at_once():
     """Two handles over the same pools (each its own workspace), their chunk
     attentions on two streams."""
