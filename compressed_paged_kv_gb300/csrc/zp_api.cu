@@ -157,7 +157,8 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     const size_t o_ap_occ = A.take(4 * static_cast<size_t>(D.num_blocks));
     const size_t o_ap_last = A.take(4 * static_cast<size_t>(D.num_blocks));
     const size_t o_ap_plan = A.take(16 * static_cast<size_t>(D.max_requests));
-    const size_t o_ca_arr = A.take(8 * static_cast<size_t>(c->num_sms));
+    const size_t ca_arr = 4 * (4 * static_cast<size_t>(c->num_sms) + 1);  // and ca_entered
+    const size_t o_ca_arr = A.take(ca_arr);
     const size_t o_ca_part = A.take(4 * zp::chunk_attn_part_floats(D.head_dim, c->num_sms));
     const size_t total = A.take(0);
 
@@ -193,6 +194,7 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     ws.ap_last = reinterpret_cast<int32_t *>(b + o_ap_last);
     ws.ap_plan = reinterpret_cast<int4 *>(b + o_ap_plan);
     ws.ca_arrived = reinterpret_cast<uint32_t *>(b + o_ca_arr);
+    ws.ca_entered = ws.ca_arrived + 4 * c->num_sms;
     ws.ca_part = reinterpret_cast<float *>(b + o_ca_part);
     c->kpools.assign(D.k_pools, D.k_pools + D.num_layers);
     c->vpools.assign(D.v_pools, D.v_pools + D.num_layers);
@@ -211,7 +213,7 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
          cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
          cudaMemset(b + o_rowmark, 0, 4 * static_cast<size_t>(D.max_requests)) == cudaSuccess &&
          cudaMemset(b + o_ap_call, 0, o_ap_occ - o_ap_call) == cudaSuccess &&
-         cudaMemset(b + o_ca_arr, 0, 8 * static_cast<size_t>(c->num_sms)) == cudaSuccess &&
+         cudaMemset(b + o_ca_arr, 0, ca_arr) == cudaSuccess &&
          cudaMemcpy(ws.kmaps, kmaps.data(), sizeof(CUtensorMap) * D.num_layers,
                     cudaMemcpyHostToDevice) == cudaSuccess &&
          cudaMemcpy(ws.vmaps, vmaps.data(), sizeof(CUtensorMap) * D.num_layers,
@@ -896,6 +898,7 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.part = c->ws.ca_part;
     a.arrived = c->ws.ca_arrived;
+    a.entered = c->ws.ca_entered;
     a.sticky = c->ws.sticky;
     return zp::launch_chunk_attn(a, c->d, c->num_sms, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
@@ -978,10 +981,6 @@ zp_status zp_cache_status(zp_cache *c, void *stream, int32_t *out_status)
     if (cudaMemcpyAsync(&v, c->ws.sticky, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaMemsetAsync(c->ws.sticky, 0, 4, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
-        return ZP_ERR_CUDA;
-    // a chunk attention that gave up waiting may have left its arrivals uncounted
-    if (v == ZP_ERR_TIMEOUT &&
-        cudaMemsetAsync(c->ws.ca_arrived, 0, 8 * static_cast<size_t>(c->num_sms), s) != cudaSuccess)
         return ZP_ERR_CUDA;
     *out_status = v;
     return ZP_OK;

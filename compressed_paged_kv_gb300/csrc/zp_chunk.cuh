@@ -42,7 +42,8 @@ struct ChunkAttnArgs {
     float logit_scale;  // scale * log2(e)
     __nv_bfloat16 *out;
     float *part;        // partial results of the items cut between CTAs
-    uint32_t *arrived;  // [2 * SMs] of them that are written; 0 between calls
+    uint32_t *arrived;  // [2][2 * SMs] of them that are written: two sets, used in turn
+    uint32_t *entered;  // CTAs that have entered a call, modulo two calls'
     int32_t *sticky;
 };
 

@@ -42,7 +42,13 @@
 // contiguous share, cut at key tiles, so that few long rows and many short
 // ones both fill the GPU.  An item cut by a border leaves partial results (m,
 // l, O) in the handle's workspace, and the CTA that arrives last joins them in
-// the fixed order of the shares: results do not depend on the timing.
+// the fixed order of the shares: results do not depend on the timing.  The
+// arrivals are counted in two sets of words that the calls use in turn.  A CTA
+// takes a number when it enters: with g CTAs a call, numbers 0 .. g - 1 (modulo
+// 2 g) belong to a call of the first set and the others to one of the second,
+// whatever the order in which they enter.  Each clears its words of the other
+// set, which no CTA of this call touches, for the next call: whatever a call
+// that gave up a wait has left uncounted is gone, with no help from the host.
 //
 // Measured, 32 heads of 128 over 8 kv heads: 2,048 tokens over 32,049, 1.04
 // TFLOP in 0.64 ms = 1.63 PFLOP/s (0.73 ms in a row: the power limit), 0.84 of
@@ -124,8 +130,8 @@ struct CaSmem {
     // Qempty[2], turn[2]; described, read [kDescs]; half, taken, done
     static constexpr int NBAR = 2 * NK + 2 * NV + 14 + 2 * kDescs + 3;
     static constexpr int off_tmem = off_bar + NBAR * 8;
-    static constexpr int off_last = off_tmem + 8;         // int [2]
-    static constexpr int BYTES = off_last + 8;
+    static constexpr int off_last = off_tmem + 8;         // int [2]; the call's set of arrivals
+    static constexpr int BYTES = off_last + 16;
     static_assert(BYTES <= 232448 && off_desc % 8 == 0 && off_bar % 8 == 0, "shared memory");
 };
 
@@ -598,6 +604,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     }
     pdl_wait();  // launched early: everything of the kernels before it is visible from here
     pdl_launch_dependents();
+
+    // the call's set of arrivals (a thread with no requests of its own in most batches)
+    if (tid == kLoadVWarp * 32) {
+        const unsigned set = 2 * gridDim.x;
+        const bool second = atomicInc(a.entered, 2 * gridDim.x - 1) >= gridDim.x;
+        uint32_t *other = a.arrived + (second ? 0 : set) + 2 * blockIdx.x;
+        other[0] = other[1] = 0;
+        sLast[2] = second ? set : 0;
+    }
 
     // the shares: thread t adds up a contiguous run of requests
     {
@@ -1389,7 +1404,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             bar_sync(9 + x, 32 * kSmWarps);
             if (r == 0 && hf == 0) {
                 const unsigned n = __popc(parts);
-                sLast[x] = atomicInc(&a.arrived[2 * bs + x], n - 1) == n - 1;
+                sLast[x] = atomicAdd(&a.arrived[sLast[2] + 2 * bs + x], 1) == n - 1;
             }
             bar_sync(9 + x, 32 * kSmWarps);
             if (sLast[x]) {

@@ -52,7 +52,8 @@ struct Workspace {
     int4 *ap_plan;        // [max_requests] tail block, fresh block, rows to copy, trigger slot
     // chunk attention (zp_paged_chunk_attn) keeps its own
     float *ca_part;       // partial results of the work items cut between SMs
-    uint32_t *ca_arrived; // [2 * SMs] of them that are written; 0 between calls
+    uint32_t *ca_arrived; // [2][2 * SMs] of them that are written: two sets, used in turn
+    uint32_t *ca_entered; // CTAs that have entered a call, modulo two calls'
 };
 
 // ------------------------------------------------------------ launch args
