@@ -34,8 +34,14 @@
 //
 // A key past the length or hidden from a row has probability 0, but 0 times an
 // infinity or NaN is NaN.  The V rows past the length in the last block are
-// cleared in shared memory; a row whose O came out NaN while its tiles held
-// values hidden from it is computed again with plain fp32 arithmetic.
+// cleared in shared memory.  Values hidden from some rows of an item and seen by
+// others cannot be: a CTA whose share gave an O that is not finite to a row with
+// keys hidden from it walks its whole share once more, "clean".  Then what is not
+// finite in a V row hidden from the item's first token counts as 0 in the
+// products, and the epilogue puts the infinities and NaNs back into the outputs of
+// the rows that see them.  A share is walked at most twice, however long its rows
+// are: with such values in every request, 160 chunks of 64 tokens over 2,000 (8
+// heads of 128) take 250 to 570 us, 109 without any.
 //
 // The grid is one CTA an SM.  Every CTA adds up the cost of all items (the
 // keys each reads, plus a fixed part) from the device arrays and takes an equal,
@@ -108,6 +114,7 @@ struct CaDesc {
     int ka, kb;  // this CTA's key tiles
     int kt;      // all its key tiles
     int w;       // cost
+    int clean;   // of the second walk
     long long x; // cost before it
 };
 
@@ -130,8 +137,10 @@ struct CaSmem {
     // Qempty[2], turn[2]; described, read [kDescs]; half, taken, done
     static constexpr int NBAR = 2 * NK + 2 * NV + 14 + 2 * kDescs + 3;
     static constexpr int off_tmem = off_bar + NBAR * 8;
-    static constexpr int off_last = off_tmem + 8;         // int [2]; the call's set of arrivals
-    static constexpr int BYTES = off_last + 16;
+    // int: last arrived [2]; the call's set of arrivals; what the walk met (1: rows to
+    // walk for again, 2: a wait given up); partial results left to the second walk [2]
+    static constexpr int off_last = off_tmem + 8;
+    static constexpr int BYTES = off_last + 24;
     static_assert(BYTES <= 232448 && off_desc % 8 == 0 && off_bar % 8 == 0, "shared memory");
 };
 
@@ -445,10 +454,9 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // Bounded waits, all for this CTA's own work: 32 M tries, which the hardware
-// lets last 72 clocks (with 640 threads waiting) to 2,600 (with one): seconds.
-// A wait ends within microseconds, but for the rows that are computed twice
-// (see the end of the epilogue): those of an item over 100,000 keys hold its CTA
-// up for 2.8 s, and no wait ran out.  No sleeping in between: the 64 ns naps of
+// lets last 72 clocks (with 640 threads waiting) to 2,600 (with one): a second or
+// more.  A wait ends within microseconds, in the second walk (see the head of the
+// file) within a few hundred.  No sleeping in between: the 64 ns naps of
 // mbar_wait cost 10 to 30 % of the kernel's time (256 speculative chunks 314 ->
 // 295 us, 16 prompts 752 -> 687 us), and a look at the clock as much.
 constexpr uint32_t kCaSpins = 1u << 25;
@@ -480,6 +488,31 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 __device__ __forceinline__ void bar_sync(uint32_t id, uint32_t threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The barrier of bar_sync; whether v holds for any of the threads.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t threads, bool v)
+{
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(any)
+        : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return any != 0;
+}
+
+// Two bf16 numbers, each 0 where it is not finite.
+__device__ __forceinline__ uint32_t finite2(uint32_t v)
+{
+    if ((v & 0x7f80u) == 0x7f80u)
+        v &= 0xffff0000u;
+    if ((v & 0x7f800000u) == 0x7f800000u)
+        v &= 0xffffu;
+    return v;
 }
 
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v)
@@ -612,6 +645,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         uint32_t *other = a.arrived + (second ? 0 : set) + 2 * blockIdx.x;
         other[0] = other[1] = 0;
         sLast[2] = second ? set : 0;
+        sLast[3] = sLast[4] = sLast[5] = 0;
     }
 
     // the shares: thread t adds up a contiguous run of requests
@@ -707,6 +741,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         ++nd;
     };
 
+    // At the end of a walk, every warp of the CTA: whether a second one follows.
+    auto walk_again = [&](bool clean) {
+        if (bad && lane == 0)
+            atomicOr(&sLast[3], 2);
+        fence_before();
+        bar_sync(0, kCaThreads);
+        return !clean && *static_cast<volatile int *>(&sLast[3]) == 1;
+    };
+    auto ended_clean = [&] { return sDesc[nd % kDescs].clean != 0; };  // at an end's description
+
     if (wi >= 2 * kSmWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         // The tiles of a ring: eight cache blocks of 16 keys, PANELS boxes each.
@@ -763,99 +807,109 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     __syncwarp();
                 }
             };
-            CaWalk wk{a, plan, tpt, {}};
-            bool more = wk.begin();
-            for (; !bad; more = wk.next()) {
-                const CaItem &it = wk.it;
-                const int j = nd % kDescs;
-                if (nd >= kDescs && !warp_wait(&read[j], (nd / kDescs - 1) & 1)) {
-                    bad = true;
-                    break;
-                }
-                CaDesc d;
-                d.row0 = it.c.first + it.tok0;
-                d.ntok = more ? it.ntok : 0;
-                d.h = it.h;
-                d.pos0 = it.c.len - it.c.n + it.tok0;
-                d.len = it.c.len;
-                d.row = it.c.row;
-                d.ka = it.ka;
-                d.kb = it.kb;
-                d.kt = it.kt;
-                d.w = it.w;
-                d.x = it.x;
-                if (lane == 0) {
-                    sDesc[j] = d;
-                    mbar_arrive(&described[j]);
-                }
-                __syncwarp();
-                ++nd;
-                if (!more)
-                    break;
-                const int len = d.kb - d.ka;
-                int ids = block_y(d, d.ka * 8 + lane);
-                int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
-                const int tiles = it.single ? 1 : 2;
-                const bool q_early = qs == 0;  // the first item's: while the block ids come
-                if (q_early)
-                    load_q(d, tiles);
-                for (int t = 0; t < len; ++t) {
-                    if (t > 0 && (t & 3) == 0) {
-                        ids = ids_next;
-                        ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
-                    }
-                    if (loaded >= NK && !warp_wait(&kempty[cur], par ^ 1)) {
+            for (bool clean = false;; clean = true) {
+                CaWalk wk{a, plan, tpt, {}};
+                bool more = wk.begin();
+                for (; !bad; more = wk.next()) {
+                    const CaItem &it = wk.it;
+                    const int j = nd % kDescs;
+                    if (nd >= kDescs && !warp_wait(&read[j], (nd / kDescs - 1) & 1)) {
                         bad = true;
                         break;
                     }
-                    load_tile(a.kmap, sK + cur * S::TILE, &kfull[cur], ids, t);
-                    ++loaded;
-                    if (++cur == NK) {
-                        cur = 0;
-                        par ^= 1;
+                    CaDesc d;
+                    d.row0 = it.c.first + it.tok0;
+                    d.ntok = more ? it.ntok : 0;
+                    d.h = it.h;
+                    d.pos0 = it.c.len - it.c.n + it.tok0;
+                    d.len = it.c.len;
+                    d.row = it.c.row;
+                    d.ka = it.ka;
+                    d.kb = it.kb;
+                    d.kt = it.kt;
+                    d.w = it.w;
+                    d.clean = clean;
+                    d.x = it.x;
+                    if (lane == 0) {
+                        sDesc[j] = d;
+                        mbar_arrive(&described[j]);
                     }
-                    if (t > 0)
-                        continue;
-                    // Q behind the first K tile, which does not wait for the item before
-                    if (!q_early)
-                        load_q(d, tiles);
-                    if (bad)
+                    __syncwarp();
+                    ++nd;
+                    if (!more)
                         break;
+                    const int len = d.kb - d.ka;
+                    int ids = block_y(d, d.ka * 8 + lane);
+                    int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
+                    const int tiles = it.single ? 1 : 2;
+                    const bool q_early = qs == 0;  // the first item's: while the block ids come
+                    if (q_early)
+                        load_q(d, tiles);
+                    for (int t = 0; t < len; ++t) {
+                        if (t > 0 && (t & 3) == 0) {
+                            ids = ids_next;
+                            ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
+                        }
+                        if (loaded >= NK && !warp_wait(&kempty[cur], par ^ 1)) {
+                            bad = true;
+                            break;
+                        }
+                        load_tile(a.kmap, sK + cur * S::TILE, &kfull[cur], ids, t);
+                        ++loaded;
+                        if (++cur == NK) {
+                            cur = 0;
+                            par ^= 1;
+                        }
+                        if (t > 0)
+                            continue;
+                        // Q behind the first K tile, which does not wait for the item before
+                        if (!q_early)
+                            load_q(d, tiles);
+                        if (bad)
+                            break;
+                    }
                 }
+                // every copy issued has landed before the CTA may exit
+                for (uint32_t k = qs > 2 ? qs - 2 : 0; k < qs; ++k)
+                    bad |= !warp_wait(&qfull[k & 1], (k >> 1) & 1);
+                for (uint32_t k = loaded > NK ? loaded - NK : 0; k < loaded; ++k)
+                    bad |= !warp_wait(&kfull[k % NK], (k / NK) & 1);
+                if (!walk_again(clean))
+                    break;
             }
-            // every copy issued has landed before the CTA may exit
-            for (uint32_t k = qs > 2 ? qs - 2 : 0; k < qs; ++k)
-                bad |= !warp_wait(&qfull[k & 1], (k >> 1) & 1);
-            for (uint32_t k = loaded > NK ? loaded - NK : 0; k < loaded; ++k)
-                bad |= !warp_wait(&kfull[k % NK], (k / NK) & 1);
         } else if (wi == kLoadVWarp) {
             // ------------------------------------------------------------- V
             uint32_t loaded = 0, cur = 0, par = 0;
-            while (const CaDesc *dp = bad ? nullptr : enter()) {
-                const CaDesc d = *dp;
-                leave();
-                const int len = d.kb - d.ka;
-                int ids = block_y(d, d.ka * 8 + lane);
-                int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
-                for (int t = 0; t < len; ++t) {
-                    if (t > 0 && (t & 3) == 0) {
-                        ids = ids_next;
-                        ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
-                    }
-                    if (loaded >= NV && !warp_wait(&vempty[cur], par ^ 1)) {
-                        bad = true;
-                        break;
-                    }
-                    load_tile(a.vmap, sV + cur * S::TILE, &vfull[cur], ids, t);
-                    ++loaded;
-                    if (++cur == NV) {
-                        cur = 0;
-                        par ^= 1;
+            for (;;) {
+                while (const CaDesc *dp = bad ? nullptr : enter()) {
+                    const CaDesc d = *dp;
+                    leave();
+                    const int len = d.kb - d.ka;
+                    int ids = block_y(d, d.ka * 8 + lane);
+                    int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
+                    for (int t = 0; t < len; ++t) {
+                        if (t > 0 && (t & 3) == 0) {
+                            ids = ids_next;
+                            ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
+                        }
+                        if (loaded >= NV && !warp_wait(&vempty[cur], par ^ 1)) {
+                            bad = true;
+                            break;
+                        }
+                        load_tile(a.vmap, sV + cur * S::TILE, &vfull[cur], ids, t);
+                        ++loaded;
+                        if (++cur == NV) {
+                            cur = 0;
+                            par ^= 1;
+                        }
                     }
                 }
+                for (uint32_t k = loaded > NV ? loaded - NV : 0; k < loaded; ++k)
+                    bad |= !warp_wait(&vfull[k % NV], (k / NV) & 1);
+                if (!walk_again(ended_clean()))
+                    break;
+                leave();
             }
-            for (uint32_t k = loaded > NV ? loaded - NV : 0; k < loaded; ++k)
-                bad |= !warp_wait(&vfull[k % NV], (k / NV) & 1);
         } else {
             // ----------------------------------------------------- products
             // One warp a stream, so that the waits of one lie beside the products of
@@ -896,171 +950,188 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     mbar_arrive(bar);
                 __syncwarp();
             };
-            while (const CaDesc *dp = bad ? nullptr : enter()) {
-                const int len = dp->kb - dp->ka, ka = dp->ka, kb = dp->kb, cached = dp->len;
-                const bool single = dp->ntok <= tpt;
-                // the stream's key tiles: t with t % 2 == x of a single item; of a
-                // pair all for B, the ones its last token sees for A
-                const int na = x == 0 ? (dp->pos0 + min(dp->ntok, tpt) + kTile - 1) / kTile : kb;
-                leave();
-                const int cnt = single ? (len + 1 - x) / 2 : max(0, min(kb, na) - ka);
-                const int last = single ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
-                const uint32_t slot = single ? qs : qs + x;
-                const uint32_t qd = __shfl_sync(0xffffffffu, qdesc + (slot & 1) * STEP, 0);
-                auto skip_k = [&] {  // a tile of the other stream's
-                    wait(&kfull[kc], kpar);
-                    if (bad)
-                        return;
-                    tell(&kempty[kc]);
-                    k_on();
-                };
-                auto skip_v = [&] {
-                    wait(&vfull[vc], vpar);
-                    if (bad)
-                        return;
-                    tell(&vempty[vc]);
-                    v_on();
-                };
-                auto issue_s = [&](uint32_t kd, int from, int to) {
-#pragma unroll
-                    for (int ks = from; ks < to; ++ks) {
-                        const uint32_t o = ((ks >> 2) * S::PANEL + (ks & 3) * 32) >> 4;
-                        mma_ss(tS, qd + o, kd + o, ID_S, ks > 0);
-                    }
-                };
-                auto done_s = [&](int t) {
-                    mma_commit(&sfull[x]);
-                    mma_commit(&kempty[kc]);
-                    if (t == last)
-                        mma_commit(&qempty[slot & 1]);
-                };
-                auto first_s = [&](bool mine, int t) {
-                    if (!mine) {
-                        skip_k();
-                        return;
-                    }
-                    wait(&kfull[kc], kpar);
-                    if (bad)
-                        return;
-                    fence_after();
-                    const uint32_t kd = __shfl_sync(0xffffffffu, kdesc + kc * STEP, 0);
-                    if (elect_one()) {
-                        issue_s(kd, 0, D / 16);
-                        done_s(t);
-                    }
-                    __syncwarp();
-                    k_on();
-                };
-                // P V with V tile t, then S with K tile `next`
-                auto burst = [&](int t, int next) {
-                    wait(&vfull[vc], vpar);
-                    const int fill = cached - (ka + t) * kTile;  // rows of the tile that are cached
-                    if (fill < kTile && (fill & (kBlk - 1)) && !bad) {
-                        // the rest of the last cache block: whatever it holds counts as 0
-                        const int end = (fill + kBlk - 1) / kBlk * kBlk;
-                        for (int c = lane; c < (end - fill) * (D / 8); c += 32)
-                            st_shared_v4(smem_u32(sV + vc * S::TILE) +
-                                             swz(fill + c / (D / 8), c % (D / 8), kTile),
-                                         make_uint4(0u, 0u, 0u, 0u));
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    if (next < len)
+            uint32_t walks = 0;
+            for (;;) {
+                while (const CaDesc *dp = bad ? nullptr : enter()) {
+                    const int len = dp->kb - dp->ka, ka = dp->ka, kb = dp->kb;
+                    const bool single = dp->ntok <= tpt;
+                    // the key from which on V is tidied, negative in the second walk
+                    const int tidy = dp->clean ? -(dp->pos0 + 1) : dp->len;
+                    // the stream's key tiles: t with t % 2 == x of a single item; of a
+                    // pair all for B, the ones its last token sees for A
+                    const int na =
+                        x == 0 ? (dp->pos0 + min(dp->ntok, tpt) + kTile - 1) / kTile : kb;
+                    leave();
+                    const int cnt = single ? (len + 1 - x) / 2 : max(0, min(kb, na) - ka);
+                    const int last = single ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
+                    const uint32_t slot = single ? qs : qs + x;
+                    const uint32_t qd = __shfl_sync(0xffffffffu, qdesc + (slot & 1) * STEP, 0);
+                    auto skip_k = [&] {  // a tile of the other stream's
                         wait(&kfull[kc], kpar);
-                    const bool first = t == (single ? x : 0);
-                    if (first) {  // the epilogue of O's last use has read it
-                        if (no > 0)
-                            wait(&oempty[x], (no - 1) & 1);
-                        ++no;
-                    }
-                    const uint32_t vd = __shfl_sync(0xffffffffu, vdesc + vc * STEP, 0);
-                    const uint32_t kd = __shfl_sync(0xffffffffu, kdesc + kc * STEP, 0);
-                    const bool more_s = next <= last;
-                    wait(&turn[x], turns++ & 1);
-                    wait(&pready[x], np++ & 1);
-                    if (bad)
-                        return;
-                    fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < kTile / 16; ++ks)
-                            mma_ts(tO, tS + ks * 8, vd + ks * (2048 >> 4), ID_O, !first || ks > 0);
-                        mma_commit(&vempty[vc]);
-                        if (t == last)
-                            mma_commit(&ofull[x]);
-                        // the other stream wakes up while the rest is queued
-                        if (more_s) {
-                            issue_s(kd, 0, D / 32);
-                            mbar_arrive(&turn[1 - x]);
-                            issue_s(kd, D / 32, D / 16);
-                            done_s(next);
-                        } else {
-                            mbar_arrive(&turn[1 - x]);
-                        }
-                    }
-                    __syncwarp();
-                    v_on();
-                    if (more_s)
-                        k_on();
-                    if (next < len && next > last) {
+                        if (bad)
+                            return;
                         tell(&kempty[kc]);
                         k_on();
-                    }
-                };
-                auto no_burst = [&] {
-                    wait(&turn[x], turns++ & 1);
-                    if (!bad)
-                        tell(&turn[1 - x]);
-                };
-                wait(&qfull[qs & 1], (qs >> 1) & 1);
-                if (!single)
-                    wait(&qfull[(qs + 1) & 1], ((qs + 1) >> 1) & 1);
-                if (bad)
-                    break;
-                if (!single)
-                    tell(&qempty[(qs + 1 - x) & 1]);  // the other stream's queries
-                if (cnt == 0)
-                    tell(&qempty[slot & 1]);
-                if (single) {  // K0 K1, then V0 K2 | V1 K3 | ..: in turn A's and B's
-                    first_s(x == 0, 0);
-                    if (len > 1)
-                        first_s(x == 1, 1);
-                    for (int t = 0; t < len && !bad; t += 2) {
-                        if (x == 1) {
-                            skip_v();
-                            if (t + 2 < len)
-                                skip_k();
+                    };
+                    auto skip_v = [&] {
+                        wait(&vfull[vc], vpar);
+                        if (bad)
+                            return;
+                        tell(&vempty[vc]);
+                        v_on();
+                    };
+                    auto issue_s = [&](uint32_t kd, int from, int to) {
+#pragma unroll
+                        for (int ks = from; ks < to; ++ks) {
+                            const uint32_t o = ((ks >> 2) * S::PANEL + (ks & 3) * 32) >> 4;
+                            mma_ss(tS, qd + o, kd + o, ID_S, ks > 0);
                         }
-                        if (t + x < len)
-                            burst(t + x, t + x + 2);
-                        else
-                            no_burst();
-                        if (x == 0 && t + 1 < len) {
-                            skip_v();
-                            if (t + 3 < len)
-                                skip_k();
+                    };
+                    auto done_s = [&](int t) {
+                        mma_commit(&sfull[x]);
+                        mma_commit(&kempty[kc]);
+                        if (t == last)
+                            mma_commit(&qempty[slot & 1]);
+                    };
+                    auto first_s = [&](bool mine, int t) {
+                        if (!mine) {
+                            skip_k();
+                            return;
+                        }
+                        wait(&kfull[kc], kpar);
+                        if (bad)
+                            return;
+                        fence_after();
+                        const uint32_t kd = __shfl_sync(0xffffffffu, kdesc + kc * STEP, 0);
+                        if (elect_one()) {
+                            issue_s(kd, 0, D / 16);
+                            done_s(t);
+                        }
+                        __syncwarp();
+                        k_on();
+                    };
+                    // P V with V tile t, then S with K tile `next`
+                    auto burst = [&](int t, int next) {
+                        wait(&vfull[vc], vpar);
+                        // rows that may hold what is not finite and counts as 0: the rest of the
+                        // last cached block, or in the second walk all but the first token's keys
+                        // (both streams may tidy a tile at once: each writes zeros alone)
+                        const int from = max(abs(tidy) - (ka + t) * kTile, 0);
+                        if (from < kTile && (tidy < 0 || (from & (kBlk - 1))) && !bad) {
+                            const int end = tidy < 0 ? kTile : (from + kBlk - 1) / kBlk * kBlk;
+                            for (int c = from * (D / 8) + lane; c < end * (D / 8); c += 32) {
+                                const uint32_t at = smem_u32(sV + vc * S::TILE) +
+                                                    swz(c / (D / 8), c % (D / 8), kTile);
+                                const uint4 v = ld_shared_v4(at);
+                                const uint4 f = make_uint4(finite2(v.x), finite2(v.y), finite2(v.z),
+                                                           finite2(v.w));
+                                if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0)
+                                    st_shared_v4(at, f);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        if (next < len)
+                            wait(&kfull[kc], kpar);
+                        const bool first = t == (single ? x : 0);
+                        if (first) {  // the epilogue of O's last use has read it
+                            if (no > 0)
+                                wait(&oempty[x], (no - 1) & 1);
+                            ++no;
+                        }
+                        const uint32_t vd = __shfl_sync(0xffffffffu, vdesc + vc * STEP, 0);
+                        const uint32_t kd = __shfl_sync(0xffffffffu, kdesc + kc * STEP, 0);
+                        const bool more_s = next <= last;
+                        wait(&turn[x], turns++ & 1);
+                        wait(&pready[x], np++ & 1);
+                        if (bad)
+                            return;
+                        fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = 0; ks < kTile / 16; ++ks)
+                                mma_ts(tO, tS + ks * 8, vd + ks * (2048 >> 4), ID_O,
+                                       !first || ks > 0);
+                            mma_commit(&vempty[vc]);
+                            if (t == last)
+                                mma_commit(&ofull[x]);
+                            // the other stream wakes up while the rest is queued
+                            if (more_s) {
+                                issue_s(kd, 0, D / 32);
+                                mbar_arrive(&turn[1 - x]);
+                                issue_s(kd, D / 32, D / 16);
+                                done_s(next);
+                            } else {
+                                mbar_arrive(&turn[1 - x]);
+                            }
+                        }
+                        __syncwarp();
+                        v_on();
+                        if (more_s)
+                            k_on();
+                        if (next < len && next > last) {
+                            tell(&kempty[kc]);
+                            k_on();
+                        }
+                    };
+                    auto no_burst = [&] {
+                        wait(&turn[x], turns++ & 1);
+                        if (!bad)
+                            tell(&turn[1 - x]);
+                    };
+                    wait(&qfull[qs & 1], (qs >> 1) & 1);
+                    if (!single)
+                        wait(&qfull[(qs + 1) & 1], ((qs + 1) >> 1) & 1);
+                    if (bad)
+                        break;
+                    if (!single)
+                        tell(&qempty[(qs + 1 - x) & 1]);  // the other stream's queries
+                    if (cnt == 0)
+                        tell(&qempty[slot & 1]);
+                    if (single) {  // K0 K1, then V0 K2 | V1 K3 | ..: in turn A's and B's
+                        first_s(x == 0, 0);
+                        if (len > 1)
+                            first_s(x == 1, 1);
+                        for (int t = 0; t < len && !bad; t += 2) {
+                            if (x == 1) {
+                                skip_v();
+                                if (t + 2 < len)
+                                    skip_k();
+                            }
+                            if (t + x < len)
+                                burst(t + x, t + x + 2);
+                            else
+                                no_burst();
+                            if (x == 0 && t + 1 < len) {
+                                skip_v();
+                                if (t + 3 < len)
+                                    skip_k();
+                            }
+                        }
+                    } else {  // K0, then V0 K1 | V1 K2 | ..
+                        first_s(cnt > 0, 0);
+                        for (int t = 0; t < len && !bad; ++t) {
+                            if (t < cnt) {
+                                burst(t, t + 1);
+                            } else {
+                                skip_v();
+                                if (t + 1 < len)
+                                    skip_k();
+                                no_burst();
+                            }
                         }
                     }
-                } else {  // K0, then V0 K1 | V1 K2 | ..
-                    first_s(cnt > 0, 0);
-                    for (int t = 0; t < len && !bad; ++t) {
-                        if (t < cnt) {
-                            burst(t, t + 1);
-                        } else {
-                            skip_v();
-                            if (t + 1 < len)
-                                skip_k();
-                            no_burst();
-                        }
-                    }
+                    qs += single ? 1 : 2;
                 }
-                qs += single ? 1 : 2;
+                // every product issued is done before the tensor memory is freed
+                if (elect_one())
+                    mma_commit(done);
+                __syncwarp();
+                bad |= !warp_wait(done, walks++ & 1);
+                if (!walk_again(ended_clean()))
+                    break;
+                leave();
             }
-            // every product issued is done before the tensor memory is freed
-            if (elect_one())
-                mma_commit(done);
-            __syncwarp();
-            bad |= !warp_wait(done, 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSmRegs));
@@ -1087,516 +1158,530 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const float ls = fmaxf(fabsf(a.logit_scale), 1e-30f);
         uint32_t ns = 0, no = 0, halves = 0;
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
-        while (const CaDesc *dp = enter()) {
-            const bool single = dp->ntok <= tpt;
-            const int len = dp->kb - dp->ka, pos0 = dp->pos0;
-            const int tile_tok = single || x == 0 ? 0 : tpt;       // its first token in the item
-            const int toks = min(dp->ntok - tile_tok, tpt);        // its tokens
-            const int tok = min(r / G, toks - 1);                  // rows past the last follow it
-            const int lim = pos0 + tile_tok + tok + 1;             // keys the row sees
-            const bool live = wq * 32 < toks * G;
-            int cnt = single ? (len + 1 - x) / 2 : len;            // key tiles
-            if (!single && x == 0)
-                cnt = max(0, min(dp->kb, (pos0 + tpt + kTile - 1) / kTile) - dp->ka);
-            if (lent && cnt > 0) {  // A has taken what B left in place of its maxima
-                if (!bad && !ca_wait(taken, halves++ & 1))
-                    bad = true;
-                bad = __any_sync(0xffffffffu, bad);
-                lent = false;
-            }
-            // keys the thread's half of the next tile still holds for the row: fewer
-            // than all for any row of the warp, and the tile is masked
-            int m_lim = lim - (dp->ka + (single ? x : 0)) * kTile - hf * HK;
-            const int m_step = single ? 2 * kTile : kTile;
-            float mref = -INFINITY, negm = 0.f;
-            float l0 = 0.f, l1 = 0.f;
-            for (int t = cnt; t > 0; --t, m_lim -= m_step) {
-                if (!bad && !ca_wait(&sfull[x], ns & 1))
-                    bad = true;
-                ++ns;
-                bad = __any_sync(0xffffffffu, bad);
-                if (bad) {
-                    if (live)
-                        bar_sync(pair_bar, 64);
-                    continue;
+        for (;;) {
+            while (const CaDesc *dp = enter()) {
+                const bool single = dp->ntok <= tpt;
+                const int len = dp->kb - dp->ka, pos0 = dp->pos0;
+                const int tile_tok = single || x == 0 ? 0 : tpt;  // its first token in the item
+                const int toks = min(dp->ntok - tile_tok, tpt);   // its tokens
+                const int tok = min(r / G, toks - 1);             // rows past the last follow it
+                const int lim = pos0 + tile_tok + tok + 1;        // keys the row sees
+                const bool live = wq * 32 < toks * G;
+                int cnt = single ? (len + 1 - x) / 2 : len;            // key tiles
+                if (!single && x == 0)
+                    cnt = max(0, min(dp->kb, (pos0 + tpt + kTile - 1) / kTile) - dp->ka);
+                if (lent && cnt > 0) {  // A has taken what B left in place of its maxima
+                    if (!bad && !ca_wait(taken, halves++ & 1))
+                        bad = true;
+                    bad = __any_sync(0xffffffffu, bad);
+                    lent = false;
                 }
-                fence_after();
-                if (live) {
-                    uint32_t sr[HK];
-#pragma unroll
-                    for (int o = 0; o < HK; o += 16)
-                        ld16(tH + o, sr, o);
-                    ld_wait(sr);
-                    float *s = reinterpret_cast<float *>(sr);
-                    if (__any_sync(0xffffffffu, m_lim < HK)) {
-#pragma unroll
-                        for (int c = 0; c < HK; ++c)
-                            s[c] = c < m_lim ? s[c] : -INFINITY;
+                // keys the thread's half of the next tile still holds for the row: fewer
+                // than all for any row of the warp, and the tile is masked
+                int m_lim = lim - (dp->ka + (single ? x : 0)) * kTile - hf * HK;
+                const int m_step = single ? 2 * kTile : kTile;
+                float mref = -INFINITY, negm = 0.f;
+                float l0 = 0.f, l1 = 0.f;
+                for (int t = cnt; t > 0; --t, m_lim -= m_step) {
+                    if (!bad && !ca_wait(&sfull[x], ns & 1))
+                        bad = true;
+                    ++ns;
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (bad) {
+                        if (live)
+                            bar_sync(pair_bar, 64);
+                        continue;
                     }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
+                    fence_after();
+                    if (live) {
+                        uint32_t sr[HK];
 #pragma unroll
-                    for (int c = 4; c < HK; c += 8) {
+                        for (int o = 0; o < HK; o += 16)
+                            ld16(tH + o, sr, o);
+                        ld_wait(sr);
+                        float *s = reinterpret_cast<float *>(sr);
+                        if (__any_sync(0xffffffffu, m_lim < HK)) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = c + 4 + e < HK ? fmaxf(fmaxf(mx[e], s[c + e]), s[c + 4 + e])
-                                                   : fmaxf(mx[e], s[c + e]);
-                    }
-                    float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    st_shared_f32(max_at, m_new);
-                    bar_sync(pair_bar, 64);  // also: both halves of S are in registers
-                    m_new = fmaxf(m_new, ld_shared_f32(max_at ^ kOther));
-                    const bool up = (m_new - mref) * ls > kRescale;  // or the first: infinite
-                    float f = 1.f;
-                    bool rescale = false;
-                    if (up) {
-                        const float old = negm;
-                        const bool fresh = mref == -INFINITY;  // (O holds nothing yet)
-                        rescale = !fresh;
-                        mref = m_new;
-                        negm = -m_new * ls;
-                        f = fresh ? 0.f : ex2_approx(negm - old);
-                        l0 *= f;
-                        l1 *= f;
-                    }
-#pragma unroll
-                    for (int c = 0; c < HK; c += PC) {
-                        uint32_t pk[PC / 2];
-#pragma unroll
-                        for (int e = 0; e < PC; e += 2) {
-                            fma2(s[c + e], s[c + e + 1], ls, negm);
-                            s[c + e] = ex2_approx(s[c + e]);
-                            s[c + e + 1] = ex2_approx(s[c + e + 1]);
-                            add2(l0, l1, s[c + e], s[c + e + 1]);
-                            pk[e / 2] = pack_bf16x2(s[c + e], s[c + e + 1]);
+                            for (int c = 0; c < HK; ++c)
+                                s[c] = c < m_lim ? s[c] : -INFINITY;
                         }
-                        if constexpr (PC == 32)
-                            st16(tP + c / 2, pk, 0);
-                        else
-                            st8(tP + c / 2, pk);
-                    }
-                    // O by the factor, this half of the row in flight at once
-                    if (__any_sync(0xffffffffu, rescale)) {
-                        uint32_t ov[HD];
+                        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                        for (int o = 0; o < HD; o += 16)
-                            ld16(tO + o, ov, o);
-                        ld_wait(ov);
+                        for (int c = 4; c < HK; c += 8) {
 #pragma unroll
-                        for (int o = 0; o < HD; o += 16) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                ov[o + e] = __float_as_uint(__uint_as_float(ov[o + e]) * f);
-                            st16(tO + o, ov, o);
+                            for (int e = 0; e < 4; ++e)
+                                mx[e] = c + 4 + e < HK ? fmaxf(fmaxf(mx[e], s[c + e]), s[c + 4 + e])
+                                                       : fmaxf(mx[e], s[c + e]);
                         }
+                        float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        st_shared_f32(max_at, m_new);
+                        bar_sync(pair_bar, 64);  // also: both halves of S are in registers
+                        m_new = fmaxf(m_new, ld_shared_f32(max_at ^ kOther));
+                        const bool up = (m_new - mref) * ls > kRescale;  // or the first: infinite
+                        float f = 1.f;
+                        bool rescale = false;
+                        if (up) {
+                            const float old = negm;
+                            const bool fresh = mref == -INFINITY;  // (O holds nothing yet)
+                            rescale = !fresh;
+                            mref = m_new;
+                            negm = -m_new * ls;
+                            f = fresh ? 0.f : ex2_approx(negm - old);
+                            l0 *= f;
+                            l1 *= f;
+                        }
+#pragma unroll
+                        for (int c = 0; c < HK; c += PC) {
+                            uint32_t pk[PC / 2];
+#pragma unroll
+                            for (int e = 0; e < PC; e += 2) {
+                                fma2(s[c + e], s[c + e + 1], ls, negm);
+                                s[c + e] = ex2_approx(s[c + e]);
+                                s[c + e + 1] = ex2_approx(s[c + e + 1]);
+                                add2(l0, l1, s[c + e], s[c + e + 1]);
+                                pk[e / 2] = pack_bf16x2(s[c + e], s[c + e + 1]);
+                            }
+                            if constexpr (PC == 32)
+                                st16(tP + c / 2, pk, 0);
+                            else
+                                st8(tP + c / 2, pk);
+                        }
+                        // O by the factor, this half of the row in flight at once
+                        if (__any_sync(0xffffffffu, rescale)) {
+                            uint32_t ov[HD];
+#pragma unroll
+                            for (int o = 0; o < HD; o += 16)
+                                ld16(tO + o, ov, o);
+                            ld_wait(ov);
+#pragma unroll
+                            for (int o = 0; o < HD; o += 16) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    ov[o + e] = __float_as_uint(__uint_as_float(ov[o + e]) * f);
+                                st16(tO + o, ov, o);
+                            }
+                        }
+                        st_wait();
                     }
-                    st_wait();
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&pready[x]);
-            }
-            // ----------------------------------------------------- epilogue
-            const CaDesc &d = *dp;
-            int G = a.Hq / a.Hkv;  // (what follows from it stays out of the key loop's registers)
-            asm volatile("" : "+r"(G));
-            float l = l0 + l1;
-            float m = mref == -INFINITY ? -INFINITY : -negm;  // base 2, scaled
-            if (cnt > 0) {
-                if (!bad && !ca_wait(&ofull[x], no & 1))
-                    bad = true;
-                ++no;
-                fence_after();
-                bad = __any_sync(0xffffffffu, bad);
-                st_shared_f32(max_at, l);  // for the other half
-                bar_sync(pair_bar, 64);
-                const float other = ld_shared_f32(max_at ^ kOther);
-                l = hf == 0 ? l + other : other + l;
-                bar_sync(pair_bar, 64);  // read before the next maximum is written
-            }
-            const bool whole = d.ka == 0 && d.kb == d.kt;
-            const bool join = single && len > 1;  // B holds the odd key tiles
-            if (single && x == 1) {
-                if (join) {  // A reads both halves of O: the lanes are the same
-                    st_shared_f32(max_at, hf == 0 ? m : l);
-                    lent = true;
                     fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(half);
+                        mbar_arrive(&pready[x]);
                 }
-                leave();
-                continue;
-            }
-            float fa = 1.f, fb = 0.f;
-            if (join) {
-                if (!bad && !ca_wait(half, halves & 1))
-                    bad = true;
-                ++halves;
-                bad = __any_sync(0xffffffffu, bad);
-                fence_after();
-                const float mb = sMax[2 * kTile + r], lb = sMax[3 * kTile + r];
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(taken);
-                const float mm = fmaxf(m, mb);
-                fa = m == -INFINITY ? 0.f : ex2_approx(m - mm);
-                fb = mb == -INFINITY ? 0.f : ex2_approx(mb - mm);
-                m = mm;
-                l = l * fa + lb * fb;
-            }
-            const bool read_o = cnt > 0 && live && !bad;
-            // XC columns of O, the halves joined
-            auto load_o = [&](int c, uint32_t (&v)[XC]) {
-                if (read_o) {
-                    ld16(tO + c, v, 0);
-                    if (join) {
-                        uint32_t w[XC];
-                        ld16(tO + kTile + c, w, 0);
-                        ld_wait(v);
-                        ld_wait(w);
+                // ----------------------------------------------------- epilogue
+                const CaDesc &d = *dp;
+                // (what follows from G stays out of the key loop's registers)
+                int G = a.Hq / a.Hkv;
+                asm volatile("" : "+r"(G));
+                float l = l0 + l1;
+                float m = mref == -INFINITY ? -INFINITY : -negm;  // base 2, scaled
+                if (cnt > 0) {
+                    if (!bad && !ca_wait(&ofull[x], no & 1))
+                        bad = true;
+                    ++no;
+                    fence_after();
+                    bad = __any_sync(0xffffffffu, bad);
+                    st_shared_f32(max_at, l);  // for the other half
+                    bar_sync(pair_bar, 64);
+                    const float other = ld_shared_f32(max_at ^ kOther);
+                    l = hf == 0 ? l + other : other + l;
+                    bar_sync(pair_bar, 64);  // read before the next maximum is written
+                }
+                const bool whole = d.ka == 0 && d.kb == d.kt;
+                // a partial result that the first walk has left already
+                const bool skip = d.clean && !whole && !(sLast[4 + x] >> (d.ka == 0) & 1);
+                const bool join = single && len > 1;  // B holds the odd key tiles
+                if (single && x == 1) {
+                    if (join) {  // A reads both halves of O: the lanes are the same
+                        st_shared_f32(max_at, hf == 0 ? m : l);
+                        lent = true;
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(half);
+                    }
+                    leave();
+                    continue;
+                }
+                float fa = 1.f, fb = 0.f;
+                if (join) {
+                    if (!bad && !ca_wait(half, halves & 1))
+                        bad = true;
+                    ++halves;
+                    bad = __any_sync(0xffffffffu, bad);
+                    fence_after();
+                    const float mb = sMax[2 * kTile + r], lb = sMax[3 * kTile + r];
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(taken);
+                    const float mm = fmaxf(m, mb);
+                    fa = m == -INFINITY ? 0.f : ex2_approx(m - mm);
+                    fb = mb == -INFINITY ? 0.f : ex2_approx(mb - mm);
+                    m = mm;
+                    l = l * fa + lb * fb;
+                }
+                const bool read_o = cnt > 0 && live && !bad;
+                // XC columns of O, the halves joined
+                auto load_o = [&](int c, uint32_t (&v)[XC]) {
+                    if (read_o) {
+                        ld16(tO + c, v, 0);
+                        if (join) {
+                            uint32_t w[XC];
+                            ld16(tO + kTile + c, w, 0);
+                            ld_wait(v);
+                            ld_wait(w);
+#pragma unroll
+                            for (int e = 0; e < XC; ++e)
+                                v[e] = __float_as_uint(__uint_as_float(v[e]) * fa +
+                                                       __uint_as_float(w[e]) * fb);
+                        } else {
+                            ld_wait(v);
+                        }
+                    } else {
 #pragma unroll
                         for (int e = 0; e < XC; ++e)
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * fa +
-                                                   __uint_as_float(w[e]) * fb);
-                    } else {
-                        ld_wait(v);
+                            v[e] = 0u;
                     }
-                } else {
+                };
+                auto o_done = [&] {  // this warp no longer reads O
+                    if (cnt > 0) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&oempty[x]);
+                            if (join)
+                                mbar_arrive(&oempty[1]);
+                        }
+                    }
+                };
+                int bs = 0;
+                unsigned parts = 1;
+                float *slot = nullptr;
+                if (!whole) {
+                    // the shares the item is cut over: lane k looks at share bs + k
+                    bs = static_cast<int>(quotient(d.x, plan.share));
+                    const int b = bs + lane;
+                    bool some = false;
+                    if (b < plan.ctas) {
+                        const long long lo = share_border(plan, b), hi = share_border(plan, b + 1);
+                        if (lo < d.x + d.w) {
+                            const int k0 = lo > d.x ? cut_tile(lo - d.x, d.kt, single) : 0;
+                            const int k1 =
+                                hi < d.x + d.w ? cut_tile(hi - d.x, d.kt, single) : d.kt;
+                            some = k0 < k1;
+                        }
+                    }
+                    parts = __ballot_sync(0xffffffffu, some);
+                    slot = slot_ptr<D>(a.part, 2 * blockIdx.x + (d.ka == 0));
+                }
+                const bool mine = r < toks * G;
+                const int row = x * kTile + r;  // within a slot
+                __nv_bfloat16 *dst =
+                    a.out +
+                    (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + d.h * G + r % G) * D +
+                    hf * HD;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float odd = 0.f;  // becomes NaN with any element of O
+#pragma unroll 1
+                for (int c = 0; c < HD; c += XC) {
+                    uint32_t v[XC];
+                    load_o(c, v);
+                    if (c + XC >= HD)
+                        o_done();
 #pragma unroll
                     for (int e = 0; e < XC; ++e)
-                        v[e] = 0u;
-                }
-            };
-            auto o_done = [&] {  // this warp no longer reads O
-                if (cnt > 0) {
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&oempty[x]);
-                        if (join)
-                            mbar_arrive(&oempty[1]);
-                    }
-                }
-            };
-            int bs = 0;
-            unsigned parts = 1;
-            float *slot = nullptr;
-            if (!whole) {
-                // the shares the item is cut over: lane k looks at share bs + k
-                bs = static_cast<int>(quotient(d.x, plan.share));
-                const int b = bs + lane;
-                bool some = false;
-                if (b < plan.ctas) {
-                    const long long lo = share_border(plan, b), hi = share_border(plan, b + 1);
-                    if (lo < d.x + d.w) {
-                        const int k0 = lo > d.x ? cut_tile(lo - d.x, d.kt, single) : 0;
-                        const int k1 =
-                            hi < d.x + d.w ? cut_tile(hi - d.x, d.kt, single) : d.kt;
-                        some = k0 < k1;
-                    }
-                }
-                parts = __ballot_sync(0xffffffffu, some);
-                slot = slot_ptr<D>(a.part, 2 * blockIdx.x + (d.ka == 0));
-            }
-            const bool mine = r < toks * G;
-            const int row = x * kTile + r;  // within a slot
-            __nv_bfloat16 *dst =
-                a.out +
-                (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + d.h * G + r % G) * D +
-                hf * HD;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            float odd = 0.f;  // becomes NaN with any element of O
-#pragma unroll 1
-            for (int c = 0; c < HD; c += XC) {
-                uint32_t v[XC];
-                load_o(c, v);
-                if (c + XC >= HD)
-                    o_done();
-#pragma unroll
-                for (int e = 0; e < XC; ++e)
-                    odd += __uint_as_float(v[e]) * 0.f;
-                if (mine && !bad) {
-                    if (whole) {
-                        uint32_t o[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            o[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * inv,
-                                               __uint_as_float(v[2 * k + 1]) * inv);
-                        st_global_v8(dst + c, o);
-                    } else {
-                        float *to = slot + static_cast<size_t>(row) * D + hf * HD + c;
-#pragma unroll
-                        for (int e = 0; e < XC; e += 8) {
+                        odd += __uint_as_float(v[e]) * 0.f;
+                    if (mine && !bad && !skip) {
+                        if (whole) {
                             uint32_t o[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                o[k] = v[e + k];
-                            st_global_v8(to + e, o);
+                                o[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * inv,
+                                                   __uint_as_float(v[2 * k + 1]) * inv);
+                            st_global_v8(dst + c, o);
+                        } else {
+                            float *to = slot + static_cast<size_t>(row) * D + hf * HD + c;
+#pragma unroll
+                            for (int e = 0; e < XC; e += 8) {
+                                uint32_t o[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    o[k] = v[e + k];
+                                st_global_v8(to + e, o);
+                            }
                         }
                     }
                 }
-            }
-            // Not finite, and values hidden from the row lay in its tiles: the row's
-            // half once more, a row a warp, from the keys that it sees
-            unsigned again = __ballot_sync(
-                0xffffffffu, mine && !bad && odd != odd && lim < min(d.len, d.kb * kTile));
-            __syncwarp();
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                const int lim_r = __shfl_sync(0xffffffffu, lim, src);
-                const float m_r = __shfl_sync(0xffffffffu, m, src);
-                const float inv_r = __shfl_sync(0xffffffffu, inv, src);
-                const int rr = wq * 32 + src;
-                constexpr int QE = D / 32, OE = HD / 32;  // elements a lane of q and of O
-                const size_t tk = static_cast<size_t>(d.row0 + tile_tok + rr / G);
-                const int hq = d.h * G + rr % G;
-                float q[QE], o[OE];
-#pragma unroll
-                for (int e = 0; e < QE; ++e)
-                    q[e] = __bfloat162float(a.q[tk * a.q_stride + hq * D + e * 32 + lane]);
-#pragma unroll
-                for (int e = 0; e < OE; ++e)
-                    o[e] = 0.f;
-                for (int key = d.ka * kTile; key < min(lim_r, d.kb * kTile); ++key) {
-                    int blk = a.tables[static_cast<size_t>(d.row) * a.stride + key / kBlk];
-                    blk = blk < 0 || blk >= a.num_blocks ? 0 : blk;
-                    const size_t at =
-                        ((static_cast<size_t>(blk) * a.Hkv + d.h) * kBlk + key % kBlk) * D;
-                    float s = 0.f;
-#pragma unroll
-                    for (int e = 0; e < QE; ++e)
-                        s = fmaf(q[e], __bfloat162float(a.kpool[at + e * 32 + lane]), s);
-#pragma unroll
-                    for (int w = 16; w; w >>= 1)
-                        s += __shfl_xor_sync(0xffffffffu, s, w);
-                    const float p =
-                        ex2_approx(fmaf(a.logit_scale < 0.f ? -s : s, ls, -m_r));
+                // Not finite, and keys of the share hidden from the row: once more
+                bool spoiled = false;
+                if (!d.clean) {
+                    spoiled = __any_sync(0xffffffffu, mine && !bad && odd != odd &&
+                                                          lim < min(d.len, d.kb * kTile));
+                    if (spoiled && lane == 0)
+                        atomicOr(&sLast[3], 1);
+                } else if (!skip) {
+                    // the values that counted as 0 though the row sees them: which of the half
+                    // row's dims hold one above 0 (or NaN), and which one below (or NaN)
+                    constexpr int OE = HD / 32;  // dims a lane
+                    uint32_t pos[OE], neg[OE];
 #pragma unroll
                     for (int e = 0; e < OE; ++e)
-                        o[e] =
-                            fmaf(p, __bfloat162float(a.vpool[at + hf * HD + e * 32 + lane]), o[e]);
-                    bool over = true;  // nothing changes a NaN any more
+                        pos[e] = neg[e] = 0u;
+                    const int from = max(d.pos0 + 1, d.ka * kTile);
+                    const int to = min(d.pos0 + d.ntok, d.kb * kTile);
+                    for (int b = from / kBlk; b * kBlk < to; ++b) {
+                        const int blk = a.tables[static_cast<size_t>(d.row) * a.stride + b];
+                        if (blk < 0 || blk >= a.num_blocks)
+                            continue;
+                        const __nv_bfloat16 *v =
+                            a.vpool + (static_cast<size_t>(blk) * a.Hkv + d.h) * kBlk * D + hf * HD;
+#pragma unroll 4
+                        for (int j = 0; j < kBlk; ++j) {
+                            const int key = b * kBlk + j;
+                            if (key < from || key >= to)
+                                continue;
 #pragma unroll
-                    for (int e = 0; e < OE; ++e)
-                        over = over && o[e] != o[e];
-                    if (__all_sync(0xffffffffu, over))
-                        break;
-                }
-#pragma unroll
-                for (int e = 0; e < OE; ++e) {
-                    const int c = hf * HD + e * 32 + lane;
-                    if (whole)
-                        a.out[(tk * a.Hq + hq) * D + c] = __float2bfloat16_rn(o[e] * inv_r);
-                    else
-                        slot[static_cast<size_t>(x * kTile + rr) * D + c] = o[e];
-                }
-            }
-            if (whole) {
-                leave();
-                continue;
-            }
-            // a partial result: the last of the item's shares to arrive joins them
-            if (mine && hf == 0)
-                reinterpret_cast<float2 *>(slot + 2 * kTile * D)[row] = make_float2(m, l);
-            __threadfence();
-            bar_sync(9 + x, 32 * kSmWarps);
-            if (r == 0 && hf == 0) {
-                const unsigned n = __popc(parts);
-                sLast[x] = atomicAdd(&a.arrived[sLast[2] + 2 * bs + x], 1) == n - 1;
-            }
-            bar_sync(9 + x, 32 * kSmWarps);
-            if (sLast[x]) {
-                __threadfence();
-                if constexpr (D == 64) {
-                    // A warp joins every eighth row, lane k weighs the k-th of them; then RW
-                    // rows at once, RB times, two shares in flight: 9 -> 4 us a pair's join.
-                    // With 128 dims the key loop loses registers to it (16 prompts 657 -> 697
-                    // us).
-                    constexpr int RW = 128 / D, RB = 4, ROWS = kTile / kSmWarps;
-                    const int first = __ffs(parts) - 1, rows = toks * G;
-                    const int w0 = hf * 4 + wq;
-                    const int row = min(w0 + (lane % ROWS) * kSmWarps, rows - 1);  // this lane's
-                    auto part_at = [&](int k) {
-                        return slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
-                               static_cast<size_t>(x * kTile) * D;
-                    };
-                    auto ml_at = [&](int k) {
-                        const float *p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
-                        return __ldcg(reinterpret_cast<const float2 *>(p + 2 * kTile * D) +
-                                      x * kTile + row);
-                    };
-                    float M = -INFINITY, L = 0.f;
-                    for (unsigned q = parts; q; q &= q - 1) {
-                        const float2 ml = ml_at(__ffs(q) - 1);
-                        const float up = fmaxf(M, ml.x);
-                        if (up > -INFINITY)
-                            L = L * ex2_approx(M - up) + ml.y * ex2_approx(ml.x - up);
-                        M = up;
-                    }
-                    const float iv = L == 0.f ? 0.f : 1.f / L;
-                    auto weight = [&](float m) {
-                        return m == -INFINITY ? 0.f : ex2_approx(m - M) * iv;
-                    };
-                    const size_t to =
-                        (static_cast<size_t>(d.row0 + tile_tok + row / G) * a.Hq + d.h * G +
-                         row % G) * D;
-                    const int col = lane % (D / 4) * 4, sub = lane / (D / 4);
-#pragma unroll 1
-                    for (int u0 = 0; u0 < ROWS; u0 += RB * RW) {
-                        if (w0 + u0 * kSmWarps >= rows)
-                            break;
-                        float4 o[RB];
-#pragma unroll
-                        for (int u = 0; u < RB; ++u)
-                            o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (unsigned q = parts; q;) {
-                            const int k0 = __ffs(q) - 1;
-                            q &= q - 1;
-                            const int k1 = q ? __ffs(q) - 1 : k0;
-                            const bool two = q != 0;
-                            q &= q - 1;
-                            const float *p0 = part_at(k0) + col, *p1 = part_at(k1) + col;
-                            float4 v0[RB], v1[RB];
-#pragma unroll
-                            for (int u = 0; u < RB; ++u) {
-                                const int at = (w0 + (u0 + u * RW + sub) * kSmWarps) * D;
-                                v0[u] = __ldcg(reinterpret_cast<const float4 *>(p0 + at));
-                                v1[u] = __ldcg(reinterpret_cast<const float4 *>(p1 + at));
+                            for (int e = 0; e < OE; ++e) {
+                                const float y = __bfloat162float(v[j * D + e * 32 + lane]);
+                                const uint32_t up = __ballot_sync(0xffffffffu, !(y < INFINITY));
+                                const uint32_t down = __ballot_sync(0xffffffffu, !(y > -INFINITY));
+                                pos[e] |= key < lim ? up : 0u;
+                                neg[e] |= key < lim ? down : 0u;
                             }
-                            const float f0 = weight(ml_at(k0).x);
-                            const float f1 = two ? weight(ml_at(k1).x) : 0.f;
+                        }
+                    }
+                    if (mine && !bad) {
 #pragma unroll
-                            for (int u = 0; u < RB; ++u) {
-                                const float g0 = __shfl_sync(0xffffffffu, f0, u0 + u * RW + sub);
-                                const float g1 = __shfl_sync(0xffffffffu, f1, u0 + u * RW + sub);
-                                o[u].x += v0[u].x * g0;
-                                o[u].y += v0[u].y * g0;
-                                o[u].z += v0[u].z * g0;
-                                o[u].w += v0[u].w * g0;
-                                if (two) {  // of the only one, it would be added twice
-                                    o[u].x += v1[u].x * g1;
-                                    o[u].y += v1[u].y * g1;
-                                    o[u].z += v1[u].z * g1;
-                                    o[u].w += v1[u].w * g1;
+                        for (int e = 0; e < OE; ++e)
+                            for (uint32_t q = pos[e] | neg[e]; q; q &= q - 1) {
+                                const int c = e * 32 + __ffs(q) - 1;
+                                const float y = !(neg[e] & q & -q)   ? INFINITY
+                                                : !(pos[e] & q & -q) ? -INFINITY
+                                                                     : INFINITY - INFINITY;
+                                if (whole) {
+                                    dst[c] = __float2bfloat16_rn(__bfloat162float(dst[c]) + y);
+                                } else {
+                                    float *to = slot + static_cast<size_t>(row) * D + hf * HD + c;
+                                    *to += y;
                                 }
                             }
-                        }
-#pragma unroll
-                        for (int u = 0; u < RB; ++u) {
-                            const int k = u0 + u * RW + sub;
-                            const unsigned long long t = __shfl_sync(0xffffffffu, to, k);
-                            if (w0 + k * kSmWarps < rows)
-                                *reinterpret_cast<uint2 *>(a.out + t + col) =
-                                    make_uint2(pack_bf16x2(o[u].x, o[u].y),
-                                               pack_bf16x2(o[u].z, o[u].w));
-                        }
                     }
-                } else {
-                    // RB rows a warp at a time: lane k weighs share bs + k, then every lane
-                    // adds up EL columns over the shares, two of them in flight
-                    constexpr int EL = 4, RB = 4;
-                    const int first = __ffs(parts) - 1;
-                    const bool in = parts >> lane & 1;
-                    const float2 *ml_p =
-                        reinterpret_cast<const float2 *>(
-                            slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
-                            2 * kTile * D) + x * kTile;
-                    const int r_begin = (hf * 4 + wq) * RB;
-                    float2 ml[RB];
-                    auto load_ml = [&](int r0) {
-#pragma unroll
-                        for (int u = 0; u < RB; ++u)
-                            ml[u] = in ? __ldcg(ml_p + r0 + u) : make_float2(-INFINITY, 0.f);
-                    };
-                    if (r_begin < toks * G)
-                        load_ml(r_begin);
-                    for (int r0 = r_begin; r0 < toks * G; r0 += kSmWarps * RB) {
-                        float f[RB], o[RB][EL];
-#pragma unroll
-                        for (int u = 0; u < RB; ++u) {
-                            float M = ml[u].x;
-#pragma unroll
-                            for (int w = 16; w; w >>= 1)
-                                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-                            f[u] = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - M);
-                            float L = ml[u].y * f[u];
-#pragma unroll
-                            for (int w = 16; w; w >>= 1)
-                                L += __shfl_xor_sync(0xffffffffu, L, w);
-                            f[u] *= L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                            for (int e = 0; e < EL; ++e)
-                                o[u][e] = 0.f;
+                }
+                if (whole || skip) {
+                    leave();
+                    continue;
+                }
+                // a partial result: the last of the item's shares to arrive joins them
+                if (mine && hf == 0)
+                    reinterpret_cast<float2 *>(slot + 2 * kTile * D)[row] = make_float2(m, l);
+                __threadfence();
+                if (bar_any(9 + x, 32 * kSmWarps, spoiled)) {  // not this one: the second walk's
+                    if (r == 0 && hf == 0)
+                        sLast[4 + x] |= 1 << (d.ka == 0);
+                    leave();
+                    continue;
+                }
+                if (r == 0 && hf == 0) {
+                    const unsigned n = __popc(parts);
+                    sLast[x] = atomicAdd(&a.arrived[sLast[2] + 2 * bs + x], 1) == n - 1;
+                }
+                bar_sync(9 + x, 32 * kSmWarps);
+                if (sLast[x]) {
+                    __threadfence();
+                    if constexpr (D == 64) {
+                        // A warp joins every eighth row, lane k weighs the k-th of them; then RW
+                        // rows at once, RB times, two shares in flight: 9 -> 4 us a pair's join.
+                        // With 128 dims the key loop loses registers to it (16 prompts 657 -> 697
+                        // us).
+                        constexpr int RW = 128 / D, RB = 4, ROWS = kTile / kSmWarps;
+                        const int first = __ffs(parts) - 1, rows = toks * G;
+                        const int w0 = hf * 4 + wq;
+                        // this lane's row
+                        const int row = min(w0 + (lane % ROWS) * kSmWarps, rows - 1);
+                        auto part_at = [&](int k) {
+                            return slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
+                                   static_cast<size_t>(x * kTile) * D;
+                        };
+                        auto ml_at = [&](int k) {
+                            const float *p = slot_ptr<D>(a.part, 2 * (bs + k) + (k == first));
+                            return __ldcg(reinterpret_cast<const float2 *>(p + 2 * kTile * D) +
+                                          x * kTile + row);
+                        };
+                        float M = -INFINITY, L = 0.f;
+                        for (unsigned q = parts; q; q &= q - 1) {
+                            const float2 ml = ml_at(__ffs(q) - 1);
+                            const float up = fmaxf(M, ml.x);
+                            if (up > -INFINITY)
+                                L = L * ex2_approx(M - up) + ml.y * ex2_approx(ml.x - up);
+                            M = up;
                         }
-                        if (r0 + kSmWarps * RB < toks * G)
-                            load_ml(r0 + kSmWarps * RB);
-                        for (unsigned q = parts; q;) {
-                            const int k0 = __ffs(q) - 1;
-                            q &= q - 1;
-                            const int k1 = q ? __ffs(q) - 1 : -1;
-                            q &= q - 1;
-                            float w[2][RB][EL];
+                        const float iv = L == 0.f ? 0.f : 1.f / L;
+                        auto weight = [&](float m) {
+                            return m == -INFINITY ? 0.f : ex2_approx(m - M) * iv;
+                        };
+                        const size_t to =
+                            (static_cast<size_t>(d.row0 + tile_tok + row / G) * a.Hq + d.h * G +
+                             row % G) * D;
+                        const int col = lane % (D / 4) * 4, sub = lane / (D / 4);
+#pragma unroll 1
+                        for (int u0 = 0; u0 < ROWS; u0 += RB * RW) {
+                            if (w0 + u0 * kSmWarps >= rows)
+                                break;
+                            float4 o[RB];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int k = h ? k1 : k0;
-                                const float *o_p =
-                                    slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
-                                    static_cast<size_t>(x * kTile + r0) * D + lane * EL;
+                            for (int u = 0; u < RB; ++u)
+                                o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (unsigned q = parts; q;) {
+                                const int k0 = __ffs(q) - 1;
+                                q &= q - 1;
+                                const int k1 = q ? __ffs(q) - 1 : k0;
+                                const bool two = q != 0;
+                                q &= q - 1;
+                                const float *p0 = part_at(k0) + col, *p1 = part_at(k1) + col;
+                                float4 v0[RB], v1[RB];
 #pragma unroll
                                 for (int u = 0; u < RB; ++u) {
+                                    const int at = (w0 + (u0 + u * RW + sub) * kSmWarps) * D;
+                                    v0[u] = __ldcg(reinterpret_cast<const float4 *>(p0 + at));
+                                    v1[u] = __ldcg(reinterpret_cast<const float4 *>(p1 + at));
+                                }
+                                const float f0 = weight(ml_at(k0).x);
+                                const float f1 = two ? weight(ml_at(k1).x) : 0.f;
 #pragma unroll
-                                    for (int e = 0; e < EL; ++e)
-                                        w[h][u][e] = 0.f;
+                                for (int u = 0; u < RB; ++u) {
+                                    const float g0 =
+                                        __shfl_sync(0xffffffffu, f0, u0 + u * RW + sub);
+                                    const float g1 =
+                                        __shfl_sync(0xffffffffu, f1, u0 + u * RW + sub);
+                                    o[u].x += v0[u].x * g0;
+                                    o[u].y += v0[u].y * g0;
+                                    o[u].z += v0[u].z * g0;
+                                    o[u].w += v0[u].w * g0;
+                                    if (two) {  // of the only one, it would be added twice
+                                        o[u].x += v1[u].x * g1;
+                                        o[u].y += v1[u].y * g1;
+                                        o[u].z += v1[u].z * g1;
+                                        o[u].w += v1[u].w * g1;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int u = 0; u < RB; ++u) {
+                                const int k = u0 + u * RW + sub;
+                                const unsigned long long t = __shfl_sync(0xffffffffu, to, k);
+                                if (w0 + k * kSmWarps < rows)
+                                    *reinterpret_cast<uint2 *>(a.out + t + col) =
+                                        make_uint2(pack_bf16x2(o[u].x, o[u].y),
+                                                   pack_bf16x2(o[u].z, o[u].w));
+                            }
+                        }
+                    } else {
+                        // RB rows a warp at a time: lane k weighs share bs + k, then every lane
+                        // adds up EL columns over the shares, two of them in flight
+                        constexpr int EL = 4, RB = 4;
+                        const int first = __ffs(parts) - 1;
+                        const bool in = parts >> lane & 1;
+                        const float2 *ml_p =
+                            reinterpret_cast<const float2 *>(
+                                slot_ptr<D>(a.part, 2 * (bs + lane) + (lane == first)) +
+                                2 * kTile * D) + x * kTile;
+                        const int r_begin = (hf * 4 + wq) * RB;
+                        float2 ml[RB];
+                        auto load_ml = [&](int r0) {
+#pragma unroll
+                            for (int u = 0; u < RB; ++u)
+                                ml[u] = in ? __ldcg(ml_p + r0 + u) : make_float2(-INFINITY, 0.f);
+                        };
+                        if (r_begin < toks * G)
+                            load_ml(r_begin);
+                        for (int r0 = r_begin; r0 < toks * G; r0 += kSmWarps * RB) {
+                            float f[RB], o[RB][EL];
+#pragma unroll
+                            for (int u = 0; u < RB; ++u) {
+                                float M = ml[u].x;
+#pragma unroll
+                                for (int w = 16; w; w >>= 1)
+                                    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+                                f[u] = ml[u].x == -INFINITY ? 0.f : ex2_approx(ml[u].x - M);
+                                float L = ml[u].y * f[u];
+#pragma unroll
+                                for (int w = 16; w; w >>= 1)
+                                    L += __shfl_xor_sync(0xffffffffu, L, w);
+                                f[u] *= L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                                for (int e = 0; e < EL; ++e)
+                                    o[u][e] = 0.f;
+                            }
+                            if (r0 + kSmWarps * RB < toks * G)
+                                load_ml(r0 + kSmWarps * RB);
+                            for (unsigned q = parts; q;) {
+                                const int k0 = __ffs(q) - 1;
+                                q &= q - 1;
+                                const int k1 = q ? __ffs(q) - 1 : -1;
+                                q &= q - 1;
+                                float w[2][RB][EL];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int k = h ? k1 : k0;
+                                    const float *o_p =
+                                        slot_ptr<D>(a.part, 2 * (bs + k) + (k == first)) +
+                                        static_cast<size_t>(x * kTile + r0) * D + lane * EL;
+#pragma unroll
+                                    for (int u = 0; u < RB; ++u) {
+#pragma unroll
+                                        for (int e = 0; e < EL; ++e)
+                                            w[h][u][e] = 0.f;
+                                        if (k < 0)
+                                            continue;
+                                        const float4 v =
+                                            __ldcg(reinterpret_cast<const float4 *>(o_p + u * D));
+                                        w[h][u][0] = v.x;
+                                        w[h][u][1] = v.y;
+                                        w[h][u][2] = v.z;
+                                        w[h][u][3] = v.w;
+                                    }
+                                }
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int k = h ? k1 : k0;
                                     if (k < 0)
                                         continue;
-                                    const float4 v =
-                                        __ldcg(reinterpret_cast<const float4 *>(o_p + u * D));
-                                    w[h][u][0] = v.x;
-                                    w[h][u][1] = v.y;
-                                    w[h][u][2] = v.z;
-                                    w[h][u][3] = v.w;
+#pragma unroll
+                                    for (int u = 0; u < RB; ++u) {
+                                        const float fk = __shfl_sync(0xffffffffu, f[u], k);
+#pragma unroll
+                                        for (int e = 0; e < EL; ++e)
+                                            o[u][e] += w[h][u][e] * fk;
+                                    }
                                 }
                             }
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int k = h ? k1 : k0;
-                                if (k < 0)
+                            for (int u = 0; u < RB; ++u) {
+                                const int rr = r0 + u;
+                                if (rr >= toks * G)
                                     continue;
+                                __nv_bfloat16 *d2 =
+                                    a.out +
+                                    (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq +
+                                     d.h * G + rr % G) * D + lane * EL;
 #pragma unroll
-                                for (int u = 0; u < RB; ++u) {
-                                    const float fk = __shfl_sync(0xffffffffu, f[u], k);
-#pragma unroll
-                                    for (int e = 0; e < EL; ++e)
-                                        o[u][e] += w[h][u][e] * fk;
-                                }
+                                for (int e = 0; e < EL; e += 2)
+                                    *reinterpret_cast<uint32_t *>(d2 + e) =
+                                        pack_bf16x2(o[u][e], o[u][e + 1]);
                             }
-                        }
-#pragma unroll
-                        for (int u = 0; u < RB; ++u) {
-                            const int rr = r0 + u;
-                            if (rr >= toks * G)
-                                continue;
-                            __nv_bfloat16 *d2 =
-                                a.out + (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq +
-                                         d.h * G + rr % G) * D + lane * EL;
-#pragma unroll
-                            for (int e = 0; e < EL; e += 2)
-                                *reinterpret_cast<uint32_t *>(d2 + e) =
-                                    pack_bf16x2(o[u][e], o[u][e + 1]);
                         }
                     }
                 }
+                leave();
             }
+            if (!walk_again(ended_clean()))
+                break;
             leave();
         }
     }
     if (bad)
         set_error(a.sticky, ZP_ERR_TIMEOUT);
-    fence_before();
-    __syncthreads();
-    if (wi == kMmaWarp) {
+    if (wi == kMmaWarp) {  // (the walk's end: no other warp uses tensor memory any more)
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(kTmemCols)

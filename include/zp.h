@@ -432,11 +432,11 @@ zp_status zp_append_kv_chunk(zp_cache *cache, int32_t layer, const void *k_new, 
  * chunk's own keys and values are read from the cache: zp_append_kv_chunk
  * comes before.  The many-query form of zp_paged_decode_attn, for any n_i from
  * one token to a whole prompt, mixed in one batch.  Keys and values a token
- * does not see never enter its output, whatever bits they hold (values that
- * are not finite cost time where they share a 128-key tile with its last
- * keys: its row is then computed twice); an output element whose token sees a
- * value element that is not finite is not finite.  The same call on the same
- * data gives the same bits.
+ * does not see never enter its output, whatever bits they hold; an output
+ * element whose token sees a value element that is not finite is not finite.
+ * An SM that comes to an output that is not finite may go through its part of
+ * the batch twice: such a call takes two to six times a clean one's time, at any
+ * length.  The same call on the same data gives the same bits.
  *
  *  q             device bf16 [total][Hq][d], 16-byte aligned, tokens q_stride
  *                elements apart
