@@ -41,6 +41,36 @@ struct Alloc {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// n bytes at p.
+struct Span {
+    const void *p;
+    unsigned long long n;
+};
+
+// Whether two spans share any byte; a null pointer shares none.
+bool overlap(const Span &x, const Span &y)
+{
+    const unsigned long long a = reinterpret_cast<uintptr_t>(x.p);
+    const unsigned long long b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p && y.p && a < b + y.n && b < a + x.n;
+}
+
+// Whether an output shares memory with an input or another output: CTAs read the
+// inputs, each for itself, while others write.
+template <size_t N, size_t M>
+bool shared_memory(const Span (&outs)[N], const Span (&ins)[M])
+{
+    for (size_t i = 0; i < N; ++i) {
+        for (size_t k = 0; k < i; ++k)
+            if (overlap(outs[i], outs[k]))
+                return true;
+        for (const Span &in : ins)
+            if (overlap(outs[i], in))
+                return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 namespace zp {
@@ -789,13 +819,6 @@ static zp_status chunk_checks(const zp_cache *c, int32_t layer, const int32_t *b
     return ZP_OK;
 }
 
-// Whether x bytes at p and y bytes at q share any; a null pointer shares none.
-static bool overlap(const void *p, unsigned long long x, const void *q, unsigned long long y)
-{
-    const unsigned long long a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return p && q && a < b + y && b < a + x;
-}
-
 // Bytes of `total` bf16 rows of `row` elements, `stride` elements apart.
 static unsigned long long row_bytes(int total, long long stride, long long row)
 {
@@ -823,10 +846,15 @@ zp_status zp_append_kv_chunk(zp_cache *c, int32_t layer, const void *k_new, int6
     if (R == 0 || total == 0)
         return ZP_OK;
     const unsigned long long pool = 2ull * c->num_blocks * c->b * row;
-    for (const void *p : {c->kpools[layer], c->vpools[layer]})
-        if (overlap(p, pool, k_new, row_bytes(total, k_stride, row)) ||
-            overlap(p, pool, v_new, row_bytes(total, v_stride, row)))
-            return ZP_ERR_INVALID_ARG;
+    const Span outs[] = {{c->kpools[layer], pool}, {c->vpools[layer], pool}};
+    const Span ins[] = {{k_new, row_bytes(total, k_stride, row)},
+                        {v_new, row_bytes(total, v_stride, row)},
+                        {starts, 4ull * R + 4},
+                        {block_tables, 4ull * num_rows * bt_stride},
+                        {lengths, 4ull * num_rows},
+                        {req_idx, 4ull * R}};
+    if (shared_memory(outs, ins))
+        return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
     zp::ChunkKvArgs a{};
@@ -870,7 +898,16 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
-    if (overlap(q, row_bytes(total, q_stride, row), out, row_bytes(total, row, row)))
+    const unsigned long long pool = 2ull * c->num_blocks * c->b * c->Hkv * c->d;
+    const Span outs[] = {{out, row_bytes(total, row, row)}};
+    const Span ins[] = {{q, row_bytes(total, q_stride, row)},
+                        {c->kpools[layer], pool},
+                        {c->vpools[layer], pool},
+                        {starts, 4ull * R + 4},
+                        {block_tables, 4ull * num_rows * bt_stride},
+                        {lengths, 4ull * num_rows},
+                        {req_idx, 4ull * R}};
+    if (shared_memory(outs, ins))
         return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
@@ -929,23 +966,20 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
-    // the CTAs of a request read the inputs each for itself: no output may change them
     const unsigned long long probs =
         esz * (static_cast<unsigned long long>(total - 1) * prob_stride + vocab);
     const unsigned long long per_row = 4ull * total, per_request = 4ull * R;
-    const struct { const void *p; unsigned long long n; }
-        outs[] = {{accepted, per_request}, {next_tokens, per_request}, {lengths, 4ull * num_rows}},
-        ins[] = {{tokens, per_row}, {accept_u, per_row}, {sample_u, per_request},
-                 {starts, per_request + 4}, {lengths ? req_idx : nullptr, per_request},
-                 {target_probs, probs}, {draft_probs, probs}};
-    for (int i = 0; i < 3; ++i) {
-        for (int k = 0; k < i; ++k)
-            if (overlap(outs[i].p, outs[i].n, outs[k].p, outs[k].n))
-                return ZP_ERR_INVALID_ARG;
-        for (const auto &in : ins)
-            if (overlap(outs[i].p, outs[i].n, in.p, in.n))
-                return ZP_ERR_INVALID_ARG;
-    }
+    const Span outs[] = {
+        {accepted, per_request}, {next_tokens, per_request}, {lengths, 4ull * num_rows}};
+    const Span ins[] = {{tokens, per_row},
+                        {accept_u, per_row},
+                        {sample_u, per_request},
+                        {starts, per_request + 4},
+                        {lengths ? req_idx : nullptr, per_request},
+                        {target_probs, probs},
+                        {draft_probs, probs}};
+    if (shared_memory(outs, ins))
+        return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
     zp::VerifyArgs a{};

@@ -28,3 +28,7 @@ def _run(exe, what):
 
 def test_a_status_clears_its_own_word_only(exe):
     _run(exe, "status")
+
+
+def test_shared_memory_is_refused(exe):
+    _run(exe, "shared")
