@@ -143,3 +143,26 @@ def test_cost(spans, Hkv, Hq, d, where):
     assert cache.status() == zp.OK
     print(f"clean {clean * 1e3:.0f} us, {where} {slow * 1e3:.0f} us")
     assert slow < 8 * clean + 0.05
+
+
+@pytest.mark.parametrize("spans,Hkv,Hq", [([(70, 600)], 1, 4), ([(64, 900)] * 100, 2, 8),
+                                          ([(3, 2000)] * 3, 2, 8), ([(5, 700)] * 300, 1, 7)])
+@pytest.mark.parametrize("power", [124, 110, 60, -60])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_and_small_values(spans, Hkv, Hq, power, d):
+    """Values near the largest bf16 number (124: up to about 2^126) and small
+    ones, under scores that climb by 12 powers of e along a row (less than what
+    makes the kernel change its reference): sums of weights above 1 overflow."""
+    b = Batch(spans, Hkv, Hq, d, seed=58, heavy=0.0)
+    b.q.copy_(torch.ones_like(b.q))
+    for i, (n, T) in enumerate(spans):
+        m = -(-T // B)
+        blocks = b.tables[i, :m].long()
+        t = torch.arange(m * B, device=DEV).view(m, 1, B, 1)
+        k = b.kp[0][blocks].float() * 0.05 + t * (12.0 / T / math.sqrt(d))
+        b.kp[0][blocks] = torch.where(t < T, k, math.nan).bfloat16()
+        b.vp[0][blocks] = (b.vp[0][blocks].float() * 2.0 ** power).bfloat16()
+    cache = b.cache()
+    b.attn(cache)
+    assert cache.status() == zp.OK
+    b.check_attn()
