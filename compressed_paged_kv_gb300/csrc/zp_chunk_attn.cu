@@ -1159,7 +1159,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         constexpr uint32_t kOther = kTile * 4;  // max_at ^ kOther: the other half's
         static_assert(S::off_max % (2 * kOther) == 0, "the halves differ in one bit");
         const uint32_t pair_bar = 1 + x * 4 + wq;  // the barrier of this warp and its other half
-        const float ls = fmaxf(fabsf(a.logit_scale), 1e-30f);
+        // (above 0, for scores of -infinity; 2^-149 times any finite one is nothing)
+        const float ls = fmaxf(fabsf(a.logit_scale), __uint_as_float(1u));
         uint32_t ns = 0, no = 0, halves = 0;
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
         for (;;) {

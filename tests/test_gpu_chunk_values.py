@@ -166,3 +166,19 @@ def test_large_and_small_values(spans, Hkv, Hq, power, d):
     b.attn(cache)
     assert cache.status() == zp.OK
     b.check_attn()
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-40, -1e-37, 2.0 ** -110])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales_near_zero_and_large_scores(scale, d):
+    """Scores of up to 1e35: a scale of zero makes every visible key weigh the
+    same, a tiny one counts as it is."""
+    spans = [(70, 600), (3, 400), (200, 200)]
+    b = Batch(spans, 2, 8, d, seed=59, heavy=0.0)
+    b.scale = scale
+    b.q.mul_(2.0 ** 55)
+    b.kp[0].mul_(2.0 ** 55)
+    cache = b.cache()
+    b.attn(cache)
+    assert cache.status() == zp.OK
+    b.check_attn()
