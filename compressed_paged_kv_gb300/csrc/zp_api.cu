@@ -957,7 +957,8 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
     if (R < 0 || R > c->max_requests || total < 0 || vocab < 1 || prob_stride < vocab ||
         (lengths && num_rows < 1))
         return ZP_ERR_INVALID_ARG;
-    if ((prob_dtype != ZP_DTYPE_F32 && prob_dtype != ZP_DTYPE_BF16) || vocab > (1 << 30))
+    if ((prob_dtype != ZP_DTYPE_F32 && prob_dtype != ZP_DTYPE_BF16) || vocab > (1 << 30) ||
+        total > (1 << 30))  // a chunk's tokens are counted 32 at a time in 32 bits
         return ZP_ERR_UNSUPPORTED;
     const size_t esz = prob_dtype == ZP_DTYPE_F32 ? 4 : 2;
     if (!aligned(target_probs, esz) || !aligned(draft_probs, esz) || !aligned(tokens, 4) ||

@@ -474,6 +474,7 @@ zp_status zp_paged_chunk_attn(zp_cache *cache, int32_t layer, const void *q, int
  * stay reserved for the row).  A request with an empty chunk is skipped: its
  * outputs and length are not written.
  *
+ *  total, vocab  at most 2^30 (ZP_ERR_UNSUPPORTED beyond)
  *  tokens        device int32 [total]; tokens[starts[i]] is not read
  *  target_probs  device [total][vocab] of prob_dtype, rows prob_stride
  *                elements apart (any, >= vocab)

@@ -213,6 +213,30 @@ static int shared()
     return 0;
 }
 
+// Packed rows and vocabularies of a verification up to 2^30.
+static int limits()
+{
+    const char *what = "limits";
+    zp_cache c;
+    c.max_requests = 4;
+    auto array = [](int i) { return reinterpret_cast<int32_t *>(uintptr_t(i) << 48); };
+    auto verify = [&](int32_t total, int32_t vocab) {
+        g_launches = 0;
+        return zp_verify_draft(&c, array(1), array(2), total, array(3), nullptr, ZP_DTYPE_F32,
+                               vocab, vocab, reinterpret_cast<float *>(array(4)),
+                               reinterpret_cast<float *>(array(5)), nullptr, 0, nullptr, 1,
+                               array(6), array(7), nullptr);
+    };
+    const int32_t most = 1 << 30;
+    CHECK(verify(most, 1) == ZP_OK && g_launches == 1);
+    CHECK(verify(4, most) == ZP_OK && g_launches == 1);
+    for (int32_t over : {most + 1, 0x7fffffff - 31, 0x7fffffff}) {
+        CHECK(verify(over, 1) == ZP_ERR_UNSUPPORTED && g_launches == 0);
+        CHECK(verify(4, over) == ZP_ERR_UNSUPPORTED && g_launches == 0);
+    }
+    return 0;
+}
+
 int main(int argc, char **argv)
 {
     const char *what = argc > 1 ? argv[1] : "";
@@ -221,6 +245,8 @@ int main(int argc, char **argv)
         bad = status();
     else if (!std::strcmp(what, "shared"))
         bad = shared();
+    else if (!std::strcmp(what, "limits"))
+        bad = limits();
     if (!bad)
         std::printf("ok\n");
     return bad;

@@ -32,3 +32,7 @@ def test_a_status_clears_its_own_word_only(exe):
 
 def test_shared_memory_is_refused(exe):
     _run(exe, "shared")
+
+
+def test_limits_of_a_verification(exe):
+    _run(exe, "limits")
