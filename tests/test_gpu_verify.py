@@ -274,3 +274,37 @@ def test_captured_call():
         graph.replay()
         assert cache.status() == zp.OK
         d.check()
+
+
+@pytest.mark.parametrize("draft", [True, False])
+def test_kept_tokens_have_the_targets_frequencies(draft):
+    """As above with borders that lie on the grid's lines, so the frequencies are
+    exact: p and q in 16ths.  u q < p and the draw from (3, 0, 0, 3) / 6 split 30
+    cells a side without a rest; without q, u < p splits 16, and the draws from
+    10, 15, 12 and 11 16ths (p without the drafted token) split 660."""
+    V = 5
+    p = torch.tensor([6, 1, 4, 5, 0], device=DEV) / 16
+    q = torch.tensor([3, 6, 5, 2, 0], device=DEV) / 16
+    n, m = (30, 30) if draft else (16, 660)
+    R = 4 * n * m
+    x = torch.arange(4, device=DEV).repeat_interleave(n * m)
+    starts = torch.arange(R + 1, device=DEV, dtype=torch.int32) * 2
+    tokens = torch.zeros(2 * R, dtype=torch.int32, device=DEV)
+    tokens[1::2] = x.int()
+    u = torch.zeros(2 * R, device=DEV)
+    u[0::2] = ((torch.arange(n, device=DEV) + 0.5) / n).repeat_interleave(m).repeat(4)
+    r = ((torch.arange(m, device=DEV) + 0.5) / m).repeat(4 * n)
+    acc, nxt = (torch.zeros(R, dtype=torch.int32, device=DEV) for _ in range(2))
+    cache = _cache(R)
+    cache.verify_draft(tokens, starts, p.expand(2 * R, V).contiguous(), u, r, acc, nxt,
+                       draft_probs=q.expand(2 * R, V).contiguous() if draft else None)
+    assert cache.status() == zp.OK
+    kept = torch.where(acc == 1, x.int(), nxt).long()
+    count = torch.zeros(4, V, dtype=torch.int64, device=DEV)
+    count.index_put_((x, kept), torch.ones_like(kept), accumulate=True)
+    if draft:  # weighted by q, the kept tokens are the target's
+        total = (count * (q[:4, None] * 16).long()).sum(0)
+        assert total.tolist() == (p * 16 * n * m).long().tolist()
+    else:  # whatever token was drafted
+        for row in count.tolist():
+            assert row == (p * n * m).long().tolist()
