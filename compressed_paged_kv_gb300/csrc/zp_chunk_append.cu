@@ -5,10 +5,10 @@
 // A pure copy (2 * Hkv * d * 2 bytes read and written a token), bound by HBM
 // for many tokens (35,000 of 8 x 128: 45 us = 6.3 TB/s, 0.93 of the copy peak)
 // and by the chain of dependent reads (chunk offsets, row and length -> block
-// id) for few (40 tokens: 8 us, the host's cost of a call).  One warp a token: it
-// finds the request by a 32-ary search of the chunk offsets (one round of loads
-// up to 32 requests, two up to 1,024), then moves the token's K and V rows 16
-// bytes a lane.
+// id) for few (40 tokens: 2.7 us on the device, calls in a captured graph; 8 us a
+// call with the host's side).  One warp a token: it finds the request by a 32-ary
+// search of the chunk offsets (one round of loads up to 32 requests, two up to
+// 1,024), then moves the token's K and V rows 16 bytes a lane.
 #include "zp_chunk.cuh"
 
 namespace zp {

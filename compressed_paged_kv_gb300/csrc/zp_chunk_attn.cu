@@ -59,15 +59,20 @@
 // set, which no CTA of this call touches, for the next call: whatever a call
 // that gave up a wait has left uncounted is gone, with no help from the host.
 //
-// Measured, 32 heads of 128 over 8 kv heads: 2,048 tokens over 32,049, 1.04
-// TFLOP in 0.64 ms = 1.63 PFLOP/s (0.73 ms in a row: the power limit), 0.84 of
-// the library products' rate; 16 prompts of 331 to 4,007 tokens in 0.63 ms = 1.2
-// PFLOP/s; 256 speculative chunks over 1,024 to 2,040 tokens, 1.64 GB in 0.28 ms
-// = 5.9 TB/s, 0.87 of the copy peak.  What bounds it: in the first two the chain
-// of a stream (product -> softmax -> product; tensor pipe 60 % busy, issue slots
-// 48 %) and 2.5 us between two items of a CTA, in the last one HBM, in batches of
-// a few chunks the chain of the start (offsets -> block ids -> first tiles) and of
-// the join.
+// P is bf16 because the product takes two operands of one type and V is bf16;
+// it makes the error of a result, relative to 64 bits, 0.0020 where the result's
+// own rounding to bf16 is 0.0015.
+//
+// Measured, calls in a row, 32 heads of 128 over 8 kv heads: 2,048 tokens over
+// 32,049, 1.04 TFLOP in 0.715 ms = 1.46 PFLOP/s, 0.84 of the library products'
+// sustained rate; 16 prompts of 331 to 4,007 tokens in 0.667 ms = 1.15 PFLOP/s; 256
+// speculative chunks over 1,024 to 2,040 tokens, 1.64 GB in 0.271 ms = 6.0 TB/s,
+// 0.89 of the copy peak.  What bounds it: in the first the power limit and, as in
+// the second, the chain of a stream (product -> softmax -> product; tensor pipe 60 %
+// busy, issue slots 48 %), in the second also 2.5 us between two items of a CTA; in
+// the last one HBM; in batches of a few chunks the chain of the start (8 chunks of
+// 5 tokens, from a cold cache, on the device: offsets -> plan 2.0 us -> block ids ->
+// first tile 7.3, in the slowest CTA 9.2) and of the join (the slowest 5 us).
 #include "zp_chunk.cuh"
 
 namespace zp {
@@ -83,7 +88,7 @@ static_assert(kSmRegs * 2 * kSmWarps + kOtherRegs * 4 <= 96 * (2 * kSmWarps + 4)
 // Costs, in keys of a pair (measured: 1.4 us for 128 of them, 0.6 for 128 of a
 // single item, whose streams take half the tiles each, and 2.7 to 2.9 us between
 // the last tile of an item and the first of the next).  With a single item's
-// keys at full cost 60 single tokens beside two prompt pieces take 85 us, not 75.
+// keys at full cost 60 single tokens beside two prompt pieces take 69 us, not 61.
 constexpr int kItemCost = 320;         // an item's fixed cost
 constexpr int kSingle = 8;             // 16ths of a pair's cost that a single item's key takes
 constexpr int kMinShare = 2 * kTile;   // least cost given to a CTA
@@ -1144,7 +1149,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         // first half of O's) and w + 4 (the others), which exchange its maximum.
         constexpr int HK = kTile / 2, HD = D / 2;
         // columns of P a store: the widest that the registers allow (16 prompts of 128
-        // dims 642 us with 16, 621 with 32; with 64 dims 32 spills three times as much)
+        // dims 679 us with 16, 667 with 32; with 64 dims 32 spill)
         constexpr int PC = D == 128 ? 32 : 16;
         const int x = wi / kSmWarps;           // tile A or B
         const int wq = wi & 3;                 // tensor-memory lanes 32 wq ..
@@ -1495,9 +1500,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     __threadfence();
                     if constexpr (D == 64) {
                         // A warp joins every eighth row, lane k weighs the k-th of them; then RW
-                        // rows at once, RB times, two shares in flight: 9 -> 4 us a pair's join.
-                        // With 128 dims the key loop loses registers to it (16 prompts 657 -> 697
-                        // us).
+                        // rows at once, RB times, two shares in flight (60 single tokens beside
+                        // two prompt pieces 61 us, 69 with the join below).  With 128 dims the
+                        // key loop loses registers to it (16 prompts 667 us with the join below,
+                        // 712 with this one; 256 speculative chunks 271, 284).
                         constexpr int RW = 128 / D, RB = 4, ROWS = kTile / kSmWarps;
                         const int first = __ffs(parts) - 1, rows = toks * G;
                         const int w0 = hf * 4 + wq;

@@ -26,10 +26,10 @@
 // level falls into finds the stretch of its run from the sums it left, reads
 // that a second time (out of L2) and finds the token.  Bound by the bytes of
 // the deciding rows for large batches (256 requests of 151,936 fp32 p and q: 218
-// MB in 48.5 us = 4.5 TB/s, 0.66 of the copy peak; the clusters of rejected
-// tokens read twice as much as the others), and by the chain of dependent reads
-// (offsets -> tokens -> their probabilities -> row -> sums -> stretch) for small
-// ones (one request of 32,000: 6.6 us).
+// MB in 48.7 us = 4.5 TB/s, 0.66 of the copy peak; of bf16 38.8 us; the clusters
+// of rejected tokens read twice as much as the others), and by the chain of
+// dependent reads (offsets -> tokens -> their probabilities -> row -> sums ->
+// stretch) for small ones (one request of 32,000: 6.7 us).
 #include "zp_chunk.cuh"
 
 namespace zp {
@@ -230,7 +230,7 @@ struct Row {
 
     // The same of the vectors v0 + lane, + 32, .. below v1, through this lane's ring
     // of 2 kVfBatch vectors, of p or of p and q: a copy is always under way, where a
-    // batch's loads wait for its additions (256 requests 51.7 -> 48.5 us).  `ends` and
+    // batch's loads wait for its additions (256 requests 51.3 -> 48.7 us).  `ends` and
     // `mark` are called after each kVfBatch vectors.  A lane reads what it copied
     // itself, so its own waits are enough.
     template <bool Q, class E, class M>
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) zp_verify_kernel(const VerifyAr
         } else if (row.q) {
             row.template stream<true>(&ring[wi][0][lane], v0, v1, lane, s2, c2, ends, mark);
         } else if (sizeof(T) == 4) {  // (not where a vector holds eight weights to add:
-            // 128 requests of 128,000 without q 18.9 us this way, 18.2 by batches)
+            // 128 requests of 128,000 without q 19.1 us this way, 18.3 by batches)
             row.template stream<false>(&ring[wi][0][lane], v0, v1, lane, s2, c2, ends, mark);
         } else {
             for (int v = v0, n = 0; v < v1; v += STEP, ++n) {
@@ -678,11 +678,12 @@ static cudaError_t launch_verify_t(const VerifyArgs &a, int ctas, cudaStream_t s
 cudaError_t launch_verify_draft(const VerifyArgs &a, bool bf16, int sms, cudaStream_t s)
 {
     // Small CTAs, as many as give every warp of theirs a batch, up to eight a
-    // request (256 requests of a vocabulary of 2,000: 7.4 us with one, 15.6 with
+    // request (256 requests of a vocabulary of 2,000: 7.7 us with one, 15.8 with
     // eight) and up to what the SMs hold at once, 1,024 threads each (256 of
-    // 151,936: 52 us with four, 54 with eight, 74 with two).  Up to two CTAs an SM
-    // and long rows: CTAs of twice the threads, for twice the loads in flight (32
-    // requests of 151,936: 14.0 us, not 15.7; but 48 of 50,257: 12.1, not 10.2).
+    // 151,936: 48.4 us with four, 52.8 with two, 46.5 with eight, 77 with one).  Up
+    // to two CTAs an SM and long rows: CTAs of twice the threads, for twice the loads
+    // in flight (32 requests of 151,936: 14.2 us, not 15.9; but 48 of 50,257: 12.3,
+    // not 10.5).
     constexpr int kSmall = 128, kLarge = 256;
     const long long R = a.R, vectors = (static_cast<long long>(a.vocab) * (bf16 ? 2 : 4) + 15) / 16;
     const int step = kSmall * kVfBatch;  // vectors of a batch of every warp of a small CTA

@@ -96,7 +96,9 @@ typedef struct {
     int32_t capacity;    /* length of free_ids, >= 1 */
 } zp_block_pool;
 
-/* Creates a handle over caller-owned pools and allocates its workspace.
+/* Creates a handle over caller-owned pools and allocates its workspace (most
+ * of it partial results of the chunk attention: 40 MB with 152 SMs and a head
+ * dim of 128, 20 MB with 64).
  * Returns ZP_ERR_INVALID_ARG / ZP_ERR_UNSUPPORTED for a bad descriptor
  * (checked before any CUDA call), ZP_ERR_CUDA if an allocation fails.
  * *out is set only on success; the current CUDA device is recorded. */
@@ -438,6 +440,9 @@ zp_status zp_append_kv_chunk(zp_cache *cache, int32_t layer, const void *k_new, 
  * zero.  An SM that comes to an output that is not finite may go through its
  * part of the batch twice: such a call takes two to six times a clean one's
  * time, at any length.  The same call on the same data gives the same bits.
+ * (A batch of nothing but single tokens is faster through
+ * zp_paged_decode_attn: by 10 % with 256 requests of 1 to 2 K tokens, by 40 %
+ * with one.)
  *
  *  q             device bf16 [total][Hq][d], 16-byte aligned, tokens q_stride
  *                elements apart

@@ -17,7 +17,8 @@
 int main()
 {
     constexpr int Hkv = 2, Hq = 8, D = 128, N = 5, T = 6000, NB = (T + 15) / 16;
-    const size_t pool = static_cast<size_t>(NB) * Hkv * 16 * D, rows = static_cast<size_t>(N) * Hq * D;
+    const size_t pool = static_cast<size_t>(NB) * Hkv * 16 * D;
+    const size_t rows = static_cast<size_t>(N) * Hq * D;
     auto values = [](size_t n, unsigned seed) {  // bf16 in about [-1, 1]
         std::vector<uint16_t> v(n);
         unsigned long long s = seed;
