@@ -437,12 +437,12 @@ zp_status zp_append_kv_chunk(zp_cache *cache, int32_t layer, const void *k_new, 
  * does not see never enter its output, whatever bits they hold; an output
  * element whose token sees a value element that is not finite is not finite.
  * No sum overflows with values up to 2^127; values below 2^-75 may count as
- * zero.  An SM that comes to an output that is not finite may go through its
- * part of the batch twice: such a call takes two to six times a clean one's
- * time, at any length.  The same call on the same data gives the same bits.
- * (A batch of nothing but single tokens is faster through
- * zp_paged_decode_attn: by 10 % with 256 requests of 1 to 2 K tokens, by 40 %
- * with one.)
+ * zero.  A token whose scores are all -infinity gets zeros.  An SM that comes
+ * to an output that is not finite may go through its part of the batch twice:
+ * such a call takes two to six times a clean one's time, at any length.  The
+ * same call on the same data gives the same bits.  (A batch of nothing but
+ * single tokens is faster through zp_paged_decode_attn: by 10 % with 256
+ * requests of 1 to 2 K tokens, by 40 % with one.)
  *
  *  q             device bf16 [total][Hq][d], 16-byte aligned, tokens q_stride
  *                elements apart

@@ -182,3 +182,38 @@ def test_scales_near_zero_and_large_scores(scale, d):
     b.attn(cache)
     assert cache.status() == zp.OK
     b.check_attn()
+
+
+@pytest.mark.parametrize("spans", [[(64, 900)] * 40, [(5, 4000), (9, 70), (200, 3000)]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity(spans, d):
+    """A request all of whose scores are -infinity gets zeros; in the others such
+    keys have no weight."""
+    b = Batch(spans, 2, 8, d, seed=60, heavy=0.0)
+    b.q.copy_(b.q.abs() + 0.1)
+    want = {}
+    for i, (n, T) in enumerate(spans):
+        a = int(b.starts_np[i])
+        blocks = b.tables[i].long()
+        k, v = b.rows_of(i)
+        gone = torch.arange(0 if i % 3 == 0 else T // 3, T - n if i % 3 else T, device=DEV)
+        b.kp[0][blocks[gone // B], :, gone % B] = -math.inf
+        if i % 3:  # the 64-bit form on finite keys: far below the others
+            k = k.clone()
+            k[gone] = -3e4
+            want[i] = attn_ref(b.q[a:a + n], k, v, b.scale)
+    cache = b.cache()
+    b.attn(cache)
+    assert cache.status() == zp.OK
+    for i, (n, T) in enumerate(spans):
+        got = b.out[int(b.starts_np[i]):int(b.starts_np[i + 1])].double()
+        if i % 3 == 0:
+            assert not bool(got.any()), i
+        else:  # keys that have no weight lend none to the bound's spread
+            k, v = b.rows_of(i)
+            seen = torch.isfinite(k).all(2).all(1).nonzero()[:, 0]
+            first = int((seen < T - n).sum())
+            _, tol = attn_ref(b.q[int(b.starts_np[i]):int(b.starts_np[i + 1])], k[seen], v[seen],
+                              b.scale)
+            assert first + n == seen.numel()
+            assert bool(((got - want[i][0]).abs() <= tol).all()), i
