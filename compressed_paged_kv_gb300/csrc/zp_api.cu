@@ -11,7 +11,9 @@
 
 #include "zp_aux.cuh"
 #include "zp_chunk.cuh"
+#include "zp_fp8.cuh"
 #include "zp_internal.cuh"
+#include "zp_sample.cuh"
 
 using zp::Workspace;
 
@@ -97,6 +99,8 @@ struct zp_cache {
     int max_requests = 0, max_blocks = 0;
     int num_sms = 0;
     std::vector<void *> kpools, vpools;  // host copies of the pool pointers
+    std::vector<float *> kscales, vscales;  // of an 8-bit cache, else empty
+    bool fp8 = false;                    // an 8-bit cache
     void *base = nullptr;
     Workspace ws{};
 };
@@ -117,9 +121,10 @@ const char *zp_status_string(zp_status s)
     }
 }
 
-zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
+// Scales null: a bf16 cache.
+static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float *const *v_scales,
+                        zp_cache **out)
 {
-    NvtxRange nvtx("zp_cache_create");
     if (!desc || !out)
         return ZP_ERR_INVALID_ARG;
     const zp_cache_desc &D = *desc;
@@ -140,6 +145,10 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     for (int l = 0; l < D.num_layers; ++l)
         if (!D.k_pools[l] || !D.v_pools[l] || !aligned(D.k_pools[l], 16) ||
             !aligned(D.v_pools[l], 16))
+            return ZP_ERR_INVALID_ARG;
+    const bool fp8 = k_scales != nullptr;
+    for (int l = 0; fp8 && l < D.num_layers; ++l)
+        if (!k_scales[l] || !v_scales[l] || !aligned(k_scales[l], 4) || !aligned(v_scales[l], 4))
             return ZP_ERR_INVALID_ARG;
 
     zp_cache *c = new (std::nothrow) zp_cache();
@@ -174,6 +183,8 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     const size_t o_vrmaps = A.take(sizeof(CUtensorMap) * D.num_layers, 128);
     const size_t o_kp = A.take(sizeof(void *) * D.num_layers);
     const size_t o_vp = A.take(sizeof(void *) * D.num_layers);
+    const size_t o_ks = A.take(fp8 ? sizeof(float *) * D.num_layers : 0);
+    const size_t o_vs = A.take(fp8 ? sizeof(float *) * D.num_layers : 0);
     const size_t o_dst = A.take(4 * entries);
     const size_t o_push = A.take(4 * entries);
     const size_t o_cnt = A.take(16);
@@ -209,6 +220,8 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     ws.vrmaps = reinterpret_cast<CUtensorMap *>(b + o_vrmaps);
     ws.kpools = reinterpret_cast<void **>(b + o_kp);
     ws.vpools = reinterpret_cast<void **>(b + o_vp);
+    ws.kscales = fp8 ? reinterpret_cast<float **>(b + o_ks) : nullptr;
+    ws.vscales = fp8 ? reinterpret_cast<float **>(b + o_vs) : nullptr;
     ws.dst_table = reinterpret_cast<int32_t *>(b + o_dst);
     ws.push_list = reinterpret_cast<int32_t *>(b + o_push);
     ws.counters = reinterpret_cast<int32_t *>(b + o_cnt);
@@ -228,11 +241,23 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     ws.ca_part = reinterpret_cast<float *>(b + o_ca_part);
     c->kpools.assign(D.k_pools, D.k_pools + D.num_layers);
     c->vpools.assign(D.v_pools, D.v_pools + D.num_layers);
+    c->fp8 = fp8;
+    if (fp8) {
+        c->kscales.assign(k_scales, k_scales + D.num_layers);
+        c->vscales.assign(v_scales, v_scales + D.num_layers);
+    }
 
     std::vector<CUtensorMap> kmaps(D.num_layers), vmaps(D.num_layers), krmaps(D.num_layers),
         vrmaps(D.num_layers);
     bool ok = true;
     for (int l = 0; l < D.num_layers && ok; ++l) {
+        if (fp8) {  // (no call on such a cache gathers single rows)
+            ok = zp::encode_fp8_pool_map(&kmaps[l], D.k_pools[l], D.num_blocks, D.num_kv_heads,
+                                         D.head_dim) &&
+                 zp::encode_fp8_pool_map(&vmaps[l], D.v_pools[l], D.num_blocks, D.num_kv_heads,
+                                         D.head_dim);
+            continue;
+        }
         ok = zp::encode_pool_map(&kmaps[l], D.k_pools[l], D.num_blocks, D.num_kv_heads,
                                  D.head_dim) &&
              zp::encode_pool_map(&vmaps[l], D.v_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim) &&
@@ -255,7 +280,11 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
          cudaMemcpy(ws.kpools, D.k_pools, sizeof(void *) * D.num_layers,
                     cudaMemcpyHostToDevice) == cudaSuccess &&
          cudaMemcpy(ws.vpools, D.v_pools, sizeof(void *) * D.num_layers,
-                    cudaMemcpyHostToDevice) == cudaSuccess;
+                    cudaMemcpyHostToDevice) == cudaSuccess &&
+         (!fp8 || (cudaMemcpy(ws.kscales, k_scales, sizeof(float *) * D.num_layers,
+                              cudaMemcpyHostToDevice) == cudaSuccess &&
+                   cudaMemcpy(ws.vscales, v_scales, sizeof(float *) * D.num_layers,
+                              cudaMemcpyHostToDevice) == cudaSuccess));
     if (!ok) {
         cudaGetLastError();
         cudaFree(c->base);
@@ -264,6 +293,21 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
     }
     *out = c;
     return ZP_OK;
+}
+
+zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out)
+{
+    NvtxRange nvtx("zp_cache_create");
+    return create(desc, nullptr, nullptr, out);
+}
+
+zp_status zp_cache_create_fp8(const zp_cache_desc *desc, float *const *k_scales,
+                              float *const *v_scales, zp_cache **out)
+{
+    NvtxRange nvtx("zp_cache_create_fp8");
+    if (!k_scales || !v_scales)
+        return ZP_ERR_INVALID_ARG;
+    return create(desc, k_scales, v_scales, out);
 }
 
 void zp_cache_destroy(zp_cache *cache)
@@ -298,6 +342,8 @@ zp_status zp_compress(zp_cache *c, int32_t *block_tables, int32_t bt_stride, int
         return ZP_ERR_INVALID_ARG;
     if (!aligned(window_q, 16) || !aligned(scores_out, 4) || !aligned(kept_out, 4))
         return ZP_ERR_INVALID_ARG;
+    if (c->fp8)
+        return ZP_ERR_UNSUPPORTED;
     const int G = c->Hq / c->Hkv;
     const int T = n_max * c->b;
     const int rows = window * G;
@@ -418,6 +464,8 @@ zp_status zp_compress_prefill(zp_cache *c, int32_t *block_tables, int32_t bt_str
     if (!aligned(window_q, 16) || !aligned(scores_out, 4) || !aligned(kept_out, 4) ||
         !aligned(workspace, 256))
         return ZP_ERR_INVALID_ARG;
+    if (c->fp8)
+        return ZP_ERR_UNSUPPORTED;
     const int G = c->Hq / c->Hkv;
     const int rows = window * G;
     if (bt_stride > c->max_blocks || static_cast<long long>(bt_stride) * c->b > zp::kPrefillMaxTokens ||
@@ -514,6 +562,64 @@ zp_status zp_compress_prefill(zp_cache *c, int32_t *block_tables, int32_t bt_str
     return ZP_OK;
 }
 
+// What the attention calls on an 8-bit cache share.
+static zp::Fp8AttnArgs fp8_attn_args(const zp_cache *c, int32_t layer, const void *q,
+                                     int64_t q_stride, const int32_t *block_tables,
+                                     int32_t bt_stride, int32_t num_rows, const int32_t *lengths,
+                                     const int32_t *req_idx, int32_t R, float scale, void *out)
+{
+    zp::Fp8AttnArgs a{};
+    a.kmap = c->ws.kmaps + layer;
+    a.vmap = c->ws.vmaps + layer;
+    a.kscale = c->kscales[layer];
+    a.vscale = c->vscales[layer];
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.q_stride = q_stride;
+    a.tables = block_tables;
+    a.stride = bt_stride;
+    a.num_rows = num_rows;
+    a.lengths = lengths;
+    a.req_idx = req_idx;
+    a.R = R;
+    a.Hkv = c->Hkv;
+    a.Hq = c->Hq;
+    a.num_blocks = c->num_blocks;
+    a.splits = 1;
+    a.bps = bt_stride;
+    a.logit_scale = scale * 1.4426950408889634f;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.sticky = c->ws.sticky;
+    return a;
+}
+
+// What the appends to an 8-bit cache share.
+static zp::Fp8KvArgs fp8_kv_args(const zp_cache *c, int32_t layer, const void *k_new,
+                                 int64_t k_stride, const void *v_new, int64_t v_stride,
+                                 const int32_t *block_tables, int32_t bt_stride, int32_t num_rows,
+                                 const int32_t *lengths, const int32_t *req_idx, int32_t R)
+{
+    zp::Fp8KvArgs a{};
+    a.kpool = static_cast<uint8_t *>(c->kpools[layer]);
+    a.vpool = static_cast<uint8_t *>(c->vpools[layer]);
+    a.kscale = c->kscales[layer];
+    a.vscale = c->vscales[layer];
+    a.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+    a.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.tables = block_tables;
+    a.stride = bt_stride;
+    a.num_rows = num_rows;
+    a.lengths = lengths;
+    a.req_idx = req_idx;
+    a.R = R;
+    a.Hkv = c->Hkv;
+    a.d = c->d;
+    a.num_blocks = c->num_blocks;
+    a.sticky = c->ws.sticky;
+    return a;
+}
+
 zp_status zp_paged_decode_attn(zp_cache *c, int32_t layer, const void *q,
                                const int32_t *block_tables, int32_t bt_stride, int32_t num_rows,
                                const int32_t *lengths, const int32_t *req_idx, int32_t R,
@@ -537,6 +643,17 @@ zp_status zp_paged_decode_attn(zp_cache *c, int32_t layer, const void *q,
     int bps = 0;
     const int splits = zp::decode_splits(static_cast<long long>(R) * c->Hkv, bt_stride,
                                          c->num_sms, &bps);
+    if (c->fp8) {
+        zp::Fp8AttnArgs a = fp8_attn_args(c, layer, q, static_cast<int64_t>(c->Hq) * c->d,
+                                          block_tables, bt_stride, num_rows, lengths, req_idx, R,
+                                          scale, out);
+        a.splits = splits;
+        a.bps = bps;
+        a.part = c->ws.dec_part;
+        return zp::launch_fp8_decode(a, c->d, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? ZP_OK
+                   : ZP_ERR_CUDA;
+    }
 
     zp::DecodeArgs da{};
     // the per-layer maps live in device memory; kernels take their address
@@ -599,7 +716,7 @@ zp_status zp_append_slots(zp_cache *c, int32_t *block_tables, int32_t bt_stride,
     a.num_blocks = c->num_blocks;
     a.L = c->L;
     a.Hkv = c->Hkv;
-    a.d = c->d;
+    a.vpr = c->d / (c->fp8 ? 16 : 8);
     a.refcount = pool->refcount;
     a.free_ids = pool->free_ids;
     a.free_count = pool->free_count;
@@ -628,6 +745,15 @@ zp_status zp_append_kv(zp_cache *c, int32_t layer, const void *k_new, const void
         return ZP_OK;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
+    if (c->fp8) {
+        const int64_t row = static_cast<int64_t>(c->Hkv) * c->d;
+        zp::Fp8KvArgs a = fp8_kv_args(c, layer, k_new, row, v_new, row, block_tables, bt_stride,
+                                      num_rows, lengths, req_idx, R);
+        a.total = R;
+        return zp::launch_fp8_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? ZP_OK
+                   : ZP_ERR_CUDA;
+    }
     zp::AppendKvArgs a{};
     a.kpool = static_cast<__nv_bfloat16 *>(c->kpools[layer]);
     a.vpool = static_cast<__nv_bfloat16 *>(c->vpools[layer]);
@@ -733,7 +859,7 @@ zp_status zp_global_redundancy(zp_cache *c, const int32_t *block_tables, int32_t
         return ZP_ERR_INVALID_ARG;
     if (R < 0 || R > c->max_requests || num_rows < 1 || bt_stride < 1)
         return ZP_ERR_INVALID_ARG;
-    if (static_cast<long long>(bt_stride) * c->b >= (1ll << 31))
+    if (c->fp8 || static_cast<long long>(bt_stride) * c->b >= (1ll << 31))
         return ZP_ERR_UNSUPPORTED;
     const long long units = static_cast<long long>(R) * c->L * c->Hkv;
     if (units >= (1ll << 31))
@@ -771,7 +897,7 @@ zp_status zp_global_redundancy_gram(zp_cache *c, const int32_t *block_tables,
         return ZP_ERR_INVALID_ARG;
     if (R < 0 || R > c->max_requests || num_rows < 1 || bt_stride < 1)
         return ZP_ERR_INVALID_ARG;
-    if (static_cast<long long>(bt_stride) * c->b >= (1ll << 31))
+    if (c->fp8 || static_cast<long long>(bt_stride) * c->b >= (1ll << 31))
         return ZP_ERR_UNSUPPORTED;
     const long long units = static_cast<long long>(R) * c->L * c->Hkv;
     const int T_cap = bt_stride * c->b;
@@ -845,8 +971,12 @@ zp_status zp_append_kv_chunk(zp_cache *c, int32_t layer, const void *k_new, int6
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
-    const unsigned long long pool = 2ull * c->num_blocks * c->b * row;
-    const Span outs[] = {{c->kpools[layer], pool}, {c->vpools[layer], pool}};
+    const unsigned long long pool = (c->fp8 ? 1ull : 2ull) * c->num_blocks * c->b * row;
+    const unsigned long long scales = 4ull * c->num_blocks * c->Hkv;
+    const Span outs[] = {{c->kpools[layer], pool},
+                         {c->vpools[layer], pool},
+                         {c->fp8 ? c->kscales[layer] : nullptr, scales},
+                         {c->fp8 ? c->vscales[layer] : nullptr, scales}};
     const Span ins[] = {{k_new, row_bytes(total, k_stride, row)},
                         {v_new, row_bytes(total, v_stride, row)},
                         {starts, 4ull * R + 4},
@@ -857,6 +987,15 @@ zp_status zp_append_kv_chunk(zp_cache *c, int32_t layer, const void *k_new, int6
         return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
+    if (c->fp8) {
+        zp::Fp8KvArgs a = fp8_kv_args(c, layer, k_new, k_stride, v_new, v_stride, block_tables,
+                                      bt_stride, num_rows, lengths, req_idx, R);
+        a.starts = starts;
+        a.total = total;
+        return zp::launch_fp8_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? ZP_OK
+                   : ZP_ERR_CUDA;
+    }
     zp::ChunkKvArgs a{};
     a.kpool = static_cast<__nv_bfloat16 *>(c->kpools[layer]);
     a.vpool = static_cast<__nv_bfloat16 *>(c->vpools[layer]);
@@ -898,11 +1037,15 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         return ZP_ERR_INVALID_ARG;
     if (R == 0 || total == 0)
         return ZP_OK;
-    const unsigned long long pool = 2ull * c->num_blocks * c->b * c->Hkv * c->d;
+    const unsigned long long pool =
+        (c->fp8 ? 1ull : 2ull) * c->num_blocks * c->b * c->Hkv * c->d;
+    const unsigned long long scales = 4ull * c->num_blocks * c->Hkv;
     const Span outs[] = {{out, row_bytes(total, row, row)}};
     const Span ins[] = {{q, row_bytes(total, q_stride, row)},
                         {c->kpools[layer], pool},
                         {c->vpools[layer], pool},
+                        {c->fp8 ? c->kscales[layer] : nullptr, scales},
+                        {c->fp8 ? c->vscales[layer] : nullptr, scales},
                         {starts, 4ull * R + 4},
                         {block_tables, 4ull * num_rows * bt_stride},
                         {lengths, 4ull * num_rows},
@@ -911,6 +1054,15 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
+    if (c->fp8) {
+        zp::Fp8AttnArgs a = fp8_attn_args(c, layer, q, q_stride, block_tables, bt_stride, num_rows,
+                                          lengths, req_idx, R, scale, out);
+        a.starts = starts;
+        a.total = total;
+        return zp::launch_fp8_decode(a, c->d, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? ZP_OK
+                   : ZP_ERR_CUDA;
+    }
     zp::ChunkAttnArgs a{};
     a.kmap = c->ws.kmaps + layer;
     a.vmap = c->ws.vmaps + layer;
@@ -1004,6 +1156,92 @@ zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *sta
                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? ZP_OK
                : ZP_ERR_CUDA;
+}
+
+// What zp_sample and zp_token_probs share: the checks of the rows and filters, then the
+// launch.  u and tokens, or probs, are the call's own.
+static zp_status sample(zp_cache *c, const void *logits, int32_t logit_dtype, int32_t vocab,
+                        int64_t logit_stride, const float *temperature, const int32_t *top_k,
+                        const float *top_p, const float *min_p, int32_t num_rows,
+                        const int32_t *req_idx, int32_t R, const float *u, int32_t *tokens,
+                        void *probs, int32_t prob_dtype, int64_t prob_stride, void *stream)
+{
+    const bool f32 = logit_dtype == ZP_DTYPE_F32;
+    if ((!f32 && logit_dtype != ZP_DTYPE_BF16) ||
+        (prob_dtype != ZP_DTYPE_F32 && prob_dtype != ZP_DTYPE_BF16) ||
+        vocab > zp::kSampleMaxVocab || R > (1 << 24))
+        return ZP_ERR_UNSUPPORTED;
+    const size_t esz = f32 ? 4 : 2, psz = prob_dtype == ZP_DTYPE_F32 ? 4 : 2;
+    if (!aligned(logits, esz) || !aligned(probs, psz) || !aligned(temperature, 4) ||
+        !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(req_idx, 4) ||
+        !aligned(u, 4) || !aligned(tokens, 4))
+        return ZP_ERR_INVALID_ARG;
+    if (R == 0)
+        return ZP_OK;
+    const unsigned long long per_row = 4ull * num_rows, per_request = 4ull * R;
+    const Span outs[] = {
+        {tokens, per_request},
+        {probs, psz * (static_cast<unsigned long long>(R - 1) * prob_stride + vocab)}};
+    const Span ins[] = {
+        {logits, esz * (static_cast<unsigned long long>(R - 1) * logit_stride + vocab)},
+        {temperature, per_row},
+        {top_k, per_row},
+        {top_p, per_row},
+        {min_p, per_row},
+        {req_idx, per_request},
+        {u, per_request}};
+    if (shared_memory(outs, ins))
+        return ZP_ERR_INVALID_ARG;
+    if (!on_device(c))
+        return ZP_ERR_INVALID_ARG;
+    zp::SampleArgs a{};
+    a.logits = logits;
+    a.vocab = vocab;
+    a.stride = logit_stride;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.num_rows = num_rows;
+    a.req_idx = req_idx;
+    a.R = R;
+    a.u = u;
+    a.tokens = tokens;
+    a.probs = probs;
+    a.prob_bf16 = prob_dtype == ZP_DTYPE_BF16;
+    a.prob_stride = prob_stride;
+    a.sticky = c->ws.sticky;
+    return zp::launch_sample(a, !f32, c->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ZP_OK
+               : ZP_ERR_CUDA;
+}
+
+zp_status zp_sample(zp_cache *c, const void *logits, int32_t logit_dtype, int32_t vocab,
+                    int64_t logit_stride, const float *temperature, const int32_t *top_k,
+                    const float *top_p, const float *min_p, int32_t num_rows,
+                    const int32_t *req_idx, const float *u, int32_t R, int32_t *tokens,
+                    void *stream)
+{
+    NvtxRange nvtx("zp_sample");
+    if (!c || (R > 0 && (!logits || !u || !tokens)) || R < 0 || R > c->max_requests ||
+        vocab < 1 || logit_stride < vocab || num_rows < 1 || (!req_idx && R > num_rows))
+        return ZP_ERR_INVALID_ARG;
+    return sample(c, logits, logit_dtype, vocab, logit_stride, temperature, top_k, top_p, min_p,
+                  num_rows, req_idx, R, u, tokens, nullptr, ZP_DTYPE_F32, vocab, stream);
+}
+
+zp_status zp_token_probs(zp_cache *c, const void *logits, int32_t logit_dtype, int32_t vocab,
+                         int64_t logit_stride, const float *temperature, const int32_t *top_k,
+                         const float *top_p, const float *min_p, int32_t num_rows,
+                         const int32_t *req_idx, int32_t R, void *probs, int32_t prob_dtype,
+                         int64_t prob_stride, void *stream)
+{
+    NvtxRange nvtx("zp_token_probs");
+    if (!c || (R > 0 && (!logits || !probs)) || R < 0 || vocab < 1 || logit_stride < vocab ||
+        prob_stride < vocab || num_rows < 1 || (!req_idx && R > num_rows))
+        return ZP_ERR_INVALID_ARG;
+    return sample(c, logits, logit_dtype, vocab, logit_stride, temperature, top_k, top_p, min_p,
+                  num_rows, req_idx, R, nullptr, nullptr, probs, prob_dtype, prob_stride, stream);
 }
 
 zp_status zp_cache_status(zp_cache *c, void *stream, int32_t *out_status)

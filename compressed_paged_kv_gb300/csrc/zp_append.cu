@@ -16,8 +16,8 @@
 //                           nothing the caller owns.
 //   zp_append_apply_kernel  one CTA per listed request: copies the filled
 //                           slots of a shared tail block (every layer, kv
-//                           head, K and V) into its fresh block with 16-byte
-//                           vectors, then commits the table entry, refcounts,
+//                           head, K and V; an 8-bit cache's scales too) into
+//                           its fresh block with 16-byte vectors, then commits the table entry, refcounts,
 //                           length and trigger row.
 // zp_append_kv is one launch per layer: one warp per (request, kv head)
 // stores the K and V rows of the new token with 16-byte stores.
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kApplyThreads) zp_append_apply_kernel(const Ap
 
     // copy-on-write: slots 0 .. rows-1 of every (layer, kv head, K/V) slab
     if (e.z > 0) {
-        const int vpr = a.d / 8;  // 16-byte vectors per token row
+        const int vpr = a.vpr;
         const int per_slab = e.z * vpr;
         const int total = a.L * a.Hkv * 2 * per_slab;
         const size_t slab = (size_t)kBlk * vpr;
@@ -187,6 +187,12 @@ __global__ void __launch_bounds__(kApplyThreads) zp_append_apply_kernel(const Ap
             const uint4 x = ld_global_nc_v4(pool + ((size_t)e.x * a.Hkv + h) * slab + off);
             pool[((size_t)e.y * a.Hkv + h) * slab + off] = x;
         }
+        if (a.ws.kscales)  // the rows of an 8-bit cache go with their blocks' scales
+            for (int v = threadIdx.x; v < a.L * a.Hkv * 2; v += kApplyThreads) {
+                const int h = (v >> 1) % a.Hkv, l = (v >> 1) / a.Hkv;
+                float *scale = v & 1 ? a.ws.vscales[l] : a.ws.kscales[l];
+                scale[(size_t)e.y * a.Hkv + h] = scale[(size_t)e.x * a.Hkv + h];
+            }
     }
     if (threadIdx.x == 0) {
         const int row = a.req_idx ? a.req_idx[i] : i;

@@ -35,6 +35,8 @@ struct Workspace {
     CUtensorMap *vrmaps; // [L]  V pool maps, same
     void **kpools;       // [L]  device copies of the pool pointers
     void **vpools;       // [L]
+    float **kscales;     // [L]  of an 8-bit cache: device copies of the scale pointers; else null
+    float **vscales;     // [L]
     int32_t *dst_table;  // [max_requests * max_blocks] plan: destination blocks
     int32_t *push_list;  // [max_requests * max_blocks] plan: blocks to free, in order
     int32_t *counters;   // [4]  plan: pops, pushes; [2] the compaction's own status
@@ -156,7 +158,7 @@ struct AppendArgs {
     int32_t stride, num_rows;
     int32_t *lengths;
     const int32_t *req_idx;
-    int32_t R, n_max, num_blocks, L, Hkv, d;
+    int32_t R, n_max, num_blocks, L, Hkv, vpr;  // vpr: 16-byte vectors of a token's row
     int32_t *refcount;
     const int32_t *free_ids;
     int32_t *free_count;

@@ -3,7 +3,7 @@
 // num_blocks * Hkv * b rows of d elements.
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
 
-#include "zp_chunk.cuh"
+#include "zp_fp8.cuh"
 
 namespace {
 
@@ -60,6 +60,24 @@ bool encode_row_map(CUtensorMap *map, const void *pool, int num_blocks, int hkv,
     CUresult res = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims,
                       strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return res == CUDA_SUCCESS;
+}
+
+// An 8-bit pool as rows of d bytes: one box is a whole (block, kv head) slab.
+bool encode_fp8_pool_map(CUtensorMap *map, const void *pool, int num_blocks, int hkv, int d)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(d),
+                          static_cast<cuuint64_t>(num_blocks) * hkv * zp::kBlk};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(zp::kBlk)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult res = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims,
+                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return res == CUDA_SUCCESS;
 }
 

@@ -3,12 +3,13 @@ every step of compression and decode attention runs in the library's CUDA
 kernels.  There is no fallback: if the library is missing or fails to load,
 every call raises.
 
-The functions keep the C names (``zp_cache_create``, ``zp_compress``,
+The functions keep the C names (``zp_cache_create``, ``zp_cache_create_fp8``, ``zp_compress``,
 ``zp_paged_decode_attn``, ``zp_append_slots``, ``zp_append_kv``,
 ``zp_compress_prefill``, ``zp_compress_prefill_workspace_size``, ``zp_global_redundancy``,
 ``zp_global_redundancy_gram``,
 ``zp_alloc_rows``, ``zp_release_rows``, ``zp_fork_rows``,
 ``zp_append_kv_chunk``, ``zp_paged_chunk_attn``, ``zp_verify_draft``,
+``zp_sample``, ``zp_token_probs``,
 ``zp_cache_status``, ``zp_cache_destroy``, ``zp_status_string``) and take raw integers (device pointers, a cudaStream_t
 as an int).  ``Cache`` wraps them for torch tensors: it reads ``data_ptr()``
 and the current stream, and keeps the pool tensors alive.
@@ -73,6 +74,9 @@ def lib():
         L = ctypes.CDLL(path)
         L.zp_cache_create.argtypes = [ctypes.POINTER(zp_cache_desc), ctypes.POINTER(P)]
         L.zp_cache_create.restype = I32
+        L.zp_cache_create_fp8.argtypes = [ctypes.POINTER(zp_cache_desc), ctypes.POINTER(P),
+                                          ctypes.POINTER(P), ctypes.POINTER(P)]
+        L.zp_cache_create_fp8.restype = I32
         L.zp_cache_destroy.argtypes = [P]
         L.zp_cache_destroy.restype = None
         L.zp_compress.argtypes = [P, P, I32, I32, P, P, I32, P, I32, I32, ctypes.c_float,
@@ -110,6 +114,10 @@ def lib():
         L.zp_verify_draft.argtypes = [P, P, P, I32, P, P, I32, I32, I64, P, P, P, I32, P, I32, P,
                                       P, P]
         L.zp_verify_draft.restype = I32
+        L.zp_sample.argtypes = [P, P, I32, I32, I64, P, P, P, P, I32, P, P, I32, P, P]
+        L.zp_sample.restype = I32
+        L.zp_token_probs.argtypes = [P, P, I32, I32, I64, P, P, P, P, I32, P, I32, P, I32, I64, P]
+        L.zp_token_probs.restype = I32
         L.zp_global_redundancy.argtypes = [P, P, I32, I32, P, P, I32, P, P]
         L.zp_global_redundancy.restype = I32
         L.zp_global_redundancy_gram.argtypes = [P, P, I32, I32, P, P, I32, P, P]
@@ -137,6 +145,16 @@ def zp_cache_create(desc: zp_cache_desc) -> int:
     st = lib().zp_cache_create(ctypes.byref(desc), ctypes.byref(h))
     if st != OK:
         raise ZpError(st, "zp_cache_create")
+    return h.value
+
+
+def zp_cache_create_fp8(desc: zp_cache_desc, k_scales, v_scales) -> int:
+    """``k_scales``, ``v_scales``: ctypes arrays of the layers' scale pointers.
+    Returns the handle (an int) or raises ZpError."""
+    h = P()
+    st = lib().zp_cache_create_fp8(ctypes.byref(desc), k_scales, v_scales, ctypes.byref(h))
+    if st != OK:
+        raise ZpError(st, "zp_cache_create_fp8")
     return h.value
 
 
@@ -243,6 +261,19 @@ def zp_verify_draft(handle, tokens, starts, total, target_probs, draft_probs, pr
                                  num_rows, req_idx, R, accepted, next_tokens, stream)
 
 
+def zp_sample(handle, logits, logit_dtype, vocab, logit_stride, temperature, top_k, top_p, min_p,
+              num_rows, req_idx, u, R, tokens, stream) -> int:
+    return lib().zp_sample(handle, logits, logit_dtype, vocab, logit_stride, temperature, top_k,
+                           top_p, min_p, num_rows, req_idx, u, R, tokens, stream)
+
+
+def zp_token_probs(handle, logits, logit_dtype, vocab, logit_stride, temperature, top_k, top_p,
+                   min_p, num_rows, req_idx, R, probs, prob_dtype, prob_stride, stream) -> int:
+    return lib().zp_token_probs(handle, logits, logit_dtype, vocab, logit_stride, temperature,
+                                top_k, top_p, min_p, num_rows, req_idx, R, probs, prob_dtype,
+                                prob_stride, stream)
+
+
 def zp_global_redundancy(handle, block_tables, bt_stride, num_rows, lengths, req_idx, R, red_out,
                          stream) -> int:
     return lib().zp_global_redundancy(P(handle), P(block_tables), bt_stride, num_rows,
@@ -307,15 +338,30 @@ def _flat(t, what, n, dtype):
 
 
 class Cache:
-    """A zp_cache over per-layer torch pools ([num_blocks][Hkv][16][d] bf16)."""
+    """A zp_cache over per-layer torch pools ([num_blocks][Hkv][16][d] bf16), or with
+    ``k_scales`` and ``v_scales`` ([num_blocks][Hkv] fp32 a layer) an 8-bit one
+    over float8_e4m3fn pools."""
 
-    def __init__(self, k_pools, v_pools, num_q_heads, max_requests, max_blocks_per_req):
+    def __init__(self, k_pools, v_pools, num_q_heads, max_requests, max_blocks_per_req,
+                 k_scales=None, v_scales=None):
         import torch
         assert len(k_pools) == len(v_pools) >= 1
+        fp8 = k_scales is not None
+        dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
         for t in list(k_pools) + list(v_pools):
-            if not (t.is_cuda and t.dtype == torch.bfloat16 and t.is_contiguous() and t.dim() == 4):
-                raise ValueError("pools must be contiguous 4-D bf16 CUDA tensors")
+            if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.dim() == 4):
+                raise ValueError(f"pools must be contiguous 4-D {dtype} CUDA tensors")
+            if fp8 and t.shape != k_pools[0].shape:
+                raise ValueError("pools must have one shape")
         nb, hkv, b, d = k_pools[0].shape
+        if fp8 != (v_scales is not None) or (
+                fp8 and not len(k_scales) == len(v_scales) == len(k_pools)):
+            raise ValueError("k_scales and v_scales must hold one tensor a layer, or both be None")
+        for t in (list(k_scales) + list(v_scales)) if fp8 else []:
+            if not (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous()
+                    and t.shape == (nb, hkv)):
+                raise ValueError("scales must be contiguous [num_blocks, Hkv] float32 CUDA tensors")
+        self.k_scales, self.v_scales = (list(k_scales), list(v_scales)) if fp8 else (None, None)
         self.k_pools, self.v_pools = list(k_pools), list(v_pools)
         self.dtype, self.int32, self.float32 = torch.bfloat16, torch.int32, torch.float32
         self.L, self.Hkv, self.Hq, self.d, self.b, self.num_blocks = (
@@ -324,7 +370,12 @@ class Cache:
         vp = (P * self.L)(*[t.data_ptr() for t in v_pools])
         desc = zp_cache_desc(self.L, hkv, num_q_heads, d, b, nb, max_requests,
                              max_blocks_per_req, kp, vp)
-        self.handle = zp_cache_create(desc)
+        if fp8:
+            ks = (P * self.L)(*[t.data_ptr() for t in k_scales])
+            vs = (P * self.L)(*[t.data_ptr() for t in v_scales])
+            self.handle = zp_cache_create_fp8(desc, ks, vs)
+        else:
+            self.handle = zp_cache_create(desc)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -488,6 +539,69 @@ class Cache:
         if check and st != OK:
             raise ZpError(st, "zp_verify_draft")
         return st
+
+    def sample(self, logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
+               req_idx=None, stream=None, check=True):
+        """logits: [R, vocab] fp32 or bf16 with contiguous rows; the filters one entry a
+        request ([rows], row i uses entry req_idx[i] or i), each optional."""
+        dtype, vocab, ls, R, rows = self._logit_rows(logits, temperature, top_k, top_p, min_p,
+                                                     req_idx)
+        _flat(u, "u", R, self.float32)
+        _flat(tokens, "tokens", R, self.int32)
+        st = zp_sample(self.handle, logits.data_ptr(), dtype, vocab, ls, _ptr(temperature),
+                       _ptr(top_k), _ptr(top_p), _ptr(min_p), rows, _ptr(req_idx), u.data_ptr(), R,
+                       tokens.data_ptr(), _stream(stream))
+        if check and st != OK:
+            raise ZpError(st, "zp_sample")
+        return st
+
+    def token_probs(self, logits, probs, temperature=None, top_k=None, top_p=None, min_p=None,
+                    req_idx=None, stream=None, check=True):
+        """logits and the filters as in ``sample``; probs: [R, vocab] fp32 or bf16 with
+        contiguous rows."""
+        dtype, vocab, ls, R, rows = self._logit_rows(logits, temperature, top_k, top_p, min_p,
+                                                     req_idx)
+        if probs.dtype not in (self.float32, self.dtype):
+            raise ValueError("probs must be [R, vocab], float32 or bfloat16")
+        ps = _row_stride(probs, "probs", (vocab,), probs.dtype)
+        if probs.shape[0] != R:
+            raise ValueError("probs must have a row for each row of logits")
+        st = zp_token_probs(self.handle, logits.data_ptr(), dtype, vocab, ls, _ptr(temperature),
+                            _ptr(top_k), _ptr(top_p), _ptr(min_p), rows, _ptr(req_idx), R,
+                            probs.data_ptr(),
+                            DTYPE_F32 if probs.dtype == self.float32 else DTYPE_BF16, ps,
+                            _stream(stream))
+        if check and st != OK:
+            raise ZpError(st, "zp_token_probs")
+        return st
+
+    def _logit_rows(self, logits, temperature, top_k, top_p, min_p, req_idx):
+        """Checks the rows of logits and their filters: (type, vocabulary, row stride, rows,
+        entries of the filters)."""
+        if logits.dim() != 2 or logits.dtype not in (self.float32, self.dtype):
+            raise ValueError("logits must be [R, vocab], float32 or bfloat16")
+        R, vocab = logits.shape
+        stride = _row_stride(logits, "logits", (vocab,), logits.dtype)
+        rows = None
+        for t, what, dtype in ((temperature, "temperature", self.float32),
+                               (top_k, "top_k", self.int32), (top_p, "top_p", self.float32),
+                               (min_p, "min_p", self.float32)):
+            if t is None:
+                continue
+            if rows is None:
+                rows = t.numel()
+            _flat(t, what, rows, dtype)
+            if t.numel() != rows:
+                raise ValueError("the filters must have as many entries as each other")
+        if req_idx is not None:
+            _flat(req_idx, "req_idx", R, self.int32)
+            if rows is None:  # no filters: any entry will do
+                rows = 0x7fffffff
+        elif rows is None:
+            rows = max(R, 1)
+        elif rows < R:
+            raise ValueError(f"{R} rows for {rows} entries of the filters")
+        return (DTYPE_F32 if logits.dtype == self.float32 else DTYPE_BF16, vocab, stride, R, rows)
 
     def alloc_rows(self, block_tables, lengths, counts, free_ids, free_count, refcount,
                    req_idx=None, stream=None, check=True):

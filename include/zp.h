@@ -27,8 +27,8 @@
  *  - A handle serves at most one call of each entry point in flight at a
  *    time.  zp_compress may run concurrently with zp_paged_decode_attn and
  *    zp_append_kv on another stream when they touch disjoint requests, and
- *    so may zp_append_kv_chunk, zp_paged_chunk_attn and zp_verify_draft beside
- *    each other and any other call.
+ *    so may zp_append_kv_chunk, zp_paged_chunk_attn, zp_verify_draft,
+ *    zp_sample and zp_token_probs beside each other and any other call.
  *    zp_compress, zp_compress_prefill, zp_append_slots, zp_alloc_rows,
  *    zp_release_rows and zp_fork_rows change the free stack or refcounts:
  *    order them (one stream, or events).  More concurrency needs
@@ -61,7 +61,7 @@ typedef int32_t zp_status;
 #define ZP_ERR_CUDA (-5)          /* a CUDA runtime call failed */
 #define ZP_ERR_TIMEOUT (-6)       /* a bounded device-side wait gave up */
 
-/* Element types of probability rows (zp_verify_draft). */
+/* Element types of rows of probabilities and logits. */
 #define ZP_DTYPE_F32 0
 #define ZP_DTYPE_BF16 1
 
@@ -103,6 +103,31 @@ typedef struct {
  * (checked before any CUDA call), ZP_ERR_CUDA if an allocation fails.
  * *out is set only on success; the current CUDA device is recorded. */
 zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out);
+
+/* Creates a handle over an 8-bit cache: pools of e4m3 numbers (one byte each, as
+ * float8_e4m3fn) in the layout above, and a scale for each (block, kv head) slab, K and
+ * V apart:
+ *     k_scales[l], v_scales[l]   device fp32 [num_blocks][num_kv_heads], caller-owned
+ * with value = scale * number.  Scales are powers of two from 2^-32 to 2^32; the
+ * calls that write rows write them (a caller that fills blocks itself writes such
+ * ones).  The same calls serve it as a bf16 cache, on bf16 tensors:
+ *   zp_append_kv, zp_append_kv_chunk  round the new rows into it: with A the largest
+ *       magnitude (NaN not counted) of the rows that the call writes into a slab and
+ *       S' the least scale with A / S' <= 448, the slab's scale becomes S = S' if
+ *       they begin at its slot 0, else max(S', scale), where a larger scale has the
+ *       numbers before them rounded again to number * (scale / S); then number = x / S
+ *       to the nearest e4m3 number (ties to even, magnitudes past 448 to 448, NaN to
+ *       NaN).  Slots past the call's rows keep their bytes.
+ *   zp_paged_decode_attn, zp_paged_chunk_attn  attend over the values; the
+ *       probabilities' products with V are rounded to fp16 at most
+ *   zp_append_slots  copies a shared tail's scales with its rows
+ *   zp_alloc_rows, zp_release_rows, zp_fork_rows, zp_verify_draft, zp_sample,
+ *       zp_token_probs, zp_cache_status  as they are
+ * zp_compress, zp_compress_prefill, zp_global_redundancy and
+ * zp_global_redundancy_gram answer ZP_ERR_UNSUPPORTED: they read and move bf16 rows.
+ * Errors as zp_cache_create; a null scale pointer is ZP_ERR_INVALID_ARG. */
+zp_status zp_cache_create_fp8(const zp_cache_desc *desc, float *const *k_scales,
+                              float *const *v_scales, zp_cache **out);
 
 /* Frees the handle and its workspace (not the pools).  NULL is a no-op.
  * The caller must make sure no work that uses the handle is in flight. */
@@ -501,6 +526,56 @@ zp_status zp_verify_draft(zp_cache *cache, const int32_t *tokens, const int32_t 
                           const float *accept_u, const float *sample_u, int32_t *lengths,
                           int32_t num_rows, const int32_t *req_idx, int32_t R, int32_t *accepted,
                           int32_t *next_tokens, void *stream);
+
+/* ------------------------------------------------------- logits to tokens
+ * The two calls below take rows of logits and filters of their requests.  With l the
+ * logits of a row and M the largest, a token's weight is exp((l - M) / temperature).
+ * Kept are
+ *     the top_k largest logits (0 or less, or vocab and more: all),
+ *     of these the shortest run of the largest whose weights sum to at least
+ *       top_p of theirs (1 and more: all; 0 and less: the largest alone),
+ *     of these the weights of at least min_p (0 and less: all; 1 and more: those
+ *       equal to the largest),
+ * equal logits in the order of their index.  A temperature of 0 keeps the first of
+ * the largest alone.  A NaN counts as -infinity, whose weight is 0; of infinite logits
+ * only they have weight.
+ * Weights are formed and summed in more than 40 bits behind the largest's point, and
+ * their sums are exact, so that neither depends on the order of the work.
+ *
+ *  logits        device [R][vocab] of logit_dtype, rows logit_stride elements apart
+ *                (any, >= vocab)
+ *  vocab         at most 360448 (ZP_ERR_UNSUPPORTED beyond)
+ *  temperature, top_k, top_p, min_p   device [num_rows] fp32, int32, fp32, fp32, each
+ *                NULL for 1, 0, 1, 0; row i uses entry req_idx[i], or i with NULL
+ *                (entries may be used by several rows: a chunk's)
+ *  R             rows of logits
+ * Outputs share no memory with inputs or each other (ZP_ERR_INVALID_ARG).  An entry
+ * out of range, a temperature below 0, infinite or NaN, a NaN among the others, or a
+ * row without any logit above -infinity is recorded as ZP_ERR_DEVICE_CHECK in the
+ * sticky status, and its token is -1, its probabilities 0. */
+
+/* Draws each row's next token from given random numbers: the lowest kept index whose
+ * running sum of weights exceeds u[i] times the sum of all kept ones.
+ *
+ *  u             device fp32 [R], in [0, 1)
+ *  tokens        device int32 [R] */
+zp_status zp_sample(zp_cache *cache, const void *logits, int32_t logit_dtype, int32_t vocab,
+                    int64_t logit_stride, const float *temperature, const int32_t *top_k,
+                    const float *top_p, const float *min_p, int32_t num_rows,
+                    const int32_t *req_idx, const float *u, int32_t R, int32_t *tokens,
+                    void *stream);
+
+/* The probabilities that zp_sample draws from: the kept weights over their sum, 0
+ * elsewhere, each rounded once from fp32.  zp_verify_draft takes them as target_probs
+ * and draft_probs.
+ *
+ *  probs         device [R][vocab] of prob_dtype, rows prob_stride elements apart
+ *                (any, >= vocab; what lies between the rows is left as it is) */
+zp_status zp_token_probs(zp_cache *cache, const void *logits, int32_t logit_dtype, int32_t vocab,
+                         int64_t logit_stride, const float *temperature, const int32_t *top_k,
+                         const float *top_p, const float *min_p, int32_t num_rows,
+                         const int32_t *req_idx, int32_t R, void *probs, int32_t prob_dtype,
+                         int64_t prob_stride, void *stream);
 
 /* Redundancy of every key against ALL keys of its (request, layer, kv
  * head): the O(N^2 b^2) score that the Lightning Redundancy Score replaces
