@@ -264,7 +264,9 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
              zp::encode_row_map(&krmaps[l], D.k_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim) &&
              zp::encode_row_map(&vrmaps[l], D.v_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim);
     }
-    ok = ok && zp::prepare_chunk_attn(D.head_dim) == cudaSuccess &&
+    ok = ok &&
+         (fp8 ? zp::prepare_fp8_chunk_attn(D.head_dim) : zp::prepare_chunk_attn(D.head_dim)) ==
+             cudaSuccess &&
          cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
          cudaMemset(b + o_rowmark, 0, 4 * static_cast<size_t>(D.max_requests)) == cudaSuccess &&
          cudaMemset(b + o_ap_call, 0, o_ap_occ - o_ap_call) == cudaSuccess &&
@@ -1054,15 +1056,6 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         return ZP_ERR_INVALID_ARG;
     if (!on_device(c))
         return ZP_ERR_INVALID_ARG;
-    if (c->fp8) {
-        zp::Fp8AttnArgs a = fp8_attn_args(c, layer, q, q_stride, block_tables, bt_stride, num_rows,
-                                          lengths, req_idx, R, scale, out);
-        a.starts = starts;
-        a.total = total;
-        return zp::launch_fp8_decode(a, c->d, static_cast<cudaStream_t>(stream)) == cudaSuccess
-                   ? ZP_OK
-                   : ZP_ERR_CUDA;
-    }
     zp::ChunkAttnArgs a{};
     a.kmap = c->ws.kmaps + layer;
     a.vmap = c->ws.vmaps + layer;
@@ -1089,8 +1082,13 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     a.arrived = c->ws.ca_arrived;
     a.entered = c->ws.ca_entered;
     a.sticky = c->ws.sticky;
-    return zp::launch_chunk_attn(a, c->d, c->num_sms, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
+    if (c->fp8) {
+        a.kscale = c->kscales[layer];
+        a.vscale = c->vscales[layer];
+    }
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return (c->fp8 ? zp::launch_fp8_chunk_attn(a, c->d, c->num_sms, s)
+                   : zp::launch_chunk_attn(a, c->d, c->num_sms, s)) == cudaSuccess
                ? ZP_OK
                : ZP_ERR_CUDA;
 }

@@ -45,6 +45,7 @@ struct ChunkAttnArgs {
     uint32_t *arrived;  // [2][2 * SMs] of them that are written: two sets, used in turn
     uint32_t *entered;  // CTAs that have entered a call, modulo two calls'
     int32_t *sticky;
+    const float *kscale, *vscale;  // of an 8-bit cache, whose pools hold bytes
 };
 
 struct VerifyArgs {

@@ -54,6 +54,9 @@ struct Fp8AttnArgs {
 
 cudaError_t launch_fp8_append(const Fp8KvArgs &a, cudaStream_t s);
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s);
+cudaError_t launch_fp8_chunk_attn(const ChunkAttnArgs &a, int d, int sms, cudaStream_t s);
+// Once a device, before launch_fp8_chunk_attn.
+cudaError_t prepare_fp8_chunk_attn(int d);
 // The swizzled 2D map of an 8-bit pool: a box is one slab, 16 rows of d bytes, with
 // the 128-byte swizzle (the 64-byte one for rows of 64).
 bool encode_fp8_pool_map(CUtensorMap *map, const void *pool, int num_blocks, int hkv, int d);

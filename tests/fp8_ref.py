@@ -138,9 +138,10 @@ class Batch8:
         return (values(p[self.layer], s[self.layer], blocks)[:T]
                 for p, s in ((self.kp, self.ks), (self.vp, self.vs)))
 
-    def check_attn(self, skip=()):
-        """The output against 64 bits, within the bound of `attn_ref`; the rows of no chunk
-        (and of the requests in `skip`) still hold 7."""
+    def check_attn(self, skip=(), split=2.0 ** -17):
+        """The output against 64 bits, within the bound of `attn_ref` (split: of the chunk
+        call; 0 for single tokens); the rows of no chunk (and of the requests in `skip`)
+        still hold 7."""
         seen = torch.zeros(self.total, dtype=torch.bool, device=self.dev)
         worst = 0.0
         for i, (n, T) in enumerate(self.spans):
@@ -148,7 +149,7 @@ class Batch8:
                 continue
             a = int(self.starts_np[i])
             k, v = self.rows_of(i)
-            want, tol = attn_ref(self.q[a:a + n], k, v, self.scale)
+            want, tol = attn_ref(self.q[a:a + n], k, v, self.scale, split)
             err = (self.out[a:a + n].double() - want).abs()
             assert bool((err <= tol).all()), (
                 i, n, T, float((err / tol).nan_to_num(math.inf).max()))
@@ -197,7 +198,7 @@ def values(pool, scale, blocks):
     return x.permute(0, 2, 1, 3).flatten(0, 1)
 
 
-def attn_ref(q, k, v, scale):
+def attn_ref(q, k, v, scale, split=0.0):
     """(out, bound) of one chunk in 64 bits: q [n, Hq, d], k and v [T, Hkv, d] (values).
 
     The bound counts: the result's rounding to bf16 (half a step, 2^-8 of the value);
@@ -207,7 +208,9 @@ def attn_ref(q, k, v, scale):
     sum of d products (d + 2 roundings of 2^-23 -- the matrix unit may truncate -- of scale
     |q| . |k|), times the two scales (4 more) and plus log2 of V's scale, of at
     most 32 (a rounding of 2^-23 of both), which enters a probability and the sum it is
-    divided by (twice); and 2^-11 of sum p |v| for the exponential (2^-22), the T-term
+    divided by (twice); with `split` (2^-17: q as two e4m3 numbers, whose steps of 2^-9
+    leave half a step of error where the largest element is above 2^7) that part of the
+    largest |q| times the sum of |k| in the logit; and 2^-11 of sum p |v| for the exponential (2^-22), the T-term
     fp32 sums and the joining of partial results."""
     n, Hq, d = q.shape
     T, Hkv, _ = k.shape
@@ -222,7 +225,8 @@ def attn_ref(q, k, v, scale):
         mag = (q[:, hq].abs() @ k[:, h].abs().T) * abs(scale)
         p = torch.softmax(s.masked_fill(hidden, -math.inf), 1)
         mag = mag.masked_fill(hidden, 0).amax(1, keepdim=True)
-        spread = 2 * ((d + 7) * 2.0 ** -23 * mag + 33 * 2.0 ** -23)
+        lost = split * abs(scale) * q[:, hq].abs().amax(1, keepdim=True) * k[:, h].abs().sum(1).max()
+        spread = 2 * ((d + 7) * 2.0 ** -23 * mag + 33 * 2.0 ** -23 + lost)
         out[:, hq] = p @ v[:, h]
         pv = p @ v[:, h].abs()
         # the largest weight of a number in the product, a row's

@@ -132,7 +132,7 @@ def test_decode(d, Hkv, Hq):
     c = b.cache()
     b.decode(c)
     assert c.status() == zp.OK
-    b.check_attn()
+    b.check_attn(split=0.0)
 
 
 @pytest.mark.parametrize("T", [1, 40, 333, 5000, 30001])
@@ -142,7 +142,7 @@ def test_decode_one_request(T):
     c = b.cache()
     b.decode(c)
     assert c.status() == zp.OK
-    b.check_attn()
+    b.check_attn(split=0.0)
 
 
 def test_decode_zero_length_and_bad_rows():
@@ -153,7 +153,7 @@ def test_decode_zero_length_and_bad_rows():
     assert c.status() == zp.OK
     assert bool((b.out[1] == 0).all())
     b.out[1] = 7.0
-    b.check_attn(skip=(1,))
+    b.check_attn(skip=(1,), split=0.0)
     b.lengths[1] = 10_000
     b.decode(c)
     assert c.status() == zp.ERR_DEVICE_CHECK
