@@ -106,6 +106,7 @@ constexpr float kAbove = kRescale + 30.f;  // of what p is taken against, over t
 constexpr float kRescale8 = 10.f;
 constexpr float kAbove8 = -5.f;
 constexpr int kScales = 16;            // key tiles whose scales are kept
+constexpr int kQTiles = 2 * kDescs;    // query tiles whose rows' factors are kept
 
 // What every CTA works out at its start.
 struct CaPlan {
@@ -149,8 +150,8 @@ struct CaSmem {
     static constexpr int off_v = off_k + NK * KTILE;
     static constexpr int off_raw = off_v + NV * TILE;
     static constexpr int off_scale = off_raw + NR * TILE8;  // float4 [kScales][8]: of key tiles
-    static constexpr int off_qf = off_scale + (F8 ? kScales * 8 * 16 : 0);  // float [128]: of Q's rows
-    static constexpr int off_max = off_qf + (F8 ? 2 * kTile * 4 : 0);  // float [2][2][128]: maxima of row halves
+    static constexpr int off_qf = off_scale + (F8 ? kScales * 8 * 16 : 0);  // float [kQTiles][128]: of Q's rows
+    static constexpr int off_max = off_qf + (F8 ? kQTiles * kTile * 4 : 0);  // float [2][2][128]: maxima of row halves
     static constexpr int off_desc = off_max + 4 * kTile * 4;  // CaDesc [kDescs]
     static constexpr int off_plan = off_desc + kDescs * static_cast<int>(sizeof(CaDesc));
     static constexpr int off_scan = off_plan + static_cast<int>(sizeof(CaPlan));  // int64 [warps]
@@ -639,42 +640,93 @@ __device__ __forceinline__ float *slot_ptr(float *part, int slot)
     return part + static_cast<size_t>(slot) * (2 * kTile * (D + 2));
 }
 
+// Rows 16 part .. + 15 of a tile of 8-bit V, as its map leaves it at `from`, to fp16 in
+// the layout of a bf16 tile at `to`, by one warp.  Rows from `first` on are tidied: to 0, or
+// with `clean` their NaN to 0.  All chunks of 16 bytes are on their way at once; each
+// becomes two.  The lanes of a 16-byte access (eight at a time) lie in different banks
+// on both sides: with 128 dims they are four chunks of rows r and r ^ 5, whose
+// swizzles differ in the bit that parts the loads' chunks and in the one that parts the
+// stores'; with 64 dims two whole rows.
+template <int D>
+__device__ __forceinline__ void convert_v(uint32_t from, uint32_t to, int part, int lane,
+                                          int first, bool clean)
+{
+    constexpr int STEPS = kTile * D / 16 / (32 * kSmWarps);
+    const int ch = D == 128 ? (lane & 3) | (lane >> 3 & 1) << 2 : lane & 3;
+    // the rows of step i: row[i & 1] + 8 * (i / 2), or row[0] + 8 i
+    int row[2];
+    uint32_t src[2], dst[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        row[k] = kTile / kSmWarps * part +
+                 (D == 128 ? (k << 1 | lane >> 4) ^ ((lane >> 2 & 1) * 5) : lane >> 2);
+        src[k] = from + swz8<D>(row[k], ch);
+        dst[k] = to + swz(row[k], 2 * ch, kTile);
+    }
+    uint4 v[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        v[i] = ld_shared_v4(src[D == 128 ? i & 1 : 0] + (D == 128 ? i / 2 * 1024 : i * 512));
+    if (first < kTile) {  // the whole warp alike
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+            if ((D == 128 ? row[i & 1] + 8 * (i / 2) : row[0] + 8 * i) >= first)
+                v[i] = clean ? make_uint4(numbers4(v[i].x), numbers4(v[i].y), numbers4(v[i].z),
+                                          numbers4(v[i].w))
+                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const uint32_t at = dst[D == 128 ? i & 1 : 0] + (D == 128 ? i / 2 : i) * 1024;
+        st_shared_v4(at, make_uint4(f16x2_of_e4m3(v[i].x), f16x2_of_e4m3(v[i].x >> 16),
+                                    f16x2_of_e4m3(v[i].y), f16x2_of_e4m3(v[i].y >> 16)));
+        st_shared_v4(at ^ 16, make_uint4(f16x2_of_e4m3(v[i].z), f16x2_of_e4m3(v[i].z >> 16),
+                                         f16x2_of_e4m3(v[i].w), f16x2_of_e4m3(v[i].w >> 16)));
+    }
+}
+
 // Q of an 8-bit cache's chunk: row r of the tile at `tile`, bf16 as its map leaves it, becomes
 // two rows of e4m3 numbers, f q = upper + lower, `upper` in place of the tile's first
 // half and `lower` in its second.  The power of two f takes the row's largest element
 // into (224, 448]; four bits of mantissa and then four more hold the eight of a bf16
 // number exactly down to a 2^-10 of that, and below it the error stays under a 2^-17 of
-// the largest.  A row is two threads', which hold half of its dims each.  Returns what a
-// logit of the row is multiplied by, scale / f (NaN for a row that is not finite).  A
-// negative scale goes into the numbers.  All of a stream's warps call it.
+// the largest.  factor[r] becomes what a logit of the row is multiplied by, scale / f (NaN
+// for a row that is not finite); a negative scale goes into the numbers.  By a stream's
+// 256 threads, ct the number of one, two neighbours a row.
 template <int D>
-__device__ __forceinline__ float split_q(uint32_t tile, int r, int hf, uint32_t max_at,
-                                         uint32_t other_at, uint32_t pair_bar, uint32_t tile_bar,
-                                         bool mine, float logit_scale)
+__device__ __forceinline__ void split_q(uint32_t tile, int ct, int rows, float logit_scale,
+                                        float *factor, uint32_t bar)
 {
-    constexpr int CH = D / 16;  // 16-byte chunks of bf16 that the thread holds
+    constexpr int CH = D / 16;     // 16-byte chunks of bf16 a thread
+    constexpr int LO = kTile * D;  // from `upper` to `lower`
+    const int r = ct >> 1, hf = ct & 1;
+    const bool any = (r & ~15) < rows;  // of the warp's 16 rows
     uint4 v[CH];
     uint32_t most = 0;
+    // (with 128 dims in another order in the second half, for the banks' sake)
+    const int flip = D == 128 ? hf * 4 : 0;
+    if (any) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        v[c] = mine ? ld_shared_v4(tile + swz(r, hf * CH + c, kTile)) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        for (int c = 0; c < CH; ++c) {
+            v[c] = ld_shared_v4(tile + swz(r, hf * CH + (c ^ flip), kTile));
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+            for (int e = 0; e < 4; ++e)
+                most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+        }
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
     }
-    st_shared_f32(max_at, __uint_as_float(most));
-    if (D == 64)
-        bar_sync(tile_bar, 32 * kSmWarps);  // rows move: all are read before any is written
+    if (D == 64)  // rows move: all are read before one is written
+        bar_sync(bar, 32 * kSmWarps);
     else
-        bar_sync(pair_bar, 64);
-    most = max(most, __float_as_uint(ld_shared_f32(other_at)));
+        __syncwarp();
+    if (!any)
+        return;
     // f = 2^e; two factors, as it may not be an fp32 number
     const int e = 8 - (static_cast<int>(most >> 23) - 127) - ((most & 0x7fffffu) > 0x600000u);
     const int e1 = max(min(e, 100), -100), e2 = e - e1;
     const float f1 = __uint_as_float(exp2_bits(e1) | (__float_as_uint(logit_scale) & 0x80000000u));
     const float f2 = __uint_as_float(exp2_bits(e2));
-    constexpr int LO = kTile * D;  // from `upper` to `lower`
 #pragma unroll
     for (int c = 0; c < CH; c += 2) {
         uint32_t up[4], lo[4];
@@ -697,16 +749,15 @@ __device__ __forceinline__ float split_q(uint32_t tile, int r, int hf, uint32_t 
             lo[2 * k] = l8[0] | l8[1] << 16;
             lo[2 * k + 1] = l8[2] | l8[3] << 16;
         }
-        if (mine) {
-            const uint32_t at = tile + swz8<D>(r, (hf * CH + c) / 2);
-            st_shared_v4(at, make_uint4(up[0], up[1], up[2], up[3]));
-            st_shared_v4(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-        }
+        const uint32_t at = tile + swz8<D>(r, (hf * CH + (c ^ flip)) / 2);
+        st_shared_v4(at, make_uint4(up[0], up[1], up[2], up[3]));
+        st_shared_v4(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
     const float back = fabsf(logit_scale) * __uint_as_float(exp2_bits(-e1)) *
                        __uint_as_float(exp2_bits(-e2));
-    // (above 0, for scores of -infinity)
-    return most < 0x7f800000u ? fmaxf(back, __uint_as_float(0x00800000u)) : INFINITY - INFINITY;
+    if (hf == 0)  // (above 0, for scores of -infinity)
+        factor[r] =
+            most < 0x7f800000u ? fmaxf(back, __uint_as_float(0x00800000u)) : INFINITY - INFINITY;
 }
 
 }  // namespace
@@ -749,7 +800,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             mbar_init(&kempty[s], 2);  // both products' warps have passed it
         }
         for (int s = 0; s < NV; ++s) {
-            mbar_init(&vfull[s], 1);
+            mbar_init(&vfull[s], F8 ? kSmWarps : 1);
             mbar_init(&vempty[s], 2);
         }
         for (int x = 0; x < 2; ++x) {
@@ -765,7 +816,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
         for (int s = 0; s < NR; ++s) {
             mbar_init(&rfull[s], 1);
-            mbar_init(&rempty[s], 1);
+            mbar_init(&rempty[s], kSmWarps);
         }
         for (int s = 0; s < kDescs; ++s) {
             mbar_init(&described[s], 1);
@@ -953,7 +1004,6 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         if (wi == kLoadWarp) {
             // ------------------------------------------- the items, Q and K
             uint32_t loaded = 0, cur = 0, par = 0, qs = 0;  // ring cursor and parity, query tiles
-            [[maybe_unused]] uint32_t raw = 0, rcur = 0, rpar = 0;  // of 8-bit V's ring
             auto load_q = [&](const CaDesc &d, int tiles) {
                 for (int x = 0; x < tiles; ++x, ++qs) {
                     const int k = qs & 1;
@@ -1050,26 +1100,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             par ^= 1;
                         }
                         // Q behind the first K tile, which does not wait for the item before
-                        if (t == 0 && !q_early)
+                        if (t > 0)
+                            continue;
+                        if (!q_early)
                             load_q(d, tiles);
                         if (bad)
                             break;
-                        if constexpr (F8) {  // V's tile behind K's
-                            if (raw >= NR && !warp_wait(&rempty[rcur], rpar ^ 1)) {
-                                bad = true;
-                                break;
-                            }
-                            load_tile(a.vmap, sm + S::off_raw + rcur * S::TILE8, &rfull[rcur], ids,
-                                      t);
-                            if (elect_one())
-                                mbar_arrive(&rfull[rcur]);
-                            __syncwarp();
-                            ++raw;
-                            if (++rcur == NR) {
-                                rcur = 0;
-                                rpar ^= 1;
-                            }
-                        }
                     }
                 }
                 // every copy issued has landed before the CTA may exit
@@ -1077,78 +1113,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     bad |= !warp_wait(&qfull[k & 1], (k >> 1) & 1);
                 for (uint32_t k = loaded > NK ? loaded - NK : 0; k < loaded; ++k)
                     bad |= !warp_wait(&kfull[k % NK], (k / NK) & 1);
-                if constexpr (F8)
-                    for (uint32_t k = raw > NR ? raw - NR : 0; k < raw; ++k)
-                        bad |= !warp_wait(&rfull[k % NR], (k / NR) & 1);
                 if (!walk_again(clean))
                     break;
             }
         } else if (wi == kLoadVWarp) {
             // ------------------------------------------------------------- V
             uint32_t loaded = 0, cur = 0, par = 0;
-            [[maybe_unused]] uint32_t rcur = 0, rpar = 0;
+            constexpr uint32_t N = F8 ? NR : NV;  // 8-bit tiles go into a ring of their own
+            uint64_t *full = F8 ? rfull : vfull, *empty = F8 ? rempty : vempty;
             for (;;) {
-                if constexpr (F8) {
-                    // 8-bit V tiles, which the other loader brings, to fp16
-                    while (const CaDesc *dp = bad ? nullptr : enter()) {
-                        const int ka = dp->ka, kb = dp->kb;
-                        // the key from which on rows are tidied: past the length all of them
-                        // are 0, in the second walk NaN counts as 0
-                        const bool clean = dp->clean != 0;
-                        const int tidy = clean ? dp->pos0 + 1 : dp->len;
-                        leave();
-                        for (int t = ka; t < kb; ++t) {
-                            if (!warp_wait(&rfull[rcur], rpar) ||
-                                (loaded >= NV && !warp_wait(&vempty[cur], par ^ 1))) {
-                                bad = true;
-                                break;
-                            }
-                            const uint32_t from = smem_u32(sm + S::off_raw + rcur * S::TILE8);
-                            const uint32_t to = smem_u32(sV + cur * S::TILE);
-                            const int first = tidy - t * kTile;  // the tile's first tidied row
-                            constexpr int CPR = D / 16;  // 16-byte chunks of an 8-bit row
-#pragma unroll 4
-                            for (int c = lane; c < kTile * CPR; c += 32) {
-                                const int row = c / CPR, ch = c % CPR;
-                                uint4 v = ld_shared_v4(from + swz8<D>(row, ch));
-                                if (row >= first)
-                                    v = clean ? make_uint4(numbers4(v.x), numbers4(v.y),
-                                                           numbers4(v.z), numbers4(v.w))
-                                              : make_uint4(0u, 0u, 0u, 0u);
-                                st_shared_v4(to + swz(row, 2 * ch, kTile),
-                                             make_uint4(f16x2_of_e4m3(v.x),
-                                                        f16x2_of_e4m3(v.x >> 16),
-                                                        f16x2_of_e4m3(v.y),
-                                                        f16x2_of_e4m3(v.y >> 16)));
-                                st_shared_v4(to + swz(row, 2 * ch + 1, kTile),
-                                             make_uint4(f16x2_of_e4m3(v.z),
-                                                        f16x2_of_e4m3(v.z >> 16),
-                                                        f16x2_of_e4m3(v.w),
-                                                        f16x2_of_e4m3(v.w >> 16)));
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (elect_one()) {
-                                mbar_arrive(&vfull[cur]);
-                                mbar_arrive(&rempty[rcur]);
-                            }
-                            __syncwarp();
-                            ++loaded;
-                            if (++cur == NV) {
-                                cur = 0;
-                                par ^= 1;
-                            }
-                            if (++rcur == NR) {
-                                rcur = 0;
-                                rpar ^= 1;
-                            }
-                        }
-                    }
-                    if (!walk_again(ended_clean()))
-                        break;
-                    leave();
-                    continue;
-                }
                 while (const CaDesc *dp = bad ? nullptr : enter()) {
                     const CaDesc d = *dp;
                     leave();
@@ -1160,20 +1133,27 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             ids = ids_next;
                             ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
                         }
-                        if (loaded >= NV && !warp_wait(&vempty[cur], par ^ 1)) {
+                        if (loaded >= N && !warp_wait(&empty[cur], par ^ 1)) {
                             bad = true;
                             break;
                         }
-                        load_tile(a.vmap, sV + cur * S::TILE, &vfull[cur], ids, t);
+                        load_tile(a.vmap,
+                                  F8 ? sm + S::off_raw + cur * S::TILE8 : sV + cur * S::TILE,
+                                  &full[cur], ids, t);
+                        if constexpr (F8) {
+                            if (elect_one())
+                                mbar_arrive(&full[cur]);
+                            __syncwarp();
+                        }
                         ++loaded;
-                        if (++cur == NV) {
+                        if (++cur == N) {
                             cur = 0;
                             par ^= 1;
                         }
                     }
                 }
-                for (uint32_t k = loaded > NV ? loaded - NV : 0; k < loaded; ++k)
-                    bad |= !warp_wait(&vfull[k % NV], (k / NV) & 1);
+                for (uint32_t k = loaded > N ? loaded - N : 0; k < loaded; ++k)
+                    bad |= !warp_wait(&full[k % N], (k / N) & 1);
                 if (!walk_again(ended_clean()))
                     break;
                 leave();
@@ -1450,8 +1430,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 int cnt = single ? (len + 1 - x) / 2 : len;            // key tiles
                 if (!single && x == 0)
                     cnt = max(0, min(dp->kb, (pos0 + tpt + kTile - 1) / kTile) - dp->ka);
-                // A has taken what B left in place of its maxima
-                if (lent && (cnt > 0 || (F8 && !single))) {
+                if (lent && cnt > 0) {  // A has taken what B left in place of its maxima
                     if (!bad && !ca_wait(taken, halves++ & 1))
                         bad = true;
                     bad = __any_sync(0xffffffffu, bad);
@@ -1460,28 +1439,56 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 // keys the thread's half of the next tile still holds for the row: fewer
                 // than all for any row of the warp, and the tile is masked
                 [[maybe_unused]] float lr = 0.f;  // F8: what a logit is multiplied by but for K's scale
+                [[maybe_unused]] const uint32_t qt = single ? qs : qs + x;
                 if constexpr (F8) {
-                    if (!single || x == 0) {
-                        const uint32_t slot = single ? qs : qs + x;
-                        if (!bad && !ca_wait(&qfull[slot & 1], (slot >> 1) & 1))
+                    // Q: a pair's tiles by their streams, a single one by B, for which A's
+                    // epilogue has no work
+                    if (!single || x == 1) {
+                        const int k = qt & 1;
+                        if (!bad && !ca_wait(&qfull[k], (qt >> 1) & 1))
                             bad = true;
-                        lr = split_q<D>(smem_u32(sQ) + (slot & 1) * S::TILE, r, hf, max_at,
-                                        max_at ^ kOther, pair_bar, 9 + x, r < toks * G,
-                                        a.logit_scale);
-                        if (single && hf == 0)
-                            sQf[r] = lr;
+                        split_q<D>(smem_u32(sQ) + k * S::TILE, tid & (32 * kSmWarps - 1),
+                                   (single ? dp->ntok : toks) * G, a.logit_scale,
+                                   sQf + qt % kQTiles * kTile, 9 + x);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(&qready[slot & 1]);
+                            mbar_arrive(&qready[k]);
                     }
                     qs += single ? 1 : 2;
                 }
+                // F8: V's tile t of the item to fp16, by this stream's warps
+                [[maybe_unused]] auto to_fp16 = [&](int t) {
+                    constexpr uint32_t N = F8 ? NR : 1;
+                    const uint32_t k = tiles + t, st = k % NV, rs = k % N;
+                    if (!bad && (!ca_wait(&rfull[rs], (k / N) & 1) ||
+                                 (k >= NV && !ca_wait(&vempty[st], (k / NV - 1) & 1))))
+                        bad = true;
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (bad)
+                        return;
+                    // the key from which on rows are tidied: past the length all of them are 0,
+                    // in the second walk NaN counts as 0
+                    const int tidy = dp->clean ? dp->pos0 + 1 : dp->len;
+                    convert_v<D>(smem_u32(sm + S::off_raw + rs * S::TILE8),
+                                 smem_u32(sV + st * S::TILE), wi & (kSmWarps - 1), lane,
+                                 tidy - (dp->ka + t) * kTile, dp->clean != 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&vfull[st]);
+                        mbar_arrive(&rempty[rs]);
+                    }
+                };
                 int m_lim = lim - (dp->ka + (single ? x : 0)) * kTile - hf * HK;
                 const int m_step = single ? 2 * kTile : kTile;
                 float mref = -INFINITY, negm = 0.f;
                 float l0 = 0.f, l1 = 0.f;
                 for (int t = cnt; t > 0; --t, m_lim -= m_step) {
+                    // (a pair's tiles are all A's, which is ahead of B)
+                    if constexpr (F8)
+                        if (single || x == 0)
+                            to_fp16(single ? x + 2 * (cnt - t) : cnt - t);
                     if (!bad && !ca_wait(&sfull[x], ns & 1))
                         bad = true;
                     ++ns;
@@ -1510,8 +1517,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             scales_at + (((tiles + (single ? x + 2 * (cnt - t) : cnt - t)) %
                                           kScales) * 8 + hf * 4) * 16;
                         if constexpr (F8) {
-                            if (single && x == 1 && t == cnt)
-                                lr = sQf[r];
+                            if (t == cnt)
+                                lr = sQf[qt % kQTiles * kTile + r];
                             m_new = -INFINITY;
 #pragma unroll
                             for (int b = 0; b < HK; b += kBlk) {
@@ -1610,8 +1617,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         mbar_arrive(&pready[x]);
                 }
                 // ----------------------------------------------------- epilogue
-                if constexpr (F8)
+                if constexpr (F8) {
+                    if (!single && x == 0)  // the tiles that B alone sees
+                        for (int t = cnt; t < len; ++t)
+                            to_fp16(t);
                     tiles += len;
+                }
                 const CaDesc &d = *dp;
                 // (what follows from G stays out of the key loop's registers)
                 int G = a.Hq / a.Hkv;
