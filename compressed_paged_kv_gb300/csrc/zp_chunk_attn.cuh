@@ -142,11 +142,13 @@ struct CaSmem {
     static constexpr int TILE8 = kTile * D;              // of 8-bit ones
     static constexpr int KTILE = F8 ? TILE8 : TILE;
     // stages of K, of V and of 8-bit V
-    static constexpr int NK = D == 128 ? (F8 ? 3 : 2) : 5, NV = D == 128 ? (F8 ? 2 : 3) : 5;
+    static constexpr int NK = D == 128 ? (F8 ? 3 : 2) : 5, NV = D == 128 ? (F8 ? 2 : 3) : F8 ? 4 : 5;
     static constexpr int NR = F8 ? (D == 128 ? 2 : 4) : 0;
     static constexpr int XC = 16;  // columns of O a step of the epilogue
     static constexpr int off_q = 0;                      // Q of A, Q of B
-    static constexpr int off_k = off_q + 2 * TILE;
+    // with 64 dims a row's numbers lie elsewhere than the row did: two more tiles for them
+    static constexpr bool SPLIT = F8 && D == 64;
+    static constexpr int off_k = off_q + (SPLIT ? 4 : 2) * TILE;
     static constexpr int off_v = off_k + NK * KTILE;
     static constexpr int off_raw = off_v + NV * TILE;
     static constexpr int off_scale = off_raw + NR * TILE8;  // float4 [kScales][8]: of key tiles
@@ -526,6 +528,20 @@ __device__ __forceinline__ bool ca_wait(uint64_t *bar, uint32_t parity)
     return false;
 }
 
+// Whether the phase is over, without a wait; a converged warp's.
+__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, done);
+}
+
 // A converged warp's wait.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
@@ -685,43 +701,38 @@ __device__ __forceinline__ void convert_v(uint32_t from, uint32_t to, int part, 
     }
 }
 
-// Q of an 8-bit cache's chunk: row r of the tile at `tile`, bf16 as its map leaves it, becomes
-// two rows of e4m3 numbers, f q = upper + lower, `upper` in place of the tile's first
-// half and `lower` in its second.  The power of two f takes the row's largest element
+// Q of an 8-bit cache's chunk: row r of the tile at `from`, bf16 as its map leaves it, becomes
+// two rows of e4m3 numbers, f q = upper + lower, `upper` in the first half of the tile at
+// `to` and `lower` in its second (with 128 dims the same tile, where a row's numbers lie
+// where the row did).  The power of two f takes the row's largest element
 // into (224, 448]; four bits of mantissa and then four more hold the eight of a bf16
 // number exactly down to a 2^-10 of that, and below it the error stays under a 2^-17 of
 // the largest.  factor[r] becomes what a logit of the row is multiplied by, scale / f (NaN
 // for a row that is not finite); a negative scale goes into the numbers.  By a stream's
 // 256 threads, ct the number of one, two neighbours a row.
 template <int D>
-__device__ __forceinline__ void split_q(uint32_t tile, int ct, int rows, float logit_scale,
-                                        float *factor, uint32_t bar)
+__device__ __forceinline__ void split_q(uint32_t from, uint32_t to, int ct, int rows,
+                                        float logit_scale, float *factor)
 {
     constexpr int CH = D / 16;     // 16-byte chunks of bf16 a thread
     constexpr int LO = kTile * D;  // from `upper` to `lower`
     const int r = ct >> 1, hf = ct & 1;
-    const bool any = (r & ~15) < rows;  // of the warp's 16 rows
+    if ((r & ~15) >= rows)  // none of the warp's 16 rows
+        return;
     uint4 v[CH];
     uint32_t most = 0;
     // (with 128 dims in another order in the second half, for the banks' sake)
     const int flip = D == 128 ? hf * 4 : 0;
-    if (any) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            v[c] = ld_shared_v4(tile + swz(r, hf * CH + (c ^ flip), kTile));
-            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+    for (int c = 0; c < CH; ++c) {
+        v[c] = ld_shared_v4(from + swz(r, hf * CH + (c ^ flip), kTile));
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
-        }
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        for (int e = 0; e < 4; ++e)
+            most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
     }
-    if (D == 64)  // rows move: all are read before one is written
-        bar_sync(bar, 32 * kSmWarps);
-    else
-        __syncwarp();
-    if (!any)
-        return;
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    __syncwarp();  // the row is read
     // f = 2^e; two factors, as it may not be an fp32 number
     const int e = 8 - (static_cast<int>(most >> 23) - 127) - ((most & 0x7fffffu) > 0x600000u);
     const int e1 = max(min(e, 100), -100), e2 = e - e1;
@@ -749,7 +760,7 @@ __device__ __forceinline__ void split_q(uint32_t tile, int ct, int rows, float l
             lo[2 * k] = l8[0] | l8[1] << 16;
             lo[2 * k + 1] = l8[2] | l8[3] << 16;
         }
-        const uint32_t at = tile + swz8<D>(r, (hf * CH + (c ^ flip)) / 2);
+        const uint32_t at = to + swz8<D>(r, (hf * CH + (c ^ flip)) / 2);
         st_shared_v4(at, make_uint4(up[0], up[1], up[2], up[3]));
         st_shared_v4(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
@@ -1174,7 +1185,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             constexpr uint32_t ID_O = ca_idesc(D, true, F8);
             constexpr uint32_t STEP = S::TILE >> 4, KSTEP = S::KTILE >> 4;
             const int x = wi - kMmaWarp;
-            const uint32_t qdesc = desc_lo(smem_u32(sQ), 16), kdesc = desc_lo(smem_u32(sK), 16);
+            const uint32_t qdesc = desc_lo(smem_u32(sQ) + (S::SPLIT ? 2 * S::TILE : 0), 16), kdesc = desc_lo(smem_u32(sK), 16);
             const uint32_t vdesc = desc_lo(smem_u32(sV), S::PANEL);
             const uint32_t tS = tmem + x * kTile, tO = tmem + 256 + x * kTile;
             uint32_t kc = 0, kpar = 0, vc = 0, vpar = 0;  // ring cursors and parities
@@ -1417,7 +1428,27 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         const float ls = fmaxf(fabsf(a.logit_scale), __uint_as_float(1u));
         uint32_t ns = 0, no = 0, halves = 0;
         [[maybe_unused]] uint32_t qs = 0, tiles = 0;  // F8: query tiles and key tiles so far
+        [[maybe_unused]] bool ahead = false;          // F8: the item's Q is split already
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
+        // F8: the item's Q to e4m3, before any of its S: a pair's tiles by their streams, a
+        // single one by B, for which A's epilogue has no work
+        [[maybe_unused]] auto split = [&](const CaDesc &d) {
+            const bool single = d.ntok <= tpt;
+            if (single && x == 0)
+                return;
+            const uint32_t t = single ? qs : qs + x, k = t & 1;
+            if (!bad && !ca_wait(&qfull[k], (t >> 1) & 1))
+                bad = true;
+            bad = __any_sync(0xffffffffu, bad);
+            const int toks = min(single || x == 0 ? d.ntok : d.ntok - tpt, tpt);
+            split_q<D>(smem_u32(sQ) + k * S::TILE, smem_u32(sQ) + (S::SPLIT ? 2 + k : k) * S::TILE,
+                       tid & (32 * kSmWarps - 1), toks * G, a.logit_scale,
+                       sQf + t % kQTiles * kTile);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&qready[k]);
+        };
         for (;;) {
             while (const CaDesc *dp = enter()) {
                 const bool single = dp->ntok <= tpt;
@@ -1441,23 +1472,12 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 [[maybe_unused]] float lr = 0.f;  // F8: what a logit is multiplied by but for K's scale
                 [[maybe_unused]] const uint32_t qt = single ? qs : qs + x;
                 if constexpr (F8) {
-                    // Q: a pair's tiles by their streams, a single one by B, for which A's
-                    // epilogue has no work
-                    if (!single || x == 1) {
-                        const int k = qt & 1;
-                        if (!bad && !ca_wait(&qfull[k], (qt >> 1) & 1))
-                            bad = true;
-                        split_q<D>(smem_u32(sQ) + k * S::TILE, tid & (32 * kSmWarps - 1),
-                                   (single ? dp->ntok : toks) * G, a.logit_scale,
-                                   sQf + qt % kQTiles * kTile, 9 + x);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&qready[k]);
-                    }
+                    if (!ahead)
+                        split(*dp);
                     qs += single ? 1 : 2;
                 }
-                // F8: V's tile t of the item to fp16, by this stream's warps
+                // F8: V's tile t of the item to fp16, by this stream's warps: a pair's are all
+                // A's, which is ahead of B; a single item's the stream's that uses them
                 [[maybe_unused]] auto to_fp16 = [&](int t) {
                     constexpr uint32_t N = F8 ? NR : 1;
                     const uint32_t k = tiles + t, st = k % NV, rs = k % N;
@@ -1476,8 +1496,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(&vfull[st]);
                         mbar_arrive(&rempty[rs]);
+                        mbar_arrive(&vfull[st]);
                     }
                 };
                 int m_lim = lim - (dp->ka + (single ? x : 0)) * kTile - hf * HK;
@@ -1485,10 +1505,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 float mref = -INFINITY, negm = 0.f;
                 float l0 = 0.f, l1 = 0.f;
                 for (int t = cnt; t > 0; --t, m_lim -= m_step) {
-                    // (a pair's tiles are all A's, which is ahead of B)
-                    if constexpr (F8)
+                    if constexpr (F8) {
                         if (single || x == 0)
                             to_fp16(single ? x + 2 * (cnt - t) : cnt - t);
+                    }
                     if (!bad && !ca_wait(&sfull[x], ns & 1))
                         bad = true;
                     ++ns;
@@ -1622,6 +1642,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         for (int t = cnt; t < len; ++t)
                             to_fp16(t);
                     tiles += len;
+                    // a next pair's Q if it is there, so that its S comes during the epilogue
+                    // (16 prompts of 64 dims 802 -> 770 us; with a single item's, whose B
+                    // A's epilogue waits for, 256 speculative chunks take 381 us, not 350)
+                    const uint32_t j = (nd + 1) % kDescs;
+                    ahead = warp_test(&described[j], ((nd + 1) / kDescs) & 1) &&
+                            sDesc[j].ntok > tpt && warp_test(&qfull[(qs + x) & 1], ((qs + x) >> 1) & 1);
+                    if (ahead)
+                        split(sDesc[j]);
                 }
                 const CaDesc &d = *dp;
                 // (what follows from G stays out of the key loop's registers)
