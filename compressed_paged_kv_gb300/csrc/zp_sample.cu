@@ -9,14 +9,20 @@
 // lowest kept index whose running sum exceeds u times the sum of all kept.
 //
 // Weights are whole numbers of 2^-44 (zp_sample.cuh), so every sum is exact and the same
-// in whatever order it is formed.
+// in whatever order it is formed.  Only where a sum decides nothing (the probabilities
+// of a row without top_p) are they plain fp32 numbers.
 //
 // One cluster of CTAs a row, which lies in their shared memory: it is read from memory
-// once.  A thread owns a contiguous run of it, so that the threads' sums, scanned, say
-// whose run a level falls into.  tau is found by a histogram over the gap to the maximum
-// (counts, and weights where a sum is asked for): the bucket in which the count or the
-// sum is reached is gathered and sorted; one of more than kList entries is cut up again by
-// the bits of its values, until it fits or holds one value alone.
+// once.  A warp owns a contiguous run of it, its lanes 16 bytes each side by side.  tau is
+// found in one of two ways:
+//   top_k of at most kList / 2: the k-th largest of the threads' maxima is a bound below
+//       which none of the k largest lies, and few others lie above it.  What does is gathered
+//       and sorted by CTA 0, which then has all that may be kept, and finds the cuts and
+//       the token by itself.
+//   else: a histogram over the gap to the maximum (counts, or weights where a sum is
+//       asked for).  The bucket in which the count or the sum is reached is gathered and
+//       sorted; one of more than kList entries is cut up again by the bits of its
+//       values, until it fits or holds one value alone.
 #include "zp_sample.cuh"
 
 namespace zp {
@@ -25,7 +31,7 @@ namespace {
 
 constexpr int kSpThreads = 512;
 constexpr int kSpCtas = 8;       // of a cluster, at most: the portable most
-constexpr int kBuckets = 2048;
+constexpr int kBuckets = 1024;
 constexpr int kList = 1024;
 constexpr int kSpWarps = kSpThreads / 32;
 
@@ -37,27 +43,54 @@ struct Cut {
     uint32_t above;   // entries above the bucket
     uint32_t in;      // and in it; at the end, those equal to tau
     uint32_t lo, hi;  // the keys of a cut bucket
-    int bucket;       // of the first histogram
+    int bucket;
     int m;            // of those equal to tau, the ones kept
     float tau;
+    int done;         // nothing is left to do for the other CTAs
 };
 
 struct SpShared {
-    uint64_t bar;
-    uint64_t mass[kBuckets];
+    uint64_t bar[kSpWarps];
     uint64_t list[kList];
     uint64_t table[1024];
     uint32_t count[kBuckets];
-    uint64_t sums[kSpCtas];      // of the CTAs
-    uint64_t scan64[kSpWarps + 1];
-    float2 ends[kSpCtas];        // the CTAs' (largest, smallest finite)
-    uint32_t scan32[kSpWarps + 1];
-    uint32_t ties[kSpCtas];
+    uint32_t low[kBuckets], high[kBuckets];  // sums of weights, in two halves
+    uint64_t runs[kSpCtas * kSpWarps];       // sums of the warps' runs
+    uint32_t ties[kSpCtas * kSpWarps];       // their entries equal to tau
+    uint64_t scan64[kSpWarps];
+    float2 ends[kSpCtas];                    // the CTAs' (largest, smallest finite)
+    uint32_t scan32[kSpWarps];
     uint32_t key_lo, key_hi, listed, equal, equal_upto;
     Cut cut;      // CTA 0's
     Cut told[2];  // what it told all, the last two times
 };
 
+__device__ __forceinline__ void unpack(const uint4 &u, float (&v)[4])
+{
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack(const uint4 &u, float (&v)[8])
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4])
+{
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8])
+{
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+}
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
@@ -94,6 +127,13 @@ __device__ __forceinline__ void max_dsmem_u32(uint32_t addr, uint32_t v)
     asm volatile("red.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ uint32_t ld_dsmem_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // The cluster's barrier, for warps that come out of loops their lanes leave one by one.
 __device__ __forceinline__ void all_ctas()
 {
@@ -113,6 +153,15 @@ __device__ __forceinline__ T warp_incl(T v, int lane)
     return v;
 }
 
+template <class T>
+__device__ __forceinline__ T warp_sum(T v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // The sum of the threads before this one; `total`: of all.
 template <class T>
 __device__ __forceinline__ T block_before(T v, T *scratch, T &total)
@@ -127,6 +176,29 @@ __device__ __forceinline__ T block_before(T v, T *scratch, T &total)
     const T wincl = warp_incl(w, lane);
     total = __shfl_sync(0xffffffffu, wincl, kSpWarps - 1);
     return __shfl_sync(0xffffffffu, wincl - w, wi) + incl - v;
+}
+
+// Sorts list[0 .. n) by the CTA, falling; n at most kList.
+__device__ __forceinline__ void sort_falling(uint64_t *list, int n)
+{
+    int size = 2;
+    while (size < n)
+        size *= 2;
+    for (int j = n + threadIdx.x; j < size; j += kSpThreads)
+        list[j] = 0;
+    for (int span = 2; span <= size; span *= 2)
+        for (int d = span / 2; d; d /= 2) {
+            __syncthreads();
+            for (int t = threadIdx.x; t < size / 2; t += kSpThreads) {
+                const int p = 2 * t - (t & (d - 1)), q = p + d;
+                const uint64_t v = list[p], w = list[q];
+                if ((v < w) == ((p & span) == 0)) {
+                    list[p] = w;
+                    list[q] = v;
+                }
+            }
+        }
+    __syncthreads();
 }
 
 // floor(u * s), u below 1 and not below 0.
@@ -163,38 +235,38 @@ __device__ __forceinline__ uint64_t target_of(float p, uint64_t s)
 
 }  // namespace
 
-// `per` elements a thread; T the logits' type.
+// A warp's run is J * 32 vectors of 16 bytes; T the logits' type.
 template <class T>
 __global__ void __launch_bounds__(kSpThreads, 2)
-    zp_sample_kernel(const __grid_constant__ SampleArgs a, int ctas, int per)
+    zp_sample_kernel(const __grid_constant__ SampleArgs a, int ctas, int J)
 {
     constexpr int VE = 16 / sizeof(T);
     extern __shared__ __align__(128) uint8_t raw[];
     SpShared &S = *reinterpret_cast<SpShared *>(raw);
-    T *x = reinterpret_cast<T *>(raw + (sizeof(SpShared) + 127) / 128 * 128);
+    uint4 *x = reinterpret_cast<uint4 *>(raw + (sizeof(SpShared) + 127) / 128 * 128);
     const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
     const int rank = static_cast<int>(cluster_ctarank());
     const int i = blockIdx.x / ctas;
-    const int seg = per * kSpThreads;
-    if (tid == 0) {
-        mbar_init(&S.bar, 1);
+    if (lane == 0) {
+        mbar_init(&S.bar[wi], 1);
         fence_mbar_init();
     }
-    __syncthreads();
+    __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
 
-    // the row as slots from the 16-byte boundary at or below its first element: it
-    // fills slots mis .. mis + vocab - 1, this CTA holds `seg` from `s0` on
+    // the row as vectors from the 16-byte boundary at or below its first element: vector
+    // g holds elements g * VE - mis ..; this warp's are g0 .. g0 + 32 J - 1
     const T *row = static_cast<const T *>(a.logits) + i * a.stride;
     const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T));
-    const int s0 = rank * seg;
-    const int lo = mis ? VE : 0, hi = (mis + a.vocab) / VE * VE;  // whole vectors
-    const int c0 = max(s0, lo), c1 = min(s0 + seg, hi);
-    if (tid == 0 && c1 > c0) {
-        mbar_arrive_expect_tx(&S.bar, static_cast<uint32_t>((c1 - c0) * sizeof(T)));
-        bulk_g2s(x + (c0 - s0), row + (c0 - mis), static_cast<uint32_t>((c1 - c0) * sizeof(T)),
-                 &S.bar);
+    const int g0 = (rank * kSpWarps + wi) * J * 32;
+    uint4 *run = x + wi * J * 32;
+    const int c0 = max(g0, mis ? 1 : 0);  // whole vectors of the row
+    const int c1 = min(g0 + J * 32, (mis + a.vocab) / VE);
+    if (lane == 0 && c1 > c0) {
+        mbar_arrive_expect_tx(&S.bar[wi], (c1 - c0) * 16);
+        bulk_g2s(run + (c0 - g0), row + (static_cast<int64_t>(c0) * VE - mis), (c1 - c0) * 16,
+                 &S.bar[wi]);
     }
 
     // the request's parameters
@@ -229,32 +301,53 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     }
     for (int k = tid; k < 1024; k += kSpThreads)
         S.table[k] = d_table.v[k];
-    for (int s = tid; s < seg; s += kSpThreads)
-        if (s0 + s < c0 || s0 + s >= c1) {
-            const int e = s0 + s - mis;
-            x[s] = e >= 0 && e < a.vocab ? row[e] : static_cast<T>(-INFINITY);
+    for (int b = tid; b < kBuckets; b += kSpThreads)
+        S.count[b] = S.low[b] = S.high[b] = 0;
+    if (tid == 0)
+        S.listed = 0;
+    for (int j = 0; j < J; ++j) {
+        const int g = g0 + j * 32 + lane;
+        if (g >= c0 && g < c1)
+            continue;
+        float v[VE];
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+            const int e = g * VE - mis + k;
+            v[k] = e >= 0 && e < a.vocab ? to_f32(row[e]) : -INFINITY;
         }
-    if (c1 > c0 && !mbar_wait(&S.bar, 0))
+        run[j * 32 + lane] = pack(v);
+    }
+    if (c1 > c0 && !mbar_wait(&S.bar[wi], 0))
         set_error(a.sticky, ZP_ERR_TIMEOUT);
-    __syncthreads();
-    cluster_arrive();  // the other CTAs have started once it is waited for
+    __syncwarp();
 
     // the largest logit and the smallest finite one; NaN becomes -infinity
-    T *mine = x + tid * per;
     float top = -INFINITY, bottom = INFINITY;
-    for (int k = 0; k < per; ++k) {
-        const float v = to_f32(mine[k]);
-        if (v != v)
-            mine[k] = static_cast<T>(-INFINITY);
-        top = fmaxf(top, v);
-        bottom = fminf(bottom, v > -INFINITY ? v : INFINITY);
+    for (int j = 0; j < J; ++j) {
+        float v[VE];
+        unpack(run[j * 32 + lane], v);
+        bool nan = false;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+            nan |= v[k] != v[k];
+            top = fmaxf(top, v[k]);
+            bottom = fminf(bottom, v[k] > -INFINITY ? v[k] : INFINITY);
+        }
+        if (nan) {
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                v[k] = v[k] != v[k] ? -INFINITY : v[k];
+            run[j * 32 + lane] = pack(v);
+        }
     }
+    const float my_top = top;
     top = value_of(__reduce_max_sync(0xffffffffu, key_of(top)));
     bottom = value_of(__reduce_min_sync(0xffffffffu, key_of(bottom)));
     float2 *warp_ends = reinterpret_cast<float2 *>(S.scan64);
     if (lane == 0)
         warp_ends[wi] = make_float2(top, bottom);
     __syncthreads();
+    cluster_arrive();  // the other CTAs have started once it is waited for
     for (int w = 0; w < kSpWarps; ++w) {
         top = fmaxf(top, warp_ends[w].x);
         bottom = fminf(bottom, warp_ends[w].y);
@@ -269,24 +362,75 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         bottom = fminf(bottom, S.ends[r].y);
     }
     const float M = top;
-    const bool none = M == -INFINITY;
-    if (!ok || none) {  // the whole cluster alike
+
+    // Writes the row's probabilities from those that `prob` gives for a value and, where ties are
+    // cut, the number of entries equal to tau before it.
+    auto write_row = [&](auto prob, bool ranked, float tau, int t) {
+        const int psz = a.prob_bf16 ? 2 : 4;
+        uint8_t *to = static_cast<uint8_t *>(a.probs) + (i * a.prob_stride - mis) * psz;
+        const bool whole = reinterpret_cast<uintptr_t>(to) % 16 == 0;
+        for (int j = 0; j < J; ++j) {
+            float v[VE], p[VE];
+            unpack(run[j * 32 + lane], v);
+            if (ranked) {
+                int n = 0;
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    n += v[k] == tau;
+                const int upto = warp_incl(n, lane);
+                int before = t + upto - n;
+                t += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    p[k] = prob(v[k], before);
+                    before += v[k] == tau;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    p[k] = prob(v[k], 0);
+            }
+            const int64_t g = g0 + j * 32 + lane;
+            if (whole && g >= c0 && g < c1) {
+                if (a.prob_bf16) {
+                    uint32_t w[VE / 2];
+#pragma unroll
+                    for (int k = 0; k < VE; k += 2)
+                        w[k / 2] = pack_bf16x2(p[k], p[k + 1]);
+                    if constexpr (VE == 8)
+                        st_global_v4(to + g * VE * 2, make_uint4(w[0], w[1], w[2], w[3]));
+                    else
+                        *reinterpret_cast<uint2 *>(to + g * VE * 2) = make_uint2(w[0], w[1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VE; k += 4)
+                        st_global_v4(to + (g * VE + k) * 4,
+                                     make_uint4(__float_as_uint(p[k]), __float_as_uint(p[k + 1]),
+                                                __float_as_uint(p[k + 2]),
+                                                __float_as_uint(p[k + 3])));
+                }
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                const int64_t e = g * VE - mis + k;
+                if (e < 0 || e >= a.vocab)
+                    continue;
+                if (a.prob_bf16)
+                    reinterpret_cast<__nv_bfloat16 *>(to)[g * VE + k] = __float2bfloat16_rn(p[k]);
+                else
+                    reinterpret_cast<float *>(to)[g * VE + k] = p[k];
+            }
+        }
+    };
+    if (!ok || M == -INFINITY) {  // the whole cluster alike
         if (rank == 0 && tid == 0) {
             set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
             if (a.tokens)
                 a.tokens[i] = -1;
         }
-        for (int s = tid; s < seg && a.probs; s += kSpThreads) {
-            const int e = s0 + s - mis;
-            if (e < 0 || e >= a.vocab)
-                continue;
-            if (a.prob_bf16)
-                static_cast<__nv_bfloat16 *>(a.probs)[i * a.prob_stride + e] =
-                    __float2bfloat16_rn(0.f);
-            else
-                static_cast<float *>(a.probs)[i * a.prob_stride + e] = 0.f;
-        }
-        all_ctas();
+        if (a.probs)
+            write_row([](float, int) { return 0.f; }, false, 0.f, 0);
         return;
     }
     auto weight_of = [&](float v) {
@@ -294,6 +438,17 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         gap(M, v, h, l);
         return weight(S.table, c, h, l);
     };
+    auto within = [&](float v) {  // min_p's part
+        float h, l;
+        gap(M, v, h, l);
+        return h < gap_h || (h == gap_h && l <= gap_l);
+    };
+    const uint64_t kNone = 0;  // (an entry of the list that is none)
+    auto entry_of = [&](float v, int j, int k) {  // falling by value, then rising by index
+        return static_cast<uint64_t>(key_of(v)) << 32 |
+               (0xffffffffu - static_cast<uint32_t>((g0 + j * 32 + lane) * VE + k));
+    };
+    auto value_at = [&](uint64_t e) { return value_of(static_cast<uint32_t>(e >> 32)); };
 
     // ---------------------------------------------------------------- the cut
     Cut cut{};
@@ -305,80 +460,91 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         const float b = v == M ? 0.f : (M - v) * per_gap;
         return min(kBuckets - 1, static_cast<int>(b));
     };
-    // Every entry of the histogram's range is counted under `place` (below 0: not at
-    // all), CTA 0 sums up, and finds the bucket in which the target is reached, with
-    // `above` entries and `mass` above the first.
-    auto histogram = [&](bool weights, auto place) {
-        for (int b = tid; b < kBuckets; b += kSpThreads) {
-            S.count[b] = 0;
-            S.mass[b] = 0;
-        }
-        __syncthreads();
-        for (int k = 0; k < per; ++k) {
-            const float v = to_f32(mine[k]);
-            const int b = v > -INFINITY ? place(v) : -1;
-            if (b < 0)
-                continue;
-            atomicAdd(&S.count[b], 1u);
-            if (weights)
-                atomicAdd(reinterpret_cast<unsigned long long *>(&S.mass[b]),
-                          static_cast<unsigned long long>(weight_of(v)));
-        }
+    // CTA 0's sums of the CTAs' histograms.
+    auto gather_sums = [&](bool counts, bool weights) {
         all_ctas();
         if (rank == 0)
             for (int b = tid; b < kBuckets; b += kSpThreads) {
                 uint32_t n = S.count[b];
-                uint64_t w = S.mass[b];
+                uint64_t w = static_cast<uint64_t>(S.high[b]) << 32 | S.low[b];
                 for (int r = 1; r < ctas; ++r) {
-                    uint32_t y;
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                                 : "=r"(y)
-                                 : "r"(dsmem_addr(&S.count[b], r))
-                                 : "memory");
-                    n += y;
+                    if (counts)
+                        n += ld_dsmem_u32(dsmem_addr(&S.count[b], r));
                     if (weights)
-                        w += ld_dsmem_u64(dsmem_addr(&S.mass[b], r));
+                        w += static_cast<uint64_t>(ld_dsmem_u32(dsmem_addr(&S.high[b], r))) << 32 |
+                             ld_dsmem_u32(dsmem_addr(&S.low[b], r));
                 }
                 S.count[b] = n;
-                S.mass[b] = w;
+                S.low[b] = static_cast<uint32_t>(w);
+                S.high[b] = static_cast<uint32_t>(w >> 32);
             }
+    };
+    auto add_weight = [&](int b, uint64_t w) {
+        const uint32_t low = static_cast<uint32_t>(w);
+        const uint32_t old = atomicAdd(&S.low[b], low);
+        const uint32_t high = static_cast<uint32_t>(w >> 32) + (old + low < old);
+        if (high)
+            atomicAdd(&S.high[b], high);
+    };
+    // Every entry above -infinity is counted under `place` (below 0: not at all).
+    auto histogram = [&](bool counts, bool weights, auto place) {
+        for (int j = 0; j < J; ++j) {
+            float v[VE];
+            unpack(run[j * 32 + lane], v);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                const int b = v[k] > -INFINITY ? place(v[k]) : -1;
+                if (b < 0)
+                    continue;
+                if (counts)
+                    atomicAdd(&S.count[b], 1u);
+                if (weights)
+                    add_weight(b, weight_of(v[k]));
+            }
+        }
+        gather_sums(counts, weights);
+    };
+    auto clear = [&] {
+        for (int b = tid; b < kBuckets; b += kSpThreads)
+            S.count[b] = S.low[b] = S.high[b] = 0;
+        __syncthreads();
     };
     // CTA 0 alone: the bucket where `above` + counts reach `k`, or `mass` + weights reach
     // `target` (k = 0), from the largest values on, which the last buckets of a `rising`
-    // histogram hold and the first of the other.
+    // histogram hold and the first of the other.  bucket < 0: fewer entries than k.
     auto find = [&](uint32_t k, uint64_t target, bool rising) {
         constexpr int PB = kBuckets / kSpThreads;
         __syncthreads();
         uint32_t n = 0, all_n;
         uint64_t w = 0, all_w;
+        uint32_t nb[PB];
+        uint64_t wb[PB];
 #pragma unroll
         for (int j = 0; j < PB; ++j) {
             const int b = rising ? kBuckets - 1 - (tid * PB + j) : tid * PB + j;
-            n += S.count[b];
-            w += S.mass[b];
+            n += nb[j] = S.count[b];
+            w += wb[j] = static_cast<uint64_t>(S.high[b]) << 32 | S.low[b];
         }
         uint32_t n0 = S.cut.above + block_before(n, S.scan32, all_n);
         uint64_t w0 = S.cut.mass + block_before(w, S.scan64, all_w);
         __syncthreads();  // S.cut is read
-        if (tid == 0 && k > all_n && !rising) {  // fewer entries above -infinity: all of them
+        if (tid == 0 && k > all_n && !rising) {
             S.cut.mass = all_w;
             S.cut.bucket = -1;
             S.cut.tau = -INFINITY;
             S.cut.m = 0x7fffffff;
         }
+#pragma unroll
         for (int j = 0; j < PB; ++j) {
-            const int b = rising ? kBuckets - 1 - (tid * PB + j) : tid * PB + j;
-            const uint32_t nb = S.count[b];
-            const uint64_t wb = S.mass[b];
-            const bool here = k ? n0 < k && n0 + nb >= k : w0 < target && w0 + wb >= target;
+            const bool here =
+                k ? n0 < k && n0 + nb[j] >= k : w0 < target && w0 + wb[j] >= target;
             if (here) {
                 S.cut.above = n0;
                 S.cut.mass = w0;
-                S.cut.in = nb;
-                S.cut.bucket = b;
+                S.cut.bucket = rising ? kBuckets - 1 - (tid * PB + j) : tid * PB + j;
             }
-            n0 += nb;
-            w0 += wb;
+            n0 += nb[j];
+            w0 += wb[j];
         }
         __syncthreads();
     };
@@ -397,16 +563,80 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         all_ctas();
         cut = S.told[turn];
     };
+    // The entries for which `inside` holds into CTA 0's list, which counts them all.
+    auto gather = [&](auto inside) {
+        for (int j = 0; j < J; ++j) {
+            float v[VE];
+            unpack(run[j * 32 + lane], v);
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                if (inside(v[k])) {
+                    const uint32_t at = add_dsmem_u32(dsmem_addr(&S.listed, 0), 1);
+                    if (at < kList)
+                        st_dsmem_u64(dsmem_addr(&S.list[at], 0), entry_of(v[k], j, k));
+                }
+        }
+        all_ctas();
+    };
+    // CTA 0: of its sorted list of n, the entry at which the count (with `above`) reaches
+    // k, or the weights (with `mass`) reach `target`; tau, what is kept of it, the weights.
+    auto cut_list = [&](int n, uint32_t k, uint64_t target, bool weights) {
+        if (tid == 0)
+            S.equal = S.equal_upto = 0;
+        constexpr int PL = kList / kSpThreads;
+        uint64_t w[PL], sum = 0, all;
+#pragma unroll
+        for (int j = 0; j < PL; ++j) {
+            const int p = tid * PL + j;
+            w[j] = weights && p < n ? weight_of(value_at(S.list[p])) : 0;
+            sum += w[j];
+        }
+        const uint64_t mass = S.cut.mass;
+        const uint32_t above = S.cut.above;
+        uint64_t at = mass + block_before(sum, S.scan64, all);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < PL; ++j) {
+            const int p = tid * PL + j;
+            const bool here =
+                p < n && (k ? above + p + 1 == k : at < target && at + w[j] >= target);
+            at += w[j];
+            if (here) {
+                S.cut.tau = value_at(S.list[p]);
+                S.cut.mass = at;
+                S.cut.lo = static_cast<uint32_t>(p);
+            }
+        }
+        __syncthreads();
+        const uint32_t key = key_of(S.cut.tau);
+        const int last = static_cast<int>(S.cut.lo);
+        for (int p = tid; p < n; p += kSpThreads)
+            if (static_cast<uint32_t>(S.list[p] >> 32) == key) {
+                atomicAdd(&S.equal, 1u);
+                if (p <= last)
+                    atomicAdd(&S.equal_upto, 1u);
+            }
+        __syncthreads();
+        if (tid == 0) {
+            S.cut.in = S.equal;
+            S.cut.m = static_cast<int>(S.equal_upto);
+        }
+        __syncthreads();
+    };
     bool counted = false;  // CTA 0 holds the first histogram's sums
     // The cut where the count reaches k, or (k = 0) the weights reach `target`.
     auto select = [&](uint32_t k, uint64_t target, bool weights) {
-        if (!counted)
-            histogram(weights, bucket_of);
+        if (!counted) {
+            clear();
+            histogram(k > 0, weights, bucket_of);
+        }
         counted = true;
         if (rank == 0) {
             __syncthreads();
-            if (tid == 0)
+            if (tid == 0) {
                 S.cut = Cut{};
+                S.listed = 0;
+            }
             find(k, target, false);
         }
         tell();
@@ -418,21 +648,29 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             const uint32_t key = key_of(v);
             return v > -INFINITY && bucket_of(v) == bucket && key >= lo && key <= hi;
         };
-        bool one = false;  // one value alone is left
-        while (cut.in > kList && !one) {
-            counted = false;
+        for (;;) {
+            gather(inside);
+            if (rank == 0 && tid == 0)
+                S.cut.in = S.listed;
             if (rank == 0 && tid == 0) {
                 S.key_lo = 0xffffffffu;
                 S.key_hi = 0;
             }
-            all_ctas();
+            tell();
+            if (cut.in <= kList)
+                break;
+            // too many: by the bits of their values
+            counted = false;
             uint32_t a0 = 0xffffffffu, a1 = 0;
-            for (int j = 0; j < per; ++j) {
-                const float v = to_f32(mine[j]);
-                if (inside(v)) {
-                    a0 = min(a0, key_of(v));
-                    a1 = max(a1, key_of(v));
-                }
+            for (int j = 0; j < J; ++j) {
+                float v[VE];
+                unpack(run[j * 32 + lane], v);
+#pragma unroll
+                for (int q = 0; q < VE; ++q)
+                    if (inside(v[q])) {
+                        a0 = min(a0, key_of(v[q]));
+                        a1 = max(a1, key_of(v[q]));
+                    }
             }
             a0 = __reduce_min_sync(0xffffffffu, a0);
             a1 = __reduce_max_sync(0xffffffffu, a1);
@@ -440,21 +678,33 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 min_dsmem_u32(dsmem_addr(&S.key_lo, 0), a0);
                 max_dsmem_u32(dsmem_addr(&S.key_hi, 0), a1);
             }
+            clear();
             all_ctas();
             if (rank == 0 && tid == 0) {
                 S.cut.lo = S.key_lo;
                 S.cut.hi = S.key_hi;
+                S.listed = 0;
             }
             tell();
             lo = cut.lo;
             hi = cut.hi;
-            one = lo == hi;
-            if (one)
-                break;
+            if (lo == hi) {  // one value alone
+                if (rank == 0 && tid == 0) {
+                    const float v = value_of(lo);
+                    const uint64_t w = weights ? weight_of(v) : 0;
+                    const int m = k ? static_cast<int>(k - cut.above)
+                                    : static_cast<int>((target - cut.mass + w - 1) / w);
+                    S.cut.tau = v;
+                    S.cut.m = m;
+                    S.cut.mass = cut.mass + w * m;
+                }
+                tell();
+                return;
+            }
             int sh = 0;
             while ((hi - lo) >> sh >= kBuckets)
                 ++sh;
-            histogram(weights, [&](float v) {
+            histogram(true, weights, [&](float v) {
                 return inside(v) ? static_cast<int>((key_of(v) - lo) >> sh) : -1;
             });
             if (rank == 0)
@@ -464,236 +714,328 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             hi = min(hi, from + ((1u << sh) - 1));
             lo = from;
         }
-        if (one) {
-            if (rank == 0 && tid == 0) {
-                const float v = value_of(lo);
-                const uint64_t w = weights ? weight_of(v) : 0;
-                const int m = k ? static_cast<int>(k - cut.above)
-                                : static_cast<int>((target - cut.mass + w - 1) / w);
-                S.cut.tau = v;
-                S.cut.m = m;
-                S.cut.mass = cut.mass + w * m;
-            }
-            tell();
-            return;
-        }
-        if (rank == 0 && tid == 0)
-            S.listed = 0;
-        all_ctas();
-        for (int j = 0; j < per; ++j) {
-            const float v = to_f32(mine[j]);
-            if (inside(v)) {
-                const uint32_t at = add_dsmem_u32(dsmem_addr(&S.listed, 0), 1);
-                if (at < kList)
-                    st_dsmem_u64(dsmem_addr(&S.list[at], 0),
-                                 static_cast<uint64_t>(key_of(v)) << 32 |
-                                     (0xffffffffu - static_cast<uint32_t>(s0 + tid * per + j)));
-            }
-        }
-        all_ctas();
         if (rank == 0) {
-            // falling by value, then rising by index
-            const int n = min(static_cast<int>(S.listed), kList);
-            int size = 2;
-            while (size < n)
-                size *= 2;
-            for (int j = n + tid; j < size; j += kSpThreads)
-                S.list[j] = 0;
-            for (int span = 2; span <= size; span *= 2)
-                for (int d = span / 2; d; d /= 2) {
-                    __syncthreads();
-                    for (int t = tid; t < size / 2; t += kSpThreads) {
-                        const int p = 2 * t - (t & (d - 1)), q = p + d;
-                        const bool falling = (p & span) == 0;
-                        const uint64_t v = S.list[p], w = S.list[q];
-                        if ((v < w) == falling) {
-                            S.list[p] = w;
-                            S.list[q] = v;
-                        }
-                    }
-                }
-            if (tid == 0)
-                S.equal = S.equal_upto = 0;
-            __syncthreads();
-            // two entries a thread, and the sums before them
-            constexpr int PL = kList / kSpThreads;
-            uint64_t w[PL], sum = 0, all;
-#pragma unroll
-            for (int j = 0; j < PL; ++j) {
-                const int p = tid * PL + j;
-                w[j] = weights && p < n
-                           ? weight_of(value_of(static_cast<uint32_t>(S.list[p] >> 32)))
-                           : 0;
-                sum += w[j];
-            }
-            uint64_t at = cut.mass + block_before(sum, S.scan64, all);
-#pragma unroll
-            for (int j = 0; j < PL; ++j) {
-                const int p = tid * PL + j;
-                const bool here = p < n && (k ? cut.above + p + 1 == k
-                                              : at < target && at + w[j] >= target);
-                at += w[j];
-                if (here) {
-                    S.cut.tau = value_of(static_cast<uint32_t>(S.list[p] >> 32));
-                    S.cut.mass = at;
-                    S.cut.lo = static_cast<uint32_t>(p);
-                }
-            }
-            __syncthreads();
-            const uint32_t key = key_of(S.cut.tau);
-            const int last = static_cast<int>(S.cut.lo);
-            for (int p = tid; p < n; p += kSpThreads)
-                if (static_cast<uint32_t>(S.list[p] >> 32) == key) {
-                    atomicAdd(&S.equal, 1u);
-                    if (p <= last)
-                        atomicAdd(&S.equal_upto, 1u);
-                }
-            __syncthreads();
-            if (tid == 0) {
-                S.cut.in = S.equal;
-                S.cut.m = static_cast<int>(S.equal_upto);
-            }
+            sort_falling(S.list, static_cast<int>(cut.in));
+            cut_list(static_cast<int>(cut.in), k, target, weights);
         }
         tell();
     };
     const bool by_mass = top_p < 1.f;
-    if (top_k > 0)
+    const bool few = top_k > 0 && top_k <= kList / 2 && top_k * 2 <= ctas * kSpThreads;
+    bool listed = false;  // CTA 0's list holds all that may be kept
+    if (few) {
+        // the k-th largest of the threads' maxima: no fewer than k entries lie in its
+        // bucket or above it
+        if (my_top > -INFINITY)
+            atomicAdd(&S.count[bucket_of(my_top)], 1u);
+        gather_sums(true, false);
+        if (rank == 0) {
+            if (tid == 0)
+                S.cut = Cut{};
+            find(static_cast<uint32_t>(top_k), 0, false);
+        }
+        tell();
+        const int most = cut.bucket < 0 ? kBuckets - 1 : cut.bucket;
+        gather([&](float v) { return v > -INFINITY && bucket_of(v) <= most; });
+        if (rank == 0) {
+            const int n = static_cast<int>(S.listed);
+            __syncthreads();
+            if (tid == 0) {
+                S.cut = Cut{};
+                S.cut.done = n <= kList;
+                S.cut.tau = -INFINITY;
+                S.cut.m = 0x7fffffff;
+            }
+            if (n <= kList) {
+                sort_falling(S.list, n);
+                int kept = n;
+                if (n >= top_k) {
+                    cut_list(n, static_cast<uint32_t>(top_k), 0, true);
+                    kept = top_k;
+                }
+                if (by_mass) {
+                    uint64_t sum = S.cut.mass;
+                    if (n < top_k) {  // all there are
+                        uint64_t s = 0;
+                        for (int p = tid; p < n; p += kSpThreads)
+                            s += weight_of(value_at(S.list[p]));
+                        block_before(s, S.scan64, sum);
+                    }
+                    const uint64_t target =
+                        top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
+                    __syncthreads();
+                    if (tid == 0)
+                        S.cut.mass = 0;
+                    __syncthreads();
+                    cut_list(n, 0, target, true);
+                    kept = static_cast<int>(S.cut.lo) + 1;
+                }
+                // in the order of their index (which the entry's low half falls with)
+                uint64_t e[kList / kSpThreads], sum = 0, total;
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kList / kSpThreads; ++j) {
+                    const int p = j * kSpThreads + tid;
+                    e[j] = p < kept ? S.list[p] : kNone;
+                    if (p < kept && !within(value_at(e[j])))
+                        e[j] = kNone;
+                    sum += e[j] ? weight_of(value_at(e[j])) : 0;
+                }
+                block_before(sum, S.scan64, total);
+                if (tid == 0)
+                    S.cut.mass = total;
+                if (a.tokens) {
+                    __syncthreads();
+#pragma unroll
+                    for (int j = 0; j < kList / kSpThreads; ++j) {
+                        const int p = j * kSpThreads + tid;
+                        if (p < kept)
+                            S.list[p] = e[j] << 32 | e[j] >> 32;
+                    }
+                    __syncthreads();
+                    sort_falling(S.list, kept);
+                    const uint64_t level =
+                        u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
+                    constexpr int PL = kList / kSpThreads;
+                    uint64_t w[PL], s = 0, all;
+#pragma unroll
+                    for (int j = 0; j < PL; ++j) {
+                        const int p = tid * PL + j;
+                        const uint64_t v = p < kept ? S.list[p] : kNone;
+                        w[j] = v ? weight_of(value_of(static_cast<uint32_t>(v))) : 0;
+                        s += w[j];
+                    }
+                    uint64_t at = block_before(s, S.scan64, all);
+#pragma unroll
+                    for (int j = 0; j < PL; ++j) {
+                        if (at <= level && level < at + w[j])
+                            a.tokens[i] =
+                                static_cast<int>(0xffffffffu - static_cast<uint32_t>(
+                                                     S.list[tid * PL + j] >> 32)) - mis;
+                        at += w[j];
+                    }
+                }
+            }
+        }
+        tell();
+        listed = cut.done != 0;
+        if (listed && a.tokens)
+            return;
+        if (!listed) {
+            cut = Cut{};
+            cut.tau = -INFINITY;
+            cut.m = 0x7fffffff;
+        }
+    }
+    if (!listed && top_k > 0)
         select(static_cast<uint32_t>(top_k), 0, by_mass);
-    if (by_mass) {
+    auto cluster_total = [&](uint64_t s) {  // of all threads' s; the warps' sums in S.runs
+        s = warp_sum(s);
+        if (lane < ctas)
+            st_dsmem_u64(dsmem_addr(&S.runs[rank * kSpWarps + wi], lane), s);
+        all_ctas();
+        uint64_t total = 0;
+        for (int r = lane; r < ctas * kSpWarps; r += 32)
+            total += S.runs[r];
+        return warp_sum(total);
+    };
+    if (!listed && by_mass) {
         uint64_t sum = cut.mass;
         if (top_k == 0) {  // of the whole row
-            uint64_t s = 0, all;
-            for (int k = 0; k < per; ++k)
-                s += weight_of(to_f32(mine[k]));
-            block_before(s, S.scan64, all);
-            if (tid < ctas)
-                st_dsmem_u64(dsmem_addr(&S.sums[rank], tid), all);
-            all_ctas();
-            sum = 0;
-            for (int r = 0; r < ctas; ++r)
-                sum += S.sums[r];
+            clear();
+            uint64_t s = 0;
+            for (int j = 0; j < J; ++j) {
+                float v[VE];
+                unpack(run[j * 32 + lane], v);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    const uint64_t w = weight_of(v[k]);
+                    s += w;
+                    if (w)
+                        add_weight(bucket_of(v[k]), w);
+                }
+            }
+            sum = cluster_total(s);
+            gather_sums(false, true);
+            counted = true;
         }
         const uint64_t target = top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
         select(0, target, true);
     }
-    const bool partial = (top_k > 0 || by_mass) && cut.m < static_cast<int>(cut.in);
+    const bool cuts = top_k > 0 || by_mass;
+    const bool partial = cuts && cut.m < static_cast<int>(cut.in);
 
     // ----------------------------------------------------------- what is kept
-    auto within = [&](float v) {  // min_p's part
-        float h, l;
-        gap(M, v, h, l);
-        return h < gap_h || (h == gap_h && l <= gap_l);
-    };
-    const int slot0 = s0 + tid * per;  // this thread's first
-    int ties_before = 0;               // entries equal to tau before it
+    int ties_before = 0;  // entries equal to tau before this warp's run
     if (partial) {
-        uint32_t n = 0, all;
-        for (int k = 0; k < per; ++k)
-            n += to_f32(mine[k]) == cut.tau;
-        ties_before = static_cast<int>(block_before(n, S.scan32, all));
-        if (tid < ctas)
-            st_dsmem_u32(dsmem_addr(&S.ties[rank], tid), all);
-        all_ctas();
-        for (int r = 0; r < rank; ++r)
-            ties_before += static_cast<int>(S.ties[r]);
-    }
-    uint64_t sum = 0, all, total = 0, before;
-    {
-        int t = ties_before;
-        for (int k = 0; k < per; ++k) {
-            const float v = to_f32(mine[k]);
-            const bool tie = v == cut.tau;
-            if ((v > cut.tau || (tie && t < cut.m)) && within(v))
-                sum += weight_of(v);
-            t += tie && partial;
+        uint32_t n = 0;
+        for (int j = 0; j < J; ++j) {
+            float v[VE];
+            unpack(run[j * 32 + lane], v);
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                n += v[k] == cut.tau;
         }
+        n = warp_sum(n);
+        if (lane < ctas)
+            st_dsmem_u32(dsmem_addr(&S.ties[rank * kSpWarps + wi], lane), n);
+        all_ctas();
+        uint32_t t = 0;
+        for (int r = lane; r < rank * kSpWarps + wi; r += 32)
+            t += S.ties[r];
+        ties_before = static_cast<int>(warp_sum(t));
     }
-    before = block_before(sum, S.scan64, all);
-    __syncthreads();
-    if (tid < ctas)
-        st_dsmem_u64(dsmem_addr(&S.sums[rank], tid), all);
-    all_ctas();
-    for (int r = 0; r < ctas; ++r) {
-        before += r < rank ? S.sums[r] : 0;
-        total += S.sums[r];
-    }
+    auto kept = [&](float v, int before) {
+        return (v > cut.tau || (v == cut.tau && (!partial || before < cut.m))) && within(v);
+    };
+    // The lane's kept weights of step j, `t` entries equal to tau before the step; t moves on.
+    auto step_sum = [&](int j, int &t) {
+        float v[VE];
+        unpack(run[j * 32 + lane], v);
+        int before = 0;
+        if (partial) {
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                n += v[k] == cut.tau;
+            const int upto = warp_incl(n, lane);
+            before = t + upto - n;
+            t += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        uint64_t s = 0;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+            if (kept(v[k], before))
+                s += weight_of(v[k]);
+            before += v[k] == cut.tau;
+        }
+        return s;
+    };
     if (a.tokens) {
-        // the thread whose run the level falls into; its warp looks through the run
+        uint64_t s = 0;
+        int t = ties_before;
+        for (int j = 0; j < J; ++j)
+            s += step_sum(j, t);
+        all_ctas();  // (S.runs may still be read)
+        const uint64_t total = cluster_total(s);
         const uint64_t level = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
-        const unsigned who = __ballot_sync(0xffffffffu, before <= level && level < before + sum);
-        if (who == 0)
+        // the run that the level falls into: four runs a lane
+        constexpr int RL = kSpCtas * kSpWarps / 32;
+        const int runs = ctas * kSpWarps;
+        uint64_t part[RL], local = 0;
+#pragma unroll
+        for (int k = 0; k < RL; ++k) {
+            part[k] = lane * RL + k < runs ? S.runs[lane * RL + k] : 0;
+            local += part[k];
+        }
+        uint64_t at = warp_incl(local, lane) - local, mine = 0;
+        bool here = false;
+#pragma unroll
+        for (int k = 0; k < RL; ++k) {
+            if (lane * RL + k == rank * kSpWarps + wi && at <= level && level < at + part[k]) {
+                here = true;
+                mine = at;
+            }
+            at += part[k];
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        if (!who)
             return;
-        const int src = __ffs(who) - 1;
-        uint64_t at = __shfl_sync(0xffffffffu, before, src);
-        int t = __shfl_sync(0xffffffffu, ties_before, src);
-        const int first = __shfl_sync(0xffffffffu, slot0, src);
-        for (int k0 = 0; k0 < per; k0 += 32) {
-            const float v = k0 + lane < per ? to_f32(x[first - s0 + k0 + lane]) : -INFINITY;
-            const bool tie = v == cut.tau;
-            const unsigned same = __ballot_sync(0xffffffffu, tie);
-            const int my_t = t + __popc(same & ((1u << lane) - 1));
-            uint64_t w = 0;
-            if ((v > cut.tau || (tie && (!partial || my_t < cut.m))) && within(v))
-                w = weight_of(v);
+        at = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+        t = ties_before;
+        for (int j = 0; j < J; ++j) {
+            int t0 = t;
+            const uint64_t w = step_sum(j, t);
             const uint64_t upto = at + warp_incl(w, lane);
             const unsigned past = __ballot_sync(0xffffffffu, upto > level);
-            if (past) {
-                if (lane == __ffs(past) - 1)
-                    a.tokens[i] = first + k0 + lane - mis;
-                return;
+            if (!past) {
+                at = __shfl_sync(0xffffffffu, upto, 31);
+                continue;
             }
-            at = __shfl_sync(0xffffffffu, upto, 31);
-            t += __popc(same);
+            float v[VE];
+            unpack(run[j * 32 + lane], v);
+            int n = 0;
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                n += partial && v[k] == cut.tau;
+            int before = t0 + warp_incl(n, lane) - n;
+            if (lane == __ffs(past) - 1) {
+                uint64_t sum = upto - w;
+                int tok = -1;
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    if (tok < 0 && kept(v[k], before)) {
+                        sum += weight_of(v[k]);
+                        if (sum > level)
+                            tok = (g0 + j * 32 + lane) * VE + k - mis;
+                    }
+                    before += v[k] == cut.tau;
+                }
+                a.tokens[i] = tok;
+            }
+            return;
         }
         return;
     }
 
-    // the probabilities: a warp's runs lie one behind the other
-    const float inv = static_cast<float>(17592186044416.0 / static_cast<double>(total));
-    const int w0 = (tid - lane) * per;
-    int t = __shfl_sync(0xffffffffu, ties_before, 0);
-    for (int k0 = 0; k0 < 32 * per; k0 += 32) {
-        const int s = w0 + k0 + lane;
-        const float v = to_f32(x[s]);
-        const bool tie = v == cut.tau;
-        int my_t = t;
-        if (partial) {
-            const unsigned same = __ballot_sync(0xffffffffu, tie);
-            my_t += __popc(same & ((1u << lane) - 1));
-            t += __popc(same);
+    // 2^-y times a number near 1 for the low parts of y: an fp32 number's worth of a weight
+    auto weight32 = [&](float v) {
+        float h, l;
+        gap(M, v, h, l);
+        const float y = h * c.ch;
+        const float e = fmaf(l, c.ch, fmaf(h, c.cl, fmaf(h, c.ch, -y)));
+        return y < 150.f ? ex2_approx(-y) * fmaf(e, -0.693147182f, 1.f) : 0.f;
+    };
+    uint64_t total = cut.mass;
+    if (!cuts || (!listed && (min_p > 0.f || !by_mass))) {
+        // (the weights of a cut by sums are known, but for what min_p takes off)
+        float s = 0.f;
+        int t = ties_before;
+        for (int j = 0; j < J; ++j) {
+            float v[VE], p[VE];
+            unpack(run[j * 32 + lane], v);
+            int before = 0;
+            if (partial) {
+                int n = 0;
+#pragma unroll
+                for (int k = 0; k < VE; ++k)
+                    n += v[k] == cut.tau;
+                const int upto = warp_incl(n, lane);
+                before = t + upto - n;
+                t += __shfl_sync(0xffffffffu, upto, 31);
+            }
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                p[k] = kept(v[k], before) ? weight32(v[k]) : 0.f;
+                before += v[k] == cut.tau;
+            }
+#pragma unroll
+            for (int k = 1; k < VE; k *= 2)
+#pragma unroll
+                for (int q = 0; q < VE; q += 2 * k)
+                    p[q] += p[q + k];
+            s += p[0];
         }
-        float p = 0.f;
-        if ((v > cut.tau || (tie && (!partial || my_t < cut.m))) && within(v)) {
-            float h, l;
-            gap(M, v, h, l);
-            const float y = h * c.ch;
-            const float e = fmaf(l, c.ch, fmaf(h, c.cl, fmaf(h, c.ch, -y)));
-            p = y < 150.f ? ex2_approx(-y) * fmaf(e, -0.693147182f, 1.f) * inv : 0.f;
-        }
-        const int e = s0 + s - mis;
-        if (e < 0 || e >= a.vocab)
-            continue;
-        if (a.prob_bf16)
-            static_cast<__nv_bfloat16 *>(a.probs)[i * a.prob_stride + e] = __float2bfloat16_rn(p);
-        else
-            static_cast<float *>(a.probs)[i * a.prob_stride + e] = p;
+        all_ctas();  // (S.runs may still be read)
+        total = cluster_total(__float2ull_rn(s * 17592186044416.f));
     }
+    const float inv = static_cast<float>(17592186044416.0 / static_cast<double>(total));
+    write_row([&](float v, int before) { return kept(v, before) ? weight32(v) * inv : 0.f; },
+              partial, cut.tau, ties_before);
 }
 
 template <class T>
 static cudaError_t launch_sample_t(const SampleArgs &a, int sms, cudaStream_t s)
 {
     constexpr size_t kShared = (sizeof(SpShared) + 127) / 128 * 128;
-    constexpr int WORD = 4 / sizeof(T);  // elements a word: a thread's run is an odd number of words
-    auto per_of = [&](int ctas) {
-        const int slots = a.vocab + 16 / static_cast<int>(sizeof(T)) - 1;
-        const int words = (slots + ctas * kSpThreads * WORD - 1) / (ctas * kSpThreads * WORD);
-        return (words | 1) * WORD;
+    constexpr int VE = 16 / sizeof(T);
+    auto steps_of = [&](int ctas) {
+        return (a.vocab + 2 * VE - 2) / VE / (ctas * kSpThreads) + 1;
     };
-    auto bytes_of = [&](int ctas) { return kShared + per_of(ctas) * kSpThreads * sizeof(T); };
+    auto bytes_of = [&](int ctas) { return kShared + steps_of(ctas) * kSpThreads * 16; };
     int ctas = 1;
-    while (ctas < kSpCtas && (bytes_of(ctas) > 110 * 1024 || a.R * 2ll * ctas <= 2ll * sms) &&
-           per_of(ctas) > 4 * WORD)
+    while (ctas < kSpCtas && (bytes_of(ctas) > 112 * 1024 || a.R * 2ll * ctas <= 2ll * sms) &&
+           steps_of(ctas) > 1)
         ctas *= 2;
     const size_t bytes = bytes_of(ctas);
     cudaError_t err = cudaFuncSetAttribute(zp_sample_kernel<T>,
@@ -715,7 +1057,7 @@ static cudaError_t launch_sample_t(const SampleArgs &a, int sms, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, zp_sample_kernel<T>, a, ctas, per_of(ctas));
+    return cudaLaunchKernelEx(&cfg, zp_sample_kernel<T>, a, ctas, steps_of(ctas));
 }
 
 cudaError_t launch_sample(const SampleArgs &a, bool bf16, int sms, cudaStream_t s)
