@@ -61,6 +61,8 @@ struct SpShared {
     float2 ends[kSpCtas];                    // the CTAs' (largest, smallest finite)
     uint32_t scan32[kSpWarps];
     uint32_t key_lo, key_hi, listed, equal, equal_upto;
+    WeightScale scale;
+    float2 gap;   // the largest gap to the maximum that min_p allows, as a pair
     Cut cut;      // CTA 0's
     Cut told[2];  // what it told all, the last two times
 };
@@ -285,18 +287,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     }
     if (top_k < 0 || top_k >= a.vocab)
         top_k = 0;
-    WeightScale c;
-    float gap_h, gap_l;  // the largest gap to the maximum that min_p allows
-    {
-        const double s = fmin(1.4426950408889634 / static_cast<double>(temp), 1.2e30);
-        c.ch = static_cast<float>(s);
-        c.cl = static_cast<float>(s - static_cast<double>(c.ch));
-        gap_h = INFINITY;
-        gap_l = 0.f;
+    if (tid == 0) {  // (64-bit arithmetic of a whole CTA would take 3 us)
+        const double d = fmin(1.4426950408889634 / static_cast<double>(temp), 1.2e30);
+        S.scale.ch = static_cast<float>(d);
+        S.scale.cl = static_cast<float>(d - static_cast<double>(S.scale.ch));
+        S.gap = make_float2(INFINITY, 0.f);
         if (min_p > 0.f) {
             const double g = -static_cast<double>(temp) * log(fmin(static_cast<double>(min_p), 1.0));
-            gap_h = static_cast<float>(g);
-            gap_l = static_cast<float>(g - static_cast<double>(gap_h));
+            S.gap.x = static_cast<float>(g);
+            S.gap.y = static_cast<float>(g - static_cast<double>(S.gap.x));
         }
     }
     for (int k = tid; k < 1024; k += kSpThreads)
@@ -348,6 +347,8 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         warp_ends[wi] = make_float2(top, bottom);
     __syncthreads();
     cluster_arrive();  // the other CTAs have started once it is waited for
+    const WeightScale c = S.scale;
+    const float gap_h = S.gap.x, gap_l = S.gap.y;
     for (int w = 0; w < kSpWarps; ++w) {
         top = fmaxf(top, warp_ends[w].x);
         bottom = fminf(bottom, warp_ends[w].y);
@@ -434,11 +435,25 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         return;
     }
     auto weight_of = [&](float v) {
-        float h, l;
-        gap(M, v, h, l);
-        return weight(S.table, c, h, l);
+        uint64_t w, same;
+        weights(S.table, c, M, v, v, w, same);
+        return w;
+    };
+    // The weights of vector j of the lane: `take` gets a value and its weight.
+    auto each_weight = [&](int j, auto take) {
+        float v[VE];
+        unpack(run[j * 32 + lane], v);
+#pragma unroll
+        for (int k = 0; k < VE; k += 2) {
+            uint64_t w0, w1;
+            weights(S.table, c, M, v[k], v[k + 1], w0, w1);
+            take(v[k], w0);
+            take(v[k + 1], w1);
+        }
     };
     auto within = [&](float v) {  // min_p's part
+        if (!(min_p > 0.f))
+            return v > -INFINITY;
         float h, l;
         gap(M, v, h, l);
         return h < gap_h || (h == gap_h && l <= gap_l);
@@ -623,6 +638,91 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         }
         __syncthreads();
     };
+    const bool by_mass = top_p < 1.f;
+    // CTA 0: the cuts of what it has gathered, if it all fitted in the list, and the token.
+    // row_sum: the weights that top_p is a part of, 0 for those of the top_k.
+    auto finish = [&](uint64_t row_sum) {
+        if (rank != 0)
+            return;
+        const int n = static_cast<int>(S.listed);
+        __syncthreads();
+        if (tid == 0) {
+            S.cut = Cut{};
+            S.cut.done = n <= kList;
+            S.cut.tau = -INFINITY;
+            S.cut.m = 0x7fffffff;
+        }
+        if (n <= kList) {
+            sort_falling(S.list, n);
+            int kept = n;
+            if (top_k > 0 && n >= top_k) {
+                cut_list(n, static_cast<uint32_t>(top_k), 0, true);
+                kept = top_k;
+            }
+            if (by_mass) {
+                uint64_t sum = row_sum ? row_sum : S.cut.mass;
+                if (!row_sum && n < top_k) {  // all there are
+                    uint64_t s = 0;
+                    for (int p = tid; p < n; p += kSpThreads)
+                        s += weight_of(value_at(S.list[p]));
+                    block_before(s, S.scan64, sum);
+                }
+                const uint64_t target =
+                    top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
+                __syncthreads();
+                if (tid == 0)
+                    S.cut.mass = 0;
+                __syncthreads();
+                cut_list(n, 0, target, true);
+                kept = static_cast<int>(S.cut.lo) + 1;
+            }
+            // in the order of their index (which the entry's low half falls with)
+            uint64_t e[kList / kSpThreads], sum = 0, total;
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kList / kSpThreads; ++j) {
+                const int p = j * kSpThreads + tid;
+                e[j] = p < kept ? S.list[p] : kNone;
+                if (p < kept && !within(value_at(e[j])))
+                    e[j] = kNone;
+                sum += e[j] ? weight_of(value_at(e[j])) : 0;
+            }
+            block_before(sum, S.scan64, total);
+            if (tid == 0)
+                S.cut.mass = total;
+            if (a.tokens) {
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kList / kSpThreads; ++j) {
+                    const int p = j * kSpThreads + tid;
+                    if (p < kept)
+                        S.list[p] = e[j] << 32 | e[j] >> 32;
+                }
+                __syncthreads();
+                sort_falling(S.list, kept);
+                const uint64_t level =
+                    u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
+                constexpr int PL = kList / kSpThreads;
+                uint64_t w[PL], s = 0, all;
+#pragma unroll
+                for (int j = 0; j < PL; ++j) {
+                    const int p = tid * PL + j;
+                    const uint64_t v = p < kept ? S.list[p] : kNone;
+                    w[j] = v ? weight_of(value_of(static_cast<uint32_t>(v))) : 0;
+                    s += w[j];
+                }
+                uint64_t at = block_before(s, S.scan64, all);
+#pragma unroll
+                for (int j = 0; j < PL; ++j) {
+                    if (at <= level && level < at + w[j])
+                        a.tokens[i] =
+                            static_cast<int>(0xffffffffu - static_cast<uint32_t>(
+                                                 S.list[tid * PL + j] >> 32)) - mis;
+                    at += w[j];
+                }
+            }
+        }
+    };
     bool counted = false;  // CTA 0 holds the first histogram's sums
     // The cut where the count reaches k, or (k = 0) the weights reach `target`.
     auto select = [&](uint32_t k, uint64_t target, bool weights) {
@@ -720,7 +820,6 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         }
         tell();
     };
-    const bool by_mass = top_p < 1.f;
     const bool few = top_k > 0 && top_k <= kList / 2 && top_k * 2 <= ctas * kSpThreads;
     bool listed = false;  // CTA 0's list holds all that may be kept
     if (few) {
@@ -737,86 +836,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         tell();
         const int most = cut.bucket < 0 ? kBuckets - 1 : cut.bucket;
         gather([&](float v) { return v > -INFINITY && bucket_of(v) <= most; });
-        if (rank == 0) {
-            const int n = static_cast<int>(S.listed);
-            __syncthreads();
-            if (tid == 0) {
-                S.cut = Cut{};
-                S.cut.done = n <= kList;
-                S.cut.tau = -INFINITY;
-                S.cut.m = 0x7fffffff;
-            }
-            if (n <= kList) {
-                sort_falling(S.list, n);
-                int kept = n;
-                if (n >= top_k) {
-                    cut_list(n, static_cast<uint32_t>(top_k), 0, true);
-                    kept = top_k;
-                }
-                if (by_mass) {
-                    uint64_t sum = S.cut.mass;
-                    if (n < top_k) {  // all there are
-                        uint64_t s = 0;
-                        for (int p = tid; p < n; p += kSpThreads)
-                            s += weight_of(value_at(S.list[p]));
-                        block_before(s, S.scan64, sum);
-                    }
-                    const uint64_t target =
-                        top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
-                    __syncthreads();
-                    if (tid == 0)
-                        S.cut.mass = 0;
-                    __syncthreads();
-                    cut_list(n, 0, target, true);
-                    kept = static_cast<int>(S.cut.lo) + 1;
-                }
-                // in the order of their index (which the entry's low half falls with)
-                uint64_t e[kList / kSpThreads], sum = 0, total;
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < kList / kSpThreads; ++j) {
-                    const int p = j * kSpThreads + tid;
-                    e[j] = p < kept ? S.list[p] : kNone;
-                    if (p < kept && !within(value_at(e[j])))
-                        e[j] = kNone;
-                    sum += e[j] ? weight_of(value_at(e[j])) : 0;
-                }
-                block_before(sum, S.scan64, total);
-                if (tid == 0)
-                    S.cut.mass = total;
-                if (a.tokens) {
-                    __syncthreads();
-#pragma unroll
-                    for (int j = 0; j < kList / kSpThreads; ++j) {
-                        const int p = j * kSpThreads + tid;
-                        if (p < kept)
-                            S.list[p] = e[j] << 32 | e[j] >> 32;
-                    }
-                    __syncthreads();
-                    sort_falling(S.list, kept);
-                    const uint64_t level =
-                        u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
-                    constexpr int PL = kList / kSpThreads;
-                    uint64_t w[PL], s = 0, all;
-#pragma unroll
-                    for (int j = 0; j < PL; ++j) {
-                        const int p = tid * PL + j;
-                        const uint64_t v = p < kept ? S.list[p] : kNone;
-                        w[j] = v ? weight_of(value_of(static_cast<uint32_t>(v))) : 0;
-                        s += w[j];
-                    }
-                    uint64_t at = block_before(s, S.scan64, all);
-#pragma unroll
-                    for (int j = 0; j < PL; ++j) {
-                        if (at <= level && level < at + w[j])
-                            a.tokens[i] =
-                                static_cast<int>(0xffffffffu - static_cast<uint32_t>(
-                                                     S.list[tid * PL + j] >> 32)) - mis;
-                        at += w[j];
-                    }
-                }
-            }
-        }
+        finish(0);
         tell();
         listed = cut.done != 0;
         if (listed && a.tokens)
@@ -844,23 +864,36 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         if (top_k == 0) {  // of the whole row
             clear();
             uint64_t s = 0;
-            for (int j = 0; j < J; ++j) {
-                float v[VE];
-                unpack(run[j * 32 + lane], v);
-#pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    const uint64_t w = weight_of(v[k]);
+            for (int j = 0; j < J; ++j)
+                each_weight(j, [&](float v, uint64_t w) {
                     s += w;
                     if (w)
-                        add_weight(bucket_of(v[k]), w);
-                }
-            }
+                        add_weight(bucket_of(v), w);
+                });
             sum = cluster_total(s);
             gather_sums(false, true);
             counted = true;
         }
         const uint64_t target = top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
-        select(0, target, true);
+        if (top_k == 0) {  // all down to the bucket of the cut, if that is not too much
+            if (rank == 0) {
+                if (tid == 0) {
+                    S.cut = Cut{};
+                    S.listed = 0;
+                }
+                find(0, target, false);
+            }
+            tell();
+            const int most = cut.bucket;
+            gather([&](float v) { return v > -INFINITY && bucket_of(v) <= most; });
+            finish(sum);
+            tell();
+            listed = cut.done != 0;
+            if (listed && a.tokens)
+                return;
+        }
+        if (!listed)
+            select(0, target, true);
     }
     const bool cuts = top_k > 0 || by_mass;
     const bool partial = cuts && cut.m < static_cast<int>(cut.in);
@@ -914,8 +947,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     if (a.tokens) {
         uint64_t s = 0;
         int t = ties_before;
-        for (int j = 0; j < J; ++j)
-            s += step_sum(j, t);
+        if (!cuts && !(min_p > 0.f))
+            for (int j = 0; j < J; ++j)
+                each_weight(j, [&](float, uint64_t w) { s += w; });
+        else
+            for (int j = 0; j < J; ++j)
+                s += step_sum(j, t);
         all_ctas();  // (S.runs may still be read)
         const uint64_t total = cluster_total(s);
         const uint64_t level = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
@@ -1019,7 +1056,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         all_ctas();  // (S.runs may still be read)
         total = cluster_total(__float2ull_rn(s * 17592186044416.f));
     }
-    const float inv = static_cast<float>(17592186044416.0 / static_cast<double>(total));
+    const float inv = 17592186044416.f / static_cast<float>(total);
     write_row([&](float v, int before) { return kept(v, before) ? weight32(v) * inv : 0.f; },
               partial, cut.tau, ties_before);
 }

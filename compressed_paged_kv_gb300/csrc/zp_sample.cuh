@@ -30,14 +30,16 @@ constexpr int kSampleMaxVocab = 352 * 1024;
 cudaError_t launch_sample(const SampleArgs &a, bool bf16, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ weights
-// w = 2^-y, y = (M - l) log2(e) / T, as a whole number of 2^-44: sums of them are exact,
+// w = 2^-y, y = (M - l) log2(e) / T, as an odd whole number of 2^-44: sums of them are exact,
 // whatever their order, up to 2^19 weights (M is the row's largest, w = 1).  Tokens are
 // decided by sums of up to 10^5 weights, each a border that a random number may hit,
 // so 2^-24 (fp32) gets several draws in a thousand wrong; and fp64 has a 64th of fp32's
 // rate here.  So y is a pair of fp32 numbers, with
 //     y = k / 1024 + g,  |g| <= 2^-11,     2^-y = 2^-(k / 1024) (1 - z + z^2/2 - z^3/6),
 //     z = g ln 2, z^4/24 < 2^-50,
-// the first factor from a table of the 1,024 fractions.  The error is below 2^-41.
+// the first factor from a table of the 1,024 fractions.  What is cut off below 2^-44 is
+// half a unit in the mean, which the lowest bit, always set, makes up for.  The error is
+// below 2^-41.
 constexpr int kWeightBits = 44;
 
 struct WeightScale {
@@ -69,15 +71,6 @@ struct WeightTable {
 
 #ifdef __CUDACC__
 
-__host__ __device__ __forceinline__ int nearest_int(float x)
-{
-#ifdef __CUDA_ARCH__
-    return __float2int_rn(x);
-#else
-    return static_cast<int>(__builtin_rintf(x));
-#endif
-}
-
 __host__ __device__ __forceinline__ int bits_of(float x)
 {
 #ifdef __CUDA_ARCH__
@@ -88,6 +81,11 @@ __host__ __device__ __forceinline__ int bits_of(float x)
     return v;
 #endif
 }
+
+constexpr float kSteps = 12288.f;   // 1.5 * 2^13: what added to p leaves multiples of 2^-10
+constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: whole numbers
+constexpr uint32_t kWholeBits = 0x4b400000u;
+constexpr float kLn2 = 0.693147182f, kLn2Low = -1.90465421e-9f;
 
 // M - l as a pair (D. E. Knuth's error-free sum); 0 at the maximum itself, even an
 // infinite one.
@@ -100,26 +98,105 @@ __host__ __device__ __forceinline__ void gap(float M, float l, float &h, float &
         h = lo = 0.f;
 }
 
-// The same for gap (h, lo).  0 past y = 48 and for what is no number.
+// The weight from p + (what follows 2^-11 of it as z): z in units of 2^-42.
+__host__ __device__ __forceinline__ uint64_t weight_of_parts(const uint64_t *table, float p,
+                                                             uint32_t t, int z)
+{
+    const uint64_t v = table[t & 1023];
+    const int n = (t >> 10) & 63;
+    const uint64_t w = v - static_cast<uint64_t>(
+                               (static_cast<int64_t>(static_cast<int>(v >> 14)) * z) >> 28);
+    return p < 48.f ? (w >> n) | 1 : 0;
+}
+
+// The weight at gap (h, lo).  0 past y = 48 and for what is no number.
 __host__ __device__ __forceinline__ uint64_t weight(const uint64_t *table, const WeightScale &c,
                                                     float h, float lo)
 {
     const float p = h * c.ch;
-    if (!(p < 48.f))
-        return 0;
     const float e = fmaf(lo, c.ch, fmaf(h, c.cl, fmaf(h, c.ch, -p)));
-    const float t = p + 12288.f;  // 1.5 * 2^13: p to a multiple of 2^-10
-    const int k = bits_of(t) - 0x46400000;
-    const float g = p - (t - 12288.f), gs = g + e, ge = e - (gs - g);
-    const float zh = gs * 0.693147182f;  // ln 2 = 0.693147182 - 1.90465421e-9
-    const float zl = fmaf(ge, 0.693147182f, fmaf(gs, -1.90465421e-9f, fmaf(gs, 0.693147182f, -zh)));
-    const float s = zl - zh * zh * fmaf(zh, -0.166666667f, 0.5f);
-    const int z = nearest_int(zh * 4398046511104.f) + nearest_int(s * 4398046511104.f);  // 2^42
-    const uint64_t v = table[k & 1023];
-    const int n = k >> 10;
-    const uint64_t w = v - static_cast<uint64_t>(
-                               (static_cast<int64_t>(static_cast<int>(v >> 14)) * z) >> 28);
-    return (w + ((1ull << n) >> 1)) >> n;
+    const float t = p + kSteps;
+    const float g = p - (t - kSteps), gs = g + e, ge = e - (gs - g);
+    const float zh = gs * kLn2;
+    const float zl = fmaf(ge, kLn2, fmaf(gs, kLn2Low, fmaf(gs, kLn2, -zh)));
+    const float s = fmaf(zh * zh, fmaf(zh, 0.166666667f, -0.5f), zl);
+    // zh + s as a whole number of 2^-42, in two steps
+    const float a = fmaf(zh, 8589934592.f, kWhole);  // 2^33
+    const float b = fmaf(s + fmaf(a - kWhole, -1.16415322e-10f, zh), 4398046511104.f, kWhole);
+    const uint32_t z = (static_cast<uint32_t>(bits_of(a)) << 9) + static_cast<uint32_t>(bits_of(b)) -
+                       ((kWholeBits << 9) + kWholeBits);
+    return weight_of_parts(table, p, static_cast<uint32_t>(bits_of(t)), static_cast<int>(z));
+}
+
+// Two fp32 numbers, each operation on both at once.
+struct Two {
+    uint64_t v;
+};
+__device__ __forceinline__ Two two(float x, float y)
+{
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ Two two(float x) { return two(x, x); }
+__device__ __forceinline__ Two operator+(Two a, Two b)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two operator-(Two a, Two b)
+{
+    Two r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ uint32_t low_bits(Two a) { return static_cast<uint32_t>(a.v); }
+__device__ __forceinline__ uint32_t high_bits(Two a) { return static_cast<uint32_t>(a.v >> 32); }
+
+// y of two logits below a finite M: its fp32 value p and the rest e.
+__device__ __forceinline__ void exponents(float M, const WeightScale &c, Two l, Two &p, Two &e)
+{
+    const Two m = two(M), h = m - l, b = h - m, lo = (m - (h - b)) - (l + b);
+    const Two ch = two(c.ch);
+    p = h * ch;
+    e = fma2(lo, ch, fma2(h, two(c.cl), fma2(h, ch, h * two(-c.ch))));
+}
+
+// The weights of two logits: weight() of each, to the bit.
+__device__ __forceinline__ void weights(const uint64_t *table, const WeightScale &c, float M,
+                                        float l0, float l1, uint64_t &w0, uint64_t &w1)
+{
+    if (fabsf(M) == INFINITY) {
+        w0 = l0 == M ? (1ull << kWeightBits) | 1 : 0;
+        w1 = l1 == M ? (1ull << kWeightBits) | 1 : 0;
+        return;
+    }
+    Two p, e;
+    exponents(M, c, two(l0, l1), p, e);
+    const Two t = p + two(kSteps), g = p - (t - two(kSteps)), gs = g + e, ge = e - (gs - g);
+    const Two ln2 = two(kLn2), zh = gs * ln2;
+    const Two zl = fma2(ge, ln2, fma2(gs, two(kLn2Low), fma2(gs, ln2, gs * two(-kLn2))));
+    const Two s = fma2(zh * zh, fma2(zh, two(0.166666667f), two(-0.5f)), zl);
+    const Two whole = two(kWhole), a = fma2(zh, two(8589934592.f), whole);
+    const Two b = fma2(s + fma2(a - whole, two(-1.16415322e-10f), zh), two(4398046511104.f), whole);
+    constexpr uint32_t off = (kWholeBits << 9) + kWholeBits;
+    w0 = weight_of_parts(table, __uint_as_float(low_bits(p)), low_bits(t),
+                         static_cast<int>((low_bits(a) << 9) + low_bits(b) - off));
+    w1 = weight_of_parts(table, __uint_as_float(high_bits(p)), high_bits(t),
+                         static_cast<int>((high_bits(a) << 9) + high_bits(b) - off));
 }
 
 #endif  // __CUDACC__
