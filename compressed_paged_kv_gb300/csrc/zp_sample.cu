@@ -23,6 +23,8 @@
 //       asked for).  The bucket in which the count or the sum is reached is gathered and
 //       sorted; one of more than kList entries is cut up again by the bits of its
 //       values, until it fits or holds one value alone.
+#include <algorithm>
+
 #include "zp_sample.cuh"
 
 namespace zp {
@@ -31,8 +33,9 @@ namespace {
 
 constexpr int kSpThreads = 512;
 constexpr int kSpCtas = 8;       // of a cluster, at most: the portable most
-constexpr int kBuckets = 1024;
+constexpr int kBuckets = 512;
 constexpr int kList = 1024;
+constexpr int kSmall = 128;      // entries that are ordered by counting
 constexpr int kSpWarps = kSpThreads / 32;
 
 __device__ const WeightTable d_table{};
@@ -54,7 +57,7 @@ struct SpShared {
     uint64_t list[kList];
     uint64_t table[1024];
     uint32_t count[kBuckets];
-    uint32_t low[kBuckets], high[kBuckets];  // sums of weights, in two halves
+    uint32_t part[3][kBuckets];  // sums of weights' bits 0 .. 15, 16 .. 31 and 32 ..
     uint64_t runs[kSpCtas * kSpWarps];       // sums of the warps' runs
     uint32_t ties[kSpCtas * kSpWarps];       // their entries equal to tau
     uint64_t scan64[kSpWarps];
@@ -110,15 +113,6 @@ __device__ __forceinline__ void st_dsmem_u32(uint32_t addr, uint32_t v)
 __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, uint64_t v)
 {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t add_dsmem_u32(uint32_t addr, uint32_t v)
-{
-    uint32_t old;
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;"
-                 : "=r"(old)
-                 : "r"(addr), "r"(v)
-                 : "memory");
-    return old;
 }
 __device__ __forceinline__ void min_dsmem_u32(uint32_t addr, uint32_t v)
 {
@@ -180,26 +174,52 @@ __device__ __forceinline__ T block_before(T v, T *scratch, T &total)
     return __shfl_sync(0xffffffffu, wincl - w, wi) + incl - v;
 }
 
-// Sorts list[0 .. n) by the CTA, falling; n at most kList.
+// Sorts list[0 .. n) by the CTA, falling; n at most kList = 2 kSpThreads.  Every thread holds
+// two neighbours' places; what lies less than 64 apart is compared in a warp's registers.
 __device__ __forceinline__ void sort_falling(uint64_t *list, int n)
 {
-    int size = 2;
+    static_assert(kList == 2 * kSpThreads, "two entries a thread");
+    const int t = threadIdx.x, lane = t & 31;
+    int size = 64;
     while (size < n)
         size *= 2;
-    for (int j = n + threadIdx.x; j < size; j += kSpThreads)
-        list[j] = 0;
-    for (int span = 2; span <= size; span *= 2)
+    const bool active = (t & ~31) * 2 < size;  // whole warps
+    __syncthreads();
+    uint64_t a = 2 * t < n ? list[2 * t] : 0, b = 2 * t + 1 < n ? list[2 * t + 1] : 0;
+    for (int span = 2; span <= size; span *= 2) {
+        const bool falling = (2 * t & span) == 0;
         for (int d = span / 2; d; d /= 2) {
-            __syncthreads();
-            for (int t = threadIdx.x; t < size / 2; t += kSpThreads) {
-                const int p = 2 * t - (t & (d - 1)), q = p + d;
-                const uint64_t v = list[p], w = list[q];
-                if ((v < w) == ((p & span) == 0)) {
-                    list[p] = w;
-                    list[q] = v;
+            if (d >= 64) {  // the partner is in another warp
+                __syncthreads();
+                if (active) {
+                    list[2 * t] = a;
+                    list[2 * t + 1] = b;
                 }
+                __syncthreads();
+                if (active) {
+                    const uint64_t x = list[2 * t ^ d], y = list[2 * t + 1 ^ d];
+                    const bool take_more = ((2 * t & d) == 0) == falling;
+                    a = (a > x) == take_more ? a : x;
+                    b = (b > y) == take_more ? b : y;
+                }
+            } else if (d >= 2) {
+                const uint64_t x = __shfl_xor_sync(0xffffffffu, a, d / 2);
+                const uint64_t y = __shfl_xor_sync(0xffffffffu, b, d / 2);
+                const bool take_more = ((2 * lane & d) == 0) == falling;
+                a = (a > x) == take_more ? a : x;
+                b = (b > y) == take_more ? b : y;
+            } else if ((a < b) == falling) {
+                const uint64_t x = a;
+                a = b;
+                b = x;
             }
         }
+    }
+    __syncthreads();
+    if (active) {
+        list[2 * t] = a;
+        list[2 * t + 1] = b;
+    }
     __syncthreads();
 }
 
@@ -301,9 +321,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     for (int k = tid; k < 1024; k += kSpThreads)
         S.table[k] = d_table.v[k];
     for (int b = tid; b < kBuckets; b += kSpThreads)
-        S.count[b] = S.low[b] = S.high[b] = 0;
-    if (tid == 0)
-        S.listed = 0;
+        S.count[b] = S.part[0][b] = S.part[1][b] = S.part[2][b] = 0;
     for (int j = 0; j < J; ++j) {
         const int g = g0 + j * 32 + lane;
         if (g >= c0 && g < c1)
@@ -451,13 +469,23 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             take(v[k + 1], w1);
         }
     };
-    auto within = [&](float v) {  // min_p's part
-        if (!(min_p > 0.f))
-            return v > -INFINITY;
+    // The least value whose weight is at least min_p: the gap of T ln(1 / min_p) to the
+    // maximum, as a value, is found to within a step or two, and the lanes test the values
+    // around.  Without min_p the least finite one.
+    float least = -3.4028235e38f;
+    if (min_p > 0.f) {
+        const double at =
+            static_cast<double>(M) - (static_cast<double>(gap_h) + static_cast<double>(gap_l));
+        const float near = fmaxf(static_cast<float>(at), least);
+        const uint32_t key = key_of(fminf(near, M)) - 16 + lane;
+        const float v = value_of(key);
         float h, l;
         gap(M, v, h, l);
-        return h < gap_h || (h == gap_h && l <= gap_l);
-    };
+        const bool enough = key >= key_of(M) || h < gap_h || (h == gap_h && l <= gap_l);
+        const unsigned m = __ballot_sync(0xffffffffu, enough);
+        least = fminf(__shfl_sync(0xffffffffu, v, m ? __ffs(m) - 1 : 31), M);
+    }
+    auto within = [&](float v) { return v >= least; };  // min_p's part
     const uint64_t kNone = 0;  // (an entry of the list that is none)
     auto entry_of = [&](float v, int j, int k) {  // falling by value, then rising by index
         return static_cast<uint64_t>(key_of(v)) << 32 |
@@ -471,35 +499,57 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     cut.m = 0x7fffffff;
     const float range = fminf(64.f / c.ch, M - bottom);
     const float per_gap = range > 0.f ? kBuckets / range : 0.f;
-    auto bucket_of = [&](float v) {  // falls with v
-        const float b = v == M ? 0.f : (M - v) * per_gap;
-        return min(kBuckets - 1, static_cast<int>(b));
+    constexpr float kBig = 3.4e38f;  // (in place of infinite logits)
+    const float big_M = fminf(M, kBig);
+    auto place_of = [&](float v) { return (big_M - fminf(v, kBig)) * per_gap; };  // falls with v
+    auto bucket_of = [&](float v) { return min(kBuckets - 1, static_cast<int>(place_of(v))); };
+    // Whether v lies in the buckets from .. to: `from` and `to` + 1 as numbers, `to` + 1
+    // infinite for the last.
+    auto in_buckets = [&](float v, float from, float end) {
+        const float at = place_of(v);
+        return at >= from && (at < end || end == INFINITY) && v > -INFINITY;
     };
-    // CTA 0's sums of the CTAs' histograms.
+    auto end_of = [&](int b) {
+        return b >= kBuckets - 1 ? INFINITY : static_cast<float>(b + 1);
+    };
+    // CTA 0's sums of the CTAs' histograms: of the weights, a bucket's 64 bits in part[1] and
+    // part[0].
     auto gather_sums = [&](bool counts, bool weights) {
+        static_assert(kBuckets == kSpThreads, "a bucket a thread");
         all_ctas();
-        if (rank == 0)
-            for (int b = tid; b < kBuckets; b += kSpThreads) {
-                uint32_t n = S.count[b];
-                uint64_t w = static_cast<uint64_t>(S.high[b]) << 32 | S.low[b];
-                for (int r = 1; r < ctas; ++r) {
-                    if (counts)
-                        n += ld_dsmem_u32(dsmem_addr(&S.count[b], r));
-                    if (weights)
-                        w += static_cast<uint64_t>(ld_dsmem_u32(dsmem_addr(&S.high[b], r))) << 32 |
-                             ld_dsmem_u32(dsmem_addr(&S.low[b], r));
-                }
-                S.count[b] = n;
-                S.low[b] = static_cast<uint32_t>(w);
-                S.high[b] = static_cast<uint32_t>(w >> 32);
-            }
+        if (rank != 0)
+            return;
+        uint32_t n[kSpCtas], w[3][kSpCtas];  // all on their way at once
+#pragma unroll
+        for (int r = 0; r < kSpCtas; ++r) {
+            n[r] = w[0][r] = w[1][r] = w[2][r] = 0;
+            if (counts && r < ctas)
+                n[r] = ld_dsmem_u32(dsmem_addr(&S.count[tid], r));
+            if (weights && r < ctas)
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    w[k][r] = ld_dsmem_u32(dsmem_addr(&S.part[k][tid], r));
+        }
+        uint32_t all = 0;
+        uint64_t sum = 0;
+#pragma unroll
+        for (int r = 0; r < kSpCtas; ++r) {
+            all += n[r];
+            sum += w[0][r] + (static_cast<uint64_t>(w[1][r]) << 16) +
+                   (static_cast<uint64_t>(w[2][r]) << 32);
+        }
+        S.count[tid] = all;
+        S.part[0][tid] = static_cast<uint32_t>(sum);
+        S.part[1][tid] = static_cast<uint32_t>(sum >> 32);
     };
+    // (a CTA has at most 2^15.5 entries, so that no sum of 16 bits of each passes 32)
     auto add_weight = [&](int b, uint64_t w) {
-        const uint32_t low = static_cast<uint32_t>(w);
-        const uint32_t old = atomicAdd(&S.low[b], low);
-        const uint32_t high = static_cast<uint32_t>(w >> 32) + (old + low < old);
+        const uint32_t low = static_cast<uint32_t>(w), high = static_cast<uint32_t>(w >> 32);
+        atomicAdd(&S.part[0][b], low & 0xffffu);
+        if (low >> 16)
+            atomicAdd(&S.part[1][b], low >> 16);
         if (high)
-            atomicAdd(&S.high[b], high);
+            atomicAdd(&S.part[2][b], high);
     };
     // Every entry above -infinity is counted under `place` (below 0: not at all).
     auto histogram = [&](bool counts, bool weights, auto place) {
@@ -521,45 +571,56 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     };
     auto clear = [&] {
         for (int b = tid; b < kBuckets; b += kSpThreads)
-            S.count[b] = S.low[b] = S.high[b] = 0;
+            S.count[b] = S.part[0][b] = S.part[1][b] = S.part[2][b] = 0;
         __syncthreads();
     };
     // CTA 0 alone: the bucket where `above` + counts reach `k`, or `mass` + weights reach
     // `target` (k = 0), from the largest values on, which the last buckets of a `rising`
-    // histogram hold and the first of the other.  bucket < 0: fewer entries than k.
+    // histogram hold and the first of the other.  bucket < 0: fewer entries than k.  `in`
+    // becomes about the number of entries up to the bucket, of a first histogram by weights.
     auto find = [&](uint32_t k, uint64_t target, bool rising) {
-        constexpr int PB = kBuckets / kSpThreads;
-        __syncthreads();
-        uint32_t n = 0, all_n;
-        uint64_t w = 0, all_w;
-        uint32_t nb[PB];
-        uint64_t wb[PB];
-#pragma unroll
-        for (int j = 0; j < PB; ++j) {
-            const int b = rising ? kBuckets - 1 - (tid * PB + j) : tid * PB + j;
-            n += nb[j] = S.count[b];
-            w += wb[j] = static_cast<uint64_t>(S.high[b]) << 32 | S.low[b];
+        const int b = rising ? kBuckets - 1 - tid : tid;  // (the thread's own sums, if falling)
+        if (rising)
+            __syncthreads();
+        const uint32_t n = S.count[b];
+        const uint64_t w = static_cast<uint64_t>(S.part[1][b]) << 32 | S.part[0][b];
+        const uint32_t upto_n = warp_incl(n, lane);
+        const uint64_t upto_w = warp_incl(w, lane);
+        if (lane == 31) {
+            S.scan32[wi] = upto_n;
+            S.scan64[wi] = upto_w;
         }
-        uint32_t n0 = S.cut.above + block_before(n, S.scan32, all_n);
-        uint64_t w0 = S.cut.mass + block_before(w, S.scan64, all_w);
-        __syncthreads();  // S.cut is read
+        __syncthreads();
+        const uint32_t sn = lane < kSpWarps ? S.scan32[lane] : 0;
+        const uint64_t sw = lane < kSpWarps ? S.scan64[lane] : 0;
+        const uint32_t in = warp_incl(sn, lane);
+        const uint64_t iw = warp_incl(sw, lane);
+        const uint32_t n0 = S.cut.above + __shfl_sync(0xffffffffu, in - sn, wi) + upto_n - n;
+        const uint64_t w0 = S.cut.mass + __shfl_sync(0xffffffffu, iw - sw, wi) + upto_w - w;
+        const uint32_t all_n = __shfl_sync(0xffffffffu, in, 31);
+        const uint64_t all_w = __shfl_sync(0xffffffffu, iw, 31);
+        __syncthreads();  // S.cut and the scans are read
+        const bool here = k ? n0 < k && n0 + n >= k : w0 < target && w0 + w >= target;
         if (tid == 0 && k > all_n && !rising) {
             S.cut.mass = all_w;
             S.cut.bucket = -1;
             S.cut.tau = -INFINITY;
             S.cut.m = 0x7fffffff;
         }
-#pragma unroll
-        for (int j = 0; j < PB; ++j) {
-            const bool here =
-                k ? n0 < k && n0 + nb[j] >= k : w0 < target && w0 + wb[j] >= target;
-            if (here) {
-                S.cut.above = n0;
-                S.cut.mass = w0;
-                S.cut.bucket = rising ? kBuckets - 1 - (tid * PB + j) : tid * PB + j;
-            }
-            n0 += nb[j];
-            w0 += wb[j];
+        if (tid == 0)
+            S.cut.in = 0;
+        if (here) {
+            S.cut.above = n0;
+            S.cut.mass = w0;
+            S.cut.bucket = b;
+        }
+        if (!rising && k == 0) {
+            __syncthreads();
+            if (w0 < target)  // 2^-44 w over the weight in the bucket's middle
+                atomicAdd(&S.cut.in,
+                          static_cast<uint32_t>(fminf(static_cast<float>(w) * 5.6843419e-14f *
+                                                          exp2f((b + 0.5f) / per_gap * c.ch),
+                                                      1e6f)) + 1);
         }
         __syncthreads();
     };
@@ -578,20 +639,58 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         all_ctas();
         cut = S.told[turn];
     };
-    // The entries for which `inside` holds into CTA 0's list, which counts them all.
+    // The entries for which `inside` holds into the CTAs' lists, and these, if that is not too
+    // much, one behind the other into CTA 0's; there, how many entries there are.
     auto gather = [&](auto inside) {
+        __syncthreads();
+        if (tid == 0)
+            S.listed = 0;
+        __syncthreads();
         for (int j = 0; j < J; ++j) {
             float v[VE];
             unpack(run[j * 32 + lane], v);
+            bool in[VE], any = false;
 #pragma unroll
             for (int k = 0; k < VE; ++k)
-                if (inside(v[k])) {
-                    const uint32_t at = add_dsmem_u32(dsmem_addr(&S.listed, 0), 1);
+                any |= in[k] = inside(v[k]);
+            if (!any)
+                continue;
+#pragma unroll
+            for (int k = 0; k < VE; ++k)
+                if (in[k]) {
+                    const uint32_t at = atomicAdd(&S.listed, 1u);
                     if (at < kList)
-                        st_dsmem_u64(dsmem_addr(&S.list[at], 0), entry_of(v[k], j, k));
+                        S.list[at] = entry_of(v[k], j, k);
                 }
         }
         all_ctas();
+        uint32_t n = S.listed;
+        if (rank == 0) {
+            // lane r: CTA r's entries, and those before them
+            const uint32_t theirs =
+                lane < ctas ? ld_dsmem_u32(dsmem_addr(&S.listed, lane)) : 0;
+            const uint32_t upto = warp_incl(theirs, lane);
+            n = __shfl_sync(0xffffffffu, upto, 31);
+            // (CTA 0's own lie at the front already)
+            uint32_t first[kSpCtas];
+#pragma unroll
+            for (int r = 0; r < kSpCtas; ++r)
+                first[r] = __shfl_sync(0xffffffffu, upto - theirs, r);
+            for (uint32_t p = tid; n <= kList && p < n; p += kSpThreads) {
+                int from = 0;
+                uint32_t at = p;
+#pragma unroll
+                for (int r = 1; r < kSpCtas; ++r)
+                    if (r < ctas && p >= first[r]) {
+                        from = r;
+                        at = p - first[r];
+                    }
+                if (from)
+                    S.list[p] = ld_dsmem_u64(dsmem_addr(&S.list[at], from));
+            }
+            __syncthreads();
+        }
+        return n;
     };
     // CTA 0: of its sorted list of n, the entry at which the count (with `above`) reaches
     // k, or the weights (with `mass`) reach `target`; tau, what is kept of it, the weights.
@@ -639,12 +738,83 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         __syncthreads();
     };
     const bool by_mass = top_p < 1.f;
-    // CTA 0: the cuts of what it has gathered, if it all fitted in the list, and the token.
+    // The same of at most kSmall entries: a thread an entry, which adds up what comes before it
+    // by value, and then by index.
+    auto finish_small = [&](int n, uint64_t row_sum) {
+        uint64_t *entries = S.list, *sums = S.list + kSmall;
+        const bool mine = tid < n;
+        const uint64_t e = mine ? entries[tid] : 0;
+        const float v = mine ? value_at(e) : -INFINITY;
+        uint64_t w = 0;
+        if (wi < kSmall / 32)
+            w = mine ? weight_of(v) : 0;
+        if (tid < kSmall)
+            sums[tid] = w;
+        if (tid == 0) {
+            S.cut.lo = 0;
+            S.equal = S.equal_upto = 0;
+        }
+        __syncthreads();
+        int rank_of = 0;
+        uint64_t above = 0;
+        const int in_k = top_k > 0 ? min(top_k, n) : n;
+        if (mine) {
+            for (int q = 0; q < n; ++q)
+                if (entries[q] > e) {
+                    ++rank_of;
+                    above += sums[q];
+                }
+            if (rank_of == in_k - 1)
+                S.scan64[0] = above + w;  // of the top_k
+        }
+        __syncthreads();
+        uint64_t target = ~0ull;
+        if (by_mass)
+            target = top_p > 0.f
+                         ? max(target_of(top_p, row_sum ? row_sum : S.scan64[0]), uint64_t(1))
+                         : 1;
+        const bool in = mine && rank_of < in_k && above < target;
+        const uint64_t kept_w = in && within(v) ? w : 0;
+        if (tid < kSmall)
+            sums[tid] = kept_w;
+        if (in)
+            atomicMax(&S.cut.lo, static_cast<uint32_t>(rank_of) + 1);
+        __syncthreads();
+        if (in && rank_of + 1 == static_cast<int>(S.cut.lo))
+            S.cut.tau = v;
+        uint64_t total = 0, before = 0;
+        if (mine)
+            for (int q = 0; q < n; ++q) {
+                total += sums[q];
+                // (the low halves fall with the index)
+                if (static_cast<uint32_t>(entries[q]) > static_cast<uint32_t>(e))
+                    before += sums[q];
+            }
+        __syncthreads();
+        if (mine && v == S.cut.tau) {
+            atomicAdd(&S.equal, 1u);
+            if (in)
+                atomicAdd(&S.equal_upto, 1u);
+        }
+        if (tid == 0)
+            S.cut.mass = total;
+        if (mine && a.tokens) {
+            const uint64_t level = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
+            if (before <= level && level < before + kept_w)
+                a.tokens[i] =
+                    static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)) - mis;
+        }
+        __syncthreads();
+        if (tid == 0) {
+            S.cut.in = S.equal;
+            S.cut.m = static_cast<int>(S.equal_upto);
+        }
+    };
+    // CTA 0: the cuts of the n entries it has gathered, if they fit in the list, and the token.
     // row_sum: the weights that top_p is a part of, 0 for those of the top_k.
-    auto finish = [&](uint64_t row_sum) {
+    auto finish = [&](int n, uint64_t row_sum) {
         if (rank != 0)
             return;
-        const int n = static_cast<int>(S.listed);
         __syncthreads();
         if (tid == 0) {
             S.cut = Cut{};
@@ -652,7 +822,9 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             S.cut.tau = -INFINITY;
             S.cut.m = 0x7fffffff;
         }
-        if (n <= kList) {
+        if (n <= kSmall) {
+            finish_small(n, row_sum);
+        } else if (n <= kList) {
             sort_falling(S.list, n);
             int kept = n;
             if (top_k > 0 && n >= top_k) {
@@ -725,34 +897,35 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     };
     bool counted = false;  // CTA 0 holds the first histogram's sums
     // The cut where the count reaches k, or (k = 0) the weights reach `target`.
-    auto select = [&](uint32_t k, uint64_t target, bool weights) {
+    // `found`: its bucket is.
+    auto select = [&](uint32_t k, uint64_t target, bool weights, bool found) {
         if (!counted) {
             clear();
             histogram(k > 0, weights, bucket_of);
         }
         counted = true;
-        if (rank == 0) {
-            __syncthreads();
-            if (tid == 0) {
-                S.cut = Cut{};
-                S.listed = 0;
+        if (!found) {
+            if (rank == 0) {
+                __syncthreads();
+                if (tid == 0)
+                    S.cut = Cut{};
+                __syncthreads();
+                find(k, target, false);
             }
-            find(k, target, false);
+            tell();
         }
-        tell();
         const int bucket = cut.bucket;
         if (bucket < 0)
             return;
         uint32_t lo = 0, hi = 0xffffffffu;
+        const float from = static_cast<float>(bucket), end = end_of(bucket);
         auto inside = [&](float v) {
-            const uint32_t key = key_of(v);
-            return v > -INFINITY && bucket_of(v) == bucket && key >= lo && key <= hi;
+            return in_buckets(v, from, end) && key_of(v) >= lo && key_of(v) <= hi;
         };
         for (;;) {
-            gather(inside);
-            if (rank == 0 && tid == 0)
-                S.cut.in = S.listed;
+            const uint32_t n = gather(inside);
             if (rank == 0 && tid == 0) {
+                S.cut.in = n;
                 S.key_lo = 0xffffffffu;
                 S.key_hi = 0;
             }
@@ -783,7 +956,6 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             if (rank == 0 && tid == 0) {
                 S.cut.lo = S.key_lo;
                 S.cut.hi = S.key_hi;
-                S.listed = 0;
             }
             tell();
             lo = cut.lo;
@@ -831,12 +1003,12 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         if (rank == 0) {
             if (tid == 0)
                 S.cut = Cut{};
+            __syncthreads();
             find(static_cast<uint32_t>(top_k), 0, false);
         }
         tell();
-        const int most = cut.bucket < 0 ? kBuckets - 1 : cut.bucket;
-        gather([&](float v) { return v > -INFINITY && bucket_of(v) <= most; });
-        finish(0);
+        const float end = end_of(cut.bucket < 0 ? kBuckets - 1 : cut.bucket);
+        finish(static_cast<int>(gather([&](float v) { return in_buckets(v, 0.f, end); })), 0);
         tell();
         listed = cut.done != 0;
         if (listed && a.tokens)
@@ -848,7 +1020,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         }
     }
     if (!listed && top_k > 0)
-        select(static_cast<uint32_t>(top_k), 0, by_mass);
+        select(static_cast<uint32_t>(top_k), 0, by_mass, false);
     auto cluster_total = [&](uint64_t s) {  // of all threads' s; the warps' sums in S.runs
         s = warp_sum(s);
         if (lane < ctas)
@@ -864,10 +1036,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         if (top_k == 0) {  // of the whole row
             clear();
             uint64_t s = 0;
+            // weights below half of (1 - top_p) / vocab are, together, less than what may be left
+            // out: the cut lies above them
+            const float low = 17592186044416.f * 0.5f * (1.f - fmaxf(top_p, 0.f)) /
+                              static_cast<float>(a.vocab);
+            const uint64_t least = max(static_cast<uint64_t>(low), uint64_t(1));
             for (int j = 0; j < J; ++j)
                 each_weight(j, [&](float v, uint64_t w) {
                     s += w;
-                    if (w)
+                    if (w >= least)
                         add_weight(bucket_of(v), w);
                 });
             sum = cluster_total(s);
@@ -875,25 +1052,28 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             counted = true;
         }
         const uint64_t target = top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
-        if (top_k == 0) {  // all down to the bucket of the cut, if that is not too much
+        bool found = top_k == 0;
+        if (found) {  // all down to the bucket of the cut, if that is not too much
             if (rank == 0) {
-                if (tid == 0) {
+                if (tid == 0)
                     S.cut = Cut{};
-                    S.listed = 0;
-                }
+                __syncthreads();
                 find(0, target, false);
             }
             tell();
-            const int most = cut.bucket;
-            gather([&](float v) { return v > -INFINITY && bucket_of(v) <= most; });
-            finish(sum);
-            tell();
-            listed = cut.done != 0;
-            if (listed && a.tokens)
-                return;
+            const float end = end_of(cut.bucket);
+            if (cut.in < kList * 9 / 10) {  // (a bucket's weights are within 9 %)
+                finish(static_cast<int>(gather([&](float v) { return in_buckets(v, 0.f, end); })),
+                       sum);
+                tell();
+                listed = cut.done != 0;
+                if (listed && a.tokens)
+                    return;
+                found = false;
+            }
         }
         if (!listed)
-            select(0, target, true);
+            select(0, target, true, found);
     }
     const bool cuts = top_k > 0 || by_mass;
     const bool partial = cuts && cut.m < static_cast<int>(cut.in);
@@ -918,12 +1098,13 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             t += S.ties[r];
         ties_before = static_cast<int>(warp_sum(t));
     }
+    const float from = fmaxf(cut.tau, least);  // the least value kept
     auto kept = [&](float v, int before) {
-        return (v > cut.tau || (v == cut.tau && (!partial || before < cut.m))) && within(v);
+        return v >= from && (!partial || v != cut.tau || before < cut.m);
     };
-    // The lane's kept weights of step j, `t` entries equal to tau before the step; t moves on.
-    auto step_sum = [&](int j, int &t) {
-        float v[VE];
+    // Which of the lane's values of step j are kept, a bit each; `t` entries equal to tau come
+    // before the step, and t moves on.
+    auto step = [&](int j, int &t, float (&v)[VE]) {
         unpack(run[j * 32 + lane], v);
         int before = 0;
         if (partial) {
@@ -935,13 +1116,26 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             before = t + upto - n;
             t += __shfl_sync(0xffffffffu, upto, 31);
         }
-        uint64_t s = 0;
+        unsigned mask = 0;
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
-            if (kept(v[k], before))
-                s += weight_of(v[k]);
+            mask |= kept(v[k], before) ? 1u << k : 0u;
             before += v[k] == cut.tau;
         }
+        return mask;
+    };
+    // The lane's kept weights of step j.
+    auto step_sum = [&](int j, int &t) {
+        float v[VE];
+        const unsigned mask = step(j, t, v);
+        uint64_t s = 0;
+#pragma unroll
+        for (int k = 0; k < VE; k += 2)
+            if (mask >> k & 3) {
+                uint64_t w0, w1;
+                weights(S.table, c, M, v[k], v[k + 1], w0, w1);
+                s += (mask >> k & 1 ? w0 : 0) + (mask >> k & 2 ? w1 : 0);
+            }
         return s;
     };
     if (a.tokens) {
@@ -950,9 +1144,40 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         if (!cuts && !(min_p > 0.f))
             for (int j = 0; j < J; ++j)
                 each_weight(j, [&](float, uint64_t w) { s += w; });
-        else
-            for (int j = 0; j < J; ++j)
-                s += step_sum(j, t);
+        else {
+            // few are kept: the values of kept ones side by side, 64 at a time
+            float *line = reinterpret_cast<float *>(&S.part[0][0]) + wi * 96;
+            static_assert(sizeof(S.part) >= kSpWarps * 96 * 4, "a line a warp");
+            int n = 0;
+            auto take = [&] {
+                uint64_t w0, w1;
+                __syncwarp();
+                weights(S.table, c, M, lane < n ? line[lane] : -INFINITY,
+                        lane + 32 < n ? line[lane + 32] : -INFINITY, w0, w1);
+                s += w0 + w1;
+                const float rest = line[lane + 64];
+                __syncwarp();
+                line[lane] = rest;
+                __syncwarp();
+                n -= 64;
+            };
+            for (int j = 0; j < J; ++j) {
+                float v[VE];
+                const unsigned mask = step(j, t, v);
+#pragma unroll
+                for (int k = 0; k < VE; ++k) {
+                    const unsigned m = __ballot_sync(0xffffffffu, mask >> k & 1);
+                    if (!m)
+                        continue;
+                    if (mask >> k & 1)
+                        line[n + __popc(m & ((1u << lane) - 1))] = v[k];
+                    n += __popc(m);
+                    if (n >= 64)
+                        take();
+                }
+            }
+            take();
+        }
         all_ctas();  // (S.runs may still be read)
         const uint64_t total = cluster_total(s);
         const uint64_t level = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
@@ -990,24 +1215,17 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 continue;
             }
             float v[VE];
-            unpack(run[j * 32 + lane], v);
-            int n = 0;
-#pragma unroll
-            for (int k = 0; k < VE; ++k)
-                n += partial && v[k] == cut.tau;
-            int before = t0 + warp_incl(n, lane) - n;
+            const unsigned mask = step(j, t0, v);
             if (lane == __ffs(past) - 1) {
                 uint64_t sum = upto - w;
                 int tok = -1;
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    if (tok < 0 && kept(v[k], before)) {
+                for (int k = 0; k < VE; ++k)
+                    if (tok < 0 && (mask >> k & 1)) {
                         sum += weight_of(v[k]);
                         if (sum > level)
                             tok = (g0 + j * 32 + lane) * VE + k - mis;
                     }
-                    before += v[k] == cut.tau;
-                }
                 a.tokens[i] = tok;
             }
             return;
@@ -1070,10 +1288,13 @@ static cudaError_t launch_sample_t(const SampleArgs &a, int sms, cudaStream_t s)
         return (a.vocab + 2 * VE - 2) / VE / (ctas * kSpThreads) + 1;
     };
     auto bytes_of = [&](int ctas) { return kShared + steps_of(ctas) * kSpThreads * 16; };
+    // As many CTAs as the SMs hold at once, two each, up to eight a row and up to a vector a
+    // lane; at least so many that two fit on an SM (96 rows of 50,257 bf16 logits with
+    // filters of all kinds: 3 CTAs a row 56 us, 2 67)
+    const int most = static_cast<int>(std::min<long long>(kSpCtas, std::max(1, 2 * sms / a.R)));
     int ctas = 1;
-    while (ctas < kSpCtas && (bytes_of(ctas) > 112 * 1024 || a.R * 2ll * ctas <= 2ll * sms) &&
-           steps_of(ctas) > 1)
-        ctas *= 2;
+    while (ctas < kSpCtas && (bytes_of(ctas) > 112 * 1024 || ctas < most) && steps_of(ctas) > 1)
+        ++ctas;
     const size_t bytes = bytes_of(ctas);
     cudaError_t err = cudaFuncSetAttribute(zp_sample_kernel<T>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
