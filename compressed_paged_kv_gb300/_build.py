@@ -24,7 +24,7 @@ SOURCES = ["zp_api.cu", "zp_compress.cu", "zp_compress_d64.cu", "zp_compress_d12
            "zp_redundancy_global.cu", "zp_redundancy_gram.cu", "zp_blocks.cu", "zp_tmap.cu",
            "zp_chunk_append.cu", "zp_chunk_attn.cu", "zp_verify.cu",
            "zp_fp8_append.cu", "zp_fp8_decode.cu",
-           "zp_fp8_chunk_attn.cu", "zp_sample.cu"]
+           "zp_fp8_chunk_attn.cu", "zp_fp8_widen.cu", "zp_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -201,6 +201,12 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
     const size_t ca_arr = 4 * (4 * static_cast<size_t>(c->num_sms) + 1);  // and ca_entered
     const size_t o_ca_arr = A.take(ca_arr);
     const size_t o_ca_part = A.take(4 * zp::chunk_attn_part_floats(D.head_dim, c->num_sms));
+    const int wide = fp8 ? zp::fp8_wide_blocks(D.num_blocks, D.num_kv_heads, D.head_dim) : 0;
+    const size_t wide_bytes = 2ull * wide * D.num_kv_heads * zp::kBlk * D.head_dim;
+    const size_t o_wide_places = A.take(fp8 ? 4 * static_cast<size_t>(D.max_requests) : 0);
+    const size_t o_wide_maps = A.take(fp8 ? 2 * sizeof(CUtensorMap) : 0, 128);
+    const size_t o_wide_k = A.take(wide_bytes);
+    const size_t o_wide_v = A.take(wide_bytes);
     const size_t total = A.take(0);
 
     if (cudaMalloc(&c->base, total) != cudaSuccess) {
@@ -239,6 +245,13 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
     ws.ca_arrived = reinterpret_cast<uint32_t *>(b + o_ca_arr);
     ws.ca_entered = ws.ca_arrived + 4 * c->num_sms;
     ws.ca_part = reinterpret_cast<float *>(b + o_ca_part);
+    if (fp8) {
+        ws.wide_places = reinterpret_cast<int32_t *>(b + o_wide_places);
+        ws.wide_maps = reinterpret_cast<CUtensorMap *>(b + o_wide_maps);
+        ws.wide_k = reinterpret_cast<__nv_bfloat16 *>(b + o_wide_k);
+        ws.wide_v = reinterpret_cast<__nv_bfloat16 *>(b + o_wide_v);
+        ws.wide_blocks = wide;
+    }
     c->kpools.assign(D.k_pools, D.k_pools + D.num_layers);
     c->vpools.assign(D.v_pools, D.v_pools + D.num_layers);
     c->fp8 = fp8;
@@ -264,9 +277,15 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
              zp::encode_row_map(&krmaps[l], D.k_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim) &&
              zp::encode_row_map(&vrmaps[l], D.v_pools[l], D.num_blocks, D.num_kv_heads, D.head_dim);
     }
-    ok = ok &&
-         (fp8 ? zp::prepare_fp8_chunk_attn(D.head_dim) : zp::prepare_chunk_attn(D.head_dim)) ==
-             cudaSuccess &&
+    CUtensorMap wide_maps[2] = {};
+    if (fp8)
+        ok = ok &&
+             zp::encode_pool_map(&wide_maps[0], ws.wide_k, wide, D.num_kv_heads, D.head_dim) &&
+             zp::encode_pool_map(&wide_maps[1], ws.wide_v, wide, D.num_kv_heads, D.head_dim) &&
+             zp::prepare_fp8_chunk_attn(D.head_dim) == cudaSuccess &&
+             cudaMemcpy(ws.wide_maps, wide_maps, sizeof(wide_maps), cudaMemcpyHostToDevice) ==
+                 cudaSuccess;
+    ok = ok && zp::prepare_chunk_attn(D.head_dim) == cudaSuccess &&
          cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
          cudaMemset(b + o_rowmark, 0, 4 * static_cast<size_t>(D.max_requests)) == cudaSuccess &&
          cudaMemset(b + o_ap_call, 0, o_ap_occ - o_ap_call) == cudaSuccess &&
@@ -1082,15 +1101,53 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     a.arrived = c->ws.ca_arrived;
     a.entered = c->ws.ca_entered;
     a.sticky = c->ws.sticky;
-    if (c->fp8) {
-        a.kscale = c->kscales[layer];
-        a.vscale = c->vscales[layer];
-    }
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return (c->fp8 ? zp::launch_fp8_chunk_attn(a, c->d, c->num_sms, s)
-                   : zp::launch_chunk_attn(a, c->d, c->num_sms, s)) == cudaSuccess
-               ? ZP_OK
-               : ZP_ERR_CUDA;
+    if (!c->fp8)
+        return zp::launch_chunk_attn(a, c->d, c->num_sms, s) == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
+    a.kscale = c->kscales[layer];
+    a.vscale = c->vscales[layer];
+    // Requests with many query rows over widened blocks, the others over the cache, if the
+    // batch has many rows a request: two kernels one after the other cost a mixed batch more
+    // than the widened blocks gain (60 single tokens beside two pieces of 900, 64 dims: 138 us
+    // that way, 118 in one kernel; 19 chunks of 64 over 8,192, none of them long: 173, 153).
+    const long long G = c->Hq / c->Hkv;
+    if (total * G >= static_cast<long long>(R) * zp::kWideMeanRows) {
+        zp::Fp8WidenArgs w{};
+        w.kpool = static_cast<const uint8_t *>(c->kpools[layer]);
+        w.vpool = static_cast<const uint8_t *>(c->vpools[layer]);
+        w.kscale = a.kscale;
+        w.vscale = a.vscale;
+        w.kwide = c->ws.wide_k;
+        w.vwide = c->ws.wide_v;
+        w.places = c->ws.wide_places;
+        w.capacity = c->ws.wide_blocks;
+        w.least = static_cast<int32_t>((zp::kWideRows + G - 1) / G);
+        w.starts = starts;
+        w.total = total;
+        w.tables = block_tables;
+        w.stride = bt_stride;
+        w.num_rows = num_rows;
+        w.lengths = lengths;
+        w.req_idx = req_idx;
+        w.R = R;
+        w.Hkv = c->Hkv;
+        w.d = c->d;
+        w.num_blocks = c->num_blocks;
+        w.sticky = c->ws.sticky;
+        if (zp::launch_fp8_widen(w, c->num_sms, s) != cudaSuccess)
+            return ZP_ERR_CUDA;
+        a.places = c->ws.wide_places;
+        zp::ChunkAttnArgs b = a;
+        b.kmap = c->ws.wide_maps;
+        b.vmap = c->ws.wide_maps + 1;
+        b.kpool = c->ws.wide_k;
+        b.vpool = c->ws.wide_v;
+        b.num_blocks = c->ws.wide_blocks;
+        b.widened = 1;
+        if (zp::launch_chunk_attn(b, c->d, c->num_sms, s) != cudaSuccess)
+            return ZP_ERR_CUDA;
+    }
+    return zp::launch_fp8_chunk_attn(a, c->d, c->num_sms, s) == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
 }
 
 zp_status zp_verify_draft(zp_cache *c, const int32_t *tokens, const int32_t *starts,

@@ -46,6 +46,11 @@ struct ChunkAttnArgs {
     uint32_t *entered;  // CTAs that have entered a call, modulo two calls'
     int32_t *sticky;
     const float *kscale, *vscale;  // of an 8-bit cache, whose pools hold bytes
+    // An 8-bit cache's batch of which some requests' blocks are widened to bf16: their first
+    // block there, below 0 for the others (null: none is).  widened: the call over those, whose
+    // pools and maps are theirs, else the one over the cache.
+    const int32_t *places;
+    int32_t widened;
 };
 
 struct VerifyArgs {

@@ -261,6 +261,28 @@ __host__ __device__ __forceinline__ void make_shares(CaPlan &pl, long long cost,
     pl.share = quotient(cost + pl.ctas - 1, pl.ctas);
 }
 
+// Request i, if it is this call's: of an 8-bit cache's batch the requests with a place
+// among the widened blocks are the call's over those, with the place for a table row, and
+// the others the call's over the cache.
+__host__ __device__ __forceinline__ bool attn_request(const ChunkAttnArgs &a, int i, ChunkReq &c,
+                                                      bool *bad)
+{
+    if (!chunk_request(a, i, c, bad))
+        return false;
+    if (!a.places)
+        return true;
+    const int at = a.places[i];
+    if (a.widened)
+        c.row = at;
+    return (at >= 0) == (a.widened != 0);
+}
+
+// Block q of the request with table row `row`.
+__device__ __forceinline__ int block_at(const ChunkAttnArgs &a, int row, int q)
+{
+    return a.widened ? row + q : a.tables[static_cast<size_t>(row) * a.stride + q];
+}
+
 // Walks this CTA's items; every role walks the same ones on its own.
 struct CaWalk {
     const ChunkAttnArgs &a;
@@ -291,7 +313,7 @@ struct CaWalk {
     {
         bool bad;
         for (; i < a.R; ++i)
-            if (chunk_request(a, i, it.c, &bad))
+            if (attn_request(a, i, it.c, &bad))
                 break;
         if (i >= a.R)
             return false;
@@ -873,7 +895,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         ChunkReq c;  // the last one
         for (int i = r0; i < r1; ++i) {
             bool bad;
-            if (chunk_request(a, i, c, &bad)) {
+            if (attn_request(a, i, c, &bad)) {
                 mine += a.Hkv * head_cost(c, tpt);
                 longest = max(longest, longest_item(c, tpt));
             }
@@ -920,7 +942,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             p.c0 = c;
             for (int i = r0; i < r1 && per > 1; ++i) {  // the request the share begins in
                 bool bad;
-                if (!chunk_request(a, i, p.c0, &bad))
+                if (!attn_request(a, i, p.c0, &bad))
                     continue;
                 p.i0 = i;
                 const long long w = a.Hkv * head_cost(p.c0, tpt);
@@ -976,7 +998,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         auto block_y = [&](const CaDesc &d, int q) {
             if (q * kBlk >= d.len)
                 return -kBlk;
-            const int blk = a.tables[(size_t)d.row * a.stride + q];
+            const int blk = block_at(a, d.row, q);
             if (blk < 0 || blk >= a.num_blocks) {
                 set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
                 return -kBlk;
@@ -1812,7 +1834,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     const int from = max(d.pos0 + 1, d.ka * kTile);
                     const int to = min(d.pos0 + d.ntok, d.kb * kTile);
                     for (int b = from / kBlk; b * kBlk < to; ++b) {
-                        const int blk = a.tables[static_cast<size_t>(d.row) * a.stride + b];
+                        const int blk = block_at(a, d.row, b);
                         if (blk < 0 || blk >= a.num_blocks)
                             continue;
                         const size_t at =

@@ -52,6 +52,33 @@ struct Fp8AttnArgs {
     int32_t *sticky;
 };
 
+// The blocks of the requests with many query rows to bf16 (zp_fp8_widen.cu).
+struct Fp8WidenArgs {
+    const uint8_t *kpool, *vpool;
+    const float *kscale, *vscale;
+    __nv_bfloat16 *kwide, *vwide;  // [capacity][Hkv][16][d]
+    int32_t *places;               // [R], out
+    int32_t capacity;              // in blocks
+    int32_t least;                 // tokens of a chunk whose request is widened
+    const int32_t *starts;
+    int32_t total;
+    const int32_t *tables;
+    int32_t stride, num_rows;
+    const int32_t *lengths;
+    const int32_t *req_idx;
+    int32_t R, Hkv, d, num_blocks;
+    int32_t *sticky;
+};
+
+// A request whose chunk has at least so many query rows (tokens times heads of a group) is
+// widened.
+constexpr int kWideRows = 1536;
+constexpr int kWideMeanRows = 768;  // of a batch's requests, for any to be widened
+constexpr size_t kWideBytes = 256u << 20;  // of widened blocks, at most
+// Blocks of the workspace for a pool of num_blocks.
+int fp8_wide_blocks(int num_blocks, int hkv, int d);
+
+cudaError_t launch_fp8_widen(const Fp8WidenArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_fp8_append(const Fp8KvArgs &a, cudaStream_t s);
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s);
 cudaError_t launch_fp8_chunk_attn(const ChunkAttnArgs &a, int d, int sms, cudaStream_t s);

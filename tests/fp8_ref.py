@@ -10,6 +10,7 @@ from compressed_paged_kv_gb300 import zp
 B = 16
 E4M3 = torch.float8_e4m3fn
 MIN_EXP, MAX_EXP = -32, 32
+WIDE_ROWS = 1536  # query rows from which on a chunk's attention may be the bf16 kernel's
 
 
 def scale_of(most):
@@ -149,7 +150,9 @@ class Batch8:
                 continue
             a = int(self.starts_np[i])
             k, v = self.rows_of(i)
-            want, tol = attn_ref(self.q[a:a + n], k, v, self.scale, split)
+            wide = split > 0 and n * (self.Hq // self.Hkv) >= WIDE_ROWS
+            want, tol = attn_ref(self.q[a:a + n], k, v, self.scale, split,
+                                 2.0 ** -8 if wide else 2.0 ** -11)
             err = (self.out[a:a + n].double() - want).abs()
             assert bool((err <= tol).all()), (
                 i, n, T, float((err / tol).nan_to_num(math.inf).max()))
@@ -198,12 +201,12 @@ def values(pool, scale, blocks):
     return x.permute(0, 2, 1, 3).flatten(0, 1)
 
 
-def attn_ref(q, k, v, scale, split=0.0):
+def attn_ref(q, k, v, scale, split=0.0, weight=2.0 ** -11):
     """(out, bound) of one chunk in 64 bits: q [n, Hq, d], k and v [T, Hkv, d] (values).
 
     The bound counts: the result's rounding to bf16 (half a step, 2^-8 of the value);
-    each probability's weight rounded to fp16 for the product with V (2^-11 of sum p |v|
-    while it is at least 2^-14, else half of 2^-24, where the largest is at least 2^5:
+    each probability's weight rounded to fp16 for the product with V (`weight`: 2^-11 of
+    sum p |v|, or 2^-8 where it is bf16, of long chunks; that while it is at least 2^-14, else half of 2^-24, where the largest is at least 2^5:
     2^-30 of the largest p |v| a key; twice that is taken); the fp32 logit in base 2, a
     sum of d products (d + 2 roundings of 2^-23 -- the matrix unit may truncate -- of scale
     |q| . |k|), times the two scales (4 more) and plus log2 of V's scale, of at
@@ -231,7 +234,7 @@ def attn_ref(q, k, v, scale, split=0.0):
         pv = p @ v[:, h].abs()
         # the largest weight of a number in the product, a row's
         most = (p * v[:, h].abs().amax(1)[None]).amax(1, keepdim=True)
-        tol[:, hq] = (2.0 ** -8 * out[:, hq].abs() + (2.0 ** -10 + spread) * pv +
+        tol[:, hq] = (2.0 ** -8 * out[:, hq].abs() + (weight + 2.0 ** -11 + spread) * pv +
                       T * 2.0 ** -29 * most)
     return out, tol
 

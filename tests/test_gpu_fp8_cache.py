@@ -180,6 +180,31 @@ def test_chunk(spans, d, Hkv, Hq):
     b.check_attn()
 
 
+@pytest.mark.parametrize("d,Hkv,Hq", [(64, 2, 4), (128, 2, 8), (64, 1, 16), (128, 4, 28)])
+@pytest.mark.parametrize("permute", [False, True])
+def test_chunk_long_beside_short(d, Hkv, Hq, permute):
+    """Long chunks, whose blocks are widened, beside short ones and single tokens."""
+    b = Batch8([(1, 300), (900, 1500), (0, 20), (5, 40), (2000, 2000), (1, 1), (17, 500),
+                (770, 771)], Hkv=Hkv, Hq=Hq, d=d, permute=permute, pad=5, seed=d + Hq)
+    c = b.cache()
+    b.attn(c)
+    assert c.status() == zp.OK
+    b.check_attn()
+    first = b.out.clone()
+    b.out.fill_(7.0)
+    b.attn(c)
+    assert torch.equal(first.view(torch.int16), b.out.view(torch.int16))
+
+
+def test_chunk_more_long_ones_than_the_workspace_holds():
+    """Requests past the widened blocks' room go the short ones' way."""
+    b = Batch8([(1600, 16000)] * 6 + [(3, 50)], Hkv=8, Hq=8, d=128, seed=5)
+    c = b.cache()
+    b.attn(c)
+    assert c.status() == zp.OK
+    b.check_attn()
+
+
 def test_refusals():
     b = Batch8([(2, 40)], Hkv=2, Hq=4, d=64)
     c = b.cache()
