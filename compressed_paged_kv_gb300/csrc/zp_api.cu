@@ -583,36 +583,6 @@ zp_status zp_compress_prefill(zp_cache *c, int32_t *block_tables, int32_t bt_str
     return ZP_OK;
 }
 
-// What the attention calls on an 8-bit cache share.
-static zp::Fp8AttnArgs fp8_attn_args(const zp_cache *c, int32_t layer, const void *q,
-                                     int64_t q_stride, const int32_t *block_tables,
-                                     int32_t bt_stride, int32_t num_rows, const int32_t *lengths,
-                                     const int32_t *req_idx, int32_t R, float scale, void *out)
-{
-    zp::Fp8AttnArgs a{};
-    a.kmap = c->ws.kmaps + layer;
-    a.vmap = c->ws.vmaps + layer;
-    a.kscale = c->kscales[layer];
-    a.vscale = c->vscales[layer];
-    a.q = static_cast<const __nv_bfloat16 *>(q);
-    a.q_stride = q_stride;
-    a.tables = block_tables;
-    a.stride = bt_stride;
-    a.num_rows = num_rows;
-    a.lengths = lengths;
-    a.req_idx = req_idx;
-    a.R = R;
-    a.Hkv = c->Hkv;
-    a.Hq = c->Hq;
-    a.num_blocks = c->num_blocks;
-    a.splits = 1;
-    a.bps = bt_stride;
-    a.logit_scale = scale * 1.4426950408889634f;
-    a.out = static_cast<__nv_bfloat16 *>(out);
-    a.sticky = c->ws.sticky;
-    return a;
-}
-
 // What the appends to an 8-bit cache share.
 static zp::Fp8KvArgs fp8_kv_args(const zp_cache *c, int32_t layer, const void *k_new,
                                  int64_t k_stride, const void *v_new, int64_t v_stride,
@@ -662,19 +632,34 @@ zp_status zp_paged_decode_attn(zp_cache *c, int32_t layer, const void *q,
         return ZP_ERR_INVALID_ARG;
 
     int bps = 0;
-    const int splits = zp::decode_splits(static_cast<long long>(R) * c->Hkv, bt_stride,
-                                         c->num_sms, &bps);
+    const long long pairs = static_cast<long long>(R) * c->Hkv;
     if (c->fp8) {
-        zp::Fp8AttnArgs a = fp8_attn_args(c, layer, q, static_cast<int64_t>(c->Hq) * c->d,
-                                          block_tables, bt_stride, num_rows, lengths, req_idx, R,
-                                          scale, out);
-        a.splits = splits;
-        a.bps = bps;
+        zp::Fp8AttnArgs a{};
+        a.splits = zp::fp8_decode_splits(pairs, bt_stride, c->num_sms, &a.bps, &a.groups);
+        a.kmap = c->ws.kmaps + layer;
+        a.vmap = c->ws.vmaps + layer;
+        a.kscale = c->kscales[layer];
+        a.vscale = c->vscales[layer];
+        a.q = static_cast<const __nv_bfloat16 *>(q);
+        a.q_stride = static_cast<int64_t>(c->Hq) * c->d;
+        a.tables = block_tables;
+        a.stride = bt_stride;
+        a.num_rows = num_rows;
+        a.lengths = lengths;
+        a.req_idx = req_idx;
+        a.R = R;
+        a.Hkv = c->Hkv;
+        a.Hq = c->Hq;
+        a.num_blocks = c->num_blocks;
+        a.logit_scale = scale * 1.4426950408889634f;
+        a.out = static_cast<__nv_bfloat16 *>(out);
         a.part = c->ws.dec_part;
+        a.sticky = c->ws.sticky;
         return zp::launch_fp8_decode(a, c->d, static_cast<cudaStream_t>(stream)) == cudaSuccess
                    ? ZP_OK
                    : ZP_ERR_CUDA;
     }
+    const int splits = zp::decode_splits(pairs, bt_stride, c->num_sms, &bps);
 
     zp::DecodeArgs da{};
     // the per-layer maps live in device memory; kernels take their address

@@ -32,23 +32,21 @@ struct Fp8KvArgs {
     int32_t *sticky;
 };
 
-// starts null: request i asks for the one row i.
 struct Fp8AttnArgs {
     const CUtensorMap *kmap, *vmap;
     const float *kscale, *vscale;
     const __nv_bfloat16 *q;
-    int64_t q_stride;  // elements from a token of q to the next
-    const int32_t *starts;
-    int32_t total;
+    int64_t q_stride;  // elements from a request's row of q to the next
     const int32_t *tables;
     int32_t stride, num_rows;
     const int32_t *lengths;
     const int32_t *req_idx;
     int32_t R, Hkv, Hq, num_blocks;
-    int32_t splits, bps;  // splits per (token, kv head), blocks per split
+    int32_t splits, bps;  // splits per (request, kv head), blocks per split
+    int32_t groups;       // clusters they are
     float logit_scale;    // scale * log2(e)
     __nv_bfloat16 *out;
-    float *part;          // [tokens][Hq][splits][2 + d] (m, l, o[d]) when splits > 1
+    float *part;          // [R][Hq][groups][d + 2] (o[d], m, l) of more than one group
     int32_t *sticky;
 };
 
@@ -80,6 +78,9 @@ int fp8_wide_blocks(int num_blocks, int hkv, int d);
 
 cudaError_t launch_fp8_widen(const Fp8WidenArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_fp8_append(const Fp8KvArgs &a, cudaStream_t s);
+// Splits per (request, kv head) of a decode over `pairs` of them; *bps: blocks per split,
+// *groups (at most 16): clusters that the splits are.
+int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *bps, int *groups);
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s);
 cudaError_t launch_fp8_chunk_attn(const ChunkAttnArgs &a, int d, int sms, cudaStream_t s);
 // Once a device, before launch_fp8_chunk_attn.

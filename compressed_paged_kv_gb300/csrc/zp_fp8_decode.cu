@@ -16,13 +16,26 @@
 // 2^-28 of that); p is taken against 2^14 over the maximum, and rounded to 11 bits down
 // to 2^-28 of the largest, where bf16 would round to 8.
 //
-// Grid (request, kv head, split), four warps a CTA.  A CTA owns a contiguous range of
-// `bps` blocks; a warp takes every fourth pair of them through its own ring of
-// kStages pairs (one TMA box a slab).  Fragments come by ldmatrix: a matrix of 8 keys x 16
-// bytes gives a lane four neighbouring dims of a key, so q's fragments are laid out to
-// match; for V, the transposed matrix gives a lane two dims of two keys, which a byte
-// permutation turns into the pairs of keys that the product takes (even and odd dims as
-// two tiles).  Warps join in shared memory, splits in a second kernel.
+// The keys are the products' rows and the heads of the group their columns, eight of
+// them (or twice eight): S^T = K Q^T, O^T = V^T P^T.  With the heads as rows, of which 16
+// would be computed for a group of four, the kernel took twice the products and twice
+// the registers.  Fragments come by ldmatrix: a matrix of 8 keys x 16 bytes gives a lane
+// four neighbouring dims of a key, so q's fragments are laid out to match; for V, the
+// transposed matrix gives a lane two dims of two keys, which a byte permutation turns
+// into the pairs of keys that the product takes, the even dims as its rows 0-7 and the odd
+// ones as 8-15.  P turns from rows of keys to rows of heads by movmatrix.
+//
+// Grid (request and split, kv head), four warps a CTA.  A CTA owns a contiguous range of `bps`
+// blocks; a warp takes every fourth pair of them through its own ring of pairs (one TMA box
+// a slab).  Warps join in shared memory, and up to eight splits, a cluster, too; more clusters
+// of a long row leave partial results to a second kernel.
+//
+// Measured, 32 heads of 128 over 8 kv heads: 256 requests of 1,024 to 2,039 tokens, 0.81 GB in
+// 133 us = 6.1 TB/s, 0.90 of the copy peak (with 16 rows of heads and two CTAs an SM 166 us);
+// one of 2,000 tokens 6.1 us, the chain row -> block ids -> slabs -> joins; bound by HBM where
+// the rows fill the GPU.
+#include <algorithm>
+
 #include "zp_fp8.cuh"
 
 namespace zp {
@@ -31,98 +44,79 @@ namespace {
 
 constexpr int kD8Warps = 4;
 constexpr int kD8Threads = kD8Warps * 32;
-constexpr int kD8Stages = 3;   // of a pair of blocks, K and V
 constexpr float kTop = 14.f;   // log2 of the largest p
+constexpr int kD8Cluster = 8;  // splits that a cluster joins
+constexpr int kD8Groups = 16;  // clusters a (request, kv head), at most
 
-template <int D>
+template <int D, int NT>
 struct D8Smem {
+    static constexpr int STAGES = D == 128 ? 2 : 3;  // of a pair of blocks, K and V
     static constexpr int SLAB = kBlk * D;
     static constexpr int STAGE = 4 * SLAB;  // K of two blocks, V of two blocks
-    static constexpr int STAGES = kD8Warps * kD8Stages * STAGE;
-    static constexpr int MERGE = kD8Warps * 16 * (D + 2) * 4;  // reuses the stages
-    static constexpr int off_bar = STAGES > MERGE ? STAGES : MERGE;
-    static constexpr int BYTES = off_bar + kD8Warps * kD8Stages * 8;
+    static constexpr int RING = kD8Warps * STAGES * STAGE;
+    static constexpr int ROW = D + 2;       // o, then (maximum, sum), of a head
+    static constexpr int MERGE = kD8Warps * 8 * NT * ROW * 4;  // reuses the ring
+    static constexpr int off_bar = RING > MERGE ? RING : MERGE;
+    static constexpr int off_part = off_bar + kD8Warps * STAGES * 8;  // the CTA's own, for the cluster
+    static constexpr int BYTES = off_part + 8 * NT * ROW * 4;
     static constexpr int ALLOC = BYTES + 1024;
 };
 
+// An 8x8 matrix of 16-bit elements, a row's two neighbours a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(kD8Threads, 2)
+// NT: eights of heads.
+template <int D, int NT>
+__global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
     zp_fp8_decode_kernel(const __grid_constant__ Fp8AttnArgs a)
 {
     pdl_wait();
-    using S = D8Smem<D>;
-    constexpr int KS = D / 16;
+    using S = D8Smem<D, NT>;
+    constexpr int KS = D / 16, ROW = S::ROW, HEADS = 8 * NT;
 
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *sm = smem_raw + (1024 - (smem_u32(smem_raw) & 1023) & 1023);
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::off_bar);
+    float *part = reinterpret_cast<float *>(sm + S::off_part);
 
     const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
-    const int r = blockIdx.x, h = blockIdx.y, split = blockIdx.z;
+    const int split = blockIdx.x % a.splits, r = blockIdx.x / a.splits, h = blockIdx.y;
     const int G = a.Hq / a.Hkv;
-    int row = 0, len = 0;
-    bool live = true;  // a row with an output
-    if (a.starts) {    // one token of a chunk, by its packed row
-        int lo = 0, hi = a.R;
-        while (hi - lo > 1) {
-            const int m = (lo + hi) / 2;
-            if (a.starts[m] <= r)
-                lo = m;
-            else
-                hi = m;
-        }
-        ChunkReq c;
-        bool bad = false;
-        live = chunk_request(a, lo, c, &bad) && r >= c.first && r < c.first + c.n;
-        if (live) {
-            row = c.row;
-            len = c.len - c.n + (r - c.first) + 1;
-        }
-        if (r == 0 && h == 0 && split == 0)
-            for (int i = tid; i < a.R; i += kD8Threads) {
-                chunk_request(a, i, c, &bad);
-                if (bad)
-                    set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
-            }
-    } else {
-        row = a.req_idx ? a.req_idx[r] : r;
-        const bool row_ok = row >= 0 && row < a.num_rows;
-        len = row_ok ? a.lengths[row] : 0;
-        if (!row_ok || len < 0 || len > a.stride * kBlk) {
-            if (tid == 0 && split == 0 && h == 0)
-                set_error(a.sticky, row_ok ? ZP_ERR_DEVICE_CHECK : ZP_ERR_INVALID_ARG);
-            len = 0;
-            row = 0;
-        }
-    }
-    if (!live) {
-        pdl_launch_dependents();
-        return;
+    int row = a.req_idx ? a.req_idx[r] : r;
+    const bool row_ok = row >= 0 && row < a.num_rows;
+    int len = row_ok ? a.lengths[row] : 0;
+    if (!row_ok || len < 0 || len > a.stride * kBlk) {
+        if (tid == 0 && split == 0 && h == 0)
+            set_error(a.sticky, row_ok ? ZP_ERR_DEVICE_CHECK : ZP_ERR_INVALID_ARG);
+        len = 0;
+        row = 0;
     }
     const int nblk = (len + kBlk - 1) / kBlk;
     const int b_begin = split * a.bps;
     const int b_end = min(nblk, b_begin + a.bps);
 
-    if (tid < kD8Warps * kD8Stages)
-        mbar_init(&bars[tid], 1);
-    if (tid == 0)
-        fence_mbar_init();
-    __syncthreads();
+    uint64_t *my_bar = bars + wi * S::STAGES;
+    if (lane < S::STAGES)
+        mbar_init(&my_bar[lane], 1);
+    fence_mbar_init();
+    __syncwarp();
 
     // this warp's pairs of blocks: wi, wi + 4, .. of the range
     const int pairs = b_end > b_begin ? (b_end - b_begin + 1) / 2 : 0;
     const int my_n = pairs > wi ? (pairs - wi + kD8Warps - 1) / kD8Warps : 0;
-    uint8_t *my_stage = sm + wi * kD8Stages * S::STAGE;
-    uint64_t *my_bar = bars + wi * kD8Stages;
+    uint8_t *my_stage = sm + wi * S::STAGES * S::STAGE;
     const int32_t *trow = a.tables + static_cast<size_t>(row) * a.stride;
 
     // block ids and scales of 16 pairs, a block a lane, and of the 16 after them
-    auto block_of = [&](int i) { return b_begin + 2 * (wi + kD8Warps * (i + (lane >> 1))) + (lane & 1); };
     auto load_id = [&](int i) {
-        const int b = block_of(i);
+        const int b = b_begin + 2 * (wi + kD8Warps * (i + (lane >> 1))) + (lane & 1);
         int id = b < b_end ? trow[b] : 0;
         if (id < 0 || id >= a.num_blocks) {
             set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
@@ -131,7 +125,7 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         return id;
     };
     auto scale_at = [&](const float *s, int id) { return s[static_cast<size_t>(id) * a.Hkv + h]; };
-    int id = load_id(0), id_next = 0;
+    int id = my_n > 0 ? load_id(0) : 0, id_next = 0;
 
     auto issue = [&](int i, int ids) {
         const int l = (i & 15) * 2;
@@ -139,7 +133,7 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         const int y1 = (__shfl_sync(0xffffffffu, ids, l + 1) * a.Hkv + h) * kBlk;
         if (lane == 0) {
             const bool two = b_begin + 2 * (wi + kD8Warps * i) + 1 < b_end;
-            const int s = i % kD8Stages;
+            const int s = i % S::STAGES;
             uint8_t *kd = my_stage + s * S::STAGE, *vd = kd + 2 * S::SLAB;
             mbar_arrive_expect_tx(&my_bar[s], two ? S::STAGE : S::STAGE / 2);
             tma_load_2d(kd, a.kmap, 0, y0, &my_bar[s]);
@@ -151,24 +145,24 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         }
         __syncwarp();
     };
-    for (int i = 0; i < my_n && i < kD8Stages; ++i)
+    for (int i = 0; i < my_n && i < S::STAGES; ++i)
         issue(i, id);
     float ks = scale_at(a.kscale, id), vs = scale_at(a.vscale, id), ks_next = 0.f, vs_next = 0.f;
 
-    // q's fragments: rows g and g + 8, dims 16 c + 4 t .. + 3 of each 16-byte chunk
-    uint32_t qa[KS][4];
-    float fr[2];  // what a logit is multiplied by, but for ks
+    // q's fragments: head 8 n + g, dims 16 c + 4 t .. + 3
+    const int g = lane >> 2, t4 = lane & 3;
+    uint32_t qb[NT][KS][2];
+    float fr[NT][2];  // heads 8 n + 2 t, + 1: what a logit is multiplied by, but for ks
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        const int g = (lane >> 2) + hh * 8;
-        const __nv_bfloat16 *src =
-            a.q + r * a.q_stride + (h * G + min(g, G - 1)) * D + (lane & 3) * 4;
+    for (int n = 0; n < NT; ++n) {
+        const int hd = n * 8 + g;
+        const __nv_bfloat16 *src = a.q + r * a.q_stride + (h * G + min(hd, G - 1)) * D + t4 * 4;
         uint2 u[KS];
         uint32_t most = 0;  // the largest finite magnitude's bits
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
             u[c] = make_uint2(0u, 0u);
-            if (g < G)
+            if (hd < G)
                 u[c] = *reinterpret_cast<const uint2 *>(src + c * 16);
             const uint32_t w[4] = {u[c].x << 16, u[c].x, u[c].y << 16, u[c].y};
 #pragma unroll
@@ -183,42 +177,45 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         const int e = 14 - (static_cast<int>(most >> 23) - 127);
         const int e1 = max(min(e, 100), -100), e2 = e - e1;
         const float f1 = __uint_as_float(exp2_bits(e1)), f2 = __uint_as_float(exp2_bits(e2));
-        fr[hh] = a.logit_scale * __uint_as_float(exp2_bits(-e1)) * __uint_as_float(exp2_bits(-e2));
+        const float back =
+            a.logit_scale * __uint_as_float(exp2_bits(-e1)) * __uint_as_float(exp2_bits(-e2));
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
-            qa[c][hh] = pack_f16x2(__uint_as_float(u[c].x << 16) * f1 * f2,
-                                   __uint_as_float(u[c].x & 0xffff0000u) * f1 * f2);
-            qa[c][2 + hh] = pack_f16x2(__uint_as_float(u[c].y << 16) * f1 * f2,
-                                       __uint_as_float(u[c].y & 0xffff0000u) * f1 * f2);
+            qb[n][c][0] = pack_f16x2(__uint_as_float(u[c].x << 16) * f1 * f2,
+                                     __uint_as_float(u[c].x & 0xffff0000u) * f1 * f2);
+            qb[n][c][1] = pack_f16x2(__uint_as_float(u[c].y << 16) * f1 * f2,
+                                     __uint_as_float(u[c].y & 0xffff0000u) * f1 * f2);
         }
+        fr[n][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
+        fr[n][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
     }
 
-    float m_run[2] = {-1e30f, -1e30f};
-    float l_run[2] = {0.f, 0.f};
-    float o[KS][8];  // dims 16 c + 4 t + {0, 2 | 1, 3} of row g, then of g + 8: two tiles
+    float m_run[NT][2], l_run[NT][2];
+    float o[NT][KS][4];  // dims 16 c + 2 g (+ 1 in [2], [3]), heads 8 n + 2 t, + 1
 #pragma unroll
-    for (int c = 0; c < KS; ++c)
+    for (int n = 0; n < NT; ++n) {
+        m_run[n][0] = m_run[n][1] = -1e30f;
+        l_run[n][0] = l_run[n][1] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            o[c][e] = 0.f;
+        for (int c = 0; c < KS; ++c)
+            o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
+    }
     bool ok = true;
     const int mi = lane >> 3;
 
     for (int i = 0; i < my_n; ++i) {
-        const int s = i % kD8Stages;
+        const int s = i % S::STAGES;
         const int b0 = b_begin + 2 * (wi + kD8Warps * i);
         const bool two = b0 + 1 < b_end;
         const int tok0 = b0 * kBlk;
         const int l = (i & 15) * 2;
-        const float ks0 = __shfl_sync(0xffffffffu, ks, l), ks1 = __shfl_sync(0xffffffffu, ks, l + 1);
-        const float vs0 = __shfl_sync(0xffffffffu, vs, l), vs1 = __shfl_sync(0xffffffffu, vs, l + 1);
         if ((i & 15) == 0 && i + 16 < my_n)
             id_next = load_id(i + 16);
         if ((i & 15) == 8 && i + 8 < my_n) {
             ks_next = scale_at(a.kscale, id_next);
             vs_next = scale_at(a.vscale, id_next);
         }
-        ok &= mbar_wait(&my_bar[s], (i / kD8Stages) & 1);
+        ok &= mbar_wait(&my_bar[s], (i / S::STAGES) & 1);
         uint8_t *kd = my_stage + s * S::STAGE, *vd = kd + 2 * S::SLAB;
         if (len - tok0 < (two ? 2 : 1) * kBlk) {
             // the slots past the length get probability 0, but 0 times a NaN is NaN: their
@@ -234,80 +231,93 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         }
         const uint32_t kb = smem_u32(kd), vb = smem_u32(vd);
 
-        // S of 32 keys: tiles of 8 keys; a matrix of tile nt, chunk c: a lane holds dims
-        // 4 t .. 4 t + 3 of key g
-        float sacc[4][4];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sacc[nt][e] = 0.f;
+        // S^T: keys 16 blk + g (in [0], [1]) and + 8, heads 8 n + 2 t, + 1
+        float sacc[2][NT][4];
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                sacc[blk][n][0] = sacc[blk][n][1] = sacc[blk][n][2] = sacc[blk][n][3] = 0.f;
             if (blk && !two)
                 break;
 #pragma unroll
             for (int c = 0; c < KS; c += 2) {
-                // matrices: keys 0-7 of chunks c, c + 1, then keys 8-15
+                // matrices: keys 0-7 and 8-15 of chunk c, then of c + 1
                 uint32_t kr[4];
-                ldsm_x4(kb + blk * S::SLAB + swz8<D>((mi >> 1) * 8 + (lane & 7), c + (mi & 1)), kr);
+                ldsm_x4(kb + blk * S::SLAB + swz8<D>((mi & 1) * 8 + (lane & 7), c + (mi >> 1)), kr);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int cc = c + (x & 1), nt = blk * 2 + (x >> 1);
-                    mma_f16(sacc[nt], qa[cc][0], qa[cc][1], qa[cc][2], qa[cc][3],
-                            f16x2_of_e4m3(kr[x]), f16x2_of_e4m3(kr[x] >> 16));
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t a0 = f16x2_of_e4m3(kr[2 * x]), a1 = f16x2_of_e4m3(kr[2 * x + 1]);
+                    const uint32_t a2 = f16x2_of_e4m3(kr[2 * x] >> 16);
+                    const uint32_t a3 = f16x2_of_e4m3(kr[2 * x + 1] >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_f16(sacc[blk][n], a0, a1, a2, a3, qb[n][c + x][0], qb[n][c + x][1]);
                 }
             }
         }
-        const float lv0 = log2f(vs0), lv1 = log2f(vs1);
+        float iv[2];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int blk = 0; blk < 2; ++blk) {
+            const float kx = __shfl_sync(0xffffffffu, ks, l + blk);
+            const float vx = __shfl_sync(0xffffffffu, vs, l + blk);
+            const float lv = log2f(vx);
+            iv[blk] = blk && !two ? 0.f : 1.f / vx;
+            const int key = blk * kBlk + g;
+            const bool in0 = tok0 + key < len && (two || !blk), in1 = tok0 + key + 8 < len && (two || !blk);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = nt * 8 + (lane & 3) * 2 + (e & 1);
-                const float v =
-                    fmaf(sacc[nt][e], fr[e >> 1] * (nt < 2 ? ks0 : ks1), nt < 2 ? lv0 : lv1);
-                sacc[nt][e] = key < kBlk * (two ? 2 : 1) && tok0 + key < len ? v : -INFINITY;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = fmaf(sacc[blk][n][e], fr[n][e & 1] * kx, lv);
+                    sacc[blk][n][e] = (e < 2 ? in0 : in1) ? v : -INFINITY;
+                }
+        }
+        uint32_t pb[2][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float corr[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(fmaxf(sacc[0][n][e], sacc[0][n][e + 2]),
+                                 fmaxf(sacc[1][n][e], sacc[1][n][e + 2]));
+                if (!two)
+                    mx = fmaxf(sacc[0][n][e], sacc[0][n][e + 2]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float m_new = fmaxf(m_run[n][e], mx);
+                corr[e] = ex2_approx(m_run[n][e] - m_new);
+                m_run[n][e] = m_new;
+                const float at = m_new - kTop;
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk) {
+                    sacc[blk][n][e] = ex2_approx(sacc[blk][n][e] - at);
+                    sacc[blk][n][e + 2] = ex2_approx(sacc[blk][n][e + 2] - at);
+                }
+                const float s0 = sacc[0][n][e] + sacc[0][n][e + 2];
+                const float s1 = sacc[1][n][e] + sacc[1][n][e + 2];
+                l_run[n][e] = fmaf(l_run[n][e], corr[e], fmaf(s0, iv[0], two ? s1 * iv[1] : 0.f));
             }
-        const float iv0 = 1.f / vs0, iv1 = two ? 1.f / vs1 : 0.f;
+            if (__any_sync(0xffffffffu, corr[0] != 1.f || corr[1] != 1.f)) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-                mx = fmaxf(mx, fmaxf(sacc[nt][hh * 2], sacc[nt][hh * 2 + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float m_new = fmaxf(m_run[hh], mx);
-            const float corr = ex2_approx(m_run[hh] - m_new);
-            m_run[hh] = m_new;
-#pragma unroll
-            for (int c = 0; c < KS; ++c) {
-                o[c][hh * 2] *= corr;
-                o[c][hh * 2 + 1] *= corr;
-                o[c][4 + hh * 2] *= corr;
-                o[c][4 + hh * 2 + 1] *= corr;
+                for (int c = 0; c < KS; ++c) {
+                    o[n][c][0] *= corr[0];
+                    o[n][c][1] *= corr[1];
+                    o[n][c][2] *= corr[0];
+                    o[n][c][3] *= corr[1];
+                }
             }
-            const float at = m_new - kTop;
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                sacc[nt][hh * 2] = ex2_approx(sacc[nt][hh * 2] - at);
-                sacc[nt][hh * 2 + 1] = ex2_approx(sacc[nt][hh * 2 + 1] - at);
+            for (int blk = 0; blk < 2; ++blk) {
+                pb[blk][n][0] = transposed(pack_f16x2(sacc[blk][n][0], sacc[blk][n][1]));
+                pb[blk][n][1] = transposed(pack_f16x2(sacc[blk][n][2], sacc[blk][n][3]));
             }
-            const float s0 = (sacc[0][hh * 2] + sacc[0][hh * 2 + 1]) +
-                             (sacc[1][hh * 2] + sacc[1][hh * 2 + 1]);
-            const float s1 = (sacc[2][hh * 2] + sacc[2][hh * 2 + 1]) +
-                             (sacc[3][hh * 2] + sacc[3][hh * 2 + 1]);
-            l_run[hh] = fmaf(l_run[hh], corr, fmaf(s0, iv0, two ? s1 * iv1 : 0.f));
         }
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
             if (blk && !two)
                 break;
-            const uint32_t p0 = pack_f16x2(sacc[blk * 2][0], sacc[blk * 2][1]);
-            const uint32_t p1 = pack_f16x2(sacc[blk * 2][2], sacc[blk * 2][3]);
-            const uint32_t p2 = pack_f16x2(sacc[blk * 2 + 1][0], sacc[blk * 2 + 1][1]);
-            const uint32_t p3 = pack_f16x2(sacc[blk * 2 + 1][2], sacc[blk * 2 + 1][3]);
 #pragma unroll
             for (int c = 0; c < KS; c += 2) {
                 // matrices: keys 0-7 and 8-15 of chunk c, then of c + 1
@@ -319,18 +329,19 @@ __global__ void __launch_bounds__(kD8Threads, 2)
                     // bytes: key 2 t (dims 2 g, 2 g + 1), key 2 t + 1 (the same)
                     const uint32_t lo = __byte_perm(vr[2 * x], 0, 0x3120);
                     const uint32_t hi = __byte_perm(vr[2 * x + 1], 0, 0x3120);
-                    float(&even)[4] = *reinterpret_cast<float(*)[4]>(&o[c + x][0]);
-                    float(&odd)[4] = *reinterpret_cast<float(*)[4]>(&o[c + x][4]);
-                    mma_f16(even, p0, p1, p2, p3, f16x2_of_e4m3(lo), f16x2_of_e4m3(hi));
-                    mma_f16(odd, p0, p1, p2, p3, f16x2_of_e4m3(lo >> 16), f16x2_of_e4m3(hi >> 16));
+                    const uint32_t a0 = f16x2_of_e4m3(lo), a1 = f16x2_of_e4m3(lo >> 16);
+                    const uint32_t a2 = f16x2_of_e4m3(hi), a3 = f16x2_of_e4m3(hi >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma_f16(o[n][c + x], a0, a1, a2, a3, pb[blk][n][0], pb[blk][n][1]);
                 }
             }
         }
         __syncwarp();
-        if (i + kD8Stages < my_n) {
+        if (i + S::STAGES < my_n) {
             fence_proxy_async_smem();
             __syncwarp();
-            issue(i + kD8Stages, ((i + kD8Stages) ^ i) & 16 ? id_next : id);
+            issue(i + S::STAGES, ((i + S::STAGES) ^ i) & 16 ? id_next : id);
         }
         if ((i & 15) == 15) {
             id = id_next;
@@ -342,114 +353,188 @@ __global__ void __launch_bounds__(kD8Threads, 2)
         set_error(a.sticky, ZP_ERR_TIMEOUT);
     pdl_launch_dependents();  // the combine kernel may be scheduled
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-        l_run[hh] += __shfl_xor_sync(0xffffffffu, l_run[hh], 1);
-        l_run[hh] += __shfl_xor_sync(0xffffffffu, l_run[hh], 2);
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], 4);
+            l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], 8);
+            l_run[n][e] += __shfl_xor_sync(0xffffffffu, l_run[n][e], 16);
+        }
     __syncthreads();  // every stage consumed: reuse the area for the merge
 
-    float *mrg = reinterpret_cast<float *>(sm);  // [warp][16][D + 2]
-    {
-        float *mine = mrg + wi * 16 * (D + 2);
+    float *mrg = reinterpret_cast<float *>(sm);  // [warp][HEADS][ROW]
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int rr = (lane >> 2) + hh * 8;
-            if ((lane & 3) == 0) {
-                mine[rr * (D + 2) + D] = m_run[hh];
-                mine[rr * (D + 2) + D + 1] = l_run[hh];
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float *mine = mrg + (wi * HEADS + n * 8 + t4 * 2 + e) * ROW;
+            if (g == 0) {
+                mine[D] = m_run[n][e];
+                mine[D + 1] = l_run[n][e];
             }
 #pragma unroll
-            for (int c = 0; c < KS; ++c) {
-                float *to = mine + rr * (D + 2) + c * 16 + (lane & 3) * 4;
-                to[0] = o[c][hh * 2];
-                to[2] = o[c][hh * 2 + 1];
-                to[1] = o[c][4 + hh * 2];
-                to[3] = o[c][4 + hh * 2 + 1];
-            }
+            for (int c = 0; c < KS; ++c)
+                *reinterpret_cast<float2 *>(mine + c * 16 + g * 2) =
+                    make_float2(o[n][c][e], o[n][c][e + 2]);
         }
-    }
     __syncthreads();
-    for (int idx = tid; idx < G * D; idx += kD8Threads) {
-        const int g = idx / D, c = idx - g * D;
-        float M = -1e30f;
-#pragma unroll
-        for (int w2 = 0; w2 < kD8Warps; ++w2)
-            M = fmaxf(M, mrg[(w2 * 16 + g) * (D + 2) + D]);
-        float L = 0.f, O = 0.f;
-#pragma unroll
-        for (int w2 = 0; w2 < kD8Warps; ++w2) {
-            const float *src = mrg + (w2 * 16 + g) * (D + 2);
-            const float f = exp2f(src[D] - M);
-            L += src[D + 1] * f;
-            O += src[c] * f;
+    // the four warps', then the cluster's; two dims a thread
+    const int cs = a.splits / a.groups, rank = split % cs;  // a cluster's CTAs
+    const size_t hq0 = static_cast<size_t>(r) * a.Hq + h * G;
+    auto join = [&](int hd, int c, const float *src, int step, int count, float &M, float &L,
+                    float2 &O) {
+        M = -1e30f;
+        for (int w = 0; w < count; ++w)
+            M = fmaxf(M, src[w * step + hd * ROW + D]);
+        L = 0.f;
+        O = make_float2(0.f, 0.f);
+        for (int w = 0; w < count; ++w) {
+            const float *p = src + w * step + hd * ROW;
+            const float f = ex2_approx(p[D] - M);
+            const float2 v = *reinterpret_cast<const float2 *>(p + c);
+            L += p[D + 1] * f;
+            O.x += v.x * f;
+            O.y += v.y * f;
         }
-        const size_t hq = static_cast<size_t>(r) * a.Hq + h * G + g;
+    };
+    auto write = [&](int hd, int c, float L, float2 O) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        __nv_bfloat16 *to = a.out + (hq0 + hd) * D + c;  // (2-byte aligned)
+        to[0] = __float2bfloat16_rn(O.x * inv);
+        to[1] = __float2bfloat16_rn(O.y * inv);
+    };
+    for (int x = tid; x < G * (D / 2); x += kD8Threads) {
+        const int hd = x / (D / 2), c = x % (D / 2) * 2;
+        float M, L;
+        float2 O;
+        join(hd, c, mrg, HEADS * ROW, kD8Warps, M, L, O);
         if (a.splits == 1) {
-            a.out[hq * D + c] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
-        } else {
-            float *p = a.part + (hq * a.splits + split) * (D + 2);
-            p[c] = O;
-            if (c == 0) {
-                p[D] = M;
-                p[D + 1] = L;
+            write(hd, c, L, O);
+            continue;
+        }
+        float *p = part + hd * ROW;
+        *reinterpret_cast<float2 *>(p + c) = O;
+        if (c == 0)
+            *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
+    }
+    if (a.splits == 1)
+        return;
+    cluster_sync();
+    // each CTA joins its part of the dims
+    for (int x = rank * kD8Threads + tid; x < G * (D / 2); x += cs * kD8Threads) {
+        const int hd = x / (D / 2), c = x % (D / 2) * 2;
+        float2 ml[kD8Cluster], v[kD8Cluster];
+#pragma unroll
+        for (int w = 0; w < kD8Cluster; ++w) {
+            ml[w] = make_float2(-1e30f, 0.f);
+            v[w] = make_float2(0.f, 0.f);
+            if (w < cs) {
+                ml[w] = ld_dsmem_f32x2(dsmem_addr(part + hd * ROW + D, w));
+                v[w] = ld_dsmem_f32x2(dsmem_addr(part + hd * ROW + c, w));
             }
         }
+        float M = -1e30f, L = 0.f;
+        float2 O = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kD8Cluster; ++w)
+            M = fmaxf(M, ml[w].x);
+#pragma unroll
+        for (int w = 0; w < kD8Cluster; ++w) {
+            const float f = ex2_approx(ml[w].x - M);
+            L += ml[w].y * f;
+            O.x += v[w].x * f;
+            O.y += v[w].y * f;
+        }
+        if (a.groups == 1) {
+            write(hd, c, L, O);
+            continue;
+        }
+        float *p = a.part + ((hq0 + hd) * a.groups + split / cs) * ROW;
+        *reinterpret_cast<float2 *>(p + c) = O;
+        if (c == 0)
+            *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
     }
+    cluster_sync();  // no CTA leaves while its part is read
 }
 
 template <int D>
 __global__ void __launch_bounds__(D) zp_fp8_combine_kernel(const Fp8AttnArgs a)
 {
     pdl_wait();
-    const int rh = blockIdx.x;  // token * Hq + hq
+    const int rh = blockIdx.x;  // request * Hq + hq
     const int c = threadIdx.x;
-    const float *base = a.part + static_cast<size_t>(rh) * a.splits * (D + 2);
+    const float *base = a.part + static_cast<size_t>(rh) * a.groups * (D + 2);
     float M = -1e30f;
-    for (int s = 0; s < a.splits; ++s)
+    for (int s = 0; s < a.groups; ++s)
         M = fmaxf(M, base[s * (D + 2) + D]);
     float L = 0.f, O = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-        const float f = exp2f(base[s * (D + 2) + D] - M);
+    for (int s = 0; s < a.groups; ++s) {
+        const float f = ex2_approx(base[s * (D + 2) + D] - M);
         L += base[s * (D + 2) + D + 1] * f;
         O += base[s * (D + 2) + c] * f;
     }
     a.out[static_cast<size_t>(rh) * D + c] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
 }
 
-template <int D>
+template <int D, int NT>
 static cudaError_t launch_fp8_decode_t(const Fp8AttnArgs &a, cudaStream_t s)
 {
-    using Sm = D8Smem<D>;
-    cudaError_t err = cudaFuncSetAttribute(zp_fp8_decode_kernel<D>,
+    using Sm = D8Smem<D, NT>;
+    cudaError_t err = cudaFuncSetAttribute(zp_fp8_decode_kernel<D, NT>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::ALLOC);
     if (err != cudaSuccess)
         return err;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.splits / a.groups);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    const unsigned tokens = static_cast<unsigned>(a.starts ? a.total : a.R);
-    cfg.gridDim = dim3(tokens, static_cast<unsigned>(a.Hkv), static_cast<unsigned>(a.splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.R),
+                       static_cast<unsigned>(a.Hkv), 1);
     cfg.blockDim = dim3(kD8Threads, 1, 1);
     cfg.dynamicSmemBytes = Sm::ALLOC;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, zp_fp8_decode_kernel<D>, a);
-    if (err != cudaSuccess || a.splits == 1)
+    cfg.numAttrs = a.splits > 1 ? 2 : 1;
+    err = cudaLaunchKernelEx(&cfg, zp_fp8_decode_kernel<D, NT>, a);
+    if (err != cudaSuccess || a.groups == 1)
         return err;
-    cfg.gridDim = dim3(tokens * static_cast<unsigned>(a.Hq), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(a.R * a.Hq), 1, 1);
     cfg.blockDim = dim3(D, 1, 1);
     cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, zp_fp8_combine_kernel<D>, a);
+}
+
+// Two CTAs an SM, of at least 8 blocks each; more than a cluster of them where each then has
+// 16 blocks, which pays for the second launch (one row of 30,000 tokens 17 us, with 16
+// splits 24).
+int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *bps, int *groups)
+{
+    const long long want = (2 * num_sms + pairs - 1) / pairs;
+    int splits = static_cast<int>(std::min<long long>({want, kD8Cluster, bt_stride / 8}));
+    splits = std::max(1, splits);
+    *groups = static_cast<int>(std::min<long long>(
+        {want / kD8Cluster, kD8Groups, bt_stride / (16 * kD8Cluster)}));
+    if (*groups > 1) {
+        splits = kD8Cluster * *groups;
+    } else {
+        *groups = 1;
+    }
+    *bps = (bt_stride + splits - 1) / splits;
+    return splits;
 }
 
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s)
 {
+    const bool wide = a.Hq / a.Hkv > 8;
     if (d == 64)
-        return launch_fp8_decode_t<64>(a, s);
+        return wide ? launch_fp8_decode_t<64, 2>(a, s) : launch_fp8_decode_t<64, 1>(a, s);
     if (d == 128)
-        return launch_fp8_decode_t<128>(a, s);
+        return wide ? launch_fp8_decode_t<128, 2>(a, s) : launch_fp8_decode_t<128, 1>(a, s);
     return cudaErrorInvalidValue;
 }
 
