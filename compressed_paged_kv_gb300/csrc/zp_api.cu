@@ -1091,6 +1091,7 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         return zp::launch_chunk_attn(a, c->d, c->num_sms, s) == cudaSuccess ? ZP_OK : ZP_ERR_CUDA;
     a.kscale = c->kscales[layer];
     a.vscale = c->vscales[layer];
+    a.duos = static_cast<int64_t>(R) * c->Hkv >= 2ll * c->num_sms;
     // Requests with many query rows over widened blocks, the others over the cache, if the
     // batch has many rows a request: two kernels one after the other cost a mixed batch more
     // than the widened blocks gain (60 single tokens beside two pieces of 900, 64 dims: 138 us

@@ -131,6 +131,7 @@ struct CaDesc {
     int kt;      // all its key tiles
     int w;       // cost
     int clean;   // of the second walk
+    int duo;     // one query tile of h for A, one of h + 1 for B
     long long x; // cost before it
 };
 
@@ -142,7 +143,8 @@ struct CaSmem {
     static constexpr int TILE8 = kTile * D;              // of 8-bit ones
     static constexpr int KTILE = F8 ? TILE8 : TILE;
     // stages of K, of V and of 8-bit V
-    static constexpr int NK = D == 128 ? (F8 ? 3 : 2) : 5, NV = D == 128 ? (F8 ? 2 : 3) : F8 ? 4 : 5;
+    static constexpr int NK = D == 128 ? (F8 ? 3 : 2) : 5;
+    static constexpr int NV = D == 128 ? (F8 ? 2 : 3) : F8 ? 4 : 5;
     static constexpr int NR = F8 ? (D == 128 ? 2 : 4) : 0;
     static constexpr int XC = 16;  // columns of O a step of the epilogue
     static constexpr int off_q = 0;                      // Q of A, Q of B
@@ -152,8 +154,9 @@ struct CaSmem {
     static constexpr int off_v = off_k + NK * KTILE;
     static constexpr int off_raw = off_v + NV * TILE;
     static constexpr int off_scale = off_raw + NR * TILE8;  // float4 [kScales][8]: of key tiles
-    static constexpr int off_qf = off_scale + (F8 ? kScales * 8 * 16 : 0);  // float [kQTiles][128]: of Q's rows
-    static constexpr int off_max = off_qf + (F8 ? kQTiles * kTile * 4 : 0);  // float [2][2][128]: maxima of row halves
+    // float [kQTiles][128] of Q's rows; float [2][2][128], the maxima of row halves
+    static constexpr int off_qf = off_scale + (F8 ? kScales * 8 * 16 : 0);
+    static constexpr int off_max = off_qf + (F8 ? kQTiles * kTile * 4 : 0);
     static constexpr int off_desc = off_max + 4 * kTile * 4;  // CaDesc [kDescs]
     static constexpr int off_plan = off_desc + kDescs * static_cast<int>(sizeof(CaDesc));
     static constexpr int off_scan = off_plan + static_cast<int>(sizeof(CaPlan));  // int64 [warps]
@@ -181,6 +184,8 @@ struct CaItem {
     int w;                  // cost
     int ka, kb;             // this CTA's key tiles
     bool single;
+    bool duo;               // h and span of two kv heads
+    int units;              // heads, or pairs of them, of the request
 };
 
 __host__ __device__ __forceinline__ int tile_tokens(int G) { return kTile / G; }
@@ -213,6 +218,25 @@ __host__ __device__ __forceinline__ long long head_cost(const ChunkReq &c, int t
 {
     return pair_prefix(c, 2 * tpt, pair_count(c.n, tpt) - 1) +
            item_cost(c.len, last_tokens(c.n, tpt) <= tpt);
+}
+
+// Whether the request's kv heads go by two (of an 8-bit cache): its one query tile of one
+// head to A and of the next to B, each with its own key tiles, instead of one after the
+// other with A and B sharing the key tiles.  Half as many ends of items, and no half to wait
+// for there: 256 chunks of 2..9 over 1,030..2,040, 8 kv heads of 128: 340 -> 304 us.  Only a
+// batch of two heads an SM or more (`duos`): 19 chunks over 1,500 took 25.7 us the one way
+// and 33.5 the other, 38 of them 48.6 and 46.3.
+__host__ __device__ __forceinline__ bool heads_by_two(int n, int tpt, int Hkv, bool duos)
+{
+    return duos && n <= tpt && Hkv % 2 == 0;
+}
+
+__host__ __device__ __forceinline__ long long request_cost(const ChunkReq &c, int tpt, int Hkv,
+                                                           bool duos)
+{
+    return heads_by_two(c.n, tpt, Hkv, duos)
+               ? static_cast<long long>(Hkv / 2) * item_cost(c.len, false)
+               : Hkv * head_cost(c, tpt);
 }
 
 // The cost of the request's longest item.
@@ -289,12 +313,13 @@ struct CaWalk {
     const CaPlan &pl;
     int tpt;
     CaItem it;
+    bool duos = false;
 
     __host__ __device__ __forceinline__ void fill()
     {
         it.tok0 = it.p * 2 * tpt;
         it.ntok = min(it.c.n - it.tok0, 2 * tpt);
-        it.single = it.ntok <= tpt;
+        it.single = it.ntok <= tpt && !it.duo;
         const int vis = it.c.len - it.c.n + it.tok0 + it.ntok;
         it.kt = (vis + kTile - 1) / kTile;
         it.w = item_cost(vis, it.single);
@@ -306,7 +331,9 @@ struct CaWalk {
     {
         it.i = i;
         it.pairs = pair_count(it.c.n, tpt);
-        it.span = head_cost(it.c, tpt);
+        it.duo = heads_by_two(it.c.n, tpt, a.Hkv, duos);
+        it.units = it.duo ? a.Hkv / 2 : a.Hkv;
+        it.span = it.duo ? item_cost(it.c.len, false) : head_cost(it.c, tpt);
     }
 
     __host__ __device__ __forceinline__ bool request(int i)
@@ -352,7 +379,7 @@ struct CaWalk {
             return false;
         if (++it.p == it.pairs) {
             it.p = 0;
-            if (++it.h == a.Hkv) {
+            if (++it.h == it.units) {
                 it.h = 0;
                 if (!request(it.i + 1))
                     return false;
@@ -826,6 +853,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 
     const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
     const int G = a.Hq / a.Hkv, tpt = tile_tokens(G);
+    const bool duos = F8 && a.duos;
 
     if (tid == 0) {
         for (int s = 0; s < NK; ++s) {
@@ -896,8 +924,9 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         for (int i = r0; i < r1; ++i) {
             bool bad;
             if (attn_request(a, i, c, &bad)) {
-                mine += a.Hkv * head_cost(c, tpt);
-                longest = max(longest, longest_item(c, tpt));
+                mine += request_cost(c, tpt, a.Hkv, duos);
+                longest = max(longest, heads_by_two(c.n, tpt, a.Hkv, duos) ? item_cost(c.len, false)
+                                                                           : longest_item(c, tpt));
             }
             if (bad && blockIdx.x == 0)
                 set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
@@ -945,7 +974,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 if (!attn_request(a, i, p.c0, &bad))
                     continue;
                 p.i0 = i;
-                const long long w = a.Hkv * head_cost(p.c0, tpt);
+                const long long w = request_cost(p.c0, tpt, a.Hkv, duos);
                 if (p.lo < before + w)
                     break;
                 before += w;
@@ -1028,11 +1057,13 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             }
             __syncwarp();
         };
-        // The scales of the block whose pool row is y: K's, log2 of V's, 1 / V's.
+        // The same pool rows of the next kv head.
+        auto next_head = [&](int ids) { return ids < 0 ? ids : ids + kBlk; };
+        // The scales of the block whose pool row is y: K's and V's.
         auto scales_of = [&](int y) {
             const int at = y < 0 ? 0 : y / kBlk;
             const float ks = y < 0 ? 1.f : a.kscale[at], vs = y < 0 ? 1.f : a.vscale[at];
-            return make_float4(ks, vs, 0.f, 0.f);
+            return make_float2(ks, vs);
         };
         if (wi == kLoadWarp) {
             // ------------------------------------------- the items, Q and K
@@ -1052,15 +1083,15 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                 "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier"
                                 "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
                                     smem_u32(sQ + k * S::TILE + p * S::PANEL)),
-                                "l"(&a.qmap), "r"(p * 64), "r"(d.h * G),
-                                "r"(d.row0 + x * tpt), "r"(smem_u32(&qfull[k]))
+                                "l"(&a.qmap), "r"(p * 64), "r"((d.h + (F8 && d.duo ? x : 0)) * G),
+                                "r"(d.row0 + (F8 && d.duo ? 0 : x * tpt)), "r"(smem_u32(&qfull[k]))
                                 : "memory");
                     }
                     __syncwarp();
                 }
             };
             for (bool clean = false;; clean = true) {
-                CaWalk wk{a, plan, tpt, {}};
+                CaWalk wk{a, plan, tpt, {}, duos};
                 bool more = wk.begin();
                 for (; !bad; more = wk.next()) {
                     const CaItem &it = wk.it;
@@ -1072,7 +1103,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     CaDesc d;
                     d.row0 = it.c.first + it.tok0;
                     d.ntok = more ? it.ntok : 0;
-                    d.h = it.h;
+                    d.h = it.duo ? 2 * it.h : it.h;
                     d.pos0 = it.c.len - it.c.n + it.tok0;
                     d.len = it.c.len;
                     d.row = it.c.row;
@@ -1081,6 +1112,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     d.kt = it.kt;
                     d.w = it.w;
                     d.clean = clean;
+                    d.duo = it.duo;
                     d.x = it.x;
                     if (lane == 0) {
                         sDesc[j] = d;
@@ -1093,15 +1125,20 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     const int len = d.kb - d.ka;
                     int ids = block_y(d, d.ka * 8 + lane);
                     int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
-                    [[maybe_unused]] float4 sc{}, sc_next{};
-                    if constexpr (F8)
-                        sc = scales_of(ids);
+                    // F8: scales, of a duo's second head too; its key tiles come in turn
+                    const bool duo = F8 && d.duo;
+                    [[maybe_unused]] float2 sc[2] = {}, sc_next[2] = {};
+                    if constexpr (F8) {
+                        sc[0] = scales_of(ids);
+                        sc[1] = duo ? scales_of(next_head(ids)) : sc[0];
+                    }
                     const int tiles = it.single ? 1 : 2;
                     const bool q_early = qs == 0;  // the first item's: while the block ids come
                     if (q_early)
                         load_q(d, tiles);
-                    for (int t = 0; t < len; ++t) {
-                        if (t > 0 && (t & 3) == 0) {
+                    for (int i = 0; i < (duo ? 2 * len : len); ++i) {
+                        const int t = duo ? i >> 1 : i, second = duo ? i & 1 : 0;
+                        if (t > 0 && (t & 3) == 0 && !second) {
                             ids = ids_next;
                             ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
                         }
@@ -1109,19 +1146,25 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             bad = true;
                             break;
                         }
-                        load_tile(a.kmap, sK + cur * S::KTILE, &kfull[cur], ids, t);
+                        load_tile(a.kmap, sK + cur * S::KTILE, &kfull[cur],
+                                  second ? next_head(ids) : ids, t);
                         if constexpr (F8) {
                             // the tile's scales, which the softmax reads once S has arrived
-                            if (t > 0 && (t & 3) == 0)
-                                sc = sc_next;
-                            if ((t & 3) == 2 && t + 2 < len)
-                                sc_next = scales_of(ids_next);
+                            if (t > 0 && (t & 3) == 0 && !second) {
+                                sc[0] = sc_next[0];
+                                sc[1] = sc_next[1];
+                            }
+                            if ((t & 3) == 2 && t + 2 < len && !second) {
+                                sc_next[0] = scales_of(ids_next);
+                                sc_next[1] = duo ? scales_of(next_head(ids_next)) : sc_next[0];
+                            }
+                            const float2 now = second ? sc[1] : sc[0];
                             if ((lane >> 3) == (t & 3))
                                 st_shared_v4(
                                     scales_at + ((loaded % kScales) * 8 + (lane & 7)) * 16,
-                                    make_uint4(__float_as_uint(sc.x),
-                                               __float_as_uint(log2f(sc.y)),
-                                               __float_as_uint(1.f / sc.y), 0u));
+                                    make_uint4(__float_as_uint(now.x),
+                                               __float_as_uint(log2f(now.y)),
+                                               __float_as_uint(1.f / now.y), 0u));
                             __syncwarp();
                             if (elect_one())
                                 mbar_arrive(&kfull[cur]);
@@ -1133,7 +1176,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             par ^= 1;
                         }
                         // Q behind the first K tile, which does not wait for the item before
-                        if (t > 0)
+                        if (i > 0)
                             continue;
                         if (!q_early)
                             load_q(d, tiles);
@@ -1161,8 +1204,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     const int len = d.kb - d.ka;
                     int ids = block_y(d, d.ka * 8 + lane);
                     int ids_next = len > 4 ? block_y(d, (d.ka + 4) * 8 + lane) : 0;
-                    for (int t = 0; t < len; ++t) {
-                        if (t > 0 && (t & 3) == 0) {
+                    const bool duo = F8 && d.duo;
+                    for (int i = 0; i < (duo ? 2 * len : len); ++i) {
+                        const int t = duo ? i >> 1 : i, second = duo ? i & 1 : 0;
+                        if (t > 0 && (t & 3) == 0 && !second) {
                             ids = ids_next;
                             ids_next = t + 4 < len ? block_y(d, (d.ka + t + 4) * 8 + lane) : 0;
                         }
@@ -1172,7 +1217,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         }
                         load_tile(a.vmap,
                                   F8 ? sm + S::off_raw + cur * S::TILE8 : sV + cur * S::TILE,
-                                  &full[cur], ids, t);
+                                  &full[cur], second ? next_head(ids) : ids, t);
                         if constexpr (F8) {
                             if (elect_one())
                                 mbar_arrive(&full[cur]);
@@ -1207,7 +1252,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             constexpr uint32_t ID_O = ca_idesc(D, true, F8);
             constexpr uint32_t STEP = S::TILE >> 4, KSTEP = S::KTILE >> 4;
             const int x = wi - kMmaWarp;
-            const uint32_t qdesc = desc_lo(smem_u32(sQ) + (S::SPLIT ? 2 * S::TILE : 0), 16), kdesc = desc_lo(smem_u32(sK), 16);
+            const uint32_t qdesc = desc_lo(smem_u32(sQ) + (S::SPLIT ? 2 * S::TILE : 0), 16);
+            const uint32_t kdesc = desc_lo(smem_u32(sK), 16);
             const uint32_t vdesc = desc_lo(smem_u32(sV), S::PANEL);
             const uint32_t tS = tmem + x * kTile, tO = tmem + 256 + x * kTile;
             uint32_t kc = 0, kpar = 0, vc = 0, vpar = 0;  // ring cursors and parities
@@ -1236,17 +1282,19 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             uint32_t walks = 0;
             for (;;) {
                 while (const CaDesc *dp = bad ? nullptr : enter()) {
-                    const int len = dp->kb - dp->ka, ka = dp->ka, kb = dp->kb;
-                    const bool single = dp->ntok <= tpt;
+                    const bool duo = F8 && dp->duo;
+                    const int ka = dp->ka, kb = dp->kb, len = duo ? 2 * (kb - ka) : kb - ka;
+                    const bool single = dp->ntok <= tpt && !duo;
+                    const bool in_turn = single || duo;  // the key tiles are A's and B's in turn
                     // the key from which on V is tidied, negative in the second walk
                     const int tidy = dp->clean ? -(dp->pos0 + 1) : dp->len;
-                    // the stream's key tiles: t with t % 2 == x of a single item; of a
-                    // pair all for B, the ones its last token sees for A
+                    // the stream's key tiles: t with t % 2 == x of a single item or a duo; of
+                    // a pair all for B, the ones its last token sees for A
                     const int na =
                         x == 0 ? (dp->pos0 + min(dp->ntok, tpt) + kTile - 1) / kTile : kb;
                     leave();
-                    const int cnt = single ? (len + 1 - x) / 2 : max(0, min(kb, na) - ka);
-                    const int last = single ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
+                    const int cnt = in_turn ? (len + 1 - x) / 2 : max(0, min(kb, na) - ka);
+                    const int last = in_turn ? 2 * (cnt - 1) + x : cnt - 1;  // the last one
                     const uint32_t slot = single ? qs : qs + x;
                     const uint32_t qd = __shfl_sync(0xffffffffu, qdesc + (slot & 1) * STEP, 0);
                     auto skip_k = [&] {  // a tile of the other stream's
@@ -1323,7 +1371,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         }
                         if (next < len)
                             wait(&kfull[kc], kpar);
-                        const bool first = t == (single ? x : 0);
+                        const bool first = t == (in_turn ? x : 0);
                         if (first) {  // the epilogue of O's last use has read it
                             if (no > 0)
                                 wait(&oempty[x], (no - 1) & 1);
@@ -1379,7 +1427,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         tell(&qempty[(qs + 1 - x) & 1]);  // the other stream's queries
                     if (cnt == 0)
                         tell(&qempty[slot & 1]);
-                    if (single) {  // K0 K1, then V0 K2 | V1 K3 | ..: in turn A's and B's
+                    if (in_turn) {  // K0 K1, then V0 K2 | V1 K3 | ..: in turn A's and B's
                         first_s(x == 0, 0);
                         if (len > 1)
                             first_s(x == 1, 1);
@@ -1452,17 +1500,17 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         [[maybe_unused]] uint32_t qs = 0, tiles = 0;  // F8: query tiles and key tiles so far
         [[maybe_unused]] bool ahead = false;          // F8: the item's Q is split already
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
-        // F8: the item's Q to e4m3, before any of its S: a pair's tiles by their streams, a
-        // single one by B, for which A's epilogue has no work
+        // F8: the item's Q to e4m3, before any of its S: two tiles by their streams, a single
+        // one by B, for which A's epilogue has no work
         [[maybe_unused]] auto split = [&](const CaDesc &d) {
-            const bool single = d.ntok <= tpt;
+            const bool single = d.ntok <= tpt && !d.duo;
             if (single && x == 0)
                 return;
             const uint32_t t = single ? qs : qs + x, k = t & 1;
             if (!bad && !ca_wait(&qfull[k], (t >> 1) & 1))
                 bad = true;
             bad = __any_sync(0xffffffffu, bad);
-            const int toks = min(single || x == 0 ? d.ntok : d.ntok - tpt, tpt);
+            const int toks = min(single || d.duo || x == 0 ? d.ntok : d.ntok - tpt, tpt);
             split_q<D>(smem_u32(sQ) + k * S::TILE, smem_u32(sQ) + (S::SPLIT ? 2 + k : k) * S::TILE,
                        tid & (32 * kSmWarps - 1), toks * G, a.logit_scale,
                        sQf + t % kQTiles * kTile);
@@ -1473,15 +1521,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         };
         for (;;) {
             while (const CaDesc *dp = enter()) {
-                const bool single = dp->ntok <= tpt;
+                const bool duo = F8 && dp->duo, single = dp->ntok <= tpt && !duo;
                 const int len = dp->kb - dp->ka, pos0 = dp->pos0;
-                const int tile_tok = single || x == 0 ? 0 : tpt;  // its first token in the item
+                // its first token in the item
+                const int tile_tok = single || duo || x == 0 ? 0 : tpt;
                 const int toks = min(dp->ntok - tile_tok, tpt);   // its tokens
                 const int tok = min(r / G, toks - 1);             // rows past the last follow it
                 const int lim = pos0 + tile_tok + tok + 1;        // keys the row sees
                 const bool live = wq * 32 < toks * G;
                 int cnt = single ? (len + 1 - x) / 2 : len;            // key tiles
-                if (!single && x == 0)
+                if (!single && !duo && x == 0)
                     cnt = max(0, min(dp->kb, (pos0 + tpt + kTile - 1) / kTile) - dp->ka);
                 if (lent && cnt > 0) {  // A has taken what B left in place of its maxima
                     if (!bad && !ca_wait(taken, halves++ & 1))
@@ -1491,18 +1540,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 }
                 // keys the thread's half of the next tile still holds for the row: fewer
                 // than all for any row of the warp, and the tile is masked
-                [[maybe_unused]] float lr = 0.f;  // F8: what a logit is multiplied by but for K's scale
+                // F8: what a logit is multiplied by but for K's scale
+                [[maybe_unused]] float lr = 0.f;
                 [[maybe_unused]] const uint32_t qt = single ? qs : qs + x;
                 if constexpr (F8) {
                     if (!ahead)
                         split(*dp);
                     qs += single ? 1 : 2;
                 }
-                // F8: V's tile t of the item to fp16, by this stream's warps: a pair's are all
-                // A's, which is ahead of B; a single item's the stream's that uses them
-                [[maybe_unused]] auto to_fp16 = [&](int t) {
+                // F8: where the stream's key tile i lies among the item's
+                auto nth = [&](int i) { return single || duo ? x + 2 * i : i; };
+                // F8: V of the stream's key tile i to fp16, by this stream's warps: a pair's tiles
+                // by A, which is ahead of B, others by the stream that uses them
+                [[maybe_unused]] auto to_fp16 = [&](int i) {
                     constexpr uint32_t N = F8 ? NR : 1;
-                    const uint32_t k = tiles + t, st = k % NV, rs = k % N;
+                    const uint32_t k = tiles + nth(i), st = k % NV, rs = k % N;
+                    const int t = single ? nth(i) : i;
                     if (!bad && (!ca_wait(&rfull[rs], (k / N) & 1) ||
                                  (k >= NV && !ca_wait(&vempty[st], (k / NV - 1) & 1))))
                         bad = true;
@@ -1528,8 +1581,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 float l0 = 0.f, l1 = 0.f;
                 for (int t = cnt; t > 0; --t, m_lim -= m_step) {
                     if constexpr (F8) {
-                        if (single || x == 0)
-                            to_fp16(single ? x + 2 * (cnt - t) : cnt - t);
+                        if (single || duo || x == 0)
+                            to_fp16(cnt - t);
                     }
                     if (!bad && !ca_wait(&sfull[x], ns & 1))
                         bad = true;
@@ -1556,8 +1609,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         float m_new;
                         // F8: the scales of this half's four blocks
                         [[maybe_unused]] const uint32_t sc_at =
-                            scales_at + (((tiles + (single ? x + 2 * (cnt - t) : cnt - t)) %
-                                          kScales) * 8 + hf * 4) * 16;
+                            scales_at + ((tiles + nth(cnt - t)) % kScales * 8 + hf * 4) * 16;
                         if constexpr (F8) {
                             if (t == cnt)
                                 lr = sQf[qt % kQTiles * kTile + r];
@@ -1660,20 +1712,22 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 }
                 // ----------------------------------------------------- epilogue
                 if constexpr (F8) {
-                    if (!single && x == 0)  // the tiles that B alone sees
+                    if (!single && !duo && x == 0)  // the tiles that B alone sees
                         for (int t = cnt; t < len; ++t)
                             to_fp16(t);
-                    tiles += len;
+                    tiles += duo ? 2 * len : len;
                     // a next pair's Q if it is there, so that its S comes during the epilogue
                     // (16 prompts of 64 dims 802 -> 770 us; with a single item's, whose B
                     // A's epilogue waits for, 256 speculative chunks take 381 us, not 350)
                     const uint32_t j = (nd + 1) % kDescs;
                     ahead = warp_test(&described[j], ((nd + 1) / kDescs) & 1) &&
-                            sDesc[j].ntok > tpt && warp_test(&qfull[(qs + x) & 1], ((qs + x) >> 1) & 1);
+                            (sDesc[j].ntok > tpt || (sDesc[j].duo && sDesc[j].ntok)) &&
+                            warp_test(&qfull[(qs + x) & 1], ((qs + x) >> 1) & 1);
                     if (ahead)
                         split(sDesc[j]);
                 }
                 const CaDesc &d = *dp;
+                const int head = d.h + (duo ? x : 0);
                 // (what follows from G stays out of the key loop's registers)
                 int G = a.Hq / a.Hkv;
                 asm volatile("" : "+r"(G));
@@ -1782,7 +1836,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                 const int row = x * kTile + r;  // within a slot
                 __nv_bfloat16 *dst =
                     a.out +
-                    (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + d.h * G + r % G) * D +
+                    (static_cast<size_t>(d.row0 + tile_tok + r / G) * a.Hq + head * G + r % G) * D +
                     hf * HD;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 float odd = 0.f;  // becomes NaN with any element of O
@@ -1838,7 +1892,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         if (blk < 0 || blk >= a.num_blocks)
                             continue;
                         const size_t at =
-                            (static_cast<size_t>(blk) * a.Hkv + d.h) * kBlk * D + hf * HD;
+                            (static_cast<size_t>(blk) * a.Hkv + head) * kBlk * D + hf * HD;
                         const __nv_bfloat16 *v = a.vpool + at;
                         [[maybe_unused]] const uint8_t *v8 =
                             reinterpret_cast<const uint8_t *>(a.vpool) + at;
@@ -1934,7 +1988,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             return m == -INFINITY ? 0.f : ex2_approx(m - M) * iv;
                         };
                         const size_t to =
-                            (static_cast<size_t>(d.row0 + tile_tok + row / G) * a.Hq + d.h * G +
+                            (static_cast<size_t>(d.row0 + tile_tok + row / G) * a.Hq + head * G +
                              row % G) * D;
                         const int col = lane % (D / 4) * 4, sub = lane / (D / 4);
 #pragma unroll 1
@@ -2077,7 +2131,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                 __nv_bfloat16 *d2 =
                                     a.out +
                                     (static_cast<size_t>(d.row0 + tile_tok + rr / G) * a.Hq +
-                                     d.h * G + rr % G) * D + lane * EL;
+                                     head * G + rr % G) * D + lane * EL;
 #pragma unroll
                                 for (int e = 0; e < EL; e += 2)
                                     *reinterpret_cast<uint32_t *>(d2 + e) =

@@ -64,6 +64,9 @@ struct SpShared {
     float2 ends[kSpCtas];                    // the CTAs' (largest, smallest finite)
     uint32_t scan32[kSpWarps];
     uint32_t key_lo, key_hi, listed, equal, equal_upto;
+    // the row's, as the functions below read it
+    float M, per_gap, least, u, top_p;
+    int top_k, mis;
     WeightScale scale;
     float2 gap;   // the largest gap to the maximum that min_p allows, as a pair
     Cut cut;      // CTA 0's
@@ -176,7 +179,7 @@ __device__ __forceinline__ T block_before(T v, T *scratch, T &total)
 
 // Sorts list[0 .. n) by the CTA, falling; n at most kList = 2 kSpThreads.  Every thread holds
 // two neighbours' places; what lies less than 64 apart is compared in a warp's registers.
-__device__ __forceinline__ void sort_falling(uint64_t *list, int n)
+__device__ __noinline__ void sort_falling(uint64_t *list, int n)
 {
     static_assert(kList == 2 * kSpThreads, "two entries a thread");
     const int t = threadIdx.x, lane = t & 31;
@@ -237,7 +240,7 @@ __device__ __forceinline__ uint64_t part_of(float u, uint64_t s)
 }
 
 // ceil(p * s), p above 0 and below 1.
-__device__ __forceinline__ uint64_t target_of(float p, uint64_t s)
+__device__ __noinline__ uint64_t target_of(float p, uint64_t s)
 {
     const uint64_t f = part_of(p, s);
     // exact when p * s has no fraction: p = m 2^-sh
@@ -253,6 +256,339 @@ __device__ __forceinline__ uint64_t target_of(float p, uint64_t s)
     else
         rest = (lo | hi) != 0;
     return f + rest;
+}
+
+// The kept sum that a row's random number asks to be exceeded.
+__device__ __forceinline__ uint64_t level_of(float u, uint64_t total)
+{
+    return u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
+}
+
+__device__ __forceinline__ float value_at(uint64_t entry)
+{
+    return value_of(static_cast<uint32_t>(entry >> 32));
+}
+
+// What follows runs once or twice a row, most of it in CTA 0 alone.  In line it made the kernel
+// 330 KB of instructions, now 165 (410 and 222 for bf16 logits); the times are the same.
+
+__device__ __noinline__ uint64_t weight_of(const SpShared &S, float v)
+{
+    uint64_t w, same;
+    weights(S.table, S.scale, S.M, v, v, w, same);
+    return w;
+}
+
+// CTA 0's sums of the CTAs' histograms: of the weights, a bucket's 64 bits in part[1] and
+// part[0].
+__device__ __noinline__ void gather_sums(SpShared &S, int ctas, int rank, bool counts, bool weights)
+{
+    const int tid = threadIdx.x;
+    static_assert(kBuckets == kSpThreads, "a bucket a thread");
+    all_ctas();
+    if (rank != 0)
+        return;
+    uint32_t n[kSpCtas], w[3][kSpCtas];  // all on their way at once
+#pragma unroll
+    for (int r = 0; r < kSpCtas; ++r) {
+        n[r] = w[0][r] = w[1][r] = w[2][r] = 0;
+        if (counts && r < ctas)
+            n[r] = ld_dsmem_u32(dsmem_addr(&S.count[tid], r));
+        if (weights && r < ctas)
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                w[k][r] = ld_dsmem_u32(dsmem_addr(&S.part[k][tid], r));
+    }
+    uint32_t all = 0;
+    uint64_t sum = 0;
+#pragma unroll
+    for (int r = 0; r < kSpCtas; ++r) {
+        all += n[r];
+        sum += w[0][r] + (static_cast<uint64_t>(w[1][r]) << 16) +
+               (static_cast<uint64_t>(w[2][r]) << 32);
+    }
+    S.count[tid] = all;
+    S.part[0][tid] = static_cast<uint32_t>(sum);
+    S.part[1][tid] = static_cast<uint32_t>(sum >> 32);
+}
+
+// CTA 0 alone: the bucket where `above` + counts reach `k`, or `mass` + weights reach
+// `target` (k = 0), from the largest values on, which the last buckets of a `rising`
+// histogram hold and the first of the other.  bucket < 0: fewer entries than k.  `in`
+// becomes about the number of entries up to the bucket, of a first histogram by weights.
+__device__ __noinline__ void find(SpShared &S, uint32_t k, uint64_t target, bool rising)
+{
+    const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
+    const int b = rising ? kBuckets - 1 - tid : tid;  // (the thread's own sums, if falling)
+    if (rising)
+        __syncthreads();
+    const uint32_t n = S.count[b];
+    const uint64_t w = static_cast<uint64_t>(S.part[1][b]) << 32 | S.part[0][b];
+    const uint32_t upto_n = warp_incl(n, lane);
+    const uint64_t upto_w = warp_incl(w, lane);
+    if (lane == 31) {
+        S.scan32[wi] = upto_n;
+        S.scan64[wi] = upto_w;
+    }
+    __syncthreads();
+    const uint32_t sn = lane < kSpWarps ? S.scan32[lane] : 0;
+    const uint64_t sw = lane < kSpWarps ? S.scan64[lane] : 0;
+    const uint32_t in = warp_incl(sn, lane);
+    const uint64_t iw = warp_incl(sw, lane);
+    const uint32_t n0 = S.cut.above + __shfl_sync(0xffffffffu, in - sn, wi) + upto_n - n;
+    const uint64_t w0 = S.cut.mass + __shfl_sync(0xffffffffu, iw - sw, wi) + upto_w - w;
+    const uint32_t all_n = __shfl_sync(0xffffffffu, in, 31);
+    const uint64_t all_w = __shfl_sync(0xffffffffu, iw, 31);
+    __syncthreads();  // S.cut and the scans are read
+    const bool here = k ? n0 < k && n0 + n >= k : w0 < target && w0 + w >= target;
+    if (tid == 0 && k > all_n && !rising) {
+        S.cut.mass = all_w;
+        S.cut.bucket = -1;
+        S.cut.tau = -INFINITY;
+        S.cut.m = 0x7fffffff;
+    }
+    if (tid == 0)
+        S.cut.in = 0;
+    if (here) {
+        S.cut.above = n0;
+        S.cut.mass = w0;
+        S.cut.bucket = b;
+    }
+    if (!rising && k == 0) {
+        __syncthreads();
+        if (w0 < target)  // 2^-44 w over the weight in the bucket's middle
+            atomicAdd(&S.cut.in,
+                      static_cast<uint32_t>(fminf(static_cast<float>(w) * 5.6843419e-14f *
+                                                      exp2f((b + 0.5f) / S.per_gap * S.scale.ch),
+                                                  1e6f)) + 1);
+    }
+    __syncthreads();
+}
+
+// CTA 0's cut to all, in two places in turn, as a CTA may still read the one before.
+__device__ __noinline__ void tell(SpShared &S, int ctas, int rank, int turn)
+{
+    if (rank == 0) {
+        __syncthreads();
+        constexpr int W = sizeof(Cut) / 4;
+        for (int k = threadIdx.x; k < W * ctas; k += kSpThreads)
+            st_dsmem_u32(dsmem_addr(reinterpret_cast<uint32_t *>(&S.told[turn]) + k % W, k / W),
+                         reinterpret_cast<const uint32_t *>(&S.cut)[k % W]);
+    }
+    all_ctas();
+}
+
+// CTA 0: of its sorted list of n, the entry at which the count (with `above`) reaches
+// k, or the weights (with `mass`) reach `target`; tau, what is kept of it, the weights.
+__device__ __noinline__ void cut_list(SpShared &S, int n, uint32_t k, uint64_t target, bool weights)
+{
+    const int tid = threadIdx.x;
+    if (tid == 0)
+        S.equal = S.equal_upto = 0;
+    constexpr int PL = kList / kSpThreads;
+    uint64_t w[PL], sum = 0, all;
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        const int p = tid * PL + j;
+        w[j] = weights && p < n ? weight_of(S, value_at(S.list[p])) : 0;
+        sum += w[j];
+    }
+    const uint64_t mass = S.cut.mass;
+    const uint32_t above = S.cut.above;
+    uint64_t at = mass + block_before(sum, S.scan64, all);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        const int p = tid * PL + j;
+        const bool here =
+            p < n && (k ? above + p + 1 == k : at < target && at + w[j] >= target);
+        at += w[j];
+        if (here) {
+            S.cut.tau = value_at(S.list[p]);
+            S.cut.mass = at;
+            S.cut.lo = static_cast<uint32_t>(p);
+        }
+    }
+    __syncthreads();
+    const uint32_t key = key_of(S.cut.tau);
+    const int last = static_cast<int>(S.cut.lo);
+    for (int p = tid; p < n; p += kSpThreads)
+        if (static_cast<uint32_t>(S.list[p] >> 32) == key) {
+            atomicAdd(&S.equal, 1u);
+            if (p <= last)
+                atomicAdd(&S.equal_upto, 1u);
+        }
+    __syncthreads();
+    if (tid == 0) {
+        S.cut.in = S.equal;
+        S.cut.m = static_cast<int>(S.equal_upto);
+    }
+    __syncthreads();
+}
+
+// CTA 0: the same of at most kSmall entries: a thread an entry, which adds up what comes before it
+// by value, and then by index.
+__device__ __noinline__ void finish_small(SpShared &S, int n, uint64_t row_sum, int32_t *token)
+{
+    const int tid = threadIdx.x, wi = tid >> 5, top_k = S.top_k;
+    const bool by_mass = S.top_p < 1.f;
+    const float top_p = S.top_p;
+    uint64_t *entries = S.list, *sums = S.list + kSmall;
+    const bool mine = tid < n;
+    const uint64_t e = mine ? entries[tid] : 0;
+    const float v = mine ? value_at(e) : -INFINITY;
+    uint64_t w = 0;
+    if (wi < kSmall / 32)
+        w = mine ? weight_of(S, v) : 0;
+    if (tid < kSmall)
+        sums[tid] = w;
+    if (tid == 0) {
+        S.cut.lo = 0;
+        S.equal = S.equal_upto = 0;
+    }
+    __syncthreads();
+    int rank_of = 0;
+    uint64_t above = 0;
+    const int in_k = top_k > 0 ? min(top_k, n) : n;
+    if (mine) {
+        for (int q = 0; q < n; ++q)
+            if (entries[q] > e) {
+                ++rank_of;
+                above += sums[q];
+            }
+        if (rank_of == in_k - 1)
+            S.scan64[0] = above + w;  // of the top_k
+    }
+    __syncthreads();
+    uint64_t target = ~0ull;
+    if (by_mass)
+        target = top_p > 0.f
+                     ? max(target_of(top_p, row_sum ? row_sum : S.scan64[0]), uint64_t(1))
+                     : 1;
+    const bool in = mine && rank_of < in_k && above < target;
+    const uint64_t kept_w = in && v >= S.least ? w : 0;
+    if (tid < kSmall)
+        sums[tid] = kept_w;
+    if (in)
+        atomicMax(&S.cut.lo, static_cast<uint32_t>(rank_of) + 1);
+    __syncthreads();
+    if (in && rank_of + 1 == static_cast<int>(S.cut.lo))
+        S.cut.tau = v;
+    uint64_t total = 0, before = 0;
+    if (mine)
+        for (int q = 0; q < n; ++q) {
+            total += sums[q];
+            // (the low halves fall with the index)
+            if (static_cast<uint32_t>(entries[q]) > static_cast<uint32_t>(e))
+                before += sums[q];
+        }
+    __syncthreads();
+    if (mine && v == S.cut.tau) {
+        atomicAdd(&S.equal, 1u);
+        if (in)
+            atomicAdd(&S.equal_upto, 1u);
+    }
+    if (tid == 0)
+        S.cut.mass = total;
+    if (mine && token) {
+        const uint64_t level = level_of(S.u, total);
+        if (before <= level && level < before + kept_w)
+            *token = static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)) - S.mis;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        S.cut.in = S.equal;
+        S.cut.m = static_cast<int>(S.equal_upto);
+    }
+}
+
+// CTA 0: the cuts of the n entries it has gathered, if they fit in the list, and the token.
+// row_sum: the weights that top_p is a part of, 0 for those of the top_k.
+__device__ __noinline__ void finish(SpShared &S, int rank, int n, uint64_t row_sum, int32_t *token)
+{
+    const int tid = threadIdx.x, top_k = S.top_k;
+    const float top_p = S.top_p;
+    const bool by_mass = top_p < 1.f;
+    if (rank != 0)
+        return;
+    __syncthreads();
+    if (tid == 0) {
+        S.cut = Cut{};
+        S.cut.done = n <= kList;
+        S.cut.tau = -INFINITY;
+        S.cut.m = 0x7fffffff;
+    }
+    if (n <= kSmall) {
+        finish_small(S, n, row_sum, token);
+    } else if (n <= kList) {
+        sort_falling(S.list, n);
+        int kept = n;
+        if (top_k > 0 && n >= top_k) {
+            cut_list(S, n, static_cast<uint32_t>(top_k), 0, true);
+            kept = top_k;
+        }
+        if (by_mass) {
+            uint64_t sum = row_sum ? row_sum : S.cut.mass;
+            if (!row_sum && n < top_k) {  // all there are
+                uint64_t s = 0;
+                for (int p = tid; p < n; p += kSpThreads)
+                    s += weight_of(S, value_at(S.list[p]));
+                block_before(s, S.scan64, sum);
+            }
+            const uint64_t target =
+                top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
+            __syncthreads();
+            if (tid == 0)
+                S.cut.mass = 0;
+            __syncthreads();
+            cut_list(S, n, 0, target, true);
+            kept = static_cast<int>(S.cut.lo) + 1;
+        }
+        // in the order of their index (which the entry's low half falls with)
+        uint64_t e[kList / kSpThreads], sum = 0, total;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kList / kSpThreads; ++j) {
+            const int p = j * kSpThreads + tid;
+            e[j] = p < kept ? S.list[p] : 0;
+            if (p < kept && !(value_at(e[j]) >= S.least))
+                e[j] = 0;
+            sum += e[j] ? weight_of(S, value_at(e[j])) : 0;
+        }
+        block_before(sum, S.scan64, total);
+        if (tid == 0)
+            S.cut.mass = total;
+        if (token) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < kList / kSpThreads; ++j) {
+                const int p = j * kSpThreads + tid;
+                if (p < kept)
+                    S.list[p] = e[j] << 32 | e[j] >> 32;
+            }
+            __syncthreads();
+            sort_falling(S.list, kept);
+            const uint64_t level = level_of(S.u, total);
+            constexpr int PL = kList / kSpThreads;
+            uint64_t w[PL], s = 0, all;
+#pragma unroll
+            for (int j = 0; j < PL; ++j) {
+                const int p = tid * PL + j;
+                const uint64_t v = p < kept ? S.list[p] : 0;
+                w[j] = v ? weight_of(S, value_of(static_cast<uint32_t>(v))) : 0;
+                s += w[j];
+            }
+            uint64_t at = block_before(s, S.scan64, all);
+#pragma unroll
+            for (int j = 0; j < PL; ++j) {
+                if (at <= level && level < at + w[j])
+                    *token = static_cast<int>(0xffffffffu - static_cast<uint32_t>(
+                                                                S.list[tid * PL + j] >> 32)) -
+                             S.mis;
+                at += w[j];
+            }
+        }
+    }
 }
 
 }  // namespace
@@ -322,6 +658,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         S.table[k] = d_table.v[k];
     for (int b = tid; b < kBuckets; b += kSpThreads)
         S.count[b] = S.part[0][b] = S.part[1][b] = S.part[2][b] = 0;
+#pragma unroll 1
     for (int j = 0; j < J; ++j) {
         const int g = g0 + j * 32 + lane;
         if (g >= c0 && g < c1)
@@ -340,6 +677,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
 
     // the largest logit and the smallest finite one; NaN becomes -infinity
     float top = -INFINITY, bottom = INFINITY;
+#pragma unroll 1
     for (int j = 0; j < J; ++j) {
         float v[VE];
         unpack(run[j * 32 + lane], v);
@@ -388,6 +726,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         const int psz = a.prob_bf16 ? 2 : 4;
         uint8_t *to = static_cast<uint8_t *>(a.probs) + (i * a.prob_stride - mis) * psz;
         const bool whole = reinterpret_cast<uintptr_t>(to) % 16 == 0;
+#pragma unroll 1
         for (int j = 0; j < J; ++j) {
             float v[VE], p[VE];
             unpack(run[j * 32 + lane], v);
@@ -452,11 +791,6 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             write_row([](float, int) { return 0.f; }, false, 0.f, 0);
         return;
     }
-    auto weight_of = [&](float v) {
-        uint64_t w, same;
-        weights(S.table, c, M, v, v, w, same);
-        return w;
-    };
     // The weights of vector j of the lane: `take` gets a value and its weight.
     auto each_weight = [&](int j, auto take) {
         float v[VE];
@@ -485,13 +819,10 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         const unsigned m = __ballot_sync(0xffffffffu, enough);
         least = fminf(__shfl_sync(0xffffffffu, v, m ? __ffs(m) - 1 : 31), M);
     }
-    auto within = [&](float v) { return v >= least; };  // min_p's part
-    const uint64_t kNone = 0;  // (an entry of the list that is none)
     auto entry_of = [&](float v, int j, int k) {  // falling by value, then rising by index
         return static_cast<uint64_t>(key_of(v)) << 32 |
                (0xffffffffu - static_cast<uint32_t>((g0 + j * 32 + lane) * VE + k));
     };
-    auto value_at = [&](uint64_t e) { return value_of(static_cast<uint32_t>(e >> 32)); };
 
     // ---------------------------------------------------------------- the cut
     Cut cut{};
@@ -512,35 +843,20 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     auto end_of = [&](int b) {
         return b >= kBuckets - 1 ? INFINITY : static_cast<float>(b + 1);
     };
-    // CTA 0's sums of the CTAs' histograms: of the weights, a bucket's 64 bits in part[1] and
-    // part[0].
-    auto gather_sums = [&](bool counts, bool weights) {
-        static_assert(kBuckets == kSpThreads, "a bucket a thread");
-        all_ctas();
-        if (rank != 0)
-            return;
-        uint32_t n[kSpCtas], w[3][kSpCtas];  // all on their way at once
-#pragma unroll
-        for (int r = 0; r < kSpCtas; ++r) {
-            n[r] = w[0][r] = w[1][r] = w[2][r] = 0;
-            if (counts && r < ctas)
-                n[r] = ld_dsmem_u32(dsmem_addr(&S.count[tid], r));
-            if (weights && r < ctas)
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    w[k][r] = ld_dsmem_u32(dsmem_addr(&S.part[k][tid], r));
-        }
-        uint32_t all = 0;
-        uint64_t sum = 0;
-#pragma unroll
-        for (int r = 0; r < kSpCtas; ++r) {
-            all += n[r];
-            sum += w[0][r] + (static_cast<uint64_t>(w[1][r]) << 16) +
-                   (static_cast<uint64_t>(w[2][r]) << 32);
-        }
-        S.count[tid] = all;
-        S.part[0][tid] = static_cast<uint32_t>(sum);
-        S.part[1][tid] = static_cast<uint32_t>(sum >> 32);
+    if (tid == 0) {
+        S.M = M;
+        S.per_gap = per_gap;
+        S.least = least;
+        S.u = u;
+        S.top_p = top_p;
+        S.top_k = top_k;
+        S.mis = mis;
+    }
+    int turn = 0;
+    auto told = [&] {  // CTA 0's cut
+        turn ^= 1;
+        tell(S, ctas, rank, turn);
+        cut = S.told[turn];
     };
     // (a CTA has at most 2^15.5 entries, so that no sum of 16 bits of each passes 32)
     auto add_weight = [&](int b, uint64_t w) {
@@ -553,6 +869,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     };
     // Every entry above -infinity is counted under `place` (below 0: not at all).
     auto histogram = [&](bool counts, bool weights, auto place) {
+#pragma unroll 1
         for (int j = 0; j < J; ++j) {
             float v[VE];
             unpack(run[j * 32 + lane], v);
@@ -564,80 +881,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 if (counts)
                     atomicAdd(&S.count[b], 1u);
                 if (weights)
-                    add_weight(b, weight_of(v[k]));
+                    add_weight(b, weight_of(S, v[k]));
             }
         }
-        gather_sums(counts, weights);
+        gather_sums(S, ctas, rank, counts, weights);
     };
     auto clear = [&] {
         for (int b = tid; b < kBuckets; b += kSpThreads)
             S.count[b] = S.part[0][b] = S.part[1][b] = S.part[2][b] = 0;
         __syncthreads();
-    };
-    // CTA 0 alone: the bucket where `above` + counts reach `k`, or `mass` + weights reach
-    // `target` (k = 0), from the largest values on, which the last buckets of a `rising`
-    // histogram hold and the first of the other.  bucket < 0: fewer entries than k.  `in`
-    // becomes about the number of entries up to the bucket, of a first histogram by weights.
-    auto find = [&](uint32_t k, uint64_t target, bool rising) {
-        const int b = rising ? kBuckets - 1 - tid : tid;  // (the thread's own sums, if falling)
-        if (rising)
-            __syncthreads();
-        const uint32_t n = S.count[b];
-        const uint64_t w = static_cast<uint64_t>(S.part[1][b]) << 32 | S.part[0][b];
-        const uint32_t upto_n = warp_incl(n, lane);
-        const uint64_t upto_w = warp_incl(w, lane);
-        if (lane == 31) {
-            S.scan32[wi] = upto_n;
-            S.scan64[wi] = upto_w;
-        }
-        __syncthreads();
-        const uint32_t sn = lane < kSpWarps ? S.scan32[lane] : 0;
-        const uint64_t sw = lane < kSpWarps ? S.scan64[lane] : 0;
-        const uint32_t in = warp_incl(sn, lane);
-        const uint64_t iw = warp_incl(sw, lane);
-        const uint32_t n0 = S.cut.above + __shfl_sync(0xffffffffu, in - sn, wi) + upto_n - n;
-        const uint64_t w0 = S.cut.mass + __shfl_sync(0xffffffffu, iw - sw, wi) + upto_w - w;
-        const uint32_t all_n = __shfl_sync(0xffffffffu, in, 31);
-        const uint64_t all_w = __shfl_sync(0xffffffffu, iw, 31);
-        __syncthreads();  // S.cut and the scans are read
-        const bool here = k ? n0 < k && n0 + n >= k : w0 < target && w0 + w >= target;
-        if (tid == 0 && k > all_n && !rising) {
-            S.cut.mass = all_w;
-            S.cut.bucket = -1;
-            S.cut.tau = -INFINITY;
-            S.cut.m = 0x7fffffff;
-        }
-        if (tid == 0)
-            S.cut.in = 0;
-        if (here) {
-            S.cut.above = n0;
-            S.cut.mass = w0;
-            S.cut.bucket = b;
-        }
-        if (!rising && k == 0) {
-            __syncthreads();
-            if (w0 < target)  // 2^-44 w over the weight in the bucket's middle
-                atomicAdd(&S.cut.in,
-                          static_cast<uint32_t>(fminf(static_cast<float>(w) * 5.6843419e-14f *
-                                                          exp2f((b + 0.5f) / per_gap * c.ch),
-                                                      1e6f)) + 1);
-        }
-        __syncthreads();
-    };
-    int turn = 0;
-    auto tell = [&] {  // CTA 0's cut to all: into two places in turn, as a CTA may still
-                       // read the one before
-        turn ^= 1;
-        if (rank == 0) {
-            __syncthreads();
-            constexpr int W = sizeof(Cut) / 4;
-            for (int k = tid; k < W * ctas; k += kSpThreads)
-                st_dsmem_u32(
-                    dsmem_addr(reinterpret_cast<uint32_t *>(&S.told[turn]) + k % W, k / W),
-                    reinterpret_cast<const uint32_t *>(&S.cut)[k % W]);
-        }
-        all_ctas();
-        cut = S.told[turn];
     };
     // The entries for which `inside` holds into the CTAs' lists, and these, if that is not too
     // much, one behind the other into CTA 0's; there, how many entries there are.
@@ -646,6 +898,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         if (tid == 0)
             S.listed = 0;
         __syncthreads();
+#pragma unroll 1
         for (int j = 0; j < J; ++j) {
             float v[VE];
             unpack(run[j * 32 + lane], v);
@@ -692,209 +945,8 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         }
         return n;
     };
-    // CTA 0: of its sorted list of n, the entry at which the count (with `above`) reaches
-    // k, or the weights (with `mass`) reach `target`; tau, what is kept of it, the weights.
-    auto cut_list = [&](int n, uint32_t k, uint64_t target, bool weights) {
-        if (tid == 0)
-            S.equal = S.equal_upto = 0;
-        constexpr int PL = kList / kSpThreads;
-        uint64_t w[PL], sum = 0, all;
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const int p = tid * PL + j;
-            w[j] = weights && p < n ? weight_of(value_at(S.list[p])) : 0;
-            sum += w[j];
-        }
-        const uint64_t mass = S.cut.mass;
-        const uint32_t above = S.cut.above;
-        uint64_t at = mass + block_before(sum, S.scan64, all);
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const int p = tid * PL + j;
-            const bool here =
-                p < n && (k ? above + p + 1 == k : at < target && at + w[j] >= target);
-            at += w[j];
-            if (here) {
-                S.cut.tau = value_at(S.list[p]);
-                S.cut.mass = at;
-                S.cut.lo = static_cast<uint32_t>(p);
-            }
-        }
-        __syncthreads();
-        const uint32_t key = key_of(S.cut.tau);
-        const int last = static_cast<int>(S.cut.lo);
-        for (int p = tid; p < n; p += kSpThreads)
-            if (static_cast<uint32_t>(S.list[p] >> 32) == key) {
-                atomicAdd(&S.equal, 1u);
-                if (p <= last)
-                    atomicAdd(&S.equal_upto, 1u);
-            }
-        __syncthreads();
-        if (tid == 0) {
-            S.cut.in = S.equal;
-            S.cut.m = static_cast<int>(S.equal_upto);
-        }
-        __syncthreads();
-    };
     const bool by_mass = top_p < 1.f;
-    // The same of at most kSmall entries: a thread an entry, which adds up what comes before it
-    // by value, and then by index.
-    auto finish_small = [&](int n, uint64_t row_sum) {
-        uint64_t *entries = S.list, *sums = S.list + kSmall;
-        const bool mine = tid < n;
-        const uint64_t e = mine ? entries[tid] : 0;
-        const float v = mine ? value_at(e) : -INFINITY;
-        uint64_t w = 0;
-        if (wi < kSmall / 32)
-            w = mine ? weight_of(v) : 0;
-        if (tid < kSmall)
-            sums[tid] = w;
-        if (tid == 0) {
-            S.cut.lo = 0;
-            S.equal = S.equal_upto = 0;
-        }
-        __syncthreads();
-        int rank_of = 0;
-        uint64_t above = 0;
-        const int in_k = top_k > 0 ? min(top_k, n) : n;
-        if (mine) {
-            for (int q = 0; q < n; ++q)
-                if (entries[q] > e) {
-                    ++rank_of;
-                    above += sums[q];
-                }
-            if (rank_of == in_k - 1)
-                S.scan64[0] = above + w;  // of the top_k
-        }
-        __syncthreads();
-        uint64_t target = ~0ull;
-        if (by_mass)
-            target = top_p > 0.f
-                         ? max(target_of(top_p, row_sum ? row_sum : S.scan64[0]), uint64_t(1))
-                         : 1;
-        const bool in = mine && rank_of < in_k && above < target;
-        const uint64_t kept_w = in && within(v) ? w : 0;
-        if (tid < kSmall)
-            sums[tid] = kept_w;
-        if (in)
-            atomicMax(&S.cut.lo, static_cast<uint32_t>(rank_of) + 1);
-        __syncthreads();
-        if (in && rank_of + 1 == static_cast<int>(S.cut.lo))
-            S.cut.tau = v;
-        uint64_t total = 0, before = 0;
-        if (mine)
-            for (int q = 0; q < n; ++q) {
-                total += sums[q];
-                // (the low halves fall with the index)
-                if (static_cast<uint32_t>(entries[q]) > static_cast<uint32_t>(e))
-                    before += sums[q];
-            }
-        __syncthreads();
-        if (mine && v == S.cut.tau) {
-            atomicAdd(&S.equal, 1u);
-            if (in)
-                atomicAdd(&S.equal_upto, 1u);
-        }
-        if (tid == 0)
-            S.cut.mass = total;
-        if (mine && a.tokens) {
-            const uint64_t level = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
-            if (before <= level && level < before + kept_w)
-                a.tokens[i] =
-                    static_cast<int>(0xffffffffu - static_cast<uint32_t>(e)) - mis;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            S.cut.in = S.equal;
-            S.cut.m = static_cast<int>(S.equal_upto);
-        }
-    };
-    // CTA 0: the cuts of the n entries it has gathered, if they fit in the list, and the token.
-    // row_sum: the weights that top_p is a part of, 0 for those of the top_k.
-    auto finish = [&](int n, uint64_t row_sum) {
-        if (rank != 0)
-            return;
-        __syncthreads();
-        if (tid == 0) {
-            S.cut = Cut{};
-            S.cut.done = n <= kList;
-            S.cut.tau = -INFINITY;
-            S.cut.m = 0x7fffffff;
-        }
-        if (n <= kSmall) {
-            finish_small(n, row_sum);
-        } else if (n <= kList) {
-            sort_falling(S.list, n);
-            int kept = n;
-            if (top_k > 0 && n >= top_k) {
-                cut_list(n, static_cast<uint32_t>(top_k), 0, true);
-                kept = top_k;
-            }
-            if (by_mass) {
-                uint64_t sum = row_sum ? row_sum : S.cut.mass;
-                if (!row_sum && n < top_k) {  // all there are
-                    uint64_t s = 0;
-                    for (int p = tid; p < n; p += kSpThreads)
-                        s += weight_of(value_at(S.list[p]));
-                    block_before(s, S.scan64, sum);
-                }
-                const uint64_t target =
-                    top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
-                __syncthreads();
-                if (tid == 0)
-                    S.cut.mass = 0;
-                __syncthreads();
-                cut_list(n, 0, target, true);
-                kept = static_cast<int>(S.cut.lo) + 1;
-            }
-            // in the order of their index (which the entry's low half falls with)
-            uint64_t e[kList / kSpThreads], sum = 0, total;
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < kList / kSpThreads; ++j) {
-                const int p = j * kSpThreads + tid;
-                e[j] = p < kept ? S.list[p] : kNone;
-                if (p < kept && !within(value_at(e[j])))
-                    e[j] = kNone;
-                sum += e[j] ? weight_of(value_at(e[j])) : 0;
-            }
-            block_before(sum, S.scan64, total);
-            if (tid == 0)
-                S.cut.mass = total;
-            if (a.tokens) {
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < kList / kSpThreads; ++j) {
-                    const int p = j * kSpThreads + tid;
-                    if (p < kept)
-                        S.list[p] = e[j] << 32 | e[j] >> 32;
-                }
-                __syncthreads();
-                sort_falling(S.list, kept);
-                const uint64_t level =
-                    u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
-                constexpr int PL = kList / kSpThreads;
-                uint64_t w[PL], s = 0, all;
-#pragma unroll
-                for (int j = 0; j < PL; ++j) {
-                    const int p = tid * PL + j;
-                    const uint64_t v = p < kept ? S.list[p] : kNone;
-                    w[j] = v ? weight_of(value_of(static_cast<uint32_t>(v))) : 0;
-                    s += w[j];
-                }
-                uint64_t at = block_before(s, S.scan64, all);
-#pragma unroll
-                for (int j = 0; j < PL; ++j) {
-                    if (at <= level && level < at + w[j])
-                        a.tokens[i] =
-                            static_cast<int>(0xffffffffu - static_cast<uint32_t>(
-                                                 S.list[tid * PL + j] >> 32)) - mis;
-                    at += w[j];
-                }
-            }
-        }
-    };
+    int32_t *token = a.tokens ? a.tokens + i : nullptr;
     bool counted = false;  // CTA 0 holds the first histogram's sums
     // The cut where the count reaches k, or (k = 0) the weights reach `target`.
     // `found`: its bucket is.
@@ -910,9 +962,9 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 if (tid == 0)
                     S.cut = Cut{};
                 __syncthreads();
-                find(k, target, false);
+                find(S, k, target, false);
             }
-            tell();
+            told();
         }
         const int bucket = cut.bucket;
         if (bucket < 0)
@@ -929,12 +981,13 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 S.key_lo = 0xffffffffu;
                 S.key_hi = 0;
             }
-            tell();
+            told();
             if (cut.in <= kList)
                 break;
             // too many: by the bits of their values
             counted = false;
             uint32_t a0 = 0xffffffffu, a1 = 0;
+#pragma unroll 1
             for (int j = 0; j < J; ++j) {
                 float v[VE];
                 unpack(run[j * 32 + lane], v);
@@ -957,20 +1010,20 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 S.cut.lo = S.key_lo;
                 S.cut.hi = S.key_hi;
             }
-            tell();
+            told();
             lo = cut.lo;
             hi = cut.hi;
             if (lo == hi) {  // one value alone
                 if (rank == 0 && tid == 0) {
                     const float v = value_of(lo);
-                    const uint64_t w = weights ? weight_of(v) : 0;
+                    const uint64_t w = weights ? weight_of(S, v) : 0;
                     const int m = k ? static_cast<int>(k - cut.above)
                                     : static_cast<int>((target - cut.mass + w - 1) / w);
                     S.cut.tau = v;
                     S.cut.m = m;
                     S.cut.mass = cut.mass + w * m;
                 }
-                tell();
+                told();
                 return;
             }
             int sh = 0;
@@ -980,17 +1033,17 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 return inside(v) ? static_cast<int>((key_of(v) - lo) >> sh) : -1;
             });
             if (rank == 0)
-                find(k, target, true);
-            tell();
+                find(S, k, target, true);
+            told();
             const uint32_t from = lo + (static_cast<uint32_t>(cut.bucket) << sh);
             hi = min(hi, from + ((1u << sh) - 1));
             lo = from;
         }
         if (rank == 0) {
             sort_falling(S.list, static_cast<int>(cut.in));
-            cut_list(static_cast<int>(cut.in), k, target, weights);
+            cut_list(S, static_cast<int>(cut.in), k, target, weights);
         }
-        tell();
+        told();
     };
     const bool few = top_k > 0 && top_k <= kList / 2 && top_k * 2 <= ctas * kSpThreads;
     bool listed = false;  // CTA 0's list holds all that may be kept
@@ -999,17 +1052,18 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         // bucket or above it
         if (my_top > -INFINITY)
             atomicAdd(&S.count[bucket_of(my_top)], 1u);
-        gather_sums(true, false);
+        gather_sums(S, ctas, rank, true, false);
         if (rank == 0) {
             if (tid == 0)
                 S.cut = Cut{};
             __syncthreads();
-            find(static_cast<uint32_t>(top_k), 0, false);
+            find(S, static_cast<uint32_t>(top_k), 0, false);
         }
-        tell();
+        told();
         const float end = end_of(cut.bucket < 0 ? kBuckets - 1 : cut.bucket);
-        finish(static_cast<int>(gather([&](float v) { return in_buckets(v, 0.f, end); })), 0);
-        tell();
+        finish(S, rank,
+               static_cast<int>(gather([&](float v) { return in_buckets(v, 0.f, end); })), 0, token);
+        told();
         listed = cut.done != 0;
         if (listed && a.tokens)
             return;
@@ -1041,6 +1095,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             const float low = 17592186044416.f * 0.5f * (1.f - fmaxf(top_p, 0.f)) /
                               static_cast<float>(a.vocab);
             const uint64_t least = max(static_cast<uint64_t>(low), uint64_t(1));
+#pragma unroll 1
             for (int j = 0; j < J; ++j)
                 each_weight(j, [&](float v, uint64_t w) {
                     s += w;
@@ -1048,7 +1103,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                         add_weight(bucket_of(v), w);
                 });
             sum = cluster_total(s);
-            gather_sums(false, true);
+            gather_sums(S, ctas, rank, false, true);
             counted = true;
         }
         const uint64_t target = top_p > 0.f ? max(target_of(top_p, sum), uint64_t(1)) : 1;
@@ -1058,14 +1113,15 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 if (tid == 0)
                     S.cut = Cut{};
                 __syncthreads();
-                find(0, target, false);
+                find(S, 0, target, false);
             }
-            tell();
+            told();
             const float end = end_of(cut.bucket);
             if (cut.in < kList * 9 / 10) {  // (a bucket's weights are within 9 %)
-                finish(static_cast<int>(gather([&](float v) { return in_buckets(v, 0.f, end); })),
-                       sum);
-                tell();
+                finish(S, rank,
+                       static_cast<int>(gather([&](float v) { return in_buckets(v, 0.f, end); })),
+                       sum, token);
+                told();
                 listed = cut.done != 0;
                 if (listed && a.tokens)
                     return;
@@ -1082,6 +1138,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     int ties_before = 0;  // entries equal to tau before this warp's run
     if (partial) {
         uint32_t n = 0;
+#pragma unroll 1
         for (int j = 0; j < J; ++j) {
             float v[VE];
             unpack(run[j * 32 + lane], v);
@@ -1142,6 +1199,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         uint64_t s = 0;
         int t = ties_before;
         if (!cuts && !(min_p > 0.f))
+#pragma unroll 1
             for (int j = 0; j < J; ++j)
                 each_weight(j, [&](float, uint64_t w) { s += w; });
         else {
@@ -1161,6 +1219,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
                 __syncwarp();
                 n -= 64;
             };
+#pragma unroll 1
             for (int j = 0; j < J; ++j) {
                 float v[VE];
                 const unsigned mask = step(j, t, v);
@@ -1180,7 +1239,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         }
         all_ctas();  // (S.runs may still be read)
         const uint64_t total = cluster_total(s);
-        const uint64_t level = u >= 1.f ? total - 1 : u > 0.f ? part_of(u, total) : 0;
+        const uint64_t level = level_of(u, total);
         // the run that the level falls into: four runs a lane
         constexpr int RL = kSpCtas * kSpWarps / 32;
         const int runs = ctas * kSpWarps;
@@ -1205,6 +1264,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
             return;
         at = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
         t = ties_before;
+#pragma unroll 1
         for (int j = 0; j < J; ++j) {
             int t0 = t;
             const uint64_t w = step_sum(j, t);
@@ -1222,7 +1282,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
 #pragma unroll
                 for (int k = 0; k < VE; ++k)
                     if (tok < 0 && (mask >> k & 1)) {
-                        sum += weight_of(v[k]);
+                        sum += weight_of(S, v[k]);
                         if (sum > level)
                             tok = (g0 + j * 32 + lane) * VE + k - mis;
                     }
@@ -1246,6 +1306,7 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         // (the weights of a cut by sums are known, but for what min_p takes off)
         float s = 0.f;
         int t = ties_before;
+#pragma unroll 1
         for (int j = 0; j < J; ++j) {
             float v[VE], p[VE];
             unpack(run[j * 32 + lane], v);
