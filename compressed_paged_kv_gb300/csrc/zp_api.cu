@@ -635,7 +635,7 @@ zp_status zp_paged_decode_attn(zp_cache *c, int32_t layer, const void *q,
     const long long pairs = static_cast<long long>(R) * c->Hkv;
     if (c->fp8) {
         zp::Fp8AttnArgs a{};
-        a.splits = zp::fp8_decode_splits(pairs, bt_stride, c->num_sms, &a.bps, &a.groups);
+        a.splits = zp::fp8_decode_splits(pairs, bt_stride, c->num_sms, &a.groups);
         a.kmap = c->ws.kmaps + layer;
         a.vmap = c->ws.vmaps + layer;
         a.kscale = c->kscales[layer];
@@ -1092,11 +1092,44 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     a.kscale = c->kscales[layer];
     a.vscale = c->vscales[layer];
     a.duos = static_cast<int64_t>(R) * c->Hkv >= 2ll * c->num_sms;
+    const long long G = c->Hq / c->Hkv;
+    const int few = zp::fp8_few_rows(total * G, R, c->Hkv, bt_stride, c->num_sms);
+    if (few > 0) {
+        zp::Fp8AttnArgs f{};
+        f.splits = zp::fp8_decode_splits(static_cast<long long>(R) * c->Hkv, bt_stride,
+                                         c->num_sms, &f.groups);
+        f.splits /= f.groups;
+        f.groups = 1;
+        f.kmap = a.kmap;
+        f.vmap = a.vmap;
+        f.kscale = a.kscale;
+        f.vscale = a.vscale;
+        f.q = a.q;
+        f.q_stride = q_stride;
+        f.starts = starts;
+        f.total = total;
+        f.tables = block_tables;
+        f.stride = bt_stride;
+        f.num_rows = num_rows;
+        f.lengths = lengths;
+        f.req_idx = req_idx;
+        f.R = R;
+        f.Hkv = c->Hkv;
+        f.Hq = c->Hq;
+        f.num_blocks = c->num_blocks;
+        f.logit_scale = a.logit_scale;
+        f.out = a.out;
+        f.sticky = c->ws.sticky;
+        if (zp::launch_fp8_few_rows(f, few, c->d, s) != cudaSuccess)
+            return ZP_ERR_CUDA;
+        if (total * G <= few)
+            return ZP_OK;
+        a.few = static_cast<int32_t>(few / G);
+    }
     // Requests with many query rows over widened blocks, the others over the cache, if the
     // batch has many rows a request: two kernels one after the other cost a mixed batch more
     // than the widened blocks gain (60 single tokens beside two pieces of 900, 64 dims: 138 us
     // that way, 118 in one kernel; 19 chunks of 64 over 8,192, none of them long: 173, 153).
-    const long long G = c->Hq / c->Hkv;
     if (total * G >= static_cast<long long>(R) * zp::kWideMeanRows) {
         zp::Fp8WidenArgs w{};
         w.kpool = static_cast<const uint8_t *>(c->kpools[layer]);

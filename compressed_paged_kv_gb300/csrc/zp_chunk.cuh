@@ -51,6 +51,7 @@ struct ChunkAttnArgs {
     // pools and maps are theirs, else the one over the cache.
     const int32_t *places;
     int32_t widened;
+    int32_t few;   // an 8-bit cache's chunks of so many tokens are another kernel's
     int32_t duos;  // an 8-bit cache's short chunks: kv heads by two (zp_chunk_attn.cuh)
 };
 

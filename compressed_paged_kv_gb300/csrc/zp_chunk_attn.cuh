@@ -287,11 +287,11 @@ __host__ __device__ __forceinline__ void make_shares(CaPlan &pl, long long cost,
 
 // Request i, if it is this call's: of an 8-bit cache's batch the requests with a place
 // among the widened blocks are the call's over those, with the place for a table row, and
-// the others the call's over the cache.
+// the others the call's over the cache, but for those of few query rows.
 __host__ __device__ __forceinline__ bool attn_request(const ChunkAttnArgs &a, int i, ChunkReq &c,
                                                       bool *bad)
 {
-    if (!chunk_request(a, i, c, bad))
+    if (!chunk_request(a, i, c, bad) || c.n <= a.few)
         return false;
     if (!a.places)
         return true;
@@ -689,13 +689,6 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16(uint32_t v)
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
     return r;
-}
-
-// The bytes of four e4m3 numbers that are NaN, as 0.
-__device__ __forceinline__ uint32_t numbers4(uint32_t v)
-{
-    const uint32_t nan = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // 0x80 a NaN
-    return v & ~(nan | (nan - (nan >> 7)));
 }
 
 // The workspace slot of a partial result: O [256][D], then (max, sum) [256].

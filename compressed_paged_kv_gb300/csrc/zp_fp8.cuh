@@ -1,6 +1,6 @@
 // zp_fp8.cuh -- launch arguments and shared device code of the calls on an 8-bit
-// cache: rows rounded into it (zp_fp8_append.cu) and the attention of single
-// tokens over it (zp_fp8_decode.cu).  Internal: not part of the C ABI.
+// cache: rows rounded into it (zp_fp8_append.cu) and the attention of few query
+// rows over it (zp_fp8_decode.cu).  Internal: not part of the C ABI.
 //
 // A pool [num_blocks][Hkv][16][d] holds e4m3 numbers, and a scale [num_blocks][Hkv]
 // goes with each of its slabs: value = scale * number.  Scales are powers of two
@@ -36,13 +36,15 @@ struct Fp8AttnArgs {
     const CUtensorMap *kmap, *vmap;
     const float *kscale, *vscale;
     const __nv_bfloat16 *q;
-    int64_t q_stride;  // elements from a request's row of q to the next
+    int64_t q_stride;  // elements from a token's row of q to the next
+    const int32_t *starts;  // of a chunk
+    int32_t total;
     const int32_t *tables;
     int32_t stride, num_rows;
     const int32_t *lengths;
     const int32_t *req_idx;
     int32_t R, Hkv, Hq, num_blocks;
-    int32_t splits, bps;  // splits per (request, kv head), blocks per split
+    int32_t splits;       // per (request, kv head)
     int32_t groups;       // clusters they are
     float logit_scale;    // scale * log2(e)
     __nv_bfloat16 *out;
@@ -78,10 +80,14 @@ int fp8_wide_blocks(int num_blocks, int hkv, int d);
 
 cudaError_t launch_fp8_widen(const Fp8WidenArgs &a, int sms, cudaStream_t s);
 cudaError_t launch_fp8_append(const Fp8KvArgs &a, cudaStream_t s);
-// Splits per (request, kv head) of a decode over `pairs` of them; *bps: blocks per split,
-// *groups (at most 16): clusters that the splits are.
-int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *bps, int *groups);
+// Splits per (request, kv head) of a decode over `pairs` of them; *groups (at most 16):
+// clusters that the splits are.
+int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *groups);
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s);
+// A chunk's requests with up to `rows` query rows (tokens times heads of a group; 8, 16 or 24),
+// groups 1; and the `rows` for a batch of so many, 0 if its requests are launch_fp8_chunk_attn's.
+int fp8_few_rows(long long rows, int R, int hkv, int bt_stride, int num_sms);
+cudaError_t launch_fp8_few_rows(const Fp8AttnArgs &a, int rows, int d, cudaStream_t s);
 cudaError_t launch_fp8_chunk_attn(const ChunkAttnArgs &a, int d, int sms, cudaStream_t s);
 // Once a device, before launch_fp8_chunk_attn.
 cudaError_t prepare_fp8_chunk_attn(int d);
@@ -137,6 +143,19 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 numbers with 0 in place of NaN.
+__device__ __forceinline__ uint32_t numbers4(uint32_t v)
+{
+    const uint32_t nan = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // 0x80 a NaN
+    return v & ~(nan | (nan - (nan >> 7)));
+}
+
+// 1 in place of NaN and 0 of the others.
+__device__ __forceinline__ uint32_t ones4(uint32_t v)
+{
+    return (((v & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0x38u;
 }
 
 // Byte offset of 16-byte chunk `ch` of row `row` in a slab of rows of D bytes as the

@@ -1,5 +1,6 @@
-// zp_fp8_decode.cu -- attention of single tokens over an 8-bit paged cache:
-// zp_paged_decode_attn of such a cache.
+// zp_fp8_decode.cu -- attention of few query rows over an 8-bit paged cache:
+// zp_paged_decode_attn of such a cache, and the requests of zp_paged_chunk_attn whose
+// chunk has up to 24 rows (tokens times heads of a group).
 //
 // A key is ks * k8 and a value vs * v8, with one ks and one vs for the 16 tokens of
 // a block: neither is multiplied out.  With t = scale (q . k8) ks + log2 vs and
@@ -16,24 +17,28 @@
 // 2^-28 of that); p is taken against 2^14 over the maximum, and rounded to 11 bits down
 // to 2^-28 of the largest, where bf16 would round to 8.
 //
-// The keys are the products' rows and the heads of the group their columns, eight of
-// them (or twice eight): S^T = K Q^T, O^T = V^T P^T.  With the heads as rows, of which 16
-// would be computed for a group of four, the kernel took twice the products and twice
-// the registers.  Fragments come by ldmatrix: a matrix of 8 keys x 16 bytes gives a lane
-// four neighbouring dims of a key, so q's fragments are laid out to match; for V, the
-// transposed matrix gives a lane two dims of two keys, which a byte permutation turns
-// into the pairs of keys that the product takes, the even dims as its rows 0-7 and the odd
-// ones as 8-15.  P turns from rows of keys to rows of heads by movmatrix.
+// The keys are the products' rows and q's rows of the kv head their columns, in eights (NT):
+// S^T = K Q^T, O^T = V^T P^T.  With the heads as rows, of which 16 would be computed for a
+// group of four, the kernel took twice the products and twice the registers.  Fragments come
+// by ldmatrix: a matrix of 8 keys x 16 bytes gives a lane four neighbouring dims of a key, so
+// q's fragments are laid out to match; for V, the transposed matrix gives a lane two dims of
+// two keys, which a byte permutation turns into the pairs of keys that the product takes, the
+// even dims as its rows 0-7 and the odd ones as 8-15.  P turns from rows of keys to rows of
+// heads by movmatrix.
 //
-// Grid (request and split, kv head), four warps a CTA.  A CTA owns a contiguous range of `bps`
-// blocks; a warp takes every fourth pair of them through its own ring of pairs (one TMA box
-// a slab).  Warps join in shared memory, and up to eight splits, a cluster, too; more clusters
-// of a long row leave partial results to a second kernel.
+// Grid (request and split, kv head), four warps a CTA.  A CTA owns a contiguous range of
+// blocks, the row's over its splits but no fewer than eight; a warp takes every fourth pair of
+// them through its own ring of pairs (one TMA box a slab).  Warps join in shared memory, and up
+// to eight splits, a cluster, too; more clusters of a long row leave partial results to a
+// second kernel.
 //
 // Measured, 32 heads of 128 over 8 kv heads: 256 requests of 1,024 to 2,039 tokens, 0.81 GB in
 // 133 us = 6.1 TB/s, 0.90 of the copy peak (with 16 rows of heads and two CTAs an SM 166 us);
-// one of 2,000 tokens 6.1 us, the chain row -> block ids -> slabs -> joins; bound by HBM where
-// the rows fill the GPU.
+// one of 2,000 tokens 6.3 us, the chain row -> block ids -> slabs -> joins; bound by HBM where
+// the rows fill the GPU.  256 chunks of 1, 4 and 6 tokens over 1,536, 0.81 GB: 146, 178 and
+// 258 us (in the kernel for tiles of 128 rows 285, 289 and 290); with more columns a warp waits
+// for its own products, three and two CTAs an SM being all that registers and rings leave
+// (schedulers issue in 45 % of the cycles).  Four eights took 300 us.
 #include <algorithm>
 
 #include "zp_fp8.cuh"
@@ -46,6 +51,7 @@ constexpr int kD8Warps = 4;
 constexpr int kD8Threads = kD8Warps * 32;
 constexpr float kTop = 14.f;   // log2 of the largest p
 constexpr int kD8Cluster = 8;  // splits that a cluster joins
+constexpr int kD8Blocks = 8;   // of a split, at least
 constexpr int kD8Groups = 16;  // clusters a (request, kv head), at most
 
 template <int D, int NT>
@@ -56,9 +62,13 @@ struct D8Smem {
     static constexpr int RING = kD8Warps * STAGES * STAGE;
     static constexpr int ROW = D + 2;       // o, then (maximum, sum), of a head
     static constexpr int MERGE = kD8Warps * 8 * NT * ROW * 4;  // reuses the ring
-    static constexpr int off_bar = RING > MERGE ? RING : MERGE;
-    static constexpr int off_part = off_bar + kD8Warps * STAGES * 8;  // the CTA's own, for the cluster
-    static constexpr int BYTES = off_part + 8 * NT * ROW * 4;
+    static constexpr int off_part = MERGE;  // the CTA's own, for the cluster
+    static constexpr int JOIN = MERGE + 8 * NT * ROW * 4;
+    static constexpr int off_bar = RING > JOIN ? RING : JOIN;
+    static constexpr int off_q = off_bar + kD8Warps * STAGES * 8;  // q's fragments, if there
+    static constexpr bool QS = NT > 2;
+    static constexpr int off_f = off_q + (QS ? NT * (D / 16) * 32 * 8 : 0);
+    static constexpr int BYTES = off_f + (QS ? 8 * NT * 4 : 0);
     static constexpr int ALLOC = BYTES + 1024;
 };
 
@@ -72,14 +82,14 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v)
 
 }  // namespace
 
-// NT: eights of heads.
-template <int D, int NT>
-__global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
+// NT: eights of columns of a warp.
+template <int D, int NT, bool CHUNK>
+__global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D == 128 ? 3 : 4)
     zp_fp8_decode_kernel(const __grid_constant__ Fp8AttnArgs a)
 {
     pdl_wait();
     using S = D8Smem<D, NT>;
-    constexpr int KS = D / 16, ROW = S::ROW, HEADS = 8 * NT;
+    constexpr int KS = D / 16, ROW = S::ROW, COLS = 8 * NT;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + (1024 - (smem_u32(smem_raw) & 1023) & 1023);
@@ -89,18 +99,31 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
     const int tid = threadIdx.x, lane = tid & 31, wi = tid >> 5;
     const int split = blockIdx.x % a.splits, r = blockIdx.x / a.splits, h = blockIdx.y;
     const int G = a.Hq / a.Hkv;
-    int row = a.req_idx ? a.req_idx[r] : r;
-    const bool row_ok = row >= 0 && row < a.num_rows;
-    int len = row_ok ? a.lengths[row] : 0;
-    if (!row_ok || len < 0 || len > a.stride * kBlk) {
-        if (tid == 0 && split == 0 && h == 0)
-            set_error(a.sticky, row_ok ? ZP_ERR_DEVICE_CHECK : ZP_ERR_INVALID_ARG);
-        len = 0;
-        row = 0;
+    ChunkReq rq{r, 1, 0, 0};
+    if constexpr (CHUNK) {
+        bool bad;
+        const bool work = chunk_request(a, r, rq, &bad);
+        if (bad && tid == 0 && split == 0 && h == 0)
+            set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
+        if (!work || rq.n > COLS / G)  // (the whole cluster alike)
+            return;
+    } else {
+        rq.row = a.req_idx ? a.req_idx[r] : r;
+        const bool row_ok = rq.row >= 0 && rq.row < a.num_rows;
+        rq.len = row_ok ? a.lengths[rq.row] : 0;
+        if (!row_ok || rq.len < 0 || rq.len > a.stride * kBlk) {
+            if (tid == 0 && split == 0 && h == 0)
+                set_error(a.sticky, row_ok ? ZP_ERR_DEVICE_CHECK : ZP_ERR_INVALID_ARG);
+            rq.len = 0;
+            rq.row = 0;
+        }
     }
+    // q's rows of the kv head, heads of a token side by side, are the columns
+    const int len = rq.len, rows = rq.n * G;
     const int nblk = (len + kBlk - 1) / kBlk;
-    const int b_begin = split * a.bps;
-    const int b_end = min(nblk, b_begin + a.bps);
+    const int bps = max(kD8Blocks, ((nblk + a.splits - 1) / a.splits + 1) & ~1);
+    const int b_begin = split * bps;
+    const int b_end = min(nblk, b_begin + bps);
 
     uint64_t *my_bar = bars + wi * S::STAGES;
     if (lane < S::STAGES)
@@ -112,7 +135,7 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
     const int pairs = b_end > b_begin ? (b_end - b_begin + 1) / 2 : 0;
     const int my_n = pairs > wi ? (pairs - wi + kD8Warps - 1) / kD8Warps : 0;
     uint8_t *my_stage = sm + wi * S::STAGES * S::STAGE;
-    const int32_t *trow = a.tables + static_cast<size_t>(row) * a.stride;
+    const int32_t *trow = a.tables + static_cast<size_t>(rq.row) * a.stride;
 
     // block ids and scales of 16 pairs, a block a lane, and of the 16 after them
     auto load_id = [&](int i) {
@@ -149,20 +172,18 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
         issue(i, id);
     float ks = scale_at(a.kscale, id), vs = scale_at(a.vscale, id), ks_next = 0.f, vs_next = 0.f;
 
-    // q's fragments: head 8 n + g, dims 16 c + 4 t .. + 3
+    // q's fragments: column 8 n + g, dims 16 c + 4 t .. + 3
     const int g = lane >> 2, t4 = lane & 3;
-    uint32_t qb[NT][KS][2];
-    float fr[NT][2];  // heads 8 n + 2 t, + 1: what a logit is multiplied by, but for ks
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int hd = n * 8 + g;
-        const __nv_bfloat16 *src = a.q + r * a.q_stride + (h * G + min(hd, G - 1)) * D + t4 * 4;
+    auto fragments = [&](int n, uint32_t (&f)[KS][2]) {
+        const int col = n * 8 + g, in = min(col, rows - 1), tok = CHUNK ? in / G : 0;
+        const __nv_bfloat16 *src =
+            a.q + (rq.first + tok) * a.q_stride + (h * G + in - tok * G) * D + t4 * 4;
         uint2 u[KS];
         uint32_t most = 0;  // the largest finite magnitude's bits
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
             u[c] = make_uint2(0u, 0u);
-            if (hd < G)
+            if (col < rows)
                 u[c] = *reinterpret_cast<const uint2 *>(src + c * 16);
             const uint32_t w[4] = {u[c].x << 16, u[c].x, u[c].y << 16, u[c].y};
 #pragma unroll
@@ -177,21 +198,57 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
         const int e = 14 - (static_cast<int>(most >> 23) - 127);
         const int e1 = max(min(e, 100), -100), e2 = e - e1;
         const float f1 = __uint_as_float(exp2_bits(e1)), f2 = __uint_as_float(exp2_bits(e2));
-        const float back =
-            a.logit_scale * __uint_as_float(exp2_bits(-e1)) * __uint_as_float(exp2_bits(-e2));
 #pragma unroll
         for (int c = 0; c < KS; ++c) {
-            qb[n][c][0] = pack_f16x2(__uint_as_float(u[c].x << 16) * f1 * f2,
-                                     __uint_as_float(u[c].x & 0xffff0000u) * f1 * f2);
-            qb[n][c][1] = pack_f16x2(__uint_as_float(u[c].y << 16) * f1 * f2,
-                                     __uint_as_float(u[c].y & 0xffff0000u) * f1 * f2);
+            f[c][0] = pack_f16x2(__uint_as_float(u[c].x << 16) * f1 * f2,
+                                 __uint_as_float(u[c].x & 0xffff0000u) * f1 * f2);
+            f[c][1] = pack_f16x2(__uint_as_float(u[c].y << 16) * f1 * f2,
+                                 __uint_as_float(u[c].y & 0xffff0000u) * f1 * f2);
         }
-        fr[n][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
-        fr[n][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+        return a.logit_scale * __uint_as_float(exp2_bits(-e1)) * __uint_as_float(exp2_bits(-e2));
+    };
+    // in registers, or (more than 16 columns) in shared memory
+    uint32_t qb[S::QS ? 1 : NT][KS][2];
+    float fr[NT][2];  // columns 8 n + 2 t, + 1: what a logit is multiplied by, but for ks
+    uint2 *sQ = reinterpret_cast<uint2 *>(sm + S::off_q);
+    if constexpr (S::QS) {
+        float *sF = reinterpret_cast<float *>(sm + S::off_f);
+        if (wi < NT) {
+            const float back = fragments(wi, qb[0]);
+#pragma unroll
+            for (int c = 0; c < KS; ++c)
+                sQ[(wi * KS + c) * 32 + lane] = make_uint2(qb[0][c][0], qb[0][c][1]);
+            if (t4 == 0)
+                sF[wi * 8 + g] = back;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            fr[n][0] = sF[n * 8 + t4 * 2];
+            fr[n][1] = sF[n * 8 + t4 * 2 + 1];
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float back = fragments(n, qb[n]);
+            fr[n][0] = __shfl_sync(0xffffffffu, back, t4 * 8);
+            fr[n][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4);
+        }
     }
 
+    // a chunk's columns 8 n + 2 t, + 1: the keys they see
+    [[maybe_unused]] int lim[NT][2];
+    [[maybe_unused]] const int sees = len - rq.n + 1;  // keys that every column sees
+    if constexpr (CHUNK) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                lim[n][e] = sees + min(n * 8 + t4 * 2 + e, rows - 1) / G;
+    }
+    
     float m_run[NT][2], l_run[NT][2];
-    float o[NT][KS][4];  // dims 16 c + 2 g (+ 1 in [2], [3]), heads 8 n + 2 t, + 1
+    float o[NT][KS][4];  // dims 16 c + 2 g (+ 1 in [2], [3]), columns 8 n + 2 t, + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m_run[n][0] = m_run[n][1] = -1e30f;
@@ -231,28 +288,60 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
         }
         const uint32_t kb = smem_u32(kd), vb = smem_u32(vd);
 
-        // S^T: keys 16 blk + g (in [0], [1]) and + 8, heads 8 n + 2 t, + 1
+        // S^T: keys 16 blk + g (in [0], [1]) and + 8, columns 8 n + 2 t, + 1
         float sacc[2][NT][4];
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
+        for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 sacc[blk][n][0] = sacc[blk][n][1] = sacc[blk][n][2] = sacc[blk][n][3] = 0.f;
-            if (blk && !two)
-                break;
+        // chunks c and c + 1 of a block's keys; f: q's fragments for them
+        auto products = [&](int blk, int c, const uint32_t (&f)[NT][2][2]) {
+            // matrices: keys 0-7 and 8-15 of chunk c, then of c + 1
+            uint32_t kr[4];
+            ldsm_x4(kb + blk * S::SLAB + swz8<D>((mi & 1) * 8 + (lane & 7), c + (mi >> 1)), kr);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t a0 = f16x2_of_e4m3(kr[2 * x]), a1 = f16x2_of_e4m3(kr[2 * x + 1]);
+                const uint32_t a2 = f16x2_of_e4m3(kr[2 * x] >> 16);
+                const uint32_t a3 = f16x2_of_e4m3(kr[2 * x + 1] >> 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_f16(sacc[blk][n], a0, a1, a2, a3, f[n][x][0], f[n][x][1]);
+            }
+        };
+        if constexpr (S::QS) {
 #pragma unroll
             for (int c = 0; c < KS; c += 2) {
-                // matrices: keys 0-7 and 8-15 of chunk c, then of c + 1
-                uint32_t kr[4];
-                ldsm_x4(kb + blk * S::SLAB + swz8<D>((mi & 1) * 8 + (lane & 7), c + (mi >> 1)), kr);
+                uint32_t f[NT][2][2];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t a0 = f16x2_of_e4m3(kr[2 * x]), a1 = f16x2_of_e4m3(kr[2 * x + 1]);
-                    const uint32_t a2 = f16x2_of_e4m3(kr[2 * x] >> 16);
-                    const uint32_t a3 = f16x2_of_e4m3(kr[2 * x + 1] >> 16);
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint2 v = sQ[(n * KS + c + x) * 32 + lane];
+                        f[n][x][0] = v.x;
+                        f[n][x][1] = v.y;
+                    }
+                products(0, c, f);
+                if (two)
+                    products(1, c, f);
+            }
+        } else {
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+                if (blk && !two)
+                    break;
+#pragma unroll
+                for (int c = 0; c < KS; c += 2) {
+                    uint32_t f[NT][2][2];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma_f16(sacc[blk][n], a0, a1, a2, a3, qb[n][c + x][0], qb[n][c + x][1]);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            f[n][x][0] = qb[n][c + x][0];
+                            f[n][x][1] = qb[n][c + x][1];
+                        }
+                    products(blk, c, f);
                 }
             }
         }
@@ -264,13 +353,17 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
             const float lv = log2f(vx);
             iv[blk] = blk && !two ? 0.f : 1.f / vx;
             const int key = blk * kBlk + g;
-            const bool in0 = tok0 + key < len && (two || !blk), in1 = tok0 + key + 8 < len && (two || !blk);
+            const bool there = two || !blk;
+            const bool in0 = tok0 + key < len && there, in1 = tok0 + key + 8 < len && there;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float v = fmaf(sacc[blk][n][e], fr[n][e & 1] * kx, lv);
-                    sacc[blk][n][e] = (e < 2 ? in0 : in1) ? v : -INFINITY;
+                    bool in = e < 2 ? in0 : in1;
+                    if constexpr (CHUNK)
+                        in = tok0 + key + (e < 2 ? 0 : 8) < lim[n][e & 1] && there;
+                    sacc[blk][n][e] = in ? v : -INFINITY;
                 }
         }
         uint32_t pb[2][NT][2];
@@ -314,6 +407,60 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
                 pb[blk][n][1] = transposed(pack_f16x2(sacc[blk][n][2], sacc[blk][n][3]));
             }
         }
+        // A value that is NaN: 0 times it is NaN, for the columns too that do not see its key.
+        // Among the keys that some do not see, NaN counts as 0 and is added to the columns that
+        // do see it: those for which a product of ones, at the NaNs and at the keys seen, is
+        // above 0.
+        [[maybe_unused]] bool nan_v = false;
+        if constexpr (CHUNK) {
+            const int last = (two ? 2 : 1) * kBlk;
+            if (rq.n > 1 && tok0 + last > sees) {
+                for (int x = lane; x < last * (D / 16); x += 32) {
+                    const uint4 v = ld_shared_v4(vb + x * 16);
+                    nan_v |= numbers4(v.x) != v.x || numbers4(v.y) != v.y ||
+                             numbers4(v.z) != v.z || numbers4(v.w) != v.w;
+                }
+                nan_v = __any_sync(0xffffffffu, nan_v);
+            }
+            if (nan_v) {
+#pragma unroll 1
+                for (int n = 0; n < NT; ++n)
+#pragma unroll 1
+                    for (int c = 0; c < KS; ++c) {
+                        float at[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int blk = 0; blk < (two ? 2 : 1); ++blk) {
+                            const int key = tok0 + blk * kBlk + g;
+                            int l0 = 0, l1 = 0;
+#pragma unroll
+                            for (int k = 0; k < NT; ++k)
+                                if (k == n) {
+                                    l0 = lim[k][0];
+                                    l1 = lim[k][1];
+                                }
+                            const uint32_t p0 = transposed(pack_f16x2(key < l0, key < l1));
+                            const uint32_t p1 = transposed(pack_f16x2(key + 8 < l0, key + 8 < l1));
+                            uint32_t vr[4];
+                            ldsm_x4_t(vb + blk * S::SLAB +
+                                          swz8<D>((mi & 1) * 8 + (lane & 7), (c & ~1) + (mi >> 1)),
+                                      vr);
+                            const uint32_t v0 = c & 1 ? vr[2] : vr[0], v1 = c & 1 ? vr[3] : vr[1];
+                            const uint32_t lo = __byte_perm(ones4(v0), 0, 0x3120);
+                            const uint32_t hi = __byte_perm(ones4(v1), 0, 0x3120);
+                            mma_f16(at, f16x2_of_e4m3(lo), f16x2_of_e4m3(lo >> 16),
+                                    f16x2_of_e4m3(hi), f16x2_of_e4m3(hi >> 16), p0, p1);
+                        }
+#pragma unroll
+                        for (int k = 0; k < NT; ++k)
+#pragma unroll
+                            for (int q = 0; q < KS; ++q)
+                                if (k == n && q == c)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (at[e] > 0.f)
+                                            o[k][q][e] = INFINITY - INFINITY;
+                    }
+            }
+        }
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
             if (blk && !two)
@@ -324,6 +471,10 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
                 uint32_t vr[4];
                 ldsm_x4_t(vb + blk * S::SLAB + swz8<D>((mi & 1) * 8 + (lane & 7), c + (mi >> 1)),
                           vr);
+                if (CHUNK && nan_v)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        vr[k] = numbers4(vr[k]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     // bytes: key 2 t (dims 2 g, 2 g + 1), key 2 t + 1 (the same)
@@ -362,12 +513,12 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
         }
     __syncthreads();  // every stage consumed: reuse the area for the merge
 
-    float *mrg = reinterpret_cast<float *>(sm);  // [warp][HEADS][ROW]
+    float *mrg = reinterpret_cast<float *>(sm);  // [warp][COLS][ROW]
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float *mine = mrg + (wi * HEADS + n * 8 + t4 * 2 + e) * ROW;
+            float *mine = mrg + (wi * COLS + n * 8 + t4 * 2 + e) * ROW;
             if (g == 0) {
                 mine[D] = m_run[n][e];
                 mine[D + 1] = l_run[n][e];
@@ -380,7 +531,11 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
     __syncthreads();
     // the four warps', then the cluster's; two dims a thread
     const int cs = a.splits / a.groups, rank = split % cs;  // a cluster's CTAs
-    const size_t hq0 = static_cast<size_t>(r) * a.Hq + h * G;
+    // the output's row of (token, head) of a column
+    auto row_of = [&](int col) {
+        const int tok = CHUNK ? col / G : 0;
+        return static_cast<size_t>(rq.first + tok) * a.Hq + h * G + col - tok * G;
+    };
     auto join = [&](int hd, int c, const float *src, int step, int count, float &M, float &L,
                     float2 &O) {
         M = -1e30f;
@@ -399,15 +554,15 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
     };
     auto write = [&](int hd, int c, float L, float2 O) {
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        __nv_bfloat16 *to = a.out + (hq0 + hd) * D + c;  // (2-byte aligned)
+        __nv_bfloat16 *to = a.out + row_of(hd) * D + c;  // (2-byte aligned)
         to[0] = __float2bfloat16_rn(O.x * inv);
         to[1] = __float2bfloat16_rn(O.y * inv);
     };
-    for (int x = tid; x < G * (D / 2); x += kD8Threads) {
+    for (int x = tid; x < rows * (D / 2); x += kD8Threads) {
         const int hd = x / (D / 2), c = x % (D / 2) * 2;
         float M, L;
         float2 O;
-        join(hd, c, mrg, HEADS * ROW, kD8Warps, M, L, O);
+        join(hd, c, mrg, COLS * ROW, kD8Warps, M, L, O);
         if (a.splits == 1) {
             write(hd, c, L, O);
             continue;
@@ -421,7 +576,7 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
         return;
     cluster_sync();
     // each CTA joins its part of the dims
-    for (int x = rank * kD8Threads + tid; x < G * (D / 2); x += cs * kD8Threads) {
+    for (int x = rank * kD8Threads + tid; x < rows * (D / 2); x += cs * kD8Threads) {
         const int hd = x / (D / 2), c = x % (D / 2) * 2;
         float2 ml[kD8Cluster], v[kD8Cluster];
 #pragma unroll
@@ -449,7 +604,7 @@ __global__ void __launch_bounds__(kD8Threads, D == 128 ? 3 : 4)
             write(hd, c, L, O);
             continue;
         }
-        float *p = a.part + ((hq0 + hd) * a.groups + split / cs) * ROW;
+        float *p = a.part + (row_of(hd) * a.groups + split / cs) * ROW;
         *reinterpret_cast<float2 *>(p + c) = O;
         if (c == 0)
             *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
@@ -476,11 +631,11 @@ __global__ void __launch_bounds__(D) zp_fp8_combine_kernel(const Fp8AttnArgs a)
     a.out[static_cast<size_t>(rh) * D + c] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool CHUNK>
 static cudaError_t launch_fp8_decode_t(const Fp8AttnArgs &a, cudaStream_t s)
 {
     using Sm = D8Smem<D, NT>;
-    cudaError_t err = cudaFuncSetAttribute(zp_fp8_decode_kernel<D, NT>,
+    cudaError_t err = cudaFuncSetAttribute(zp_fp8_decode_kernel<D, NT, CHUNK>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, Sm::ALLOC);
     if (err != cudaSuccess)
         return err;
@@ -499,7 +654,7 @@ static cudaError_t launch_fp8_decode_t(const Fp8AttnArgs &a, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = a.splits > 1 ? 2 : 1;
-    err = cudaLaunchKernelEx(&cfg, zp_fp8_decode_kernel<D, NT>, a);
+    err = cudaLaunchKernelEx(&cfg, zp_fp8_decode_kernel<D, NT, CHUNK>, a);
     if (err != cudaSuccess || a.groups == 1)
         return err;
     cfg.gridDim = dim3(static_cast<unsigned>(a.R * a.Hq), 1, 1);
@@ -512,30 +667,57 @@ static cudaError_t launch_fp8_decode_t(const Fp8AttnArgs &a, cudaStream_t s)
 // Two CTAs an SM, of at least 8 blocks each; more than a cluster of them where each then has
 // 16 blocks, which pays for the second launch (one row of 30,000 tokens 17 us, with 16
 // splits 24).
-int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *bps, int *groups)
+int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *groups)
 {
     const long long want = (2 * num_sms + pairs - 1) / pairs;
     int splits = static_cast<int>(std::min<long long>({want, kD8Cluster, bt_stride / 8}));
     splits = std::max(1, splits);
     *groups = static_cast<int>(std::min<long long>(
         {want / kD8Cluster, kD8Groups, bt_stride / (16 * kD8Cluster)}));
-    if (*groups > 1) {
+    if (*groups > 1)
         splits = kD8Cluster * *groups;
-    } else {
+    else
         *groups = 1;
-    }
-    *bps = (bt_stride + splits - 1) / splits;
     return splits;
+}
+
+// Rows up to which a batch's chunks are this file's, none (0) if it is not for it: the mean
+// rounded up, to 16, or to 24 of a mean up to 20, as the requests above it cost a second kernel
+// (256 chunks of 2 to 9 tokens, four heads a group: 314 us that way, 298 without).  Too few
+// units (request, kv head) for the splits to fill the GPU want short rows (one request of four
+// tokens, 8 kv heads: 2,000 keys 9.6 us, 8,192 20 and 30,000 56; the other kernel 20.6, 24.9 and
+// 38).
+int fp8_few_rows(long long rows, int R, int hkv, int bt_stride, int num_sms)
+{
+    const long long mean = (rows + R - 1) / R;
+    const int few = static_cast<int>((std::min<long long>(mean, 24) + 7) / 8 * 8);
+    const bool filled = static_cast<long long>(R) * hkv * kD8Cluster >= 2 * num_sms;
+    if (mean > 20 || (!filled && static_cast<long long>(few) * bt_stride > 8192))
+        return 0;
+    return few;
 }
 
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s)
 {
     const bool wide = a.Hq / a.Hkv > 8;
     if (d == 64)
-        return wide ? launch_fp8_decode_t<64, 2>(a, s) : launch_fp8_decode_t<64, 1>(a, s);
+        return wide ? launch_fp8_decode_t<64, 2, false>(a, s) : launch_fp8_decode_t<64, 1, false>(a, s);
     if (d == 128)
-        return wide ? launch_fp8_decode_t<128, 2>(a, s) : launch_fp8_decode_t<128, 1>(a, s);
+        return wide ? launch_fp8_decode_t<128, 2, false>(a, s) : launch_fp8_decode_t<128, 1, false>(a, s);
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_fp8_few_rows(const Fp8AttnArgs &a, int rows, int d, cudaStream_t s)
+{
+    switch (rows | d) {
+    case 8 | 64: return launch_fp8_decode_t<64, 1, true>(a, s);
+    case 16 | 64: return launch_fp8_decode_t<64, 2, true>(a, s);
+    case 24 | 64: return launch_fp8_decode_t<64, 3, true>(a, s);
+    case 8 | 128: return launch_fp8_decode_t<128, 1, true>(a, s);
+    case 16 | 128: return launch_fp8_decode_t<128, 2, true>(a, s);
+    case 24 | 128: return launch_fp8_decode_t<128, 3, true>(a, s);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace zp
