@@ -771,21 +771,23 @@ __device__ __forceinline__ void split_q(uint32_t from, uint32_t to, int ct, int 
         const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            most = max(most, max((w[e] << 16) & 0x7fff0000u, w[e] & 0x7fff0000u));
+            most = __vmaxu2(most, w[e] & 0x7fff7fffu);
     }
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = max(most << 16, most & 0xffff0000u);
     __syncwarp();  // the row is read
     // f = 2^e; two factors, as it may not be an fp32 number
     const int e = 8 - (static_cast<int>(most >> 23) - 127) - ((most & 0x7fffffu) > 0x600000u);
     const int e1 = max(min(e, 100), -100), e2 = e - e1;
     const float f1 = __uint_as_float(exp2_bits(e1) | (__float_as_uint(logit_scale) & 0x80000000u));
     const float f2 = __uint_as_float(exp2_bits(e2));
-#pragma unroll
+    // a loop, as the code runs once an item and comes from memory (256 chunks of 2 to 9: in line 304 us, so 299)
+#pragma unroll 1
     for (int c = 0; c < CH; c += 2) {
         uint32_t up[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint32_t w[4] = {v[c + k].x, v[c + k].y, v[c + k].z, v[c + k].w};
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
             uint32_t u8[4], l8[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -805,6 +807,9 @@ __device__ __forceinline__ void split_q(uint32_t from, uint32_t to, int ct, int 
         const uint32_t at = to + swz8<D>(r, (hf * CH + (c ^ flip)) / 2);
         st_shared_v4(at, make_uint4(up[0], up[1], up[2], up[3]));
         st_shared_v4(at + LO, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+        for (int k = 0; k + 2 < CH; ++k)
+            v[k] = v[k + 2];
     }
     const float back = fabsf(logit_scale) * __uint_as_float(exp2_bits(-e1)) *
                        __uint_as_float(exp2_bits(-e2));
