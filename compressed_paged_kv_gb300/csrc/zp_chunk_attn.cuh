@@ -781,7 +781,8 @@ __device__ __forceinline__ void split_q(uint32_t from, uint32_t to, int ct, int 
     const int e1 = max(min(e, 100), -100), e2 = e - e1;
     const float f1 = __uint_as_float(exp2_bits(e1) | (__float_as_uint(logit_scale) & 0x80000000u));
     const float f2 = __uint_as_float(exp2_bits(e2));
-    // a loop, as the code runs once an item and comes from memory (256 chunks of 2 to 9: in line 304 us, so 299)
+    // a loop, as the code runs once an item and comes from memory (256 chunks of 2 to 9: in line
+    // 304 us, so 299)
 #pragma unroll 1
     for (int c = 0; c < CH; c += 2) {
         uint32_t up[4], lo[4];
