@@ -51,7 +51,7 @@ def run(cache, logits, u, t=None, k=None, p=None, m=None, idx=None, prob=torch.f
 
 def check(cache, logits, u, t=None, k=None, p=None, m=None, idx=None, prob=torch.float32):
     """Against 64 bits.  A token may differ only where u lies within 2^-38 of a border
-    (weights are off by 2^-41 at most, and their sums by V times that at worst); a
+    (weights are off by 2^-40 at most, and their sums by V times that at worst); a
     probability by 2^-18 of itself (the fp32 exponent's rounding, of at most 2^-24 times
     150, and the exponential's 2^-22), rounded to its type (2^-8 in bf16)."""
     R, V = logits.shape
