@@ -199,3 +199,46 @@ def test_offsets_that_are_none(n):
     b.attn(c)
     assert c.status() == zp.ERR_DEVICE_CHECK
     b.check_attn(skip=(2, 3))
+
+
+MIXES = [[(4, 70), (3, 200), (1, 33)], [(20, 300), (30, 40)], [(9, 130 + i) for i in range(80)],
+         [(100, 500), (60, 60)], [(400, 700)]]
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-30, 2.0])
+@pytest.mark.parametrize("spans", MIXES, ids=[str(i) for i in range(len(MIXES))])
+def test_scales_of_the_logits(spans, scale):
+    b = Batch8(spans, Hkv=4, Hq=16, d=64, seed=5)
+    b.scale = scale
+    run(b)
+    b.check_attn()
+
+
+@pytest.mark.parametrize("power", [-90, 90])
+@pytest.mark.parametrize("spans", MIXES, ids=[str(i) for i in range(len(MIXES))])
+def test_queries_of_every_size(spans, power):
+    """Rows of q from 2^-90 to 2^90, taken back by the scale; rows of zeros."""
+    b = Batch8(spans, Hkv=2, Hq=8, d=128, seed=6, packed=False)
+    b.q = (b.q.float() * 2.0 ** power).bfloat16()
+    b.q[::5] = 0
+    b.scale *= 2.0 ** -power
+    run(b)
+    b.check_attn()
+
+
+@pytest.mark.parametrize("spans", MIXES, ids=[str(i) for i in range(len(MIXES))])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_every_size(spans, d):
+    """Blocks of values whose scales lie up to 2^50 apart."""
+    b = Batch8(spans, Hkv=2, Hq=8, d=d, seed=8, spread=50)
+    run(b)
+    b.check_attn()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_tokens_of_every_size(d):
+    b = Batch8([(1, 20 * i + 1) for i in range(40)], Hkv=2, Hq=8, d=d, seed=8, spread=50,
+               packed=False)
+    b.scale = -0.3
+    b.decode(b.cache())
+    b.check_attn(split=0.0)
