@@ -50,6 +50,7 @@ namespace {
 constexpr int kD8Warps = 4;
 constexpr int kD8Threads = kD8Warps * 32;
 constexpr float kTop = 14.f;   // log2 of the largest p
+constexpr float kHuge = 3e38f;  // minus the maximum of no keys (an infinity less itself is NaN)
 constexpr int kD8Cluster = 8;  // splits that a cluster joins
 constexpr int kD8Blocks = 8;   // of a split, at least
 constexpr int kD8Groups = 16;  // clusters a (request, kv head), at most
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
     float o[NT][KS][4];  // dims 16 c + 2 g (+ 1 in [2], [3]), columns 8 n + 2 t, + 1
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        m_run[n][0] = m_run[n][1] = -1e30f;
+        m_run[n][0] = m_run[n][1] = -kHuge;
         l_run[n][0] = l_run[n][1] = 0.f;
 #pragma unroll
         for (int c = 0; c < KS; ++c)
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
     };
     auto join = [&](int hd, int c, const float *src, int step, int count, float &M, float &L,
                     float2 &O) {
-        M = -1e30f;
+        M = -kHuge;
         for (int w = 0; w < count; ++w)
             M = fmaxf(M, src[w * step + hd * ROW + D]);
         L = 0.f;
@@ -581,14 +582,14 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
         float2 ml[kD8Cluster], v[kD8Cluster];
 #pragma unroll
         for (int w = 0; w < kD8Cluster; ++w) {
-            ml[w] = make_float2(-1e30f, 0.f);
+            ml[w] = make_float2(-kHuge, 0.f);
             v[w] = make_float2(0.f, 0.f);
             if (w < cs) {
                 ml[w] = ld_dsmem_f32x2(dsmem_addr(part + hd * ROW + D, w));
                 v[w] = ld_dsmem_f32x2(dsmem_addr(part + hd * ROW + c, w));
             }
         }
-        float M = -1e30f, L = 0.f;
+        float M = -kHuge, L = 0.f;
         float2 O = make_float2(0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kD8Cluster; ++w)
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(D) zp_fp8_combine_kernel(const Fp8AttnArgs a)
     const int rh = blockIdx.x;  // request * Hq + hq
     const int c = threadIdx.x;
     const float *base = a.part + static_cast<size_t>(rh) * a.groups * (D + 2);
-    float M = -1e30f;
+    float M = -kHuge;
     for (int s = 0; s < a.groups; ++s)
         M = fmaxf(M, base[s * (D + 2) + D]);
     float L = 0.f, O = 0.f;

@@ -119,12 +119,18 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out);
  *       to the nearest e4m3 number (ties to even, magnitudes past 448 to 448, NaN to
  *       NaN).  Slots past the call's rows keep their bytes.
  *   zp_paged_decode_attn, zp_paged_chunk_attn  attend over the values; the
- *       probabilities' products with V are rounded to fp16 at most
+ *       probabilities are rounded to fp16 for the product with V, or to bf16 in the
+ *       chunks of 1,536 query rows (tokens times heads of a kv head) and more of a
+ *       batch of 768 a request and more in the mean, whose blocks are widened to bf16
+ *       first; chunks of more than 24 rows take q to 2^-17 of its row's largest element,
+ *       and their scores (scaled, in base 2) are below 2^20 in magnitude, where fp32
+ *       tells them apart
  *   zp_append_slots  copies a shared tail's scales with its rows
  *   zp_alloc_rows, zp_release_rows, zp_fork_rows, zp_verify_draft, zp_sample,
  *       zp_token_probs, zp_cache_status  as they are
  * zp_compress, zp_compress_prefill, zp_global_redundancy and
  * zp_global_redundancy_gram answer ZP_ERR_UNSUPPORTED: they read and move bf16 rows.
+ * The workspace is that of zp_cache_create and up to 256 MB for widened blocks.
  * Errors as zp_cache_create; a null scale pointer is ZP_ERR_INVALID_ARG. */
 zp_status zp_cache_create_fp8(const zp_cache_desc *desc, float *const *k_scales,
                               float *const *v_scales, zp_cache **out);

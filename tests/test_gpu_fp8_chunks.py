@@ -242,3 +242,27 @@ def test_single_tokens_of_every_size(d):
     b.scale = -0.3
     b.decode(b.cache())
     b.check_attn(split=0.0)
+
+
+@pytest.mark.parametrize("n,scale", [(1, 1e33), (1, -1e33), (4, 1e33), (4, -1e33), (30, 1e4),
+                                     (30, -1e4), (400, 1e4), (400, -1e4)])
+def test_the_first_key_alone_at_any_score(n, scale):
+    """The first token of a prompt sees its own key, whose weight is 1 however low its score is.
+    (Chunks of many rows take p in one step from a product and the maximum, whose rounding
+    is within the 2 that fp16 leaves above 2^15 for scores below 2^23 in base 2: the header
+    allows 2^20, and |q . k| is below 2^6 here.)"""
+    b = Batch8([(n, n)] * 3, Hkv=2, Hq=8, d=64, seed=4, packed=False)
+    b.scale = scale
+    c = run(b)
+    if n == 1:
+        want = b.out.clone()
+        b.out.fill_(7.0)
+        b.decode(c)
+        assert c.status() == zp.OK and torch.equal(b.out, want)
+    for i in range(3):
+        _, v = b.rows_of(i)
+        got = b.out[int(b.starts_np[i])].double().view(2, 4, 64)
+        # p v / p: p rounded for the product (2^-11 in fp16, 2^-8 in bf16) and not in the sum, then
+        # the result (2^-8); twice the fp32 roundings of both
+        rel = 2.0 ** -8 + (2.0 ** -8 if 4 * n >= 1536 else 2.0 ** -11) * (1 + 2.0 ** -8) + 2.0 ** -20
+        assert bool(((got - v[0][:, None]).abs() <= v[0][:, None].abs() * rel).all())
