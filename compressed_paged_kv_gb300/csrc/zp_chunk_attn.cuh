@@ -89,7 +89,7 @@
 // widened to bf16 first (zp_fp8_widen.cu).  Chunks of few rows are zp_fp8_decode.cu's.
 //
 // Measured, 256 chunks of 2 to 9 tokens over 1,024 to 2,038 keys, 32 heads of 128 over 8, 0.83 GB in
-// 299 us, 2.8 TB/s (a bf16 cache, of twice the bytes: 266); 19 chunks of 64 over 8,192 158 us (117).
+// 302 us, 2.7 TB/s (a bf16 cache, of twice the bytes: 266); 19 chunks of 64 over 8,192 158 us (117).
 // What bounds it: with few rows a tile, the two warps of a stream that have them (a row's 64 columns
 // take one warp 1.4 to 2.2 us of the 2.8 us between key tiles) and 13 us of Q, joins and output
 // between items; with many, the chain of a stream, longer by V's conversion.
@@ -166,6 +166,7 @@ struct CaSmem {
     static constexpr int NK = D == 128 ? (F8 ? 3 : 2) : 5;
     static constexpr int NV = D == 128 ? (F8 ? 2 : 3) : F8 ? 4 : 5;
     static constexpr int NR = F8 ? (D == 128 ? 2 : 4) : 0;
+    static_assert(NR <= NV, "a V tile that has come implies the release before last of its place");
     static constexpr int XC = 16;  // columns of O a step of the epilogue
     static constexpr int off_q = 0;                      // Q of A, Q of B
     // with 64 dims a row's numbers lie elsewhere than the row did: two more tiles for them
@@ -182,9 +183,9 @@ struct CaSmem {
     static constexpr int off_scan = off_plan + static_cast<int>(sizeof(CaPlan));  // int64 [warps]
     static constexpr int off_bar = off_scan + kCaThreads / 32 * 8;
     // K full, empty; V full, empty; Sfull[2], Pready[2], Ofull[2], Oempty[2], Qfull[2],
-    // Qempty[2], turn[2]; described, read [kDescs]; half, taken, done; 8-bit V full, empty;
-    // Qready[2]
-    static constexpr int NBAR = 2 * NK + 2 * NV + 14 + 2 * kDescs + 3 + (F8 ? 2 * NR + 2 : 0);
+    // Qempty[2], turn[2]; described, read [kDescs]; half, taken, done; 8-bit V full for A, for B,
+    // empty; Qready[2]
+    static constexpr int NBAR = 2 * NK + 2 * NV + 14 + 2 * kDescs + 3 + (F8 ? 3 * NR + 2 : 0);
     static constexpr int off_tmem = off_bar + NBAR * 8;
     // int: last arrived [2]; the call's set of arrivals; what the walk met (1: rows to
     // walk for again, 2: a wait given up); partial results left to the second walk [2]
@@ -864,7 +865,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     uint64_t *ofull = pready + 2, *oempty = ofull + 2, *qfull = oempty + 2, *qempty = qfull + 2;
     uint64_t *turn = qempty + 2, *described = turn + 2, *read = described + kDescs;
     uint64_t *half = read + kDescs, *taken = half + 1, *done = taken + 1;
-    uint64_t *rfull = done + 1, *rempty = rfull + NR, *qready = rempty + NR;  // F8 alone
+    uint64_t *rfull = done + 1, *rempty = rfull + 2 * NR, *qready = rempty + NR;  // F8 alone
     const uint32_t scales_at = smem_u32(sm + S::off_scale);
     float *sQf = reinterpret_cast<float *>(sm + S::off_qf);
     uint32_t *sTmem = reinterpret_cast<uint32_t *>(sm + S::off_tmem);
@@ -896,6 +897,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         }
         for (int s = 0; s < NR; ++s) {
             mbar_init(&rfull[s], 1);
+            mbar_init(&rfull[NR + s], 1);
             mbar_init(&rempty[s], kSmWarps);
         }
         for (int s = 0; s < kDescs; ++s) {
@@ -1215,7 +1217,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
             // ------------------------------------------------------------- V
             uint32_t loaded = 0, cur = 0, par = 0;
             constexpr uint32_t N = F8 ? NR : NV;  // 8-bit tiles go into a ring of their own
-            uint64_t *full = F8 ? rfull : vfull, *empty = F8 ? rempty : vempty;
+            uint64_t *empty = F8 ? rempty : vempty;
+            // 8-bit: the tiles that A converts have barriers of their own, and so do B's, as a
+            // stream does not wait for the other's: it could take the phase before last, of a
+            // tile that it did not wait for, for the one that it waits for
+            [[maybe_unused]] uint32_t owned[2] = {0, 0};
             for (;;) {
                 while (const CaDesc *dp = bad ? nullptr : enter()) {
                     const CaDesc d = *dp;
@@ -1234,12 +1240,18 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                             bad = true;
                             break;
                         }
+                        uint64_t *full = &vfull[cur];
+                        if constexpr (F8) {
+                            const bool b = d.ntok <= tpt && (i & 1);  // in turn, and B's
+                            full = &rfull[(b ? NR : 0) + (b ? owned[1] : owned[0]) % N];
+                            ++(b ? owned[1] : owned[0]);
+                        }
                         load_tile(a.vmap,
-                                  F8 ? sm + S::off_raw + cur * S::TILE8 : sV + cur * S::TILE,
-                                  &full[cur], second ? next_head(ids) : ids, t);
+                                  F8 ? sm + S::off_raw + cur * S::TILE8 : sV + cur * S::TILE, full,
+                                  second ? next_head(ids) : ids, t);
                         if constexpr (F8) {
                             if (elect_one())
-                                mbar_arrive(&full[cur]);
+                                mbar_arrive(full);
                             __syncwarp();
                         }
                         ++loaded;
@@ -1249,8 +1261,16 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                         }
                     }
                 }
-                for (uint32_t k = loaded > N ? loaded - N : 0; k < loaded; ++k)
-                    bad |= !warp_wait(&full[k % N], (k / N) & 1);
+                auto landed = [&](uint64_t *full, uint32_t n) {
+                    for (uint32_t k = n > N ? n - N : 0; k < n; ++k)
+                        bad |= !warp_wait(&full[k % N], (k / N) & 1);
+                };
+                if constexpr (F8) {
+                    landed(rfull, owned[0]);
+                    landed(rfull + NR, owned[1]);
+                } else {
+                    landed(vfull, loaded);
+                }
                 if (!walk_again(ended_clean()))
                     break;
                 leave();
@@ -1516,7 +1536,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         // (above 0, for scores of -infinity; 2^-149 times any finite one is nothing)
         const float ls = fmaxf(fabsf(a.logit_scale), __uint_as_float(1u));
         uint32_t ns = 0, no = 0, halves = 0;
-        [[maybe_unused]] uint32_t qs = 0, tiles = 0;  // F8: query tiles and key tiles so far
+        // F8: query tiles, key tiles and, of these, the stream's V tiles so far
+        [[maybe_unused]] uint32_t qs = 0, tiles = 0, raws = 0;
         [[maybe_unused]] bool ahead = false;          // F8: the item's Q is split already
         bool lent = false;  // B: its (max, sum) of a join lie in sMax
         // F8: the item's Q to e4m3, before any of its S: two tiles by their streams, a single
@@ -1575,9 +1596,10 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                     constexpr uint32_t N = F8 ? NR : 1;
                     const uint32_t k = tiles + nth(i), st = k % NV, rs = k % N;
                     const int t = single ? nth(i) : i;
-                    if (!bad && (!ca_wait(&rfull[rs], (k / N) & 1) ||
+                    if (!bad && (!ca_wait(&rfull[x * NR + raws % N], (raws / N) & 1) ||
                                  (k >= NV && !ca_wait(&vempty[st], (k / NV - 1) & 1))))
                         bad = true;
+                    ++raws;
                     bad = __any_sync(0xffffffffu, bad);
                     if (bad)
                         return;

@@ -266,3 +266,23 @@ def test_the_first_key_alone_at_any_score(n, scale):
         # the result (2^-8); twice the fp32 roundings of both
         rel = 2.0 ** -8 + (2.0 ** -8 if 4 * n >= 1536 else 2.0 ** -11) * (1 + 2.0 ** -8) + 2.0 ** -20
         assert bool(((got - v[0][:, None]).abs() <= v[0][:, None].abs() * rel).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_items_before_long_ones(d):
+    """Many items a CTA of one key tile, which one stream has no part in, and of several, odd and
+    even numbers of them, single ones, pairs and two heads at a time."""
+    spans = []
+    for i in range(240):
+        n = 6 + i % 20
+        spans.append((n, n + (i * 37 % 90 if i % 3 else 130 + i * 53 % 900)))
+    spans[50] = spans[170] = (70, 500)
+    for Hkv in (3, 2):
+        b = Batch8(spans, Hkv=Hkv, Hq=4 * Hkv, d=d, seed=Hkv)
+        c = run(b)
+        b.check_attn()
+        want = b.out.clone()
+        for _ in range(5):
+            b.out.fill_(7.0)
+            b.attn(c)
+            assert torch.equal(b.out, want)
