@@ -554,7 +554,7 @@ zp_status zp_verify_draft(zp_cache *cache, const int32_t *tokens, const int32_t 
  *  temperature, top_k, top_p, min_p   device [num_rows] fp32, int32, fp32, fp32, each
  *                NULL for 1, 0, 1, 0; row i uses entry req_idx[i], or i with NULL
  *                (entries may be used by several rows: a chunk's)
- *  R             rows of logits
+ *  R             rows of logits (of zp_sample at most max_requests)
  * Outputs share no memory with inputs or each other (ZP_ERR_INVALID_ARG).  An entry
  * out of range, a temperature below 0, infinite or NaN, a NaN among the others, or a
  * row without any logit above -infinity is recorded as ZP_ERR_DEVICE_CHECK in the
