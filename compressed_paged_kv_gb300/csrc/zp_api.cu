@@ -1093,8 +1093,15 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     a.vscale = c->vscales[layer];
     a.duos = static_cast<int64_t>(R) * c->Hkv >= 2ll * c->num_sms;
     const long long G = c->Hq / c->Hkv;
-    const int few = zp::fp8_few_rows(total * G, R, c->Hkv, bt_stride, c->num_sms);
-    if (few > 0) {
+    const zp::FewRows few = zp::fp8_few_rows(total * G, R, c->Hkv, static_cast<int>(G), bt_stride,
+                                             c->num_sms);
+    if (few.first > 0) {
+        // the longer ones first: the others' CTAs then start as theirs end
+        const int most = std::max(few.first, few.second);
+        const bool longer = total * G > most;
+        a.few = static_cast<int32_t>(most / G);
+        if (longer && zp::launch_fp8_chunk_attn(a, c->d, c->num_sms, s) != cudaSuccess)
+            return ZP_ERR_CUDA;
         zp::Fp8AttnArgs f{};
         f.splits = zp::fp8_decode_splits(static_cast<long long>(R) * c->Hkv, bt_stride,
                                          c->num_sms, &f.groups);
@@ -1120,11 +1127,14 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         f.logit_scale = a.logit_scale;
         f.out = a.out;
         f.sticky = c->ws.sticky;
-        if (zp::launch_fp8_few_rows(f, few, c->d, s) != cudaSuccess)
-            return ZP_ERR_CUDA;
-        if (total * G <= few)
-            return ZP_OK;
-        a.few = static_cast<int32_t>(few / G);
+        f.follows = longer;
+        for (const int rows : {few.first, few.second}) {
+            if (rows > 0 && zp::launch_fp8_few_rows(f, rows, c->d, s) != cudaSuccess)
+                return ZP_ERR_CUDA;
+            f.over = static_cast<int32_t>(rows / G);
+            f.follows = 1;
+        }
+        return ZP_OK;
     }
     // Requests with many query rows over widened blocks, the others over the cache, if the
     // batch has many rows a request: two kernels one after the other cost a mixed batch more

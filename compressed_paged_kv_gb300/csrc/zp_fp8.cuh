@@ -37,8 +37,9 @@ struct Fp8AttnArgs {
     const float *kscale, *vscale;
     const __nv_bfloat16 *q;
     int64_t q_stride;  // elements from a token's row of q to the next
-    const int32_t *starts;  // of a chunk
-    int32_t total;
+    const int32_t *starts;  // of a chunk: its requests of more than `over` tokens
+    int32_t total, over;
+    int32_t follows;        // behind a kernel that it may overlap: it waits for that at its end
     const int32_t *tables;
     int32_t stride, num_rows;
     const int32_t *lengths;
@@ -84,9 +85,12 @@ cudaError_t launch_fp8_append(const Fp8KvArgs &a, cudaStream_t s);
 // clusters that the splits are.
 int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *groups);
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s);
-// A chunk's requests with up to `rows` query rows (tokens times heads of a group; 8, 16 or 24),
-// groups 1; and the `rows` for a batch of so many, 0 if its requests are launch_fp8_chunk_attn's.
-int fp8_few_rows(long long rows, int R, int hkv, int bt_stride, int num_sms);
+// The rows (tokens times heads of a group; 8, 16 or 24) up to which a batch's requests are
+// launch_fp8_few_rows's, in one or two launches; 0: none, all are launch_fp8_chunk_attn's.
+struct FewRows {
+    int first, second;
+};
+FewRows fp8_few_rows(long long rows, int R, int hkv, int G, int bt_stride, int num_sms);
 cudaError_t launch_fp8_few_rows(const Fp8AttnArgs &a, int rows, int d, cudaStream_t s);
 cudaError_t launch_fp8_chunk_attn(const ChunkAttnArgs &a, int d, int sms, cudaStream_t s);
 // Once a device, before launch_fp8_chunk_attn.

@@ -52,6 +52,10 @@ constexpr int kD8Threads = kD8Warps * 32;
 constexpr float kTop = 14.f;   // log2 of the largest p
 constexpr float kHuge = 3e38f;  // minus the maximum of no keys (an infinity less itself is NaN)
 constexpr int kD8Cluster = 8;  // splits that a cluster joins
+#ifndef FEWMEAN
+#define FEWMEAN 128
+#endif
+constexpr int kFewMean = FEWMEAN;
 constexpr int kD8Blocks = 8;   // of a split, at least
 constexpr int kD8Groups = 16;  // clusters a (request, kv head), at most
 
@@ -88,7 +92,17 @@ template <int D, int NT, bool CHUNK>
 __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D == 128 ? 3 : 4)
     zp_fp8_decode_kernel(const __grid_constant__ Fp8AttnArgs a)
 {
-    pdl_wait();
+    if constexpr (CHUNK) {
+        // A launch behind another of the same call takes other requests: it starts as that one's
+        // CTAs end (it was let start when the work before the call was done and visible).  The
+        // first CTAs, and with them the grid, end no sooner than that one, so that who waits for
+        // this grid waits for both.
+        if (!a.follows)
+            pdl_wait();
+        pdl_launch_dependents();
+    } else {
+        pdl_wait();
+    }
     using S = D8Smem<D, NT>;
     constexpr int KS = D / 16, ROW = S::ROW, COLS = 8 * NT;
 
@@ -102,12 +116,24 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
     const int G = a.Hq / a.Hkv;
     ChunkReq rq{r, 1, 0, 0};
     if constexpr (CHUNK) {
-        bool bad;
-        const bool work = chunk_request(a, r, rq, &bad);
+        // By the offsets first, as in some batches most CTAs have no more to do.  The first launch
+        // of a call checks every request but the longer ones (not past the total: so there is
+        // another kernel, which checks them).
+        const int n = __ldcg(a.starts + r + 1) - __ldcg(a.starts + r);
+        const bool longer = n > COLS / G && n <= a.total;
+        bool bad = false, work = false;
+        if (a.over == 0 ? !longer : n > a.over && n <= COLS / G) {
+            if (a.follows)  // it did not wait: nothing of older work's from the SM's cache
+                __threadfence();
+            work = chunk_request(a, r, rq, &bad);
+        }
         if (bad && tid == 0 && split == 0 && h == 0)
             set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
-        if (!work || rq.n > COLS / G)  // (the whole cluster alike)
+        if (!work || rq.n > COLS / G) {  // (the whole cluster alike)
+            if (a.follows && blockIdx.x == 0)
+                pdl_wait();
             return;
+        }
     } else {
         rq.row = a.req_idx ? a.req_idx[r] : r;
         const bool row_ok = rq.row >= 0 && rq.row < a.num_rows;
@@ -503,7 +529,8 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
     }
     if (!ok && lane == 0)
         set_error(a.sticky, ZP_ERR_TIMEOUT);
-    pdl_launch_dependents();  // the combine kernel may be scheduled
+    if constexpr (!CHUNK)
+        pdl_launch_dependents();  // the combine kernel may be scheduled
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -573,8 +600,11 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
         if (c == 0)
             *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
     }
-    if (a.splits == 1)
+    if (a.splits == 1) {
+        if (CHUNK && a.follows && blockIdx.x == 0)
+            pdl_wait();
         return;
+    }
     cluster_sync();
     // each CTA joins its part of the dims
     for (int x = rank * kD8Threads + tid; x < rows * (D / 2); x += cs * kD8Threads) {
@@ -611,6 +641,8 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
             *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
     }
     cluster_sync();  // no CTA leaves while its part is read
+    if (CHUNK && a.follows && blockIdx.x == 0)
+        pdl_wait();
 }
 
 template <int D>
@@ -682,20 +714,28 @@ int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *groups)
     return splits;
 }
 
-// Rows up to which a batch's chunks are this file's, none (0) if it is not for it: the mean
-// rounded up, to 16, or to 24 of a mean up to 20, as the requests above it cost a second kernel
-// (256 chunks of 2 to 9 tokens, four heads a group: 314 us that way, 298 without).  Too few
-// units (request, kv head) for the splits to fill the GPU want short rows (one request of four
-// tokens, 8 kv heads: 2,000 keys 9.6 us, 8,192 20 and 30,000 56; the other kernel 20.6, 24.9 and
-// 38).
-int fp8_few_rows(long long rows, int R, int hkv, int bt_stride, int num_sms)
+// Rows up to which a batch's chunks are this file's, in up to two launches (0: none).  A large batch
+// has one for up to 16 (8 of a mean of 8 or less) and one for up to 24, if its mean is not so high that
+// it has few such chunks.  A small one, where a launch more costs more than it gains, has the
+// one of its mean, if that is at most 20.  Too few units (request, kv head) for the splits to
+// fill the GPU want short rows (one request of four tokens, 8 kv heads: 2,000 keys 9.6 us, 8,192 20
+// and 30,000 56; the other kernel 20.6, 24.9 and 38).
+FewRows fp8_few_rows(long long rows, int R, int hkv, int G, int bt_stride, int num_sms)
 {
-    const long long mean = (rows + R - 1) / R;
+    const long long mean = (rows + R - 1) / R, units = static_cast<long long>(R) * hkv;
+    FewRows f{0, 0};
+    if (units >= 4 * num_sms) {
+        if (mean <= kFewMean) {
+            f.first = mean <= 8 && G <= 8 ? 8 : 16;
+            f.second = mean <= 24 && 24 / G > f.first / G && rows > f.first ? 24 : 0;
+        }
+        return f;
+    }
     const int few = static_cast<int>((std::min<long long>(mean, 24) + 7) / 8 * 8);
-    const bool filled = static_cast<long long>(R) * hkv * kD8Cluster >= 2 * num_sms;
-    if (mean > 20 || (!filled && static_cast<long long>(few) * bt_stride > 8192))
-        return 0;
-    return few;
+    const bool filled = units * kD8Cluster >= 2 * num_sms;
+    if (mean <= 20 && (filled || static_cast<long long>(few) * bt_stride <= 8192))
+        f.first = few;
+    return f;
 }
 
 cudaError_t launch_fp8_decode(const Fp8AttnArgs &a, int d, cudaStream_t s)

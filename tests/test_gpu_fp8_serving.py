@@ -393,3 +393,54 @@ def test_offsets_past_32_bits():
     c.sample(logits, u, got[0], top_p=top_p)
     c.sample(small, u, got[1], top_p=top_p)
     assert torch.equal(*got) and c.status() == zp.OK
+
+
+def test_launches_that_overlap():
+    """A large batch of chunks of all lengths goes to three kernels that run into each other; what
+    the calls around them write and read is in order: q, lengths and rows change right before a
+    call, and its output is read, and written over, right behind it."""
+    R = 160
+    b = Batch8([(1 + i * 7 % 12, 30 + i * 29 % 500) for i in range(R)], Hkv=8, Hq=32, d=128, seed=31)
+    c = b.cache()
+    g = torch.Generator(device=DEV).manual_seed(5)
+    qs = [torch.randn(b.total, 32, 128, generator=g, device=DEV).bfloat16() for _ in range(4)]
+    cuts = [torch.zeros_like(b.lengths), (b.lengths > 40).int() * 13]
+    full, q = b.lengths.clone(), torch.empty_like(qs[0])
+    b.q = q
+
+    def call(k):
+        q.copy_(qs[k % 4])
+        b.lengths.copy_(full - cuts[k % 2])
+        b.attn(c)
+
+    want = []
+    for k in range(4):
+        call(k)
+        torch.cuda.synchronize()
+        want.append(b.out.clone())
+        b.lengths.copy_(full)
+        if k % 2 == 0:
+            b.check_attn()
+    got = [torch.empty_like(b.out) for _ in range(24)]
+    torch.cuda.synchronize()
+    for k in range(24):  # no host wait in between
+        call(k)
+        got[k].copy_(b.out)
+        b.out.fill_(7.0)
+    torch.cuda.synchronize()
+    for k in range(24):
+        assert torch.equal(got[k], want[k % 4]), k
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for k in range(4):
+            call(k)
+            got[k].copy_(b.out)
+            b.out.fill_(7.0)
+    for _ in range(5):
+        for k in range(4):
+            got[k].fill_(0.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in range(4):
+            assert torch.equal(got[k], want[k]), k
+    assert c.status() == zp.OK
