@@ -52,10 +52,6 @@ constexpr int kD8Threads = kD8Warps * 32;
 constexpr float kTop = 14.f;   // log2 of the largest p
 constexpr float kHuge = 3e38f;  // minus the maximum of no keys (an infinity less itself is NaN)
 constexpr int kD8Cluster = 8;  // splits that a cluster joins
-#ifndef FEWMEAN
-#define FEWMEAN 128
-#endif
-constexpr int kFewMean = FEWMEAN;
 constexpr int kD8Blocks = 8;   // of a split, at least
 constexpr int kD8Groups = 16;  // clusters a (request, kv head), at most
 
@@ -714,18 +710,21 @@ int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *groups)
     return splits;
 }
 
-// Rows up to which a batch's chunks are this file's, in up to two launches (0: none).  A large batch
-// has one for up to 16 (8 of a mean of 8 or less) and one for up to 24, if its mean is not so high that
-// it has few such chunks.  A small one, where a launch more costs more than it gains, has the
-// one of its mean, if that is at most 20.  Too few units (request, kv head) for the splits to
-// fill the GPU want short rows (one request of four tokens, 8 kv heads: 2,000 keys 9.6 us, 8,192 20
-// and 30,000 56; the other kernel 20.6, 24.9 and 38).
+// A large batch has a launch for up to 16 rows (8 of a mean of 8 or less), unless its mean says that
+// hardly any chunk has so few, and one for up to 24 of a mean of no more.  Measured with 8 kv heads
+// against the other kernel alone: 256 chunks of 2 to 9 tokens, four heads a group, 270 and 304 us; of
+// 1 to 5, 214 and 307; 200 single tokens beside 8 pieces of 600, 276 and 375; where none is short, 256
+// of 8 tokens 303 and 297, of 20 tokens 326 and 320.  A small batch, where a launch more costs
+// more than it gains (38 chunks of 2 to 9: 61 and 78 us with two), has the one of its mean, if that
+// is at most 20.  Too few units (request, kv head) for the splits to fill the GPU want short rows
+// (one request of four tokens: 2,000 keys 9.6 us, 8,192 20 and 30,000 56; the other kernel 20.6,
+// 24.9 and 38).
 FewRows fp8_few_rows(long long rows, int R, int hkv, int G, int bt_stride, int num_sms)
 {
     const long long mean = (rows + R - 1) / R, units = static_cast<long long>(R) * hkv;
     FewRows f{0, 0};
     if (units >= 4 * num_sms) {
-        if (mean <= kFewMean) {
+        if (mean <= 128) {
             f.first = mean <= 8 && G <= 8 ? 8 : 16;
             f.second = mean <= 24 && 24 / G > f.first / G && rows > f.first ? 24 : 0;
         }

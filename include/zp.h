@@ -122,9 +122,9 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out);
  *       probabilities are rounded to fp16 for the product with V, or to bf16 in the
  *       chunks of 1,536 query rows (tokens times heads of a kv head) and more of a
  *       batch of 768 a request and more in the mean, whose blocks are widened to bf16
- *       first; chunks of more than 24 rows take q to 2^-17 of its row's largest element,
- *       and their scores (scaled, in base 2) are below 2^20 in magnitude, where fp32
- *       tells them apart
+ *       first; zp_paged_chunk_attn may take q to 2^-17 of its row's largest element, and
+ *       its scores (scaled, in base 2) are below 2^20 in magnitude, where fp32 tells
+ *       them apart
  *   zp_append_slots  copies a shared tail's scales with its rows
  *   zp_alloc_rows, zp_release_rows, zp_fork_rows, zp_verify_draft, zp_sample,
  *       zp_token_probs, zp_cache_status  as they are

@@ -40,8 +40,10 @@ cudaError_t launch_fp8_decode(const Fp8AttnArgs &, int, cudaStream_t)
 }
 cudaError_t launch_fp8_few_rows(const Fp8AttnArgs &a, int rows, int, cudaStream_t)
 {
-    g_calls += a.groups == 1 && a.splits >= 1 && a.splits <= 8 ? "f" : "?";
-    g_few = rows;
+    const bool first = a.over == 0, behind = !g_calls.empty();
+    const bool ok = a.groups == 1 && a.splits >= 1 && a.splits <= 8 && a.follows == behind;
+    g_calls += !ok ? "?" : first ? "f" : "g";
+    g_few = first ? rows : g_few * 100 + rows;
     return cudaSuccess;
 }
 cudaError_t launch_fp8_widen(const Fp8WidenArgs &, int, cudaStream_t)
@@ -252,7 +254,7 @@ static int calls()
     const int batch = 0;
     Line m;
     zp_cache c = handle(m, 512);
-    const size_t most = 4096;
+    const size_t most = 8193;
     int32_t *starts = m.take<int32_t>(4 * 513), *tables = m.take<int32_t>(4 * 512 * 2048);
     int32_t *lengths = m.take<int32_t>(4 * 512), *req_idx = m.take<int32_t>(4 * 512);
     uint8_t *q = m.take<uint8_t>(most * 8192), *out = m.take<uint8_t>(most * 8192);
@@ -265,18 +267,28 @@ static int calls()
                                  R, scale, o ? o : out, nullptr);
         return g_calls;
     };
-    // by the mean of the rows (four heads a group): up to 16, up to 20, above, 768 and more
-    CHECK(attn(256, 256, 128) == "fc" && g_few == 8 && g_attn.few == 2);
-    CHECK(attn(256, 4 * 256, 128) == "fc" && g_few == 16 && g_attn.few == 4);
-    CHECK(attn(256, 5 * 256, 128) == "fc" && g_few == 24 && g_attn.few == 6);
-    CHECK(attn(256, 5 * 256 + 1, 128) == "c" && g_attn.few == 0 && g_attn.duos == 1);
+    // a large batch by the mean of the rows (four heads a group): up to 8, up to 24, up to 128,
+    // above; the longer ones first, the others behind them and each other
+    CHECK(attn(256, 2 * 256, 128) == "cfg" && g_few == 824 && g_attn.few == 6);
+    CHECK(attn(256, 2 * 256 + 1, 128) == "cfg" && g_few == 1624 && g_attn.few == 6);
+    CHECK(attn(256, 6 * 256, 128) == "cfg" && g_few == 1624 && g_attn.few == 6);
+    CHECK(attn(256, 6 * 256 + 1, 128) == "cf" && g_few == 16 && g_attn.few == 4);
+    CHECK(attn(256, 32 * 256, 128) == "cf" && g_few == 16 && g_attn.few == 4);
+    CHECK(attn(256, 32 * 256 + 1, 128) == "c" && g_attn.few == 0 && g_attn.duos == 1);
+    // no more rows in all than the first launch's, or the second's: nothing for the others
+    CHECK(attn(256, 2, 128) == "f" && attn(256, 6, 128) == "fg" && attn(256, 7, 128) == "cfg");
+    // a smaller one: up to 20, the launch of its mean
+    CHECK(attn(38, 38 * 2, 128) == "cf" && g_few == 8 && g_attn.few == 2);
+    CHECK(attn(38, 38 * 4, 128) == "cf" && g_few == 16 && g_attn.few == 4);
+    CHECK(attn(38, 38 * 5, 128) == "cf" && g_few == 24 && g_attn.few == 6);
+    CHECK(attn(38, 38 * 5 + 1, 128) == "c" && g_attn.few == 0);
     CHECK(attn(37, 37 * 30, 128) == "c" && g_attn.duos == 0);
     CHECK(attn(4, 4 * 191, 128) == "c" && attn(4, 4 * 192, 128) == "wbc");
     // all of them few: no other kernel
     CHECK(attn(1, 4, 128) == "f" && attn(1, 5, 128) == "f" && g_few == 24);
     // few units and a wide table
     CHECK(attn(1, 4, 512) == "f" && attn(1, 4, 513) == "c" && attn(1, 5, 342) == "c");
-    CHECK(attn(38, 38 * 4, 2000) == "fc");
+    CHECK(attn(38, 38 * 4, 2000) == "cf");
     CHECK(attn(0, 0, 128).empty() && st == ZP_OK && attn(3, 0, 128).empty() && st == ZP_OK);
     // refusals
     auto refused = [&](const std::string &x) { return x.empty() && st == ZP_ERR_INVALID_ARG; };
