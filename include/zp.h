@@ -545,8 +545,9 @@ zp_status zp_verify_draft(zp_cache *cache, const int32_t *tokens, const int32_t 
  * equal logits in the order of their index.  A temperature of 0 keeps the first of
  * the largest alone.  A NaN counts as -infinity, whose weight is 0; of infinite logits
  * only they have weight.
- * Weights are formed and summed in more than 40 bits behind the largest's point, and
- * their sums are exact, so that neither depends on the order of the work.
+ * Weights are formed to 2^-40 of the largest, and their sums are exact, so that no
+ * result depends on the order of the work: a cut or a draw whose border lies within
+ * vocab * 2^-40 of the largest weight may fall to either side, the same one every time.
  *
  *  logits        device [R][vocab] of logit_dtype, rows logit_stride elements apart
  *                (any, >= vocab)
