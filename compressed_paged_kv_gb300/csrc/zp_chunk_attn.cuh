@@ -712,6 +712,17 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16(uint32_t v)
     return r;
 }
 
+// What a logit over an 8-bit cache is multiplied by: its row's factor times its block's scale.
+// Never 0, so that a masked score, -infinity, stays that (a row of zeros has a factor of about
+// 2^-138, a block of zeros a scale of 2^-32), and finite, so that a score of 0 does; NaN stays NaN.
+__device__ __forceinline__ float logit_factor(float row, float scale)
+{
+    float f;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(row * scale), "f"(__uint_as_float(0x00800000u)));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(f), "f"(__uint_as_float(0x7f7fffffu)));
+    return f;
+}
+
 // The workspace slot of a partial result: O [256][D], then (max, sum) [256].
 template <int D>
 __device__ __forceinline__ float *slot_ptr(float *part, int slot)
@@ -835,9 +846,8 @@ __device__ __forceinline__ void split_q(uint32_t from, uint32_t to, int ct, int 
     }
     const float back = fabsf(logit_scale) * __uint_as_float(exp2_bits(-e1)) *
                        __uint_as_float(exp2_bits(-e2));
-    if (hf == 0)  // (above 0, for scores of -infinity)
-        factor[r] =
-            most < 0x7f800000u ? fmaxf(back, __uint_as_float(0x00800000u)) : INFINITY - INFINITY;
+    if (hf == 0)
+        factor[r] = most < 0x7f800000u ? back : INFINITY - INFINITY;
 }
 
 }  // namespace
@@ -1664,7 +1674,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                                     mx[1] = fmaxf(mx[1], s[b + c + 1]);
                                 }
                                 const float4 sc = ld_shared_f32x4(sc_at + b / kBlk * 16);
-                                m_new = fmaxf(m_new, fmaf(fmaxf(mx[0], mx[1]), lr * sc.x, sc.y));
+                                m_new = fmaxf(
+                                    m_new, fmaf(fmaxf(mx[0], mx[1]), logit_factor(lr, sc.x), sc.y));
                             }
                         } else {
                             float mx[4] = {s[0], s[1], s[2], s[3]};
@@ -1702,7 +1713,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
 #pragma unroll
                                 for (int b = 0; b < PC; b += kBlk) {
                                     const float4 sc = ld_shared_f32x4(sc_at + (c + b) / kBlk * 16);
-                                    const float mul = lr * sc.x, add = sc.y + negm;
+                                    const float mul = logit_factor(lr, sc.x), add = sc.y + negm;
                                     float g0 = 0.f, g1 = 0.f;
 #pragma unroll
                                     for (int e = b; e < b + kBlk; e += 2) {
