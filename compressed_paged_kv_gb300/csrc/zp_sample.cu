@@ -835,9 +835,10 @@ __global__ void __launch_bounds__(kSpThreads, 2)
     Cut cut{};
     cut.tau = -INFINITY;
     cut.m = 0x7fffffff;
+    // (finite, as the maximum's place, 0 times it, is 0: of a range below 1.5e-36 it would not be)
+    constexpr float kBig = 3.4e38f;  // (also in place of infinite logits)
     const float range = fminf(64.f / c.ch, M - bottom);
-    const float per_gap = range > 0.f ? kBuckets / range : 0.f;
-    constexpr float kBig = 3.4e38f;  // (in place of infinite logits)
+    const float per_gap = range > 0.f ? fminf(kBuckets / range, kBig) : 0.f;
     const float big_M = fminf(M, kBig);
     auto place_of = [&](float v) { return (big_M - fminf(v, kBig)) * per_gap; };  // falls with v
     auto bucket_of = [&](float v) { return min(kBuckets - 1, static_cast<int>(place_of(v))); };
