@@ -648,10 +648,11 @@ __global__ void __launch_bounds__(kSpThreads, 2)
         temp = 1.f;
         top_k = 1;
     }
+    temp = fminf(fmaxf(temp, kLeastTemp), kMostTemp);
     if (top_k < 0 || top_k >= a.vocab)
         top_k = 0;
     if (tid == 0) {  // (64-bit arithmetic of a whole CTA would take 3 us)
-        const double d = fmin(1.4426950408889634 / static_cast<double>(temp), 1.2e30);
+        const double d = 1.4426950408889634 / static_cast<double>(temp);
         S.scale.ch = static_cast<float>(d);
         S.scale.cl = static_cast<float>(d - static_cast<double>(S.scale.ch));
         S.gap = make_float2(INFINITY, 0.f);

@@ -48,6 +48,12 @@ struct WeightScale {
     float ch, cl;  // log2(e) / T as a pair
 };
 
+// The temperatures that are taken as they are: log2(e) / T, the range of gaps that have weight and
+// the buckets over it, 64 T ln 2 and 8 log2(e) / T, are fp32 numbers.  Past 2^100 cl is a multiple of
+// 2^-149, which puts y off by up to 2^-25 and a weight by 2^-24 of itself.
+constexpr float kLeastTemp = 7.5231638452626401e-37f;  // 2^-120
+constexpr float kMostTemp = 1.3292279957849159e36f;    // 2^120
+
 struct WeightTable {
     uint64_t v[1024];
     constexpr WeightTable() : v()

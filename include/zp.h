@@ -543,11 +543,12 @@ zp_status zp_verify_draft(zp_cache *cache, const int32_t *tokens, const int32_t 
  *     of these the weights of at least min_p (0 and less: all; 1 and more: those
  *       equal to the largest),
  * equal logits in the order of their index.  A temperature of 0 keeps the first of
- * the largest alone.  A NaN counts as -infinity, whose weight is 0; of infinite logits
- * only they have weight.
- * Weights are formed to 2^-40 of the largest, and their sums are exact, so that no
- * result depends on the order of the work: a cut or a draw whose border lies within
- * vocab * 2^-40 of the largest weight may fall to either side, the same one every time.
+ * the largest alone; others below 2^-120 count as that, and those above 2^120 as that.
+ * A NaN counts as -infinity, whose weight is 0; of infinite logits only they have weight.
+ * Weights are formed to 2^-40 of the largest (and, at temperatures above 2^100, to 2^-24
+ * of themselves), and their sums are exact, so that no result depends on the order of the
+ * work: a cut or a draw whose border lies within vocab * 2^-40 of the largest weight (2^-23
+ * of the sum at those temperatures) may fall to either side, the same one every time.
  *
  *  logits        device [R][vocab] of logit_dtype, rows logit_stride elements apart
  *                (any, >= vocab)
