@@ -286,6 +286,7 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
              cudaMemcpy(ws.wide_maps, wide_maps, sizeof(wide_maps), cudaMemcpyHostToDevice) ==
                  cudaSuccess;
     ok = ok && zp::prepare_chunk_attn(D.head_dim) == cudaSuccess &&
+         zp::prepare_sample() == cudaSuccess &&
          cudaMemset(c->base, 0, o_kmaps) == cudaSuccess &&
          cudaMemset(b + o_rowmark, 0, 4 * static_cast<size_t>(D.max_requests)) == cudaSuccess &&
          cudaMemset(b + o_ap_call, 0, o_ap_occ - o_ap_call) == cudaSuccess &&

@@ -1349,28 +1349,48 @@ __global__ void __launch_bounds__(kSpThreads, 2)
               partial, cut.tau, ties_before);
 }
 
+// Vectors a lane of a row's `ctas` CTAs, and their shared memory; T the logits' type.
+template <class T>
+static int steps_of(int vocab, int ctas)
+{
+    constexpr int VE = 16 / sizeof(T);
+    return (vocab + 2 * VE - 2) / VE / (ctas * kSpThreads) + 1;
+}
+template <class T>
+static size_t bytes_of(int vocab, int ctas)
+{
+    constexpr size_t kShared = (sizeof(SpShared) + 127) / 128 * 128;
+    return kShared + static_cast<size_t>(steps_of<T>(vocab, ctas)) * kSpThreads * 16;
+}
+
+// Up to which a call has fewer CTAs a row than kSpCtas: two of them fit on an SM.
+constexpr size_t kSpBytes = 112 * 1024;
+
+template <class T>
+static cudaError_t prepare_sample_t()
+{
+    const size_t most = std::max(kSpBytes, bytes_of<T>(kSampleMaxVocab, kSpCtas));
+    return cudaFuncSetAttribute(zp_sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(most));
+}
+
+cudaError_t prepare_sample()
+{
+    const cudaError_t err = prepare_sample_t<float>();
+    return err != cudaSuccess ? err : prepare_sample_t<__nv_bfloat16>();
+}
+
 template <class T>
 static cudaError_t launch_sample_t(const SampleArgs &a, int sms, cudaStream_t s)
 {
-    constexpr size_t kShared = (sizeof(SpShared) + 127) / 128 * 128;
-    constexpr int VE = 16 / sizeof(T);
-    auto steps_of = [&](int ctas) {
-        return (a.vocab + 2 * VE - 2) / VE / (ctas * kSpThreads) + 1;
-    };
-    auto bytes_of = [&](int ctas) { return kShared + steps_of(ctas) * kSpThreads * 16; };
     // As many CTAs as the SMs hold at once, two each, up to eight a row and up to a vector a
     // lane; at least so many that two fit on an SM (96 rows of 50,257 bf16 logits with
     // filters of all kinds: 3 CTAs a row 56 us, 2 67)
     const int most = static_cast<int>(std::min<long long>(kSpCtas, std::max(1, 2 * sms / a.R)));
     int ctas = 1;
-    while (ctas < kSpCtas && (bytes_of(ctas) > 112 * 1024 || ctas < most) && steps_of(ctas) > 1)
+    while (ctas < kSpCtas && (bytes_of<T>(a.vocab, ctas) > kSpBytes || ctas < most) &&
+           steps_of<T>(a.vocab, ctas) > 1)
         ++ctas;
-    const size_t bytes = bytes_of(ctas);
-    cudaError_t err = cudaFuncSetAttribute(zp_sample_kernel<T>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(bytes));
-    if (err != cudaSuccess)
-        return err;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1381,11 +1401,11 @@ static cudaError_t launch_sample_t(const SampleArgs &a, int sms, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.R) * static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(kSpThreads, 1, 1);
-    cfg.dynamicSmemBytes = bytes;
+    cfg.dynamicSmemBytes = bytes_of<T>(a.vocab, ctas);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, zp_sample_kernel<T>, a, ctas, steps_of(ctas));
+    return cudaLaunchKernelEx(&cfg, zp_sample_kernel<T>, a, ctas, steps_of<T>(a.vocab, ctas));
 }
 
 cudaError_t launch_sample(const SampleArgs &a, bool bf16, int sms, cudaStream_t s)

@@ -27,6 +27,9 @@ struct SampleArgs {
 // Vocabulary limit: a row lies in the shared memory of eight CTAs.
 constexpr int kSampleMaxVocab = 352 * 1024;
 
+// Once a device, before launch_sample: the most shared memory that any call needs.  (It is the
+// kernels' own state, which calls from several threads share: a call does not set it.)
+cudaError_t prepare_sample();
 cudaError_t launch_sample(const SampleArgs &a, bool bf16, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ weights
