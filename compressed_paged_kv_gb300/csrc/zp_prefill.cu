@@ -640,9 +640,10 @@ static cudaError_t launch_for_d(const PrefillArgs &a, int mt, int units, cudaStr
                               : launch_passes<D, 4>(a, units, s);
     if (e != cudaSuccess)
         return e;
+    // (the most of any call: calls of other threads share the limit)
     const int sel_smem = a.T_cap * 4;
     e = cudaFuncSetAttribute(zp_prefill_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sel_smem);
+                             kPrefillMaxTokens * 4);
     if (e != cudaSuccess)
         return e;
     zp_prefill_select_kernel<<<static_cast<unsigned>(units), kSelThreads, sel_smem, s>>>(a);
