@@ -73,6 +73,15 @@ struct D8Smem {
     static constexpr int ALLOC = BYTES + 1024;
 };
 
+// An infinity as the largest number, so that a score of 0 times it is 0; NaN stays NaN.
+__device__ __forceinline__ float finite(float x)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(__uint_as_float(0xff7fffffu)));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(__uint_as_float(0x7f7fffffu)));
+    return y;
+}
+
 // An 8x8 matrix of 16-bit elements, a row's two neighbours a lane, transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t v)
 {
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v = fmaf(sacc[blk][n][e], fr[n][e & 1] * kx, lv);
+                    const float v = fmaf(sacc[blk][n][e], finite(fr[n][e & 1] * kx), lv);
                     bool in = e < 2 ? in0 : in1;
                     if constexpr (CHUNK)
                         in = tok0 + key + (e < 2 ? 0 : 8) < lim[n][e & 1] && there;

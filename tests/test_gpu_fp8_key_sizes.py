@@ -108,3 +108,9 @@ def check_a_query_that_meets_no_key(path, d):
 @pytest.mark.parametrize("path", ["tile", "heads", "pairs", "widened"])
 def test_huge_keys_that_a_huge_query_does_not_meet(path, d):
     check_a_query_that_meets_no_key(path, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("path", ["single", "few"])
+def test_few_rows_of_huge_queries_that_meet_no_key(path, d):
+    check_a_query_that_meets_no_key(path, d)
