@@ -198,7 +198,7 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
     const size_t o_ap_occ = A.take(4 * static_cast<size_t>(D.num_blocks));
     const size_t o_ap_last = A.take(4 * static_cast<size_t>(D.num_blocks));
     const size_t o_ap_plan = A.take(16 * static_cast<size_t>(D.max_requests));
-    const size_t ca_arr = 4 * (4 * static_cast<size_t>(c->num_sms) + 1);  // and ca_entered
+    const size_t ca_arr = 4 * (4 * static_cast<size_t>(c->num_sms) + 2);  // and the words behind
     const size_t o_ca_arr = A.take(ca_arr);
     const size_t o_ca_part = A.take(4 * zp::chunk_attn_part_floats(D.head_dim, c->num_sms));
     const int wide = fp8 ? zp::fp8_wide_blocks(D.num_blocks, D.num_kv_heads, D.head_dim) : 0;
@@ -244,6 +244,7 @@ static zp_status create(const zp_cache_desc *desc, float *const *k_scales, float
     ws.ap_plan = reinterpret_cast<int4 *>(b + o_ap_plan);
     ws.ca_arrived = reinterpret_cast<uint32_t *>(b + o_ca_arr);
     ws.ca_entered = ws.ca_arrived + 4 * c->num_sms;
+    ws.ca_visible = ws.ca_entered + 1;
     ws.ca_part = reinterpret_cast<float *>(b + o_ca_part);
     if (fp8) {
         ws.wide_places = reinterpret_cast<int32_t *>(b + o_wide_places);
@@ -1101,6 +1102,7 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         const int most = std::max(few.first, few.second);
         const bool longer = total * G > most;
         a.few = static_cast<int32_t>(most / G);
+        a.visible = longer || few.second > 0 ? c->ws.ca_visible : nullptr;
         if (longer && zp::launch_fp8_chunk_attn(a, c->d, c->num_sms, s) != cudaSuccess)
             return ZP_ERR_CUDA;
         zp::Fp8AttnArgs f{};
@@ -1129,9 +1131,14 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
         f.out = a.out;
         f.sticky = c->ws.sticky;
         f.follows = longer;
+        f.visible = a.visible;
         for (const int rows : {few.first, few.second}) {
-            if (rows > 0 && zp::launch_fp8_few_rows(f, rows, c->d, s) != cudaSuccess)
+            f.last = rows == few.second || few.second == 0;
+            if (rows > 0 && zp::launch_fp8_few_rows(f, rows, c->d, s) != cudaSuccess) {
+                if (f.follows)  // no last kernel clears the word
+                    cudaMemsetAsync(f.visible, 0, 4, s);
                 return ZP_ERR_CUDA;
+            }
             f.over = static_cast<int32_t>(rows / G);
             f.follows = 1;
         }

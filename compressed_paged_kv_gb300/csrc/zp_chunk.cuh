@@ -52,6 +52,7 @@ struct ChunkAttnArgs {
     const int32_t *places;
     int32_t widened;
     int32_t few;   // an 8-bit cache's chunks of so many tokens are another kernel's
+    uint32_t *visible;  // if kernels behind this one overlap it: their word (zp_fp8.cuh)
     int32_t duos;  // an 8-bit cache's short chunks: kv heads by two (zp_chunk_attn.cuh)
 };
 

@@ -933,6 +933,8 @@ __global__ void __launch_bounds__(kCaThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&a.qmap) : "memory");
     }
     pdl_wait();  // launched early: everything of the kernels before it is visible from here
+    if (F8 && a.visible && blockIdx.x == 0 && tid == 0)
+        say_visible(a.visible);
     pdl_launch_dependents();
 
     // the call's set of arrivals (a thread with no requests of its own in most batches)

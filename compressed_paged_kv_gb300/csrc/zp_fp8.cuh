@@ -39,7 +39,9 @@ struct Fp8AttnArgs {
     int64_t q_stride;  // elements from a token's row of q to the next
     const int32_t *starts;  // of a chunk: its requests of more than `over` tokens
     int32_t total, over;
-    int32_t follows;        // behind a kernel that it may overlap: it waits for that at its end
+    int32_t follows;        // behind a kernel of the call that it may overlap
+    int32_t last;           // of such kernels
+    uint32_t *visible;      // their word; null where one kernel takes all requests
     const int32_t *tables;
     int32_t stride, num_rows;
     const int32_t *lengths;
@@ -100,6 +102,30 @@ cudaError_t prepare_fp8_chunk_attn(int d);
 bool encode_fp8_pool_map(CUtensorMap *map, const void *pool, int num_blocks, int hkv, int d);
 
 #ifdef __CUDACC__
+
+// Kernels of one call that overlap: a later one takes other requests than those before it, and may
+// start as soon as the first has been let start, without the wait by which the work before the call
+// becomes visible to a grid.  So the first kernel, behind its own wait, releases a word
+// of the workspace, and every thread of a later one begins with an acquire of it: what was visible
+// to the first then is to the later one, and by the fence to its TMA loads.  A thread that does not
+// find the word waits for the first kernel's end instead.  The last kernel clears the word when all
+// before it have ended.
+__device__ __forceinline__ void say_visible(uint32_t *word)
+{
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(1u) : "memory");
+}
+__device__ __forceinline__ void await_visible(const uint32_t *word)
+{
+    uint32_t said;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(said) : "l"(word) : "memory");
+    if (!said)
+        pdl_wait();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+__device__ __forceinline__ void clear_visible(uint32_t *word)
+{
+    asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(word), "r"(0u) : "memory");
+}
 
 // The exponent of the least scale that takes `most` (>= 0, or infinite) into 448.
 __host__ __device__ __forceinline__ int fp8_scale_exp(uint32_t most_bits)

@@ -98,12 +98,16 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
     zp_fp8_decode_kernel(const __grid_constant__ Fp8AttnArgs a)
 {
     if constexpr (CHUNK) {
-        // A launch behind another of the same call takes other requests: it starts as that one's
-        // CTAs end (it was let start when the work before the call was done and visible).  The
-        // first CTAs, and with them the grid, end no sooner than that one, so that who waits for
-        // this grid waits for both.
-        if (!a.follows)
+        // A launch behind another of the same call starts as that one's CTAs end.  The first CTAs,
+        // and with them the grid, end no sooner than that one, so that who waits for this grid
+        // waits for both (end_of_grid below).
+        if (a.follows) {
+            await_visible(a.visible);
+        } else {
             pdl_wait();
+            if (a.visible && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+                say_visible(a.visible);
+        }
         pdl_launch_dependents();
     } else {
         pdl_wait();
@@ -120,6 +124,13 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
     const int split = blockIdx.x % a.splits, r = blockIdx.x / a.splits, h = blockIdx.y;
     const int G = a.Hq / a.Hkv;
     ChunkReq rq{r, 1, 0, 0};
+    [[maybe_unused]] auto end_of_grid = [&] {
+        if (!a.follows || blockIdx.x != 0)
+            return;
+        pdl_wait();
+        if (a.last && blockIdx.y == 0 && tid == 0)
+            clear_visible(a.visible);
+    };
     if constexpr (CHUNK) {
         // By the offsets first, as in some batches most CTAs have no more to do.  The first launch
         // of a call checks every request but the longer ones (not past the total: so there is
@@ -127,16 +138,12 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
         const int n = __ldcg(a.starts + r + 1) - __ldcg(a.starts + r);
         const bool longer = n > COLS / G && n <= a.total;
         bool bad = false, work = false;
-        if (a.over == 0 ? !longer : n > a.over && n <= COLS / G) {
-            if (a.follows)  // it did not wait: nothing of older work's from the SM's cache
-                __threadfence();
+        if (a.over == 0 ? !longer : n > a.over && n <= COLS / G)
             work = chunk_request(a, r, rq, &bad);
-        }
         if (bad && tid == 0 && split == 0 && h == 0)
             set_error(a.sticky, ZP_ERR_DEVICE_CHECK);
         if (!work || rq.n > COLS / G) {  // (the whole cluster alike)
-            if (a.follows && blockIdx.x == 0)
-                pdl_wait();
+            end_of_grid();
             return;
         }
     } else {
@@ -606,8 +613,8 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
             *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
     }
     if (a.splits == 1) {
-        if (CHUNK && a.follows && blockIdx.x == 0)
-            pdl_wait();
+        if constexpr (CHUNK)
+            end_of_grid();
         return;
     }
     cluster_sync();
@@ -646,8 +653,8 @@ __global__ void __launch_bounds__(kD8Threads, NT > 2 ? (D == 128 ? 2 : 3) : D ==
             *reinterpret_cast<float2 *>(p + D) = make_float2(M, L);
     }
     cluster_sync();  // no CTA leaves while its part is read
-    if (CHUNK && a.follows && blockIdx.x == 0)
-        pdl_wait();
+    if constexpr (CHUNK)
+        end_of_grid();
 }
 
 template <int D>

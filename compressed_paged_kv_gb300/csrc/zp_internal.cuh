@@ -56,6 +56,7 @@ struct Workspace {
     float *ca_part;       // partial results of the work items cut between SMs
     uint32_t *ca_arrived; // [2][2 * SMs] of them that are written: two sets, used in turn
     uint32_t *ca_entered; // CTAs that have entered a call, modulo two calls'
+    uint32_t *ca_visible; // the word of an 8-bit cache's chunk call whose kernels overlap
     // an 8-bit cache: blocks widened for a chunk call
     __nv_bfloat16 *wide_k, *wide_v; // [wide_blocks][Hkv][16][d]
     CUtensorMap *wide_maps;         // of the two
