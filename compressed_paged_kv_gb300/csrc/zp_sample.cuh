@@ -139,46 +139,86 @@ __host__ __device__ __forceinline__ uint64_t weight(const uint64_t *table, const
     return weight_of_parts(table, p, static_cast<uint32_t>(bits_of(t)), static_cast<int>(z));
 }
 
-// Two fp32 numbers, each operation on both at once.
+__host__ __device__ __forceinline__ float float_of(uint32_t x)
+{
+#ifdef __CUDA_ARCH__
+    return __uint_as_float(x);
+#else
+    float v;
+    __builtin_memcpy(&v, &x, 4);
+    return v;
+#endif
+}
+
+// Two fp32 numbers, each operation on both at once (on the host one after the other).
 struct Two {
     uint64_t v;
 };
-__device__ __forceinline__ Two two(float x, float y)
+__host__ __device__ __forceinline__ uint32_t low_bits(Two a) { return static_cast<uint32_t>(a.v); }
+__host__ __device__ __forceinline__ uint32_t high_bits(Two a)
+{
+    return static_cast<uint32_t>(a.v >> 32);
+}
+__host__ __device__ __forceinline__ Two two(float x, float y)
 {
     Two r;
+#ifdef __CUDA_ARCH__
     asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+#else
+    r.v = static_cast<uint64_t>(static_cast<uint32_t>(bits_of(y))) << 32 |
+          static_cast<uint32_t>(bits_of(x));
+#endif
     return r;
 }
-__device__ __forceinline__ Two two(float x) { return two(x, x); }
-__device__ __forceinline__ Two operator+(Two a, Two b)
+__host__ __device__ __forceinline__ Two two(float x) { return two(x, x); }
+__host__ __device__ __forceinline__ Two operator+(Two a, Two b)
 {
+#ifdef __CUDA_ARCH__
     Two r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
+#else
+    return two(float_of(low_bits(a)) + float_of(low_bits(b)),
+               float_of(high_bits(a)) + float_of(high_bits(b)));
+#endif
 }
-__device__ __forceinline__ Two operator-(Two a, Two b)
+__host__ __device__ __forceinline__ Two operator-(Two a, Two b)
 {
+#ifdef __CUDA_ARCH__
     Two r;
     asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
+#else
+    return two(float_of(low_bits(a)) - float_of(low_bits(b)),
+               float_of(high_bits(a)) - float_of(high_bits(b)));
+#endif
 }
-__device__ __forceinline__ Two operator*(Two a, Two b)
+__host__ __device__ __forceinline__ Two operator*(Two a, Two b)
 {
+#ifdef __CUDA_ARCH__
     Two r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
+#else
+    return two(float_of(low_bits(a)) * float_of(low_bits(b)),
+               float_of(high_bits(a)) * float_of(high_bits(b)));
+#endif
 }
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+__host__ __device__ __forceinline__ Two fma2(Two a, Two b, Two c)
 {
+#ifdef __CUDA_ARCH__
     Two r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
     return r;
+#else
+    return two(fmaf(float_of(low_bits(a)), float_of(low_bits(b)), float_of(low_bits(c))),
+               fmaf(float_of(high_bits(a)), float_of(high_bits(b)), float_of(high_bits(c))));
+#endif
 }
-__device__ __forceinline__ uint32_t low_bits(Two a) { return static_cast<uint32_t>(a.v); }
-__device__ __forceinline__ uint32_t high_bits(Two a) { return static_cast<uint32_t>(a.v >> 32); }
 
 // y of two logits below a finite M: its fp32 value p and the rest e.
-__device__ __forceinline__ void exponents(float M, const WeightScale &c, Two l, Two &p, Two &e)
+__host__ __device__ __forceinline__ void exponents(float M, const WeightScale &c, Two l, Two &p,
+                                                   Two &e)
 {
     const Two m = two(M), h = m - l, b = h - m, lo = (m - (h - b)) - (l + b);
     const Two ch = two(c.ch);
@@ -187,8 +227,9 @@ __device__ __forceinline__ void exponents(float M, const WeightScale &c, Two l, 
 }
 
 // The weights of two logits: weight() of each, to the bit.
-__device__ __forceinline__ void weights(const uint64_t *table, const WeightScale &c, float M,
-                                        float l0, float l1, uint64_t &w0, uint64_t &w1)
+__host__ __device__ __forceinline__ void weights(const uint64_t *table, const WeightScale &c,
+                                                 float M, float l0, float l1, uint64_t &w0,
+                                                 uint64_t &w1)
 {
     if (fabsf(M) == INFINITY) {
         w0 = l0 == M ? (1ull << kWeightBits) | 1 : 0;
@@ -204,9 +245,9 @@ __device__ __forceinline__ void weights(const uint64_t *table, const WeightScale
     const Two whole = two(kWhole), a = fma2(zh, two(8589934592.f), whole);
     const Two b = fma2(s + fma2(a - whole, two(-1.16415322e-10f), zh), two(4398046511104.f), whole);
     constexpr uint32_t off = (kWholeBits << 9) + kWholeBits;
-    w0 = weight_of_parts(table, __uint_as_float(low_bits(p)), low_bits(t),
+    w0 = weight_of_parts(table, float_of(low_bits(p)), low_bits(t),
                          static_cast<int>((low_bits(a) << 9) + low_bits(b) - off));
-    w1 = weight_of_parts(table, __uint_as_float(high_bits(p)), high_bits(t),
+    w1 = weight_of_parts(table, float_of(high_bits(p)), high_bits(t),
                          static_cast<int>((high_bits(a) << 9) + high_bits(b) - off));
 }
 
