@@ -1146,8 +1146,8 @@ zp_status zp_paged_chunk_attn(zp_cache *c, int32_t layer, const void *q, int64_t
     }
     // Requests with many query rows over widened blocks, the others over the cache, if the
     // batch has many rows a request: two kernels one after the other cost a mixed batch more
-    // than the widened blocks gain (60 single tokens beside two pieces of 900, 64 dims: 138 us
-    // that way, 118 in one kernel; 19 chunks of 64 over 8,192, none of them long: 173, 153).
+    // than the widened blocks gain (60 single tokens beside two pieces of 900, 64 dims: 133 us
+    // that way, 118 in one kernel; 19 chunks of 64 over 8,192, none of them long: 174, 159).
     if (total * G >= static_cast<long long>(R) * zp::kWideMeanRows) {
         zp::Fp8WidenArgs w{};
         w.kpool = static_cast<const uint8_t *>(c->kpools[layer]);

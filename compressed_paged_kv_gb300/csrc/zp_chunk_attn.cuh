@@ -88,8 +88,8 @@
 // A request of many query rows has its V tiles converted once for every 256 of them: those are
 // widened to bf16 first (zp_fp8_widen.cu).  Chunks of few rows are zp_fp8_decode.cu's.
 //
-// Measured, 256 chunks of 8 tokens over 1,536 keys, 32 heads of 128 over 8, 0.81 GB in 297 us, 2.7
-// TB/s (a bf16 cache, of twice the bytes: 262); 19 chunks of 64 over 8,192 158 us (117).
+// Measured, 256 chunks of 8 tokens over 1,536 keys, 32 heads of 128 over 8, 0.81 GB in 295 us, 2.7
+// TB/s (a bf16 cache, of twice the bytes: 260); 19 chunks of 64 over 8,192 159 us (116).
 // What bounds it: with few rows a tile, the two warps of a stream that have them (a row's 64 columns
 // take one warp 1.4 to 2.2 us of the 2.8 us between key tiles) and 13 us of Q, joins and output
 // between items; with many, the chain of a stream, longer by V's conversion.

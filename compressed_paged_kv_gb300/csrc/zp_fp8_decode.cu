@@ -34,9 +34,9 @@
 //
 // Measured, 32 heads of 128 over 8 kv heads: 256 requests of 1,024 to 2,039 tokens, 0.81 GB in
 // 133 us = 6.1 TB/s, 0.90 of the copy peak (with 16 rows of heads and two CTAs an SM 166 us);
-// one of 2,000 tokens 6.3 us, the chain row -> block ids -> slabs -> joins; bound by HBM where
-// the rows fill the GPU.  256 chunks of 1, 4 and 6 tokens over 1,536, 0.81 GB: 146, 178 and
-// 258 us (in the kernel for tiles of 128 rows 285, 289 and 290); with more columns a warp waits
+// one of 2,000 tokens 6.5 us, the chain row -> block ids -> slabs -> joins; bound by HBM where
+// the rows fill the GPU.  256 chunks of 1, 4 and 6 tokens over 1,536, 0.81 GB: 149, 182 and
+// 262 us (in the kernel for tiles of 128 rows 289, 295 and 297); with more columns a warp waits
 // for its own products, three and two CTAs an SM being all that registers and rings leave
 // (schedulers issue in 45 % of the cycles).  Four eights took 300 us.
 #include <algorithm>
@@ -728,13 +728,13 @@ int fp8_decode_splits(long long pairs, int bt_stride, int num_sms, int *groups)
 
 // A large batch has a launch for up to 16 rows (8 of a mean of 8 or less), unless its mean says that
 // hardly any chunk has so few, and one for up to 24 of a mean of no more.  Measured with 8 kv heads
-// against the other kernel alone: 256 chunks of 2 to 9 tokens, four heads a group, 270 and 304 us; of
-// 1 to 5, 214 and 307; 200 single tokens beside 8 pieces of 600, 276 and 375; where none is short, 256
-// of 8 tokens 303 and 297, of 20 tokens 326 and 320.  A small batch, where a launch more costs
-// more than it gains (38 chunks of 2 to 9: 61 and 78 us with two), has the one of its mean, if that
-// is at most 20.  Too few units (request, kv head) for the splits to fill the GPU want short rows
-// (one request of four tokens: 2,000 keys 9.6 us, 8,192 20 and 30,000 56; the other kernel 20.6,
-// 24.9 and 38).
+// against the other kernel alone: 256 chunks of 2 to 9 tokens, four heads a group, 273 and 303 us; of
+// 1 to 5, 217 and 305; 200 single tokens beside 8 pieces of 600, 279 and 373; where none is short, 256
+// of 8 tokens 302 and 295, of 20 tokens 325 and 318.  A small batch, where a launch more costs
+// more than it gains (38 chunks of 2 to 9 over 1,500: 47 and 73 us with two), has the one of its mean,
+// if that is at most 20.  Too few units (request, kv head) for the splits to fill the GPU want short
+// rows (one request of four tokens: 2,000 keys 10 us, 8,192 21 and 30,000 57; the other kernel 20.5,
+// 25 and 37).
 FewRows fp8_few_rows(long long rows, int R, int hkv, int G, int bt_stride, int num_sms)
 {
     const long long mean = (rows + R - 1) / R, units = static_cast<long long>(R) * hkv;

@@ -11,8 +11,8 @@
 // in turn, 16 bytes a thread at a time.  Bound by HBM: one byte read and two written an element.
 //
 // Measured, with the bf16 kernel behind it against the 8-bit kernel alone: 2,048 tokens over 30,001,
-// 32 heads of 128 over 8, 733 us and 857; 16 prompts of 331 to 4,007, 28 heads of 64 over 4, 472 and
-// 674.  Of a bf16 cache the first takes 647.  This kernel alone, from cold caches: 39 us (4.7 TB/s) and
+// 32 heads of 128 over 8, 687 us and 879; 16 prompts of 331 to 4,007, 28 heads of 64 over 4, 467 and
+// 644.  Of a bf16 cache the first takes 645.  This kernel alone, from cold caches: 39 us (4.7 TB/s) and
 // 16.7 (with eight vectors a thread on their way and four CTAs an SM 40 and 18.4).
 #include "zp_fp8.cuh"
 

@@ -117,7 +117,10 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out);
  *       they begin at its slot 0, else max(S', scale), where a larger scale has the
  *       numbers before them rounded again to number * (scale / S); then number = x / S
  *       to the nearest e4m3 number (ties to even, magnitudes past 448 to 448, NaN to
- *       NaN).  Slots past the call's rows keep their bytes.
+ *       NaN).  Slots past the call's rows keep their bytes.  A block's scale never
+ *       falls while it holds tokens: drafted rows that raised it and were then
+ *       rejected (zp_verify_draft) leave the rows before them as they were rounded
+ *       again, with the larger scale, until the block is written from its slot 0
  *   zp_paged_decode_attn, zp_paged_chunk_attn  attend over the values; the
  *       probabilities are rounded to fp16 for the product with V, or to bf16 in the
  *       chunks of 1,536 query rows (tokens times heads of a kv head) and more of a
@@ -556,7 +559,8 @@ zp_status zp_verify_draft(zp_cache *cache, const int32_t *tokens, const int32_t 
  *  temperature, top_k, top_p, min_p   device [num_rows] fp32, int32, fp32, fp32, each
  *                NULL for 1, 0, 1, 0; row i uses entry req_idx[i], or i with NULL
  *                (entries may be used by several rows: a chunk's)
- *  R             rows of logits (of zp_sample at most max_requests)
+ *  R             rows of logits (of zp_sample at most max_requests, of
+ *                zp_token_probs at most 2^24, ZP_ERR_UNSUPPORTED beyond)
  * Outputs share no memory with inputs or each other (ZP_ERR_INVALID_ARG).  An entry
  * out of range, a temperature below 0, infinite or NaN, a NaN among the others, or a
  * row without any logit above -infinity is recorded as ZP_ERR_DEVICE_CHECK in the
