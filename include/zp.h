@@ -122,10 +122,11 @@ zp_status zp_cache_create(const zp_cache_desc *desc, zp_cache **out);
  *       rejected (zp_verify_draft) leave the rows before them as they were rounded
  *       again, with the larger scale, until the block is written from its slot 0
  *   zp_paged_decode_attn, zp_paged_chunk_attn  attend over the values; the
- *       probabilities are rounded to fp16 for the product with V, or to bf16 in the
- *       chunks of 1,536 query rows (tokens times heads of a kv head) and more of a
- *       batch of 768 a request and more in the mean, whose blocks are widened to bf16
- *       first; zp_paged_chunk_attn may take q to 2^-17 of its row's largest element, and
+ *       probabilities are rounded to fp16 for the product with V (each, times its block's
+ *       V scale, to 2^-11 of itself down to 2^-19 of the row's largest such product, and
+ *       to 2^-30 of the largest below that), or to bf16 in the chunks of 1,536 query
+ *       rows (tokens times heads of a kv head) and more of a batch of 768 a request and
+ *       more in the mean, whose blocks are widened to bf16 first; zp_paged_chunk_attn may take q to 2^-17 of its row's largest element, and
  *       its scores (scaled, in base 2) are below 2^20 in magnitude, where fp32 tells
  *       them apart
  *   zp_append_slots  copies a shared tail's scales with its rows
